@@ -13,3 +13,7 @@ from ._binding import (  # noqa: F401
     attn_prefill_window, attn_strerror, attn_sync_check, attn_version, decode, decode_counters,
     decode_packed, decode_split, decode_split_packed, load, merge, prefill, prefill_schedule,
     prefill_varlen, prefill_window, sync_check)
+from ._serving import (  # noqa: F401
+    attn_decode_paged, attn_decode_paged_splits, attn_evict, attn_key_weights, attn_prefill_paged,
+    attn_prefill_paged_splits, attn_rope_append, decode_paged, evict, key_weights, prefill_paged, rope_append,
+    rope_frequencies)

@@ -68,6 +68,17 @@ def load(path: str | None = None):
         lib.attn_decode_noalloc.argtypes = [vp, vp, vp, vp] + [i] * 5 + [f, i, i, vp, vp, i, vp]
         lib.attn_decode_noalloc_scratch_bytes.argtypes = []
         lib.attn_decode_noalloc_scratch_bytes.restype = ull
+        ll = ctypes.c_longlong
+        lib.attn_rope_append.argtypes = [vp] * 3 + [ll] * 3 + [vp] * 8 + [i] * 7 + [f] + [i] * 3 + [vp]
+        lib.attn_prefill_paged.argtypes = [vp] * 8 + [i] * 12 + [f, i, i, vp, vp, i, vp]
+        lib.attn_prefill_paged_splits.argtypes = [i] * 7
+        lib.attn_decode_paged.argtypes = [vp] * 5 + [i] * 7 + [f, i, i, vp, vp, vp, vp, i, vp, vp]
+        lib.attn_decode_paged_splits.argtypes = [i] * 3 + [vp]
+        lib.attn_key_weights.argtypes = [vp] * 7 + [ll] + [i] * 12 + [f, i, vp]
+        lib.attn_evict.argtypes = [vp, vp, ll] + [vp] * 4 + [i] * 9 + [vp] * 3 + [i] * 3 + [vp] * 3
+        for name in ("attn_rope_append", "attn_prefill_paged", "attn_prefill_paged_splits", "attn_decode_paged",
+                     "attn_decode_paged_splits", "attn_key_weights", "attn_evict"):
+            getattr(lib, name).restype = i
         for name in ("attn_prefill_fwd", "attn_prefill_varlen", "attn_prefill_window",
                      "attn_prefill_varlen_window", "attn_prefill_packed", "attn_decode_packed",
                      "attn_decode_split_packed",

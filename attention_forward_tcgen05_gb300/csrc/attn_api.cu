@@ -79,12 +79,12 @@ int encode_bf16_4d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1,
 // {64, G, 1, 128/G, 1} holds 128/G positions x the G heads of one group, 128
 // rows of 128 bytes in shared memory (row = position-in-box * G + head-in-group).
 int encode_bf16_q5d(CUtensorMap* map, const void* base, uint64_t d, uint64_t G, uint64_t Hq,
-                    uint64_t ns, uint64_t nb) {
+                    uint64_t ns, uint64_t nb, uint32_t rows = attn::kPrefillTileM) {
   EncodeTiledFn enc = encoder();
   if (enc == nullptr) return ATTN_ERR_CUDA;
   const cuuint64_t dims[5] = {d, G, Hq / G, ns, nb};
   const cuuint64_t strides[4] = {d * 2, d * G * 2, d * Hq * 2, d * Hq * ns * 2};
-  const cuuint32_t box[5] = {64, (cuuint32_t)G, 1, (cuuint32_t)(attn::kPrefillTileM / G), 1};
+  const cuuint32_t box[5] = {64, (cuuint32_t)G, 1, (cuuint32_t)(rows / G), 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides,
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -103,6 +103,11 @@ int from_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA
 }  // namespace
 
 namespace attn {
+
+uint32_t* device_err_word() { return err_word(); }
+int encode_q_map(CUtensorMap* map, const void* base, int d, int G, int Hq, int ns, int nb, int rows) {
+  return encode_bf16_q5d(map, base, d, G, Hq, ns, nb, rows);
+}
 
 int check_decode_split_args(const void* q, const void* kcache, const void* vcache, const int* kv_lens,
                             int B, int Hq, int Hkv, int d, int max_kv, float scale, int n_splits,
@@ -267,7 +272,7 @@ const char* attn_strerror(int status) {
     case ATTN_ERR_CUDA: return "CUDA runtime or launch error";
     case ATTN_ERR_DEVICE_TIMEOUT: return "a kernel's bounded pipeline wait timed out";
     case ATTN_ERR_SCRATCH_TOO_SMALL: return "problem too large for the library's static decode scratch (24 MiB)";
-    case ATTN_ERR_DEVICE_INPUT: return "a kernel found a device-side input (kv_lens) changed while it ran";
+    case ATTN_ERR_DEVICE_INPUT: return "a kernel found a device-side input (kv_lens, a page table, a cache position) wrong or changed while it ran";
     default: return "unknown status";
   }
 }
@@ -407,6 +412,9 @@ int attn_merge(const float* part_o, const float* part_lse, void* o, float* lse, 
   attn::MergeArgs a;
   a.part_o = part_o; a.part_lse = part_lse; a.o = o; a.lse = lse;
   a.B = B; a.Hq = Hq; a.n_splits = n_splits; a.d = d; a.o_bf16 = o_dtype == ATTN_BF16 ? 1 : 0;
+  a.lse_by_head = 0;
+  a.cu_q = nullptr;
+  a.n_seq = 0;
   return from_cuda(attn::launch_merge(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -8,6 +8,16 @@
 
 namespace attn {
 
+// A paged K/V cache: pools [num_pages][page_size][Hkv][d], key j of sequence b in slot
+// j % page_size of page table[b][j / page_size] (table [B][max_pages]).  table ==
+// nullptr: a dense cache [B][page_size][Hkv][d].
+struct PagedKV {
+  const uint16_t* k;
+  const uint16_t* v;
+  const int* table;
+  int max_pages, page_size, num_pages;
+};
+
 // Prefill launch description (already validated by the C-ABI layer).
 // Fixed-length batches: cu_q == nullptr, q/o [B][Sq][Hq][d], k/v [B][Skv][Hkv][d],
 // lse [B][Hq][Sq]; with kv_lens != nullptr sequence b has only the keys
@@ -49,6 +59,7 @@ struct PrefillArgs {
   int halves;
   float* part_o;
   float* part_lse;
+  PagedKV kv;  // prefill_paged.cu only: the cache instead of tm_k / tm_v
 };
 
 #ifdef __CUDACC__
@@ -128,6 +139,7 @@ struct DecodeArgs {
   void* o;       // [B][Hq][d], fp32 or bf16 (o_bf16)
   float* lse;    // [B][Hq]
   int o_bf16;
+  PagedKV kv;    // decode_paged.cu only: the cache instead of tm_k / tm_v
 };
 
 struct MergeArgs {
@@ -136,6 +148,58 @@ struct MergeArgs {
   void* o;
   float* lse;
   int B, Hq, n_splits, d, o_bf16;
+  // packed prefill (B = its total_q): lse [Hq][B] instead of [B][Hq], rows of the tokens
+  // [cu_q[0], cu_q[n_seq]) only
+  int lse_by_head;
+  const int* cu_q;
+  int n_seq;
+};
+
+// Rotary positions and the cache append (rope.cu).
+struct RopeArgs {
+  const uint16_t *q, *k, *v;              // rows of token t at + t * stride (elements)
+  long long q_stride, k_stride, v_stride;
+  const int* positions;                   // [total], or nullptr: the token's key index
+  const double* inv_freq;                 // [rot / 2]
+  uint16_t* q_out;                        // [total][Hq][d]
+  uint16_t *kc, *vc;                      // the pools of kv, written
+  PagedKV kv;
+  const int *cu_q, *kv_lens;              // cu_q == nullptr: one token per sequence
+  int B, Hq, Hkv, total, d, rot, interleaved;
+  float amp;
+  uint32_t* err;
+};
+
+// Accumulated attention weights (key_weights.cu).
+struct KeyWeightArgs {
+  CUtensorMap tm_q;  // 5-D query map {d, pack, Hq / pack, total_q, 1} (tensor-core path)
+  const uint16_t* q;
+  const float* lse;  // lse of (head h, token t) at h * lse_hs + t * lse_ts
+  long long lse_hs, lse_ts;
+  PagedKV kv;
+  const int *cu_q, *kv_lens;  // cu_q == nullptr: one token per sequence
+  float* weights;             // [B][Hkv][w_stride]
+  long long w_stride;
+  int B, Hq, Hkv, total_q, max_sq, d, pack, causal, window, n_sink, accumulate;
+  float scale;
+  uint32_t* err;
+};
+// Few query rows per (sequence, KV head): the CUDA-core path, which needs no map.
+bool key_weights_few_rows(int max_sq, int G);
+int key_weights_q_rows(int d);  // rows of a query tile of the tensor-core path
+
+// Eviction (evict.cu).
+struct EvictArgs {
+  const float* weights;  // [B][Hkv][w_stride]
+  float* weights_out;    // same shape, may be `weights`; or nullptr
+  long long w_stride;
+  PagedKV src, dst;      // dst.table == src.table and pools: in place
+  uint16_t *dk, *dv;     // the pools of dst, written
+  const int* kv_lens;
+  int* new_lens;         // [B]
+  int* kept;             // [B][Hkv][budget]
+  int B, Hkv, d, budget, n_recent, n_sink, in_place;
+  uint32_t* err;
 };
 
 // Rows of a K / V stage loaded by one TMA box in the decode kernel (two
@@ -182,13 +246,24 @@ cudaError_t launch_prefill_d512(const PrefillArgs& a, cudaStream_t stream);
 constexpr int kD512PairRingBytes = 6 * 16384;
 constexpr int kD512PairSlotBytes = 32768;
 constexpr int kD512PairVBoxRows = kD512PairSlotBytes >= 16384 ? 128 : kD512PairSlotBytes / 128;
+// Packed varlen batches over a paged cache (prefill_paged.cu): d in {64, 128, 256}, pack
+// <= 128; halves: every sequence's rows fit one query tile (d <= 128).
+cudaError_t launch_prefill_paged(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_empty_kv(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_split(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_paged(const DecodeArgs& a, cudaStream_t stream);
 // The persistent prefill's unit schedule for BH = B * Hq heads over `grid` CTAs:
 // sched = offsets[grid + 1] followed by each CTA's units; returns the unit count,
 // 0 when the launch keeps the wave deal (sched left empty), -1 on bad arguments.
 int build_prefill_schedule(int BH, int Sq, int Skv, int causal, int grid, std::vector<int>& sched);
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_key_weights(const KeyWeightArgs& a, cudaStream_t stream);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+// This device's error word (attn_api.cu), or nullptr.
+uint32_t* device_err_word();
+// 5-D query map of the packed tiles: {d, G, Hq / G, ns, nb}, box {64, G, 1, rows / G, 1}.
+int encode_q_map(CUtensorMap* map, const void* base, int d, int G, int Hq, int ns, int nb, int rows);
 cudaError_t launch_wait_timeout_probe(uint64_t limit_ns, uint32_t* err, cudaStream_t stream);
 
 }  // namespace attn

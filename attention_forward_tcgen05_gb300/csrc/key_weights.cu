@@ -1,0 +1,460 @@
+// key_weights.cu -- accumulated attention weight of every cached key.
+//
+//   W[b,hk,j] (+)= sum over the new rows i of sequence b and the G heads h of KV head hk of
+//                  exp(scale * q[i,h] . k[j,hk] - lse[i,h]),   admissible (i, j) only,
+// the column sums of the softmax whose row sums the attention call left in lse.  A key's
+// sum has one owner, which adds its terms in a fixed order: no atomics, the same bits
+// each time.  Two kernels, by how many query rows a KV head has in a sequence:
+//   * up to kRowsMax (a decode step): the keys are streamed from HBM once and nothing else
+//     matters; CUDA cores, lane = key;
+//   * more: S^T = K Q^T on the tensor cores, so a key is a TMEM lane and a thread sums its
+//     own row; one ex2 per pair (32 a cycle per SM) and the MMA (512 cycles per 128 x 128
+//     tile at d = 128) take equally long.
+#include <cmath>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The rows of a sequence and which keys they admit: key j and position p (key index of the
+// row) with j <= p if causal, and with a window j > p - window or j < n_sink.
+__device__ __forceinline__ bool admits(int j, long long p, int causal, int window, int n_sink) {
+  if (causal && j > p) return false;
+  return window <= 0 || j > p - window || j < n_sink;
+}
+
+__device__ __forceinline__ void put_weight(const KeyWeightArgs& a, int b, int hk, int j, float w) {
+  float* dst = a.weights + ((size_t)b * a.Hkv + hk) * a.w_stride + j;
+  *dst = a.accumulate ? *dst + w : w;
+}
+
+// ------------------------------------------------------------------ few rows
+constexpr int kRowsMax = 16;
+constexpr int kRowWarps = 4;
+
+template <int D>
+struct RowCfg {
+  static constexpr int kStages = D == 256 ? 2 : 3;
+  static constexpr int kStageBytes = 32 * D * 2;  // 32 keys
+  static constexpr int kSmem = kRowWarps * kStages * kStageBytes + 1024;
+};
+
+// One CTA per (sequence, KV head, range of `chunk` keys); each warp takes every fourth
+// 32-key tile of it through a ring of its own (cp.async groups, no barriers).
+template <int D, int RMAX>
+__global__ void __launch_bounds__(kRowWarps * 32) key_weights_rows_kernel(const KeyWeightArgs a, int chunk) {
+  using C = RowCfg<D>;
+  constexpr int ST = C::kStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_bh = a.B * a.Hkv;
+  const int bh = (int)(blockIdx.x % n_bh), hk = bh % a.Hkv, b = bh / a.Hkv;
+  const int cap = a.kv.max_pages * a.kv.page_size;
+  const SeqExtent e = seq_extent(b, a.cu_q ? a.max_sq : 1, cap, a.cu_q, a.kv_lens, a.total_q);
+  const int base = a.cu_q ? e.qbase : b;
+  const int lo = (int)(blockIdx.x / n_bh) * chunk, hi = min(e.Skv, lo + chunk);
+  if (lo >= hi) return;
+  const int G = a.Hq / a.Hkv, R = e.Sq * G;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(16) uint16_t qs[RMAX * D];
+  __shared__ float nl[RMAX];  // -lse * log2 e
+  uint8_t* ring = smem + warp * ST * C::kStageBytes;
+
+  int ri[1];
+  int tile = lo + warp * 32, issued = 0;  // tiles of this warp: tile, tile + 128, ...
+  auto issue = [&]() {
+    if (tile < hi) {
+      paged_rows<1>(a.kv, b, tile, hi, lane, a.err, ri);
+      paged_gather<D, 1>(smem_u32(ring + (issued % ST) * C::kStageBytes), 32 * 128, a.kv.k, a.Hkv, hk, lane, ri);
+    }
+    cp_async_commit();
+    ++issued;
+    tile += kRowWarps * 32;
+  };
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s) issue();
+  for (int i = threadIdx.x; i < RMAX * (D / 8); i += kRowWarps * 32) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < R) {
+      const int pos = r / G, h = hk * G + r % G;
+      x = *reinterpret_cast<const uint4*>(a.q + ((size_t)(base + pos) * a.Hq + h) * D + c * 8);
+      if (c == 0) nl[r] = -kLog2e * a.lse[(size_t)h * a.lse_hs + (size_t)(base + pos) * a.lse_ts];
+    }
+    *reinterpret_cast<uint4*>(qs + r * D + c * 8) = x;
+  }
+  __syncthreads();
+  const float sl2 = a.scale * kLog2e;
+  const long long off = (long long)e.Skv - e.Sq;
+  int done = 0;
+  for (int j0 = lo + warp * 32; j0 < hi; j0 += kRowWarps * 32) {
+    issue();
+    cp_async_wait<ST - 1>();
+    __syncwarp();
+    const uint8_t* kt = ring + (done % ST) * C::kStageBytes + lane * 128;
+    float al[RMAX], ah[RMAX];
+#pragma unroll
+    for (int r = 0; r < RMAX; ++r) al[r] = ah[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 kv = *reinterpret_cast<const uint4*>(kt + (c >> 3) * (32 * 128) + (((c & 7) ^ (lane & 7)) << 4));
+#pragma unroll
+      for (int r = 0; r < RMAX; ++r) {
+        if (r < R) {
+          const uint4 qv = *reinterpret_cast<const uint4*>(qs + r * D + c * 8);
+          fma_bf16x2_f32(qv.x, kv.x, al[r], ah[r]);
+          fma_bf16x2_f32(qv.y, kv.y, al[r], ah[r]);
+          fma_bf16x2_f32(qv.z, kv.z, al[r], ah[r]);
+          fma_bf16x2_f32(qv.w, kv.w, al[r], ah[r]);
+        }
+      }
+    }
+    const int j = j0 + lane;
+    float w = 0.f;
+#pragma unroll
+    for (int r = 0; r < RMAX; ++r) {
+      if (r < R) {
+        const float p = ex2_approx(fmaf(al[r] + ah[r], sl2, nl[r]));
+        if (admits(j, (long long)(r / G) + off, a.causal, a.window, a.n_sink) && nl[r] != INFINITY) w += p;
+      }
+    }
+    if (j < hi) put_weight(a, b, hk, j, w);
+    __syncwarp();  // every lane has read the tile before its slot is refilled
+    ++done;
+  }
+  cp_async_wait<0>();
+}
+
+// ------------------------------------------------------------------ many rows
+// CTA: 256 keys (two M = 128 tiles) of one (sequence, KV head), resident in shared memory;
+// the query rows of the group's heads stream past in tiles of QN rows (whole positions).
+// Two key tiles per query tile halve the query traffic from L2 (64 bytes a cycle per SM
+// otherwise).  Warps 0-3 / 4-7: the two key tiles' sums (thread = key); warp 8: MMA
+// issue; warp 9: query tiles by TMA, their lse by plain loads.  S^T is double buffered in
+// TMEM, so the MMA of one query tile runs under the exponentials of the one before.  The
+// CTAs of a cluster share the keys and take every cs-th query tile; their sums meet in
+// rank 0, in rank order.
+template <int D>
+struct TileCfg {
+  static constexpr int QN = D == 256 ? 64 : 128;  // query rows of a tile
+  static constexpr int kKeys = 256;
+  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kPanels = D / 64;
+  static constexpr int kKPanel = 128 * 128;               // one panel of a 128-key tile
+  static constexpr int kKTile = kPanels * kKPanel;
+  static constexpr int kQPanel = QN * 128;
+  static constexpr int kQTile = kPanels * kQPanel;
+  static constexpr int kQOff = 2 * kKTile;
+  static constexpr int kLseOff = kQOff + kStages * kQTile;   // [stage][QN] floats
+  static constexpr int kSumOff = kLseOff + kStages * QN * 4; // [256] floats
+  static constexpr int kBarOff = kSumOff + kKeys * 4;
+  static constexpr int kNumBars = 2 * kStages + 2 * 2 * 2;   // full, empty, S[tile][buf], free[tile][buf]
+  static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
+  static constexpr int kThreads = 12 * 32;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+template <int D>
+__global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
+    key_weights_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const KeyWeightArgs a, int pack, int cs) {
+  using C = TileCfg<D>;
+  constexpr int QN = C::QN;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)blockIdx.x % cs;
+  const int u = (int)blockIdx.x / cs, n_bh = a.B * a.Hkv;
+  const int kb = u / n_bh;  // key block: under a causal mask the first ones see the most rows and start first
+  const int hk = u % n_bh % a.Hkv, b = u % n_bh / a.Hkv;
+  const int cap = a.kv.max_pages * a.kv.page_size;
+  const SeqExtent e = seq_extent(b, a.cu_q ? a.max_sq : 1, cap, a.cu_q, a.kv_lens, a.total_q);
+  const int base = a.cu_q ? e.qbase : b;
+  const int k0 = kb * C::kKeys;
+  if (k0 >= e.Skv) return;  // the whole cluster: nothing of it waits on a peer
+  const int Gall = a.Hq / a.Hkv, G = pack, n_hu = Gall / G;  // head groups of the KV head
+  const int PT = QN / G;                  // positions of a query tile
+  const long long off = (long long)e.Skv - e.Sq;  // key index of row i: i + off
+  // positions [i0, i1) that admit a key of this block
+  long long i0 = 0, i1 = e.Sq;
+  const int k_last = min(e.Skv, k0 + C::kKeys) - 1;
+  if (a.causal) i0 = max(0LL, (long long)k0 - off);
+  if (a.window > 0 && k0 >= a.n_sink) i1 = min(i1, (long long)k_last + a.window - off);
+  const int t0 = (int)(i0 / PT);
+  const int tiles = i1 > i0 ? (int)((i1 + PT - 1) / PT) - t0 : 0;
+  const int total_tiles = tiles * n_hu;
+  const int n = total_tiles > rank ? (total_tiles - rank + cs - 1) / cs : 0;  // this CTA's tiles
+  // i-th of them: tile index x = rank + i * cs; head group x % n_hu, positions from (t0 + x / n_hu) * PT
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem;
+  uint8_t* sQ = smem + C::kQOff;
+  float* sL = reinterpret_cast<float*>(smem + C::kLseOff);
+  float* sSum = reinterpret_cast<float*>(smem + C::kSumOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* bar_S = empty + C::kStages;  // [tile][buf] S^T computed
+  uint64_t* bar_F = bar_S + 4;           // [tile][buf] S^T read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_F + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1 + 8);  // the MMA's reads, and each sum warp's reads of the lse
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar_S[i], 1);
+      mbar_init(&bar_F[i], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp < 8) {  // the block's keys: warp w gathers rows 32 w ..
+    int ri[1];
+    paged_rows<1>(a.kv, b, k0 + warp * 32, e.Skv, lane, a.err, ri);
+    paged_gather<D, 1>(smem_u32(sK + (warp >> 2) * C::kKTile + (warp & 3) * 32 * 128), C::kKPanel, a.kv.k, a.Hkv,
+                       hk, lane, ri);
+    cp_async_commit();
+    // rows of a query tile past its whole positions: no copy ever writes them, and as
+    // zeros (with lse terms of -inf) they add nothing
+    const int used = PT * G, pad = (QN - used) * 8;  // 16-byte chunks of one panel
+    for (int i = threadIdx.x; i < pad * C::kPanels * C::kStages; i += 256)
+      *reinterpret_cast<uint4*>(sQ + (i / pad) * C::kQPanel + used * 128 + (i % pad) * 16) = make_uint4(0, 0, 0, 0);
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool two = k0 + 128 < e.Skv;  // the second key tile exists
+
+  if (warp == 9) {
+    // ---- query tiles ----
+    if (lane == 0) tma_prefetch_desc(&tm_q);
+    int i = 0;
+    for (; i < n; ++i) {
+      const int s = i % C::kStages;
+      const int x = rank + i * cs, hu = hk * n_hu + x % n_hu, p0 = (t0 + x / n_hu) * PT;
+      float v[QN / 32];  // read before the wait for the slot
+#pragma unroll
+      for (int k = 0; k < QN / 32; ++k) {
+        const int c = k * 32 + lane, pos = p0 + c / G;
+        v[k] = -INFINITY;
+        if (c < PT * G && pos < e.Sq)
+          v[k] = -kLog2e * a.lse[(size_t)(hu * G + c % G) * a.lse_hs + (size_t)(base + pos) * a.lse_ts];
+        // a row without keys (lse = -inf) contributes nothing
+        if (v[k] == INFINITY) v[k] = -INFINITY;
+      }
+      if (!mbar_wait_warp(&empty[s], ((uint32_t)(i / C::kStages) & 1u) ^ 1u, a.err, abort_flag)) break;
+#pragma unroll
+      for (int k = 0; k < QN / 32; ++k) sL[s * QN + k * 32 + lane] = v[k];
+      __syncwarp();
+      mbar_arrive_expect_tx_e(&full[s], (uint32_t)(PT * G) * 128u * C::kPanels);
+#pragma unroll
+      for (int p = 0; p < C::kPanels; ++p)
+        tma_load_5d_e(sQ + s * C::kQTile + p * C::kQPanel, &tm_q, &full[s], p * 64, 0, hu, base + p0, 0);
+    }
+    if (i < n)  // aborted: the copies in flight land before shared memory is released
+      for (int u = max(0, i - C::kStages); u < i; ++u)
+        mbar_wait(&full[u % C::kStages], (uint32_t)(u / C::kStages) & 1u, nullptr, nullptr, 100000000ull);
+  } else if (warp == 8) {
+    // ---- MMA: S^T of both key tiles ----
+    constexpr uint32_t idesc = idesc_bf16_f32(128, QN, 0, 0);
+    const uint64_t dk = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
+    const uint64_t dq0 = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
+    bool ok = true;
+    for (int i = 0; ok && i < n; ++i) {
+      const int s = i % C::kStages, buf = i & 1;
+      const uint32_t ph = ((uint32_t)(i >> 1) & 1u) ^ 1u;
+      ok = mbar_wait_warp(&full[s], (uint32_t)(i / C::kStages) & 1u, a.err, abort_flag);
+      const uint64_t dq = dq0 + (uint64_t)((s * C::kQTile) >> 4);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || (t == 1 && !two)) continue;
+        ok = mbar_wait_warp(&bar_F[t * 2 + buf], ph, a.err, abort_flag);
+        if (!ok) continue;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t ok_ = (uint64_t)((t * C::kKTile + (kk >> 2) * C::kKPanel + (kk & 3) * 32) >> 4);
+          const uint64_t oq_ = (uint64_t)(((kk >> 2) * C::kQPanel + (kk & 3) * 32) >> 4);
+          mma_ss_e(tmem + (t * 2 + buf) * 128, dk + ok_, dq + oq_, idesc, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_e(&bar_S[t * 2 + buf]);
+      }
+      if (ok) mma_commit_e(&empty[s]);
+    }
+  } else if (warp < 8) {
+    // ---- sums ----
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int j = k0 + t * 128 + r;  // this thread's key
+    const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const float sl2 = a.scale * kLog2e;
+    const uint64_t sl2x2 = f2pack(sl2, sl2);
+    const int j_lo = k0 + t * 128, j_hi = j_lo + 127;
+    float acc = 0.f;
+    bool ok = true;
+    for (int i = 0; i < n && (t == 0 || two); ++i) {
+      const int s = i % C::kStages, buf = i & 1;
+      const int x = rank + i * cs, p0 = (t0 + x / n_hu) * PT;
+      // lse of the tile (the producer's writes), then S^T
+      bool got = mbar_wait(&full[s], (uint32_t)(i / C::kStages) & 1u, a.err, abort_flag);
+      got = got && mbar_wait(&bar_S[t * 2 + buf], (uint32_t)(i >> 1) & 1u, a.err, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // columns [c_lo, c_hi) admit this thread's key (a column's position: p0 + c / G)
+      int c_lo = 0, c_hi = (int)min((long long)(PT * G), ((long long)e.Sq - p0) * G);
+      const long long d0 = (long long)j - off - p0;  // first causal position, tile-relative
+      const bool edge = e.Sq - p0 < PT || (a.causal && j_hi > (long long)p0 + off) ||
+                        (a.window > 0 && j_hi >= a.n_sink && j_lo <= (long long)p0 + PT - 1 + off - a.window);
+      if (edge) {
+        if (a.causal && d0 > 0) c_lo = (int)min((long long)QN, d0 * G);
+        if (a.window > 0 && j >= a.n_sink) {
+          const long long w = d0 + a.window;
+          c_hi = w <= 0 ? 0 : (int)min((long long)c_hi, w * G);
+        }
+      }
+      const float4* lp = reinterpret_cast<const float4*>(sL + s * QN);
+      uint64_t a0 = f2pack(0.f, 0.f), a1 = a0;
+#pragma unroll
+      for (int c0 = 0; c0 < QN; c0 += 32) {
+        uint32_t sr[32];
+        tmem_ld32(lane_addr + (t * 2 + buf) * 128 + c0, sr);
+        tmem_wait_ld();
+        if (c0 == QN - 32) {  // S^T is in registers: its buffer may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_F[t * 2 + buf]);
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < 8; ++q4) {
+          const float4 l4 = lp[(c0 >> 2) + q4];
+          float x0, x1, x2, x3;
+          f2unpack(fma2(f2pack(__uint_as_float(sr[4 * q4]), __uint_as_float(sr[4 * q4 + 1])), sl2x2,
+                        f2pack(l4.x, l4.y)), x0, x1);
+          f2unpack(fma2(f2pack(__uint_as_float(sr[4 * q4 + 2]), __uint_as_float(sr[4 * q4 + 3])), sl2x2,
+                        f2pack(l4.z, l4.w)), x2, x3);
+          float p[4] = {ex2_approx(x0), ex2_approx(x1), ex2_approx(x2), ex2_approx(x3)};
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int c = c0 + 4 * q4 + k;
+              if (c < c_lo || c >= c_hi) p[k] = 0.f;
+            }
+          }
+          a0 = add2(a0, f2pack(p[0], p[1]));
+          a1 = add2(a1, f2pack(p[2], p[3]));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      float s0, s1;
+      f2unpack(add2(a0, a1), s0, s1);
+      acc += s0 + s1;
+    }
+    // a missing second key tile reads nothing but still counts on the query slots
+    if (t == 1 && !two) {
+      for (int i = 0; i < n; ++i) {
+        const int s = i % C::kStages;
+        if (!mbar_wait_warp(&full[s], (uint32_t)(i / C::kStages) & 1u, a.err, abort_flag)) break;
+        if (lane == 0) mbar_arrive(&empty[s]);
+      }
+    }
+    if (cs == 1) {
+      if (ok && j < e.Skv) put_weight(a, b, hk, j, acc);
+    } else {
+      sSum[t * 128 + r] = ok ? acc : NAN;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (cs > 1) {
+    cluster_sync_all();  // every rank's sums are written
+    if (rank == 0 && threadIdx.x < C::kKeys) {
+      const int j = k0 + (int)threadIdx.x;
+      float w = 0.f;
+      for (int r = 0; r < cs; ++r) w += ld_cluster_f32(mapa_shared(smem_u32(sSum + threadIdx.x), (uint32_t)r));
+      if (j < e.Skv) put_weight(a, b, hk, j, w);
+    }
+    cluster_sync_all();  // and read before their CTA's shared memory goes
+  }
+}
+
+template <int D>
+cudaError_t launch_rows(const KeyWeightArgs& a, int rows, cudaStream_t stream) {
+  using C = RowCfg<D>;
+  const long long units = (long long)a.B * a.Hkv;
+  const int cap = a.kv.max_pages * a.kv.page_size;
+  // ranges of keys: about eight CTAs an SM in all, 128 to 2048 keys each
+  int chunk = 2048;
+  while (chunk > 128 && units * ((cap + chunk - 1) / chunk) < 8 * 152) chunk /= 2;
+  auto kern = rows <= 4 ? key_weights_rows_kernel<D, 4>
+                        : (rows <= 8 ? key_weights_rows_kernel<D, 8> : key_weights_rows_kernel<D, kRowsMax>);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(units * ((cap + chunk - 1) / chunk)), kRowWarps * 32, C::kSmem, stream>>>(a, chunk);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_tiles(const KeyWeightArgs& a, cudaStream_t stream) {
+  using C = TileCfg<D>;
+  auto kern = key_weights_tiles_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int cap = a.kv.max_pages * a.kv.page_size;
+  const int blocks = (cap + C::kKeys - 1) / C::kKeys;
+  const long long units = (long long)blocks * a.B * a.Hkv;
+  const int PT = C::QN / a.pack;
+  const long long q_tiles = ((long long)a.max_sq + PT - 1) / PT * (a.Hq / a.Hkv / a.pack);
+  int cs = 1;  // CTAs of a cluster: up to eight, while SMs are idle and each keeps two tiles
+  while (cs < 8 && units * cs < 2 * 152 && q_tiles >= 4 * cs) cs *= 2;
+  cudaLaunchConfig_t cfg = {};
+  if (units * cs > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cs;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a.tm_q, a, (int)a.pack, cs);
+}
+
+}  // namespace
+
+bool key_weights_few_rows(int max_sq, int G) { return (long long)max_sq * G <= kRowsMax; }
+int key_weights_q_rows(int d) { return d == 256 ? TileCfg<256>::QN : TileCfg<128>::QN; }
+
+cudaError_t launch_key_weights(const KeyWeightArgs& a, cudaStream_t stream) {
+  const bool few = key_weights_few_rows(a.max_sq, a.Hq / a.Hkv);
+  const int rows = a.max_sq * (a.Hq / a.Hkv);
+  switch (a.d) {
+    case 64: return few ? launch_rows<64>(a, rows, stream) : launch_tiles<64>(a, stream);
+    case 128: return few ? launch_rows<128>(a, rows, stream) : launch_tiles<128>(a, stream);
+    case 256: return few ? launch_rows<256>(a, rows, stream) : launch_tiles<256>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace attn

@@ -1,0 +1,308 @@
+// paged_api.cu -- the C ABI of the paged-cache serving calls (include/attn.h): argument
+// validation and launches of rope.cu, prefill_paged.cu, decode_paged.cu, key_weights.cu
+// and evict.cu.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "attn.h"
+#include "internal.h"
+
+namespace {
+
+constexpr int kSms = 152;               // SMs of a GB300
+constexpr long long kMaxKeys = 1LL << 30;  // keys of one sequence's table, slots of a pool
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool ok16(const void* p) { return p != nullptr && aligned(p, 16); }
+bool ok4(const void* p) { return p != nullptr && aligned(p, 4); }
+bool ok_dim(int d) { return d == 64 || d == 128 || d == 256; }
+bool ok_scale(float s) { return std::isfinite(s) && s > 0.f; }
+int from_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+cudaStream_t stream_of(attn_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// Sizes of a cache: a table [B][max_pages] over a pool, or (no table) one page of
+// page_size keys per sequence.
+int check_cache(const int* table, int B, int max_pages, int page_size, int num_pages) {
+  if (max_pages < 1 || page_size < 1 || num_pages < 0) return ATTN_ERR_INVALID_ARG;
+  if ((long long)max_pages * page_size > kMaxKeys || (long long)num_pages * page_size > 2 * kMaxKeys - 1)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(table, 4)) return ATTN_ERR_INVALID_ARG;
+  if (table == nullptr && (max_pages != 1 || num_pages < B)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+int check_heads(int B, int Hq, int Hkv) {
+  return B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+}
+
+attn::PagedKV cache(const attn_bf16_t* k, const attn_bf16_t* v, const int* table, int max_pages, int page_size,
+                    int num_pages) {
+  return attn::PagedKV{k, v, table, max_pages, page_size, num_pages};
+}
+
+// Query heads that share a tile of `rows` rows: the largest divisor of G whose whole
+// positions fill at least 7/8 of the tile (1 always does).
+int pack_heads(int G, int rows) {
+  for (int p = G < rows ? G : rows; p > 1; --p)
+    if (G % p == 0 && rows / p * p * 8 >= rows * 7) return p;
+  return 1;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16_t* v, long long q_stride,
+                     long long k_stride, long long v_stride, const int* positions, const double* inv_freq,
+                     attn_bf16_t* q_out, attn_bf16_t* kcache, attn_bf16_t* vcache, const int* page_table,
+                     const int* cu_seqlens_q, const int* kv_lens, int B, int Hq, int Hkv, int total, int d,
+                     int rot_dim, int interleaved, float amp, int max_pages, int page_size, int num_pages,
+                     attn_stream_t stream) {
+  int rc = check_heads(B, Hq, Hkv);
+  if (rc != ATTN_OK) return rc;
+  if (total < 0 || (cu_seqlens_q == nullptr && total != B) || !std::isfinite(amp)) return ATTN_ERR_INVALID_ARG;
+  if (!ok_dim(d) || rot_dim < 0 || rot_dim > d || rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+  rc = check_cache(page_table, B, max_pages, page_size, num_pages);
+  if (rc != ATTN_OK) return rc;
+  if (B == 0 || total == 0) return ATTN_OK;
+  if (!ok16(k) || !ok16(v) || !ok16(kcache) || !ok16(vcache) || !ok4(kv_lens)) return ATTN_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || !aligned(q, 16) || !aligned(q_out, 16)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(positions, 4) || !aligned(cu_seqlens_q, 4)) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (inv_freq == nullptr || !aligned(inv_freq, 8))) return ATTN_ERR_INVALID_ARG;
+  // rows of tokens: at least the heads' width, in whole 16-byte units
+  if (k_stride < (long long)Hkv * d || v_stride < (long long)Hkv * d || k_stride % 8 || v_stride % 8)
+    return ATTN_ERR_INVALID_ARG;
+  if (q && (q_stride < (long long)Hq * d || q_stride % 8)) return ATTN_ERR_INVALID_ARG;
+  // in place only over itself: a contiguous q
+  if (q && q == q_out && q_stride != (long long)Hq * d) return ATTN_ERR_INVALID_ARG;
+  if ((long long)(Hq + 2LL * Hkv) * (d / 16) > 0x7FFFFFFFLL) return ATTN_ERR_INVALID_ARG;
+  attn::RopeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.positions = positions; a.inv_freq = inv_freq; a.q_out = q_out;
+  a.kc = kcache; a.vc = vcache;
+  a.kv = cache(kcache, vcache, page_table, max_pages, page_size, num_pages);
+  a.cu_q = cu_seqlens_q; a.kv_lens = kv_lens;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.total = total; a.d = d; a.rot = rot_dim;
+  a.interleaved = interleaved ? 1 : 0; a.amp = amp;
+  a.err = attn::device_err_word();
+  if (a.err == nullptr) return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_rope_append(a, stream_of(stream)));
+}
+
+int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, int max_kv, int d) {
+  if (check_heads(B, Hq, Hkv) != ATTN_OK || total_q < 0 || max_sq < 0 || max_kv < 0 || !ok_dim(d))
+    return ATTN_ERR_INVALID_ARG;
+  const int G = Hq / Hkv, pack = pack_heads(G, attn::kPrefillTileM), pos = attn::kPrefillTileM / pack;
+  const bool halves = d <= 128 && max_sq <= pos;
+  // blocks of query rows that exist, one unit each, and a unit's time over all keys
+  const long long block = d <= 128 && !halves ? 2 * pos : pos;
+  const long long blocks = std::min<long long>((long long)total_q / block + B, (max_sq + block - 1) / block * B);
+  const long long units = std::max(1LL, blocks * (Hq / pack));
+  const double tile_us = (d == 64 ? 0.7 : d == 128 ? 1.0 : 1.2) * (halves ? 0.5 : 1.0);
+  const double tiles = (max_kv + 127) / 128;
+  double best = 0;
+  int n_best = 1;
+  for (int n = 1; n <= 32 && n <= std::max(1.0, tiles / 2); ++n) {
+    const double waves = (double)((units * n + kSms - 1) / kSms);
+    // each unit's own start and end; the partials out and in again, and the merge's launch
+    const double us = waves * (tiles / n * tile_us + 3.0) +
+                      (n > 1 ? 4.0 + (double)total_q * Hq * d * 8.0 * n / 5.0e6 : 0.0);
+    if (n == 1 || us < best * 0.97) {
+      best = us;
+      n_best = n;
+    }
+  }
+  return n_best;
+}
+
+int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const attn_bf16_t* vcache, void* o, float* lse,
+                       const int* page_table, const int* cu_seqlens_q, const int* kv_lens, int B, int Hq, int Hkv,
+                       int total_q, int max_sq, int max_pages, int page_size, int num_pages, int d, int causal,
+                       int window, int n_sink, float scale, int n_splits, int min_rows_per_split, float* part_o,
+                       float* part_lse, int o_dtype, attn_stream_t stream) {
+  int rc = check_heads(B, Hq, Hkv);
+  if (rc != ATTN_OK) return rc;
+  if (total_q < 0 || max_sq < 0 || window < 0 || n_sink < 0 || !ok_scale(scale)) return ATTN_ERR_INVALID_ARG;
+  if (n_splits < 1 || n_splits > 1024 || min_rows_per_split < 0) return ATTN_ERR_INVALID_ARG;
+  if (window > 0 && !causal) return ATTN_ERR_INVALID_ARG;
+  if (!ok_dim(d) || (o_dtype != ATTN_F32 && o_dtype != ATTN_BF16)) return ATTN_ERR_UNSUPPORTED;
+  if (window > 0 && n_splits > 1) return ATTN_ERR_UNSUPPORTED;
+  rc = check_cache(page_table, B, max_pages, page_size, num_pages);
+  if (rc != ATTN_OK) return rc;
+  if (B == 0 || total_q == 0 || max_sq == 0) return ATTN_OK;
+  if (!ok16(q) || !ok16(kcache) || !ok16(vcache) || !ok16(o) || !ok16(lse) || !ok4(cu_seqlens_q) || !ok4(kv_lens) ||
+      !ok4(page_table))
+    return ATTN_ERR_INVALID_ARG;
+  if (n_splits > 1 && (!ok16(part_o) || !ok4(part_lse))) return ATTN_ERR_INVALID_ARG;
+  if ((long long)total_q * Hq >= (1LL << 31) || (long long)max_sq * (Hq / Hkv) >= (1LL << 30))
+    return ATTN_ERR_INVALID_ARG;
+  attn::PrefillArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.o = o;
+  a.lse = lse;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.Sq = max_sq; a.Skv = max_pages * page_size; a.d = d;
+  a.causal = causal ? 1 : 0;
+  a.o_bf16 = o_dtype == ATTN_BF16 ? 1 : 0;
+  a.scale = scale;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.cu_q = cu_seqlens_q;
+  a.kv_lens = kv_lens;
+  a.total_q = total_q;
+  a.pack = pack_heads(Hq / Hkv, attn::kPrefillTileM);
+  a.n_splits = n_splits;
+  a.split_min = min_rows_per_split;
+  a.part_o = part_o;
+  a.part_lse = part_lse;
+  // every sequence's rows fit one tile: the other tile takes half of the keys
+  a.halves = (window == 0 && d <= 128 && max_sq <= attn::kPrefillTileM / a.pack) ? 1 : 0;
+  a.kv = cache(kcache, vcache, page_table, max_pages, page_size, num_pages);
+  a.err = attn::device_err_word();
+  if (a.err == nullptr) return ATTN_ERR_CUDA;
+  rc = attn::encode_q_map(&a.tm_q, q, d, a.pack, Hq, total_q, 1, attn::kPrefillTileM);
+  a.o_tma = (o_dtype == ATTN_BF16 && n_splits <= 1) ? 1 : 0;
+  if (rc == ATTN_OK && a.o_tma) rc = attn::encode_q_map(&a.tm_o, o, d, a.pack, Hq, total_q, 1, attn::kPrefillTileM);
+  if (rc != ATTN_OK) return rc;
+  rc = from_cuda(attn::launch_prefill_paged(a, stream_of(stream)));
+  if (rc != ATTN_OK || n_splits == 1) return rc;
+  attn::MergeArgs m;
+  m.part_o = part_o; m.part_lse = part_lse; m.o = o; m.lse = lse;
+  m.B = total_q; m.Hq = Hq; m.n_splits = n_splits; m.d = d; m.o_bf16 = a.o_bf16;
+  m.lse_by_head = 1;
+  m.cu_q = cu_seqlens_q;
+  m.n_seq = B;
+  return from_cuda(attn::launch_merge(m, stream_of(stream)));
+}
+
+int attn_decode_paged_splits(int B, int Hkv, int max_kv, int* min_rows) {
+  if (B < 0 || Hkv < 1 || max_kv < 0 || min_rows == nullptr) return ATTN_ERR_INVALID_ARG;
+  const long long units = std::max(1LL, (long long)B * Hkv);
+  long long rows = std::max(128LL, (long long)max_kv * units / (16 * kSms));
+  rows = (rows + 63) / 64 * 64;
+  long long n = std::max(1LL, (max_kv + rows - 1) / rows);
+  if (n > 64) {
+    n = 64;
+    rows = ((max_kv + n - 1) / n + 63) / 64 * 64;
+  }
+  *min_rows = (int)rows;
+  return (int)n;
+}
+
+int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const attn_bf16_t* vcache,
+                      const int* page_table, const int* kv_lens, int B, int Hq, int Hkv, int d, int max_pages,
+                      int page_size, int num_pages, float scale, int n_splits, int min_rows_per_split, float* part_o,
+                      float* part_lse, void* o, float* lse, int o_dtype, unsigned int* counters,
+                      attn_stream_t stream) {
+  int rc = check_heads(B, Hq, Hkv);
+  if (rc == ATTN_OK) rc = check_cache(page_table, B, max_pages, page_size, num_pages);
+  if (rc == ATTN_OK)
+    // (the dense cache's row limit does not apply: max_kv = 1 here)
+    rc = attn::check_decode_split_args(q, kcache, vcache, kv_lens, B, Hq, Hkv, d, 1, scale, n_splits,
+                                       min_rows_per_split, part_o, part_lse, true);
+  if (rc == ATTN_OK) rc = attn::check_merge_args(part_o, part_lse, o, lse, B, Hq, n_splits, d, o_dtype, true);
+  if (rc != ATTN_OK || B == 0) return rc;
+  if (!ok4(counters) || !ok4(page_table)) return ATTN_ERR_INVALID_ARG;
+  attn::DecodeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q; a.kv_lens = kv_lens; a.part_o = part_o; a.part_lse = part_lse;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.d = d; a.max_kv = max_pages * page_size;
+  a.n_splits = n_splits; a.min_rows = min_rows_per_split; a.scale = scale;
+  a.done = counters; a.o = o; a.lse = lse; a.o_bf16 = o_dtype == ATTN_BF16 ? 1 : 0;
+  a.kv = cache(kcache, vcache, page_table, max_pages, page_size, num_pages);
+  a.err = attn::device_err_word();
+  if (a.err == nullptr) return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_decode_paged(a, stream_of(stream)));
+}
+
+int attn_key_weights(const attn_bf16_t* q, const float* lse, const attn_bf16_t* kcache, const int* page_table,
+                     const int* cu_seqlens_q, const int* kv_lens, float* weights, long long w_stride, int B, int Hq,
+                     int Hkv, int total_q, int max_sq, int d, int max_pages, int page_size, int num_pages, int causal,
+                     int window, int n_sink, float scale, int accumulate, attn_stream_t stream) {
+  int rc = check_heads(B, Hq, Hkv);
+  if (rc != ATTN_OK) return rc;
+  if (total_q < 0 || max_sq < 0 || window < 0 || n_sink < 0 || !ok_scale(scale)) return ATTN_ERR_INVALID_ARG;
+  if (window > 0 && !causal) return ATTN_ERR_INVALID_ARG;
+  if (cu_seqlens_q == nullptr && (total_q != B || max_sq != 1)) return ATTN_ERR_INVALID_ARG;
+  if (!ok_dim(d)) return ATTN_ERR_UNSUPPORTED;
+  rc = check_cache(page_table, B, max_pages, page_size, num_pages);
+  if (rc != ATTN_OK) return rc;
+  if (w_stride < (long long)max_pages * page_size) return ATTN_ERR_INVALID_ARG;
+  if (B == 0) return ATTN_OK;
+  if (!ok16(kcache) || !ok4(kv_lens) || !ok4(weights) || !aligned(cu_seqlens_q, 4)) return ATTN_ERR_INVALID_ARG;
+  if (total_q == 0) max_sq = 0;  // no rows: the sums are zero (or stay, if accumulated)
+  else if (!ok16(q) || !ok4(lse)) return ATTN_ERR_INVALID_ARG;
+  if ( (long long)total_q * Hq >= (1LL << 31) || (long long)max_sq * (Hq / Hkv) >= (1LL << 30))
+    return ATTN_ERR_INVALID_ARG;
+  attn::KeyWeightArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q; a.lse = lse;
+  a.lse_hs = cu_seqlens_q ? total_q : 1;  // [Hq][total_q], or the decode's [B][Hq]
+  a.lse_ts = cu_seqlens_q ? 1 : Hq;
+  a.kv = cache(kcache, nullptr, page_table, max_pages, page_size, num_pages);
+  a.cu_q = cu_seqlens_q; a.kv_lens = kv_lens;
+  a.weights = weights; a.w_stride = w_stride;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.total_q = total_q; a.max_sq = max_sq; a.d = d;
+  a.causal = causal ? 1 : 0; a.window = window; a.n_sink = n_sink; a.accumulate = accumulate ? 1 : 0;
+  a.scale = scale;
+  a.err = attn::device_err_word();
+  if (a.err == nullptr) return ATTN_ERR_CUDA;
+  if (!attn::key_weights_few_rows(max_sq, Hq / Hkv)) {
+    const int rows = attn::key_weights_q_rows(d);
+    a.pack = pack_heads(Hq / Hkv, rows);
+    rc = attn::encode_q_map(&a.tm_q, q, d, a.pack, Hq, total_q, 1, rows);
+    if (rc != ATTN_OK) return rc;
+  }
+  return from_cuda(attn::launch_key_weights(a, stream_of(stream)));
+}
+
+int attn_evict(const float* weights, float* weights_out, long long w_stride, attn_bf16_t* kcache, attn_bf16_t* vcache,
+               const int* page_table, const int* kv_lens, int B, int Hkv, int d, int max_pages, int page_size,
+               int num_pages, int budget, int n_recent, int n_sink, attn_bf16_t* k_dst, attn_bf16_t* v_dst,
+               const int* dst_table, int dst_max_pages, int dst_page_size, int dst_num_pages, int* kept, int* new_lens,
+               attn_stream_t stream) {
+  int rc = check_heads(B, Hkv, Hkv);
+  if (rc != ATTN_OK) return rc;
+  if (budget < 1 || n_recent < 0 || n_sink < 0 || (long long)n_recent + n_sink > budget) return ATTN_ERR_INVALID_ARG;
+  if (!ok_dim(d)) return ATTN_ERR_UNSUPPORTED;
+  rc = check_cache(page_table, B, max_pages, page_size, num_pages);
+  if (rc != ATTN_OK) return rc;
+  const long long cap = (long long)max_pages * page_size;
+  if (w_stride < cap) return ATTN_ERR_INVALID_ARG;
+  const bool in_place = k_dst == nullptr;
+  if (in_place != (v_dst == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!in_place) {
+    rc = check_cache(dst_table, B, dst_max_pages, dst_page_size, dst_num_pages);
+    if (rc != ATTN_OK) return rc;
+    if ((long long)dst_max_pages * dst_page_size < (budget < cap ? budget : cap)) return ATTN_ERR_INVALID_ARG;
+    // a destination that is the source itself is the in-place form, called as such
+    if (k_dst == kcache && v_dst == vcache && dst_table == page_table) return ATTN_ERR_INVALID_ARG;
+  }
+  if ((long long)B * Hkv > 0x7FFFFFFFLL) return ATTN_ERR_INVALID_ARG;
+  if (B == 0) return ATTN_OK;
+  if (!ok4(weights) || !aligned(weights_out, 4) || !ok16(kcache) || !ok16(vcache) || !ok4(kv_lens) || !ok4(kept) ||
+      !ok4(new_lens) || !aligned(k_dst, 16) || !aligned(v_dst, 16))
+    return ATTN_ERR_INVALID_ARG;
+  attn::EvictArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.weights = weights; a.weights_out = weights_out; a.w_stride = w_stride;
+  a.src = cache(kcache, vcache, page_table, max_pages, page_size, num_pages);
+  a.in_place = in_place ? 1 : 0;
+  if (in_place) {
+    a.dst = a.src;
+    a.dk = kcache; a.dv = vcache;
+  } else {
+    a.dst = cache(k_dst, v_dst, dst_table, dst_max_pages, dst_page_size, dst_num_pages);
+    a.dk = k_dst; a.dv = v_dst;
+  }
+  a.kv_lens = kv_lens; a.new_lens = new_lens; a.kept = kept;
+  a.B = B; a.Hkv = Hkv; a.d = d; a.budget = budget; a.n_recent = n_recent; a.n_sink = n_sink;
+  a.err = attn::device_err_word();
+  if (a.err == nullptr) return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_evict(a, stream_of(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,153 @@
+// rope.cu -- rotary positions of a batch's new tokens and the append of their keys and
+// values to the cache, in one pass over the projections' outputs.
+//
+// For token t with position p and rotated pair i (frequency f_i, radians per position):
+//   (x1, x2) -> amp * (x1 cos(p f_i) - x2 sin(p f_i), x1 sin(p f_i) + x2 cos(p f_i)),
+// pairs (i, i + rot/2) in the half layout, (2i, 2i + 1) in the interleaved one; the head's
+// dims past rot_dim pass through.  Every 16-byte chunk is read once and written once, so
+// HBM bounds long batches and the launch bounds short ones.
+//
+// Angles.  p f_i in fp32 is off by 0.06 radians at p = 10^6, so the angle is kept as a
+// fraction of a turn in 64-bit fixed point: f_i / 2 pi is taken to 2^-64 turns once per
+// CTA (in fp64: its relative error 2^-52 is the one that is left), and the product with
+// the 32-bit position wraps modulo one turn by itself, exactly.  The top 32 bits go to
+// sincospi as a signed half turn (2^-25 of it rounded away).  fp64 per token instead would
+// cost the few fp64 lanes of this GPU about as long as the copy itself.
+#include <cmath>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+
+// rotates the pairs (a.e, b.e) of two 16-byte chunks (half layout: b is the partner chunk)
+__device__ __forceinline__ void rotate_half(uint4& a, uint4& b, const float2* cs) {
+  uint32_t* pa = reinterpret_cast<uint32_t*>(&a);
+  uint32_t* pb = reinterpret_cast<uint32_t*>(&b);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
+    const float x0 = lo_f(pa[e]), x1 = hi_f(pa[e]), y0 = lo_f(pb[e]), y1 = hi_f(pb[e]);
+    pa[e] = pack_bf16x2(x0 * c0.x - y0 * c0.y, x1 * c1.x - y1 * c1.y);
+    pb[e] = pack_bf16x2(x0 * c0.y + y0 * c0.x, x1 * c1.y + y1 * c1.x);
+  }
+}
+// rotates the four pairs inside one chunk (interleaved layout)
+__device__ __forceinline__ void rotate_inter(uint4& a, const float2* cs) {
+  uint32_t* pa = reinterpret_cast<uint32_t*>(&a);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 c = cs[e];
+    const float x = lo_f(pa[e]), y = hi_f(pa[e]);
+    pa[e] = pack_bf16x2(x * c.x - y * c.y, x * c.y + y * c.x);
+  }
+}
+
+// One CTA takes `tokens` consecutive tokens.  A work item is two chunks of one head: the
+// two partners of the half layout, or two neighbours.  rot = 0 copies.
+template <bool INTER>
+__global__ void __launch_bounds__(kThreads)
+    rope_append_kernel(const RopeArgs a, int tokens) {
+  __shared__ unsigned long long turn[128];  // f_i / 2 pi, units of 2^-64 turns
+  __shared__ float2 cs[128];                // (cos, sin) * amp of the token's pairs
+  __shared__ int where[2];                  // cache row of the token (-1: none), its sequence's end
+  const int half = a.rot / 2;
+  for (int i = threadIdx.x; i < half; i += kThreads) {
+    const double x = a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+    turn[i] = (unsigned long long)((x - floor(x)) * 18446744073709551616.0);
+  }
+  const int cpr = a.d / 8, rc = a.rot / 8;  // chunks of a head, rotated ones (rot % 16 == 0)
+  const int n_q = a.q ? a.Hq : 0;
+  const int ipr = cpr / 2;  // items of a head
+  const int items = (n_q + 2 * a.Hkv) * ipr;
+  const int t_end = min(a.total, (int)(blockIdx.x + 1) * tokens);
+  for (int t = blockIdx.x * tokens; t < t_end; ++t) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      // the token's sequence: the last b with cu[b] <= t (cu is non-decreasing)
+      int b = t, i = 0, n = 1;
+      bool live = t < a.B;
+      if (a.cu_q) {
+        int lo = 0, hi = a.B;  // cu[lo] <= t < cu[hi] (or t behind the last sequence)
+        live = t >= a.cu_q[0] && t < a.cu_q[a.B];
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
+        }
+        b = lo;
+        i = t - a.cu_q[b];
+        n = a.cu_q[b + 1] - a.cu_q[b];
+      }
+      int row = -2;  // behind the last sequence: the token's rows are left as they are
+      if (live) {
+        const long long cap = (long long)a.kv.max_pages * a.kv.page_size;
+        const long long j = (long long)a.kv_lens[b] - n + i;  // key index
+        if (j < 0 || j >= cap) {
+          atomicCAS(a.err, kErrNone, kErrBadShape);
+          row = -1;
+        } else {
+          row = paged_row(a.kv, b, (int)j, a.err);
+        }
+        where[1] = a.positions ? a.positions[t] : (int)j;
+      }
+      where[0] = row;
+    }
+    __syncthreads();
+    const int row = where[0];
+    if (row == -2) continue;
+    const long long pos = where[1];
+    for (int i = threadIdx.x; i < half; i += kThreads) {
+      const unsigned long long w = turn[i] * (unsigned long long)pos;
+      const float x = (float)(int)(w >> 32) * 4.656612873077393e-10f;  // half turns in [-1, 1): 2^-31
+      float s, c;
+      sincospif(x, &s, &c);
+      cs[i] = make_float2(c * a.amp, s * a.amp);
+    }
+    __syncthreads();
+    for (int it = threadIdx.x; it < items; it += kThreads) {
+      const int h = it / ipr, x = it - h * ipr;
+      const bool is_q = h < n_q, is_k = !is_q && h < n_q + a.Hkv;
+      const int hk = is_q ? 0 : (is_k ? h - n_q : h - n_q - a.Hkv);
+      if (!is_q && row < 0) continue;  // no place in the cache
+      const uint16_t* src = is_q ? a.q + (size_t)t * a.q_stride + (size_t)h * a.d
+                                 : (is_k ? a.k + (size_t)t * a.k_stride + (size_t)hk * a.d
+                                         : a.v + (size_t)t * a.v_stride + (size_t)hk * a.d);
+      uint16_t* dst = is_q ? a.q_out + ((size_t)t * a.Hq + h) * a.d
+                           : (is_k ? a.kc : a.vc) + ((size_t)row * a.Hkv + hk) * a.d;
+      // the item's chunks: rotated partners (c, c + rc/2) first, then the rest two by two
+      int c0, c1;
+      if (!INTER && x < rc / 2) { c0 = x; c1 = x + rc / 2; }
+      else { c0 = 2 * x; c1 = 2 * x + 1; }
+      uint4 u0 = *reinterpret_cast<const uint4*>(src + c0 * 8), u1 = *reinterpret_cast<const uint4*>(src + c1 * 8);
+      if (is_q || is_k) {
+        if (INTER) {
+          if (c0 < rc) rotate_inter(u0, cs + c0 * 4);
+          if (c1 < rc) rotate_inter(u1, cs + c1 * 4);
+        } else if (x < rc / 2) {
+          rotate_half(u0, u1, cs + c0 * 8);
+        }
+      }
+      *reinterpret_cast<uint4*>(dst + c0 * 8) = u0;
+      *reinterpret_cast<uint4*>(dst + c1 * 8) = u1;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream) {
+  const int tokens = 1;
+  const unsigned grid = (unsigned)((a.total + tokens - 1) / tokens);
+  if (a.interleaved) rope_append_kernel<true><<<grid, kThreads, 0, stream>>>(a, tokens);
+  else rope_append_kernel<false><<<grid, kThreads, 0, stream>>>(a, tokens);
+  return cudaGetLastError();
+}
+
+}  // namespace attn

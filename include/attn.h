@@ -55,7 +55,7 @@ typedef struct CUstream_st* attn_stream_t; /* == cudaStream_t */
 #define ATTN_ERR_CUDA (-3)           /* a CUDA runtime/driver call or a launch failed */
 #define ATTN_ERR_DEVICE_TIMEOUT (-4) /* a kernel's bounded wait ran out (attn_sync_check only) */
 #define ATTN_ERR_SCRATCH_TOO_SMALL (-5) /* attn_decode_noalloc: problem exceeds the static scratch */
-#define ATTN_ERR_DEVICE_INPUT (-6)   /* a kernel found device-side inputs changed under it (attn_sync_check only) */
+#define ATTN_ERR_DEVICE_INPUT (-6)   /* a kernel found a device-side input wrong or changed under it (attn_sync_check only) */
 
 /* output dtype codes */
 #define ATTN_F32 0
@@ -385,11 +385,162 @@ int attn_decode_noalloc(const attn_bf16_t* q, const attn_bf16_t* kcache, const a
 unsigned long long attn_decode_noalloc_scratch_bytes(void);
 
 /*
+ * Serving calls over a paged cache
+ * --------------------------------
+ * (The pages have no counterpart: these are the calls a serving loop makes before,
+ * between and after the attention above.)
+ *
+ * A cache is a pair of pools, bf16 [num_pages][page_size][Hkv][d], and a table int32
+ * [B][max_pages] (device): key j of sequence b lies in slot j % page_size of page
+ * page_table[b][j / page_size].  page_size is any number >= 1; max_pages * page_size <=
+ * 2^30, num_pages * page_size < 2^31; kv_lens[b] is clamped to [0, max_pages * page_size].
+ * Table entries past a sequence's keys are never read (-1, say, is fine there), nor are
+ * slots past them as data: they may hold anything, NaN too.  An entry in use that is no
+ * page of the pool is reported as ATTN_ERR_DEVICE_INPUT by attn_sync_check; its rows read
+ * as zeros and are not written.  Rows below kv_lens must be finite even where a mask hides
+ * them (a weight of zero times NaN is NaN on the tensor cores).
+ * Where page_table may be NULL, NULL means the dense cache [B][max_kv][Hkv][d] of the
+ * calls above: max_pages = 1, page_size = max_kv, num_pages >= B.
+ * cu_seqlens_q [B+1] (device) is clamped to [0, total]; tokens behind the last sequence are
+ * neither read nor written.
+ * All of these calls can be captured into a CUDA graph (nothing is allocated, looked up by
+ * shape or synchronised), after one call of the library on that device.
+ */
+
+/*
+ * attn_rope_append -- rotary positions of the new tokens, and their keys and values into
+ * the cache.
+ *
+ * Sequence b has Sq_b = cu_seqlens_q[b+1] - cu_seqlens_q[b] new tokens (cu_seqlens_q ==
+ * NULL: one each, total == B) and kv_lens[b] keys with them: token i is key
+ * kv_lens[b] - Sq_b + i.  With p its position and a = p * inv_freq[m], pair m of each head
+ * of q and k becomes
+ *   (x1 cos a - x2 sin a, x1 sin a + x2 cos a) * amp,
+ * x1, x2 at m and m + rot_dim/2, or (interleaved) at 2m and 2m + 1; dims from rot_dim on
+ * are copied.  Angles are exact to 2^-31 of a turn at any position (64-bit fixed point).
+ * q_out gets the rotated queries, the cache the rotated keys and the values.
+ *
+ * Arguments
+ *   q, k, v      bf16, token t's heads [Hq][d] / [Hkv][d] at t * stride elements; strides
+ *                at least the heads' width and multiples of 8 (views of one projection's
+ *                output).  q == q_out == NULL: keys and values only
+ *   positions    int32 [total] (device, may be negative) or NULL: the key index
+ *   inv_freq     fp64 [rot_dim/2] (device), radians per position; unused for rot_dim 0
+ *   q_out        bf16 [total][Hq][d]; may be q if q's stride is Hq * d
+ *   rot_dim      0 (append only), 16, 32, .. d;  d in {64, 128, 256};  amp finite
+ * A token whose key index is negative or past the table's capacity is not stored, and
+ * reported as ATTN_ERR_DEVICE_INPUT by attn_sync_check (its query is still rotated).
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
+ */
+int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16_t* v, long long q_stride,
+                     long long k_stride, long long v_stride, const int* positions, const double* inv_freq,
+                     attn_bf16_t* q_out, attn_bf16_t* kcache, attn_bf16_t* vcache, const int* page_table,
+                     const int* cu_seqlens_q, const int* kv_lens, int B, int Hq, int Hkv, int total, int d,
+                     int rot_dim, int interleaved, float amp, int max_pages, int page_size, int num_pages,
+                     attn_stream_t stream);
+
+/*
+ * attn_prefill_paged -- attn_prefill_varlen over a paged cache (window = 0), or
+ * attn_prefill_varlen_window (window >= 1, causal).
+ *
+ * Any Hq / Hkv: the query heads of a KV head share the rows of the MMA tiles, so each
+ * K/V row is gathered once per group.  n_splits > 1 (window = 0 only) cuts each sequence's
+ * keys as attn_decode_split does, each split's rows rounded up to 128, and joins the
+ * partials part_o fp32 [total_q][Hq][n_splits][d], part_lse fp32 [total_q][Hq][n_splits]
+ * in a second launch; with n_splits = 1 they may be NULL.
+ *
+ * Arguments: as attn_prefill_varlen, with page_table int32 [B][max_pages]; d in
+ * {64, 128, 256}; max_sq * Hq / Hkv < 2^30.
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
+ */
+int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const attn_bf16_t* vcache, void* o, float* lse,
+                       const int* page_table, const int* cu_seqlens_q, const int* kv_lens, int B, int Hq, int Hkv,
+                       int total_q, int max_sq, int max_pages, int page_size, int num_pages, int d, int causal,
+                       int window, int n_sink, float scale, int n_splits, int min_rows_per_split, float* part_o,
+                       float* part_lse, int o_dtype, attn_stream_t stream);
+
+/* The n_splits (>= 1) that suits a prefill of these sizes, max_kv keys in the longest
+ * sequence (host only); ATTN_ERR_INVALID_ARG for bad sizes. */
+int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, int max_kv, int d);
+
+/*
+ * attn_decode_paged -- attn_decode over a paged cache: one launch, the same split rule,
+ * partials, counters and results.
+ *
+ * Arguments: as attn_decode, with page_table int32 [B][max_pages] and pools
+ * [num_pages][page_size][Hkv][d] in place of the caches and max_kv.
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
+ */
+int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const attn_bf16_t* vcache,
+                      const int* page_table, const int* kv_lens, int B, int Hq, int Hkv, int d, int max_pages,
+                      int page_size, int num_pages, float scale, int n_splits, int min_rows_per_split, float* part_o,
+                      float* part_lse, void* o, float* lse, int o_dtype, unsigned int* counters,
+                      attn_stream_t stream);
+
+/* The n_splits (>= 1) and min_rows_per_split that suit a decode of these sizes, max_kv
+ * keys in the longest sequence (host only); ATTN_ERR_INVALID_ARG for bad sizes. */
+int attn_decode_paged_splits(int B, int Hkv, int max_kv, int* min_rows_per_split);
+
+/*
+ * attn_key_weights -- the attention weight that every cached key received.
+ *
+ *   W[b,hk,j] = sum over the new rows i of sequence b and the heads h of hk's group of
+ *               exp(scale * q[i,h] . k[j,hk] - lse[i,h]),
+ * over the (i, j) that the attention call admitted; rows with lse = -inf add nothing.
+ * weights[b][hk][j] becomes weights + W (accumulate != 0) or W, for j < kv_lens[b]; other
+ * entries stay as they are.  Sums are fp32, in a fixed order: the same inputs give the same
+ * bits.
+ *
+ * Arguments
+ *   q, lse       an attention call's queries and log-sum-exps: with cu_seqlens_q, q bf16
+ *                [total_q][Hq][d], lse fp32 [Hq][total_q]; with cu_seqlens_q == NULL (one row
+ *                per sequence: total_q = B, max_sq = 1), lse [B][Hq]
+ *   weights      fp32 [B][Hkv][w_stride], w_stride >= max_pages * page_size
+ *   page_table   may be NULL (dense cache);  d in {64, 128, 256}
+ *   causal, window, n_sink, scale   as in the attention call (window = 0: none)
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
+ */
+int attn_key_weights(const attn_bf16_t* q, const float* lse, const attn_bf16_t* kcache, const int* page_table,
+                     const int* cu_seqlens_q, const int* kv_lens, float* weights, long long w_stride, int B, int Hq,
+                     int Hkv, int total_q, int max_sq, int d, int max_pages, int page_size, int num_pages, int causal,
+                     int window, int n_sink, float scale, int accumulate, attn_stream_t stream);
+
+/*
+ * attn_evict -- shrink every sequence to at most `budget` keys per KV head, by weight.
+ *
+ * A sequence of at most budget keys keeps them all.  Otherwise each KV head keeps the first
+ * n_sink keys, the last n_recent, and of those between the budget - n_sink - n_recent with
+ * the largest weights (equal weights: the lowest index; -0 equals +0, NaN is above
+ * everything).  The kept keys, in order, become keys 0 .. n-1, n = min(kv_lens[b], budget):
+ * their K and V rows and (weights_out != NULL) weights move there, and weights_out[n ..
+ * kv_lens[b]) becomes 0.  Rotated keys keep the positions they were rotated to; pass
+ * attn_rope_append positions from then on.
+ *   k_dst == v_dst == NULL: in place.  No page may belong to two sequences, and
+ *       weights_out may be weights.
+ *   else into the pools k_dst / v_dst through dst_table (or dense, NULL), which must not
+ *       overlap what is read; the source stays as it is.
+ *
+ * Arguments
+ *   weights, weights_out  fp32 [B][Hkv][w_stride], w_stride >= max_pages * page_size
+ *   budget       >= 1;  n_recent, n_sink >= 0, n_recent + n_sink <= budget
+ *   kept         int32 [B][Hkv][budget]: old index of each key, -1 from n on
+ *   new_lens     int32 [B]: n; may be kv_lens
+ *   page_table   may be NULL (dense cache);  d in {64, 128, 256}
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
+ */
+int attn_evict(const float* weights, float* weights_out, long long w_stride, attn_bf16_t* kcache, attn_bf16_t* vcache,
+               const int* page_table, const int* kv_lens, int B, int Hkv, int d, int max_pages, int page_size,
+               int num_pages, int budget, int n_recent, int n_sink, attn_bf16_t* k_dst, attn_bf16_t* v_dst,
+               const int* dst_table, int dst_max_pages, int dst_page_size, int dst_num_pages, int* kept, int* new_lens,
+               attn_stream_t stream);
+
+/*
  * attn_sync_check -- synchronise `stream`, then read and clear this device's
  * error word.  Returns ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT (a kernel's bounded
  * wait gave up; that kernel's outputs are invalid), ATTN_ERR_DEVICE_INPUT (a
  * kernel found a device-side input inconsistent with its launch, e.g. kv_lens
- * changed while attn_decode_split ran; that call's outputs are invalid) or
+ * changed while attn_decode_split ran, or a page-table entry in use that is no page of the
+ * pool; that call's outputs are invalid) or
  * ATTN_ERR_CUDA.  The first error recorded since the last check is reported.
  */
 int attn_sync_check(attn_stream_t stream);
