@@ -39,6 +39,8 @@ class AttnError(RuntimeError):
 def load(path: str | None = None):
     """Load libattn.so (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -73,7 +75,7 @@ def load(path: str | None = None):
         lib.attn_prefill_paged.argtypes = [vp] * 8 + [i] * 12 + [f, i, i, vp, vp, i, vp]
         lib.attn_prefill_paged_splits.argtypes = [i] * 7
         lib.attn_decode_paged.argtypes = [vp] * 5 + [i] * 7 + [f, i, i, vp, vp, vp, vp, i, vp, vp]
-        lib.attn_decode_paged_splits.argtypes = [i] * 3 + [vp]
+        lib.attn_decode_paged_splits.argtypes = [i] * 5 + [vp]
         lib.attn_key_weights.argtypes = [vp] * 7 + [ll] + [i] * 12 + [f, i, vp]
         lib.attn_evict.argtypes = [vp, vp, ll] + [vp] * 4 + [i] * 9 + [vp] * 3 + [i] * 3 + [vp] * 3
         for name in ("attn_rope_append", "attn_prefill_paged", "attn_prefill_paged_splits", "attn_decode_paged",

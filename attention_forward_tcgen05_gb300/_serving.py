@@ -36,8 +36,8 @@ def attn_decode_paged(*args) -> int:
     return load().attn_decode_paged(*args)
 
 
-def attn_decode_paged_splits(B, Hkv, max_kv, min_rows) -> int:
-    return load().attn_decode_paged_splits(B, Hkv, max_kv, min_rows)
+def attn_decode_paged_splits(B, Hq, Hkv, max_kv, d, min_rows) -> int:
+    return load().attn_decode_paged_splits(B, Hq, Hkv, max_kv, d, min_rows)
 
 
 def attn_key_weights(*args) -> int:
@@ -49,120 +49,104 @@ def attn_evict(*args) -> int:
 
 
 # ------------------------------------------------------------------ argument checks
-class _Call:
-    """The device of a call (every tensor lies on it) and the stream it goes to."""
+# A decode step makes these calls many times over on a few microseconds of GPU work, so the
+# checks are kept short: one pass over a tensor's attributes, device and stream as integers.
+def _device(lead, name):
+    try:
+        dev = lead.get_device()
+    except AttributeError:
+        dev = -1
+    if dev < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return dev
 
-    def __init__(self, lead, name, stream):
-        torch = _torch()
-        if not isinstance(lead, torch.Tensor) or not lead.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        self.device = lead.device
-        self.stream = stream
-        current = torch.cuda.current_device()
-        self._guard = None if self.device.index == current else torch.cuda.device(self.device)
-        if self._guard is not None:
-            self._guard.__enter__()
-        try:
-            own = torch.cuda.current_stream()
-            if stream is not None and stream.device != self.device:
-                raise ValueError("the stream belongs to another device than the tensors")
-            self.handle = (stream or own).cuda_stream
-            self._foreign = stream is not None and stream.cuda_stream != own.cuda_stream
-        except BaseException:
-            self.close()
-            raise
 
-    def close(self):
-        if self._guard is not None:
-            self._guard.__exit__(None, None, None)
+def _elsewhere(call, lead, stream):
+    """``call()`` with the tensors' device and the given stream current: outputs and
+    workspaces then belong to that stream, and the outputs are marked as used by the
+    caller's."""
+    torch = _torch()
+    if stream is not None and stream.device != lead.device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    with torch.cuda.device(lead.device):
+        own = torch.cuda.current_stream()
+        if stream is None or stream == own:
+            return call()
+        with torch.cuda.stream(stream):
+            result = call()
+        for t in result if isinstance(result, tuple) else (result,):
+            if t is not None:
+                t.record_stream(own)
+        return result
 
-    def __enter__(self):
-        return self
 
-    def __exit__(self, *exc):
-        self.close()
+def _need(t, name, dtype, ndim, dev, contiguous=True):
+    """The tensor's pointer; raises unless it is what the call reads or writes."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.dim() == ndim and (not contiguous or t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda or t.get_device() != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on device {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}{ndim}-D tensor")
 
-    def check(self, t, name, dtype, ndim, contiguous=True):
-        if not isinstance(t, _torch().Tensor) or t.device != self.device:
-            raise TypeError(f"{name} must be a CUDA tensor on {self.device}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.dim() != ndim or (contiguous and not t.is_contiguous()):
-            raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}{ndim}-D tensor")
-        return t.data_ptr()
 
-    def shape(self, t, name, *want):
-        if tuple(t.shape) != want:
-            raise ValueError(f"{name} must have shape {list(want)}, got {list(t.shape)}")
+def _sized(t, name, dtype, dev, *want):
+    """A contiguous tensor of exactly that shape: its pointer."""
+    p = _need(t, name, dtype, len(want), dev)
+    if t.shape != want:
+        raise ValueError(f"{name} must have shape {list(want)}, got {list(t.shape)}")
+    return p
 
-    def output(self, t, name, dtype, *want):
-        """An output given by the caller, checked."""
-        p = self.check(t, name, dtype, len(want))
-        self.shape(t, name, *want)
-        return p
 
-    def scratch(self, *shape):
-        """fp32 workspace that lives until the call's work on its stream is done."""
-        t = _torch().empty(shape, dtype=_torch().float32, device=self.device)
-        if self._foreign:
-            t.record_stream(self.stream)
-        return t
-
-    def result(self, shape, dtype):
-        t = _torch().empty(shape, dtype=dtype, device=self.device)
-        if self._foreign:
-            t.record_stream(self.stream)
-        return t
-
-    def cache(self, kcache, vcache, page_table, B, need_table=False):
-        """(k, v, table pointers, Hkv, d, max_pages, page_size, num_pages) of a cache."""
-        bf16 = _torch().bfloat16
-        kp = self.check(kcache, "kcache", bf16, 4)
-        vp = self.check(vcache, "vcache", bf16, 4) if vcache is not None else None
-        n, page, Hkv, d = kcache.shape
-        if vcache is not None and vcache.shape != kcache.shape:
+def _cache(kcache, vcache, page_table, B, dev, need_table=False):
+    """(k, v, table pointers, Hkv, d, max_pages, page_size, num_pages) of a cache."""
+    torch = _torch()
+    kp = _need(kcache, "kcache", torch.bfloat16, 4, dev)
+    n, page, Hkv, d = shape = kcache.shape
+    vp = None
+    if vcache is not None:
+        vp = _need(vcache, "vcache", torch.bfloat16, 4, dev)
+        if vcache.shape != shape:
             raise ValueError("kcache and vcache must have the same shape")
-        if page_table is None:
-            if need_table:
-                raise TypeError("page_table must be a CUDA tensor")
-            if n != B:
-                raise ValueError(f"a dense cache must have one row per sequence: {n} for {B}")
-            return kp, vp, None, Hkv, d, 1, page, n
-        tp = self.check(page_table, "page_table", _torch().int32, 2)
-        if page_table.shape[0] != B:
-            raise ValueError(f"page_table must have one row per sequence: {page_table.shape[0]} for {B}")
-        return kp, vp, tp, Hkv, d, page_table.shape[1], page, n
+    if page_table is None and not need_table:
+        if n != B:
+            raise ValueError(f"a dense cache must have one row per sequence: {n} for {B}")
+        return kp, vp, None, Hkv, d, 1, page, n
+    tp = _need(page_table, "page_table", torch.int32, 2, dev)
+    rows, width = page_table.shape
+    if rows != B:
+        raise ValueError(f"page_table must have one row per sequence: {rows} for {B}")
+    return kp, vp, tp, Hkv, d, width, page, n
 
 
 def _out_code(dtype):
     torch = _torch()
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return ATTN_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return ATTN_F32
     raise TypeError(f"unsupported output dtype {dtype}")
 
 
-def _stream_counters(n, c):
-    """Zeroed completion counters for a decode_paged call on c's stream: a buffer for each
-    stream (its calls are ordered), and one of its own for a call being captured (two graphs
-    may replay at the same time)."""
+def _stream_counters(n, dev, handle):
+    """Zeroed completion counters for a decode_paged call: a buffer for each stream (its
+    calls are ordered), and one of its own for a call being captured (two graphs may replay
+    at the same time).  Returns the tensor."""
     torch = _torch()
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(n, dtype=torch.int32, device=c.device)
-    key = (c.device.type, c.device.index, c.handle)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.zeros(n, dtype=torch.int32, device="cuda")
+    key = ("cuda", dev, handle)
     buf = _counters.get(key)
     if buf is None or buf.numel() < n:
         with _lock:
-            buf = torch.zeros(max(n, 4096), dtype=torch.int32, device=c.device)
-            torch.cuda.synchronize(c.device)  # zeroed before the stream uses it, and no longer in use
+            buf = torch.zeros(max(n, 4096), dtype=torch.int32, device="cuda")
+            torch.cuda.synchronize(dev)  # zeroed before the stream uses it, and no longer in use
             _counters[key] = buf
     return buf
-
-
-def _raise(rc, what):
-    if rc != ATTN_OK:
-        raise AttnError(rc, what)
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -201,14 +185,16 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, device="cuda", factor:
     return f.to(device), amp
 
 
-def _token_rows(c, t, name, total, H, d):
+def _token_rows(t, name, dev, total, H, d):
     """Rows of tokens [total, H, d] with any stride between tokens (a view of a fused
     projection's output, say): (pointer, stride in elements)."""
-    p = c.check(t, name, _torch().bfloat16, 3, contiguous=False)
-    c.shape(t, name, total, H, d)
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+    p = _need(t, name, _torch().bfloat16, 3, dev, contiguous=False)
+    if t.shape != (total, H, d):
+        raise ValueError(f"{name} must have shape {[total, H, d]}, got {list(t.shape)}")
+    row, head, one = t.stride()
+    if one != 1 or (H > 1 and head != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return p, (t.stride(0) if total > 1 else H * d)
+    return p, (row if total > 1 else H * d)
 
 
 def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_seqlens_q=None, positions=None,
@@ -224,38 +210,42 @@ def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_
     Writes kcache / vcache; returns the rotated q [total,Hq,d] (``out`` if given; it may be
     q itself when q is contiguous), or None without q."""
     torch = _torch()
-    with _Call(k, "k", stream) as c:
-        if k.dim() != 3:
-            raise ValueError("k must be a 3-D tensor")
-        total = k.shape[0]
-        np_ = c.check(kv_lens, "kv_lens", torch.int32, 1)
-        B = kv_lens.shape[0]
-        kp, vp, tp, Hkv, d, max_pages, page, n_pages = c.cache(kcache, vcache, page_table, B)
-        kr, ks = _token_rows(c, k, "k", total, Hkv, d)
-        vr, vs = _token_rows(c, v, "v", total, Hkv, d)
-        Hq, qr, qs, op = Hkv, None, 0, None
-        if q is not None:
-            Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
-            qr, qs = _token_rows(c, q, "q", total, Hq, d)
-            if out is None:
-                out = c.result((total, Hq, d), torch.bfloat16)
-            op = c.output(out, "out", torch.bfloat16, total, Hq, d)
-        elif out is not None:
-            raise ValueError("out without q")
-        cu = pos = fr = None
-        if cu_seqlens_q is not None:
-            cu = c.output(cu_seqlens_q, "cu_seqlens_q", torch.int32, B + 1)
-        elif total != B:
-            raise ValueError("without cu_seqlens_q there must be one token per sequence")
-        if positions is not None:
-            pos = c.output(positions, "positions", torch.int32, total)
-        rot = 0
-        if inv_freq is not None:
-            fr = c.check(inv_freq, "inv_freq", torch.float64, 1)
-            rot = 2 * inv_freq.shape[0]
-        _raise(load().attn_rope_append(qr, kr, vr, qs, ks, vs, pos, fr, op, kp, vp, tp, cu, np_, B, Hq, Hkv, total, d,
-                                       rot, int(interleaved), amp, max_pages, page, n_pages, c.handle),
-               "attn_rope_append")
+    dev = _device(k, "k")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table, cu_seqlens_q,
+                                              positions, interleaved, amp, out), k, stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
+    total, B = k.shape[0], kv_lens.shape[0]
+    kp, vp, tp, Hkv, d, max_pages, page, n_pages = _cache(kcache, vcache, page_table, B, dev)
+    kr, ks = _token_rows(k, "k", dev, total, Hkv, d)
+    vr, vs = _token_rows(v, "v", dev, total, Hkv, d)
+    Hq, qr, qs, op = Hkv, None, 0, None
+    if q is not None:
+        Hq = q.shape[1]
+        qr, qs = _token_rows(q, "q", dev, total, Hq, d)
+        if out is None:
+            out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device="cuda")
+            op = out.data_ptr()
+        else:
+            op = _sized(out, "out", torch.bfloat16, dev, total, Hq, d)
+    elif out is not None:
+        raise ValueError("out without q")
+    cu = pos = fr = None
+    if cu_seqlens_q is not None:
+        cu = _sized(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, B + 1)
+    elif total != B:
+        raise ValueError("without cu_seqlens_q there must be one token per sequence")
+    if positions is not None:
+        pos = _sized(positions, "positions", torch.int32, dev, total)
+    rot = 0
+    if inv_freq is not None:
+        fr = _need(inv_freq, "inv_freq", torch.float64, 1, dev)
+        rot = 2 * inv_freq.shape[0]
+    rc = load().attn_rope_append(qr, kr, vr, qs, ks, vs, pos, fr, op, kp, vp, tp, cu, np_, B, Hq, Hkv, total, d, rot,
+                                 int(interleaved), amp, max_pages, page, n_pages, handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope_append")
     return out
 
 
@@ -270,38 +260,54 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
     joined through ``parts``, optional fp32 (part_o [total_q,Hq,n_splits,d], part_lse
     [total_q,Hq,n_splits]).  window > 0 takes no splits."""
     torch = _torch()
-    with _Call(q, "q", stream) as c:
-        qp = c.check(q, "q", torch.bfloat16, 3)
-        np_ = c.check(kv_lens, "kv_lens", torch.int32, 1)
-        B = kv_lens.shape[0]
-        kp, vp, tp, Hkv, d, max_pages, page, n_pages = c.cache(kcache, vcache, page_table, B, need_table=True)
-        total, Hq = q.shape[0], q.shape[1]
-        c.shape(q, "q", total, Hq, d)
-        cu = c.output(cu_seqlens_q, "cu_seqlens_q", torch.int32, B + 1)
-        if scale is None:
-            scale = 1.0 / math.sqrt(d)
-        if out is None:
-            o, lse = c.result((total, Hq, d), out_dtype or torch.bfloat16), c.result((Hq, total), torch.float32)
+    dev = _device(q, "q")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq, causal,
+                                                scale, out_dtype, None, out, window, n_sink, n_splits,
+                                                min_rows_per_split, max_kv, parts), q, stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    qp = _need(q, "q", torch.bfloat16, 3, dev)
+    np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
+    B = kv_lens.shape[0]
+    kp, vp, tp, Hkv, d, max_pages, page, n_pages = _cache(kcache, vcache, page_table, B, dev, need_table=True)
+    total, Hq, dq = q.shape
+    if dq != d:
+        raise ValueError(f"q and the cache differ in head dim: {dq} and {d}")
+    cu = _sized(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, B + 1)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        o = torch.empty((total, Hq, d), dtype=out_dtype or torch.bfloat16, device="cuda")
+        lse = torch.empty((Hq, total), dtype=torch.float32, device="cuda")
+        op, lp = o.data_ptr(), lse.data_ptr()
+    else:
+        o, lse = out
+        op = _sized(o, "out[0]", o.dtype, dev, total, Hq, d)
+        lp = _sized(lse, "out[1]", torch.float32, dev, Hq, total)
+    code = _out_code(o.dtype)
+    lib = load()
+    if n_splits == 0:
+        n_splits = 1
+        if parts is not None:
+            n_splits = parts[0].shape[2]
+        elif not window:
+            n_splits = max(1, lib.attn_prefill_paged_splits(B, Hq, Hkv, total, max_sq,
+                                                            max_pages * page if max_kv is None else max_kv, d))
+    pp = ps = None
+    if n_splits > 1:
+        if parts is None:  # both partials in one allocation
+            rows = total * Hq * n_splits
+            work = torch.empty(rows * (d + 1), dtype=torch.float32, device="cuda")
+            pp = work.data_ptr()
+            ps = pp + rows * d * 4
         else:
-            o, lse = out
-        code = _out_code(o.dtype)
-        op = c.output(o, "out[0]", o.dtype, total, Hq, d)
-        lp = c.output(lse, "out[1]", torch.float32, Hq, total)
-        if n_splits == 0:
-            if window or parts is not None or Hq % Hkv:
-                n_splits = 1 if parts is None else parts[0].shape[2]
-            else:
-                n_splits = max(1, load().attn_prefill_paged_splits(B, Hq, Hkv, total, int(max_sq),
-                                                                   max_pages * page if max_kv is None else max_kv, d))
-        pp = ps = None
-        if n_splits > 1:
-            if parts is None:
-                parts = c.scratch(total, Hq, n_splits, d), c.scratch(total, Hq, n_splits)
-            pp = c.output(parts[0], "parts[0]", torch.float32, total, Hq, n_splits, d)
-            ps = c.output(parts[1], "parts[1]", torch.float32, total, Hq, n_splits)
-        _raise(load().attn_prefill_paged(qp, kp, vp, op, lp, tp, cu, np_, B, Hq, Hkv, total, int(max_sq), max_pages,
-                                         page, n_pages, d, int(causal), window, n_sink, scale, n_splits,
-                                         min_rows_per_split, pp, ps, code, c.handle), "attn_prefill_paged")
+            pp = _sized(parts[0], "parts[0]", torch.float32, dev, total, Hq, n_splits, d)
+            ps = _sized(parts[1], "parts[1]", torch.float32, dev, total, Hq, n_splits)
+    rc = lib.attn_prefill_paged(qp, kp, vp, op, lp, tp, cu, np_, B, Hq, Hkv, total, max_sq, max_pages, page, n_pages,
+                                d, int(causal), window, n_sink, scale, n_splits, min_rows_per_split, pp, ps, code,
+                                handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_prefill_paged")
     return o, lse
 
 
@@ -312,45 +318,65 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
     with page_table.  n_splits = 0 chooses the splits and their least rows from the sizes
     and max_kv (the longest sequence's keys, by default the table's width)."""
     torch = _torch()
-    with _Call(q, "q", stream) as c:
-        qp = c.check(q, "q", torch.bfloat16, 3)
-        np_ = c.check(kv_lens, "kv_lens", torch.int32, 1)
-        B, Hq = q.shape[0], q.shape[1]
-        c.shape(kv_lens, "kv_lens", B)
-        kp, vp, tp, Hkv, d, max_pages, page, n_pages = c.cache(kcache, vcache, page_table, B, need_table=True)
-        c.shape(q, "q", B, Hq, d)
-        if scale is None:
-            scale = 1.0 / math.sqrt(d)
-        if n_splits == 0:
-            if parts is not None:
-                n_splits = parts[0].shape[2]
-            else:
-                rows = ctypes.c_int(1)
-                n_splits = load().attn_decode_paged_splits(B, Hkv, max_pages * page if max_kv is None else max_kv,
-                                                           ctypes.addressof(rows))
-                min_rows_per_split = rows.value
-        if parts is None:
-            parts = c.scratch(B, Hq, n_splits, d), c.scratch(B, Hq, n_splits)
-        pp = c.output(parts[0], "parts[0]", torch.float32, B, Hq, n_splits, d)
-        ps = c.output(parts[1], "parts[1]", torch.float32, B, Hq, n_splits)
-        if out is None:
-            o, lse = c.result((B, Hq, d), out_dtype or torch.bfloat16), c.result((B, Hq), torch.float32)
+    dev = _device(q, "q")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits, min_rows_per_split,
+                                               scale, out_dtype, None, out, parts, counters, max_kv), q, stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    qp = _need(q, "q", torch.bfloat16, 3, dev)
+    B, Hq, dq = q.shape
+    np_ = _sized(kv_lens, "kv_lens", torch.int32, dev, B)
+    kp, vp, tp, Hkv, d, max_pages, page, n_pages = _cache(kcache, vcache, page_table, B, dev, need_table=True)
+    if dq != d:
+        raise ValueError(f"q and the cache differ in head dim: {dq} and {d}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = load()
+    if n_splits == 0:
+        if parts is not None:
+            n_splits = parts[0].shape[2]
         else:
-            o, lse = out
-        code = _out_code(o.dtype)
-        op = c.output(o, "out[0]", o.dtype, B, Hq, d)
-        lp = c.output(lse, "out[1]", torch.float32, B, Hq)
-        if counters is None:
-            counters = _stream_counters(B * Hq, c)
-        elif counters.dtype != torch.int32 or counters.device != c.device or counters.numel() < B * Hq:
-            raise TypeError("counters must be a CUDA int32 tensor of at least B*Hq entries")
-        _raise(load().attn_decode_paged(qp, kp, vp, tp, np_, B, Hq, Hkv, d, max_pages, page, n_pages, scale, n_splits,
-                                        min_rows_per_split, pp, ps, op, lp, code, counters.data_ptr(), c.handle),
-               "attn_decode_paged")
+            rows = ctypes.c_int(1)
+            n_splits = lib.attn_decode_paged_splits(B, Hq, Hkv, max_pages * page if max_kv is None else max_kv, d,
+                                                    ctypes.addressof(rows))
+            min_rows_per_split = rows.value
+    if parts is None:  # both partials in one allocation
+        rows = B * Hq * n_splits
+        work = torch.empty(rows * (d + 1), dtype=torch.float32, device="cuda")
+        pp = work.data_ptr()
+        ps = pp + rows * d * 4
+    else:
+        pp = _sized(parts[0], "parts[0]", torch.float32, dev, B, Hq, n_splits, d)
+        ps = _sized(parts[1], "parts[1]", torch.float32, dev, B, Hq, n_splits)
+    if out is None:
+        o = torch.empty((B, Hq, d), dtype=out_dtype or torch.bfloat16, device="cuda")
+        lse = torch.empty((B, Hq), dtype=torch.float32, device="cuda")
+        op, lp = o.data_ptr(), lse.data_ptr()
+    else:
+        o, lse = out
+        op = _sized(o, "out[0]", o.dtype, dev, B, Hq, d)
+        lp = _sized(lse, "out[1]", torch.float32, dev, B, Hq)
+    code = _out_code(o.dtype)
+    if counters is None:
+        counters = _stream_counters(B * Hq, dev, handle)
+    elif counters.dtype != torch.int32 or counters.get_device() != dev or counters.numel() < B * Hq:
+        raise TypeError("counters must be a CUDA int32 tensor of at least B*Hq entries")
+    rc = lib.attn_decode_paged(qp, kp, vp, tp, np_, B, Hq, Hkv, d, max_pages, page, n_pages, scale, n_splits,
+                               min_rows_per_split, pp, ps, op, lp, code, counters.data_ptr(), handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_paged")
     return o, lse
 
 
 # ------------------------------------------------------------------ weights and eviction
+def _weight_rows(weights, dev, B, Hkv, capacity):
+    p = _need(weights, "weights", _torch().float32, 3, dev)
+    b, h, n = weights.shape
+    if b != B or h != Hkv or n < capacity:
+        raise ValueError(f"weights must be [{B}, {Hkv}, at least {capacity}], got {[b, h, n]}")
+    return p, n
+
+
 def key_weights(q, lse, kcache, kv_lens, weights, page_table=None, cu_seqlens_q=None, max_sq: int = 1,
                 causal: bool = True, window: int = 0, n_sink: int = 0, scale: float | None = None,
                 accumulate: bool = True, stream=None):
@@ -362,30 +388,34 @@ def key_weights(q, lse, kcache, kv_lens, weights, page_table=None, cu_seqlens_q=
     causal, window, n_sink and scale as in that call.  Entries at or past kv_lens[b] stay
     as they are.  Returns weights."""
     torch = _torch()
-    with _Call(q, "q", stream) as c:
-        qp = c.check(q, "q", torch.bfloat16, 3)
-        np_ = c.check(kv_lens, "kv_lens", torch.int32, 1)
-        B = kv_lens.shape[0]
-        kp, _, tp, Hkv, d, max_pages, page, n_pages = c.cache(kcache, None, page_table, B)
-        total, Hq = q.shape[0], q.shape[1]
-        c.shape(q, "q", total, Hq, d)
-        cu = None
-        if cu_seqlens_q is not None:
-            cu = c.output(cu_seqlens_q, "cu_seqlens_q", torch.int32, B + 1)
-            lp = c.output(lse, "lse", torch.float32, Hq, total)
-        else:
-            if total != B:
-                raise ValueError("without cu_seqlens_q there must be one row per sequence")
-            lp = c.output(lse, "lse", torch.float32, B, Hq)
-            max_sq = 1
-        wp = c.check(weights, "weights", torch.float32, 3)
-        if weights.shape[0] != B or weights.shape[1] != Hkv or weights.shape[2] < max_pages * page:
-            raise ValueError(f"weights must be [B, Hkv, at least {max_pages * page}], got {list(weights.shape)}")
-        if scale is None:
-            scale = 1.0 / math.sqrt(d)
-        _raise(load().attn_key_weights(qp, lp, kp, tp, cu, np_, wp, weights.shape[2], B, Hq, Hkv, total, int(max_sq),
-                                       d, max_pages, page, n_pages, int(causal), window, n_sink, scale,
-                                       int(accumulate), c.handle), "attn_key_weights")
+    dev = _device(q, "q")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: key_weights(q, lse, kcache, kv_lens, weights, page_table, cu_seqlens_q, max_sq,
+                                              causal, window, n_sink, scale, accumulate), q, stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    qp = _need(q, "q", torch.bfloat16, 3, dev)
+    np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
+    B = kv_lens.shape[0]
+    kp, _, tp, Hkv, d, max_pages, page, n_pages = _cache(kcache, None, page_table, B, dev)
+    total, Hq, dq = q.shape
+    if dq != d:
+        raise ValueError(f"q and the cache differ in head dim: {dq} and {d}")
+    cu = None
+    if cu_seqlens_q is not None:
+        cu = _sized(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, B + 1)
+        lp = _sized(lse, "lse", torch.float32, dev, Hq, total)
+    else:
+        if total != B:
+            raise ValueError("without cu_seqlens_q there must be one row per sequence")
+        lp = _sized(lse, "lse", torch.float32, dev, B, Hq)
+        max_sq = 1
+    wp, w_stride = _weight_rows(weights, dev, B, Hkv, max_pages * page)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    rc = load().attn_key_weights(qp, lp, kp, tp, cu, np_, wp, w_stride, B, Hq, Hkv, total, max_sq, d, max_pages, page,
+                                 n_pages, int(causal), window, n_sink, scale, int(accumulate), handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_key_weights")
     return weights
 
 
@@ -402,33 +432,38 @@ def evict(weights, kcache, vcache, kv_lens, budget: int, n_recent: int = 0, n_si
     of each key, -1 past the end; new kv_lens int32 [B]), into ``out`` if given (the new
     lengths may be kv_lens itself)."""
     torch = _torch()
-    with _Call(kcache, "kcache", stream) as c:
-        np_ = c.check(kv_lens, "kv_lens", torch.int32, 1)
-        B = kv_lens.shape[0]
-        kp, vp, tp, Hkv, d, max_pages, page, n_pages = c.cache(kcache, vcache, page_table, B)
-        wp = c.check(weights, "weights", torch.float32, 3)
-        if weights.shape[0] != B or weights.shape[1] != Hkv or weights.shape[2] < max_pages * page:
-            raise ValueError(f"weights must be [B, Hkv, at least {max_pages * page}], got {list(weights.shape)}")
-        k2 = v2 = t2 = None
-        m2 = p2 = n2 = 0
-        w2 = wp
-        if dst is not None:
-            dk, dv, dt, dw = dst
-            if dv is None:
-                raise TypeError("dst needs both caches")
-            k2, v2, t2, H2, d2, m2, p2, n2 = c.cache(dk, dv, dt, B)
-            if (H2, d2) != (Hkv, d):
-                raise ValueError("dst must have the cache's heads and head dim")
-            w2 = None
-            if dw is not None:
-                w2 = c.output(dw, "dst weights", torch.float32, *weights.shape)
-        budget = int(budget)
-        if out is None:
-            kept, lens = c.result((B, Hkv, max(budget, 0)), torch.int32), c.result((B,), torch.int32)
-        else:
-            kept, lens = out
-        ep = c.output(kept, "out[0]", torch.int32, B, Hkv, budget)
-        lp = c.output(lens, "out[1]", torch.int32, B)
-        _raise(load().attn_evict(wp, w2, weights.shape[2], kp, vp, tp, np_, B, Hkv, d, max_pages, page, n_pages,
-                                 budget, n_recent, n_sink, k2, v2, t2, m2, p2, n2, ep, lp, c.handle), "attn_evict")
+    dev = _device(kcache, "kcache")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: evict(weights, kcache, vcache, kv_lens, budget, n_recent, n_sink, page_table, dst,
+                                        out), kcache, stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
+    B = kv_lens.shape[0]
+    if vcache is None:
+        raise TypeError("vcache must be a CUDA tensor")
+    kp, vp, tp, Hkv, d, max_pages, page, n_pages = _cache(kcache, vcache, page_table, B, dev)
+    wp, w_stride = _weight_rows(weights, dev, B, Hkv, max_pages * page)
+    k2 = v2 = t2 = None
+    m2 = p2 = n2 = 0
+    w2 = wp
+    if dst is not None:
+        dk, dv, dt, dw = dst
+        if dv is None:
+            raise TypeError("dst needs both caches")
+        k2, v2, t2, H2, d2, m2, p2, n2 = _cache(dk, dv, dt, B, dev)
+        if H2 != Hkv or d2 != d:
+            raise ValueError("dst must have the cache's heads and head dim")
+        w2 = None if dw is None else _sized(dw, "dst weights", torch.float32, dev, B, Hkv, w_stride)
+    if out is None:
+        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device="cuda")
+        lens = torch.empty(B, dtype=torch.int32, device="cuda")
+        ep, lp = kept.data_ptr(), lens.data_ptr()
+    else:
+        kept, lens = out
+        ep = _sized(kept, "out[0]", torch.int32, dev, B, Hkv, budget)
+        lp = _sized(lens, "out[1]", torch.int32, dev, B)
+    rc = load().attn_evict(wp, w2, w_stride, kp, vp, tp, np_, B, Hkv, d, max_pages, page, n_pages, budget, n_recent,
+                           n_sink, k2, v2, t2, m2, p2, n2, ep, lp, handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_evict")
     return kept, lens

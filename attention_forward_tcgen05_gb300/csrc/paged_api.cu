@@ -178,8 +178,8 @@ int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const at
   return from_cuda(attn::launch_merge(m, stream_of(stream)));
 }
 
-int attn_decode_paged_splits(int B, int Hkv, int max_kv, int* min_rows) {
-  if (B < 0 || Hkv < 1 || max_kv < 0 || min_rows == nullptr) return ATTN_ERR_INVALID_ARG;
+int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int* min_rows) {
+  if (check_heads(B, Hq, Hkv) != ATTN_OK || max_kv < 0 || !ok_dim(d) || min_rows == nullptr) return ATTN_ERR_INVALID_ARG;
   const long long units = std::max(1LL, (long long)B * Hkv);
   long long rows = std::max(128LL, (long long)max_kv * units / (16 * kSms));
   rows = (rows + 63) / 64 * 64;

@@ -479,7 +479,7 @@ int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const att
 
 /* The n_splits (>= 1) and min_rows_per_split that suit a decode of these sizes, max_kv
  * keys in the longest sequence (host only); ATTN_ERR_INVALID_ARG for bad sizes. */
-int attn_decode_paged_splits(int B, int Hkv, int max_kv, int* min_rows_per_split);
+int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int* min_rows_per_split);
 
 /*
  * attn_key_weights -- the attention weight that every cached key received.
