@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["attn_api.cu", "paged_api.cu", "prefill.cu", "prefill_paged.cu", "prefill_pair.cu", "prefill_d512.cu",
            "prefill_persist.cu", "decode.cu", "decode_paged.cu", "decode_noalloc.cu", "rope.cu", "key_weights.cu",
            "evict.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "paged.cuh", "prefill_kernel.cuh", "decode_kernel.cuh"]
+HEADERS = ["ptx.cuh", "internal.h", "paged.cuh", "prefill_kernel.cuh", "decode_common.cuh", "mma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

@@ -1,14 +1,280 @@
-// decode_paged.cu -- launches of the one-token decode over a paged cache (the kernel:
-// decode_kernel.cuh with PAGED).
-#include "decode_kernel.cuh"
+// decode_paged.cu -- one-token GQA decode over a paged cache: split-KV partials and their
+// LSE-weighted merge in one launch, the split rule, launch order and combine of decode.cu.
+//
+// One CTA per (sequence, KV head, split, group of up to 16 query heads); its four warps take
+// 32-key runs of the split in turn and share nothing until the end.  Each warp gathers 16
+// keys of K and V at a time into a ring of its own (cp.async groups: no barrier, no
+// producer warp), and does on its own fragments
+//   S^T = K Q^T        16 keys x 8 heads per mma, the queries resident in registers,
+//   P = 2^(S - m),     m a running reference that is moved (and O rescaled) only when a
+//                      score exceeds it by 2^8, so that the usual step needs no maximum
+//                      across lanes; it cancels in O / l,
+//   O^T += V^T P^T     P^T by movmatrix from the score fragments.
+// P goes into the product as two bf16 terms (value and remainder, 2^-17 of P left out), so
+// that O is good to fp32 outputs; O, l and m are fp32.  With heads as the 8-wide side of the
+// mma a step of 16 keys costs about 250 warp instructions at d = 128 against 700 on fp32
+// cores per head group of 4, and the kernel runs at the rate of the gathers.
+#include <cmath>
+
+#include "decode_common.cuh"
+#include "internal.h"
+#include "mma.cuh"
+#include "paged.cuh"
+#include "ptx.cuh"
 
 namespace attn {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kMoveThreshold = 8.f;  // log2: the reference m moves when a score exceeds it by 2^8
+
+template <int D, int NB>
+struct DecodePagedCfg {
+  static constexpr int kHeads = 8 * NB;
+  static constexpr int kPanel = 16 * 128;          // one 64-column panel of 16 keys
+  static constexpr int kTile = 16 * D * 2;         // K or V of 16 keys
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kStages = D == 64 ? 6 : 3;  // a warp's ring: 24, 24, 48 KB
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kComb = kWarps * kHeads * (D + 2) * 4;
+  static constexpr int kSmem = (kRing > kComb ? kRing : kComb) + 1024;
+  static constexpr int kMinBlocks = D == 256 ? 1 : 2;
+};
+
+template <int D, int NB>
+__global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks)
+    decode_paged_kernel(const DecodeArgs a, int heads_per_cta, int ordered) {
+  using C = DecodePagedCfg<D, NB>;
+  constexpr int ST = C::kStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int Gall = a.Hq / a.Hkv, n_hg = (Gall + heads_per_cta - 1) / heads_per_cta;
+  const int per_unit = a.Hkv * n_hg;
+  const int pos = (int)(blockIdx.x / per_unit), w_in = (int)(blockIdx.x % per_unit);
+  const int hk = w_in / n_hg, g0 = w_in % n_hg * heads_per_cta;
+  const int G = min(heads_per_cta, Gall - g0);
+  int b, s_idx;
+  if (ordered) {
+    const int2 u = unit_at(pos, a.kv_lens, a.B, a.max_kv, a.n_splits, a.min_rows, lane);
+    b = u.x;
+    s_idx = u.y;
+    if (b < 0) {  // kv_lens changed while the launch ran (see decode.cu): reported, nothing written
+      if (threadIdx.x == 0) atomicCAS(a.err, kErrNone, kErrBadShape);
+      return;
+    }
+  } else {
+    b = pos / a.n_splits;
+    s_idx = pos % a.n_splits;
+  }
+  int L = a.kv_lens[b];
+  L = L < 0 ? 0 : (L > a.max_kv ? a.max_kv : L);
+  long long chunk = ((long long)L + a.n_splits - 1) / a.n_splits;
+  if (chunk < a.min_rows) chunk = a.min_rows;
+  if (chunk < 1) chunk = 1;
+  const long long lo_ll = (long long)s_idx * chunk, hi_ll = lo_ll + chunk;
+  const int lo = (int)(lo_ll < L ? lo_ll : L), hi = (int)(hi_ll < L ? hi_ll : L);
+  const size_t orow0 = (size_t)b * a.Hq + (size_t)hk * Gall + g0;  // (sequence, first query head)
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+
+  if (lo >= hi) {  // empty split: o = 0, lse = -inf
+    for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
+      const size_t row = (orow0 + i / D) * a.n_splits + s_idx;
+      a.part_o[row * D + i % D] = 0.f;
+      if (i % D == 0) a.part_lse[row] = -INFINITY;
+    }
+  } else {
+    uint8_t* ring = smem + warp * ST * C::kStage;
+    // this warp's 16-key steps: step i covers keys from lo + ((i / 2) * kWarps + warp) * 32 + (i % 2) * 16
+    const int runs = (hi - lo + 31) / 32;
+    const int n = 2 * (runs > warp ? (runs - warp + kWarps - 1) / kWarps : 0);
+    auto key0 = [&](int i) { return lo + ((i >> 1) * kWarps + warp) * 32 + (i & 1) * 16; };
+    int ri[1] = {-1}, rn[1];  // pool rows of the run being issued, and of the next one
+    paged_rows<1>(a.kv, b, key0(0), hi, lane, a.err, rn);
+    auto issue = [&](int i) {
+      if (i < n) {
+        if ((i & 1) == 0) {
+          ri[0] = rn[0];
+          if (i + 2 < n) paged_rows<1>(a.kv, b, key0(i + 2), hi, lane, a.err, rn);
+        }
+        const uint32_t dst = smem_u32(ring + (i % ST) * C::kStage);
+        paged_gather_rows<D, 16>(dst, C::kPanel, a.kv.k, a.Hkv, hk, lane, ri[0], (i & 1) * 16);
+        paged_gather_rows<D, 16>(dst + C::kTile, C::kPanel, a.kv.v, a.Hkv, hk, lane, ri[0], (i & 1) * 16);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) issue(i);
+
+    uint32_t qf[NB][D / 16][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int g = nb * 8 + (lane >> 2);
+      load_q_frags<D>(qf[nb], [&](int r) { return a.q + (orow0 + r) * D; }, g, g < G, lane);
+    }
+    float o[NB][D / 16][4], m[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb][0] = m[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) o[nb][t][0] = o[nb][t][1] = o[nb][t][2] = o[nb][t][3] = 0.f;
+    }
+    const float sl2 = a.scale * kLog2e;
+
+    for (int i = 0; i < n; ++i) {
+      issue(i + ST - 1);
+      cp_async_wait<ST - 1>();
+      __syncwarp();
+      const uint32_t kt = smem_u32(ring + (i % ST) * C::kStage), vt = kt + C::kTile;
+      // S^T: key lane / 4 (+ 8), heads 2 (lane % 4) + {0, 1}; two chains along the head dim
+      float s[NB][4], s2[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nb][e] = s2[nb][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t f[4];
+        ldmatrix_x4(frag_keys<C::kPanel>(kt, kk, lane), f);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma_16816((kk & 1) ? s2[nb] : s[nb], f, qf[nb][kk][0], qf[nb][kk][1]);
+      }
+      const int left = hi - key0(i);  // keys of this step that exist (may be <= 0)
+      bool move = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[nb][e] = (s[nb][e] + s2[nb][e]) * sl2;
+          if (left < 16 && (lane >> 2) + (e >> 1) * 8 >= left) s[nb][e] = -INFINITY;
+          move = move || s[nb][e] > m[nb][e & 1] + kMoveThreshold;
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[nb][e], s[nb][e + 2]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, off));
+            const float mn = fmaxf(m[nb][e], x);
+            const float c = m[nb][e] == mn ? 1.f : ex2_approx(m[nb][e] - mn);
+            m[nb][e] = mn;
+            l[nb][e] *= c;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+              o[nb][t][e] *= c;
+              o[nb][t][e + 2] *= c;
+            }
+          }
+        }
+      }
+      uint32_t ph[NB][2], pl[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // keys lane / 4 + 8 h
+          // (a warp whose keys are all missing so far has m = -inf: no term)
+          const float p0 = m[nb][0] == -INFINITY ? 0.f : ex2_approx(s[nb][2 * h] - m[nb][0]);
+          const float p1 = m[nb][1] == -INFINITY ? 0.f : ex2_approx(s[nb][2 * h + 1] - m[nb][1]);
+          l[nb][0] += p0;
+          l[nb][1] += p1;
+          const uint32_t v = pack_bf16x2(p0, p1);
+          ph[nb][h] = movmatrix_trans(v);
+          pl[nb][h] = movmatrix_trans(pack_bf16x2(p0 - __uint_as_float(v << 16), p1 - __uint_as_float(v & 0xFFFF0000u)));
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) {
+        uint32_t f[4];
+        ldmatrix_x4_trans(frag_dims<C::kPanel>(vt, t, lane), f);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          mma_16816(o[nb][t], f, ph[nb][0], ph[nb][1]);
+          mma_16816(o[nb][t], f, pl[nb][0], pl[nb][1]);
+        }
+      }
+      __syncwarp();  // every lane has read the stage before it is refilled
+    }
+
+    // ---- the four warps' (m, l, O) through shared memory ----
+    cp_async_wait<0>();
+    __syncthreads();
+    float* comb = reinterpret_cast<float*>(smem);  // [warp][head][D + 2]
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[nb][e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+        float* cw = comb + (warp * C::kHeads + nb * 8 + (lane & 3) * 2 + e) * (D + 2);
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+          cw[t * 16 + (lane >> 2)] = o[nb][t][e];
+          cw[t * 16 + 8 + (lane >> 2)] = o[nb][t][e + 2];
+        }
+        if (lane < 4) {
+          cw[D] = m[nb][e];
+          cw[D + 1] = x;
+        }
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
+      const int g = i / D, t = i % D;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[(w * C::kHeads + g) * (D + 2) + D]);
+      float ls = 0.f, acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* cw = comb + (w * C::kHeads + g) * (D + 2);
+        const float f = ex2_approx(cw[D] - M);  // warps without keys: m = -inf -> 0
+        ls = fmaf(cw[D + 1], f, ls);
+        acc = fmaf(cw[t], f, acc);
+      }
+      const size_t row = (orow0 + g) * a.n_splits + s_idx;
+      a.part_o[row * D + t] = acc / ls;
+      if (t == 0) a.part_lse[row] = (M + log2f(ls)) * kLn2;
+    }
+  }
+  combine_if_last<D, kWarps>(a.done + orow0, a.n_splits, a.part_o, a.part_lse, a.o, a.lse, orow0, G, a.o_bf16,
+                             [] { __syncthreads(); });
+}
+
+template <int D, int NB>
+cudaError_t launch_t(const DecodeArgs& a, int heads_per_cta, cudaStream_t stream) {
+  using C = DecodePagedCfg<D, NB>;
+  auto kern = decode_paged_kernel<D, NB>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int n_hg = (a.Hq / a.Hkv + heads_per_cta - 1) / heads_per_cta;
+  const long long ctas = (long long)a.B * a.n_splits * a.Hkv * n_hg;
+  if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  // longest splits first (one sequence has nothing to order)
+  const int ordered = a.B > 1 && a.B <= kOrderMaxBatch ? 1 : 0;
+  kern<<<(unsigned)ctas, kWarps * 32, C::kSmem, stream>>>(a, heads_per_cta, ordered);
+  return cudaGetLastError();
+}
+
+// Heads of a group that one CTA takes: all up to 16, else equal shares of at most 16 (their
+// CTAs are neighbours and read the same rows, from L2).
+template <int D>
+cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
+  const int G = a.Hq / a.Hkv, n_hg = (G + 15) / 16, hpc = (G + n_hg - 1) / n_hg;
+  return hpc <= 8 ? launch_t<D, 1>(a, hpc, stream) : launch_t<D, 2>(a, hpc, stream);
+}
+
+}  // namespace
 
 cudaError_t launch_decode_paged(const DecodeArgs& a, cudaStream_t stream) {
   switch (a.d) {
-    case 64: return launch_decode_g<64, true>(a, stream);
-    case 128: return launch_decode_g<128, true>(a, stream);
-    case 256: return launch_decode_g<256, true>(a, stream);
+    case 64: return launch_d<64>(a, stream);
+    case 128: return launch_d<128>(a, stream);
+    case 256: return launch_d<256>(a, stream);
     default: return cudaErrorInvalidValue;
   }
 }

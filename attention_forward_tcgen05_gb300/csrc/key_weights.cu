@@ -6,13 +6,14 @@
 // sum has one owner, which adds its terms in a fixed order: no atomics, the same bits
 // each time.  Two kernels, by how many query rows a KV head has in a sequence:
 //   * up to kRowsMax (a decode step): the keys are streamed from HBM once and nothing else
-//     matters; CUDA cores, lane = key;
+//     matters; warp-level mma on rows gathered by each warp for itself;
 //   * more: S^T = K Q^T on the tensor cores, so a key is a TMEM lane and a thread sums its
 //     own row; one ex2 per pair (32 a cycle per SM) and the MMA (512 cycles per 128 x 128
 //     tile at d = 128) take equally long.
 #include <cmath>
 
 #include "internal.h"
+#include "mma.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -20,13 +21,6 @@ namespace attn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-
-// The rows of a sequence and which keys they admit: key j and position p (key index of the
-// row) with j <= p if causal, and with a window j > p - window or j < n_sink.
-__device__ __forceinline__ bool admits(int j, long long p, int causal, int window, int n_sink) {
-  if (causal && j > p) return false;
-  return window <= 0 || j > p - window || j < n_sink;
-}
 
 __device__ __forceinline__ void put_weight(const KeyWeightArgs& a, int b, int hk, int j, float w) {
   float* dst = a.weights + ((size_t)b * a.Hkv + hk) * a.w_stride + j;
@@ -39,15 +33,17 @@ constexpr int kRowWarps = 4;
 
 template <int D>
 struct RowCfg {
-  static constexpr int kStages = D == 256 ? 2 : 3;
-  static constexpr int kStageBytes = 32 * D * 2;  // 32 keys
-  static constexpr int kSmem = kRowWarps * kStages * kStageBytes + 1024;
+  static constexpr int kPanel = 16 * 128;
+  static constexpr int kStage = 16 * D * 2;                          // K of 16 keys
+  static constexpr int kStages = D == 64 ? 8 : (D == 128 ? 6 : 3);  // a warp's ring: 16, 24, 24 KB
+  static constexpr int kSmem = kRowWarps * kStages * kStage + 1024;
 };
 
-// One CTA per (sequence, KV head, range of `chunk` keys); each warp takes every fourth
-// 32-key tile of it through a ring of its own (cp.async groups, no barriers).
-template <int D, int RMAX>
-__global__ void __launch_bounds__(kRowWarps * 32) key_weights_rows_kernel(const KeyWeightArgs a, int chunk) {
+// One CTA per (sequence, KV head, range of `chunk` keys).  As in decode_paged.cu a warp
+// gathers 16 keys at a time into its own ring and multiplies them with the resident query
+// rows (up to 8 NB); a key's terms then lie in four lanes.
+template <int D, int NB>
+__global__ void __launch_bounds__(kRowWarps * 32, 2) key_weights_rows_kernel(const KeyWeightArgs a, int chunk) {
   using C = RowCfg<D>;
   constexpr int ST = C::kStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -61,71 +57,94 @@ __global__ void __launch_bounds__(kRowWarps * 32) key_weights_rows_kernel(const 
   const int G = a.Hq / a.Hkv, R = e.Sq * G;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(16) uint16_t qs[RMAX * D];
-  __shared__ float nl[RMAX];  // -lse * log2 e
-  uint8_t* ring = smem + warp * ST * C::kStageBytes;
+  uint8_t* ring = smem + warp * ST * C::kStage;
 
-  int ri[1];
-  int tile = lo + warp * 32, issued = 0;  // tiles of this warp: tile, tile + 128, ...
-  auto issue = [&]() {
-    if (tile < hi) {
-      paged_rows<1>(a.kv, b, tile, hi, lane, a.err, ri);
-      paged_gather<D, 1>(smem_u32(ring + (issued % ST) * C::kStageBytes), 32 * 128, a.kv.k, a.Hkv, hk, lane, ri);
+  const int runs = (hi - lo + 31) / 32;
+  const int n = 2 * (runs > warp ? (runs - warp + kRowWarps - 1) / kRowWarps : 0);
+  auto key0 = [&](int i) { return lo + ((i >> 1) * kRowWarps + warp) * 32 + (i & 1) * 16; };
+  int ri[1] = {-1}, rn[1];
+  paged_rows<1>(a.kv, b, key0(0), hi, lane, a.err, rn);
+  auto issue = [&](int i) {
+    if (i < n) {
+      if ((i & 1) == 0) {
+        ri[0] = rn[0];
+        if (i + 2 < n) paged_rows<1>(a.kv, b, key0(i + 2), hi, lane, a.err, rn);
+      }
+      paged_gather_rows<D, 16>(smem_u32(ring + (i % ST) * C::kStage), C::kPanel, a.kv.k, a.Hkv, hk, lane, ri[0],
+                               (i & 1) * 16);
     }
     cp_async_commit();
-    ++issued;
-    tile += kRowWarps * 32;
   };
 #pragma unroll
-  for (int s = 0; s < ST - 1; ++s) issue();
-  for (int i = threadIdx.x; i < RMAX * (D / 8); i += kRowWarps * 32) {
-    const int r = i / (D / 8), c = i % (D / 8);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < R) {
-      const int pos = r / G, h = hk * G + r % G;
-      x = *reinterpret_cast<const uint4*>(a.q + ((size_t)(base + pos) * a.Hq + h) * D + c * 8);
-      if (c == 0) nl[r] = -kLog2e * a.lse[(size_t)h * a.lse_hs + (size_t)(base + pos) * a.lse_ts];
-    }
-    *reinterpret_cast<uint4*>(qs + r * D + c * 8) = x;
-  }
-  __syncthreads();
-  const float sl2 = a.scale * kLog2e;
+  for (int i = 0; i < ST - 1; ++i) issue(i);
+
+  // row r: position r / G, head r % G.  This lane's columns: rows 8 nb + 2 (lane % 4) + {0, 1},
+  // each with -lse log2 e and the keys it admits (j <= last, and j >= first or j < n_sink)
   const long long off = (long long)e.Skv - e.Sq;
-  int done = 0;
-  for (int j0 = lo + warp * 32; j0 < hi; j0 += kRowWarps * 32) {
-    issue();
+  uint32_t qf[NB][D / 16][2];
+  float nl[NB][2];
+  int last[NB][2], first[NB][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int row = nb * 8 + (lane >> 2);
+    load_q_frags<D>(qf[nb], [&](int r) { return a.q + ((size_t)(base + r / G) * a.Hq + hk * G + r % G) * D; }, row,
+                    row < R, lane);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = nb * 8 + (lane & 3) * 2 + k;
+      nl[nb][k] = 0.f;
+      last[nb][k] = -1;  // admits nothing
+      first[nb][k] = 0;
+      if (r < R) {
+        const int pos = r / G, h = hk * G + r % G;
+        const float v = a.lse[(size_t)h * a.lse_hs + (size_t)(base + pos) * a.lse_ts];
+        const long long p = (long long)pos + off;
+        nl[nb][k] = -kLog2e * v;
+        if (v != -INFINITY) last[nb][k] = a.causal ? (int)max(-1LL, p) : 0x7FFFFFFF;
+        if (a.window > 0) first[nb][k] = (int)max(0LL, p - a.window + 1);
+      }
+    }
+  }
+  const int sink = a.window > 0 ? a.n_sink : 0;
+  const float sl2 = a.scale * kLog2e;
+  for (int i = 0; i < n; ++i) {
+    issue(i + ST - 1);
     cp_async_wait<ST - 1>();
     __syncwarp();
-    const uint8_t* kt = ring + (done % ST) * C::kStageBytes + lane * 128;
-    float al[RMAX], ah[RMAX];
+    const uint32_t kt = smem_u32(ring + (i % ST) * C::kStage);
+    float s[NB][4], s2[NB][4];
 #pragma unroll
-    for (int r = 0; r < RMAX; ++r) al[r] = ah[r] = 0.f;
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 kv = *reinterpret_cast<const uint4*>(kt + (c >> 3) * (32 * 128) + (((c & 7) ^ (lane & 7)) << 4));
+      for (int k = 0; k < 4; ++k) s[nb][k] = s2[nb][k] = 0.f;
 #pragma unroll
-      for (int r = 0; r < RMAX; ++r) {
-        if (r < R) {
-          const uint4 qv = *reinterpret_cast<const uint4*>(qs + r * D + c * 8);
-          fma_bf16x2_f32(qv.x, kv.x, al[r], ah[r]);
-          fma_bf16x2_f32(qv.y, kv.y, al[r], ah[r]);
-          fma_bf16x2_f32(qv.z, kv.z, al[r], ah[r]);
-          fma_bf16x2_f32(qv.w, kv.w, al[r], ah[r]);
-        }
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t f[4];
+      ldmatrix_x4(frag_keys<C::kPanel>(kt, kk, lane), f);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) mma_16816((kk & 1) ? s2[nb] : s[nb], f, qf[nb][kk][0], qf[nb][kk][1]);
+    }
+    float w[2] = {0.f, 0.f};  // keys j and j + 8
+    const int j = key0(i) + (lane >> 2);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = k & 1, jj = j + (k >> 1) * 8;
+        const float p = ex2_approx(fmaf(s[nb][k] + s2[nb][k], sl2, nl[nb][c]));
+        if (jj <= last[nb][c] && (jj >= first[nb][c] || jj < sink)) w[k >> 1] += p;
       }
     }
-    const int j = j0 + lane;
-    float w = 0.f;
 #pragma unroll
-    for (int r = 0; r < RMAX; ++r) {
-      if (r < R) {
-        const float p = ex2_approx(fmaf(al[r] + ah[r], sl2, nl[r]));
-        if (admits(j, (long long)(r / G) + off, a.causal, a.window, a.n_sink) && nl[r] != INFINITY) w += p;
-      }
+    for (int o = 1; o < 4; o <<= 1) {
+      w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], o);
+      w[1] += __shfl_xor_sync(0xFFFFFFFFu, w[1], o);
     }
-    if (j < hi) put_weight(a, b, hk, j, w);
-    __syncwarp();  // every lane has read the tile before its slot is refilled
-    ++done;
+    if ((lane & 3) == 0) {
+      if (j < hi) put_weight(a, b, hk, j, w[0]);
+      if (j + 8 < hi) put_weight(a, b, hk, j + 8, w[1]);
+    }
+    __syncwarp();  // every lane has read the stage before it is refilled
   }
   cp_async_wait<0>();
 }
@@ -240,28 +259,41 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
   if (warp == 9) {
     // ---- query tiles ----
     if (lane == 0) tma_prefetch_desc(&tm_q);
+    // this lane's columns of a tile: their position in it and their head (-1: no such row)
+    int cp[QN / 32], ch[QN / 32];
+#pragma unroll
+    for (int k = 0; k < QN / 32; ++k) {
+      const int c = k * 32 + lane;
+      cp[k] = c / G;
+      ch[k] = c < PT * G ? c % G : -1;
+    }
+    // -lse log2 e of the tile's columns; nothing where there is no row or it saw no key
+    auto load_lse = [&](int i, float (&v)[QN / 32]) {
+      const int x = rank + i * cs, hu = hk * n_hu + x % n_hu, p0 = (t0 + x / n_hu) * PT;
+#pragma unroll
+      for (int k = 0; k < QN / 32; ++k) {
+        v[k] = INFINITY;
+        if (ch[k] >= 0 && p0 + cp[k] < e.Sq) {
+          const float y = a.lse[(size_t)(hu * G + ch[k]) * a.lse_hs + (size_t)(base + p0 + cp[k]) * a.lse_ts];
+          v[k] = y == -INFINITY ? INFINITY : y;
+        }
+      }
+    };
+    float v[QN / 32];
+    if (n > 0) load_lse(0, v);
     int i = 0;
     for (; i < n; ++i) {
       const int s = i % C::kStages;
       const int x = rank + i * cs, hu = hk * n_hu + x % n_hu, p0 = (t0 + x / n_hu) * PT;
-      float v[QN / 32];  // read before the wait for the slot
-#pragma unroll
-      for (int k = 0; k < QN / 32; ++k) {
-        const int c = k * 32 + lane, pos = p0 + c / G;
-        v[k] = -INFINITY;
-        if (c < PT * G && pos < e.Sq)
-          v[k] = -kLog2e * a.lse[(size_t)(hu * G + c % G) * a.lse_hs + (size_t)(base + pos) * a.lse_ts];
-        // a row without keys (lse = -inf) contributes nothing
-        if (v[k] == INFINITY) v[k] = -INFINITY;
-      }
       if (!mbar_wait_warp(&empty[s], ((uint32_t)(i / C::kStages) & 1u) ^ 1u, a.err, abort_flag)) break;
 #pragma unroll
-      for (int k = 0; k < QN / 32; ++k) sL[s * QN + k * 32 + lane] = v[k];
+      for (int k = 0; k < QN / 32; ++k) sL[s * QN + k * 32 + lane] = -kLog2e * v[k];
       __syncwarp();
       mbar_arrive_expect_tx_e(&full[s], (uint32_t)(PT * G) * 128u * C::kPanels);
 #pragma unroll
       for (int p = 0; p < C::kPanels; ++p)
         tma_load_5d_e(sQ + s * C::kQTile + p * C::kQPanel, &tm_q, &full[s], p * 64, 0, hu, base + p0, 0);
+      if (i + 1 < n) load_lse(i + 1, v);  // in flight while the next slot drains
     }
     if (i < n)  // aborted: the copies in flight land before shared memory is released
       for (int u = max(0, i - C::kStages); u < i; ++u)
@@ -404,8 +436,7 @@ cudaError_t launch_rows(const KeyWeightArgs& a, int rows, cudaStream_t stream) {
   // ranges of keys: about eight CTAs an SM in all, 128 to 2048 keys each
   int chunk = 2048;
   while (chunk > 128 && units * ((cap + chunk - 1) / chunk) < 8 * 152) chunk /= 2;
-  auto kern = rows <= 4 ? key_weights_rows_kernel<D, 4>
-                        : (rows <= 8 ? key_weights_rows_kernel<D, 8> : key_weights_rows_kernel<D, kRowsMax>);
+  auto kern = rows <= 8 ? key_weights_rows_kernel<D, 1> : key_weights_rows_kernel<D, 2>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)(units * ((cap + chunk - 1) / chunk)), kRowWarps * 32, C::kSmem, stream>>>(a, chunk);

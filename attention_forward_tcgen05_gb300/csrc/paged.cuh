@@ -36,11 +36,6 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// one arrival on `bar` (counted in its expected arrivals) once every earlier
-// cp.async of this thread has landed
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 
 // The pool rows of 32 * NR consecutive keys from j0, as lane registers: lane's ri[h]
 // is the row of key j0 + 32 h + lane, -1 at or past `end`.
@@ -54,12 +49,12 @@ __device__ __forceinline__ void paged_rows(const PagedKV& kv, int b, int j0, int
   }
 }
 
-// The whole warp gathers those rows (D bf16 of KV head hk each) into a tile of D / 64
-// panels of 128-byte swizzled rows, `panel_bytes` apart (the layout a 128B-swizzled
-// tensor copy gives; `dst` on a 1024-byte boundary).
-template <int D, int NR>
-__device__ __forceinline__ void paged_gather(uint32_t dst, int panel_bytes, const uint16_t* pool, int Hkv, int hk,
-                                             int lane, const int (&ri)[NR]) {
+// The whole warp gathers ROWS rows (D bf16 of KV head hk each; the rows of lanes from
+// `first` on in ri) into a tile of D / 64 panels of 128-byte swizzled rows, `panel_bytes`
+// apart (the layout a 128B-swizzled tensor copy gives; `dst` on a 1024-byte boundary).
+template <int D, int ROWS>
+__device__ __forceinline__ void paged_gather_rows(uint32_t dst, int panel_bytes, const uint16_t* pool, int Hkv, int hk,
+                                                  int lane, int ri, int first) {
   constexpr int CPR = D / 8;     // 16-byte chunks of a row
   constexpr int RPI = 32 / CPR;  // rows of one warp copy
   const int c = lane % CPR, rsub = lane / CPR;
@@ -67,15 +62,19 @@ __device__ __forceinline__ void paged_gather(uint32_t dst, int panel_bytes, cons
   const int cx = (c & 7) ^ rsub;  // rsub < RPI <= 4 and rows step by RPI: the XORs below do not meet
   const uint8_t* base = reinterpret_cast<const uint8_t*>(pool + (size_t)hk * D + c * 8);
   const uint32_t row_bytes = (uint32_t)Hkv * D * 2u;
-#pragma unroll
-  for (int h = 0; h < NR; ++h) {
 #pragma unroll 8
-    for (int i = 0; i < 32 / RPI; ++i) {
-      const int r = __shfl_sync(0xFFFFFFFFu, ri[h], i * RPI + rsub);
-      const uint8_t* src = base + (uint64_t)(uint32_t)max(r, 0) * row_bytes;
-      cp_async16(lane_dst + (h * 32 + i * RPI) * 128 + ((cx ^ ((i * RPI) & 7)) << 4), src, r < 0 ? 0u : 16u);
-    }
+  for (int i = 0; i < ROWS / RPI; ++i) {
+    const int r = __shfl_sync(0xFFFFFFFFu, ri, first + i * RPI + rsub);
+    const uint8_t* src = base + (uint64_t)(uint32_t)max(r, 0) * row_bytes;
+    cp_async16(lane_dst + i * RPI * 128 + ((cx ^ ((i * RPI) & 7)) << 4), src, r < 0 ? 0u : 16u);
   }
+}
+template <int D, int NR>
+__device__ __forceinline__ void paged_gather(uint32_t dst, int panel_bytes, const uint16_t* pool, int Hkv, int hk,
+                                             int lane, const int (&ri)[NR]) {
+#pragma unroll
+  for (int h = 0; h < NR; ++h)
+    paged_gather_rows<D, 32>(dst + h * 32 * 128, panel_bytes, pool, Hkv, hk, lane, ri[h], 0);
 }
 
 }  // namespace attn
