@@ -108,6 +108,9 @@ uint32_t* device_err_word() { return err_word(); }
 int encode_q_map(CUtensorMap* map, const void* base, int d, int G, int Hq, int ns, int nb, int rows) {
   return encode_bf16_q5d(map, base, d, G, Hq, ns, nb, rows);
 }
+int encode_pool_map(CUtensorMap* map, const void* base, int d, int Hkv, int page_size, int num_pages, int rows) {
+  return encode_bf16_4d(map, base, d, Hkv, page_size, num_pages, rows);
+}
 
 int check_decode_split_args(const void* q, const void* kcache, const void* vcache, const int* kv_lens,
                             int B, int Hq, int Hkv, int d, int max_kv, float scale, int n_splits,

@@ -16,6 +16,7 @@ struct PagedKV {
   const uint16_t* v;
   const int* table;
   int max_pages, page_size, num_pages;
+  int box_rows;  // prefill_paged.cu: rows of a tensor copy (64 or 128), 0: rows are gathered
 };
 
 // Prefill launch description (already validated by the C-ABI layer).
@@ -264,6 +265,8 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 uint32_t* device_err_word();
 // 5-D query map of the packed tiles: {d, G, Hq / G, ns, nb}, box {64, G, 1, rows / G, 1}.
 int encode_q_map(CUtensorMap* map, const void* base, int d, int G, int Hq, int ns, int nb, int rows);
+// 4-D map of a pool {d, Hkv, page_size, num_pages}, box {64, 1, rows, 1}.
+int encode_pool_map(CUtensorMap* map, const void* base, int d, int Hkv, int page_size, int num_pages, int rows);
 cudaError_t launch_wait_timeout_probe(uint64_t limit_ns, uint32_t* err, cudaStream_t stream);
 
 }  // namespace attn

@@ -11,6 +11,7 @@
 //     own row; one ex2 per pair (32 a cycle per SM) and the MMA (512 cycles per 128 x 128
 //     tile at d = 128) take equally long.
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "mma.cuh"
@@ -153,28 +154,34 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) key_weights_rows_kernel(con
 // CTA: 256 keys (two M = 128 tiles) of one (sequence, KV head), resident in shared memory;
 // the query rows of the group's heads stream past in tiles of QN rows (whole positions).
 // Two key tiles per query tile halve the query traffic from L2 (64 bytes a cycle per SM
-// otherwise).  Warps 0-3 / 4-7: the two key tiles' sums (thread = key); warp 8: MMA
-// issue; warp 9: query tiles by TMA, their lse by plain loads.  S^T is double buffered in
-// TMEM, so the MMA of one query tile runs under the exponentials of the one before.  The
+// otherwise).  Sixteen warps sum (thread = key): a warpgroup for each key tile and parity of
+// the query tile, each with a TMEM buffer of its own, read in two halves.  With eight warps
+// and one wait for all of S^T a query tile took 1.4 us, its warps mostly waiting together
+// for the buffers, barriers and loads; sixteen take 1.0 us, of which the exponentials are
+// 0.54.  Warp 16: MMA issue; warp 17: query tiles by TMA; warp 18: their lse by plain loads,
+// through a ring of its own, so that a query slot is free again as soon as the MMA has read
+// it (with one ring for both: 1.5 us).  The
 // CTAs of a cluster share the keys and take every cs-th query tile; their sums meet in
 // rank 0, in rank order.
 template <int D>
 struct TileCfg {
   static constexpr int QN = D == 256 ? 64 : 128;  // query rows of a tile
   static constexpr int kKeys = 256;
-  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kStages = D == 64 ? 6 : (D == 128 ? 4 : 3);  // ring of query tiles
+  static constexpr int kLse = D == 256 ? 4 : 8;                     // ring of their lse
   static constexpr int kPanels = D / 64;
   static constexpr int kKPanel = 128 * 128;               // one panel of a 128-key tile
   static constexpr int kKTile = kPanels * kKPanel;
   static constexpr int kQPanel = QN * 128;
   static constexpr int kQTile = kPanels * kQPanel;
   static constexpr int kQOff = 2 * kKTile;
-  static constexpr int kLseOff = kQOff + kStages * kQTile;   // [stage][QN] floats
-  static constexpr int kSumOff = kLseOff + kStages * QN * 4; // [256] floats
-  static constexpr int kBarOff = kSumOff + kKeys * 4;
-  static constexpr int kNumBars = 2 * kStages + 2 * 2 * 2;   // full, empty, S[tile][buf], free[tile][buf]
+  static constexpr int kLseOff = kQOff + kStages * kQTile;   // [slot][QN] floats
+  static constexpr int kSumOff = kQOff;                      // [parity][256] floats, at the end
+  static constexpr int kBarOff = kLseOff + kLse * QN * 4;
+  static constexpr int kNumBars = 2 * kStages + 2 * kLse + 2 * 2 * 2;  // full, empty, of each ring; S, free [tile][buf]
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
-  static constexpr int kThreads = 12 * 32;
+  static constexpr int kSumWarps = 16;
+  static constexpr int kThreads = (kSumWarps + 3) * 32;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -215,7 +222,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
   float* sSum = reinterpret_cast<float*>(smem + C::kSumOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + C::kStages;
-  uint64_t* bar_S = empty + C::kStages;  // [tile][buf] S^T computed
+  uint64_t* fullL = empty + C::kStages;
+  uint64_t* emptyL = fullL + C::kLse;
+  uint64_t* bar_S = emptyL + C::kLse;    // [tile][buf] S^T computed
   uint64_t* bar_F = bar_S + 4;           // [tile][buf] S^T read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_F + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -223,7 +232,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1 + 8);  // the MMA's reads, and each sum warp's reads of the lse
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < C::kLse; ++s) {
+      mbar_init(&fullL[s], 1);
+      mbar_init(&emptyL[s], 8);  // the warps that sum the tile
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar_S[i], 1);
@@ -232,7 +245,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == C::kSumWarps) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -255,50 +268,72 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const bool two = k0 + 128 < e.Skv;  // the second key tile exists
+  float sum = 0.f;                    // of this thread's key
 
-  if (warp == 9) {
+  // tile i of this CTA: its head group and first position
+  auto tile_at = [&](int i, int& hu, int& p0) {
+    const int x = rank + i * cs, q = n_hu == 1 ? x : x / n_hu;
+    hu = hk * n_hu + (x - q * n_hu);
+    p0 = (t0 + q) * PT;
+  };
+  if (warp == C::kSumWarps + 1) {
     // ---- query tiles ----
     if (lane == 0) tma_prefetch_desc(&tm_q);
-    // this lane's columns of a tile: their position in it and their head (-1: no such row)
-    int cp[QN / 32], ch[QN / 32];
+    int i = 0;
+    for (; i < n; ++i) {
+      const int s = i % C::kStages;
+      int hu, p0;
+      tile_at(i, hu, p0);
+      if (!mbar_wait_warp(&empty[s], ((uint32_t)(i / C::kStages) & 1u) ^ 1u, a.err, abort_flag)) break;
+      mbar_arrive_expect_tx_e(&full[s], (uint32_t)(PT * G) * 128u * C::kPanels);
+#pragma unroll
+      for (int q = 0; q < C::kPanels; ++q)
+        tma_load_5d_e(sQ + s * C::kQTile + q * C::kQPanel, &tm_q, &full[s], q * 64, 0, hu, base + p0, 0);
+    }
+    if (i < n)  // aborted: the copies in flight land before shared memory is released
+      for (int u = max(0, i - C::kStages); u < i; ++u)
+        mbar_wait(&full[u % C::kStages], (uint32_t)(u / C::kStages) & 1u, nullptr, nullptr, 100000000ull);
+  } else if (warp == C::kSumWarps + 2) {
+    // ---- -lse log2 e of the tiles' columns, read kAhead tiles before they are stored ----
+    int cp[QN / 32], ch[QN / 32];  // this lane's columns: position in the tile, head (-1: no row)
 #pragma unroll
     for (int k = 0; k < QN / 32; ++k) {
       const int c = k * 32 + lane;
       cp[k] = c / G;
       ch[k] = c < PT * G ? c % G : -1;
     }
-    // -lse log2 e of the tile's columns; nothing where there is no row or it saw no key
     auto load_lse = [&](int i, float (&v)[QN / 32]) {
-      const int x = rank + i * cs, hu = hk * n_hu + x % n_hu, p0 = (t0 + x / n_hu) * PT;
+      int hu, p0;
+      tile_at(i, hu, p0);
 #pragma unroll
       for (int k = 0; k < QN / 32; ++k) {
         v[k] = INFINITY;
-        if (ch[k] >= 0 && p0 + cp[k] < e.Sq) {
-          const float y = a.lse[(size_t)(hu * G + ch[k]) * a.lse_hs + (size_t)(base + p0 + cp[k]) * a.lse_ts];
-          v[k] = y == -INFINITY ? INFINITY : y;
-        }
+        if (ch[k] >= 0 && p0 + cp[k] < e.Sq)
+          v[k] = a.lse[(size_t)(hu * G + ch[k]) * a.lse_hs + (size_t)(base + p0 + cp[k]) * a.lse_ts];
       }
     };
-    float v[QN / 32];
-    if (n > 0) load_lse(0, v);
-    int i = 0;
-    for (; i < n; ++i) {
-      const int s = i % C::kStages;
-      const int x = rank + i * cs, hu = hk * n_hu + x % n_hu, p0 = (t0 + x / n_hu) * PT;
-      if (!mbar_wait_warp(&empty[s], ((uint32_t)(i / C::kStages) & 1u) ^ 1u, a.err, abort_flag)) break;
+    constexpr int kAhead = 2;
+    float v[kAhead][QN / 32];
 #pragma unroll
-      for (int k = 0; k < QN / 32; ++k) sL[s * QN + k * 32 + lane] = -kLog2e * v[k];
-      __syncwarp();
-      mbar_arrive_expect_tx_e(&full[s], (uint32_t)(PT * G) * 128u * C::kPanels);
+    for (int p = 0; p < kAhead; ++p)
+      if (p < n) load_lse(p, v[p]);
+    bool ok = true;
+    for (int i0 = 0; ok && i0 < n; i0 += kAhead) {
 #pragma unroll
-      for (int p = 0; p < C::kPanels; ++p)
-        tma_load_5d_e(sQ + s * C::kQTile + p * C::kQPanel, &tm_q, &full[s], p * 64, 0, hu, base + p0, 0);
-      if (i + 1 < n) load_lse(i + 1, v);  // in flight while the next slot drains
+      for (int p = 0; p < kAhead; ++p) {
+        const int i = i0 + p, s = i % C::kLse;
+        if (!ok || i >= n) continue;
+        ok = mbar_wait_warp(&emptyL[s], ((uint32_t)(i / C::kLse) & 1u) ^ 1u, a.err, abort_flag);
+        if (!ok) continue;
+#pragma unroll
+        for (int k = 0; k < QN / 32; ++k)  // nothing where there is no row or it saw no key
+          sL[s * QN + k * 32 + lane] = v[p][k] == -INFINITY ? -INFINITY : -kLog2e * v[p][k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&fullL[s]);
+        if (i + kAhead < n) load_lse(i + kAhead, v[p]);
+      }
     }
-    if (i < n)  // aborted: the copies in flight land before shared memory is released
-      for (int u = max(0, i - C::kStages); u < i; ++u)
-        mbar_wait(&full[u % C::kStages], (uint32_t)(u / C::kStages) & 1u, nullptr, nullptr, 100000000ull);
-  } else if (warp == 8) {
+  } else if (warp == C::kSumWarps) {
     // ---- MMA: S^T of both key tiles ----
     constexpr uint32_t idesc = idesc_bf16_f32(128, QN, 0, 0);
     const uint64_t dk = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
@@ -325,9 +360,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
       }
       if (ok) mma_commit_e(&empty[s]);
     }
-  } else if (warp < 8) {
+  } else if (warp < C::kSumWarps) {
     // ---- sums ----
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int t = (warp >> 2) & 1, par = warp >> 3, r = (warp & 3) * 32 + lane;
     const int j = k0 + t * 128 + r;  // this thread's key
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sl2 = a.scale * kLog2e;
@@ -335,11 +370,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
     const int j_lo = k0 + t * 128, j_hi = j_lo + 127;
     float acc = 0.f;
     bool ok = true;
-    for (int i = 0; i < n && (t == 0 || two); ++i) {
-      const int s = i % C::kStages, buf = i & 1;
-      const int x = rank + i * cs, p0 = (t0 + x / n_hu) * PT;
-      // lse of the tile (the producer's writes), then S^T
-      bool got = mbar_wait(&full[s], (uint32_t)(i / C::kStages) & 1u, a.err, abort_flag);
+    for (int i = par; i < n && (t == 0 || two); i += 2) {
+      const int s = i % C::kLse, buf = par;
+      int hu, p0;
+      tile_at(i, hu, p0);
+      bool got = mbar_wait(&fullL[s], (uint32_t)(i / C::kLse) & 1u, a.err, abort_flag);
       got = got && mbar_wait(&bar_S[t * 2 + buf], (uint32_t)(i >> 1) & 1u, a.err, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, got)) {
         ok = false;
@@ -358,74 +393,76 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
           c_hi = w <= 0 ? 0 : (int)min((long long)c_hi, w * G);
         }
       }
-      const float4* lp = reinterpret_cast<const float4*>(sL + s * QN);
+      const float* lp = sL + s * QN;
+      const uint32_t s_addr = lane_addr + (t * 2 + buf) * 128;
       uint64_t a0 = f2pack(0.f, 0.f), a1 = a0;
+      uint32_t sr[64];
+      auto terms = [&](int c0, auto edge_tag) {  // EDGE: some columns may not admit the key
+        constexpr bool EDGE = decltype(edge_tag)::value;
 #pragma unroll
-      for (int c0 = 0; c0 < QN; c0 += 32) {
-        uint32_t sr[32];
-        tmem_ld32(lane_addr + (t * 2 + buf) * 128 + c0, sr);
-        tmem_wait_ld();
-        if (c0 == QN - 32) {  // S^T is in registers: its buffer may be overwritten
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_F[t * 2 + buf]);
-        }
-#pragma unroll
-        for (int q4 = 0; q4 < 8; ++q4) {
-          const float4 l4 = lp[(c0 >> 2) + q4];
+        for (int c = 0; c < 64; c += 4) {
+          const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(lp + c0 + c);
           float x0, x1, x2, x3;
-          f2unpack(fma2(f2pack(__uint_as_float(sr[4 * q4]), __uint_as_float(sr[4 * q4 + 1])), sl2x2,
-                        f2pack(l4.x, l4.y)), x0, x1);
-          f2unpack(fma2(f2pack(__uint_as_float(sr[4 * q4 + 2]), __uint_as_float(sr[4 * q4 + 3])), sl2x2,
-                        f2pack(l4.z, l4.w)), x2, x3);
+          f2unpack(fma2(f2pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2x2, l4.x), x0, x1);
+          f2unpack(fma2(f2pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl2x2, l4.y), x2, x3);
           float p[4] = {ex2_approx(x0), ex2_approx(x1), ex2_approx(x2), ex2_approx(x3)};
-          if (edge) {
+          if constexpr (EDGE) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int c = c0 + 4 * q4 + k;
-              if (c < c_lo || c >= c_hi) p[k] = 0.f;
-            }
+            for (int k = 0; k < 4; ++k)
+              if (c0 + c + k < c_lo || c0 + c + k >= c_hi) p[k] = 0.f;
           }
           a0 = add2(a0, f2pack(p[0], p[1]));
           a1 = add2(a1, f2pack(p[2], p[3]));
         }
+      };
+#pragma unroll
+      for (int c0 = 0; c0 < QN; c0 += 64) {
+        tmem_ld32(s_addr + c0, sr);
+        tmem_ld32(s_addr + c0 + 32, sr + 32);
+        tmem_wait_ld();
+        if (c0 + 64 == QN) {  // all of S^T has been read: the MMA may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_F[t * 2 + buf]);
+        }
+        if (edge) terms(c0, std::true_type{});
+        else terms(c0, std::false_type{});
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
+      if (lane == 0) mbar_arrive(&emptyL[s]);
       float s0, s1;
       f2unpack(add2(a0, a1), s0, s1);
       acc += s0 + s1;
     }
-    // a missing second key tile reads nothing but still counts on the query slots
+    // a missing second key tile reads nothing but still counts on the lse slots
     if (t == 1 && !two) {
-      for (int i = 0; i < n; ++i) {
-        const int s = i % C::kStages;
-        if (!mbar_wait_warp(&full[s], (uint32_t)(i / C::kStages) & 1u, a.err, abort_flag)) break;
-        if (lane == 0) mbar_arrive(&empty[s]);
+      for (int i = par; i < n; i += 2) {
+        const int s = i % C::kLse;
+        if (!mbar_wait_warp(&fullL[s], (uint32_t)(i / C::kLse) & 1u, a.err, abort_flag)) break;
+        if (lane == 0) mbar_arrive(&emptyL[s]);
       }
     }
-    if (cs == 1) {
-      if (ok && j < e.Skv) put_weight(a, b, hk, j, acc);
-    } else {
-      sSum[t * 128 + r] = ok ? acc : NAN;
-    }
+    sum = ok ? acc : NAN;
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == C::kSumWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  } else if (warp < C::kSumWarps) {  // the query ring is free: its last tile has been read
+    sSum[threadIdx.x] = sum;  // [parity][key]
   }
-  if (cs > 1) {
-    cluster_sync_all();  // every rank's sums are written
-    if (rank == 0 && threadIdx.x < C::kKeys) {
-      const int j = k0 + (int)threadIdx.x;
-      float w = 0.f;
-      for (int r = 0; r < cs; ++r) w += ld_cluster_f32(mapa_shared(smem_u32(sSum + threadIdx.x), (uint32_t)r));
-      if (j < e.Skv) put_weight(a, b, hk, j, w);
-    }
-    cluster_sync_all();  // and read before their CTA's shared memory goes
+  if (cs > 1) cluster_sync_all();  // every rank's sums are written
+  else __syncthreads();
+  if (rank == 0 && threadIdx.x < C::kKeys) {
+    const int j = k0 + (int)threadIdx.x;
+    float w = sum + sSum[C::kKeys + threadIdx.x];
+    for (int r = 1; r < cs; ++r)
+      w += ld_cluster_f32(mapa_shared(smem_u32(sSum + threadIdx.x), (uint32_t)r)) +
+           ld_cluster_f32(mapa_shared(smem_u32(sSum + C::kKeys + threadIdx.x), (uint32_t)r));
+    if (j < e.Skv) put_weight(a, b, hk, j, w);
   }
+  if (cs > 1) cluster_sync_all();  // and read before their CTA's shared memory goes
 }
 
 template <int D>
@@ -454,8 +491,12 @@ cudaError_t launch_tiles(const KeyWeightArgs& a, cudaStream_t stream) {
   const long long units = (long long)blocks * a.B * a.Hkv;
   const int PT = C::QN / a.pack;
   const long long q_tiles = ((long long)a.max_sq + PT - 1) / PT * (a.Hq / a.Hkv / a.pack);
-  int cs = 1;  // CTAs of a cluster: up to eight, while SMs are idle and each keeps two tiles
-  while (cs < 8 && units * cs < 2 * 152 && q_tiles >= 4 * cs) cs *= 2;
+  // CTAs of a cluster, while SMs are idle and each keeps two query tiles: clusters of four
+  // reach nearly every SM, of eight 120 of them (15 clusters), so eight only where all run at
+  // once (52 units of a 3314-token prompt: 101, 56, 80 us in clusters of 2, 4, 8)
+  int cs = 1;
+  while (cs < 4 && units * cs < 152 && q_tiles >= 4 * cs) cs *= 2;
+  if (cs == 4 && units <= 15 && q_tiles >= 16) cs = 8;
   cudaLaunchConfig_t cfg = {};
   if (units * cs > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cfg.gridDim = dim3((unsigned)(units * cs));

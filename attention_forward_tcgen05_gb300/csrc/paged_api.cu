@@ -39,7 +39,7 @@ int check_heads(int B, int Hq, int Hkv) {
 
 attn::PagedKV cache(const attn_bf16_t* k, const attn_bf16_t* v, const int* table, int max_pages, int page_size,
                     int num_pages) {
-  return attn::PagedKV{k, v, table, max_pages, page_size, num_pages};
+  return attn::PagedKV{k, v, table, max_pages, page_size, num_pages, 0};
 }
 
 // Query heads that share a tile of `rows` rows: the largest divisor of G whose whole
@@ -166,6 +166,11 @@ int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const at
   rc = attn::encode_q_map(&a.tm_q, q, d, a.pack, Hq, total_q, 1, attn::kPrefillTileM);
   a.o_tma = (o_dtype == ATTN_BF16 && n_splits <= 1) ? 1 : 0;
   if (rc == ATTN_OK && a.o_tma) rc = attn::encode_q_map(&a.tm_o, o, d, a.pack, Hq, total_q, 1, attn::kPrefillTileM);
+  a.kv.box_rows = page_size % 128 == 0 ? 128 : (page_size % 64 == 0 ? 64 : 0);
+  if (rc == ATTN_OK && a.kv.box_rows > 0) {
+    rc = attn::encode_pool_map(&a.tm_k, kcache, d, Hkv, page_size, num_pages, a.kv.box_rows);
+    if (rc == ATTN_OK) rc = attn::encode_pool_map(&a.tm_v, vcache, d, Hkv, page_size, num_pages, a.kv.box_rows);
+  }
   if (rc != ATTN_OK) return rc;
   rc = from_cuda(attn::launch_prefill_paged(a, stream_of(stream)));
   if (rc != ATTN_OK || n_splits == 1) return rc;

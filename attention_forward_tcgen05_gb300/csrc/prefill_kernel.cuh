@@ -162,8 +162,9 @@ __device__ __forceinline__ TileInfo tile_info(int q0, int Sr, int Sq, int G, int
 // position, its G <= 128 head rows):
 // both query tiles hold the same rows and take the two halves of the unit's keys,
 // so their S -> softmax -> P.V chains overlap; the halves merge in the epilogue.
-// PAGED (packed varlen batches): K/V rows come from the pages of kv, gathered by the
-// producer warps (paged.cuh), rows past the sequence's keys as zeros; a query tile
+// PAGED (packed varlen batches): K/V rows come from the pages of kv, by tensor copies of
+// kv.box_rows rows or gathered by the producer warps (paged.cuh), rows past the sequence's
+// keys as zeros; a query tile
 // holds floor(128 / G) whole positions (any G), and key splits start on a KV tile.
 template <int D, bool WIN, bool SPLIT, bool HALVES, bool PAGED>
 __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
@@ -353,7 +354,58 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
       uint64_t* const full = is_k ? bar_fullK : bar_fullV;
       uint64_t* const empty = is_k ? bar_emptyK : bar_emptyV;
       uint8_t* const ring = is_k ? sK : sV;
-      if constexpr (PAGED) {
+      const CUtensorMap* const map = is_k ? &tm_k : &tm_v;
+      if (PAGED && kv.box_rows > 0) {
+        // Pages of whole 64-row boxes: tensor copies, 128 / box_rows a panel.  (A page that
+        // is none is out of the map's bounds: zeros.)  The tile with the sequence's last
+        // keys is gathered, so that rows past them arrive as zeros.
+        const int boxes = C::kStageRows / kv.box_rows;
+        const int* const tab = kv.table + (size_t)b * kv.max_pages;
+        int u = 0;
+        for (; u < n_st; ++u) {
+          const int s = u % stages;
+          const int key0 = item_key(u) * C::kStageRows;
+          const bool whole = key0 + C::kStageRows <= Skv;
+          int page[2], slot[2];  // of each box, read before the wait
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (whole && x < boxes) {
+              const int j = key0 + x * kv.box_rows, e = j / kv.page_size;
+              page[x] = __ldg(tab + e);
+              slot[x] = j - e * kv.page_size;
+              if ((unsigned)page[x] >= (unsigned)kv.num_pages && lane == 0) atomicCAS(err, kErrNone, kErrBadShape);
+            }
+          }
+          if (!mbar_wait_warp(&empty[s], ((uint32_t)(u / stages) & 1u) ^ 1u, err, abort_flag)) break;
+          if (whole) {
+            mbar_arrive_expect_tx_e(&full[s], C::kKVStageBytes);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (x < boxes) {
+#pragma unroll
+                for (int p = 0; p < C::kPanels; ++p)
+                  tma_load_4d_e(ring + s * C::kKVStageBytes + p * C::kKVPanelBytes + x * kv.box_rows * 128, map,
+                                &full[s], p * 64, hk, slot[x], page[x]);
+              }
+            }
+          } else {
+            constexpr int NR = C::kStageRows / 32;
+            int ri[NR];
+            paged_rows<NR>(kv, b, key0, Skv, lane, err, ri);
+            paged_gather<D, NR>(smem_u32(ring + s * C::kKVStageBytes), C::kKVPanelBytes, is_k ? kv.k : kv.v, Hkv, hk,
+                                lane, ri);
+            cp_async_commit();
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+          }
+        }
+        if (u < n_st) {
+          for (int u2 = max(0, u - stages); u2 < u; ++u2)
+            mbar_wait(&full[u2 % stages], (uint32_t)(u2 / stages) & 1u, nullptr, nullptr, 100000000ull);
+        }
+      } else if constexpr (PAGED) {
         // The warp gathers a stage (128 rows) and hands it over when its copies have
         // landed and are fenced for the tensor core's reads; the copies of one more
         // stage stay in flight meanwhile, unless the ring is full.
@@ -385,7 +437,6 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
         cp_async_wait<0>();
         hand_over(u);
       } else {
-      const CUtensorMap* const map = is_k ? &tm_k : &tm_v;
       int u = 0;
       for (; u < n_st; ++u) {
         const int s = u % stages;

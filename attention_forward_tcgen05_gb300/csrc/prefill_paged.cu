@@ -22,7 +22,7 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t stream) {
   const long long units = n_blocks_q * (a.Hq / G) * a.B * n_splits;
   if (units > 0x7FFFFFFFLL || rows > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   kern<<<(unsigned)units, C::kThreads, C::kSmemBytes, stream>>>(
-      a.tm_q, a.tm_q, a.tm_q, a.tm_o, a.o_tma, a.o, a.lse, a.Hq, a.Hkv, a.Sq, a.Skv, a.causal, a.o_bf16, a.scale,
+      a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.o_tma, a.o, a.lse, a.Hq, a.Hkv, a.Sq, a.Skv, a.causal, a.o_bf16, a.scale,
       (a.Hq / G) * a.B, a.err, a.cu_q, a.kv_lens, a.total_q, a.window, a.n_sink, G, n_splits, a.split_min,
       a.part_o, a.part_lse, 0, 0, a.kv);
   return cudaGetLastError();
