@@ -73,7 +73,7 @@ def load(path: str | None = None):
         ll = ctypes.c_longlong
         lib.attn_rope_append.argtypes = [vp] * 3 + [ll] * 3 + [vp] * 8 + [i] * 7 + [f] + [i] * 3 + [vp]
         lib.attn_prefill_paged.argtypes = [vp] * 8 + [i] * 12 + [f, i, i, vp, vp, i, vp]
-        lib.attn_prefill_paged_splits.argtypes = [i] * 7
+        lib.attn_prefill_paged_splits.argtypes = [i] * 7 + [vp]
         lib.attn_decode_paged.argtypes = [vp] * 5 + [i] * 7 + [f, i, i, vp, vp, vp, vp, i, vp, vp]
         lib.attn_decode_paged_splits.argtypes = [i] * 5 + [vp]
         lib.attn_key_weights.argtypes = [vp] * 7 + [ll] + [i] * 12 + [f, i, vp]

@@ -28,8 +28,8 @@ def attn_prefill_paged(*args) -> int:
     return load().attn_prefill_paged(*args)
 
 
-def attn_prefill_paged_splits(B, Hq, Hkv, total_q, max_sq, max_kv, d) -> int:
-    return load().attn_prefill_paged_splits(B, Hq, Hkv, total_q, max_sq, max_kv, d)
+def attn_prefill_paged_splits(B, Hq, Hkv, total_q, max_sq, max_kv, d, min_rows) -> int:
+    return load().attn_prefill_paged_splits(B, Hq, Hkv, total_q, max_sq, max_kv, d, min_rows)
 
 
 def attn_decode_paged(*args) -> int:
@@ -291,8 +291,11 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
         if parts is not None:
             n_splits = parts[0].shape[2]
         elif not window:
+            rows = ctypes.c_int(1)
             n_splits = max(1, lib.attn_prefill_paged_splits(B, Hq, Hkv, total, max_sq,
-                                                            max_pages * page if max_kv is None else max_kv, d))
+                                                            max_pages * page if max_kv is None else max_kv, d,
+                                                            ctypes.addressof(rows)))
+            min_rows_per_split = rows.value
     pp = ps = None
     if n_splits > 1:
         if parts is None:  # both partials in one allocation

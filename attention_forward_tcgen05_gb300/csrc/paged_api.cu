@@ -93,29 +93,35 @@ int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16
   return from_cuda(attn::launch_rope_append(a, stream_of(stream)));
 }
 
-int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, int max_kv, int d) {
-  if (check_heads(B, Hq, Hkv) != ATTN_OK || total_q < 0 || max_sq < 0 || max_kv < 0 || !ok_dim(d))
+int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, int max_kv, int d, int* min_rows) {
+  if (check_heads(B, Hq, Hkv) != ATTN_OK || total_q < 0 || max_sq < 0 || max_kv < 0 || !ok_dim(d) ||
+      min_rows == nullptr)
     return ATTN_ERR_INVALID_ARG;
-  const int G = Hq / Hkv, pack = pack_heads(G, attn::kPrefillTileM), pos = attn::kPrefillTileM / pack;
+  const int pack = pack_heads(Hq / Hkv, attn::kPrefillTileM), pos = attn::kPrefillTileM / pack;
   const bool halves = d <= 128 && max_sq <= pos;
-  // blocks of query rows that exist, one unit each, and a unit's time over all keys
+  // blocks of query rows that exist, one unit each, and a unit's time for a tile of keys
   const long long block = d <= 128 && !halves ? 2 * pos : pos;
   const long long blocks = std::min<long long>((long long)total_q / block + B, (max_sq + block - 1) / block * B);
   const long long units = std::max(1LL, blocks * (Hq / pack));
-  const double tile_us = (d == 64 ? 0.7 : d == 128 ? 1.0 : 1.2) * (halves ? 0.5 : 1.0);
+  const double tile_us = halves ? 1.2 : (d == 64 ? 1.4 : 1.8);
   const double tiles = (max_kv + 127) / 128;
+  // a batch's sequences are taken to be 0.6 of the longest on average
+  const double mean = B > 1 ? 0.6 : 1.0;
   double best = 0;
   int n_best = 1;
   for (int n = 1; n <= 32 && n <= std::max(1.0, tiles / 2); ++n) {
-    const double waves = (double)((units * n + kSms - 1) / kSms);
-    // each unit's own start and end; the partials out and in again, and the merge's launch
-    const double us = waves * (tiles / n * tile_us + 3.0) +
-                      (n > 1 ? 4.0 + (double)total_q * Hq * d * 8.0 * n / 5.0e6 : 0.0);
+    const double rows = std::ceil(tiles / n);  // of a split, in tiles
+    const double live = (double)units * std::max(1.0, std::min((double)n, mean * tiles / rows + (n > 1 && B > 1 ? 0.5 : 0)));
+    // waves of units, each with its own start and end; the partials out and in again, and
+    // the merge's launch
+    const double us = std::ceil(live / kSms) * (rows * tile_us + 4.0) +
+                      (n > 1 ? 4.0 + (double)total_q * Hq * d * 8.0 * n * mean / 5.0e6 : 0.0);
     if (n == 1 || us < best * 0.97) {
       best = us;
       n_best = n;
     }
   }
+  *min_rows = (int)std::ceil(tiles / n_best) * 128;
   return n_best;
 }
 
@@ -166,7 +172,12 @@ int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const at
   rc = attn::encode_q_map(&a.tm_q, q, d, a.pack, Hq, total_q, 1, attn::kPrefillTileM);
   a.o_tma = (o_dtype == ATTN_BF16 && n_splits <= 1) ? 1 : 0;
   if (rc == ATTN_OK && a.o_tma) rc = attn::encode_q_map(&a.tm_o, o, d, a.pack, Hq, total_q, 1, attn::kPrefillTileM);
-  a.kv.box_rows = page_size % 128 == 0 ? 128 : (page_size % 64 == 0 ? 64 : 0);
+  // Tensor copies of the largest power of two of rows (8 to 128; the swizzle repeats every 8)
+  // that divides the page; other pages are gathered.  Pages of 16 / 64 keys, copies against
+  // gathers: 164 / 162 against 248 / 242 us (eight chunks, 145 GFLOP), the same to 128 rows: the
+  // producer warps' instructions are what the softmax warps miss.
+  for (a.kv.box_rows = 128; a.kv.box_rows >= 8 && page_size % a.kv.box_rows != 0;) a.kv.box_rows /= 2;
+  if (a.kv.box_rows < 8) a.kv.box_rows = 0;
   if (rc == ATTN_OK && a.kv.box_rows > 0) {
     rc = attn::encode_pool_map(&a.tm_k, kcache, d, Hkv, page_size, num_pages, a.kv.box_rows);
     if (rc == ATTN_OK) rc = attn::encode_pool_map(&a.tm_v, vcache, d, Hkv, page_size, num_pages, a.kv.box_rows);

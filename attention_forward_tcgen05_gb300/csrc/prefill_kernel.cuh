@@ -220,6 +220,14 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
     const long long lo = (long long)sp * chunk;
     klo = (int)min((long long)Skv, lo);
     khi = (int)min((long long)Skv, lo + chunk);
+    if (PAGED && klo >= khi) {  // an empty split: the merge reads only its lse
+      for (int r = threadIdx.x; r < NQ * TR; r += C::kThreads) {
+        const int row = qb * NQ * TR + r;
+        if (row < Sr)
+          part_lse[((size_t)(ext.qbase + row / G) * Hq + hu * G + row % G) * NSPL + sp] = -INFINITY;
+      }
+      return;
+    }
   }
 
   extern __shared__ uint8_t smem_raw[];
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
       uint8_t* const ring = is_k ? sK : sV;
       const CUtensorMap* const map = is_k ? &tm_k : &tm_v;
       if (PAGED && kv.box_rows > 0) {
-        // Pages of whole 64-row boxes: tensor copies, 128 / box_rows a panel.  (A page that
+        // Pages of whole boxes: tensor copies, 128 / box_rows a panel.  (A page that
         // is none is out of the map's bounds: zeros.)  The tile with the sequence's last
         // keys is gathered, so that rows past them arrive as zeros.
         const int boxes = C::kStageRows / kv.box_rows;
@@ -366,27 +374,22 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
           const int s = u % stages;
           const int key0 = item_key(u) * C::kStageRows;
           const bool whole = key0 + C::kStageRows <= Skv;
-          int page[2], slot[2];  // of each box, read before the wait
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (whole && x < boxes) {
-              const int j = key0 + x * kv.box_rows, e = j / kv.page_size;
-              page[x] = __ldg(tab + e);
-              slot[x] = j - e * kv.page_size;
-              if ((unsigned)page[x] >= (unsigned)kv.num_pages && lane == 0) atomicCAS(err, kErrNone, kErrBadShape);
-            }
+          int page = 0, slot = 0;  // lane x: of box x, read before the wait
+          if (whole && lane < boxes) {
+            const int j = key0 + lane * kv.box_rows, e = j / kv.page_size;
+            page = __ldg(tab + e);
+            slot = j - e * kv.page_size;
+            if ((unsigned)page >= (unsigned)kv.num_pages) atomicCAS(err, kErrNone, kErrBadShape);
           }
           if (!mbar_wait_warp(&empty[s], ((uint32_t)(u / stages) & 1u) ^ 1u, err, abort_flag)) break;
           if (whole) {
             mbar_arrive_expect_tx_e(&full[s], C::kKVStageBytes);
+            for (int x = 0; x < boxes; ++x) {
+              const int pg = __shfl_sync(0xFFFFFFFFu, page, x), sl = __shfl_sync(0xFFFFFFFFu, slot, x);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (x < boxes) {
-#pragma unroll
-                for (int p = 0; p < C::kPanels; ++p)
-                  tma_load_4d_e(ring + s * C::kKVStageBytes + p * C::kKVPanelBytes + x * kv.box_rows * 128, map,
-                                &full[s], p * 64, hk, slot[x], page[x]);
-              }
+              for (int p = 0; p < C::kPanels; ++p)
+                tma_load_4d_e(ring + s * C::kKVStageBytes + p * C::kKVPanelBytes + x * kv.box_rows * 128, map,
+                              &full[s], p * 64, hk, sl, pg);
             }
           } else {
             constexpr int NR = C::kStageRows / 32;

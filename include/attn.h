@@ -447,7 +447,8 @@ int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16
  * K/V row is gathered once per group.  n_splits > 1 (window = 0 only) cuts each sequence's
  * keys as attn_decode_split does, each split's rows rounded up to 128, and joins the
  * partials part_o fp32 [total_q][Hq][n_splits][d], part_lse fp32 [total_q][Hq][n_splits]
- * in a second launch; with n_splits = 1 they may be NULL.
+ * in a second launch (part_o of an empty split is left unwritten); with n_splits = 1 they may
+ * be NULL.
  *
  * Arguments: as attn_prefill_varlen, with page_table int32 [B][max_pages]; d in
  * {64, 128, 256}; max_sq * Hq / Hkv < 2^30.
@@ -459,9 +460,10 @@ int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const at
                        int window, int n_sink, float scale, int n_splits, int min_rows_per_split, float* part_o,
                        float* part_lse, int o_dtype, attn_stream_t stream);
 
-/* The n_splits (>= 1) that suits a prefill of these sizes, max_kv keys in the longest
- * sequence (host only); ATTN_ERR_INVALID_ARG for bad sizes. */
-int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, int max_kv, int d);
+/* The n_splits (>= 1) and min_rows_per_split that suit a prefill of these sizes, max_kv
+ * keys in the longest sequence (host only); ATTN_ERR_INVALID_ARG for bad sizes. */
+int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, int max_kv, int d,
+                              int* min_rows_per_split);
 
 /*
  * attn_decode_paged -- attn_decode over a paged cache: one launch, the same split rule,
