@@ -343,14 +343,21 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
             n_splits = lib.attn_decode_paged_splits(B, Hq, Hkv, max_pages * page if max_kv is None else max_kv, d,
                                                     ctypes.addressof(rows))
             min_rows_per_split = rows.value
-    if parts is None:  # both partials in one allocation
-        rows = B * Hq * n_splits
-        work = torch.empty(rows * (d + 1), dtype=torch.float32, device="cuda")
-        pp = work.data_ptr()
-        ps = pp + rows * d * 4
-    else:
-        pp = _sized(parts[0], "parts[0]", torch.float32, dev, B, Hq, n_splits, d)
-        ps = _sized(parts[1], "parts[1]", torch.float32, dev, B, Hq, n_splits)
+    pp = ps = cp = None
+    if n_splits > 1:
+        if parts is None:  # both partials in one allocation
+            rows = B * Hq * n_splits
+            work = torch.empty(rows * (d + 1), dtype=torch.float32, device="cuda")
+            pp = work.data_ptr()
+            ps = pp + rows * d * 4
+        else:
+            pp = _sized(parts[0], "parts[0]", torch.float32, dev, B, Hq, n_splits, d)
+            ps = _sized(parts[1], "parts[1]", torch.float32, dev, B, Hq, n_splits)
+        if counters is None:
+            counters = _stream_counters(B * Hq, dev, handle)
+        elif counters.dtype != torch.int32 or counters.get_device() != dev or counters.numel() < B * Hq:
+            raise TypeError("counters must be a CUDA int32 tensor of at least B*Hq entries")
+        cp = counters.data_ptr()
     if out is None:
         o = torch.empty((B, Hq, d), dtype=out_dtype or torch.bfloat16, device="cuda")
         lse = torch.empty((B, Hq), dtype=torch.float32, device="cuda")
@@ -360,12 +367,8 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
         op = _sized(o, "out[0]", o.dtype, dev, B, Hq, d)
         lp = _sized(lse, "out[1]", torch.float32, dev, B, Hq)
     code = _out_code(o.dtype)
-    if counters is None:
-        counters = _stream_counters(B * Hq, dev, handle)
-    elif counters.dtype != torch.int32 or counters.get_device() != dev or counters.numel() < B * Hq:
-        raise TypeError("counters must be a CUDA int32 tensor of at least B*Hq entries")
     rc = lib.attn_decode_paged(qp, kp, vp, tp, np_, B, Hq, Hkv, d, max_pages, page, n_pages, scale, n_splits,
-                               min_rows_per_split, pp, ps, op, lp, code, counters.data_ptr(), handle)
+                               min_rows_per_split, pp, ps, op, lp, code, cp, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged")
     return o, lse

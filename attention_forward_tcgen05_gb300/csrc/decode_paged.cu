@@ -1,5 +1,5 @@
 // decode_paged.cu -- one-token GQA decode over a paged cache: split-KV partials and their
-// LSE-weighted merge in one launch, the split rule, launch order and combine of decode.cu.
+// LSE-weighted merge in one launch, the split rule and combine of decode.cu.
 //
 // One CTA per (sequence, KV head, split, group of up to 16 query heads); its four warps take
 // 32-key runs of the split in turn and share nothing until the end.  Each warp gathers 16
@@ -28,22 +28,28 @@ namespace {
 constexpr int kWarps = 4;
 constexpr float kMoveThreshold = 8.f;  // log2: the reference m moves when a score exceeds it by 2^8
 
+// CTAs of one SM (also the split rule's)
+constexpr int decode_paged_ctas(int d, int nb) { return d == 256 ? 1 : (nb == 1 ? 3 : 2); }
+
 template <int D, int NB>
 struct DecodePagedCfg {
   static constexpr int kHeads = 8 * NB;
   static constexpr int kPanel = 16 * 128;          // one 64-column panel of 16 keys
   static constexpr int kTile = 16 * D * 2;         // K or V of 16 keys
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = D == 64 ? 6 : 3;  // a warp's ring: 24, 24, 48 KB
+  // a warp's ring (16, 16 or 24, 48 KB) and the CTAs of an SM: with heads for one mma side,
+  // three small CTAs hide one another's start and end (1024 units of about 550 keys: 51 us
+  // against 53 with two of three stages; 64 ragged sequences of up to 8192: 192 against 210)
+  static constexpr int kStages = D == 64 ? 4 : (D == 128 && NB == 1 ? 2 : 3);
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kComb = kWarps * kHeads * (D + 2) * 4;
   static constexpr int kSmem = (kRing > kComb ? kRing : kComb) + 1024;
-  static constexpr int kMinBlocks = D == 256 ? 1 : 2;
+  static constexpr int kMinBlocks = decode_paged_ctas(D, NB);
 };
 
 template <int D, int NB>
 __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks)
-    decode_paged_kernel(const DecodeArgs a, int heads_per_cta, int ordered) {
+    decode_paged_kernel(const DecodeArgs a, int heads_per_cta) {
   using C = DecodePagedCfg<D, NB>;
   constexpr int ST = C::kStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -52,19 +58,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
   const int pos = (int)(blockIdx.x / per_unit), w_in = (int)(blockIdx.x % per_unit);
   const int hk = w_in / n_hg, g0 = w_in % n_hg * heads_per_cta;
   const int G = min(heads_per_cta, Gall - g0);
-  int b, s_idx;
-  if (ordered) {
-    const int2 u = unit_at(pos, a.kv_lens, a.B, a.max_kv, a.n_splits, a.min_rows, lane);
-    b = u.x;
-    s_idx = u.y;
-    if (b < 0) {  // kv_lens changed while the launch ran (see decode.cu): reported, nothing written
-      if (threadIdx.x == 0) atomicCAS(a.err, kErrNone, kErrBadShape);
-      return;
-    }
-  } else {
-    b = pos / a.n_splits;
-    s_idx = pos % a.n_splits;
-  }
+  const int b = pos / a.n_splits, s_idx = pos % a.n_splits;
   int L = a.kv_lens[b];
   L = L < 0 ? 0 : (L > a.max_kv ? a.max_kv : L);
   long long chunk = ((long long)L + a.n_splits - 1) / a.n_splits;
@@ -77,12 +71,20 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
-  if (lo >= hi) {  // empty split: o = 0, lse = -inf
-    for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
-      const size_t row = (orow0 + i / D) * a.n_splits + s_idx;
-      a.part_o[row * D + i % D] = 0.f;
-      if (i % D == 0) a.part_lse[row] = -INFINITY;
+  // one split is the result itself: no partials, no merge
+  auto put = [&](int g, int t, float x, float lse) {
+    const size_t row = orow0 + g;
+    if (a.n_splits > 1) {
+      a.part_o[(row * a.n_splits + s_idx) * D + t] = x;
+      if (t == 0) a.part_lse[row * a.n_splits + s_idx] = lse;
+    } else {
+      if (a.o_bf16) reinterpret_cast<uint16_t*>(a.o)[row * D + t] = (uint16_t)pack_bf16x2(x, 0.f);
+      else reinterpret_cast<float*>(a.o)[row * D + t] = x;
+      if (t == 0) a.lse[row] = lse;
     }
+  };
+  if (lo >= hi) {  // empty split: o = 0, lse = -inf
+    for (int i = threadIdx.x; i < G * D; i += kWarps * 32) put(i / D, i % D, 0.f, -INFINITY);
   } else {
     uint8_t* ring = smem + warp * ST * C::kStage;
     // this warp's 16-key steps: step i covers keys from lo + ((i / 2) * kWarps + warp) * 32 + (i % 2) * 16
@@ -236,11 +238,10 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
         ls = fmaf(cw[D + 1], f, ls);
         acc = fmaf(cw[t], f, acc);
       }
-      const size_t row = (orow0 + g) * a.n_splits + s_idx;
-      a.part_o[row * D + t] = acc / ls;
-      if (t == 0) a.part_lse[row] = (M + log2f(ls)) * kLn2;
+      put(g, t, acc / ls, (M + log2f(ls)) * kLn2);
     }
   }
+  if (a.n_splits == 1) return;
   combine_if_last<D, kWarps>(a.done + orow0, a.n_splits, a.part_o, a.part_lse, a.o, a.lse, orow0, G, a.o_bf16,
                              [] { __syncthreads(); });
 }
@@ -254,9 +255,7 @@ cudaError_t launch_t(const DecodeArgs& a, int heads_per_cta, cudaStream_t stream
   const int n_hg = (a.Hq / a.Hkv + heads_per_cta - 1) / heads_per_cta;
   const long long ctas = (long long)a.B * a.n_splits * a.Hkv * n_hg;
   if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  // longest splits first (one sequence has nothing to order)
-  const int ordered = a.B > 1 && a.B <= kOrderMaxBatch ? 1 : 0;
-  kern<<<(unsigned)ctas, kWarps * 32, C::kSmem, stream>>>(a, heads_per_cta, ordered);
+  kern<<<(unsigned)ctas, kWarps * 32, C::kSmem, stream>>>(a, heads_per_cta);
   return cudaGetLastError();
 }
 
@@ -269,6 +268,11 @@ cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+int decode_paged_slots(int d, int G, int sms) {
+  const int n_hg = (G + 15) / 16, hpc = (G + n_hg - 1) / n_hg;
+  return sms * decode_paged_ctas(d, hpc <= 8 ? 1 : 2);
+}
 
 cudaError_t launch_decode_paged(const DecodeArgs& a, cudaStream_t stream) {
   switch (a.d) {

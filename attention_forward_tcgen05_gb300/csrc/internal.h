@@ -253,6 +253,8 @@ cudaError_t launch_prefill_paged(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_empty_kv(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_split(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_paged(const DecodeArgs& a, cudaStream_t stream);
+// CTAs of that kernel that `sms` SMs run at once.
+int decode_paged_slots(int d, int G, int sms);
 // The persistent prefill's unit schedule for BH = B * Hq heads over `grid` CTAs:
 // sched = offsets[grid + 1] followed by each CTA's units; returns the unit count,
 // 0 when the launch keeps the wave deal (sched left empty), -1 on bad arguments.

@@ -196,15 +196,16 @@ int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const at
 
 int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int* min_rows) {
   if (check_heads(B, Hq, Hkv) != ATTN_OK || max_kv < 0 || !ok_dim(d) || min_rows == nullptr) return ATTN_ERR_INVALID_ARG;
-  const long long units = std::max(1LL, (long long)B * Hkv);
-  long long rows = std::max(128LL, (long long)max_kv * units / (16 * kSms));
-  rows = (rows + 63) / 64 * 64;
-  long long n = std::max(1LL, (max_kv + rows - 1) / rows);
-  if (n > 64) {
-    n = 64;
-    rows = ((max_kv + n - 1) / n + 63) / 64 * 64;
-  }
-  *min_rows = (int)rows;
+  // as many CTAs as run at once: one wave, its splits at least 192 rows; beyond 48 splits the
+  // merge takes longer than the keys it saves.  A batch's lengths differ, so a few splits are
+  // rounded up (64 units of up to 8000 keys: 57 us with 3 splits, 78 with 2); from half a wave
+  // of units on, whole sequences do best (1024 units of up to 1000 keys: 51 against 59 us).
+  const int G = Hq / Hkv;
+  const double units = std::max(1.0, (double)B * Hkv * ((G + 15) / 16));
+  const double q = attn::decode_paged_slots(d, G, kSms) / units;
+  long long n = q < 2 ? 1 : (long long)(q <= 8 && B > 1 ? std::ceil(q) : q);
+  n = std::max(1LL, std::min(std::min(n, 48LL), (max_kv + 191LL) / 192));
+  *min_rows = n > 1 ? 192 : 1;
   return (int)n;
 }
 
@@ -218,10 +219,11 @@ int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const att
   if (rc == ATTN_OK)
     // (the dense cache's row limit does not apply: max_kv = 1 here)
     rc = attn::check_decode_split_args(q, kcache, vcache, kv_lens, B, Hq, Hkv, d, 1, scale, n_splits,
-                                       min_rows_per_split, part_o, part_lse, true);
-  if (rc == ATTN_OK) rc = attn::check_merge_args(part_o, part_lse, o, lse, B, Hq, n_splits, d, o_dtype, true);
+                                       min_rows_per_split, part_o, part_lse, n_splits > 1);
+  if (rc == ATTN_OK)
+    rc = attn::check_merge_args(part_o, part_lse, o, lse, B, Hq, n_splits, d, o_dtype, n_splits > 1);
   if (rc != ATTN_OK || B == 0) return rc;
-  if (!ok4(counters) || !ok4(page_table)) return ATTN_ERR_INVALID_ARG;
+  if (!ok4(page_table) || (n_splits > 1 && !ok4(counters))) return ATTN_ERR_INVALID_ARG;
   attn::DecodeArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = q; a.kv_lens = kv_lens; a.part_o = part_o; a.part_lse = part_lse;

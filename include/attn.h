@@ -467,7 +467,8 @@ int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, i
 
 /*
  * attn_decode_paged -- attn_decode over a paged cache: one launch, the same split rule,
- * partials, counters and results.
+ * partials, counters and results (to rounding).  With n_splits = 1 the result is written
+ * directly: part_o, part_lse and counters are not touched and may be NULL.
  *
  * Arguments: as attn_decode, with page_table int32 [B][max_pages] and pools
  * [num_pages][page_size][Hkv][d] in place of the caches and max_kv.
