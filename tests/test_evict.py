@@ -216,8 +216,8 @@ def test_evict(d, kind, budget, n_recent, n_sink, where):
         assert torch.equal(wg.cpu().view(torch.int32), w.view(torch.int32))
 
 
-def test_evict_row_longer_than_shared_memory():
-    """60,000 keys: weights are read again from memory instead of shared memory."""
+def test_evict_rows_of_several_blocks():
+    """60,000 keys: four blocks of weights, three of them read again at each pass."""
     L, d = 60000, 64
     g = torch.Generator().manual_seed(5)
     kc = torch.randn(1, L, 1, d, generator=g).bfloat16()
