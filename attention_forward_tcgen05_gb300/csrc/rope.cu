@@ -50,104 +50,110 @@ __device__ __forceinline__ void rotate_inter(uint4& a, const float2* cs) {
   }
 }
 
-// One CTA takes `tokens` consecutive tokens.  A work item is two chunks of one head: the
-// two partners of the half layout, or two neighbours.  rot = 0 copies.
-template <bool INTER>
-__global__ void __launch_bounds__(kThreads)
-    rope_append_kernel(const RopeArgs a, int tokens) {
-  __shared__ unsigned long long turn[128];  // f_i / 2 pi, units of 2^-64 turns
-  __shared__ float2 cs[128];                // (cos, sin) * amp of the token's pairs
-  __shared__ int where[2];                  // cache row of the token (-1: none), its sequence's end
-  const int half = a.rot / 2;
+// One CTA takes up to kTokens consecutive tokens: their places in the cache (a chain of
+// dependent loads) and their angles are found side by side, and the copies of all of them
+// follow without a barrier between.  A work item is two chunks of one head: the two partners
+// of the half layout, or two neighbours.  rot = 0 copies.
+template <bool INTER, int kTokens>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a) {
+  __shared__ unsigned long long turn[128];       // f_i / 2 pi, units of 2^-64 turns
+  __shared__ float2 cs[kTokens * 128];           // (cos, sin) * amp of each token's pairs
+  __shared__ int place[kTokens], at[kTokens];    // cache row (-1: none, -2: no sequence), position
+  const int half = a.rot / 2, t0 = blockIdx.x * kTokens, nt = min(kTokens, a.total - t0);
   for (int i = threadIdx.x; i < half; i += kThreads) {
     const double x = a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
     turn[i] = (unsigned long long)((x - floor(x)) * 18446744073709551616.0);
   }
+  if ((int)threadIdx.x >= kThreads - nt) {
+    // (the last threads, whose warp has no frequency to convert up to d = 256)
+    const int s = kThreads - 1 - (int)threadIdx.x, t = t0 + s;
+    // the token's sequence: the last b with cu[b] <= t (cu is non-decreasing)
+    int b = t, i = 0, n = 1;
+    bool live = t < a.B;
+    if (a.cu_q) {
+      int lo = 0, hi = a.B;  // cu[lo] <= t < cu[hi] (or t behind the last sequence)
+      live = t >= a.cu_q[0] && t < a.cu_q[a.B];
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
+      }
+      b = lo;
+      i = t - a.cu_q[b];
+      n = a.cu_q[b + 1] - a.cu_q[b];
+    }
+    int row = -2;  // behind the last sequence: the token's rows are left as they are
+    if (live) {
+      const long long cap = (long long)a.kv.max_pages * a.kv.page_size;
+      const long long j = (long long)a.kv_lens[b] - n + i;  // key index
+      if (j < 0 || j >= cap) {
+        atomicCAS(a.err, kErrNone, kErrBadShape);
+        row = -1;
+      } else {
+        row = paged_row(a.kv, b, (int)j, a.err);
+      }
+      at[s] = a.positions ? a.positions[t] : (int)j;
+    }
+    place[s] = row;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+    const int s = kTokens == 1 ? 0 : i / half, m = i - s * half;
+    const unsigned long long w = turn[m] * (unsigned long long)(long long)at[s];
+    const float x = (float)(int)(w >> 32) * 4.656612873077393e-10f;  // half turns in [-1, 1): 2^-31
+    float sn, c;
+    sincospif(x, &sn, &c);
+    cs[s * 128 + m] = make_float2(c * a.amp, sn * a.amp);
+  }
+  __syncthreads();
   const int cpr = a.d / 8, rc = a.rot / 8;  // chunks of a head, rotated ones (rot % 16 == 0)
   const int n_q = a.q ? a.Hq : 0;
   const int ipr = cpr / 2;  // items of a head
   const int items = (n_q + 2 * a.Hkv) * ipr;
-  const int t_end = min(a.total, (int)(blockIdx.x + 1) * tokens);
-  for (int t = blockIdx.x * tokens; t < t_end; ++t) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      // the token's sequence: the last b with cu[b] <= t (cu is non-decreasing)
-      int b = t, i = 0, n = 1;
-      bool live = t < a.B;
-      if (a.cu_q) {
-        int lo = 0, hi = a.B;  // cu[lo] <= t < cu[hi] (or t behind the last sequence)
-        live = t >= a.cu_q[0] && t < a.cu_q[a.B];
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) / 2;
-          if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
-        }
-        b = lo;
-        i = t - a.cu_q[b];
-        n = a.cu_q[b + 1] - a.cu_q[b];
+#pragma unroll 2
+  for (int it = threadIdx.x; it < nt * items; it += kThreads) {
+    const int s = kTokens == 1 ? 0 : it / items, in = it - s * items, t = t0 + s;
+    const int h = in / ipr, x = in - h * ipr;
+    const int row = place[s];
+    const bool is_q = h < n_q, is_k = !is_q && h < n_q + a.Hkv;
+    const int hk = is_q ? 0 : (is_k ? h - n_q : h - n_q - a.Hkv);
+    if (row == -2 || (!is_q && row < 0)) continue;  // no sequence, or no place in the cache
+    const uint16_t* src = is_q ? a.q + (size_t)t * a.q_stride + (size_t)h * a.d
+                               : (is_k ? a.k + (size_t)t * a.k_stride + (size_t)hk * a.d
+                                       : a.v + (size_t)t * a.v_stride + (size_t)hk * a.d);
+    uint16_t* dst = is_q ? a.q_out + ((size_t)t * a.Hq + h) * a.d
+                         : (is_k ? a.kc : a.vc) + ((size_t)row * a.Hkv + hk) * a.d;
+    // the item's chunks: rotated partners (c, c + rc/2) first, then the rest two by two
+    int c0, c1;
+    if (!INTER && x < rc / 2) { c0 = x; c1 = x + rc / 2; }
+    else { c0 = 2 * x; c1 = 2 * x + 1; }
+    uint4 u0 = *reinterpret_cast<const uint4*>(src + c0 * 8), u1 = *reinterpret_cast<const uint4*>(src + c1 * 8);
+    if (is_q || is_k) {
+      const float2* c = cs + s * 128;
+      if (INTER) {
+        if (c0 < rc) rotate_inter(u0, c + c0 * 4);
+        if (c1 < rc) rotate_inter(u1, c + c1 * 4);
+      } else if (x < rc / 2) {
+        rotate_half(u0, u1, c + c0 * 8);
       }
-      int row = -2;  // behind the last sequence: the token's rows are left as they are
-      if (live) {
-        const long long cap = (long long)a.kv.max_pages * a.kv.page_size;
-        const long long j = (long long)a.kv_lens[b] - n + i;  // key index
-        if (j < 0 || j >= cap) {
-          atomicCAS(a.err, kErrNone, kErrBadShape);
-          row = -1;
-        } else {
-          row = paged_row(a.kv, b, (int)j, a.err);
-        }
-        where[1] = a.positions ? a.positions[t] : (int)j;
-      }
-      where[0] = row;
     }
-    __syncthreads();
-    const int row = where[0];
-    if (row == -2) continue;
-    const long long pos = where[1];
-    for (int i = threadIdx.x; i < half; i += kThreads) {
-      const unsigned long long w = turn[i] * (unsigned long long)pos;
-      const float x = (float)(int)(w >> 32) * 4.656612873077393e-10f;  // half turns in [-1, 1): 2^-31
-      float s, c;
-      sincospif(x, &s, &c);
-      cs[i] = make_float2(c * a.amp, s * a.amp);
-    }
-    __syncthreads();
-    for (int it = threadIdx.x; it < items; it += kThreads) {
-      const int h = it / ipr, x = it - h * ipr;
-      const bool is_q = h < n_q, is_k = !is_q && h < n_q + a.Hkv;
-      const int hk = is_q ? 0 : (is_k ? h - n_q : h - n_q - a.Hkv);
-      if (!is_q && row < 0) continue;  // no place in the cache
-      const uint16_t* src = is_q ? a.q + (size_t)t * a.q_stride + (size_t)h * a.d
-                                 : (is_k ? a.k + (size_t)t * a.k_stride + (size_t)hk * a.d
-                                         : a.v + (size_t)t * a.v_stride + (size_t)hk * a.d);
-      uint16_t* dst = is_q ? a.q_out + ((size_t)t * a.Hq + h) * a.d
-                           : (is_k ? a.kc : a.vc) + ((size_t)row * a.Hkv + hk) * a.d;
-      // the item's chunks: rotated partners (c, c + rc/2) first, then the rest two by two
-      int c0, c1;
-      if (!INTER && x < rc / 2) { c0 = x; c1 = x + rc / 2; }
-      else { c0 = 2 * x; c1 = 2 * x + 1; }
-      uint4 u0 = *reinterpret_cast<const uint4*>(src + c0 * 8), u1 = *reinterpret_cast<const uint4*>(src + c1 * 8);
-      if (is_q || is_k) {
-        if (INTER) {
-          if (c0 < rc) rotate_inter(u0, cs + c0 * 4);
-          if (c1 < rc) rotate_inter(u1, cs + c1 * 4);
-        } else if (x < rc / 2) {
-          rotate_half(u0, u1, cs + c0 * 8);
-        }
-      }
-      *reinterpret_cast<uint4*>(dst + c0 * 8) = u0;
-      *reinterpret_cast<uint4*>(dst + c1 * 8) = u1;
-    }
+    *reinterpret_cast<uint4*>(dst + c0 * 8) = u0;
+    *reinterpret_cast<uint4*>(dst + c1 * 8) = u1;
   }
+}
+
+template <int kTokens>
+cudaError_t launch_t(const RopeArgs& a, cudaStream_t stream) {
+  const unsigned grid = (unsigned)((a.total + kTokens - 1) / kTokens);
+  if (a.interleaved) rope_append_kernel<true, kTokens><<<grid, kThreads, 0, stream>>>(a);
+  else rope_append_kernel<false, kTokens><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream) {
-  const int tokens = 1;
-  const unsigned grid = (unsigned)((a.total + tokens - 1) / tokens);
-  if (a.interleaved) rope_append_kernel<true><<<grid, kThreads, 0, stream>>>(a, tokens);
-  else rope_append_kernel<false><<<grid, kThreads, 0, stream>>>(a, tokens);
-  return cudaGetLastError();
+  // one token a CTA while that leaves SMs idle, else eight
+  return a.total >= 8 * 152 * 2 ? launch_t<8>(a, stream) : launch_t<1>(a, stream);
 }
 
 }  // namespace attn
