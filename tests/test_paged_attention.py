@@ -130,7 +130,7 @@ def _run(case, **kw):
 
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("Hq,Hkv,page", [(4, 2, 16), (7, 1, 48), (5, 5, 128)])
+@pytest.mark.parametrize("Hq,Hkv,page", [(4, 2, 16), (7, 1, 48), (5, 5, 128), (2, 1, 8), (3, 1, 20), (1, 1, 1)])
 @pytest.mark.parametrize("seqs", [MIXED, SHORT], ids=["mixed", "short"])
 def test_chunks(d, causal, Hq, Hkv, page, seqs):
     case = _chunk_case(seqs, Hq, Hkv, d, page, 400 + d + page)
@@ -159,7 +159,7 @@ def test_chunk_head_groups(G):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("window,n_sink", [(1, 0), (100, 4), (256, 130), (2000, 7)])
 def test_chunk_window(d, window, n_sink):
-    for seqs, page in ((MIXED, 16), (SHORT, 48)):
+    for seqs, page in ((MIXED, 16), (SHORT, 48), (MIXED, 20)):
         case = _chunk_case(seqs, 7, 1, d, page, 450 + d + window)
         q, kc, vc, cu, kv = case[:5]
         scale = 1.0 / np.sqrt(d)
