@@ -158,30 +158,38 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) key_weights_rows_kernel(con
 // the query tile, each with a TMEM buffer of its own, read in two halves.  With eight warps
 // and one wait for all of S^T a query tile took 1.4 us, its warps mostly waiting together
 // for the buffers, barriers and loads; sixteen take 1.0 us, of which the exponentials are
-// 0.54.  Warp 16: MMA issue; warp 17: query tiles by TMA; warp 18: their lse by plain loads,
-// through a ring of its own, so that a query slot is free again as soon as the MMA has read
-// it (with one ring for both: 1.5 us).  The
+// 0.54.  Warps 16, 19: MMA issue, one key tile each
+// (a single warp's waits between the products left the tensor pipe idle for a third of the
+// time); warp 17: query tiles by TMA; warp 18: their lse, by plain loads
+// into sixteen further columns of the product, K' = (K, 1, 1, 1), Q' = (Q, -lse / scale in
+// three bf16 terms), so that S^T comes out as q . k - lse / scale: read from shared memory
+// under the exponentials instead, a value a column cost as many wavefronts as the MMA's
+// operands.  The
 // CTAs of a cluster share the keys and take every cs-th query tile; their sums meet in
 // rank 0, in rank order.
 template <int D>
 struct TileCfg {
   static constexpr int QN = D == 256 ? 64 : 128;  // query rows of a tile
   static constexpr int kKeys = 256;
-  static constexpr int kStages = D == 64 ? 6 : (D == 128 ? 4 : 3);  // ring of query tiles
-  static constexpr int kLse = D == 256 ? 4 : 8;                     // ring of their lse
+  static constexpr int kStages = D == 64 ? 6 : (D == 128 ? 4 : 2);  // ring of query tiles
+  static constexpr int kLse = 4;                                    // ring of their lse columns
   static constexpr int kPanels = D / 64;
   static constexpr int kKPanel = 128 * 128;               // one panel of a 128-key tile
   static constexpr int kKTile = kPanels * kKPanel;
   static constexpr int kQPanel = QN * 128;
   static constexpr int kQTile = kPanels * kQPanel;
   static constexpr int kQOff = 2 * kKTile;
-  static constexpr int kLseOff = kQOff + kStages * kQTile;   // [slot][QN] floats
+  // sixteen more columns of the product, without swizzle: three of ones beside the keys, and
+  // -lse / scale beside the queries
+  static constexpr int kOnesOff = kQOff + kStages * kQTile;  // [128 rows][16]
+  static constexpr int kExtTile = QN * 32;
+  static constexpr int kLseOff = kOnesOff + 128 * 32;        // [slot][QN rows][16]
   static constexpr int kSumOff = kQOff;                      // [parity][256] floats, at the end
-  static constexpr int kBarOff = kLseOff + kLse * QN * 4;
+  static constexpr int kBarOff = kLseOff + kLse * kExtTile;
   static constexpr int kNumBars = 2 * kStages + 2 * kLse + 2 * 2 * 2;  // full, empty, of each ring; S, free [tile][buf]
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   static constexpr int kSumWarps = 16;
-  static constexpr int kThreads = (kSumWarps + 3) * 32;
+  static constexpr int kThreads = (kSumWarps + 4) * 32;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem;
   uint8_t* sQ = smem + C::kQOff;
-  float* sL = reinterpret_cast<float*>(smem + C::kLseOff);
+  uint8_t* sL = smem + C::kLseOff;
   float* sSum = reinterpret_cast<float*>(smem + C::kSumOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + C::kStages;
@@ -232,11 +240,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // both key tiles' products
     }
     for (int s = 0; s < C::kLse; ++s) {
       mbar_init(&fullL[s], 1);
-      mbar_init(&emptyL[s], 8);  // the warps that sum the tile
+      mbar_init(&emptyL[s], 2);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar_S[i], 1);
@@ -260,6 +268,12 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
     const int used = PT * G, pad = (QN - used) * 8;  // 16-byte chunks of one panel
     for (int i = threadIdx.x; i < pad * C::kPanels * C::kStages; i += 256)
       *reinterpret_cast<uint4*>(sQ + (i / pad) * C::kQPanel + used * 128 + (i % pad) * 16) = make_uint4(0, 0, 0, 0);
+    // 8-row blocks of 16 bytes: columns 0-7 of row r at (r / 8) * 256 + (r % 8) * 16, then 8-15
+    for (int i = threadIdx.x; i < 128 * 2; i += 256)  // ones in columns 0, 1, 2
+      *reinterpret_cast<uint4*>(smem + C::kOnesOff + i * 16) =
+          (i & 8) ? make_uint4(0, 0, 0, 0) : make_uint4(0x3F803F80u, 0x00003F80u, 0, 0);
+    for (int i = threadIdx.x; i < C::kLse * C::kExtTile / 16; i += 256)
+      *reinterpret_cast<uint4*>(sL + i * 16) = make_uint4(0, 0, 0, 0);
     cp_async_wait<0>();
     fence_proxy_async_smem();
   }
@@ -294,7 +308,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
       for (int u = max(0, i - C::kStages); u < i; ++u)
         mbar_wait(&full[u % C::kStages], (uint32_t)(u / C::kStages) & 1u, nullptr, nullptr, 100000000ull);
   } else if (warp == C::kSumWarps + 2) {
-    // ---- -lse log2 e of the tiles' columns, read kAhead tiles before they are stored ----
+    // ---- -lse / scale of the tiles' rows, as three bf16 terms (2^-24 of it left out), read
+    // kAhead tiles before they are stored ----
     int cp[QN / 32], ch[QN / 32];  // this lane's columns: position in the tile, head (-1: no row)
 #pragma unroll
     for (int k = 0; k < QN / 32; ++k) {
@@ -312,6 +327,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
           v[k] = a.lse[(size_t)(hu * G + ch[k]) * a.lse_hs + (size_t)(base + p0 + cp[k]) * a.lse_ts];
       }
     };
+    const float inv_scale = 1.f / a.scale;
     constexpr int kAhead = 2;
     float v[kAhead][QN / 32];
 #pragma unroll
@@ -326,39 +342,54 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
         ok = mbar_wait_warp(&emptyL[s], ((uint32_t)(i / C::kLse) & 1u) ^ 1u, a.err, abort_flag);
         if (!ok) continue;
 #pragma unroll
-        for (int k = 0; k < QN / 32; ++k)  // nothing where there is no row or it saw no key
-          sL[s * QN + k * 32 + lane] = v[p][k] == -INFINITY ? -INFINITY : -kLog2e * v[p][k];
+        for (int k = 0; k < QN / 32; ++k) {
+          const int c = k * 32 + lane;
+          float x = -v[p][k] * inv_scale;
+          // nothing where there is no row, or it saw no key (lse = -inf) or only infinite ones
+          if (x > 1e38f || x < -1e38f) x = -1e38f;
+          const uint32_t hi = pack_bf16x2(x, 0.f);
+          const float r1 = x - __uint_as_float(hi << 16);
+          const uint32_t mid = pack_bf16x2(r1, 0.f);
+          const float r2 = r1 - __uint_as_float(mid << 16);
+          *reinterpret_cast<uint2*>(sL + s * C::kExtTile + (c >> 3) * 256 + (c & 7) * 16) =
+              make_uint2((hi & 0xFFFFu) | mid << 16, pack_bf16x2(r2, 0.f));
+        }
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&fullL[s]);
         if (i + kAhead < n) load_lse(i + kAhead, v[p]);
       }
     }
-  } else if (warp == C::kSumWarps) {
-    // ---- MMA: S^T of both key tiles ----
+  } else if (warp == C::kSumWarps || warp == C::kSumWarps + 3) {
+    // ---- MMA: S^T of one key tile (a missing second one only counts on the slots) ----
+    const int t = warp == C::kSumWarps ? 0 : 1;
     constexpr uint32_t idesc = idesc_bf16_f32(128, QN, 0, 0);
-    const uint64_t dk = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
+    const uint64_t dk = smem_desc(smem_u32(sK + t * C::kKTile), 16, 1024, kSwizzle128B);
     const uint64_t dq0 = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
-    bool ok = true;
-    for (int i = 0; ok && i < n; ++i) {
-      const int s = i % C::kStages, buf = i & 1;
-      const uint32_t ph = ((uint32_t)(i >> 1) & 1u) ^ 1u;
-      ok = mbar_wait_warp(&full[s], (uint32_t)(i / C::kStages) & 1u, a.err, abort_flag);
-      const uint64_t dq = dq0 + (uint64_t)((s * C::kQTile) >> 4);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (!ok || (t == 1 && !two)) continue;
-        ok = mbar_wait_warp(&bar_F[t * 2 + buf], ph, a.err, abort_flag);
-        if (!ok) continue;
+    const uint64_t d1 = smem_desc(smem_u32(smem + C::kOnesOff), 128, 256, kSwizzleNone);
+    const uint64_t dl0 = smem_desc(smem_u32(sL), 128, 256, kSwizzleNone);
+    for (int i = 0; i < n; ++i) {
+      const int s = i % C::kStages, sl = i % C::kLse, buf = i & 1;
+      if ((t == 0 || two) &&
+          !mbar_wait_warp(&bar_F[t * 2 + buf], ((uint32_t)(i >> 1) & 1u) ^ 1u, a.err, abort_flag))
+        break;
+      if (!mbar_wait_warp(&full[s], (uint32_t)(i / C::kStages) & 1u, a.err, abort_flag)) break;
+      if (!mbar_wait_warp(&fullL[sl], (uint32_t)(i / C::kLse) & 1u, a.err, abort_flag)) break;
+      if (t == 0 || two) {
         tc_fence_after();
+        const uint64_t dq = dq0 + (uint64_t)((s * C::kQTile) >> 4);
+        const uint32_t d_tmem = tmem + (t * 2 + buf) * 128;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t ok_ = (uint64_t)((t * C::kKTile + (kk >> 2) * C::kKPanel + (kk & 3) * 32) >> 4);
+          const uint64_t ok_ = (uint64_t)(((kk >> 2) * C::kKPanel + (kk & 3) * 32) >> 4);
           const uint64_t oq_ = (uint64_t)(((kk >> 2) * C::kQPanel + (kk & 3) * 32) >> 4);
-          mma_ss_e(tmem + (t * 2 + buf) * 128, dk + ok_, dq + oq_, idesc, kk > 0 ? 1u : 0u);
+          mma_ss_e(d_tmem, dk + ok_, dq + oq_, idesc, kk > 0 ? 1u : 0u);
         }
+        mma_ss_e(d_tmem, d1, dl0 + (uint64_t)((sl * C::kExtTile) >> 4), idesc, 1u);
         mma_commit_e(&bar_S[t * 2 + buf]);
       }
-      if (ok) mma_commit_e(&empty[s]);
+      mma_commit_e(&empty[s]);
+      mma_commit_e(&emptyL[sl]);
     }
   } else if (warp < C::kSumWarps) {
     // ---- sums ----
@@ -371,11 +402,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
     float acc = 0.f;
     bool ok = true;
     for (int i = par; i < n && (t == 0 || two); i += 2) {
-      const int s = i % C::kLse, buf = par;
+      const int buf = par;
       int hu, p0;
       tile_at(i, hu, p0);
-      bool got = mbar_wait(&fullL[s], (uint32_t)(i / C::kLse) & 1u, a.err, abort_flag);
-      got = got && mbar_wait(&bar_S[t * 2 + buf], (uint32_t)(i >> 1) & 1u, a.err, abort_flag);
+      const bool got = mbar_wait(&bar_S[t * 2 + buf], (uint32_t)(i >> 1) & 1u, a.err, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, got)) {
         ok = false;
         break;
@@ -393,7 +423,6 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
           c_hi = w <= 0 ? 0 : (int)min((long long)c_hi, w * G);
         }
       }
-      const float* lp = sL + s * QN;
       const uint32_t s_addr = lane_addr + (t * 2 + buf) * 128;
       uint64_t a0 = f2pack(0.f, 0.f), a1 = a0;
       uint32_t sr[64];
@@ -401,10 +430,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
         constexpr bool EDGE = decltype(edge_tag)::value;
 #pragma unroll
         for (int c = 0; c < 64; c += 4) {
-          const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(lp + c0 + c);
           float x0, x1, x2, x3;
-          f2unpack(fma2(f2pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2x2, l4.x), x0, x1);
-          f2unpack(fma2(f2pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl2x2, l4.y), x2, x3);
+          f2unpack(mul2(f2pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2x2), x0, x1);
+          f2unpack(mul2(f2pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl2x2), x2, x3);
           float p[4] = {ex2_approx(x0), ex2_approx(x1), ex2_approx(x2), ex2_approx(x3)};
           if constexpr (EDGE) {
 #pragma unroll
@@ -428,19 +456,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
         if (edge) terms(c0, std::true_type{});
         else terms(c0, std::false_type{});
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&emptyL[s]);
       float s0, s1;
       f2unpack(add2(a0, a1), s0, s1);
       acc += s0 + s1;
-    }
-    // a missing second key tile reads nothing but still counts on the lse slots
-    if (t == 1 && !two) {
-      for (int i = par; i < n; i += 2) {
-        const int s = i % C::kLse;
-        if (!mbar_wait_warp(&fullL[s], (uint32_t)(i / C::kLse) & 1u, a.err, abort_flag)) break;
-        if (lane == 0) mbar_arrive(&emptyL[s]);
-      }
     }
     sum = ok ? acc : NAN;
   }

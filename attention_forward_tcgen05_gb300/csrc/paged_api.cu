@@ -245,7 +245,7 @@ int attn_key_weights(const attn_bf16_t* q, const float* lse, const attn_bf16_t* 
   if (total_q < 0 || max_sq < 0 || window < 0 || n_sink < 0 || !ok_scale(scale)) return ATTN_ERR_INVALID_ARG;
   if (window > 0 && !causal) return ATTN_ERR_INVALID_ARG;
   if (cu_seqlens_q == nullptr && (total_q != B || max_sq != 1)) return ATTN_ERR_INVALID_ARG;
-  if (!ok_dim(d)) return ATTN_ERR_UNSUPPORTED;
+  if (!ok_dim(d) || scale < 1e-30f || scale > 1e30f) return ATTN_ERR_UNSUPPORTED;  // (lse / scale is formed)
   rc = check_cache(page_table, B, max_pages, page_size, num_pages);
   if (rc != ATTN_OK) return rc;
   if (w_stride < (long long)max_pages * page_size) return ATTN_ERR_INVALID_ARG;

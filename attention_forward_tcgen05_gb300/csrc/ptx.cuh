@@ -540,7 +540,8 @@ __device__ __forceinline__ void tma_load_4d_pair_e(void* smem_dst, const CUtenso
 // ---------------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading and
 // stride byte offsets (both >> 4), fixed version bits 46-48 = 0b001, swizzle
-// mode in bits 61-63 (2 = 128-byte swizzle).
+// mode in bits 61-63 (2 = 128-byte swizzle; 0 = none: a K-major operand is made of 128-byte
+// blocks of 8 rows x 16 bytes, `lbo` apart along K and `sbo` along the rows).
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes,
                                               uint32_t swizzle_mode) {
   uint64_t d = 0;
@@ -552,6 +553,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes
   return d;
 }
 
+constexpr uint32_t kSwizzleNone = 0;
 constexpr uint32_t kSwizzle128B = 2;
 
 // Instruction descriptor for kind::f16 with bf16 A/B, fp32 accumulator.

@@ -500,7 +500,8 @@ int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int* min
  *                per sequence: total_q = B, max_sq = 1), lse [B][Hq]
  *   weights      fp32 [B][Hkv][w_stride], w_stride >= max_pages * page_size
  *   page_table   may be NULL (dense cache);  d in {64, 128, 256}
- *   causal, window, n_sink, scale   as in the attention call (window = 0: none)
+ *   causal, window, n_sink, scale   as in the attention call (window = 0: none); scale in
+ *                [1e-30, 1e30]
  * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
  */
 int attn_key_weights(const attn_bf16_t* q, const float* lse, const attn_bf16_t* kcache, const int* page_table,

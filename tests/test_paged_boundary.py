@@ -145,6 +145,7 @@ def test_weights():
     for name in ("q", "lse", "w"):
         assert WEIGHTS(**{name: N}) == INVALID
     assert WEIGHTS(q=M) == INVALID
+    assert WEIGHTS(scale=1e-31) == UNSUPPORTED and WEIGHTS(scale=2e30) == UNSUPPORTED
     assert WEIGHTS(total=1 << 30) == INVALID and WEIGHTS(max_sq=1 << 30) == INVALID
 
 
