@@ -155,6 +155,76 @@ __device__ __forceinline__ TileInfo tile_info(int q0, int Sr, int Sq, int G, int
   return ti;
 }
 
+// ---- launch order of a packed batch's units (paged cache) ----
+// Sequences bring histories of different lengths, so a short chunk's block may be the
+// longest unit of all: the blocks start by their number of KV tiles, most first.  A warp
+// finds the block of a rank: the number of blocks with at least x tiles is a closed form per
+// sequence (tiles grow along its blocks), so a bisection over x gives the rank's tiles, and
+// a scan over the sequences the block among equals.
+constexpr int kOrderMaxSeqs = 128;  // four a lane; larger batches keep the block-by-block order
+
+// (sequence, block) of rank r, or (-1, -1) past the last block; the whole warp calls it.
+__device__ __noinline__ int2 block_of_rank(int r, int B, int Sq_max, int Skv_max, const int* __restrict__ cu_q,
+                                           const int* __restrict__ kv_lens, int total_q, int causal, int BP, int BN,
+                                           int lane) {
+  constexpr int K = kOrderMaxSeqs / 32;
+  int n[K], off[K], nb[K], top = 0;  // rows, key index of row 0, blocks
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int b = k * 32 + lane;
+    n[k] = off[k] = nb[k] = 0;
+    if (b < B) {
+      const SeqExtent e = seq_extent(b, Sq_max, Skv_max, cu_q, kv_lens, total_q);
+      n[k] = e.Sq;
+      off[k] = e.Skv - e.Sq;
+      nb[k] = (e.Sq + BP - 1) / BP;
+      if (nb[k] > 0) top = max(top, (e.Skv + BN - 1) / BN);
+    }
+  }
+  // blocks of sequence k with at least x tiles (0 tiles: all)
+  auto at_least = [&](int k, int x) -> int {
+    if (nb[k] == 0 || x <= 0) return nb[k];
+    const long long y = (long long)(x - 1) * BN;  // such a block's last row admits key y
+    if (!causal) return (long long)n[k] + off[k] > y ? nb[k] : 0;
+    const long long last = y - off[k];            // ... so it is at or past this row
+    if (last >= n[k]) return 0;
+    return last < 0 ? nb[k] : nb[k] - (int)(last / BP);
+  };
+  auto count = [&](int x) -> int {
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) c += at_least(k, x);
+    return (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)c);
+  };
+  if (r >= count(0)) return make_int2(-1, -1);
+  int lo = 0, hi = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)top) + 1;  // count(lo) > r >= count(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (count(mid) > r) lo = mid;
+    else hi = mid;
+  }
+  int q = r - count(lo + 1);  // among the blocks of exactly lo tiles, sequence by sequence
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int above = at_least(k, lo + 1), c = at_least(k, lo) - above;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, incl - c <= q && q < incl);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      // a sequence's blocks with more tiles are its last ones
+      const int blk = __shfl_sync(0xFFFFFFFFu, nb[k] - above - 1 - (q - (incl - c)), src);
+      return make_int2(k * 32 + src, blk);
+    }
+    q -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  return make_int2(-1, -1);
+}
+
 // WIN: causal sliding window with attention sinks (window, n_sink); without it
 // both are ignored and the tile list is every KV tile.  SPLIT: key splits with
 // decode partials (n_splits, split_min, part_o, part_lse); without it they are ignored.
@@ -201,10 +271,25 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
   // are neighbours, so that head's K/V stay in L2 while they run
   // (key splits: block by block too)
   const bool by_block = causal || (PAGED && SPLIT);
-  const int qb = by_block ? (n_blocks_q - 1 - u / (HB * NSPL)) : (u % n_blocks_q);
+  int qb = by_block ? (n_blocks_q - 1 - u / (HB * NSPL)) : (u % n_blocks_q);
   const int sp = by_block ? (u % (HB * NSPL)) / HB : 0;
   const int hb = by_block ? u % HB : u / n_blocks_q;
-  const int hu = hb % Hu, b = hb / Hu;
+  int hu = hb % Hu, b = hb / Hu;
+  if constexpr (PAGED && !WIN && !SPLIT) {
+    const int B = HB / Hu;
+    if (B > 1 && B <= kOrderMaxSeqs) {
+      __shared__ int2 unit_sh;
+      if (warp == 0) {
+        const int2 x = block_of_rank(u / Hu, B, Sq_max, Skv_max, cu_q, kv_lens, total_q, causal, NQ * TR / G, BN, lane);
+        if (lane == 0) unit_sh = x;
+      }
+      __syncthreads();
+      b = unit_sh.x;
+      qb = unit_sh.y;
+      hu = u % Hu;
+      if (b < 0) return;  // past the batch's blocks (whole CTA)
+    }
+  }
   const int hk = (hu * G) / (Hq / Hkv);
   // this sequence's query positions and keys (fixed-length or packed varlen batch)
   const SeqExtent ext = seq_extent(b, Sq_max, Skv_max, cu_q, kv_lens, total_q);
