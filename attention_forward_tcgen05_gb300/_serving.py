@@ -16,7 +16,18 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._binding import ATTN_BF16, ATTN_F32, ATTN_OK, AttnError, _counters, _lock, _torch, load
+from ._binding import ATTN_BF16, ATTN_F32, ATTN_OK, AttnError, _counters, _lock, load
+
+
+_module = None
+
+
+def _torch():
+    global _module
+    if _module is None:
+        import torch
+        _module = torch
+    return _module
 
 
 # ------------------------------------------------------------------ raw C ABI
@@ -132,21 +143,27 @@ def _out_code(dtype):
     raise TypeError(f"unsupported output dtype {dtype}")
 
 
-def _stream_counters(n, dev, handle):
-    """Zeroed completion counters for a decode_paged call: a buffer for each stream (its
-    calls are ordered), and one of its own for a call being captured (two graphs may replay
-    at the same time).  Returns the tensor."""
+_partials = {}  # (device, stream handle) -> fp32 workspace of decode_paged
+
+
+def _decode_workspace(heads, floats, dev, handle):
+    """(zeroed completion counters, fp32 partials) for a decode_paged call of `heads` rows:
+    kept for each stream, whose calls are ordered (one launch each), and made anew for a
+    call being captured (two graphs may replay at the same time)."""
     torch = _torch()
     if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.zeros(n, dtype=torch.int32, device="cuda")
-    key = ("cuda", dev, handle)
-    buf = _counters.get(key)
-    if buf is None or buf.numel() < n:
+        return (torch.zeros(heads, dtype=torch.int32, device="cuda"),
+                torch.empty(floats, dtype=torch.float32, device="cuda"))
+    key = (dev, handle)
+    counters, work = _counters.get(key), _partials.get(key)
+    if counters is None or counters.numel() < heads:
         with _lock:
-            buf = torch.zeros(max(n, 4096), dtype=torch.int32, device="cuda")
+            counters = torch.zeros(max(heads, 4096), dtype=torch.int32, device="cuda")
             torch.cuda.synchronize(dev)  # zeroed before the stream uses it, and no longer in use
-            _counters[key] = buf
-    return buf
+            _counters[key] = counters
+    if work is None or work.numel() < floats:
+        work = _partials[key] = torch.empty(floats, dtype=torch.float32, device="cuda")
+    return counters, work
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -225,7 +242,7 @@ def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_
         Hq = q.shape[1]
         qr, qs = _token_rows(q, "q", dev, total, Hq, d)
         if out is None:
-            out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device="cuda")
+            out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device="cuda")  # (q may be strided)
             op = out.data_ptr()
         else:
             op = _sized(out, "out", torch.bfloat16, dev, total, Hq, d)
@@ -277,7 +294,7 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        o = torch.empty((total, Hq, d), dtype=out_dtype or torch.bfloat16, device="cuda")
+        o = torch.empty_like(q) if out_dtype in (None, torch.bfloat16) else torch.empty_like(q, dtype=out_dtype)
         lse = torch.empty((Hq, total), dtype=torch.float32, device="cuda")
         op, lp = o.data_ptr(), lse.data_ptr()
     else:
@@ -345,21 +362,22 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
             min_rows_per_split = rows.value
     pp = ps = cp = None
     if n_splits > 1:
-        if parts is None:  # both partials in one allocation
-            rows = B * Hq * n_splits
-            work = torch.empty(rows * (d + 1), dtype=torch.float32, device="cuda")
+        rows = B * Hq * n_splits
+        if parts is None or counters is None:
+            own, work = _decode_workspace(B * Hq, rows * (d + 1) if parts is None else 0, dev, handle)
+        if parts is None:
             pp = work.data_ptr()
             ps = pp + rows * d * 4
         else:
             pp = _sized(parts[0], "parts[0]", torch.float32, dev, B, Hq, n_splits, d)
             ps = _sized(parts[1], "parts[1]", torch.float32, dev, B, Hq, n_splits)
         if counters is None:
-            counters = _stream_counters(B * Hq, dev, handle)
+            counters = own
         elif counters.dtype != torch.int32 or counters.get_device() != dev or counters.numel() < B * Hq:
             raise TypeError("counters must be a CUDA int32 tensor of at least B*Hq entries")
         cp = counters.data_ptr()
     if out is None:
-        o = torch.empty((B, Hq, d), dtype=out_dtype or torch.bfloat16, device="cuda")
+        o = torch.empty_like(q) if out_dtype in (None, torch.bfloat16) else torch.empty_like(q, dtype=out_dtype)
         lse = torch.empty((B, Hq), dtype=torch.float32, device="cuda")
         op, lp = o.data_ptr(), lse.data_ptr()
     else:
