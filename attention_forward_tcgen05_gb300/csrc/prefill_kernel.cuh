@@ -159,43 +159,35 @@ __device__ __forceinline__ TileInfo tile_info(int q0, int Sr, int Sq, int G, int
 // Sequences bring histories of different lengths, so a short chunk's block may be the
 // longest unit of all: the blocks start by their number of KV tiles, most first.  A warp
 // finds the block of a rank: the number of blocks with at least x tiles is a closed form per
-// sequence (tiles grow along its blocks), so a bisection over x gives the rank's tiles, and
-// a scan over the sequences the block among equals.
-constexpr int kOrderMaxSeqs = 128;  // four a lane; larger batches keep the block-by-block order
+// sequence (lane = sequence; tiles grow along its blocks), so a bisection over x gives the
+// rank's tiles, and a scan over the lanes the block among equals.
+constexpr int kOrderMaxSeqs = 32;  // larger batches keep the block-by-block order
 
 // (sequence, block) of rank r, or (-1, -1) past the last block; the whole warp calls it.
+// BP: positions of a block.
 __device__ __noinline__ int2 block_of_rank(int r, int B, int Sq_max, int Skv_max, const int* __restrict__ cu_q,
                                            const int* __restrict__ kv_lens, int total_q, int causal, int BP, int BN,
                                            int lane) {
-  constexpr int K = kOrderMaxSeqs / 32;
-  int n[K], off[K], nb[K], top = 0;  // rows, key index of row 0, blocks
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int b = k * 32 + lane;
-    n[k] = off[k] = nb[k] = 0;
-    if (b < B) {
-      const SeqExtent e = seq_extent(b, Sq_max, Skv_max, cu_q, kv_lens, total_q);
-      n[k] = e.Sq;
-      off[k] = e.Skv - e.Sq;
-      nb[k] = (e.Sq + BP - 1) / BP;
-      if (nb[k] > 0) top = max(top, (e.Skv + BN - 1) / BN);
-    }
+  int n = 0, off = 0, nb = 0, top = 0;  // rows, key index of row 0, blocks, tiles of the last one
+  if (lane < B) {
+    const SeqExtent e = seq_extent(lane, Sq_max, Skv_max, cu_q, kv_lens, total_q);
+    n = e.Sq;
+    off = e.Skv - e.Sq;
+    nb = (n + BP - 1) / BP;
+    if (nb > 0) top = (e.Skv + BN - 1) / BN;
   }
-  // blocks of sequence k with at least x tiles (0 tiles: all)
-  auto at_least = [&](int k, int x) -> int {
-    if (nb[k] == 0 || x <= 0) return nb[k];
-    const long long y = (long long)(x - 1) * BN;  // such a block's last row admits key y
-    if (!causal) return (long long)n[k] + off[k] > y ? nb[k] : 0;
-    const long long last = y - off[k];            // ... so it is at or past this row
-    if (last >= n[k]) return 0;
-    return last < 0 ? nb[k] : nb[k] - (int)(last / BP);
+  const float inv = 1.f / (float)BP;
+  // blocks with at least x tiles: those whose last row admits key (x - 1) * BN
+  auto at_least = [&](int x) -> int {
+    if (x <= 0 || x > top) return x <= 0 ? nb : 0;
+    const int row = (x - 1) * BN - off;  // the first row that admits it (< n, as x <= top)
+    if (!causal || row < 0) return nb;
+    int q = (int)((float)row * inv);     // row / BP: the quotient, or one beside it
+    q += (q + 1) * BP <= row ? 1 : 0;
+    q -= q * BP > row ? 1 : 0;
+    return nb - q;
   };
-  auto count = [&](int x) -> int {
-    int c = 0;
-#pragma unroll
-    for (int k = 0; k < K; ++k) c += at_least(k, x);
-    return (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)c);
-  };
+  auto count = [&](int x) { return (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)at_least(x)); };
   if (r >= count(0)) return make_int2(-1, -1);
   int lo = 0, hi = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)top) + 1;  // count(lo) > r >= count(hi)
   while (hi - lo > 1) {
@@ -203,26 +195,20 @@ __device__ __noinline__ int2 block_of_rank(int r, int B, int Sq_max, int Skv_max
     if (count(mid) > r) lo = mid;
     else hi = mid;
   }
-  int q = r - count(lo + 1);  // among the blocks of exactly lo tiles, sequence by sequence
+  // among the blocks of exactly lo tiles, sequence by sequence
+  const int above = at_least(lo + 1), c = at_least(lo) - above;
+  const int q = r - (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)above);
+  int incl = c;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int above = at_least(k, lo + 1), c = at_least(k, lo) - above;
-    int incl = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, incl - c <= q && q < incl);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      // a sequence's blocks with more tiles are its last ones
-      const int blk = __shfl_sync(0xFFFFFFFFu, nb[k] - above - 1 - (q - (incl - c)), src);
-      return make_int2(k * 32 + src, blk);
-    }
-    q -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += x;
   }
-  return make_int2(-1, -1);
+  const unsigned hit = __ballot_sync(0xFFFFFFFFu, incl - c <= q && q < incl);
+  if (hit == 0) return make_int2(-1, -1);
+  const int src = __ffs(hit) - 1;
+  // a sequence's blocks with more tiles are its last ones
+  return make_int2(src, __shfl_sync(0xFFFFFFFFu, nb - above - 1 - (q - (incl - c)), src));
 }
 
 // WIN: causal sliding window with attention sinks (window, n_sink); without it
