@@ -10,8 +10,12 @@
 //                      score exceeds it by 2^8, so that the usual step needs no maximum
 //                      across lanes; it cancels in O / l,
 //   O^T += V^T P^T     P^T by movmatrix from the score fragments.
-// P goes into the product as two bf16 terms (value and remainder, 2^-17 of P left out), so
-// that O is good to fp32 outputs; O, l and m are fp32.  With heads as the 8-wide side of the
+// O, l and m are fp32.  P goes into the product as bf16 terms.  For a bf16 output two (the
+// value and its remainder: at most 2^-17 of P left out).  For an fp32 output three (2^-25),
+// and each step's product starts from zero and is added to O in fp32, as the mma's own
+// accumulation truncates: against fp64 on 131k keys that is off by 5e-7 of O, two terms
+// accumulated in the mma by 2.9e-6, fp32 matrix products by 9e-7; the third term costs 1.5 %
+// where HBM bounds and 15 % with 16 heads.  With heads as the 8-wide side of the
 // mma a step of 16 keys costs about 250 warp instructions at d = 128 against 700 on fp32
 // cores per head group of 4, and the kernel runs at the rate of the gathers.
 #include <cmath>
@@ -47,7 +51,8 @@ struct DecodePagedCfg {
   static constexpr int kMinBlocks = decode_paged_ctas(D, NB);
 };
 
-template <int D, int NB>
+// F32: the output is fp32 (see above); else bf16.
+template <int D, int NB, bool F32>
 __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks)
     decode_paged_kernel(const DecodeArgs a, int heads_per_cta) {
   using C = DecodePagedCfg<D, NB>;
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
           }
         }
       }
-      uint32_t ph[NB][2], pl[NB][2];
+      uint32_t ph[NB][2], pl[NB][2], pr[NB][2];  // P^T in three terms
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -184,8 +189,12 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
           l[nb][0] += p0;
           l[nb][1] += p1;
           const uint32_t v = pack_bf16x2(p0, p1);
+          const float r0 = p0 - __uint_as_float(v << 16), r1 = p1 - __uint_as_float(v & 0xFFFF0000u);
+          const uint32_t w = pack_bf16x2(r0, r1);
           ph[nb][h] = movmatrix_trans(v);
-          pl[nb][h] = movmatrix_trans(pack_bf16x2(p0 - __uint_as_float(v << 16), p1 - __uint_as_float(v & 0xFFFF0000u)));
+          pl[nb][h] = movmatrix_trans(w);
+          if constexpr (F32)
+            pr[nb][h] = movmatrix_trans(pack_bf16x2(r0 - __uint_as_float(w << 16), r1 - __uint_as_float(w & 0xFFFF0000u)));
         }
       }
 #pragma unroll
@@ -194,8 +203,17 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
         ldmatrix_x4_trans(frag_dims<C::kPanel>(vt, t, lane), f);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          mma_16816(o[nb][t], f, ph[nb][0], ph[nb][1]);
-          mma_16816(o[nb][t], f, pl[nb][0], pl[nb][1]);
+          if constexpr (F32) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_16816(c, f, pr[nb][0], pr[nb][1]);
+            mma_16816(c, f, pl[nb][0], pl[nb][1]);
+            mma_16816(c, f, ph[nb][0], ph[nb][1]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[nb][t][k] += c[k];
+          } else {
+            mma_16816(o[nb][t], f, ph[nb][0], ph[nb][1]);
+            mma_16816(o[nb][t], f, pl[nb][0], pl[nb][1]);
+          }
         }
       }
       __syncwarp();  // every lane has read the stage before it is refilled
@@ -249,7 +267,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
 template <int D, int NB>
 cudaError_t launch_t(const DecodeArgs& a, int heads_per_cta, cudaStream_t stream) {
   using C = DecodePagedCfg<D, NB>;
-  auto kern = decode_paged_kernel<D, NB>;
+  auto kern = a.o_bf16 ? decode_paged_kernel<D, NB, false> : decode_paged_kernel<D, NB, true>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const int n_hg = (a.Hq / a.Hkv + heads_per_cta - 1) / heads_per_cta;

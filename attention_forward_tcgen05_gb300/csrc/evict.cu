@@ -207,7 +207,6 @@ __global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictArg
   __shared__ int place[2][kMoveRows];                   // pool rows: from, to
   const int hk = blockIdx.x % a.Hkv, range = blockIdx.x / a.Hkv % ranges, b = blockIdx.x / a.Hkv / ranges;
   const int bh = b * a.Hkv + hk;
-  cudaGridDependencySynchronize();  // the kept list is written (launched under the selection's end)
   const int cap = a.src.max_pages * a.src.page_size;
   const int n = min(min(max(a.kv_lens[b], 0), cap), a.budget);
   if (hk == 0 && range == 0 && threadIdx.x == 0) a.new_lens[b] = n;
@@ -301,16 +300,8 @@ cudaError_t launch_move(const EvictArgs& a, cudaStream_t stream) {
   const int ranges = rows > 0 ? (rows + kMoveRows - 1) / kMoveRows : 1;
   const long long ctas = (long long)a.B * a.Hkv * ranges;
   if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_copy_kernel<D>, a, ranges);
+  evict_copy_kernel<D><<<(unsigned)ctas, kMoveThreads, 0, stream>>>(a, ranges);
+  return cudaGetLastError();
 }
 
 }  // namespace

@@ -74,6 +74,26 @@ def test_decode_ragged_workload():
     log_parity("decode_paged " + s.name, eo, el)
 
 
+@pytest.mark.parametrize("d,Hq,Hkv,n_splits", [(64, 8, 1, 1), (128, 28, 4, 3), (256, 16, 1, 2)])
+def test_decode_fp32_output(d, Hq, Hkv, n_splits):
+    """An fp32 O is good to fp32 sums: off by at most 2^-18 of sum p |v|.  That holds the score's
+    fp32 dot product (the mma's truncation, d 2^-23 of scale sum |q k| at most, on average the
+    root of that), ex2 (2^-22), P's three terms (2^-25) and the sums' roundings."""
+    lens = torch.tensor([3000, 1, 77, 1500], dtype=torch.int32)
+    q, kc, vc = W.decode_inputs(4, Hq, Hkv, d, lens, 320 + d)
+    kp, vp, table = make_pages(kc, vc, lens, 16, 320)
+    o, _ = attn.decode_paged(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), lens.cuda(), n_splits,
+                             out_dtype=torch.float32)
+    attn.sync_check()
+    o = o.double().cpu()
+    G = Hq // Hkv
+    for b, L in enumerate(lens.tolist()):
+        for h in range(Hq):
+            k, v = kc[b, :L, h // G].double(), vc[b, :L, h // G].double()
+            p = torch.softmax(q[b, h].double() @ k.T / np.sqrt(d), -1)
+            assert ((o[b, h] - p @ v).abs() <= 2.0 ** -18 * (p @ v.abs())).all(), (b, h)
+
+
 def test_decode_shared_pages():
     """Two sequences that share their first pages (a common prefix)."""
     lens = torch.tensor([200, 170], dtype=torch.int32)
