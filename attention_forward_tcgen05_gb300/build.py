@@ -17,10 +17,10 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libattn.so")
 BUILD_DIR = os.path.join(HERE, "_build")
-SOURCES = ["attn_api.cu", "paged_api.cu", "prefill.cu", "prefill_paged.cu", "prefill_pair.cu", "prefill_d512.cu",
+SOURCES = ["attn_api.cu", "paged_api.cu", "prefill.cu", "prefill_paged.cu", "prefill_paged_f32.cu", "prefill_pair.cu", "prefill_d512.cu",
            "prefill_persist.cu", "decode.cu", "decode_paged.cu", "decode_noalloc.cu", "rope.cu", "key_weights.cu",
            "evict.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "paged.cuh", "prefill_kernel.cuh", "decode_common.cuh", "mma.cuh"]
+HEADERS = ["ptx.cuh", "internal.h", "paged.cuh", "prefill_kernel.cuh", "prefill_paged.cuh", "decode_common.cuh", "mma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

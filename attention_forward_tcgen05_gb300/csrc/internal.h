@@ -249,7 +249,9 @@ constexpr int kD512PairSlotBytes = 32768;
 constexpr int kD512PairVBoxRows = kD512PairSlotBytes >= 16384 ? 128 : kD512PairSlotBytes / 128;
 // Packed varlen batches over a paged cache (prefill_paged.cu): d in {64, 128, 256}, pack
 // <= 128; halves: every sequence's rows fit one query tile (d <= 128).
+// The f32 form for fp32 outputs (of the call, splits or not).
 cudaError_t launch_prefill_paged(const PrefillArgs& a, cudaStream_t stream);
+cudaError_t launch_prefill_paged_f32(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_empty_kv(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_split(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_paged(const DecodeArgs& a, cudaStream_t stream);

@@ -183,7 +183,8 @@ int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const at
     if (rc == ATTN_OK) rc = attn::encode_pool_map(&a.tm_v, vcache, d, Hkv, page_size, num_pages, a.kv.box_rows);
   }
   if (rc != ATTN_OK) return rc;
-  rc = from_cuda(attn::launch_prefill_paged(a, stream_of(stream)));
+  rc = from_cuda(a.o_bf16 ? attn::launch_prefill_paged(a, stream_of(stream))
+                          : attn::launch_prefill_paged_f32(a, stream_of(stream)));
   if (rc != ATTN_OK || n_splits == 1) return rc;
   attn::MergeArgs m;
   m.part_o = part_o; m.part_lse = part_lse; m.o = o; m.lse = lse;

@@ -29,12 +29,12 @@ template <int D, bool H>
 cudaError_t launch_prefill_grid(const PrefillArgs& a, cudaStream_t stream, long long unit0, long long grid,
                                 int row_halves) {
   using C = PrefillCfg<D, H>;
-  auto kern = fmha_fwd_kernel<D, false, false, false, false>;
+  auto kern = fmha_fwd_kernel<D, false, false, false, false, false>;
   if constexpr (H) {
-    kern = a.n_splits > 1 ? fmha_fwd_kernel<D, false, true, true, false> : fmha_fwd_kernel<D, false, false, true, false>;
+    kern = a.n_splits > 1 ? fmha_fwd_kernel<D, false, true, true, false, false> : fmha_fwd_kernel<D, false, false, true, false, false>;
   } else {
-    if (a.window > 0) kern = fmha_fwd_kernel<D, true, false, false, false>;
-    else if (a.n_splits > 1) kern = fmha_fwd_kernel<D, false, true, false, false>;
+    if (a.window > 0) kern = fmha_fwd_kernel<D, true, false, false, false, false>;
+    else if (a.n_splits > 1) kern = fmha_fwd_kernel<D, false, true, false, false, false>;
   }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;

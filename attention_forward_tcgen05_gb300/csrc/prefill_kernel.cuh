@@ -222,7 +222,10 @@ __device__ __noinline__ int2 block_of_rank(int r, int B, int Sq_max, int Skv_max
 // kv.box_rows rows or gathered by the producer warps (paged.cuh), rows past the sequence's
 // keys as zeros; a query tile
 // holds floor(128 / G) whole positions (any G), and key splits start on a KV tile.
-template <int D, bool WIN, bool SPLIT, bool HALVES, bool PAGED>
+// FINE (fp32 outputs over pages): P goes into P.V as two bf16 terms, its value and the
+// remainder, the second over the other half of S's columns (2^-17 of P left out instead of
+// 2^-9), and O is divided by the exact row sum.
+template <int D, bool WIN, bool SPLIT, bool HALVES, bool PAGED, bool FINE>
 __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
     fmha_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -576,6 +579,11 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
         for (int kk = 0; kk < BN / 16; ++kk)  // 16 keys = 8 TMEM columns of bf16 pairs, 2048 B of V
           mma_ts_e(d_tmem, p_tmem + kk * 8, dv + (uint64_t)(kk * (2048 >> 4)), idesc_o,
                    (j > 0 || kk > 0) ? 1u : 0u);
+        if constexpr (FINE) {
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts_e(d_tmem, p_tmem + BN / 2 + kk * 8, dv + (uint64_t)(kk * (2048 >> 4)), idesc_o, 1u);
+        }
         mma_commit_e(&bar_O[t]);
         if (j == ti[t].n_kv - 1) mma_commit_e(&bar_Fin[t]);
         return true;
@@ -803,15 +811,21 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
           pk[e] = pack_bf16x2(p0, p1);
           lex2 = add2(lex2, f2pack(p0, p1));
-          add_bf16x2_f32(pk[e], lrd0, lrd1);
+          if constexpr (FINE) {
+            sr[32 * h + e] = pack_bf16x2(p0 - __uint_as_float(pk[e] << 16),
+                                         p1 - __uint_as_float(pk[e] & 0xFFFF0000u));
+          } else {
+            add_bf16x2_f32(pk[e], lrd0, lrd1);
+          }
         }
         tmem_st16(s_addr + 16 * h, pk);  // P: bf16 pairs over the first BN/2 columns of S
+        if constexpr (FINE) tmem_st16(s_addr + BN / 2 + 16 * h, sr + 32 * h);
       }
       {
         float a0, a1;
         f2unpack(lex2, a0, a1);
         l += a0 + a1;
-        l_rnd += lrd0 + lrd1;
+        l_rnd += FINE ? a0 + a1 : lrd0 + lrd1;
       }
       // publish P(j): the MMA warp reads it as the A operand of P.V
       tmem_wait_st();

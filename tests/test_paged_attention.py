@@ -163,6 +163,33 @@ def test_chunks(d, causal, Hq, Hkv, page, seqs):
         check_lse(lse.cpu().numpy(), rl)
 
 
+@pytest.mark.parametrize("d,seqs,n_splits", [(64, MIXED, 1), (128, MIXED, 3), (256, MIXED, 1), (128, SHORT, 1)])
+def test_chunk_fp32_output(d, seqs, n_splits):
+    """An fp32 O is off by at most 2^-15 of sum p |v|: P's two terms leave out 2^-17 of it, the
+    mma's accumulation truncates 2^-24 in each of its L / 8 steps (2^-17 at 1200 keys), the
+    score's dot product and ex2 are below 2^-18."""
+    case = _chunk_case(seqs, 4, 2, d, 16, 440 + d)
+    q, kc, vc, cu, kv = case[:5]
+    scale = 1.0 / np.sqrt(d)
+    o, _ = _run(case, scale=scale, out_dtype=torch.float32, n_splits=n_splits)
+    o = o.double().cpu().numpy()
+    from tests.paged_cases import admitted
+    for b in range(len(seqs)):
+        a, e, L = int(cu[b]), int(cu[b + 1]), int(kv[b])
+        if L == 0 or a == e:
+            assert not o[a:e].any()
+            continue
+        ok = admitted(e - a, L, True)
+        for h in range(4):
+            k, v = kc[b, :L, h // 2].double().numpy(), vc[b, :L, h // 2].double().numpy()
+            s = np.where(ok, scale * (q[a:e, h].double().numpy() @ k.T), -np.inf)
+            live = ok.any(1)
+            p = np.zeros_like(s)
+            p[live] = np.exp(s[live] - s[live].max(1, keepdims=True))
+            p[live] /= p[live].sum(1, keepdims=True)
+            assert (abs(o[a:e, h] - p @ v) <= 2.0 ** -15 * (p @ abs(v))).all(), (b, h)
+
+
 @pytest.mark.parametrize("G", [1, 3, 9, 16, 24, 67, 100, 128, 150])
 def test_chunk_head_groups(G):
     """Head groups that do and do not divide a tile, of one and of several tiles."""
