@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 
 from ._binding import ATTN_BF16, ATTN_F32, ATTN_OK, AttnError, _counters, _lock, load
 
@@ -143,27 +144,37 @@ def _out_code(dtype):
     raise TypeError(f"unsupported output dtype {dtype}")
 
 
-_partials = {}  # (device, stream handle) -> fp32 workspace of decode_paged
+# Workspaces of prefill_paged and decode_paged: kept for each stream, whose launches are
+# ordered; a call holds the lock while it makes its launches, so that another thread's on the
+# same stream do not come between two of them.  A call being captured gets its own (two graphs
+# may replay at the same time).
+_partials = {}  # (device, stream handle) -> fp32
+_launching = threading.Lock()
 
 
-def _decode_workspace(heads, floats, dev, handle):
-    """(zeroed completion counters, fp32 partials) for a decode_paged call of `heads` rows:
-    kept for each stream, whose calls are ordered (one launch each), and made anew for a
-    call being captured (two graphs may replay at the same time)."""
+def _workspace(floats, dev, handle):
+    """fp32 workspace for split partials."""
     torch = _torch()
     if torch._C._cuda_isCurrentStreamCapturing():
-        return (torch.zeros(heads, dtype=torch.int32, device="cuda"),
-                torch.empty(floats, dtype=torch.float32, device="cuda"))
-    key = (dev, handle)
-    counters, work = _counters.get(key), _partials.get(key)
-    if counters is None or counters.numel() < heads:
-        with _lock:
-            counters = torch.zeros(max(heads, 4096), dtype=torch.int32, device="cuda")
-            torch.cuda.synchronize(dev)  # zeroed before the stream uses it, and no longer in use
-            _counters[key] = counters
+        return torch.empty(floats, dtype=torch.float32, device="cuda")
+    work = _partials.get((dev, handle))
     if work is None or work.numel() < floats:
-        work = _partials[key] = torch.empty(floats, dtype=torch.float32, device="cuda")
-    return counters, work
+        work = _partials[dev, handle] = torch.empty(floats, dtype=torch.float32, device="cuda")
+    return work
+
+
+def _stream_counters(n, dev, handle):
+    """Zeroed completion counters of n rows."""
+    torch = _torch()
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.zeros(n, dtype=torch.int32, device="cuda")
+    counters = _counters.get((dev, handle))
+    if counters is None or counters.numel() < n:
+        with _lock:
+            counters = torch.zeros(max(n, 4096), dtype=torch.int32, device="cuda")
+            torch.cuda.synchronize(dev)  # zeroed before the stream uses it, and no longer in use
+            _counters[dev, handle] = counters
+    return counters
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -315,17 +326,18 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
             min_rows_per_split = rows.value
     pp = ps = None
     if n_splits > 1:
-        if parts is None:  # both partials in one allocation
+        if parts is None:
             rows = total * Hq * n_splits
-            work = torch.empty(rows * (d + 1), dtype=torch.float32, device="cuda")
+            work = _workspace(rows * (d + 1), dev, handle)
             pp = work.data_ptr()
             ps = pp + rows * d * 4
         else:
             pp = _sized(parts[0], "parts[0]", torch.float32, dev, total, Hq, n_splits, d)
             ps = _sized(parts[1], "parts[1]", torch.float32, dev, total, Hq, n_splits)
-    rc = lib.attn_prefill_paged(qp, kp, vp, op, lp, tp, cu, np_, B, Hq, Hkv, total, max_sq, max_pages, page, n_pages,
-                                d, int(causal), window, n_sink, scale, n_splits, min_rows_per_split, pp, ps, code,
-                                handle)
+    with _launching:
+        rc = lib.attn_prefill_paged(qp, kp, vp, op, lp, tp, cu, np_, B, Hq, Hkv, total, max_sq, max_pages, page,
+                                    n_pages, d, int(causal), window, n_sink, scale, n_splits, min_rows_per_split, pp,
+                                    ps, code, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_prefill_paged")
     return o, lse
@@ -363,16 +375,15 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
     pp = ps = cp = None
     if n_splits > 1:
         rows = B * Hq * n_splits
-        if parts is None or counters is None:
-            own, work = _decode_workspace(B * Hq, rows * (d + 1) if parts is None else 0, dev, handle)
         if parts is None:
+            work = _workspace(rows * (d + 1), dev, handle)
             pp = work.data_ptr()
             ps = pp + rows * d * 4
         else:
             pp = _sized(parts[0], "parts[0]", torch.float32, dev, B, Hq, n_splits, d)
             ps = _sized(parts[1], "parts[1]", torch.float32, dev, B, Hq, n_splits)
         if counters is None:
-            counters = own
+            counters = _stream_counters(B * Hq, dev, handle)
         elif counters.dtype != torch.int32 or counters.get_device() != dev or counters.numel() < B * Hq:
             raise TypeError("counters must be a CUDA int32 tensor of at least B*Hq entries")
         cp = counters.data_ptr()
@@ -385,8 +396,9 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
         op = _sized(o, "out[0]", o.dtype, dev, B, Hq, d)
         lp = _sized(lse, "out[1]", torch.float32, dev, B, Hq)
     code = _out_code(o.dtype)
-    rc = lib.attn_decode_paged(qp, kp, vp, tp, np_, B, Hq, Hkv, d, max_pages, page, n_pages, scale, n_splits,
-                               min_rows_per_split, pp, ps, op, lp, code, cp, handle)
+    with _launching:
+        rc = lib.attn_decode_paged(qp, kp, vp, tp, np_, B, Hq, Hkv, d, max_pages, page, n_pages, scale, n_splits,
+                                   min_rows_per_split, pp, ps, op, lp, code, cp, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged")
     return o, lse

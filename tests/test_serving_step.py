@@ -240,6 +240,44 @@ def test_steps_on_two_streams_at_once():
     attn.sync_check()
 
 
+def test_threads_on_one_stream():
+    """Two host threads make split calls on the same stream: their launches and workspaces do
+    not mix."""
+    import threading
+    states = [_state(11, new=[30, 1, 0, 17, 3]), _state(12, new=[9, 20, 5, 1, 30])]
+    one = [_state(13, B=9), _state(14, B=9)]
+    want, got, errors = [], [[], []], []
+
+    def chunk(s):
+        q = s["x"][:, :Hq].contiguous()
+        return attn.prefill_paged(q, s["kc"], s["vc"], s["table"], s["cu"], s["lens"], s["max_sq"], n_splits=3)
+
+    def token(s):
+        return attn.decode_paged(s["x"][:, :Hq].contiguous(), s["kc"], s["vc"], s["table"], s["lens"], 4)
+
+    want = [(chunk(s), token(o)) for s, o in zip(states, one)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            for _ in range(50):
+                got[i].append((chunk(states[i]), token(one[i])))
+        except Exception as e:  # pragma: no cover
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for i in (0, 1):
+        for c, o in got[i]:
+            _same(list(c) + list(o), list(want[i][0]) + list(want[i][1]))
+    attn.sync_check()
+
+
 def test_long_pools():
     """Rows behind 2^31 elements of a pool: append, weights and both forms of eviction."""
     page, H, D = 256, 8, 256
