@@ -92,13 +92,8 @@ def _elsewhere(call, lead, stream):
         return result
 
 
-def _need(t, name, dtype, ndim, dev, contiguous=True):
-    """The tensor's pointer; raises unless it is what the call reads or writes."""
-    try:
-        if t.get_device() == dev and t.dtype is dtype and t.dim() == ndim and (not contiguous or t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:
-        pass
+def _refuse(t, name, dtype, ndim, dev, contiguous=True):
+    """Why a tensor is not what the call reads or writes."""
     if not isinstance(t, _torch().Tensor) or not t.is_cuda or t.get_device() != dev:
         raise TypeError(f"{name} must be a CUDA tensor on device {dev}")
     if t.dtype != dtype:
@@ -106,12 +101,25 @@ def _need(t, name, dtype, ndim, dev, contiguous=True):
     raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}{ndim}-D tensor")
 
 
+def _need(t, name, dtype, ndim, dev):
+    """A contiguous tensor's pointer."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.is_contiguous() and t.dim() == ndim:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, ndim, dev)
+
+
 def _sized(t, name, dtype, dev, *want):
     """A contiguous tensor of exactly that shape: its pointer."""
-    p = _need(t, name, dtype, len(want), dev)
-    if t.shape != want:
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.is_contiguous() and t.shape == want:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if _need(t, name, dtype, len(want), dev) is not None:
         raise ValueError(f"{name} must have shape {list(want)}, got {list(t.shape)}")
-    return p
 
 
 def _cache(kcache, vcache, page_table, B, dev, need_table=False):
@@ -213,16 +221,21 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, device="cuda", factor:
     return f.to(device), amp
 
 
-def _token_rows(t, name, dev, total, H, d):
+def _token_rows(t, name, bf16, dev, total, H, d):
     """Rows of tokens [total, H, d] with any stride between tokens (a view of a fused
     projection's output, say): (pointer, stride in elements)."""
-    p = _need(t, name, _torch().bfloat16, 3, dev, contiguous=False)
+    try:
+        good = t.get_device() == dev and t.dtype is bf16 and t.dim() == 3
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse(t, name, bf16, 3, dev, contiguous=False)
     if t.shape != (total, H, d):
         raise ValueError(f"{name} must have shape {[total, H, d]}, got {list(t.shape)}")
     row, head, one = t.stride()
     if one != 1 or (H > 1 and head != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return p, (row if total > 1 else H * d)
+    return t.data_ptr(), (row if total > 1 else H * d)
 
 
 def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_seqlens_q=None, positions=None,
@@ -246,12 +259,12 @@ def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_
     np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
     total, B = k.shape[0], kv_lens.shape[0]
     kp, vp, tp, Hkv, d, max_pages, page, n_pages = _cache(kcache, vcache, page_table, B, dev)
-    kr, ks = _token_rows(k, "k", dev, total, Hkv, d)
-    vr, vs = _token_rows(v, "v", dev, total, Hkv, d)
+    kr, ks = _token_rows(k, "k", torch.bfloat16, dev, total, Hkv, d)
+    vr, vs = _token_rows(v, "v", torch.bfloat16, dev, total, Hkv, d)
     Hq, qr, qs, op = Hkv, None, 0, None
     if q is not None:
         Hq = q.shape[1]
-        qr, qs = _token_rows(q, "q", dev, total, Hq, d)
+        qr, qs = _token_rows(q, "q", torch.bfloat16, dev, total, Hq, d)
         if out is None:
             out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device="cuda")  # (q may be strided)
             op = out.data_ptr()
@@ -299,6 +312,7 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
     B = kv_lens.shape[0]
     kp, vp, tp, Hkv, d, max_pages, page, n_pages = _cache(kcache, vcache, page_table, B, dev, need_table=True)
     total, Hq, dq = q.shape
+    max_sq = int(max_sq)
     if dq != d:
         raise ValueError(f"q and the cache differ in head dim: {dq} and {d}")
     cu = _sized(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, B + 1)
@@ -336,7 +350,7 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
             ps = _sized(parts[1], "parts[1]", torch.float32, dev, total, Hq, n_splits)
     with _launching:
         rc = lib.attn_prefill_paged(qp, kp, vp, op, lp, tp, cu, np_, B, Hq, Hkv, total, max_sq, max_pages, page,
-                                    n_pages, d, int(causal), window, n_sink, scale, n_splits, min_rows_per_split, pp,
+                                    n_pages, d, int(causal), int(window), int(n_sink), scale, n_splits, min_rows_per_split, pp,
                                     ps, code, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_prefill_paged")
@@ -448,8 +462,8 @@ def key_weights(q, lse, kcache, kv_lens, weights, page_table=None, cu_seqlens_q=
     wp, w_stride = _weight_rows(weights, dev, B, Hkv, max_pages * page)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    rc = load().attn_key_weights(qp, lp, kp, tp, cu, np_, wp, w_stride, B, Hq, Hkv, total, max_sq, d, max_pages, page,
-                                 n_pages, int(causal), window, n_sink, scale, int(accumulate), handle)
+    rc = load().attn_key_weights(qp, lp, kp, tp, cu, np_, wp, w_stride, B, Hq, Hkv, total, int(max_sq), d, max_pages, page,
+                                 n_pages, int(causal), int(window), int(n_sink), scale, int(accumulate), handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_key_weights")
     return weights
@@ -473,6 +487,7 @@ def evict(weights, kcache, vcache, kv_lens, budget: int, n_recent: int = 0, n_si
         return _elsewhere(lambda: evict(weights, kcache, vcache, kv_lens, budget, n_recent, n_sink, page_table, dst,
                                         out), kcache, stream)
     handle = torch._C._cuda_getCurrentRawStream(dev)
+    budget, n_recent, n_sink = int(budget), int(n_recent), int(n_sink)
     np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
     B = kv_lens.shape[0]
     if vcache is None:

@@ -438,8 +438,8 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
       uint8_t* const ring = is_k ? sK : sV;
       const CUtensorMap* const map = is_k ? &tm_k : &tm_v;
       if (PAGED && kv.box_rows > 0) {
-        // Pages of whole boxes: tensor copies, 128 / box_rows a panel.  (A page that
-        // is none is out of the map's bounds: zeros.)  The tile with the sequence's last
+        // Pages of whole boxes: tensor copies, 128 / box_rows a panel.  (A page that is none
+        // is read at the first one past the map's bounds: zeros.)  The tile with the sequence's last
         // keys is gathered, so that rows past them arrive as zeros.
         const int boxes = C::kStageRows / kv.box_rows;
         const int* const tab = kv.table + (size_t)b * kv.max_pages;
@@ -453,7 +453,10 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
             const int j = key0 + lane * kv.box_rows, e = j / kv.page_size;
             page = __ldg(tab + e);
             slot = j - e * kv.page_size;
-            if ((unsigned)page >= (unsigned)kv.num_pages) atomicCAS(err, kErrNone, kErrBadShape);
+            if ((unsigned)page >= (unsigned)kv.num_pages) {
+              atomicCAS(err, kErrNone, kErrBadShape);
+              page = kv.num_pages;
+            }
           }
           if (!mbar_wait_warp(&empty[s], ((uint32_t)(u / stages) & 1u) ^ 1u, err, abort_flag)) break;
           if (whole) {

@@ -404,7 +404,7 @@ unsigned long long attn_decode_noalloc_scratch_bytes(void);
  * cu_seqlens_q [B+1] (device) is clamped to [0, total]; tokens behind the last sequence are
  * neither read nor written.
  * All of these calls can be captured into a CUDA graph (nothing is allocated, looked up by
- * shape or synchronised), after one call of the library on that device.
+ * shape or synchronised), after a first call of their kind and head dim on that device.
  */
 
 /*

@@ -128,6 +128,22 @@ def test_bad_page_is_reported():
     assert torch.equal(o, good)
 
 
+def test_bad_page_of_whole_tiles_is_reported():
+    """The same where whole tiles are copied by pages: the other sequence stands."""
+    q, kc, vc, lens, kp, vp, table = _decode_case([500, 700], 8, 2, 128, 64, 314)
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    good, _ = attn.prefill_paged(q.cuda(), kp, vp, table, cu, lens.cuda(), 1, out_dtype=torch.float32)
+    attn.sync_check()
+    for bad in (-1, kp.shape[0], 2 ** 31 - 1, -2 ** 31):
+        t = table.clone()
+        t[1, 2] = bad
+        o, _ = attn.prefill_paged(q.cuda(), kp, vp, t, cu, lens.cuda(), 1, out_dtype=torch.float32)
+        with pytest.raises(attn.AttnError) as e:
+            attn.sync_check()
+        assert e.value.status == attn.ATTN_ERR_DEVICE_INPUT
+        assert torch.equal(o[0], good[0])
+
+
 # ------------------------------------------------------------------ chunks
 MIXED = [(1, 1), (77, 300), (128, 128), (300, 1200), (0, 50), (200, 150), (129, 1000), (3, 0), (36, 36)]
 SHORT = [(1, 1), (5, 300), (9, 9), (3, 1200), (0, 50), (8, 2), (4, 129)]
