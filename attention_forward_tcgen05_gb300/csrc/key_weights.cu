@@ -370,11 +370,18 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
     const uint64_t dl0 = smem_desc(smem_u32(sL), 128, 256, kSwizzleNone);
     for (int i = 0; i < n; ++i) {
       const int s = i % C::kStages, sl = i % C::kLse, buf = i & 1;
-      if ((t == 0 || two) &&
-          !mbar_wait_warp(&bar_F[t * 2 + buf], ((uint32_t)(i >> 1) & 1u) ^ 1u, a.err, abort_flag))
-        break;
-      if (!mbar_wait_warp(&full[s], (uint32_t)(i / C::kStages) & 1u, a.err, abort_flag)) break;
-      if (!mbar_wait_warp(&fullL[sl], (uint32_t)(i / C::kLse) & 1u, a.err, abort_flag)) break;
+      const uint32_t ph_f = ((uint32_t)(i >> 1) & 1u) ^ 1u, ph_q = (uint32_t)(i / C::kStages) & 1u,
+                     ph_l = (uint32_t)(i / C::kLse) & 1u;
+      const bool free_f = t == 1 && !two;  // no product, no buffer to wait for
+      // all three at once (a trip to each barrier in turn is three times the time, and the
+      // tensor pipe runs dry under it), and one by one only where they are not ready
+      const bool r0 = free_f || mbar_test(&bar_F[t * 2 + buf], ph_f);
+      const bool r1 = mbar_test(&full[s], ph_q), r2 = mbar_test(&fullL[sl], ph_l);
+      if (!__all_sync(0xFFFFFFFFu, r0 & r1 & r2)) {
+        if (!free_f && !mbar_wait_warp(&bar_F[t * 2 + buf], ph_f, a.err, abort_flag)) break;
+        if (!mbar_wait_warp(&full[s], ph_q, a.err, abort_flag)) break;
+        if (!mbar_wait_warp(&fullL[sl], ph_l, a.err, abort_flag)) break;
+      }
       if (t == 0 || two) {
         tc_fence_after();
         const uint64_t dq = dq0 + (uint64_t)((s * C::kQTile) >> 4);

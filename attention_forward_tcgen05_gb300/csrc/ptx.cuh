@@ -95,8 +95,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   }
 }
 
-// Whether that phase has completed, without waiting (whole warp, warp-uniform result).
-__device__ __forceinline__ bool mbar_test_warp(uint64_t* bar, uint32_t parity) {
+// Whether that phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -105,7 +105,10 @@ __device__ __forceinline__ bool mbar_test_warp(uint64_t* bar, uint32_t parity) {
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
-  return __all_sync(0xFFFFFFFFu, ok != 0);
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_test_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_test(bar, parity));
 }
 
 // ---------------------------------------------------------------- TMA
