@@ -75,7 +75,7 @@ def load(path: str | None = None):
         lib.attn_prefill_paged.argtypes = [vp] * 8 + [i] * 12 + [f, i, i, vp, vp, i, vp]
         lib.attn_prefill_paged_splits.argtypes = [i] * 7 + [vp]
         lib.attn_decode_paged.argtypes = [vp] * 5 + [i] * 7 + [f, i, i, vp, vp, vp, vp, i, vp, vp]
-        lib.attn_decode_paged_splits.argtypes = [i] * 5 + [vp]
+        lib.attn_decode_paged_splits.argtypes = [i] * 6 + [vp]
         lib.attn_key_weights.argtypes = [vp] * 7 + [ll] + [i] * 12 + [f, i, vp]
         lib.attn_evict.argtypes = [vp, vp, ll] + [vp] * 4 + [i] * 9 + [vp] * 3 + [i] * 3 + [vp] * 3
         for name in ("attn_rope_append", "attn_prefill_paged", "attn_prefill_paged_splits", "attn_decode_paged",

@@ -48,8 +48,8 @@ def attn_decode_paged(*args) -> int:
     return load().attn_decode_paged(*args)
 
 
-def attn_decode_paged_splits(B, Hq, Hkv, max_kv, d, min_rows) -> int:
-    return load().attn_decode_paged_splits(B, Hq, Hkv, max_kv, d, min_rows)
+def attn_decode_paged_splits(B, Hq, Hkv, max_kv, d, o_dtype, min_rows) -> int:
+    return load().attn_decode_paged_splits(B, Hq, Hkv, max_kv, d, o_dtype, min_rows)
 
 
 def attn_key_weights(*args) -> int:
@@ -377,6 +377,15 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
         raise ValueError(f"q and the cache differ in head dim: {dq} and {d}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    if out is None:
+        o = torch.empty_like(q) if out_dtype in (None, torch.bfloat16) else torch.empty_like(q, dtype=out_dtype)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device="cuda")
+        op, lp = o.data_ptr(), lse.data_ptr()
+    else:
+        o, lse = out
+        op = _sized(o, "out[0]", o.dtype, dev, B, Hq, d)
+        lp = _sized(lse, "out[1]", torch.float32, dev, B, Hq)
+    code = _out_code(o.dtype)
     lib = load()
     if n_splits == 0:
         if parts is not None:
@@ -384,7 +393,7 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
         else:
             rows = ctypes.c_int(1)
             n_splits = lib.attn_decode_paged_splits(B, Hq, Hkv, max_pages * page if max_kv is None else max_kv, d,
-                                                    ctypes.addressof(rows))
+                                                    code, ctypes.addressof(rows))
             min_rows_per_split = rows.value
     pp = ps = cp = None
     if n_splits > 1:
@@ -401,15 +410,6 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
         elif counters.dtype != torch.int32 or counters.get_device() != dev or counters.numel() < B * Hq:
             raise TypeError("counters must be a CUDA int32 tensor of at least B*Hq entries")
         cp = counters.data_ptr()
-    if out is None:
-        o = torch.empty_like(q) if out_dtype in (None, torch.bfloat16) else torch.empty_like(q, dtype=out_dtype)
-        lse = torch.empty((B, Hq), dtype=torch.float32, device="cuda")
-        op, lp = o.data_ptr(), lse.data_ptr()
-    else:
-        o, lse = out
-        op = _sized(o, "out[0]", o.dtype, dev, B, Hq, d)
-        lp = _sized(lse, "out[1]", torch.float32, dev, B, Hq)
-    code = _out_code(o.dtype)
     with _launching:
         rc = lib.attn_decode_paged(qp, kp, vp, tp, np_, B, Hq, Hkv, d, max_pages, page, n_pages, scale, n_splits,
                                    min_rows_per_split, pp, ps, op, lp, code, cp, handle)

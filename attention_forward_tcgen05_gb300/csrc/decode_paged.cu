@@ -1,7 +1,7 @@
 // decode_paged.cu -- one-token GQA decode over a paged cache: split-KV partials and their
 // LSE-weighted merge in one launch, the split rule and combine of decode.cu.
 //
-// One CTA per (sequence, KV head, split, group of up to 16 query heads); its four warps take
+// One CTA per (sequence, KV head, split), groups of up to 16 query heads; its four warps take
 // 32-key runs of the split in turn and share nothing until the end.  Each warp gathers 16
 // keys of K and V at a time into a ring of its own (cp.async groups: no barrier, no
 // producer warp), and does on its own fragments
@@ -54,15 +54,12 @@ struct DecodePagedCfg {
 // F32: the output is fp32 (see above); else bf16.
 template <int D, int NB, bool F32>
 __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks)
-    decode_paged_kernel(const DecodeArgs a, int heads_per_cta) {
+    decode_paged_kernel(const DecodeArgs a) {
   using C = DecodePagedCfg<D, NB>;
   constexpr int ST = C::kStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int Gall = a.Hq / a.Hkv, n_hg = (Gall + heads_per_cta - 1) / heads_per_cta;
-  const int per_unit = a.Hkv * n_hg;
-  const int pos = (int)(blockIdx.x / per_unit), w_in = (int)(blockIdx.x % per_unit);
-  const int hk = w_in / n_hg, g0 = w_in % n_hg * heads_per_cta;
-  const int G = min(heads_per_cta, Gall - g0);
+  const int G = a.Hq / a.Hkv;
+  const int pos = (int)(blockIdx.x / a.Hkv), hk = (int)(blockIdx.x % a.Hkv);
   const int b = pos / a.n_splits, s_idx = pos % a.n_splits;
   int L = a.kv_lens[b];
   L = L < 0 ? 0 : (L > a.max_kv ? a.max_kv : L);
@@ -71,7 +68,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
   if (chunk < 1) chunk = 1;
   const long long lo_ll = (long long)s_idx * chunk, hi_ll = lo_ll + chunk;
   const int lo = (int)(lo_ll < L ? lo_ll : L), hi = (int)(hi_ll < L ? hi_ll : L);
-  const size_t orow0 = (size_t)b * a.Hq + (size_t)hk * Gall + g0;  // (sequence, first query head)
+  const size_t orow0 = (size_t)b * a.Hq + (size_t)hk * G;  // (sequence, first query head)
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -265,31 +262,27 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
 }
 
 template <int D, int NB>
-cudaError_t launch_t(const DecodeArgs& a, int heads_per_cta, cudaStream_t stream) {
+cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
   using C = DecodePagedCfg<D, NB>;
   auto kern = a.o_bf16 ? decode_paged_kernel<D, NB, false> : decode_paged_kernel<D, NB, true>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int n_hg = (a.Hq / a.Hkv + heads_per_cta - 1) / heads_per_cta;
-  const long long ctas = (long long)a.B * a.n_splits * a.Hkv * n_hg;
+  const long long ctas = (long long)a.B * a.n_splits * a.Hkv;
   if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  kern<<<(unsigned)ctas, kWarps * 32, C::kSmem, stream>>>(a, heads_per_cta);
+  kern<<<(unsigned)ctas, kWarps * 32, C::kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
-// Heads of a group that one CTA takes: all up to 16, else equal shares of at most 16 (their
-// CTAs are neighbours and read the same rows, from L2).
+// A CTA takes a whole group: larger ones than 16 run on the prefill's tiles (paged_api.cu).
 template <int D>
 cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
-  const int G = a.Hq / a.Hkv, n_hg = (G + 15) / 16, hpc = (G + n_hg - 1) / n_hg;
-  return hpc <= 8 ? launch_t<D, 1>(a, hpc, stream) : launch_t<D, 2>(a, hpc, stream);
+  return a.Hq / a.Hkv <= 8 ? launch_t<D, 1>(a, stream) : launch_t<D, 2>(a, stream);
 }
 
 }  // namespace
 
 int decode_paged_slots(int d, int G, int sms) {
-  const int n_hg = (G + 15) / 16, hpc = (G + n_hg - 1) / n_hg;
-  return sms * decode_paged_ctas(d, hpc <= 8 ? 1 : 2);
+  return sms * decode_paged_ctas(d, G <= 8 ? 1 : 2);
 }
 
 cudaError_t launch_decode_paged(const DecodeArgs& a, cudaStream_t stream) {

@@ -42,12 +42,82 @@ attn::PagedKV cache(const attn_bf16_t* k, const attn_bf16_t* v, const int* table
   return attn::PagedKV{k, v, table, max_pages, page_size, num_pages, 0};
 }
 
+// Whether a decode runs on the prefill's tensor-core tiles, a group's heads as their rows,
+// instead of on warp-level mma, where heads above 8 cost as much again and above 16 read
+// their keys again.  A tile's start and end take 7 us, so bf16 outputs of groups of 9 to 16
+// go there while one wave of tiles holds them (64 units of up to 8000 keys, groups of 16: 38
+// against 52 us; 256 units of up to 300 keys: 20 against 13 us), larger groups always (64
+// units, groups of 32: 38 against 74 us; at d = 256, groups of 20: 68 against 134 us).  fp32
+// outputs of up to 16 heads stay: the tiles keep P to two terms, mma to three.
+bool decode_on_tiles(int B, int Hq, int Hkv, int o_dtype) {
+  const int G = Hq / Hkv;
+  return G > 16 || (G > 8 && o_dtype == ATTN_BF16 && (long long)B * Hkv <= kSms);
+}
+
 // Query heads that share a tile of `rows` rows: the largest divisor of G whose whole
 // positions fill at least 7/8 of the tile (1 always does).
 int pack_heads(int G, int rows) {
   for (int p = G < rows ? G : rows; p > 1; --p)
     if (G % p == 0 && rows / p * p * 8 >= rows * 7) return p;
   return 1;
+}
+
+// Key splits of a prefill over pages with `pack` heads a tile, and their least rows.
+int prefill_splits(int B, int Hq, int total_q, int max_sq, int max_kv, int d, int pack, int* min_rows) {
+  const int pos = attn::kPrefillTileM / pack;
+  const bool halves = d <= 128 && max_sq <= pos;
+  // blocks of query rows that exist, one unit each, and a unit's time for a tile of keys
+  const long long block = d <= 128 && !halves ? 2 * pos : pos;
+  const long long blocks = std::min<long long>((long long)total_q / block + B, (max_sq + block - 1) / block * B);
+  const long long units = std::max(1LL, blocks * (Hq / pack));
+  const double tile_us = halves ? 1.2 : (d == 64 ? 1.4 : 1.8);
+  const double tiles = (max_kv + 127) / 128;
+  // a batch's sequences are taken to be 0.6 of the longest on average
+  const double mean = B > 1 ? 0.6 : 1.0;
+  double best = 0;
+  int n_best = 1;
+  for (int n = 1; n <= 32 && n <= std::max(1.0, tiles / 2); ++n) {
+    const double rows = std::ceil(tiles / n);  // of a split, in tiles
+    const double live = (double)units * std::max(1.0, std::min((double)n, mean * tiles / rows + (n > 1 && B > 1 ? 0.5 : 0)));
+    // waves of units, each with its own start and end; the partials out and in again, and
+    // the merge's launch
+    const double us = std::ceil(live / kSms) * (rows * tile_us + 4.0) +
+                      (n > 1 ? 4.0 + (double)total_q * Hq * d * 8.0 * n * mean / 5.0e6 : 0.0);
+    if (n == 1 || us < best * 0.97) {
+      best = us;
+      n_best = n;
+    }
+  }
+  *min_rows = (int)std::ceil(tiles / n_best) * 128;
+  return n_best;
+}
+
+// The launches of a prefill over pages (arguments checked, a.pack and the rows set): query and
+// output maps over [nb][ns][Hq][d], pool maps, the kernel, and the merge of key splits into
+// m.
+int launch_paged(attn::PrefillArgs& a, const attn_bf16_t* q, int ns, int nb, attn::MergeArgs& m, cudaStream_t s) {
+  a.err = attn::device_err_word();
+  if (a.err == nullptr) return ATTN_ERR_CUDA;
+  int rc = attn::encode_q_map(&a.tm_q, q, a.d, a.pack, a.Hq, ns, nb, attn::kPrefillTileM);
+  a.o_tma = (a.o_bf16 && a.n_splits <= 1) ? 1 : 0;
+  if (rc == ATTN_OK && a.o_tma) rc = attn::encode_q_map(&a.tm_o, a.o, a.d, a.pack, a.Hq, ns, nb, attn::kPrefillTileM);
+  // Tensor copies of the largest power of two of rows (8 to 128; the swizzle repeats every 8)
+  // that divides the page; other pages are gathered.  Pages of 16 / 64 keys, copies against
+  // gathers: 164 / 162 against 248 / 242 us (eight chunks, 145 GFLOP), the same to 128 rows: the
+  // producer warps' instructions are what the softmax warps miss.
+  for (a.kv.box_rows = 128; a.kv.box_rows >= 8 && a.kv.page_size % a.kv.box_rows != 0;) a.kv.box_rows /= 2;
+  if (a.kv.box_rows < 8) a.kv.box_rows = 0;
+  if (rc == ATTN_OK && a.kv.box_rows > 0) {
+    rc = attn::encode_pool_map(&a.tm_k, a.kv.k, a.d, a.Hkv, a.kv.page_size, a.kv.num_pages, a.kv.box_rows);
+    if (rc == ATTN_OK)
+      rc = attn::encode_pool_map(&a.tm_v, a.kv.v, a.d, a.Hkv, a.kv.page_size, a.kv.num_pages, a.kv.box_rows);
+  }
+  if (rc != ATTN_OK) return rc;
+  rc = from_cuda(a.o_bf16 ? attn::launch_prefill_paged(a, s) : attn::launch_prefill_paged_f32(a, s));
+  if (rc != ATTN_OK || a.n_splits == 1) return rc;
+  m.part_o = a.part_o; m.part_lse = a.part_lse; m.o = a.o; m.lse = a.lse;
+  m.Hq = a.Hq; m.n_splits = a.n_splits; m.d = a.d; m.o_bf16 = a.o_bf16;
+  return from_cuda(attn::launch_merge(m, s));
 }
 
 }  // namespace
@@ -97,32 +167,7 @@ int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, i
   if (check_heads(B, Hq, Hkv) != ATTN_OK || total_q < 0 || max_sq < 0 || max_kv < 0 || !ok_dim(d) ||
       min_rows == nullptr)
     return ATTN_ERR_INVALID_ARG;
-  const int pack = pack_heads(Hq / Hkv, attn::kPrefillTileM), pos = attn::kPrefillTileM / pack;
-  const bool halves = d <= 128 && max_sq <= pos;
-  // blocks of query rows that exist, one unit each, and a unit's time for a tile of keys
-  const long long block = d <= 128 && !halves ? 2 * pos : pos;
-  const long long blocks = std::min<long long>((long long)total_q / block + B, (max_sq + block - 1) / block * B);
-  const long long units = std::max(1LL, blocks * (Hq / pack));
-  const double tile_us = halves ? 1.2 : (d == 64 ? 1.4 : 1.8);
-  const double tiles = (max_kv + 127) / 128;
-  // a batch's sequences are taken to be 0.6 of the longest on average
-  const double mean = B > 1 ? 0.6 : 1.0;
-  double best = 0;
-  int n_best = 1;
-  for (int n = 1; n <= 32 && n <= std::max(1.0, tiles / 2); ++n) {
-    const double rows = std::ceil(tiles / n);  // of a split, in tiles
-    const double live = (double)units * std::max(1.0, std::min((double)n, mean * tiles / rows + (n > 1 && B > 1 ? 0.5 : 0)));
-    // waves of units, each with its own start and end; the partials out and in again, and
-    // the merge's launch
-    const double us = std::ceil(live / kSms) * (rows * tile_us + 4.0) +
-                      (n > 1 ? 4.0 + (double)total_q * Hq * d * 8.0 * n * mean / 5.0e6 : 0.0);
-    if (n == 1 || us < best * 0.97) {
-      best = us;
-      n_best = n;
-    }
-  }
-  *min_rows = (int)std::ceil(tiles / n_best) * 128;
-  return n_best;
+  return prefill_splits(B, Hq, total_q, max_sq, max_kv, d, pack_heads(Hq / Hkv, attn::kPrefillTileM), min_rows);
 }
 
 int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const attn_bf16_t* vcache, void* o, float* lse,
@@ -167,42 +212,26 @@ int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const at
   // every sequence's rows fit one tile: the other tile takes half of the keys
   a.halves = (window == 0 && d <= 128 && max_sq <= attn::kPrefillTileM / a.pack) ? 1 : 0;
   a.kv = cache(kcache, vcache, page_table, max_pages, page_size, num_pages);
-  a.err = attn::device_err_word();
-  if (a.err == nullptr) return ATTN_ERR_CUDA;
-  rc = attn::encode_q_map(&a.tm_q, q, d, a.pack, Hq, total_q, 1, attn::kPrefillTileM);
-  a.o_tma = (o_dtype == ATTN_BF16 && n_splits <= 1) ? 1 : 0;
-  if (rc == ATTN_OK && a.o_tma) rc = attn::encode_q_map(&a.tm_o, o, d, a.pack, Hq, total_q, 1, attn::kPrefillTileM);
-  // Tensor copies of the largest power of two of rows (8 to 128; the swizzle repeats every 8)
-  // that divides the page; other pages are gathered.  Pages of 16 / 64 keys, copies against
-  // gathers: 164 / 162 against 248 / 242 us (eight chunks, 145 GFLOP), the same to 128 rows: the
-  // producer warps' instructions are what the softmax warps miss.
-  for (a.kv.box_rows = 128; a.kv.box_rows >= 8 && page_size % a.kv.box_rows != 0;) a.kv.box_rows /= 2;
-  if (a.kv.box_rows < 8) a.kv.box_rows = 0;
-  if (rc == ATTN_OK && a.kv.box_rows > 0) {
-    rc = attn::encode_pool_map(&a.tm_k, kcache, d, Hkv, page_size, num_pages, a.kv.box_rows);
-    if (rc == ATTN_OK) rc = attn::encode_pool_map(&a.tm_v, vcache, d, Hkv, page_size, num_pages, a.kv.box_rows);
-  }
-  if (rc != ATTN_OK) return rc;
-  rc = from_cuda(a.o_bf16 ? attn::launch_prefill_paged(a, stream_of(stream))
-                          : attn::launch_prefill_paged_f32(a, stream_of(stream)));
-  if (rc != ATTN_OK || n_splits == 1) return rc;
   attn::MergeArgs m;
-  m.part_o = part_o; m.part_lse = part_lse; m.o = o; m.lse = lse;
-  m.B = total_q; m.Hq = Hq; m.n_splits = n_splits; m.d = d; m.o_bf16 = a.o_bf16;
+  m.B = total_q;
   m.lse_by_head = 1;
   m.cu_q = cu_seqlens_q;
   m.n_seq = B;
-  return from_cuda(attn::launch_merge(m, stream_of(stream)));
+  return launch_paged(a, q, total_q, 1, m, stream_of(stream));
 }
 
-int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int* min_rows) {
-  if (check_heads(B, Hq, Hkv) != ATTN_OK || max_kv < 0 || !ok_dim(d) || min_rows == nullptr) return ATTN_ERR_INVALID_ARG;
+int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int o_dtype, int* min_rows) {
+  if (check_heads(B, Hq, Hkv) != ATTN_OK || max_kv < 0 || !ok_dim(d) || min_rows == nullptr ||
+      (o_dtype != ATTN_BF16 && o_dtype != ATTN_F32))
+    return ATTN_ERR_INVALID_ARG;
+  if (decode_on_tiles(B, Hq, Hkv, o_dtype))
+    return prefill_splits(B, Hq, B, 1, max_kv, d, std::min(Hq / Hkv, attn::kPrefillTileM), min_rows);
   // as many CTAs as run at once: one wave, its splits at least 192 rows; beyond 48 splits the
   // merge takes longer than the keys it saves.  A batch's lengths differ, so a few splits are
   // rounded up (64 units of up to 8000 keys: 57 us with 3 splits, 78 with 2); from half a wave
   // of units on, whole sequences do best (1024 units of up to 1000 keys: 51 against 59 us).
   const int G = Hq / Hkv;
-  const double units = std::max(1.0, (double)B * Hkv * ((G + 15) / 16));
+  const double units = std::max(1.0, (double)B * Hkv);
   const double q = attn::decode_paged_slots(d, G, kSms) / units;
   long long n = q < 2 ? 1 : (long long)(q <= 8 && B > 1 ? std::ceil(q) : q);
   n = std::max(1LL, std::min(std::min(n, 48LL), (max_kv + 191LL) / 192));
@@ -225,6 +254,28 @@ int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const att
     rc = attn::check_merge_args(part_o, part_lse, o, lse, B, Hq, n_splits, d, o_dtype, n_splits > 1);
   if (rc != ATTN_OK || B == 0) return rc;
   if (!ok4(page_table) || (n_splits > 1 && !ok4(counters))) return ATTN_ERR_INVALID_ARG;
+  if (decode_on_tiles(B, Hq, Hkv, o_dtype)) {
+    // a group's heads as the rows of one tensor-core tile: its keys are read once
+    attn::PrefillArgs p;
+    std::memset(&p, 0, sizeof(p));
+    p.o = o; p.lse = lse;
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = 1; p.Skv = max_pages * page_size; p.d = d;
+    p.causal = 1;
+    p.o_bf16 = o_dtype == ATTN_BF16 ? 1 : 0;
+    p.scale = scale;
+    p.kv_lens = kv_lens;
+    p.pack = Hq / Hkv;
+    p.n_splits = n_splits; p.split_min = min_rows_per_split;
+    p.part_o = part_o; p.part_lse = part_lse;
+    p.halves = d <= 128 ? 1 : 0;
+    p.kv = cache(kcache, vcache, page_table, max_pages, page_size, num_pages);
+    attn::MergeArgs m;
+    m.B = B;
+    m.lse_by_head = 0;
+    m.cu_q = nullptr;
+    m.n_seq = 0;
+    return launch_paged(p, q, 1, B, m, stream_of(stream));
+  }
   attn::DecodeArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = q; a.kv_lens = kv_lens; a.part_o = part_o; a.part_lse = part_lse;

@@ -218,10 +218,10 @@ __device__ __noinline__ int2 block_of_rank(int r, int B, int Sq_max, int Skv_max
 // position, its G <= 128 head rows):
 // both query tiles hold the same rows and take the two halves of the unit's keys,
 // so their S -> softmax -> P.V chains overlap; the halves merge in the epilogue.
-// PAGED (packed varlen batches): K/V rows come from the pages of kv, by tensor copies of
-// kv.box_rows rows or gathered by the producer warps (paged.cuh), rows past the sequence's
-// keys as zeros; a query tile
-// holds floor(128 / G) whole positions (any G), and key splits start on a KV tile.
+// PAGED (packed varlen batches, or one token each with kv_lens): K/V rows come from the pages
+// of kv, by tensor copies of kv.box_rows rows or gathered by the producer warps (paged.cuh),
+// rows past the sequence's keys as zeros; a query tile holds floor(128 / G) whole positions
+// (any G), and key splits start on a KV tile.
 // FINE (fp32 outputs over pages): P goes into P.V as two bf16 terms, its value and the
 // remainder, the second over the other half of S's columns (2^-17 of P left out instead of
 // 2^-9), and O is divided by the exact row sum.
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
       for (int r = threadIdx.x; r < NQ * TR; r += C::kThreads) {
         const int row = qb * NQ * TR + r;
         if (row < Sr)
-          part_lse[((size_t)(ext.qbase + row / G) * Hq + hu * G + row % G) * NSPL + sp] = -INFINITY;
+          part_lse[(((size_t)ext.bq * ext.rows + ext.qbase + row / G) * Hq + hu * G + row % G) * NSPL + sp] = -INFINITY;
       }
       return;
     }
@@ -881,8 +881,9 @@ __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
     const int hq = hu * G + qg;  // query head of this row
     // with key splits the row is a decode partial: part_o / part_lse [B][Hq][n_splits]
     const bool partial = SPLIT;
-    // (packed varlen: [total_q][Hq][n_splits])
-    const size_t prow = ((PAGED ? (size_t)ext.qbase + (row_ok ? qpos : 0) : (size_t)b) * Hq + hq) * NSPL + sp;
+    // (paged: row of the batch's slab of q, [total_q][Hq][n_splits] for packed varlen)
+    const size_t prow =
+        ((PAGED ? (size_t)ext.bq * ext.rows + ext.qbase + (row_ok ? qpos : 0) : (size_t)b) * Hq + hq) * NSPL + sp;
     const size_t orow = partial ? prow
                                 : ((size_t)ext.bq * ext.rows + ext.qbase + (size_t)(row_ok ? qpos : 0)) * Hq + hq;
     void* const out = partial ? static_cast<void*>(part_o) : o_ptr;

@@ -468,7 +468,10 @@ int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, i
 /*
  * attn_decode_paged -- attn_decode over a paged cache: one launch, the same split rule,
  * partials, counters and results (to rounding).  With n_splits = 1 the result is written
- * directly: part_o, part_lse and counters are not touched and may be NULL.
+ * directly: part_o, part_lse and counters are not touched and may be NULL.  Groups of more than
+ * 16 query heads (bf16 outputs: more than 8 when B * Hkv <= 152) run on the tensor-core tiles
+ * of attn_prefill_paged instead: splits of whole 128-key tiles, part_o of empty ones unwritten,
+ * merged in a second launch without the counters.
  *
  * Arguments: as attn_decode, with page_table int32 [B][max_pages] and pools
  * [num_pages][page_size][Hkv][d] in place of the caches and max_kv.
@@ -482,7 +485,7 @@ int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const att
 
 /* The n_splits (>= 1) and min_rows_per_split that suit a decode of these sizes, max_kv
  * keys in the longest sequence (host only); ATTN_ERR_INVALID_ARG for bad sizes. */
-int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int* min_rows_per_split);
+int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int o_dtype, int* min_rows_per_split);
 
 /*
  * attn_key_weights -- the attention weight that every cached key received.

@@ -32,14 +32,26 @@ def _check_decode(o, lse, q, kc, vc, lens, scale, bf16):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (14, 2), (8, 1), (12, 1), (40, 2)])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (14, 2), (8, 1), (12, 1), (40, 2), (128, 1), (67, 1)])
 @pytest.mark.parametrize("page", [1, 16, 48, 256])
 def test_decode(d, Hq, Hkv, page):
     q, kc, vc, lens, kp, vp, table = _decode_case(LENS, Hq, Hkv, d, page, 300 + d + page)
     scale = 1.0 / np.sqrt(d)
-    for out_dtype, kw in ((torch.float32, {}), (torch.bfloat16, dict(n_splits=5, min_rows_per_split=33))):
+    for out_dtype, kw in ((torch.float32, {}), (torch.bfloat16, {}),
+                          (torch.bfloat16, dict(n_splits=5, min_rows_per_split=33))):
         o, lse = attn.decode_paged(q.cuda(), kp, vp, table, lens.cuda(), scale=scale, out_dtype=out_dtype, **kw)
         _check_decode(o, lse, q, kc, vc, lens, scale, out_dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(32, 2, 64), (12, 1, 128), (24, 2, 256), (16, 1, 128)])
+def test_decode_of_many_sequences(Hq, Hkv, d):
+    """Groups of 9 to 16 heads in more sequences than one wave of tiles holds (160 units)."""
+    rng = np.random.default_rng(9)
+    lens = [int(x) for x in rng.integers(0, 200, 160 // Hkv)]
+    q, kc, vc, lens, kp, vp, table = _decode_case(lens, Hq, Hkv, d, 16, 330 + d)
+    for n_splits in (0, 1, 3):
+        o, lse = attn.decode_paged(q.cuda(), kp, vp, table, lens.cuda(), n_splits)
+        _check_decode(o, lse, q, kc, vc, lens, 1.0 / np.sqrt(d), True)
 
 
 @pytest.mark.parametrize("n_splits,min_rows", [(1, 0), (3, 100), (8, 1)])

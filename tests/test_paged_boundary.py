@@ -170,15 +170,17 @@ def test_split_rules():
     assert attn.attn_prefill_paged_splits(1, 3, 2, 1, 1, 1, 64, r) == INVALID
     assert attn.attn_prefill_paged_splits(1, 4, 2, 1, 1, 1, 96, r) == INVALID
     assert attn.attn_prefill_paged_splits(1, 4, 2, 1, 1, 1, 64, N) == INVALID
-    assert attn.attn_decode_paged_splits(1, 3, 2, 1, 64, r) == INVALID
-    assert attn.attn_decode_paged_splits(1, 4, 2, -1, 64, r) == INVALID
-    assert attn.attn_decode_paged_splits(1, 4, 2, 1, 64, N) == INVALID
+    assert attn.attn_decode_paged_splits(1, 3, 2, 1, 64, 0, r) == INVALID
+    assert attn.attn_decode_paged_splits(1, 4, 2, -1, 64, 0, r) == INVALID
+    assert attn.attn_decode_paged_splits(1, 4, 2, 1, 64, 0, N) == INVALID
+    assert attn.attn_decode_paged_splits(1, 4, 2, 1, 64, 2, r) == INVALID
     for B in (0, 1, 7, 64, 4096):
-        for Hq, Hkv in ((1, 1), (28, 4), (128, 1), (300, 2)):
+        for Hq, Hkv in ((1, 1), (28, 4), (32, 2), (128, 1), (300, 2)):
             for kv in (0, 1, 300, 5000, 1 << 20, 1 << 30):
                 for d in (64, 128, 256):
-                    n = attn.attn_decode_paged_splits(B, Hq, Hkv, kv, d, r)
-                    assert 1 <= n <= 1024 and rows.value >= 0 and (n == 1 or n * 192 < kv + 192)
+                    for dtype in (0, 1):
+                        n = attn.attn_decode_paged_splits(B, Hq, Hkv, kv, d, dtype, r)
+                        assert 1 <= n <= 1024 and rows.value >= 0 and (n == 1 or n * 192 < kv + 192)
                     for sq in (0, 1, 9, 600, 70000):
                         n = attn.attn_prefill_paged_splits(B, Hq, Hkv, B * sq, sq, kv, d, r)
                         # enough splits of rows.value rows for every key, and none of them idle
@@ -186,8 +188,8 @@ def test_split_rules():
     # few rows against many keys are split, a full batch is not
     assert attn.attn_prefill_paged_splits(1, 28, 4, 8, 8, 30000, 128, r) >= 8
     assert attn.attn_prefill_paged_splits(64, 28, 4, 64 * 512, 512, 4096, 128, r) == 1
-    assert attn.attn_decode_paged_splits(1, 28, 4, 30000, 128, r) >= 16
-    assert attn.attn_decode_paged_splits(512, 32, 8, 4096, 128, r) == 1
+    assert attn.attn_decode_paged_splits(1, 28, 4, 30000, 128, 0, r) >= 16
+    assert attn.attn_decode_paged_splits(512, 32, 8, 4096, 128, 0, r) == 1
 
 
 def test_helpers_refuse_host_tensors():
