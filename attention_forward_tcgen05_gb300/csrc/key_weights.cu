@@ -157,16 +157,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) key_weights_rows_kernel(con
 // otherwise).  Sixteen warps sum (thread = key): a warpgroup for each key tile and parity of
 // the query tile, each with a TMEM buffer of its own, read in two halves.  With eight warps
 // and one wait for all of S^T a query tile took 1.4 us, its warps mostly waiting together
-// for the buffers, barriers and loads; sixteen take 1.0 us, of which the exponentials are
-// 0.54.  Warps 16, 19: MMA issue, one key tile each
-// (a single warp's waits between the products left the tensor pipe idle for a third of the
-// time); warp 17: query tiles by TMA; warp 18: their lse, by plain loads
-// into sixteen further columns of the product, K' = (K, 1, 1, 1), Q' = (Q, -lse / scale in
-// three bf16 terms), so that S^T comes out as q . k - lse / scale: read from shared memory
-// under the exponentials instead, a value a column cost as many wavefronts as the MMA's
-// operands.  The
-// CTAs of a cluster share the keys and take every cs-th query tile; their sums meet in
-// rank 0, in rank order.
+// for the buffers, barriers and loads; sixteen take 0.86 us, of which the exponentials are
+// 0.54.  Warps 16, 19: MMA issue, one key tile each (a single warp's waits between the
+// products left the tensor pipe idle for a third of the time); warp 17: query tiles by TMA;
+// warp 18: their lse, by plain loads into sixteen further columns of the product,
+// K' = (K, 1, 1, 1), Q' = (Q, -lse / scale in three bf16 terms), so that S^T comes out as
+// q . k - lse / scale: read from shared memory under the exponentials instead, a value a
+// column cost as many wavefronts as the MMA's operands.  The CTAs of a cluster share the
+// keys and take every cs-th query tile; their sums meet in rank 0, in rank order.
 template <int D>
 struct TileCfg {
   static constexpr int QN = D == 256 ? 64 : 128;  // query rows of a tile
@@ -518,7 +516,7 @@ cudaError_t launch_tiles(const KeyWeightArgs& a, cudaStream_t stream) {
   const long long q_tiles = ((long long)a.max_sq + PT - 1) / PT * (a.Hq / a.Hkv / a.pack);
   // CTAs of a cluster, while SMs are idle and each keeps two query tiles: clusters of four
   // reach nearly every SM, of eight 120 of them (15 clusters), so eight only where all run at
-  // once (52 units of a 3314-token prompt: 101, 56, 80 us in clusters of 2, 4, 8)
+  // once (52 units of a 3314-token prompt: 84, 48, 73 us in clusters of 2, 4, 8)
   int cs = 1;
   while (cs < 4 && units * cs < 152 && q_tiles >= 4 * cs) cs *= 2;
   if (cs == 4 && units <= 15 && q_tiles >= 16) cs = 8;

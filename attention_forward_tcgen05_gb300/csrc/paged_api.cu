@@ -71,7 +71,7 @@ int prefill_splits(int B, int Hq, int total_q, int max_sq, int max_kv, int d, in
   const long long blocks = std::min<long long>((long long)total_q / block + B, (max_sq + block - 1) / block * B);
   const long long units = std::max(1LL, blocks * (Hq / pack));
   const double tile_us = halves ? 1.2 : (d == 64 ? 1.4 : 1.8);
-  const double tiles = (max_kv + 127) / 128;
+  const double tiles = (max_kv + 127LL) / 128;
   // a batch's sequences are taken to be 0.6 of the longest on average
   const double mean = B > 1 ? 0.6 : 1.0;
   double best = 0;
@@ -88,7 +88,7 @@ int prefill_splits(int B, int Hq, int total_q, int max_sq, int max_kv, int d, in
       n_best = n;
     }
   }
-  *min_rows = (int)std::ceil(tiles / n_best) * 128;
+  *min_rows = (int)std::min(std::ceil(tiles / n_best) * 128, (double)0x7FFFFF80);
   return n_best;
 }
 
@@ -206,7 +206,7 @@ int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const at
   a.total_q = total_q;
   a.pack = pack_heads(Hq / Hkv, attn::kPrefillTileM);
   a.n_splits = n_splits;
-  a.split_min = min_rows_per_split;
+  a.split_min = std::min(min_rows_per_split, max_pages * page_size);  // (rounded up to a tile there)
   a.part_o = part_o;
   a.part_lse = part_lse;
   // every sequence's rows fit one tile: the other tile takes half of the keys
@@ -265,7 +265,7 @@ int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const att
     p.scale = scale;
     p.kv_lens = kv_lens;
     p.pack = Hq / Hkv;
-    p.n_splits = n_splits; p.split_min = min_rows_per_split;
+    p.n_splits = n_splits; p.split_min = std::min(min_rows_per_split, max_pages * page_size);
     p.part_o = part_o; p.part_lse = part_lse;
     p.halves = d <= 128 ? 1 : 0;
     p.kv = cache(kcache, vcache, page_table, max_pages, page_size, num_pages);

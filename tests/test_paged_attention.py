@@ -231,6 +231,21 @@ def test_chunk_head_groups(G):
             check_lse(lse.cpu().numpy(), rl)
 
 
+def test_splits_of_more_rows_than_any_sequence():
+    """The largest min_rows_per_split an int holds: one split takes every key."""
+    big = (1 << 31) - 1
+    case = _chunk_case(MIXED, 4, 2, 128, 16, 445)
+    q, kc, vc, cu, kv = case[:5]
+    ro, rl = oracle.sdpa_varlen(q, kc, vc, cu, kv, True, 0.1)
+    o, lse = _run(case, scale=0.1, out_dtype=torch.float32, n_splits=3, min_rows_per_split=big)
+    check_o(o.cpu().numpy(), ro, False)
+    check_lse(lse.cpu().numpy(), rl)
+    for Hq in (4, 12, 20):
+        q, kc, vc, lens, kp, vp, table = _decode_case(LENS, Hq, 1, 64, 16, 446)
+        o, lse = attn.decode_paged(q.cuda(), kp, vp, table, lens.cuda(), 3, big, 0.125)
+        _check_decode(o, lse, q, kc, vc, lens, 0.125, True)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("window,n_sink", [(1, 0), (100, 4), (256, 130), (2000, 7)])
 def test_chunk_window(d, window, n_sink):

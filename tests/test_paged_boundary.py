@@ -185,6 +185,11 @@ def test_split_rules():
                         n = attn.attn_prefill_paged_splits(B, Hq, Hkv, B * sq, sq, kv, d, r)
                         # enough splits of rows.value rows for every key, and none of them idle
                         assert 1 <= n <= 32 and rows.value % 128 == 0 and n * rows.value >= kv, (B, Hq, kv, d, sq)
+    # the largest length an int holds
+    for B in (1, 4096):
+        assert 1 <= attn.attn_prefill_paged_splits(B, 28, 4, B, 1, (1 << 31) - 1, 128, r) <= 32
+        assert 0 < rows.value and rows.value % 128 == 0
+        assert 1 <= attn.attn_decode_paged_splits(B, 64, 2, (1 << 31) - 1, 128, 1, r) <= 48 and rows.value > 0
     # few rows against many keys are split, a full batch is not
     assert attn.attn_prefill_paged_splits(1, 28, 4, 8, 8, 30000, 128, r) >= 8
     assert attn.attn_prefill_paged_splits(64, 28, 4, 64 * 512, 512, 4096, 128, r) == 1
