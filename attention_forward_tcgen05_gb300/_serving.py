@@ -14,6 +14,7 @@ of the other calls.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import threading
 
@@ -150,6 +151,22 @@ def _out_code(dtype):
     if dtype is torch.float32:
         return ATTN_F32
     raise TypeError(f"unsupported output dtype {dtype}")
+
+
+# The split rules, kept by their sizes: the loops of a decode come with the same ones, and a
+# foreign call takes 3 us of a helper's 20.
+@functools.lru_cache(maxsize=1024)
+def _prefill_splits(B, Hq, Hkv, total, max_sq, max_kv, d):
+    rows = ctypes.c_int(1)
+    n = attn_prefill_paged_splits(B, Hq, Hkv, total, max_sq, max_kv, d, ctypes.addressof(rows))
+    return max(n, 1), rows.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_splits(B, Hq, Hkv, max_kv, d, code):
+    rows = ctypes.c_int(1)
+    n = attn_decode_paged_splits(B, Hq, Hkv, max_kv, d, code, ctypes.addressof(rows))
+    return max(n, 1), rows.value
 
 
 # Workspaces of prefill_paged and decode_paged: kept for each stream, whose launches are
@@ -333,11 +350,8 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
         if parts is not None:
             n_splits = parts[0].shape[2]
         elif not window:
-            rows = ctypes.c_int(1)
-            n_splits = max(1, lib.attn_prefill_paged_splits(B, Hq, Hkv, total, max_sq,
-                                                            max_pages * page if max_kv is None else max_kv, d,
-                                                            ctypes.addressof(rows)))
-            min_rows_per_split = rows.value
+            n_splits, min_rows_per_split = _prefill_splits(B, Hq, Hkv, total, max_sq,
+                                                           max_pages * page if max_kv is None else max_kv, d)
     pp = ps = None
     if n_splits > 1:
         if parts is None:
@@ -391,10 +405,8 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
         if parts is not None:
             n_splits = parts[0].shape[2]
         else:
-            rows = ctypes.c_int(1)
-            n_splits = lib.attn_decode_paged_splits(B, Hq, Hkv, max_pages * page if max_kv is None else max_kv, d,
-                                                    code, ctypes.addressof(rows))
-            min_rows_per_split = rows.value
+            n_splits, min_rows_per_split = _decode_splits(B, Hq, Hkv, max_pages * page if max_kv is None else max_kv,
+                                                          d, code)
     pp = ps = cp = None
     if n_splits > 1:
         rows = B * Hq * n_splits
@@ -507,7 +519,7 @@ def evict(weights, kcache, vcache, kv_lens, budget: int, n_recent: int = 0, n_si
         w2 = None if dw is None else _sized(dw, "dst weights", torch.float32, dev, B, Hkv, w_stride)
     if out is None:
         kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device="cuda")
-        lens = torch.empty(B, dtype=torch.int32, device="cuda")
+        lens = torch.empty_like(kv_lens)
         ep, lp = kept.data_ptr(), lens.data_ptr()
     else:
         kept, lens = out

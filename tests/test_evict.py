@@ -216,9 +216,40 @@ def test_evict(d, kind, budget, n_recent, n_sink, where):
         assert torch.equal(wg.cpu().view(torch.int32), w.view(torch.int32))
 
 
-def test_evict_rows_of_several_blocks():
-    """60,000 keys: four blocks of weights, three of them read again at each pass."""
-    L, d = 60000, 64
+@pytest.mark.parametrize("kind", ["random", "ties", "special"])
+@pytest.mark.parametrize("in_place", [True, False], ids=["in_place", "pages"])
+@pytest.mark.parametrize("B,Hkv,cap", [(9, 1, 9000), (60, 1, 8200), (5, 8, 3000)])
+def test_evict_rows_in_slices(kind, in_place, B, Hkv, cap):
+    """Rows that 4, 2 and 1 CTAs share, some shorter than a slice; the weights alone."""
+    rng = np.random.default_rng(6)
+    L = rng.integers(0, cap + 1, B)
+    L[:5] = [cap, 33, 0, 1, cap // 8]
+    w = weird_weights(B, Hkv, cap, kind, 7)
+    kc = torch.zeros(B, cap, Hkv, 64, dtype=torch.bfloat16, device="cuda")
+    wg, w2 = w.cuda(), torch.full((B, Hkv, cap), 9.0, device="cuda")
+    dst = None if in_place else (torch.zeros_like(kc), torch.zeros_like(kc), None, w2)
+    lens = torch.from_numpy(L.astype(np.int32)).cuda()
+    for budget, n_recent, n_sink in ((700, 100, 4), (33, 0, 0)):
+        if in_place:
+            wg.copy_(w)
+        kept, new = attn.evict(wg, kc, kc.clone(), lens, budget, n_recent, n_sink, dst=dst)
+        attn.sync_check()
+        kept, got = kept.cpu().numpy(), (wg if in_place else w2).cpu()
+        for b in range(B):
+            n = min(int(L[b]), budget)
+            assert new[b].item() == n
+            for h in range(Hkv):
+                idx = kept_ref(w[b, h].numpy(), int(L[b]), budget, n_recent, n_sink)
+                assert np.array_equal(kept[b, h, :n], idx) and (kept[b, h, n:] == -1).all(), (b, h)
+                assert torch.equal(got[b, h, :n].view(torch.int32), w[b, h, idx].view(torch.int32)), (b, h)
+                assert (got[b, h, n:int(L[b])] == 0).all()
+
+
+@pytest.mark.parametrize("L", [60000, 64000, 130000])
+def test_evict_rows_of_several_blocks(L):
+    """60,000 and 64,000 keys: four and eight slices of a block each.  130,000: blocks that each
+    pass reads again."""
+    d = 64
     g = torch.Generator().manual_seed(5)
     kc = torch.randn(1, L, 1, d, generator=g).bfloat16()
     w = torch.rand(1, 1, L, generator=g).mul(50).round()  # many ties
