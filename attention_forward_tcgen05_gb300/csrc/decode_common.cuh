@@ -145,7 +145,7 @@ constexpr int kMergeBatch = 8;
 // head) row, by one warp: lane = DPL consecutive dims.  The partials are read
 // through L2 (ld.global.cg): in the fused decode other CTAs of the same launch
 // wrote them, and this SM's L1 may not see those writes.
-template <int D>
+template <int D, int BATCH = kMergeBatch>
 __device__ __noinline__ void merge_row(const float* __restrict__ part_o,
                                           const float* __restrict__ part_lse, void* o,
                                           float* __restrict__ lse, size_t row, size_t lse_row,
@@ -169,18 +169,18 @@ __device__ __noinline__ void merge_row(const float* __restrict__ part_o,
       wsum += w;
       uint32_t live = __ballot_sync(0xFFFFFFFFu, w > 0.f);  // empty splits are never read
       while (live) {
-        // up to kMergeBatch non-empty splits per round: their loads are issued together
-        int idx[kMergeBatch];
-        float wk[kMergeBatch];
+        // up to BATCH non-empty splits per round: their loads are issued together
+        int idx[BATCH];
+        float wk[BATCH];
 #pragma unroll
-        for (int u = 0; u < kMergeBatch; ++u) {
+        for (int u = 0; u < BATCH; ++u) {
           idx[u] = live ? __ffs(live) - 1 : -1;
           if (live) live &= live - 1;
           wk[u] = __shfl_sync(0xFFFFFFFFu, w, idx[u] < 0 ? 0 : idx[u]);
         }
-        float x[kMergeBatch][DPL];
+        float x[BATCH][DPL];
 #pragma unroll
-        for (int u = 0; u < kMergeBatch; ++u) {
+        for (int u = 0; u < BATCH; ++u) {
           if (idx[u] >= 0) {
             const float* src = po + (size_t)(s0 + idx[u]) * D;
 #pragma unroll
@@ -192,7 +192,7 @@ __device__ __noinline__ void merge_row(const float* __restrict__ part_o,
           }
         }
 #pragma unroll
-        for (int u = 0; u < kMergeBatch; ++u) {
+        for (int u = 0; u < BATCH; ++u) {
           if (idx[u] >= 0) {
 #pragma unroll
             for (int e = 0; e < DPL; ++e) acc[e] = fmaf(wk[u], x[u][e], acc[e]);
@@ -228,7 +228,7 @@ __device__ __noinline__ void merge_row(const float* __restrict__ part_o,
 // into o and lse and puts the counter back to zero, so the counters are zero
 // again when the launch ends.  Called by the first NWARPS warps of the CTA
 // together; `sync` is their barrier.
-template <int D, int NWARPS, class Sync>
+template <int D, int NWARPS, int BATCH = kMergeBatch, class Sync>
 __device__ __forceinline__ void combine_if_last(unsigned* done, int n_splits,
                                                 const float* part_o, const float* part_lse,
                                                 void* o, float* lse, size_t row0, int G,
@@ -249,7 +249,7 @@ __device__ __forceinline__ void combine_if_last(unsigned* done, int n_splits,
   if (!last_sh) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int g = warp; g < G; g += NWARPS)
-    merge_row<D>(part_o, part_lse, o, lse, row0 + g, row0 + g, n_splits, o_bf16, lane);
+    merge_row<D, BATCH>(part_o, part_lse, o, lse, row0 + g, row0 + g, n_splits, o_bf16, lane);
 }
 
 }  // namespace

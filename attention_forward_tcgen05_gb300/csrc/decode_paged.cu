@@ -1,7 +1,7 @@
 // decode_paged.cu -- one-token GQA decode over a paged cache: split-KV partials and their
 // LSE-weighted merge in one launch, the split rule and combine of decode.cu.
 //
-// One CTA per (sequence, KV head, split), groups of up to 16 query heads; its four warps take
+// One CTA per (sequence, KV head, split), groups of up to 16 query heads; its warps take
 // 32-key runs of the split in turn and share nothing until the end.  Each warp gathers 16
 // keys of K and V at a time into a ring of its own (cp.async groups: no barrier, no
 // producer warp), and does on its own fragments
@@ -29,34 +29,37 @@
 namespace attn {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr float kMoveThreshold = 8.f;  // log2: the reference m moves when a score exceeds it by 2^8
 
 // CTAs of one SM (also the split rule's)
 constexpr int decode_paged_ctas(int d, int nb) { return d == 256 ? 1 : (nb == 1 ? 3 : 2); }
 
-template <int D, int NB>
+template <int D, int NB, int W>
 struct DecodePagedCfg {
   static constexpr int kHeads = 8 * NB;
   static constexpr int kPanel = 16 * 128;          // one 64-column panel of 16 keys
   static constexpr int kTile = 16 * D * 2;         // K or V of 16 keys
   static constexpr int kStage = 2 * kTile;
-  // a warp's ring (16, 16 or 24, 48 KB) and the CTAs of an SM: with heads for one mma side,
-  // three small CTAs hide one another's start and end (1024 units of about 550 keys: 51 us
-  // against 53 with two of three stages; 64 ragged sequences of up to 8192: 192 against 210)
-  static constexpr int kStages = D == 64 ? 4 : (D == 128 && NB == 1 ? 2 : 3);
-  static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kComb = kWarps * kHeads * (D + 2) * 4;
+  // Narrow CTAs (W = 4) share an SM; a warp's ring is 16, 16 or 24, 48 KB.  With heads for one
+  // mma side, three small CTAs hide one another's start and end (1024 units of about 550 keys:
+  // 51 us against 53 with two of three stages; 64 ragged sequences of up to 8192: 192 against
+  // 210).  A wide CTA has an SM to itself: a step of 16 keys takes a warp 0.7 us, mostly waiting
+  // on its own instructions, so few CTAs need many warps (4 units of 16000 keys in 32 splits:
+  // 13.8 us with 8 warps, 14.2 with 12, 18.7 with 4, whatever their rings' depth).
+  static constexpr int kStages = W > 4 ? 196608 / (W * kStage) : (D == 64 ? 4 : (D == 128 && NB == 1 ? 2 : 3));
+  static constexpr int kAhead = W > 4 ? kStages / 2 + 1 : 1;  // runs whose pool rows are known ahead
+  static constexpr int kRing = W * kStages * kStage;
+  static constexpr int kComb = W * kHeads * (D + 2) * 4;
   static constexpr int kSmem = (kRing > kComb ? kRing : kComb) + 1024;
-  static constexpr int kMinBlocks = decode_paged_ctas(D, NB);
+  static constexpr int kMinBlocks = W > 4 ? 1 : decode_paged_ctas(D, NB);
 };
 
 // F32: the output is fp32 (see above); else bf16.
-template <int D, int NB, bool F32>
-__global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks)
+template <int D, int NB, bool F32, int W>
+__global__ void __launch_bounds__(W * 32, DecodePagedCfg<D, NB, W>::kMinBlocks)
     decode_paged_kernel(const DecodeArgs a) {
-  using C = DecodePagedCfg<D, NB>;
-  constexpr int ST = C::kStages;
+  using C = DecodePagedCfg<D, NB, W>;
+  constexpr int ST = C::kStages, AH = C::kAhead;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.Hq / a.Hkv;
   const int pos = (int)(blockIdx.x / a.Hkv), hk = (int)(blockIdx.x % a.Hkv);
@@ -86,24 +89,28 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
     }
   };
   if (lo >= hi) {  // empty split: o = 0, lse = -inf
-    for (int i = threadIdx.x; i < G * D; i += kWarps * 32) put(i / D, i % D, 0.f, -INFINITY);
+    for (int i = threadIdx.x; i < G * D; i += W * 32) put(i / D, i % D, 0.f, -INFINITY);
   } else {
     uint8_t* ring = smem + warp * ST * C::kStage;
-    // this warp's 16-key steps: step i covers keys from lo + ((i / 2) * kWarps + warp) * 32 + (i % 2) * 16
+    // this warp's 16-key steps: step i covers keys from lo + ((i / 2) * W + warp) * 32 + (i % 2) * 16
     const int runs = (hi - lo + 31) / 32;
-    const int n = 2 * (runs > warp ? (runs - warp + kWarps - 1) / kWarps : 0);
-    auto key0 = [&](int i) { return lo + ((i >> 1) * kWarps + warp) * 32 + (i & 1) * 16; };
-    int ri[1] = {-1}, rn[1];  // pool rows of the run being issued, and of the next one
-    paged_rows<1>(a.kv, b, key0(0), hi, lane, a.err, rn);
+    const int n = 2 * (runs > warp ? (runs - warp + W - 1) / W : 0);
+    auto key0 = [&](int i) { return lo + ((i >> 1) * W + warp) * 32 + (i & 1) * 16; };
+    int ri = -1, rn[AH][1];  // pool rows of the run being issued, and of the next ones
+#pragma unroll
+    for (int r = 0; r < AH; ++r)
+      if (2 * r < n || r == 0) paged_rows<1>(a.kv, b, key0(2 * r), hi, lane, a.err, rn[r]);
     auto issue = [&](int i) {
       if (i < n) {
         if ((i & 1) == 0) {
-          ri[0] = rn[0];
-          if (i + 2 < n) paged_rows<1>(a.kv, b, key0(i + 2), hi, lane, a.err, rn);
+          ri = rn[0][0];
+#pragma unroll
+          for (int r = 0; r + 1 < AH; ++r) rn[r][0] = rn[r + 1][0];
+          if (i + 2 * AH < n) paged_rows<1>(a.kv, b, key0(i + 2 * AH), hi, lane, a.err, rn[AH - 1]);
         }
         const uint32_t dst = smem_u32(ring + (i % ST) * C::kStage);
-        paged_gather_rows<D, 16>(dst, C::kPanel, a.kv.k, a.Hkv, hk, lane, ri[0], (i & 1) * 16);
-        paged_gather_rows<D, 16>(dst + C::kTile, C::kPanel, a.kv.v, a.Hkv, hk, lane, ri[0], (i & 1) * 16);
+        paged_gather_rows<D, 16>(dst, C::kPanel, a.kv.k, a.Hkv, hk, lane, ri, (i & 1) * 16);
+        paged_gather_rows<D, 16>(dst + C::kTile, C::kPanel, a.kv.v, a.Hkv, hk, lane, ri, (i & 1) * 16);
       }
       cp_async_commit();
     };
@@ -240,14 +247,14 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
       }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
+    for (int i = threadIdx.x; i < G * D; i += W * 32) {
       const int g = i / D, t = i % D;
       float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[(w * C::kHeads + g) * (D + 2) + D]);
+      for (int w = 0; w < W; ++w) M = fmaxf(M, comb[(w * C::kHeads + g) * (D + 2) + D]);
       float ls = 0.f, acc = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float* cw = comb + (w * C::kHeads + g) * (D + 2);
         const float f = ex2_approx(cw[D] - M);  // warps without keys: m = -inf -> 0
         ls = fmaf(cw[D + 1], f, ls);
@@ -257,26 +264,34 @@ __global__ void __launch_bounds__(kWarps * 32, DecodePagedCfg<D, NB>::kMinBlocks
     }
   }
   if (a.n_splits == 1) return;
-  combine_if_last<D, kWarps>(a.done + orow0, a.n_splits, a.part_o, a.part_lse, a.o, a.lse, orow0, G, a.o_bf16,
+  // (partials loaded at once: 8, 16 or 24 took 22.4, 21.3, 21.0 us for 48 splits of 4 units)
+  constexpr int kBatch = D == 256 ? 16 : 24;
+  combine_if_last<D, W, kBatch>(a.done + orow0, a.n_splits, a.part_o, a.part_lse, a.o, a.lse, orow0, G, a.o_bf16,
                              [] { __syncthreads(); });
 }
 
-template <int D, int NB>
+template <int D, int NB, int W>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
-  using C = DecodePagedCfg<D, NB>;
-  auto kern = a.o_bf16 ? decode_paged_kernel<D, NB, false> : decode_paged_kernel<D, NB, true>;
+  using C = DecodePagedCfg<D, NB, W>;
+  auto kern = a.o_bf16 ? decode_paged_kernel<D, NB, false, W> : decode_paged_kernel<D, NB, true, W>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const long long ctas = (long long)a.B * a.n_splits * a.Hkv;
   if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  kern<<<(unsigned)ctas, kWarps * 32, C::kSmem, stream>>>(a);
+  kern<<<(unsigned)ctas, W * 32, C::kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
 // A CTA takes a whole group: larger ones than 16 run on the prefill's tiles (paged_api.cu).
+template <int D, int NB>
+cudaError_t launch_nb(const DecodeArgs& a, cudaStream_t stream) {
+  constexpr int kWide = D == 256 ? (NB == 1 ? 6 : 4) : 8;  // (d = 256: what shared memory and registers hold)
+  if ((long long)a.B * a.n_splits * a.Hkv <= 152) return launch_t<D, NB, kWide>(a, stream);
+  return launch_t<D, NB, 4>(a, stream);
+}
 template <int D>
 cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
-  return a.Hq / a.Hkv <= 8 ? launch_t<D, 1>(a, stream) : launch_t<D, 2>(a, stream);
+  return a.Hq / a.Hkv <= 8 ? launch_nb<D, 1>(a, stream) : launch_nb<D, 2>(a, stream);
 }
 
 }  // namespace

@@ -226,15 +226,25 @@ int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int o_dt
     return ATTN_ERR_INVALID_ARG;
   if (decode_on_tiles(B, Hq, Hkv, o_dtype))
     return prefill_splits(B, Hq, B, 1, max_kv, d, std::min(Hq / Hkv, attn::kPrefillTileM), min_rows);
-  // as many CTAs as run at once: one wave, its splits at least 192 rows; beyond 48 splits the
-  // merge takes longer than the keys it saves.  A batch's lengths differ, so a few splits are
-  // rounded up (64 units of up to 8000 keys: 57 us with 3 splits, 78 with 2); from half a wave
-  // of units on, whole sequences do best (1024 units of up to 1000 keys: 51 against 59 us).
-  const int G = Hq / Hkv;
   const double units = std::max(1.0, (double)B * Hkv);
-  const double q = attn::decode_paged_slots(d, G, kSms) / units;
-  long long n = q < 2 ? 1 : (long long)(q <= 8 && B > 1 ? std::ceil(q) : q);
-  n = std::max(1LL, std::min(std::min(n, 48LL), (max_kv + 191LL) / 192));
+  const long long alone = (long long)(kSms / units);  // splits of a unit while each has an SM
+  long long n;
+  if (alone >= (d == 256 ? 1 : 4)) {
+    // one CTA of many warps an SM; above 32 splits only of 1024 keys and more, as the merge
+    // grows with them (4 units of 16000 keys: 13.8 us with 32, 14.9 with 38; of 117000: 48 with
+    // 38, 52 with 19; one unit of 100000: 24 with 64, 31 with 32)
+    n = std::min(std::min(alone, 64LL), std::max(32LL, max_kv / 1024LL));
+  } else if (alone == 1 && max_kv <= 2048) {
+    n = 1;  // short sequences whole, with an SM each (128 units: 15.8 us, 21 with narrow CTAs)
+  } else {
+    // as many narrow CTAs as run at once.  A batch's lengths differ, so a few splits are
+    // rounded up (64 units of up to 8000 keys: 26.6 us with 8 splits, 29.3 with 2 wide ones);
+    // from half a wave of units on, whole sequences do best (1024 units of up to 1000 keys: 51
+    // against 59 us)
+    const double q = attn::decode_paged_slots(d, Hq / Hkv, kSms) / units;
+    n = q < 2 ? 1 : (long long)(q <= 8 && B > 1 ? std::ceil(q) : q);
+  }
+  n = std::max(1LL, std::min(n, (max_kv + 191LL) / 192));
   *min_rows = n > 1 ? 192 : 1;
   return (int)n;
 }

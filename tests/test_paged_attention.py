@@ -43,15 +43,17 @@ def test_decode(d, Hq, Hkv, page):
         _check_decode(o, lse, q, kc, vc, lens, scale, out_dtype == torch.bfloat16)
 
 
-@pytest.mark.parametrize("Hq,Hkv,d", [(32, 2, 64), (12, 1, 128), (24, 2, 256), (16, 1, 128)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(32, 2, 64), (12, 1, 128), (24, 2, 256), (16, 1, 128), (4, 2, 64), (7, 1, 128),
+                                      (8, 1, 256)])
 def test_decode_of_many_sequences(Hq, Hkv, d):
-    """Groups of 9 to 16 heads in more sequences than one wave of tiles holds (160 units)."""
+    """160 units: more CTAs than SMs, and than one wave of tiles holds for groups of 9 to 16."""
     rng = np.random.default_rng(9)
     lens = [int(x) for x in rng.integers(0, 200, 160 // Hkv)]
     q, kc, vc, lens, kp, vp, table = _decode_case(lens, Hq, Hkv, d, 16, 330 + d)
     for n_splits in (0, 1, 3):
-        o, lse = attn.decode_paged(q.cuda(), kp, vp, table, lens.cuda(), n_splits)
-        _check_decode(o, lse, q, kc, vc, lens, 1.0 / np.sqrt(d), True)
+        for dt in (torch.bfloat16, torch.float32):
+            o, lse = attn.decode_paged(q.cuda(), kp, vp, table, lens.cuda(), n_splits, out_dtype=dt)
+            _check_decode(o, lse, q, kc, vc, lens, 1.0 / np.sqrt(d), dt is torch.bfloat16)
 
 
 @pytest.mark.parametrize("n_splits,min_rows", [(1, 0), (3, 100), (8, 1)])
