@@ -10,6 +10,7 @@
 //   * more: S^T = K Q^T on the tensor cores, so a key is a TMEM lane and a thread sums its
 //     own row; one ex2 per pair (32 a cycle per SM) and the MMA (512 cycles per 128 x 128
 //     tile at d = 128) take equally long.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -36,7 +37,10 @@ template <int D>
 struct RowCfg {
   static constexpr int kPanel = 16 * 128;
   static constexpr int kStage = 16 * D * 2;                          // K of 16 keys
-  static constexpr int kStages = D == 64 ? 8 : (D == 128 ? 6 : 3);  // a warp's ring: 16, 24, 24 KB
+  // a warp's ring: 6, 8, 16 KB.  A step is mostly a warp waiting on its own instructions, so
+  // four CTAs an SM (three at d = 256) beat two of deeper rings: 64 sequences of up to 8192
+  // keys 98 us against 110, 4 units of 117000 keys 26 against 33; a fifth and sixth add nothing
+  static constexpr int kStages = D == 64 ? 3 : 2;
   static constexpr int kSmem = kRowWarps * kStages * kStage + 1024;
 };
 
@@ -44,7 +48,7 @@ struct RowCfg {
 // gathers 16 keys at a time into its own ring and multiplies them with the resident query
 // rows (up to 8 NB); a key's terms then lie in four lanes.
 template <int D, int NB>
-__global__ void __launch_bounds__(kRowWarps * 32, 2) key_weights_rows_kernel(const KeyWeightArgs a, int chunk) {
+__global__ void __launch_bounds__(kRowWarps * 32, 4) key_weights_rows_kernel(const KeyWeightArgs a, int chunk) {
   using C = RowCfg<D>;
   constexpr int ST = C::kStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -493,9 +497,10 @@ cudaError_t launch_rows(const KeyWeightArgs& a, int rows, cudaStream_t stream) {
   using C = RowCfg<D>;
   const long long units = (long long)a.B * a.Hkv;
   const int cap = a.kv.max_pages * a.kv.page_size;
-  // ranges of keys: about eight CTAs an SM in all, 128 to 2048 keys each
-  int chunk = 2048;
-  while (chunk > 128 && units * ((cap + chunk - 1) / chunk) < 8 * 152) chunk /= 2;
+  // ranges of 128 to 2048 keys: one wave of four CTAs an SM if that is enough (4 units of 32000
+  // keys: 7 us, 9 with ranges of half the length, 12 of a quarter)
+  const long long share = (units * cap + 4 * 152 - 1) / (4 * 152);
+  const int chunk = (int)std::min(2048LL, std::max(1LL, (share + 127) / 128) * 128);
   auto kern = rows <= 8 ? key_weights_rows_kernel<D, 1> : key_weights_rows_kernel<D, 2>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
