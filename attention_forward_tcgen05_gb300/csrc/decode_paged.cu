@@ -32,7 +32,7 @@ namespace {
 constexpr float kMoveThreshold = 8.f;  // log2: the reference m moves when a score exceeds it by 2^8
 
 // CTAs of one SM (also the split rule's)
-constexpr int decode_paged_ctas(int d, int nb) { return d == 256 ? 1 : (nb == 1 ? 3 : 2); }
+constexpr int decode_paged_ctas(int d, int nb) { return d == 256 ? 1 : (nb == 2 ? 2 : (d == 128 ? 3 : 4)); }
 
 template <int D, int NB, int W>
 struct DecodePagedCfg {
@@ -40,13 +40,16 @@ struct DecodePagedCfg {
   static constexpr int kPanel = 16 * 128;          // one 64-column panel of 16 keys
   static constexpr int kTile = 16 * D * 2;         // K or V of 16 keys
   static constexpr int kStage = 2 * kTile;
-  // Narrow CTAs (W = 4) share an SM; a warp's ring is 16, 16 or 24, 48 KB.  With heads for one
-  // mma side, three small CTAs hide one another's start and end (1024 units of about 550 keys:
-  // 51 us against 53 with two of three stages; 64 ragged sequences of up to 8192: 192 against
-  // 210).  A wide CTA has an SM to itself: a step of 16 keys takes a warp 0.7 us, mostly waiting
-  // on its own instructions, so few CTAs need many warps (4 units of 16000 keys in 32 splits:
-  // 13.8 us with 8 warps, 14.2 with 12, 18.7 with 4, whatever their rings' depth).
-  static constexpr int kStages = W > 4 ? 196608 / (W * kStage) : (D == 64 ? 4 : (D == 128 && NB == 1 ? 2 : 3));
+  // A step of 16 keys takes a warp 0.7 us, mostly waiting on its own instructions, so an SM
+  // needs many warps more than deep rings.  Narrow CTAs (W = 4) share it and hide one another's
+  // start and end: three at d = 128 (1024 units of about 550 keys: 51 us against 53 with two of
+  // three stages; 64 ragged sequences of up to 8192: 192 against 210), four at d = 64 (64 x 8
+  // units of up to 8000 keys: 106 us, 116 with three of four stages, 110 with five of two).  A
+  // wide CTA has an SM to itself, for calls of few CTAs (4 units of 16000 keys in 32 splits: 13.8
+  // us with 8 warps, 14.2 with 12, 18.7 with 4, whatever their rings' depth), and at d = 256,
+  // where 6 warps of two stages fill it (64 x 4 units of up to 4000 keys: 123 us, 140 with 4).
+  static constexpr int kStages =
+      W > 4 ? 196608 / (W * kStage) : (D == 64 && NB == 2 ? 4 : (D == 128 && NB == 1 ? 2 : 3));
   static constexpr int kAhead = W > 4 ? kStages / 2 + 1 : 1;  // runs whose pool rows are known ahead
   static constexpr int kRing = W * kStages * kStage;
   static constexpr int kComb = W * kHeads * (D + 2) * 4;
@@ -285,9 +288,9 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
 // A CTA takes a whole group: larger ones than 16 run on the prefill's tiles (paged_api.cu).
 template <int D, int NB>
 cudaError_t launch_nb(const DecodeArgs& a, cudaStream_t stream) {
-  constexpr int kWide = D == 256 ? (NB == 1 ? 6 : 4) : 8;  // (d = 256: what shared memory and registers hold)
-  if ((long long)a.B * a.n_splits * a.Hkv <= 152) return launch_t<D, NB, kWide>(a, stream);
-  return launch_t<D, NB, 4>(a, stream);
+  if constexpr (D == 256) return launch_t<D, NB, NB == 1 ? 6 : 4>(a, stream);  // (two mma sides: registers for 4)
+  else if ((long long)a.B * a.n_splits * a.Hkv <= 152) return launch_t<D, NB, 8>(a, stream);
+  else return launch_t<D, NB, 4>(a, stream);
 }
 template <int D>
 cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
