@@ -47,7 +47,8 @@ struct DecodePagedCfg {
   // units of up to 8000 keys: 106 us, 116 with three of four stages, 110 with five of two).  A
   // wide CTA has an SM to itself, for calls of few CTAs (4 units of 16000 keys in 32 splits: 13.8
   // us with 8 warps, 14.2 with 12, 18.7 with 4, whatever their rings' depth; d = 64, 6 units of
-  // up to 131072: 38 us with 12 or 16 warps, 41 with 8), and at d = 256, where 6 warps of two stages fill it (64 x 4 units of up to 4000 keys: 123 us, 140 with 4).
+  // up to 131072: 38 us with 12 or 16 warps, 41 with 8), and at d = 256, where 6 warps of two
+  // stages fill it (64 x 4 units of up to 4000 keys: 123 us, 140 with 4).
   static constexpr int kStages =
       W > 4 ? 196608 / (W * kStage) : (D == 64 && NB == 2 ? 4 : (D == 128 && NB == 1 ? 2 : 3));
   static constexpr int kAhead = W > 4 ? kStages / 2 + 1 : 1;  // runs whose pool rows are known ahead

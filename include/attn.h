@@ -483,8 +483,8 @@ int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const att
                       float* part_lse, void* o, float* lse, int o_dtype, unsigned int* counters,
                       attn_stream_t stream);
 
-/* The n_splits (>= 1) and min_rows_per_split that suit a decode of these sizes, max_kv
- * keys in the longest sequence (host only); ATTN_ERR_INVALID_ARG for bad sizes. */
+/* The n_splits (>= 1) and min_rows_per_split that suit a decode of these sizes and output
+ * type, max_kv keys in the longest sequence (host only); ATTN_ERR_INVALID_ARG for bad ones. */
 int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int o_dtype, int* min_rows_per_split);
 
 /*
