@@ -27,6 +27,9 @@ ATTN_F32 = 0
 ATTN_BF16 = 1
 
 _lock = threading.Lock()
+# held by a helper while it launches kernels that use a kept workspace or kept completion
+# counters, and by sync_check while it zeroes the counters
+_launching = threading.Lock()
 _lib = None
 
 
@@ -381,7 +384,9 @@ def merge(part_o, part_lse, out_dtype=None, stream=None, out=None):
     return o, lse
 
 
-_counters = {}  # (device type, index) -> the shared zeroed completion counters of decode()
+# Zeroed completion counters kept between calls: of decode() by (device type, index), of
+# decode_paged() by (device index, stream handle).
+_counters = {}
 
 
 def decode_counters(n: int, device):
@@ -432,9 +437,10 @@ def decode(q, kcache, vcache, kv_lens, n_splits: int, min_rows_per_split: int = 
         counters = decode_counters(B * Hq, q.device)
     elif counters.dtype != torch.int32 or not counters.is_cuda or counters.numel() < B * Hq:
         raise TypeError("counters must be a CUDA int32 tensor of at least B*Hq entries")
-    rc = attn_decode(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(kv_lens), B, Hq, Hkv, d, max_kv,
-                     scale, n_splits, min_rows_per_split, _ptr(part_o), _ptr(part_lse), _ptr(o),
-                     _ptr(lse), _out_code(o.dtype), _ptr(counters), _stream_handle(stream))
+    with _launching:
+        rc = attn_decode(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(kv_lens), B, Hq, Hkv, d, max_kv,
+                         scale, n_splits, min_rows_per_split, _ptr(part_o), _ptr(part_lse), _ptr(o),
+                         _ptr(lse), _out_code(o.dtype), _ptr(counters), _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode")
     return o, lse
@@ -502,12 +508,20 @@ def decode_packed(q, kcache, vcache, kv_lens, scale: float | None = None, out_dt
 
 def sync_check(stream=None) -> None:
     """Synchronise `stream` and raise if a kernel recorded a device-side error.  After
-    such an error the shared decode counters are zeroed again (their count is void)."""
+    such an error the kept decode counters are zeroed again (a call that was cut short
+    leaves its count behind); that waits for the devices they are on, as the error may be
+    another stream's and calls on all of them may be counting."""
     rc = attn_sync_check(_stream_handle(stream))
     if rc != ATTN_OK:
-        with _lock:
-            bufs = list(_counters.values())
-        for buf in bufs:
-            buf.zero_()
-            _torch().cuda.synchronize(buf.device)
+        synchronize = _torch().cuda.synchronize
+        with _launching:
+            with _lock:
+                bufs = list(_counters.values())
+            devices = list(dict.fromkeys(buf.device for buf in bufs))
+            for device in devices:
+                synchronize(device)
+            for buf in bufs:
+                buf.zero_()
+            for device in devices:
+                synchronize(device)
         raise AttnError(rc, "attn_sync_check")

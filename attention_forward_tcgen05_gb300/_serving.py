@@ -16,9 +16,8 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
-import threading
 
-from ._binding import ATTN_BF16, ATTN_F32, ATTN_OK, AttnError, _counters, _lock, load
+from ._binding import ATTN_BF16, ATTN_F32, ATTN_OK, AttnError, _counters, _launching, _lock, load
 
 
 _module = None
@@ -170,11 +169,10 @@ def _decode_splits(B, Hq, Hkv, max_kv, d, code):
 
 
 # Workspaces of prefill_paged and decode_paged: kept for each stream, whose launches are
-# ordered; a call holds the lock while it makes its launches, so that another thread's on the
+# ordered; a call holds _launching while it makes its launches, so that another thread's on the
 # same stream do not come between two of them.  A call being captured gets its own (two graphs
 # may replay at the same time).
 _partials = {}  # (device, stream handle) -> fp32
-_launching = threading.Lock()
 
 
 def _workspace(floats, dev, handle):

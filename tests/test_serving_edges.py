@@ -1,0 +1,85 @@
+"""Calls of the paged serving functions at the edge of what they document: errors on one
+stream beside work on another, arguments left out, the largest sizes."""
+import pytest
+import torch
+
+import attention_forward_tcgen05_gb300 as attn
+from attention_forward_tcgen05_gb300 import _binding
+
+
+# ------------------------------------------------------------------ sync_check
+class _Buffer:
+    """A stand-in for a counter buffer that notes when it is zeroed."""
+
+    def __init__(self, device, log):
+        self.device, self.log = device, log
+
+    def zero_(self):
+        self.log.append(("zero", self.device, _binding._launching.locked()))
+
+
+def test_counters_are_zeroed_only_between_synchronisations(monkeypatch):
+    """After a device error the shared counters are zeroed with every device that owns one
+    idle: synchronised before (another stream may be counting on its buffer) and after (the
+    next launch may be on any stream), and no split call launches in between."""
+    log = []
+    bufs = {("cuda", 0): _Buffer("cuda:0", log), (0, 77): _Buffer("cuda:0", log), (1, 5): _Buffer("cuda:1", log)}
+    monkeypatch.setattr(_binding, "_counters", bufs)
+    monkeypatch.setattr(_binding, "_stream_handle", lambda stream: None)
+    monkeypatch.setattr(_binding, "attn_sync_check", lambda s: attn.ATTN_ERR_DEVICE_INPUT)
+    monkeypatch.setattr(torch.cuda, "synchronize",
+                        lambda device=None: log.append(("sync", str(device), _binding._launching.locked())))
+    with pytest.raises(attn.AttnError):
+        attn.sync_check()
+    assert all(locked for _, _, locked in log)
+    zeroed = [i for i, x in enumerate(log) if x[0] == "zero"]
+    assert len(zeroed) == 3
+    for device in ("cuda:0", "cuda:1"):
+        synced = [i for i, x in enumerate(log) if x[:2] == ("sync", device)]
+        mine = [i for i in zeroed if log[i][1] == device]
+        assert min(synced) < min(mine) and max(synced) > max(mine)
+    assert not _binding._launching.locked()
+
+
+@pytest.mark.gpu
+def test_an_error_on_one_stream_leaves_the_decodes_of_another():
+    """A bad page is reported on one stream, again and again, while split decodes run on
+    another: those, and the ones after, come out as alone."""
+    B, Hq, Hkv, d, page = 32, 32, 8, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    lens = torch.randint(2000, 4097, (B,), generator=g, device="cuda", dtype=torch.int32)
+    table = torch.randperm(B * 64, generator=g, device="cuda").to(torch.int32).view(B, 64)
+    kp, vp = (torch.randn(B * 64, page, Hkv, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(B, Hq, d, generator=g, device="cuda").bfloat16()
+    bad = torch.full((1, 1), -1, dtype=torch.int32, device="cuda")
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    busy = torch.cuda.Stream()
+    outs = [(torch.empty(B, Hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(B, Hq, device="cuda"))
+            for _ in range(40)]
+    torch.cuda.synchronize()
+
+    def decode(out=None):
+        with torch.cuda.stream(busy):
+            return attn.decode_paged(q, kp, vp, table, lens, 9, out=out)
+
+    o, lse = decode()
+    torch.cuda.synchronize()
+    attn.sync_check()
+    want = o.clone(), lse.clone()
+    for i, out in enumerate(outs):
+        out[0].fill_(float("nan"))
+    torch.cuda.synchronize()
+    reported = 0
+    for i, out in enumerate(outs):
+        decode(out)
+        if i % 4 == 3:
+            attn.decode_paged(q[:1], kp, vp, bad, one, 1)
+            with pytest.raises(attn.AttnError) as e:
+                attn.sync_check()
+            assert e.value.status == attn.ATTN_ERR_DEVICE_INPUT
+            reported += 1
+    torch.cuda.synchronize()
+    attn.sync_check()
+    assert reported == 10
+    for i, (o, lse) in enumerate(outs):
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), i
