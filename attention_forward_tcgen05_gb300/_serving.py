@@ -437,17 +437,22 @@ def _weight_rows(weights, dev, B, Hkv, capacity):
     return p, n
 
 
-def key_weights(q, lse, kcache, kv_lens, weights, page_table=None, cu_seqlens_q=None, max_sq: int = 1,
+def key_weights(q, lse, kcache, kv_lens, weights, page_table=None, cu_seqlens_q=None, max_sq: int | None = None,
                 causal: bool = True, window: int = 0, n_sink: int = 0, scale: float | None = None,
                 accumulate: bool = True, stream=None):
     """Add the attention weight that each cached key received from the new rows to
     ``weights`` fp32 [B,Hkv,>= capacity] (attn_key_weights), or set it (accumulate=False).
 
     q and lse are an attention call's: q [total_q,Hq,d], lse [Hq,total_q] with cu_seqlens_q
-    int32 [B+1] and max_sq; or, without cu_seqlens_q, a decode's q [B,Hq,d], lse [B,Hq].
-    causal, window, n_sink and scale as in that call.  Entries at or past kv_lens[b] stay
-    as they are.  Returns weights."""
+    int32 [B+1] and max_sq, the longest sequence's rows (a longer one is reported by
+    sync_check); or, without cu_seqlens_q, a decode's q [B,Hq,d], lse [B,Hq].  causal,
+    window, n_sink and scale as in that call.  Entries at or past kv_lens[b] stay as they
+    are.  Returns weights."""
     torch = _torch()
+    if cu_seqlens_q is None:
+        max_sq = 1
+    elif max_sq is None:
+        raise ValueError("cu_seqlens_q needs max_sq, the longest sequence's rows")
     dev = _device(q, "q")
     if stream is not None or dev != torch._C._cuda_getDevice():
         return _elsewhere(lambda: key_weights(q, lse, kcache, kv_lens, weights, page_table, cu_seqlens_q, max_sq,
@@ -468,7 +473,6 @@ def key_weights(q, lse, kcache, kv_lens, weights, page_table=None, cu_seqlens_q=
         if total != B:
             raise ValueError("without cu_seqlens_q there must be one row per sequence")
         lp = _sized(lse, "lse", torch.float32, dev, B, Hq)
-        max_sq = 1
     wp, w_stride = _weight_rows(weights, dev, B, Hkv, max_pages * page)
     if scale is None:
         scale = 1.0 / math.sqrt(d)

@@ -29,6 +29,14 @@ __device__ __forceinline__ void put_weight(const KeyWeightArgs& a, int b, int hk
   *dst = a.accumulate ? *dst + w : w;
 }
 
+// Rows of sequence b, which the launch was sized for, are at most max_sq: more are reported,
+// as the positions of the first max_sq would be taken for the last ones.
+__device__ __forceinline__ void check_rows(const KeyWeightArgs& a, int b) {
+  if (a.cu_q == nullptr || threadIdx.x != 0) return;
+  const int c0 = min(max(a.cu_q[b], 0), a.total_q), c1 = min(a.cu_q[b + 1], a.total_q);
+  if (c1 - c0 > a.max_sq) atomicCAS(a.err, kErrNone, kErrBadShape);
+}
+
 // ------------------------------------------------------------------ few rows
 constexpr int kRowsMax = 16;
 constexpr int kRowWarps = 4;
@@ -58,6 +66,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4) key_weights_rows_kernel(con
   const SeqExtent e = seq_extent(b, a.cu_q ? a.max_sq : 1, cap, a.cu_q, a.kv_lens, a.total_q);
   const int base = a.cu_q ? e.qbase : b;
   const int lo = (int)(blockIdx.x / n_bh) * chunk, hi = min(e.Skv, lo + chunk);
+  if (lo == 0 && hk == 0) check_rows(a, b);
   if (lo >= hi) return;
   const int G = a.Hq / a.Hkv, R = e.Sq * G;
   extern __shared__ uint8_t smem_raw[];
@@ -209,6 +218,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
   const SeqExtent e = seq_extent(b, a.cu_q ? a.max_sq : 1, cap, a.cu_q, a.kv_lens, a.total_q);
   const int base = a.cu_q ? e.qbase : b;
   const int k0 = kb * C::kKeys;
+  if (kb == 0 && hk == 0 && rank == 0) check_rows(a, b);
   if (k0 >= e.Skv) return;  // the whole cluster: nothing of it waits on a peer
   const int Gall = a.Hq / a.Hkv, G = pack, n_hu = Gall / G;  // head groups of the KV head
   const int PT = QN / G;                  // positions of a query tile

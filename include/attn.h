@@ -501,6 +501,8 @@ int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int o_dt
  *   q, lse       an attention call's queries and log-sum-exps: with cu_seqlens_q, q bf16
  *                [total_q][Hq][d], lse fp32 [Hq][total_q]; with cu_seqlens_q == NULL (one row
  *                per sequence: total_q = B, max_sq = 1), lse [B][Hq]
+ *   max_sq       >= every sequence's rows; a longer sequence is reported as
+ *                ATTN_ERR_DEVICE_INPUT by attn_sync_check
  *   weights      fp32 [B][Hkv][w_stride], w_stride >= max_pages * page_size
  *   page_table   may be NULL (dense cache);  d in {64, 128, 256}
  *   causal, window, n_sink, scale   as in the attention call (window = 0: none); scale in

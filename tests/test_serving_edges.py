@@ -5,6 +5,7 @@ import torch
 
 import attention_forward_tcgen05_gb300 as attn
 from attention_forward_tcgen05_gb300 import _binding
+from attention_forward_tcgen05_gb300 import workloads as W
 
 
 # ------------------------------------------------------------------ sync_check
@@ -83,3 +84,38 @@ def test_an_error_on_one_stream_leaves_the_decodes_of_another():
     assert reported == 10
     for i, (o, lse) in enumerate(outs):
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), i
+
+
+# ------------------------------------------------------------------ key weights
+def test_key_weights_of_packed_rows_need_max_sq():
+    """Left out, the launch would be sized for one row a sequence: refused, whatever else is
+    wrong with the call."""
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    c = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16)
+    w, lens, cu = torch.zeros(2, 2, 16), torch.ones(2, dtype=torch.int32), torch.tensor([0, 2, 4], dtype=torch.int32)
+    with pytest.raises(ValueError, match="max_sq"):
+        attn.key_weights(x, w[:, 0, :4], c, lens, w, cu_seqlens_q=cu)
+    with pytest.raises(TypeError):  # (given, the host tensors are what is wrong)
+        attn.key_weights(x, w[:, 0, :4], c, lens, w, cu_seqlens_q=cu, max_sq=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [[3, 2], [40, 2], [2, 40]])
+@pytest.mark.parametrize("G", [1, 4])
+def test_key_weights_report_a_sequence_above_max_sq(rows, G):
+    Hkv, d = 2, 64
+    kv = torch.tensor([100, 100], dtype=torch.int32)
+    q, kc, _, cu = W.varlen_inputs(2, G * Hkv, Hkv, d, torch.tensor(rows, dtype=torch.int32), kv, 31)
+    lse = torch.zeros(G * Hkv, sum(rows), device="cuda")
+    w = torch.zeros(2, Hkv, 100, device="cuda")
+
+    def call(max_sq):
+        attn.key_weights(q.cuda(), lse, kc.cuda(), kv.cuda(), w, cu_seqlens_q=cu.cuda(), max_sq=max_sq)
+        attn.sync_check()
+
+    call(max(rows))
+    call(1000)
+    with pytest.raises(attn.AttnError) as e:
+        call(max(rows) - 1)
+    assert e.value.status == attn.ATTN_ERR_DEVICE_INPUT
+    call(max(rows))
