@@ -78,8 +78,9 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
         if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
       }
       b = lo;
-      i = t - a.cu_q[b];
-      n = a.cu_q[b + 1] - a.cu_q[b];
+      const int c0 = max(a.cu_q[b], 0);  // (clamped to [0, total], as the attention calls do)
+      i = t - c0;
+      n = min(a.cu_q[b + 1], a.total) - c0;
     }
     int row = -2;  // behind the last sequence: the token's rows are left as they are
     if (live) {

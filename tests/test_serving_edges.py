@@ -119,3 +119,33 @@ def test_key_weights_report_a_sequence_above_max_sq(rows, G):
         call(max(rows) - 1)
     assert e.value.status == attn.ATTN_ERR_DEVICE_INPUT
     call(max(rows))
+
+
+# ------------------------------------------------------------------ rotary append
+@pytest.mark.gpu
+@pytest.mark.parametrize("long", [False, True], ids=["one_a_cta", "eight_a_cta"])
+def test_append_clamps_cu_seqlens_as_attention_does(long):
+    """cu_seqlens_q whose first entry lies below 0 and whose last one above total: the append
+    counts a sequence's tokens within [0, total], as the attention calls do, so both put the
+    same token at the same key."""
+    n = [1500, 7, 1200] if long else [5, 7, 4]
+    lens = [n[0] + 3, 20, n[2] + 9]
+    T, Hkv, d, page = sum(n), 2, 64, 32
+    cu = torch.tensor([-6, n[0], n[0] + n[1], T + 8], dtype=torch.int32)
+    width = -(-max(lens) // page)
+    table = torch.randperm(3 * width, generator=torch.Generator().manual_seed(2)).to(torch.int32).view(3, width)
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(T, Hkv, d, generator=g).bfloat16() for _ in range(2))
+    kp = torch.zeros(3 * width, page, Hkv, d, dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    kv = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    attn.rope_append(None, k.cuda(), v.cuda(), kp, vp, kv, None, page_table=table.cuda(), cu_seqlens_q=cu.cuda())
+    attn.sync_check()
+    want_k, want_v = torch.zeros_like(kp.cpu()), torch.zeros_like(kp.cpu())
+    t = 0
+    for b in range(3):
+        for i in range(n[b]):
+            j = lens[b] - n[b] + i
+            want_k[table[b, j // page], j % page], want_v[table[b, j // page], j % page] = k[t], v[t]
+            t += 1
+    assert torch.equal(kp.cpu(), want_k) and torch.equal(vp.cpu(), want_v)
