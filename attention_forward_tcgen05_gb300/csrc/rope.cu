@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
       int lo = 0, hi = a.B;  // cu[lo] <= t < cu[hi] (or t behind the last sequence)
       live = t >= a.cu_q[0] && t < a.cu_q[a.B];
       while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
+        const int mid = lo + (hi - lo) / 2;  // (lo + hi may pass an int)
         if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
       }
       b = lo;

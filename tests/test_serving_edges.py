@@ -149,3 +149,21 @@ def test_append_clamps_cu_seqlens_as_attention_does(long):
             want_k[table[b, j // page], j % page], want_v[table[b, j // page], j % page] = k[t], v[t]
             t += 1
     assert torch.equal(kp.cpu(), want_k) and torch.equal(vp.cpu(), want_v)
+
+
+@pytest.mark.gpu
+def test_append_to_more_sequences_than_half_an_int():
+    """1.6e9 sequences, the tokens in the last one: the search for a token's sequence adds two
+    of their numbers.  (19 GB of lengths, offsets and table.)"""
+    B, Hkv, d = (1 << 30) + (1 << 29), 1, 64
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens, cu, table = torch.zeros(B, **i32), torch.zeros(B + 1, **i32), torch.zeros(B, 1, **i32)
+    lens[-1], cu[-1], table[-1] = 8, 8, 1
+    k = torch.randn(8, Hkv, d, device="cuda").bfloat16()
+    kp = torch.zeros(2, 8, Hkv, d, dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    attn.rope_append(None, k, -k, kp, vp, lens, None, page_table=table, cu_seqlens_q=cu)
+    attn.sync_check()
+    assert torch.equal(kp[1], k) and torch.equal(vp[1], -k) and not kp[0].any()
+    del lens, cu, table
+    torch.cuda.empty_cache()
