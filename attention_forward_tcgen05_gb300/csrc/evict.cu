@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(kSelThreads, kSelThreads == 1024 ? 1 : (kClust
     __syncthreads();
   };
   if (hi - lo <= kBlock) copy_in(lo);
-  for (int i = n + rank * kSelThreads + threadIdx.x; i < a.budget; i += cs * kSelThreads) kept[i] = -1;
+  // (unsigned: a step past a budget near 2^31 is no int)
+  for (unsigned i = n + rank * kSelThreads + threadIdx.x; i < (unsigned)a.budget; i += cs * kSelThreads) kept[i] = -1;
 
   uint32_t prefix = 0;  // the threshold's bits so far
   int want = L > n ? n - a.n_sink - a.n_recent : 0;

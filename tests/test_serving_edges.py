@@ -167,3 +167,23 @@ def test_append_to_more_sequences_than_half_an_int():
     assert torch.equal(kp[1], k) and torch.equal(vp[1], -k) and not kp[0].any()
     del lens, cu, table
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ eviction
+@pytest.mark.gpu
+def test_evict_with_the_largest_budget():
+    """A budget of 2^31 - 1 keys, with room for them in `kept`: every key stays, the rest of
+    `kept` is -1 up to its end.  (8.6 GB.)"""
+    L, d, budget = 5, 64, 2 ** 31 - 1
+    kc = torch.randn(1, 16, 1, d, device="cuda").bfloat16()
+    vc, w, lens = -kc, torch.rand(1, 1, 16, device="cuda"), torch.tensor([L], dtype=torch.int32, device="cuda")
+    before = kc.clone()
+    kept = torch.zeros(1, 1, budget, dtype=torch.int32, device="cuda")
+    new = torch.empty_like(lens)
+    attn.evict(w, kc, vc, lens, budget, out=(kept, new))
+    attn.sync_check()
+    assert new.item() == L and kept[0, 0, :L].tolist() == list(range(L))
+    assert all((part == -1).all().item() for part in kept[0, 0, L:].split(1 << 28))
+    assert torch.equal(kc, before)
+    del kept
+    torch.cuda.empty_cache()
