@@ -352,12 +352,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Evict
     for (int p = 0; p < NP; ++p) {
       const int i = lo + p * RPP + r0;
       dst[p] = -1;
+      x[p] = make_uint4(0, 0, 0, 0);  // (a row of a bad page)
       if (i < n && kept[i] != i) {
         const int s = paged_row(a.src, b, kept[i], a.err);
-        if (s >= 0) {
-          dst[p] = paged_row(a.src, b, i, a.err);
+        dst[p] = paged_row(a.src, b, i, a.err);
+        if (s >= 0)
           x[p] = *reinterpret_cast<const uint4*>(pool + ((size_t)s * a.Hkv + hk) * D + slice * 32 + c * 8);
-        }
       }
     }
     __syncthreads();  // every row of this step is read before one is written

@@ -187,3 +187,37 @@ def test_evict_with_the_largest_budget():
     assert torch.equal(kc, before)
     del kept
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [True, False], ids=["in_place", "pages"])
+def test_evict_from_a_bad_page(in_place):
+    """A table entry that is no page, under kept keys: reported; its keys' rows read as zeros
+    in both forms, rows that would go to it are not written, and the others stand."""
+    page, Hkv, d, L, budget = 16, 2, 64, 64, 24
+    g = torch.Generator().manual_seed(4)
+    kp = torch.randn(6, page, Hkv, d, generator=g).bfloat16()
+    vp = torch.randn(6, page, Hkv, d, generator=g).bfloat16()
+    table = torch.tensor([[4, 0, 5, 1]], dtype=torch.int32)
+    w = torch.zeros(1, Hkv, L)
+    heavy = list(range(8, 12)) + list(range(36, 56))  # keys that stay: of pages 0, 2 and 3
+    w[:, :, heavy] = 1.0
+    for entry in (2, 1):  # the page that is read, the page that is written
+        t = table.clone()
+        t[0, entry] = 77
+        kg, vg = kp.cuda(), vp.cuda()
+        kd, vd = (kg, vg) if in_place else (torch.full_like(kg, 3), torch.full_like(vg, 3))
+        t2 = t if in_place else torch.tensor([[2, 77 if entry == 1 else 3]], dtype=torch.int32)
+        kept, _ = attn.evict(w.cuda(), kg, vg, torch.tensor([L], dtype=torch.int32, device="cuda"), budget,
+                             page_table=t.cuda(), dst=None if in_place else (kd, vd, t2.cuda(), None))
+        with pytest.raises(attn.AttnError) as e:
+            attn.sync_check()
+        assert e.value.status == attn.ATTN_ERR_DEVICE_INPUT
+        assert kept[0, 0].tolist() == heavy and kept[0, 1].tolist() == heavy
+        for got, src, fill in ((kd, kp, kp), (vd, vp, vp)):
+            want = fill.clone() if in_place else torch.full_like(fill, 3)
+            for i, j in enumerate(heavy):
+                to, frm = int(t2[0, i // page]), int(t[0, j // page])
+                if to < 6:
+                    want[to, i % page] = src[frm, j % page] if frm < 6 else 0
+            assert torch.equal(got.cpu(), want), entry
