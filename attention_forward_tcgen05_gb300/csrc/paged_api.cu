@@ -320,7 +320,8 @@ int attn_key_weights(const attn_bf16_t* q, const float* lse, const attn_bf16_t* 
   if (!ok16(kcache) || !ok4(kv_lens) || !ok4(weights) || !aligned(cu_seqlens_q, 4)) return ATTN_ERR_INVALID_ARG;
   if (total_q == 0) max_sq = 0;  // no rows: the sums are zero (or stay, if accumulated)
   else if (!ok16(q) || !ok4(lse)) return ATTN_ERR_INVALID_ARG;
-  if ( (long long)total_q * Hq >= (1LL << 31) || (long long)max_sq * (Hq / Hkv) >= (1LL << 30))
+  if ((long long)total_q * Hq >= (1LL << 31) || (long long)max_sq * (Hq / Hkv) >= (1LL << 30) ||
+      (long long)B * Hkv > 0x7FFFFFFFLL)
     return ATTN_ERR_INVALID_ARG;
   attn::KeyWeightArgs a;
   std::memset(&a, 0, sizeof(a));

@@ -5,6 +5,7 @@ import torch
 
 import attention_forward_tcgen05_gb300 as attn
 from attention_forward_tcgen05_gb300 import _binding
+from attention_forward_tcgen05_gb300 import build as attn_build
 from attention_forward_tcgen05_gb300 import workloads as W
 
 
@@ -221,3 +222,19 @@ def test_evict_from_a_bad_page(in_place):
                 if to < 6:
                     want[to, i % page] = src[frm, j % page] if frm < 6 else 0
             assert torch.equal(got.cpu(), want), entry
+
+
+# ------------------------------------------------------------------ sizes the kernels cannot index
+@pytest.fixture(scope="module")
+def lib():
+    attn_build.build()
+    return attn.load()
+
+
+def test_key_weights_refuse_more_units_than_an_int(lib):
+    """A CTA finds its (sequence, KV head) by their product: 2^31 of them are refused."""
+    #  q lse kc table cu lens w stride B Hq Hkv total max_sq d max_pages page pages causal window sink scale acc stream
+    def call(B, Hkv):
+        return attn.attn_key_weights(16, 16, 16, 16, 16, 16, 16, 1, B, Hkv, Hkv, 7, 5, 64, 1, 1, 9, 1, 0, 0, 0.5, 1, None)
+    assert call(1 << 28, 8) == attn.ATTN_ERR_INVALID_ARG
+    assert call(1 << 30, 4) == attn.ATTN_ERR_INVALID_ARG
