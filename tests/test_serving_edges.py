@@ -9,6 +9,12 @@ from attention_forward_tcgen05_gb300 import build as attn_build
 from attention_forward_tcgen05_gb300 import workloads as W
 
 
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    attn_build.build()
+    return attn.load()
+
+
 # ------------------------------------------------------------------ sync_check
 class _Buffer:
     """A stand-in for a counter buffer that notes when it is zeroed."""
@@ -225,13 +231,7 @@ def test_evict_from_a_bad_page(in_place):
 
 
 # ------------------------------------------------------------------ sizes the kernels cannot index
-@pytest.fixture(scope="module")
-def lib():
-    attn_build.build()
-    return attn.load()
-
-
-def test_key_weights_refuse_more_units_than_an_int(lib):
+def test_key_weights_refuse_more_units_than_an_int():
     """A CTA finds its (sequence, KV head) by their product: 2^31 of them are refused."""
     #  q lse kc table cu lens w stride B Hq Hkv total max_sq d max_pages page pages causal window sink scale acc stream
     def call(B, Hkv):
