@@ -37,6 +37,9 @@ int check_heads(int B, int Hq, int Hkv) {
   return B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ? ATTN_ERR_INVALID_ARG : ATTN_OK;
 }
 
+// Bytes of a slot (its Hkv rows), which the row gathers hold in 32 bits.
+int check_slot(int Hkv, int d) { return (long long)Hkv * d >= (1LL << 31) ? ATTN_ERR_INVALID_ARG : ATTN_OK; }
+
 attn::PagedKV cache(const attn_bf16_t* k, const attn_bf16_t* v, const int* table, int max_pages, int page_size,
                     int num_pages) {
   return attn::PagedKV{k, v, table, max_pages, page_size, num_pages, 0};
@@ -188,6 +191,7 @@ int attn_prefill_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const at
   if (!ok_dim(d) || (o_dtype != ATTN_F32 && o_dtype != ATTN_BF16)) return ATTN_ERR_UNSUPPORTED;
   if (window > 0 && n_splits > 1) return ATTN_ERR_UNSUPPORTED;
   rc = check_cache(page_table, B, max_pages, page_size, num_pages);
+  if (rc == ATTN_OK) rc = check_slot(Hkv, d);
   if (rc != ATTN_OK) return rc;
   if (B == 0 || total_q == 0 || max_sq == 0) return ATTN_OK;
   if (!ok16(q) || !ok16(kcache) || !ok16(vcache) || !ok16(o) || !ok16(lse) || !ok4(cu_seqlens_q) || !ok4(kv_lens) ||
@@ -261,6 +265,7 @@ int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const att
                       attn_stream_t stream) {
   int rc = check_heads(B, Hq, Hkv);
   if (rc == ATTN_OK) rc = check_cache(page_table, B, max_pages, page_size, num_pages);
+  if (rc == ATTN_OK && ok_dim(d)) rc = check_slot(Hkv, d);
   if (rc == ATTN_OK)
     // (the dense cache's row limit does not apply: max_kv = 1 here)
     rc = attn::check_decode_split_args(q, kcache, vcache, kv_lens, B, Hq, Hkv, d, 1, scale, n_splits,
@@ -314,6 +319,7 @@ int attn_key_weights(const attn_bf16_t* q, const float* lse, const attn_bf16_t* 
   if (cu_seqlens_q == nullptr && (total_q != B || max_sq != 1)) return ATTN_ERR_INVALID_ARG;
   if (!ok_dim(d) || scale < 1e-30f || scale > 1e30f) return ATTN_ERR_UNSUPPORTED;  // (lse / scale is formed)
   rc = check_cache(page_table, B, max_pages, page_size, num_pages);
+  if (rc == ATTN_OK) rc = check_slot(Hkv, d);
   if (rc != ATTN_OK) return rc;
   if (w_stride < (long long)max_pages * page_size) return ATTN_ERR_INVALID_ARG;
   if (B == 0) return ATTN_OK;

@@ -393,7 +393,8 @@ unsigned long long attn_decode_noalloc_scratch_bytes(void);
  * A cache is a pair of pools, bf16 [num_pages][page_size][Hkv][d], and a table int32
  * [B][max_pages] (device): key j of sequence b lies in slot j % page_size of page
  * page_table[b][j / page_size].  page_size is any number >= 1; max_pages * page_size <=
- * 2^30, num_pages * page_size < 2^31; kv_lens[b] is clamped to [0, max_pages * page_size].
+ * 2^30, num_pages * page_size < 2^31, Hkv * d < 2^31; kv_lens[b] is clamped to
+ * [0, max_pages * page_size].
  * Table entries past a sequence's keys are never read (-1, say, is fine there), nor are
  * slots past them as data: they may hold anything, NaN too.  An entry in use that is no
  * page of the pool is reported as ATTN_ERR_DEVICE_INPUT by attn_sync_check; its rows read

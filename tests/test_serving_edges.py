@@ -238,3 +238,17 @@ def test_key_weights_refuse_more_units_than_an_int():
         return attn.attn_key_weights(16, 16, 16, 16, 16, 16, 16, 1, B, Hkv, Hkv, 7, 5, 64, 1, 1, 9, 1, 0, 0, 0.5, 1, None)
     assert call(1 << 28, 8) == attn.ATTN_ERR_INVALID_ARG
     assert call(1 << 30, 4) == attn.ATTN_ERR_INVALID_ARG
+
+
+def test_slots_above_4_gb_are_refused():
+    """The row gathers hold a slot's bytes, Hkv * d * 2, in 32 bits."""
+    big = 1 << 23  # heads of 256 dims
+    for Hkv, want in ((big, attn.ATTN_ERR_INVALID_ARG), (big - 1, attn.ATTN_OK)):
+        # (B = 0: nothing is launched; the sizes are checked first)
+        rc = [attn.attn_prefill_paged(16, 16, 16, 16, 16, 16, 16, 16, 0, Hkv, Hkv, 0, 0, 1, 1, 9, 256, 1, 0, 0, 0.5, 1,
+                                      1, None, None, 0, None),
+              attn.attn_decode_paged(16, 16, 16, 16, 16, 0, Hkv, Hkv, 256, 1, 1, 9, 0.5, 1, 1, None, None, 16, 16, 0,
+                                     None, None),
+              attn.attn_key_weights(16, 16, 16, 16, 16, 16, 16, 1, 0, Hkv, Hkv, 0, 0, 256, 1, 1, 9, 1, 0, 0, 0.5, 1,
+                                    None)]
+        assert rc == [want] * 3, (Hkv, rc)
