@@ -1,12 +1,17 @@
 """Calls of the paged serving functions at the edge of what they document: errors on one
 stream beside work on another, arguments left out, the largest sizes."""
+import numpy as np
 import pytest
 import torch
 
+import oracle
 import attention_forward_tcgen05_gb300 as attn
 from attention_forward_tcgen05_gb300 import _binding
 from attention_forward_tcgen05_gb300 import build as attn_build
 from attention_forward_tcgen05_gb300 import workloads as W
+from tests.paged_cases import gather, make_pages
+from tests.test_evict import lse_of, weights_ref
+from tests.tolerances import check_lse, check_o
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -252,3 +257,140 @@ def test_slots_above_4_gb_are_refused():
               attn.attn_key_weights(16, 16, 16, 16, 16, 16, 16, 1, 0, Hkv, Hkv, 0, 0, 256, 1, 1, 9, 1, 0, 0, 0.5, 1,
                                     None)]
         assert rc == [want] * 3, (Hkv, rc)
+
+
+# ------------------------------------------------------------------ forms beside the common ones
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("mask", [(True, 0, 0), (False, 0, 0), (True, 150, 4)], ids=["causal", "full", "window"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (14, 1)])
+def test_key_weights_of_eight_ctas_a_block(d, mask, Hq, Hkv):
+    """Few key blocks and many query rows: clusters of eight share a block of keys, and every
+    rank's sum counts once.  (At most 15 blocks, at least 16 query tiles; both ways of ending:
+    set and accumulated.)"""
+    causal, window, n_sink = mask
+    sq, kv = torch.tensor([900], dtype=torch.int32), torch.tensor([1100], dtype=torch.int32)
+    q, kc, _, cu = W.varlen_inputs(1, Hq, Hkv, d, sq, kv, 700 + d)
+    scale = d ** -0.5
+    lse = lse_of(q, kc, cu, kv, Hkv, scale, causal, window, n_sink)
+    (ref, bound), = weights_ref(q, lse, kc, cu, kv, Hkv, scale, causal, window, n_sink)
+    w0 = torch.rand(1, Hkv, 1100)
+    for acc in (False, True):
+        w = w0.cuda()
+        attn.key_weights(q.cuda(), lse.cuda(), kc.cuda(), kv.cuda(), w, cu_seqlens_q=cu.cuda(), max_sq=900,
+                         causal=causal, window=window, n_sink=n_sink, scale=scale, accumulate=acc)
+        attn.sync_check()
+        want = ref + (w0[0].double().numpy() if acc else 0)
+        got = w[0].cpu().double().numpy()
+        assert (abs(got - want) <= bound + (abs(want) * 2.0 ** -24 if acc else 0)).all()
+
+
+def _bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [[1, 1, 1], [7, 300, 2]], ids=["tokens", "chunks"])
+def test_a_table_wider_than_its_lengths(rows):
+    """A table with room for 131,072 keys over sequences of up to 2,000: results as from the
+    tight one (launch shapes follow the width, sums of key weights keep their order only within
+    a split of the rows, attention its splits: compared to the tolerances of either)."""
+    Hq, Hkv, d, page = 8, 2, 64, 32
+    kv = torch.tensor([2000, 300, 77], dtype=torch.int32)
+    q, kc, vc, cu = W.varlen_inputs(3, Hq, Hkv, d, torch.tensor(rows, dtype=torch.int32), kv, 710)
+    kp, vp, tight = make_pages(kc, vc, kv, page, 710)
+    wide = torch.full((3, 131072 // page), -1, dtype=torch.int32)
+    wide[:, :tight.shape[1]] = tight
+    ro, rl = oracle.sdpa_varlen(q, kc, vc, cu, kv, True, 0.125)
+    one = max(rows) == 1
+    lens, cug, qg = kv.cuda(), cu.cuda(), q.cuda()
+    ref = kept0 = None
+    for table in (tight, wide):
+        cap = table.shape[1] * page
+        tg, kg, vg = table.cuda(), kp.cuda(), vp.cuda()
+        for max_kv in (None, 2000):
+            if one:
+                o, lse = attn.decode_paged(qg, kg, vg, tg, lens, scale=0.125, out_dtype=torch.float32, max_kv=max_kv)
+                check_lse(lse.T.cpu().numpy(), rl)
+            else:
+                o, lse = attn.prefill_paged(qg, kg, vg, tg, cug, lens, max(rows), scale=0.125, out_dtype=torch.float32,
+                                            max_kv=max_kv)
+                check_lse(lse.cpu().numpy(), rl)
+            attn.sync_check()
+            check_o(o.cpu().numpy(), ro, False)
+        w = torch.full((3, Hkv, cap), 5.0, device="cuda")
+        attn.key_weights(qg, lse, kg, lens, w, page_table=tg, cu_seqlens_q=None if one else cug, max_sq=max(rows),
+                         scale=0.125, accumulate=False)
+        attn.sync_check()
+        fp32_lse = (lse.T if one else lse).cpu()
+        ref = weights_ref(q, fp32_lse, kc, cu, kv, Hkv, 0.125, True)
+        for b, (want, bound) in enumerate(ref):
+            L = int(kv[b])
+            assert (abs(w[b, :, :L].cpu().double().numpy() - want) <= bound).all()
+            assert (w[b, :, L:] == 5).all()
+        score = torch.rand(3, Hkv, cap, generator=torch.Generator().manual_seed(1))
+        score[:, :, :tight.shape[1] * page] = torch.rand(3, Hkv, tight.shape[1] * page,
+                                                         generator=torch.Generator().manual_seed(2))
+        kept, new = attn.evict(score.cuda(), kg, vg, lens, 128, 16, 4, page_table=tg)
+        attn.sync_check()
+        kept0 = kept if kept0 is None else kept0
+        assert torch.equal(kept, kept0) and new.tolist() == [128, 128, 77]
+        for b in range(3):
+            n = min(128, int(kv[b]))
+            for h in range(Hkv):
+                idx = kept[b, h, :n].cpu().long()
+                assert torch.equal(gather(kg.cpu(), tight, b, n, page)[:, h], kc[b, idx, h])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 20])
+def test_windowed_chunks_with_bf16_outputs(d, page):
+    rows, keys = [1, 77, 128, 300, 0, 200, 3], [1, 300, 128, 1200, 50, 150, 0]
+    sq, kv = torch.tensor(rows, dtype=torch.int32), torch.tensor(keys, dtype=torch.int32)
+    q, kc, vc, cu = W.varlen_inputs(len(rows), 7, 1, d, sq, kv, 720 + d)
+    kp, vp, table = make_pages(kc, vc, kv, page, 720)
+    scale = d ** -0.5
+    for window, n_sink in ((1, 0), (100, 4), (2 ** 31 - 1, 2 ** 31 - 1)):
+        o, lse = attn.prefill_paged(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), cu.cuda(), kv.cuda(), max(rows),
+                                    scale=scale, window=window, n_sink=n_sink)
+        attn.sync_check()
+        ro, rl = oracle.sdpa_varlen_window(q, kc, vc, cu, kv, min(window, 4096), min(n_sink, 4096), scale)
+        check_o(o.float().cpu().numpy(), ro, True)
+        check_lse(lse.cpu().numpy(), rl)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n_splits", [1, 3])
+def test_chunks_of_many_sequences(causal, n_splits):
+    """40 sequences: more than are ordered by their tiles."""
+    rng = np.random.default_rng(8)
+    sq = torch.from_numpy(rng.integers(0, 150, 40).astype(np.int32))
+    kv = torch.from_numpy(rng.integers(0, 600, 40).astype(np.int32))
+    q, kc, vc, cu = W.varlen_inputs(40, 4, 2, 64, sq, kv, 730)
+    kp, vp, table = make_pages(kc, vc, kv, 16, 730)
+    ro, rl = oracle.sdpa_varlen(q, kc, vc, cu, kv, causal, 0.125)
+    for dt in (torch.bfloat16, torch.float32):
+        o, lse = attn.prefill_paged(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), cu.cuda(), kv.cuda(), int(sq.max()),
+                                    causal=causal, scale=0.125, out_dtype=dt, n_splits=n_splits)
+        attn.sync_check()
+        check_o(o.float().cpu().numpy(), ro, dt is torch.bfloat16)
+        check_lse(lse.cpu().numpy(), rl)
+
+
+@pytest.mark.gpu
+def test_calls_repeat_their_bits():
+    """The same call on the same inputs, other calls between: the same bits, splits or not."""
+    q, kc, vc, cu = W.varlen_inputs(3, 8, 2, 128, torch.tensor([5, 200, 1]), torch.tensor([900, 700, 300]), 740)
+    kv = torch.tensor([900, 700, 300], dtype=torch.int32)
+    kp, vp, table = (x.cuda() for x in make_pages(kc, vc, kv, 16, 740))
+    lens, cug, qg = kv.cuda(), cu.cuda(), q.cuda()
+    first = {}
+    for _ in range(4):
+        for n in (1, 3):
+            out = (*attn.prefill_paged(qg, kp, vp, table, cug, lens, 200, n_splits=n),
+                   *attn.decode_paged(qg[:3].contiguous(), kp, vp, table, lens, n))
+            attn.sync_check()
+            for a, b in zip(out, first.setdefault(n, [t.clone() for t in out])):
+                assert torch.equal(_bits(a), _bits(b))
