@@ -171,7 +171,7 @@ def _decode_splits(B, Hq, Hkv, max_kv, d, code):
 # Workspaces of prefill_paged and decode_paged: kept for each stream, whose launches are
 # ordered; a call holds _launching while it makes its launches, so that another thread's on the
 # same stream do not come between two of them.  A call being captured gets its own (two graphs
-# may replay at the same time).
+# may replay at the same time).  They grow to the largest call seen and stay for the process.
 _partials = {}  # (device, stream handle) -> fp32
 
 
@@ -211,7 +211,9 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, device="cuda", factor:
     ``"linear"`` divides every f_i by factor; ``"ntk"`` raises the base by
     factor^(rot_dim / (rot_dim - 2)); ``"yarn"`` keeps the pairs that turn at least
     ``high_turns`` times over ``original_length`` positions, divides those that turn at
-    most ``low_turns`` times, blends linearly between, and sets amp = 0.1 ln(factor) + 1."""
+    most ``low_turns`` times, blends between (linearly in the number of turns), and sets
+    amp = 0.1 ln(factor) + 1.  (A checkpoint whose frequencies were blended otherwise, over
+    the pair's index between rounded bounds, say, brings its own: pass them as inv_freq.)"""
     torch = _torch()
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even and positive")
@@ -314,7 +316,9 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
     results, with page_table.  n_splits key splits of each sequence (0: chosen from the
     sizes and max_kv, the longest sequence's keys, by default the table's width) are
     joined through ``parts``, optional fp32 (part_o [total_q,Hq,n_splits,d], part_lse
-    [total_q,Hq,n_splits]).  window > 0 takes no splits."""
+    [total_q,Hq,n_splits]; by default a workspace kept for the stream).  window > 0 takes
+    no splits.  Give max_kv where the table is wider than its sequences are long: sized
+    for the table, most splits would hold no keys."""
     torch = _torch()
     dev = _device(q, "q")
     if stream is not None or dev != torch._C._cuda_getDevice():
@@ -374,7 +378,8 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
                  max_kv: int | None = None):
     """``decode`` over a paged cache (attn_decode_paged): the same arguments and results,
     with page_table.  n_splits = 0 chooses the splits and their least rows from the sizes
-    and max_kv (the longest sequence's keys, by default the table's width)."""
+    and max_kv (the longest sequence's keys, by default the table's width; give it where
+    the table is wider).  The split partials and counters are kept for the stream."""
     torch = _torch()
     dev = _device(q, "q")
     if stream is not None or dev != torch._C._cuda_getDevice():

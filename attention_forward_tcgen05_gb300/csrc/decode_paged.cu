@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(W * 32, DecodePagedCfg<D, NB, W>::kMinBlocks)
       __syncwarp();  // every lane has read the stage before it is refilled
     }
 
-    // ---- the four warps' (m, l, O) through shared memory ----
+    // ---- the warps' (m, l, O) through shared memory ----
     cp_async_wait<0>();
     __syncthreads();
     float* comb = reinterpret_cast<float*>(smem);  // [warp][head][D + 2]

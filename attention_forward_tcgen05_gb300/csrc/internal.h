@@ -16,7 +16,7 @@ struct PagedKV {
   const uint16_t* v;
   const int* table;
   int max_pages, page_size, num_pages;
-  int box_rows;  // prefill_paged.cu: rows of a tensor copy (64 or 128), 0: rows are gathered
+  int box_rows;  // prefill_paged.cu: rows of a tensor copy (a power of two, 8 to 128), 0: rows are gathered
 };
 
 // Prefill launch description (already validated by the C-ABI layer).
@@ -185,7 +185,7 @@ struct KeyWeightArgs {
   float scale;
   uint32_t* err;
 };
-// Few query rows per (sequence, KV head): the CUDA-core path, which needs no map.
+// Few query rows per (sequence, KV head): the warp-level mma path, which needs no map.
 bool key_weights_few_rows(int max_sq, int G);
 int key_weights_q_rows(int d);  // rows of a query tile of the tensor-core path
 

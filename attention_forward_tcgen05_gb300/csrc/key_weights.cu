@@ -47,7 +47,7 @@ struct RowCfg {
   static constexpr int kStage = 16 * D * 2;                          // K of 16 keys
   // a warp's ring: 6, 8, 16 KB.  A step is mostly a warp waiting on its own instructions, so
   // four CTAs an SM (three at d = 256) beat two of deeper rings: 64 sequences of up to 8192
-  // keys 98 us against 110, 4 units of 117000 keys 26 against 33; a fifth and sixth add nothing
+  // keys 99 us against 110, 4 units of 117000 keys 23 against 33; a fifth and sixth add nothing
   static constexpr int kStages = D == 64 ? 3 : 2;
   static constexpr int kSmem = kRowWarps * kStages * kStage + 1024;
 };

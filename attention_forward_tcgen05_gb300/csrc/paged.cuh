@@ -2,11 +2,12 @@
 // asynchronous copies that gather them into shared memory.
 //
 // A cache is a pool of pages, k / v [num_pages][page_size][Hkv][d]; key j of
-// sequence b lies in slot j % page_size of page table[b][j / page_size].  A tensor
-// copy would need one box per page, and the copy engine's cost is per box (small
-// pages run several times below the HBM rate), so rows are gathered by cp.async:
-// one warp instruction moves 512 bytes of 32 / (d / 8) rows, from any page size and
-// any first row, and a row that does not exist arrives as zeros without being read.
+// sequence b lies in slot j % page_size of page table[b][j / page_size].  One cp.async of a
+// warp moves 512 bytes of 32 / (d / 8) rows, from any page size and any first row, and a row
+// that does not exist arrives as zeros without being read; the decode and the key weights,
+// which HBM bounds, gather every row so, each warp for itself.  The prefill, whose softmax
+// warps want the issue slots, copies pages of 8 rows and more by TMA (paged_api.cu) and
+// gathers only a sequence's last tile and other pages.
 #pragma once
 #include "internal.h"
 #include "ptx.cuh"

@@ -1,7 +1,6 @@
 // prefill_kernel.cuh -- exact attention forward (FMHA) on the 5th-generation tensor cores,
-// one CTA per query block: used for head dims 64 and 128 (head dim 256 runs on
-// CTA pairs, prefill_pair.cu; the d = 256 configuration below is kept for
-// comparison and is not launched).
+// one CTA per query block: used for head dims 64 and 128, and over pages for 256 too
+// (over dense keys head dim 256 runs on CTA pairs, prefill_pair.cu).
 //
 // Per CTA: NQ query tiles of 128 rows of one (batch, query head), streamed
 // against K/V tiles of BN = 128 rows of the matching KV head, which arrive by

@@ -7,10 +7,12 @@
 // once per group of heads.
 //
 // What bounds it and what was measured (GB300, device time; floor in brackets).  Steps of 256
-// rows x 128 keys at d = 128 take 1.75 us, 0.6 of the tensor rate: the softmax's instruction
-// issue bounds them as in the dense kernel, and reading a group's keys once instead of once
-// per head lets them run closer to it (a 2,000-row chunk of a 32k-key prompt 662 us [469]
-// against 808 us with one head per tile over a dense cache).  Tensor copies against gathers:
+// rows x 128 keys at d = 128 take 1.75 us.  In a 2,000-row chunk of a 32k-key prompt (656 us and
+// a merge; 675 [469] together, 707 a call in a long series, where the power cap lowers the
+// clock) the tensor pipe is active 62 % of the time, issue slots 45 %, the exponential unit 31 %:
+// no unit is full, and the chain of a tile (S from TMEM, maximum, exponentials, P to TMEM, the
+// next product) is the time.  One head per tile over a dense cache takes 808 us: a group's keys
+// are then read once per head.  Tensor copies against gathers:
 // 164 against 248 us for eight ragged chunks (145 GFLOP) from pages of 16.  A unit's start and
 // end take 7 us; with 3.5 units an SM that is a sixth of the eight chunks' 145 us [78].  fp32
 // outputs: 199 us, 5e-6 of O off against 1.6e-3 with P in one term.

@@ -9,9 +9,9 @@
 //
 // Angles.  p f_i in fp32 is off by 0.06 radians at p = 10^6, so the angle is kept as a
 // fraction of a turn in 64-bit fixed point: f_i / 2 pi is taken to 2^-64 turns once per
-// CTA (in fp64: its relative error 2^-52 is the one that is left), and the product with
-// the 32-bit position wraps modulo one turn by itself, exactly.  The top 32 bits go to
-// sincospi as a signed half turn (2^-25 of it rounded away).  fp64 per token instead would
+// CTA (in fp64: its relative error, below 2^-52, is multiplied by the position), and the
+// product with the 32-bit position wraps modulo one turn by itself, exactly.  The top 32 bits
+// go to sincospi as a signed half turn (2^-25 of it, 2^-26 of a turn, rounded away).  fp64 per token instead would
 // cost the few fp64 lanes of this GPU about as long as the copy itself.
 #include <cmath>
 

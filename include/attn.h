@@ -418,8 +418,9 @@ unsigned long long attn_decode_noalloc_scratch_bytes(void);
  * of q and k becomes
  *   (x1 cos a - x2 sin a, x1 sin a + x2 cos a) * amp,
  * x1, x2 at m and m + rot_dim/2, or (interleaved) at 2m and 2m + 1; dims from rot_dim on
- * are copied.  Angles are exact to 2^-31 of a turn at any position (64-bit fixed point).
- * q_out gets the rotated queries, the cache the rotated keys and the values.
+ * are copied.  An angle is off by at most |p * inv_freq / 2 pi| * 2^-52 (the frequency's
+ * division by 2 pi in fp64) + 2^-25 (its rounding to fp32) of a turn.  q_out gets the rotated
+ * queries, the cache the rotated keys and the values.
  *
  * Arguments
  *   q, k, v      bf16, token t's heads [Hq][d] / [Hkv][d] at t * stride elements; strides
@@ -472,7 +473,9 @@ int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, i
  * directly: part_o, part_lse and counters are not touched and may be NULL.  Groups of more than
  * 16 query heads (bf16 outputs: more than 8 when B * Hkv <= 152) run on the tensor-core tiles
  * of attn_prefill_paged instead: splits of whole 128-key tiles, part_o of empty ones unwritten,
- * merged in a second launch without the counters.
+ * merged in a second launch without the counters.  The weights then go into P.V as there, in one
+ * bf16 term for bf16 outputs (2^-9 of each left out) and two for fp32 ones (2^-17), elsewhere in
+ * two (2^-17) and three (2^-25).
  *
  * Arguments: as attn_decode, with page_table int32 [B][max_pages] and pools
  * [num_pages][page_size][Hkv][d] in place of the caches and max_kv.
