@@ -61,8 +61,10 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
   __shared__ int place[kTokens], at[kTokens];    // cache row (-1: none, -2: no sequence), position
   const int half = a.rot / 2, t0 = blockIdx.x * kTokens, nt = min(kTokens, a.total - t0);
   for (int i = threadIdx.x; i < half; i += kThreads) {
-    const double x = a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
-    turn[i] = (unsigned long long)((x - floor(x)) * 18446744073709551616.0);
+    const double x = a.inv_freq[i] * 0.15915494309189535, y = fabs(x);  // 1 / (2 pi)
+    // the fraction of |x|, which is exact (that of a small negative x would be rounded to 2^-54)
+    const unsigned long long f = (unsigned long long)((y - floor(y)) * 18446744073709551616.0);
+    turn[i] = x < 0 ? 0ull - f : f;
   }
   if ((int)threadIdx.x >= kThreads - nt) {
     // (the last threads, whose warp has no frequency to convert up to d = 256)

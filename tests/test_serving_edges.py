@@ -1,5 +1,8 @@
 """Calls of the paged serving functions at the edge of what they document: errors on one
 stream beside work on another, arguments left out, the largest sizes."""
+import math
+from decimal import Decimal, localcontext
+
 import numpy as np
 import pytest
 import torch
@@ -11,7 +14,7 @@ from attention_forward_tcgen05_gb300 import build as attn_build
 from attention_forward_tcgen05_gb300 import workloads as W
 from tests.paged_cases import gather, make_pages
 from tests.test_evict import lse_of, weights_ref
-from tests.tolerances import check_lse, check_o
+from tests.tolerances import check_lse, check_o, half_ulp_bf16
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -179,6 +182,40 @@ def test_append_to_more_sequences_than_half_an_int():
     assert torch.equal(kp[1], k) and torch.equal(vp[1], -k) and not kp[0].any()
     del lens, cu, table
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sign", [1, -1])
+def test_far_angles_of_either_sign(sign):
+    """The angle itself, at positions above 2^30: with x = (1, 0) the second output is sin a,
+    and near a multiple of pi bf16 resolves it to less than the angle's bound, which is
+    |p f / 2 pi| 2^-52 + 2^-25 of a turn (times 2 pi in radians; sincospi and the product add
+    2^-21 of the value)."""
+    inv_2pi = Decimal("0.15915494309189533576888376337251436203445964574045644874766734405889679763")
+    T, d = 32768, 64
+    pos = np.random.default_rng(11).integers(2 ** 30, 2 ** 31 - 1, T).astype(np.int32)
+    freq = sign * attn.rope_frequencies(d, device="cpu")[0]
+    x = torch.zeros(T, 1, d, dtype=torch.bfloat16, device="cuda")
+    x[..., :d // 2] = 1
+    kp = torch.zeros(1, T, 1, d, dtype=torch.bfloat16, device="cuda")
+    lens, cu = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([T], [0, T]))
+    attn.rope_append(None, x, x, kp, torch.zeros_like(kp), lens, freq.cuda(), cu_seqlens_q=cu,
+                     positions=torch.from_numpy(pos).cuda())
+    attn.sync_check()
+    got = kp[0, :, 0, d // 2:].double().cpu().numpy()
+    checked = 0
+    with localcontext() as ctx:
+        ctx.prec = 60
+        for m in range(d // 4, d // 2):  # f <= 0.01
+            f = Decimal(float(freq[m])) * inv_2pi
+            for t in np.flatnonzero(abs(got[:, m]) < 2.0 ** -11):
+                turns = f * int(pos[t])
+                a = 2 * np.pi * float(turns - turns.to_integral_value())
+                want = math.sin(a)
+                tol = 2 * np.pi * (float(abs(turns)) * 2.0 ** -52 + 2.0 ** -25) + abs(want) * 2.0 ** -21
+                assert abs(got[t, m] - want) <= half_ulp_bf16(abs(want) + tol) + tol, (m, pos[t])
+                checked += 1
+    assert checked > 50
 
 
 # ------------------------------------------------------------------ eviction
