@@ -223,7 +223,7 @@ __device__ __noinline__ int2 block_of_rank(int r, int B, int Sq_max, int Skv_max
 // (any G), and key splits start on a KV tile.
 // FINE (fp32 outputs over pages): P goes into P.V as two bf16 terms, its value and the
 // remainder, the second over the other half of S's columns (2^-17 of P left out instead of
-// 2^-9), and O is divided by the exact row sum.
+// 2^-8), and O is divided by the exact row sum.
 template <int D, bool WIN, bool SPLIT, bool HALVES, bool PAGED, bool FINE>
 __global__ void __launch_bounds__(PrefillCfg<D, HALVES>::kThreads, 1)
     fmha_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

@@ -474,7 +474,7 @@ int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, i
  * 16 query heads (bf16 outputs: more than 8 when B * Hkv <= 152) run on the tensor-core tiles
  * of attn_prefill_paged instead: splits of whole 128-key tiles, part_o of empty ones unwritten,
  * merged in a second launch without the counters.  The weights then go into P.V as there, in one
- * bf16 term for bf16 outputs (2^-9 of each left out) and two for fp32 ones (2^-17), elsewhere in
+ * bf16 term for bf16 outputs (2^-8 of each left out) and two for fp32 ones (2^-17), elsewhere in
  * two (2^-17) and three (2^-25).
  *
  * Arguments: as attn_decode, with page_table int32 [B][max_pages] and pools
