@@ -73,10 +73,20 @@ def _device(lead, name):
     return dev
 
 
-def _elsewhere(call, lead, stream):
+def _record(x, stream):
+    """Mark the tensors of nested arguments as used by a stream: their memory is not given
+    out again before what it has queued is done."""
+    if isinstance(x, (tuple, list)):
+        for y in x:
+            _record(y, stream)
+    elif isinstance(x, _torch().Tensor):
+        x.record_stream(stream)
+
+
+def _elsewhere(call, lead, stream, inputs):
     """``call()`` with the tensors' device and the given stream current: outputs and
     workspaces then belong to that stream, and the outputs are marked as used by the
-    caller's."""
+    caller's, the inputs as used by the given one."""
     torch = _torch()
     if stream is not None and stream.device != lead.device:
         raise ValueError("the stream belongs to another device than the tensors")
@@ -86,9 +96,8 @@ def _elsewhere(call, lead, stream):
             return call()
         with torch.cuda.stream(stream):
             result = call()
-        for t in result if isinstance(result, tuple) else (result,):
-            if t is not None:
-                t.record_stream(own)
+        _record(inputs, stream)
+        _record(result, own)
         return result
 
 
@@ -271,7 +280,8 @@ def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_
     dev = _device(k, "k")
     if stream is not None or dev != torch._C._cuda_getDevice():
         return _elsewhere(lambda: rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table, cu_seqlens_q,
-                                              positions, interleaved, amp, out), k, stream)
+                                              positions, interleaved, amp, out), k, stream,
+                          (q, k, v, kcache, vcache, kv_lens, inv_freq, page_table, cu_seqlens_q, positions, out))
     handle = torch._C._cuda_getCurrentRawStream(dev)
     np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
     total, B = k.shape[0], kv_lens.shape[0]
@@ -324,7 +334,8 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
     if stream is not None or dev != torch._C._cuda_getDevice():
         return _elsewhere(lambda: prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq, causal,
                                                 scale, out_dtype, None, out, window, n_sink, n_splits,
-                                                min_rows_per_split, max_kv, parts), q, stream)
+                                                min_rows_per_split, max_kv, parts), q, stream,
+                          (q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, out, parts))
     handle = torch._C._cuda_getCurrentRawStream(dev)
     qp = _need(q, "q", torch.bfloat16, 3, dev)
     np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
@@ -384,7 +395,8 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
     dev = _device(q, "q")
     if stream is not None or dev != torch._C._cuda_getDevice():
         return _elsewhere(lambda: decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits, min_rows_per_split,
-                                               scale, out_dtype, None, out, parts, counters, max_kv), q, stream)
+                                               scale, out_dtype, None, out, parts, counters, max_kv), q, stream,
+                          (q, kcache, vcache, page_table, kv_lens, out, parts, counters))
     handle = torch._C._cuda_getCurrentRawStream(dev)
     qp = _need(q, "q", torch.bfloat16, 3, dev)
     B, Hq, dq = q.shape
@@ -461,7 +473,8 @@ def key_weights(q, lse, kcache, kv_lens, weights, page_table=None, cu_seqlens_q=
     dev = _device(q, "q")
     if stream is not None or dev != torch._C._cuda_getDevice():
         return _elsewhere(lambda: key_weights(q, lse, kcache, kv_lens, weights, page_table, cu_seqlens_q, max_sq,
-                                              causal, window, n_sink, scale, accumulate), q, stream)
+                                              causal, window, n_sink, scale, accumulate), q, stream,
+                          (q, lse, kcache, kv_lens, weights, page_table, cu_seqlens_q))
     handle = torch._C._cuda_getCurrentRawStream(dev)
     qp = _need(q, "q", torch.bfloat16, 3, dev)
     np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
@@ -504,7 +517,7 @@ def evict(weights, kcache, vcache, kv_lens, budget: int, n_recent: int = 0, n_si
     dev = _device(kcache, "kcache")
     if stream is not None or dev != torch._C._cuda_getDevice():
         return _elsewhere(lambda: evict(weights, kcache, vcache, kv_lens, budget, n_recent, n_sink, page_table, dst,
-                                        out), kcache, stream)
+                                        out), kcache, stream, (weights, kcache, vcache, kv_lens, page_table, dst, out))
     handle = torch._C._cuda_getCurrentRawStream(dev)
     budget, n_recent, n_sink = int(budget), int(n_recent), int(n_sink)
     np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)

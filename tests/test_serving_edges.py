@@ -431,3 +431,51 @@ def test_calls_repeat_their_bits():
             attn.sync_check()
             for a, b in zip(out, first.setdefault(n, [t.clone() for t in out])):
                 assert torch.equal(_bits(a), _bits(b))
+
+
+# ------------------------------------------------------------------ streams
+@pytest.mark.gpu
+def test_inputs_dropped_after_a_call_on_another_stream():
+    """The stream argument, with inputs that the caller lets go of right after the call while
+    the stream is still busy with work before it: their memory is not handed out again before
+    the call has read them."""
+    B, Hq, Hkv, d, page, L = 4, 8, 2, 64, 16, 96
+    g = torch.Generator(device="cuda").manual_seed(9)
+
+    def bf16(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").bfloat16()
+
+    pool = B * L // page, page, Hkv, d
+    q, k, v, kc, vc = bf16(B, Hq, d), bf16(B, Hkv, d), bf16(B, Hkv, d), bf16(*pool), bf16(*pool)
+    table = torch.arange(pool[0], dtype=torch.int32, device="cuda").view(B, -1)
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    lse, w = torch.randn(B, Hq, generator=g, device="cuda") + 5, torch.rand(B, Hkv, L, generator=g, device="cuda")
+    freq = attn.rope_frequencies(d)[0]
+    calls = [  # inputs, and the call that is made with copies of them
+        ((q, k, v, kc, vc, lens, freq, table), lambda a, s: attn.rope_append(*a, stream=s)),
+        ((q, kc, vc, table, cu, lens), lambda a, s: attn.prefill_paged(*a, 1, n_splits=1, stream=s)[0]),
+        ((q, kc, vc, table, lens), lambda a, s: attn.decode_paged(*a, 3, stream=s)[0]),
+        ((q, lse, kc, lens, w, table), lambda a, s: attn.key_weights(*a, accumulate=False, stream=s)),
+        ((w, kc, vc, lens, table), lambda a, s: attn.evict(*a[:4], 40, 4, 2, page_table=a[4], stream=s)[0]),
+    ]
+    busy, front = torch.cuda.Stream(), torch.zeros(1 << 28, device="cuda")
+    for inputs, call in calls:
+        want = call([t.clone() for t in inputs], None).clone()
+        call([t.clone() for t in inputs], busy)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(busy):
+            for _ in range(20):  # some milliseconds
+                front.add_(1)
+        args = [t.clone() for t in inputs]
+        busy.wait_stream(torch.cuda.current_stream())
+        got = call(args, busy)
+        if any(got is a for a in args):  # (the weights themselves: what else was given goes)
+            args = [a for a in args if a is got]
+        else:
+            args = None
+        others = [torch.full_like(t, -1) for t in inputs for _ in range(3)]  # of the same sizes
+        torch.cuda.synchronize()
+        attn.sync_check()
+        assert torch.equal(_bits(got), _bits(want))
+        del others, args
