@@ -17,3 +17,6 @@ from ._serving import (  # noqa: F401
     attn_decode_paged, attn_decode_paged_splits, attn_evict, attn_key_weights, attn_prefill_paged,
     attn_prefill_paged_splits, attn_rope_append, decode_paged, evict, key_weights, prefill_paged, rope_append,
     rope_frequencies)
+from ._backward import (  # noqa: F401
+    attn_prefill_backward, attn_prefill_backward_workspace, attn_prefill_varlen_backward, prefill_backward,
+    prefill_varlen_backward)

@@ -81,7 +81,11 @@ def load(path: str | None = None):
         lib.attn_decode_paged_splits.argtypes = [i] * 6 + [vp]
         lib.attn_key_weights.argtypes = [vp] * 7 + [ll] + [i] * 12 + [f, i, vp]
         lib.attn_evict.argtypes = [vp, vp, ll] + [vp] * 4 + [i] * 9 + [vp] * 3 + [i] * 3 + [vp] * 3
-        for name in ("attn_rope_append", "attn_prefill_paged", "attn_prefill_paged_splits", "attn_decode_paged",
+        lib.attn_prefill_backward.argtypes = [vp] * 10 + [i] * 9 + [f, i, vp, ull, vp]
+        lib.attn_prefill_varlen_backward.argtypes = [vp] * 12 + [i] * 10 + [f, i, i, vp, ull, vp]
+        lib.attn_prefill_backward_workspace.argtypes = [i] * 3 + [ll] + [i] * 3
+        lib.attn_prefill_backward_workspace.restype = ull
+        for name in ("attn_prefill_backward", "attn_prefill_varlen_backward", "attn_rope_append", "attn_prefill_paged", "attn_prefill_paged_splits", "attn_decode_paged",
                      "attn_decode_paged_splits", "attn_key_weights", "attn_evict"):
             getattr(lib, name).restype = i
         for name in ("attn_prefill_fwd", "attn_prefill_varlen", "attn_prefill_window",

@@ -203,6 +203,27 @@ struct EvictArgs {
   uint32_t* err;
 };
 
+// Gradients of the prefill (prefill_backward.cu).  Fixed-length (cu_q == nullptr): q, o, dout,
+// dq [B][Sq][Hq][d], lse [B][Hq][Sq], total_q = B * Sq; packed: [total_q][Hq][d], lse
+// [Hq][total_q], Sq the longest sequence, kv_lens set.  k, v, dk, dv [B][Skv][Hkv][d].
+struct BackwardArgs {
+  CUtensorMap tm_q, tm_do, tm_k, tm_v;  // 4-D maps {d, H, rows, batch}, box {64, 1, 128, 1}
+  const uint16_t *q, *dout, *k, *v;
+  const void* o;
+  const float *lse, *dlse;              // dlse may be nullptr
+  uint16_t *dq, *dk, *dv;
+  const int *cu_q, *kv_lens;
+  int B, Hq, Hkv, Sq, Skv, total_q, d, causal, window, n_sink, o_bf16, fill;
+  float scale;
+  uint32_t* err;
+  // workspace
+  int *pre_k, *pre_q;                   // items before each group of the two passes, and all of them
+  float2* stat;                         // [rows of lse] lse log2 e (+inf: the row takes no part), D
+  uint4* ext;                           // the same as bf16 columns of the dK/dV pass, 128 rows more
+  float *part_k, *part_q;               // [ctas][2][accumulators * d / 4][128][4] sums of cut units
+  int ctas_k, ctas_q;
+};
+
 // Rows of a K / V stage loaded by one TMA box in the decode kernel (two
 // consumer warps share a stage, 32 rows each).
 constexpr int kDecodeStageRows = 64;
@@ -265,6 +286,7 @@ cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_key_weights(const KeyWeightArgs& a, cudaStream_t stream);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t stream);
 // This device's error word (attn_api.cu), or nullptr.
 uint32_t* device_err_word();
 // 5-D query map of the packed tiles: {d, G, Hq / G, ns, nb}, box {64, G, 1, rows / G, 1}.

@@ -548,6 +548,63 @@ int attn_evict(const float* weights, float* weights_out, long long w_stride, att
                attn_stream_t stream);
 
 /*
+ * Gradients
+ * ---------
+ * (The pages have no counterpart: they stop at the forward pass.)
+ *
+ * attn_prefill_backward -- the gradients of attn_prefill_fwd (window = 0) and
+ * attn_prefill_window (window >= 1) with respect to q, k and v.
+ *
+ * With P_ij = exp(scale * q_i . k_j - lse_i) over the keys that row i admits, dout = dL/do and
+ * D_i = dout_i . o_i - dlse_i,
+ *   dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dout_i . v_j - D_i),
+ *   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,
+ * dk and dv summed over the query heads of a KV head.  P and dS go into their products rounded to
+ * bf16 (2^-8 of each; the gradients' own rounding is 2^-8), everything else is fp32.  A row that
+ * admits no key (lse = -inf) takes no part: its dq is 0.  Every sum has a fixed order: the same
+ * inputs give the same bits.
+ *
+ * Arguments
+ *   dout, q   bf16 [B][Sq][Hq][d],  k, v  bf16 [B][Skv][Hkv][d]
+ *   o         the forward call's o (fp32 or bf16 per o_dtype; D is as exact as it), lse its
+ *             fp32 [B][Hq][Sq]
+ *   dlse      fp32 [B][Hq][Sq]: dL/dlse, or NULL where the loss does not use lse
+ *   dq, dk, dv  like q, k, v, written whole
+ *   causal, window, n_sink, scale  as in the forward call (window = 0: none, >= 1: causal);
+ *             scale in [1e-30, 1e30]
+ *   work      attn_prefill_backward_workspace(B, Hq, Hkv, B * Sq, Sq, Skv, d) bytes, 256-byte
+ *             aligned, contents of no matter; calls that may run at the same time need their own
+ *   d in {64, 128};  B * Sq * Hq, B * Skv * Hkv and the number of 128 x 128 tiles of all heads
+ *   below 2^31
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.  Can be captured
+ * into a CUDA graph after a first call of its head dim on the device.
+ */
+int attn_prefill_backward(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16_t* v,
+                          const void* o, const float* lse, const float* dlse, attn_bf16_t* dq, attn_bf16_t* dk,
+                          attn_bf16_t* dv, int B, int Hq, int Hkv, int Sq, int Skv, int d, int causal, int window,
+                          int n_sink, float scale, int o_dtype, void* work, unsigned long long work_bytes,
+                          attn_stream_t stream);
+
+/*
+ * attn_prefill_varlen_backward -- the same for attn_prefill_varlen and
+ * attn_prefill_varlen_window: dout, q, o, dq [total_q][Hq][d], lse and dlse [Hq][total_q], caches and
+ * their gradients [B][max_kv][Hkv][d].  Rows of no sequence and slots at or past kv_lens[b] are not
+ * used; their gradients become 0 (fill != 0) or stay as they are.  A sequence longer than max_sq is
+ * reported as ATTN_ERR_DEVICE_INPUT by attn_sync_check.
+ *   work      attn_prefill_backward_workspace(B, Hq, Hkv, total_q, max_sq, max_kv, d) bytes
+ */
+int attn_prefill_varlen_backward(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16_t* kcache,
+                                 const attn_bf16_t* vcache, const void* o, const float* lse, const float* dlse,
+                                 attn_bf16_t* dq, attn_bf16_t* dkcache, attn_bf16_t* dvcache, const int* cu_seqlens_q,
+                                 const int* kv_lens, int B, int Hq, int Hkv, int total_q, int max_sq, int max_kv,
+                                 int d, int causal, int window, int n_sink, float scale, int o_dtype, int fill,
+                                 void* work, unsigned long long work_bytes, attn_stream_t stream);
+
+/* Bytes of their workspace (host only); 0 for sizes that they refuse. */
+unsigned long long attn_prefill_backward_workspace(int B, int Hq, int Hkv, long long total_q, int max_sq, int max_kv,
+                                                   int d);
+
+/*
  * attn_sync_check -- synchronise `stream`, then read and clear this device's
  * error word.  Returns ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT (a kernel's bounded
  * wait gave up; that kernel's outputs are invalid), ATTN_ERR_DEVICE_INPUT (a
