@@ -29,9 +29,9 @@ int check_sizes(const Sizes& z) {
   if (z.d != 64 && z.d != 128) return ATTN_ERR_UNSUPPORTED;
   if (z.rows * z.Hq >= (1LL << 31) || (long long)z.B * z.Skv * z.Hkv >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
   if ((long long)z.Hq * z.d >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
-  // tile pairs of all heads, which the kernels count in 32 bits
+  // tile pairs of all heads (and some for each unit's start), which the kernels count in 32 bits
   const long long tq = (z.Sq + 127LL) / 128, tk = (z.Skv + 127LL) / 128;
-  if (tq * z.B * tk >= (1LL << 31) / z.Hq) return ATTN_ERR_INVALID_ARG;
+  if ((tq + 8) * z.B * (tk + 8) >= (1LL << 31) / z.Hq) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 

@@ -45,7 +45,11 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kT = 128;           // rows of a tile
-constexpr int kMinItems = 2;      // items of a slice, at least
+// A run of a unit's items costs its start and end (the F tiles' copy, the sums' way out) beside its
+// items, about as much as kRunCost of them: units of few items would otherwise fill some slices
+// with nothing but starts and ends.
+constexpr int kRunCost = 2;
+constexpr int kMinCost = 2 + kRunCost;  // of a slice
 
 template <int D, bool KV>
 struct BwdCfg {
@@ -117,14 +121,13 @@ template <bool KV>
 __device__ __forceinline__ int unit_items(const BackwardArgs& a, const Unit& u) {
   return KV ? u.nt * (a.Hq / a.Hkv) : u.nt;
 }
+__device__ __forceinline__ int unit_cost(int items) { return items > 0 ? items + kRunCost : 0; }
 // Groups (sequence, F tile) of the pass: each holds a unit per head.
 __host__ __device__ __forceinline__ int f_tiles(const BackwardArgs& a, bool kv) {
   return ((kv ? a.Skv : a.Sq) + kT - 1) / kT;
 }
-// Items of a slice.
-__device__ __forceinline__ int slice_items(int total, int ctas) {
-  return max((total + ctas - 1) / ctas, kMinItems);
-}
+// The slices' share of the units' costs.
+__device__ __forceinline__ int slice_cost(int total, int ctas) { return max((total + ctas - 1) / ctas, kMinCost); }
 
 // ------------------------------------------------------------------ rows' lse and D, the item list
 constexpr int kPrepThreads = 256;
@@ -154,9 +157,9 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi, uint32_t& mid, uin
   lo = pack_bf16x2(r1 - __uint_as_float(mid << 16), 0.f) & 0xFFFFu;
 }
 
-// Exclusive prefix of the groups' items (all heads of a group) by one CTA; pre[n] the total.
+// Exclusive prefix of the groups' costs (all heads of a group) by one CTA; pre[n] the total.
 template <bool KV>
-__device__ void scan_items(const BackwardArgs& a, int* pre) {
+__device__ void scan_costs(const BackwardArgs& a, int* pre) {
   __shared__ int sums[kPrepThreads / 32];
   const int nx = f_tiles(a, KV), n = a.B * nx, H = KV ? a.Hkv : a.Hq;
   const int per = (n + kPrepThreads - 1) / kPrepThreads;
@@ -168,7 +171,7 @@ __device__ void scan_items(const BackwardArgs& a, int* pre) {
       const int c0 = min(max(a.cu_q[b], 0), a.total_q), c1 = min(a.cu_q[b + 1], a.total_q);
       if (c1 - c0 > a.Sq) atomicCAS(a.err, kErrNone, kErrBadShape);
     }
-  for (int g = lo; g < hi; ++g) s += unit_items<KV>(a, unit_of<KV>(a, g / nx, g % nx)) * H;
+  for (int g = lo; g < hi; ++g) s += unit_cost(unit_items<KV>(a, unit_of<KV>(a, g / nx, g % nx))) * H;
   int incl = s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -182,7 +185,7 @@ __device__ void scan_items(const BackwardArgs& a, int* pre) {
   for (int w = 0; w < warp; ++w) at += sums[w];
   for (int g = lo; g < hi; ++g) {
     pre[g] = at;
-    at += unit_items<KV>(a, unit_of<KV>(a, g / nx, g % nx)) * H;
+    at += unit_cost(unit_items<KV>(a, unit_of<KV>(a, g / nx, g % nx))) * H;
   }
   if (hi == n && lo < n) pre[n] = at;
   if (n == 0 && threadIdx.x == 0) pre[0] = 0;
@@ -192,8 +195,8 @@ __device__ void scan_items(const BackwardArgs& a, int* pre) {
 template <int D, bool OBF16>
 __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __grid_constant__ BackwardArgs a) {
   if (blockIdx.x < 2) {
-    if (blockIdx.x == 0) scan_items<true>(a, a.pre_k);
-    else scan_items<false>(a, a.pre_q);
+    if (blockIdx.x == 0) scan_costs<true>(a, a.pre_k);
+    else scan_costs<false>(a, a.pre_q);
     return;
   }
   constexpr int L = D / 8;
@@ -234,15 +237,15 @@ template <bool KV>
 struct Walk {
   const BackwardArgs& a;
   const int* pre;
-  int nx, n_groups, H, pos, end;  // next item and end of the slice
-  int g, g0, cnt;                 // group, its first item, items of one of its units
+  int nx, n_groups, H, pos, end;  // place in the list of costs, end of the slice
+  int g, g0, cnt;                 // group, its place, items of one of its units
   Unit u;
   int b, x;
   __device__ __forceinline__ Walk(const BackwardArgs& a_, int lane)
       : a(a_), pre(KV ? a_.pre_k : a_.pre_q), H(KV ? a_.Hkv : a_.Hq) {
     nx = f_tiles(a, KV);
     n_groups = a.B * nx;
-    const int total = pre[n_groups], per = slice_items(total, (int)gridDim.x);
+    const int total = pre[n_groups], per = slice_cost(total, (int)gridDim.x);
     pos = (int)min((long long)total, (long long)blockIdx.x * per);
     end = min(total, pos + per);
     g = 0; g0 = 0; cnt = 0; b = x = 0;
@@ -269,16 +272,20 @@ struct Walk {
   }
   // the next run: head h, its items [i0, i0 + n); false at the end of the slice
   __device__ __forceinline__ bool next(int& h, int& i0, int& n) {
-    if (pos >= end) return false;
-    while (pos >= g0 + cnt * H) {
-      ++g;
-      enter();
+    while (pos < end) {
+      while (pos >= g0 + unit_cost(cnt) * H) {
+        ++g;
+        enter();
+      }
+      const int cost = unit_cost(cnt);
+      h = (pos - g0) / cost;
+      const int at = pos - g0 - h * cost, to = min(cost, at + end - pos);  // of the unit's cost
+      pos += to - at;
+      i0 = max(0, at - kRunCost);
+      n = max(0, to - kRunCost) - i0;
+      if (n > 0) return true;
     }
-    h = (pos - g0) / cnt;
-    i0 = pos - g0 - h * cnt;
-    n = min(cnt - i0, end - pos);
-    pos += n;
-    return true;
+    return false;
   }
 };
 
@@ -311,6 +318,18 @@ struct ItemWalk {
     }
   }
 };
+
+// the lowest n of 32 bits, n clamped to [0, 32]
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); }
+// bf16 pairs: element i stays where bit i is set, else becomes 0
+template <int N>
+__device__ __forceinline__ void keep_bits(uint32_t* t, uint32_t in) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    t[c] = (in & (1u << (2 * c))) ? t[c] : t[c] & 0xFFFF0000u;
+    t[c] = (in & (2u << (2 * c))) ? t[c] : t[c] & 0x0000FFFFu;
+  }
+}
 
 template <int D, bool KV>
 __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
@@ -662,14 +681,14 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
           s[c] = __float_as_uint(e0);
           s[c + 1] = __float_as_uint(e1);
         }
+        // this thread's columns as bits (a weight out of them may be inf, dP of a column that is no
+        // row anything: both products' operands are cleared after their rounding)
+        uint32_t in[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
         if (mask) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const int k = c0 + c;
-            const bool in = k < hi && (k >= lo || k < sink);
-            // (both factors: dP of a column that is no row may be anything)
-            s[c] = in ? s[c] : 0u;
-            p[c] = in ? p[c] : 0u;
+          for (int q = 0; q < 2; ++q) {
+            const int c1 = c0 + q * 32;
+            in[q] = (bits_below(hi - c1) & ~bits_below(lo - c1)) | bits_below(min(sink, hi) - c1);
           }
         }
         if constexpr (KV) {
@@ -679,6 +698,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 16; ++c)
               t[c] = pack_bf16x2(__uint_as_float(s[q * 32 + 2 * c]), __uint_as_float(s[q * 32 + 2 * c + 1]));
+            if (mask) keep_bits<16>(t, in[q]);
             tmem_st16(sc + q * 16, t);
           }
           tmem_wait_st();
@@ -694,6 +714,10 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
           float x0, x1;
           f2unpack(mul2(g, f2pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]))), x0, x1);
           t[c] = pack_bf16x2(x0, x1);
+        }
+        if (mask) {
+          keep_bits<16>(t, in[0]);
+          keep_bits<16>(t + 16, in[1]);
         }
         tmem_st32(sc + (KV ? 32 : 0), t);
         tmem_wait_st();
@@ -798,7 +822,7 @@ __device__ void join(const BackwardArgs& a, int c, int ctas, int zero_cta, int z
     }
     return;
   }
-  const int per = slice_items(total, ctas);
+  const int per = slice_cost(total, ctas);
   const long long at = (long long)c * per;
   if (c == 0 || at >= total) return;
   int lo = 0, hi = n_groups;
@@ -813,10 +837,10 @@ __device__ void join(const BackwardArgs& a, int c, int ctas, int zero_cta, int z
   const int b = lo / nx, f0 = lo % nx * kT;
   const Unit u = unit_of<KV>(a, b, lo % nx);
   const int cnt = unit_items<KV>(a, u);
-  const int h = (int)(at - pre[lo]) / cnt;
-  const int u0 = pre[lo] + h * cnt, u1 = u0 + cnt;  // the unit's items
-  const int c0 = u0 / per, c1 = (u1 - 1) / per;     // its slices
-  if (u0 == at || c != c0 + 1) return;
+  const int cost = unit_cost(cnt), h = (int)(at - pre[lo]) / cost;
+  const int u0 = pre[lo] + h * cost + kRunCost, u1 = u0 + cnt;  // the places of the unit's items
+  const int c0 = u0 / per, c1 = (u1 - 1) / per;                 // its slices
+  if (at <= u0 || c != c0 + 1) return;
   const float4* part = reinterpret_cast<const float4*>(KV ? a.part_k : a.part_q);
   constexpr int kSlot = kT * D * kAccs / 4;
   // 8 columns of a row at a time
