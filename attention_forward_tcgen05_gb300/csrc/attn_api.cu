@@ -112,6 +112,20 @@ int encode_pool_map(CUtensorMap* map, const void* base, int d, int Hkv, int page
   return encode_bf16_4d(map, base, d, Hkv, page_size, num_pages, rows);
 }
 
+int encode_panel_map(CUtensorMap* map, const void* base, int d, int H, int S, int B, int rows) {
+  EncodeTiledFn enc = encoder();
+  if (enc == nullptr) return ATTN_ERR_CUDA;
+  const cuuint64_t row = (cuuint64_t)H * d * 2;
+  const cuuint64_t dims[5] = {64, (cuuint64_t)S, (cuuint64_t)d / 64, (cuuint64_t)H, (cuuint64_t)B};
+  const cuuint64_t strides[4] = {row, 128, (cuuint64_t)d * 2, row * S};
+  const cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)d / 64, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 int check_decode_split_args(const void* q, const void* kcache, const void* vcache, const int* kv_lens,
                             int B, int Hq, int Hkv, int d, int max_kv, float scale, int n_splits,
                             int min_rows, const void* part_o, const void* part_lse, bool check_parts) {

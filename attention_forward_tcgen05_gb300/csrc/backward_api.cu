@@ -29,15 +29,15 @@ int check_sizes(const Sizes& z) {
   if (z.d != 64 && z.d != 128) return ATTN_ERR_UNSUPPORTED;
   if (z.rows * z.Hq >= (1LL << 31) || (long long)z.B * z.Skv * z.Hkv >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
   if ((long long)z.Hq * z.d >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
-  // tile pairs of all heads (and some for each unit's start), which the kernels count in 32 bits
-  const long long tq = (z.Sq + 127LL) / 128, tk = (z.Skv + 127LL) / 128;
+  // tiles of 64 x 128 of all heads (and some for each unit's start), which the kernels count in 32 bits
+  const long long tq = (z.Sq + 63LL) / 64, tk = (z.Skv + 127LL) / 128;
   if ((tq + 8) * z.B * (tk + 8) >= (1LL << 31) / z.Hq) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 
 // Byte offsets of the workspace's parts.
 struct Layout {
-  size_t pre_k, pre_q, stat, ext, part_k, part_q, bytes;
+  size_t pre_k, pre_q, stat, ext1, ext2, part_k, part_q, bytes;
   int ctas;
 };
 Layout layout_of(const Sizes& z) {
@@ -54,7 +54,8 @@ Layout layout_of(const Sizes& z) {
   l.pre_k = take((size_t)(z.B * tk + 1) * 4);
   l.pre_q = take((size_t)(z.B * tq + 1) * 4);
   l.stat = take((size_t)z.rows * z.Hq * 8);
-  l.ext = take(((size_t)z.rows * z.Hq + 128) * 16);
+  l.ext1 = take(((size_t)z.rows * z.Hq + 128) * 16);
+  l.ext2 = take(((size_t)z.rows * z.Hq + 128) * 16);
   l.part_k = take((size_t)l.ctas * 2 * 128 * z.d * 2 * 4);
   l.part_q = take((size_t)l.ctas * 2 * 128 * z.d * 4);
   l.bytes = at;
@@ -84,10 +85,13 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   if (rows && keys && z.Sq > 0) {
     // packed rows are one batch slab
     const int ns = cu_q ? (int)z.rows : z.Sq, nb = cu_q ? 1 : z.B;
-    rc = attn::encode_pool_map(&a.tm_q, q, z.d, z.Hq, ns, nb, 128);
-    if (rc == ATTN_OK) rc = attn::encode_pool_map(&a.tm_do, dout, z.d, z.Hq, ns, nb, 128);
-    if (rc == ATTN_OK) rc = attn::encode_pool_map(&a.tm_k, k, z.d, z.Hkv, z.Skv, z.B, 128);
-    if (rc == ATTN_OK) rc = attn::encode_pool_map(&a.tm_v, v, z.d, z.Hkv, z.Skv, z.B, 128);
+    const int tn = attn::backward_tile_rows(z.d);
+    rc = attn::encode_panel_map(&a.tm_q, q, z.d, z.Hq, ns, nb, 128);
+    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_do, dout, z.d, z.Hq, ns, nb, 128);
+    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_k, k, z.d, z.Hkv, z.Skv, z.B, 128);
+    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_v, v, z.d, z.Hkv, z.Skv, z.B, 128);
+    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_qy, q, z.d, z.Hq, ns, nb, tn);
+    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_doy, dout, z.d, z.Hq, ns, nb, tn);
     if (rc != ATTN_OK) return rc;
   }
   a.q = q; a.dout = dout; a.k = k; a.v = v; a.o = o; a.lse = lse; a.dlse = dlse;
@@ -102,7 +106,9 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   a.pre_k = reinterpret_cast<int*>(w + l.pre_k);
   a.pre_q = reinterpret_cast<int*>(w + l.pre_q);
   a.stat = reinterpret_cast<float2*>(w + l.stat);
-  a.ext = reinterpret_cast<uint4*>(w + l.ext);
+  a.ext1 = reinterpret_cast<uint4*>(w + l.ext1);
+  a.ext2 = reinterpret_cast<uint4*>(w + l.ext2);
+  a.tn_k = attn::backward_tile_rows(z.d);
   a.part_k = reinterpret_cast<float*>(w + l.part_k);
   a.part_q = reinterpret_cast<float*>(w + l.part_q);
   a.ctas_k = a.ctas_q = l.ctas;

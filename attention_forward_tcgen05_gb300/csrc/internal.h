@@ -207,7 +207,8 @@ struct EvictArgs {
 // dq [B][Sq][Hq][d], lse [B][Hq][Sq], total_q = B * Sq; packed: [total_q][Hq][d], lse
 // [Hq][total_q], Sq the longest sequence, kv_lens set.  k, v, dk, dv [B][Skv][Hkv][d].
 struct BackwardArgs {
-  CUtensorMap tm_q, tm_do, tm_k, tm_v;  // 4-D maps {d, H, rows, batch}, box {64, 1, 128, 1}
+  CUtensorMap tm_q, tm_do, tm_k, tm_v;  // encode_panel_map, 128 rows
+  CUtensorMap tm_qy, tm_doy;            // tn_k rows
   const uint16_t *q, *dout, *k, *v;
   const void* o;
   const float *lse, *dlse;              // dlse may be nullptr
@@ -219,10 +220,12 @@ struct BackwardArgs {
   // workspace
   int *pre_k, *pre_q;                   // items before each group of the two passes, and all of them
   float2* stat;                         // [rows of lse] lse log2 e (+inf: the row takes no part), D
-  uint4* ext;                           // the same as bf16 columns of the dK/dV pass, 128 rows more
+  uint4 *ext1, *ext2;                   // the same as bf16 columns of the dK/dV pass, 128 rows more
   float *part_k, *part_q;               // [ctas][2][accumulators * d / 4][128][4] sums of cut units
   int ctas_k, ctas_q;
+  int tn_k;                             // rows of a streamed tile of the dK/dV pass
 };
+int backward_tile_rows(int d);  // tn_k
 
 // Rows of a K / V stage loaded by one TMA box in the decode kernel (two
 // consumer warps share a stage, 32 rows each).
@@ -293,6 +296,9 @@ uint32_t* device_err_word();
 int encode_q_map(CUtensorMap* map, const void* base, int d, int G, int Hq, int ns, int nb, int rows);
 // 4-D map of a pool {d, Hkv, page_size, num_pages}, box {64, 1, rows, 1}.
 int encode_pool_map(CUtensorMap* map, const void* base, int d, int Hkv, int page_size, int num_pages, int rows);
+// 5-D map {64, S, d / 64, H, B} of rows [B][S][H][d], box {64, rows, d / 64, 1, 1}: all 64-column
+// panels of a tile in one copy.
+int encode_panel_map(CUtensorMap* map, const void* base, int d, int H, int S, int B, int rows);
 cudaError_t launch_wait_timeout_probe(uint64_t limit_ns, uint32_t* err, cudaStream_t stream);
 
 }  // namespace attn

@@ -31,8 +31,8 @@
 // that every row sees, nor groups of odd sizes leave SMs idle.  A unit cut between CTAs
 // goes out as fp32 partials, which a last launch sums in slice order.
 //
-// Warps: 0-7 softmax (thread = row of F; warpgroup w takes 64 of the tile's 128 columns),
-// 8 MMA issue, 9 / 10 the rings of Y1 and Y2, 11 the F tiles.
+// Warps: 0-7 softmax (thread = row of F, 64 columns of an item), 8 / 9 S and dP with their F tiles, 10
+// the second products, 11 the rings of Y1 and Y2.
 #include <algorithm>
 #include <cmath>
 
@@ -48,36 +48,44 @@ constexpr int kT = 128;           // rows of a tile
 // A run of a unit's items costs its start and end (the F tiles' copy, the sums' way out) beside its
 // items, about as much as kRunCost of them: units of few items would otherwise fill some slices
 // with nothing but starts and ends.
-constexpr int kRunCost = 2;
+constexpr int kRunCost = 3;
 constexpr int kMinCost = 2 + kRunCost;  // of a slice
 
+// Columns of S and dP per item.  128, halved between the softmax warpgroups, where TMEM holds
+// two S and one dP beside the sums; the dK/dV pass at d = 128 has 256 columns for both: 64, two
+// buffers of each, an item for each warpgroup in turn.
 template <int D, bool KV>
 struct BwdCfg {
+  static constexpr int TN = (KV && D == 128) ? 64 : 128;  // rows of a Y tile
+  static constexpr int NS = 2;                            // S buffers
+  static constexpr int ND = TN == 64 ? 2 : 1;             // dP buffers
+  static constexpr int kArrive = TN == 64 ? 4 : 8;        // softmax warps of an item
   static constexpr int kPanels = D / 64;
-  static constexpr int kPanel = kT * 128;
-  static constexpr int kTile = kPanels * kPanel;
-  static constexpr int NS = (KV && D == 128) ? 1 : 2;                    // S buffers
-  static constexpr int kSt1 = D == 64 ? 4 : (KV ? 2 : 3);                // ring of Y1
-  static constexpr int kSt2 = D == 64 ? 4 : 2;                           // ring of Y2
-  static constexpr int kY1Off = 2 * kTile;
-  static constexpr int kY2Off = kY1Off + kSt1 * kTile;
-  // lse and D columns of a Q tile (16 bytes a row), the ones beside K, beside V, and zeros:
-  // the second eight columns of all of them
-  static constexpr int kExt = KV ? kT * 16 : 0;
-  static constexpr int kExtOff = kY2Off + kSt2 * kTile;
-  static constexpr int kOnesLOff = kExtOff + kSt1 * kExt;
-  static constexpr int kOnesDOff = kOnesLOff + kExt;
-  static constexpr int kZeroOff = kOnesDOff + kExt;
-  static constexpr int kBarOff = kZeroOff + kExt;
-  static constexpr int kNumBars = 2 * kSt1 + 2 * kSt2 + 2 + NS + 2 + 2 * NS + 2;
+  static constexpr int kFPanel = kT * 128;
+  static constexpr int kFTile = kPanels * kFPanel;
+  static constexpr int kYPanel = TN * 128;
+  static constexpr int kYTile = kPanels * kYPanel;
+  static constexpr int kSt1 = (D == 128 && !KV) ? 3 : 4;  // ring of Y1
+  static constexpr int kSt2 = (D == 128 && !KV) ? 2 : 4;  // ring of Y2
+  static constexpr int kY1Off = 2 * kFTile;
+  static constexpr int kY2Off = kY1Off + kSt1 * kYTile;
+  // columns beside the dK/dV pass's tiles, 16 bytes a row: lse beside Q, D beside g, ones beside K
+  // and V, and zeros, the second eight columns of all of them
+  static constexpr int kExt = KV ? TN * 16 : 0;
+  static constexpr int kOnes = KV ? kT * 16 : 0;
+  static constexpr int kExt1Off = kY2Off + kSt2 * kYTile;
+  static constexpr int kExt2Off = kExt1Off + kSt1 * kExt;
+  static constexpr int kOnesOff = kExt2Off + kSt2 * kExt;
+  static constexpr int kZeroOff = kOnesOff + kOnes;
+  static constexpr int kBarOff = kZeroOff + kOnes;
+  static constexpr int kNumBars = 2 * kSt1 + 2 * kSt2 + 4 + 4 * NS + 2 * ND + 2;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static constexpr uint32_t kAcc1 = KV ? D : 0;  // TMEM columns; acc0 at 0
   static constexpr uint32_t kS = kAcc1 + D;
-  static constexpr uint32_t kDP = kS + NS * 128;
-  static_assert(kDP + 128 <= 512, "TMEM budget");
+  static constexpr uint32_t kDP = kS + NS * TN;
+  static_assert(kDP + ND * TN <= 512, "TMEM budget");
   static constexpr int kThreads = 384;
-  static constexpr int kSoftRegs = 208, kCtlRegs = 80;  // as in the forward kernels: 63488 <= 384 * 168
 };
 
 // Extent of a unit: which Y tiles its F tile meets.
@@ -105,8 +113,8 @@ __device__ __forceinline__ Unit unit_of(const BackwardArgs& a, int b, int x) {
     long long hi = u.Sq;
     if (a.window > 0 && f0 >= a.n_sink) hi = min(hi, last + (long long)a.window - u.off);
     if (hi <= lo) return u;
-    u.t0 = (int)(lo / kT);
-    u.nt = (int)((hi + kT - 1) / kT) - u.t0;
+    u.t0 = (int)(lo / a.tn_k);
+    u.nt = (int)((hi + a.tn_k - 1) / a.tn_k) - u.t0;
   } else {
     if (f0 >= u.Sq) return u;
     const int last = min(u.Sq, f0 + kT) - 1;
@@ -228,7 +236,8 @@ __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __gri
   uint32_t l0, l1, l2, d0, d1, d2;
   split3(x, l0, l1, l2);
   split3(-s, d0, d1, d2);
-  a.ext[i] = make_uint4(l0 | l1 << 16, l2 | d0 << 16, d1 | d2 << 16, 0u);
+  a.ext1[i] = make_uint4(l0 | l1 << 16, l2, 0u, 0u);
+  a.ext2[i] = make_uint4(d0 | d1 << 16, d2, 0u, 0u);
 }
 
 // ------------------------------------------------------------------ the two passes
@@ -293,26 +302,27 @@ struct Walk {
 template <bool KV>
 struct ItemWalk {
   int h, t, row0;
+  __device__ __forceinline__ ItemWalk() : h(0), t(0), row0(0) {}
   __device__ __forceinline__ ItemWalk(const BackwardArgs& a, const Unit& u, int unit_head, int i) {
     if constexpr (KV) {
       const int q = i / u.nt;
       h = unit_head * (a.Hq / a.Hkv) + q;
       t = i - q * u.nt;
-      row0 = (u.t0 + t) * kT;
+      row0 = (u.t0 + t) * a.tn_k;
     } else {
       h = unit_head / (a.Hq / a.Hkv);
       t = i;
       row0 = tile_list_key(u.tl, t) * kT;
     }
   }
-  __device__ __forceinline__ void step(const Unit& u) {
+  __device__ __forceinline__ void step(const BackwardArgs& a, const Unit& u) {
     ++t;
     if constexpr (KV) {
       if (t == u.nt) {
         t = 0;
         ++h;
       }
-      row0 = (u.t0 + t) * kT;
+      row0 = (u.t0 + t) * a.tn_k;
     } else {
       row0 = tile_list_key(u.tl, t) * kT;
     }
@@ -331,40 +341,86 @@ __device__ __forceinline__ void keep_bits(uint32_t* t, uint32_t in) {
   }
 }
 
+// 8 columns of 4 rows, one row a lane (unit c: columns 8 c ..), to one column unit a lane: lane i of
+// four gets unit i of each row.
+__device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
+#pragma unroll
+  for (int k = 1; k <= 2; ++k) {
+    const bool up = lane & k;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & k) continue;
+      uint4 &lo = u[c], &hi = u[c | k];
+      uint4 x = up ? lo : hi;  // what goes to the lane k away
+      x.x = __shfl_xor_sync(0xFFFFFFFFu, x.x, k);
+      x.y = __shfl_xor_sync(0xFFFFFFFFu, x.y, k);
+      x.z = __shfl_xor_sync(0xFFFFFFFFu, x.z, k);
+      x.w = __shfl_xor_sync(0xFFFFFFFFu, x.w, k);
+      if (up) lo = x;
+      else hi = x;
+    }
+  }
+}
+
+// A ring of Y tiles and the items it still has to bring.
+template <bool KV>
+struct Stream {
+  Walk<KV> w;
+  ItemWalk<KV> y;
+  int h, i0, n, m, it;
+  bool live;
+  __device__ __forceinline__ Stream(const BackwardArgs& a, const Walk<KV>& w_) : w(w_), y(), m(0), it(0) {
+    live = w.next(h, i0, n);
+    if (live) y = ItemWalk<KV>(a, w.u, h, i0);
+  }
+  __device__ __forceinline__ void step(const BackwardArgs& a) {
+    ++it;
+    if (++m < n) {
+      y.step(a, w.u);
+      return;
+    }
+    m = 0;
+    live = w.next(h, i0, n);
+    if (live) y = ItemWalk<KV>(a, w.u, h, i0);
+  }
+};
+
 template <int D, bool KV>
 __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
     backward_kernel(const __grid_constant__ BackwardArgs a) {
   using C = BwdCfg<D, KV>;
-  constexpr int NS = C::NS;
+  constexpr int NS = C::NS, ND = C::ND, TN = C::TN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const CUtensorMap &tm_f1 = KV ? a.tm_k : a.tm_q, &tm_f2 = KV ? a.tm_v : a.tm_do;
-  const CUtensorMap &tm_y1 = KV ? a.tm_q : a.tm_k, &tm_y2 = KV ? a.tm_do : a.tm_v;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full1 = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty1 = full1 + C::kSt1;
   uint64_t* full2 = empty1 + C::kSt1;
   uint64_t* empty2 = full2 + C::kSt2;
-  uint64_t* fullF = empty2 + C::kSt2;
-  uint64_t* emptyF = fullF + 1;
-  uint64_t* bar_S = emptyF + 1;        // [NS] S computed
-  uint64_t* bar_dP = bar_S + NS;       // dP computed
-  uint64_t* bar_dPr = bar_dP + 1;      // dP read
-  uint64_t* bar_P = bar_dPr + 1;       // [NS] P stored
+  uint64_t* fullF = empty2 + C::kSt2;  // [2] F tiles
+  uint64_t* emptyF = fullF + 2;
+  uint64_t* bar_S = emptyF + 2;        // [NS] S computed
+  uint64_t* bar_Sr = bar_S + NS;       // [NS] its P and dS used up
+  uint64_t* bar_P = bar_Sr + NS;       // [NS] P stored
   uint64_t* bar_dS = bar_P + NS;       // [NS] dS stored
-  uint64_t* bar_acc = bar_dS + NS;     // a run's sums complete
+  uint64_t* bar_dP = bar_dS + NS;      // [ND] dP computed
+  uint64_t* bar_dPr = bar_dP + ND;     // [ND] dP read
+  uint64_t* bar_acc = bar_dPr + ND;    // a run's sums complete
   uint64_t* bar_accr = bar_acc + 1;    // they are read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_accr + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kSt1; ++s) { mbar_init(&full1[s], 1); mbar_init(&empty1[s], 1); }
-    for (int s = 0; s < C::kSt2; ++s) { mbar_init(&full2[s], 1); mbar_init(&empty2[s], 1); }
-    mbar_init(fullF, 1);
-    mbar_init(emptyF, 1);
-    for (int s = 0; s < NS; ++s) { mbar_init(&bar_S[s], 1); mbar_init(&bar_P[s], 8); mbar_init(&bar_dS[s], 8); }
-    mbar_init(bar_dP, 1);
-    mbar_init(bar_dPr, 8);
+    for (int s = 0; s < C::kSt2; ++s) { mbar_init(&full2[s], 1); mbar_init(&empty2[s], KV ? 2 : 1); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&fullF[s], 1); mbar_init(&emptyF[s], 1); }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&bar_S[s], 1);
+      mbar_init(&bar_Sr[s], 1);
+      mbar_init(&bar_P[s], C::kArrive);
+      mbar_init(&bar_dS[s], C::kArrive);
+    }
+    for (int s = 0; s < ND; ++s) { mbar_init(&bar_dP[s], 1); mbar_init(&bar_dPr[s], C::kArrive); }
     mbar_init(bar_acc, 1);
     mbar_init(bar_accr, 8);
     *abort_flag = 0;
@@ -375,9 +431,8 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
     tmem_relinquish();
   }
   if constexpr (KV) {
-    for (int i = threadIdx.x; i < kT; i += C::kThreads) {  // row i: columns 0-2, 3-5, none
-      *reinterpret_cast<uint4*>(smem + C::kOnesLOff + i * 16) = make_uint4(0x3F803F80u, 0x00003F80u, 0, 0);
-      *reinterpret_cast<uint4*>(smem + C::kOnesDOff + i * 16) = make_uint4(0, 0x3F800000u, 0x3F803F80u, 0);
+    for (int i = threadIdx.x; i < kT; i += C::kThreads) {
+      *reinterpret_cast<uint4*>(smem + C::kOnesOff + i * 16) = make_uint4(0x3F803F80u, 0x00003F80u, 0, 0);
       *reinterpret_cast<uint4*>(smem + C::kZeroOff + i * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
@@ -389,219 +444,185 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
 
   Walk<KV> w(a, lane);
   int h, i0, n;
-  if (warp >= 8) {
-    setmaxnreg_dec<C::kCtlRegs>();
-    if (warp == 9 || warp == 10) {
-      // ---- rings of Y1 (warp 9, with the lse and D columns) and Y2 (warp 10) ----
-      const bool first = warp == 9;
-      const CUtensorMap* map = first ? &tm_y1 : &tm_y2;
-      uint64_t* full = first ? full1 : full2;
-      uint64_t* empty = first ? empty1 : empty2;
-      const int stages = first ? C::kSt1 : C::kSt2;
-      uint8_t* ring = smem + (first ? C::kY1Off : C::kY2Off);
-      const uint16_t* base = KV ? (first ? a.q : a.dout) : (first ? a.k : a.v);
-      const int Hy = KV ? a.Hq : a.Hkv;
-      if (lane == 0) tma_prefetch_desc(map);
-      int it = 0;
-      bool ok = true;
-      while (ok && w.next(h, i0, n)) {
-        ItemWalk<KV> y(a, w.u, h, i0);
-        const int rows = KV ? w.u.Sq : w.u.Skv;        // Y rows of the sequence
-        const bool slab = KV ? a.cu_q != nullptr : a.kv_lens != nullptr;  // other rows may follow them
-        const int row_base = KV ? w.u.qbase : w.u.kbase;
-        for (int m = 0; m < n; ++m, ++it, y.step(w.u)) {
-          const int s = it % stages;
-          ok = mbar_wait_warp(&empty[s], ((uint32_t)(it / stages) & 1u) ^ 1u, a.err, abort_flag);
+  if (warp == 8 || warp == 9) {
+    // ---- first products: S = F1 Y1^T (warp 8), dP = F2 Y2^T (warp 9), and their F tiles ----
+    constexpr uint32_t idesc = idesc_bf16_f32(128, TN, 0, 0);
+    const bool first = warp == 8;
+    const CUtensorMap* map = KV ? (first ? &a.tm_k : &a.tm_v) : (first ? &a.tm_q : &a.tm_do);
+    uint8_t* sF = smem + (first ? 0 : C::kFTile);
+    uint64_t *fF = fullF + (first ? 0 : 1), *eF = emptyF + (first ? 0 : 1);
+    uint64_t* full = first ? full1 : full2;
+    uint64_t *done = first ? bar_S : bar_dP, *freed = first ? bar_Sr : bar_dPr;
+    const int stages = first ? C::kSt1 : C::kSt2, bufs = first ? NS : ND;
+    const uint64_t df = smem_desc(smem_u32(sF), 16, 1024, kSwizzle128B);
+    const uint64_t dy = smem_desc(smem_u32(smem + (first ? C::kY1Off : C::kY2Off)), 16, 1024, kSwizzle128B);
+    const uint32_t out = tmem + (first ? C::kS : C::kDP);
+    const uint32_t ext = smem_u32(smem + (first ? C::kExt1Off : C::kExt2Off)), zero = smem_u32(smem + C::kZeroOff);
+    const uint64_t d1 = smem_desc(smem_u32(smem + C::kOnesOff), C::kOnes, 128, kSwizzleNone);
+    if (lane == 0) tma_prefetch_desc(map);
+    int it = 0, run = 0;
+    bool ok = true;
+    while (ok && w.next(h, i0, n)) {
+      if (!mbar_wait_warp(eF, ((uint32_t)run & 1u) ^ 1u, a.err, abort_flag)) break;
+      const bool packed = !KV && a.cu_q != nullptr;
+      mbar_arrive_expect_tx_e(fF, C::kFTile);
+      tma_load_5d_e(sF, map, fF, 0, packed ? w.u.qbase + w.x * kT : w.x * kT, 0, h, packed ? 0 : w.b);
+      ok = mbar_wait_warp(fF, (uint32_t)run & 1u, a.err, abort_flag);
+      for (int m = 0; ok && m < n; ++m, ++it) {
+        const int s = it % stages, buf = it % bufs;
+        const uint32_t ph_f = (uint32_t)(it / stages) & 1u, ph_b = ((uint32_t)(it / bufs) & 1u) ^ 1u;
+        // both at once, one by one only where they are not ready
+        const bool r0 = mbar_test(&full[s], ph_f), r1 = mbar_test(&freed[buf], ph_b);
+        if (!__all_sync(0xFFFFFFFFu, r0 & r1)) {
+          ok = mbar_wait_warp(&freed[buf], ph_b, a.err, abort_flag) &&
+               mbar_wait_warp(&full[s], ph_f, a.err, abort_flag);
           if (!ok) break;
-          uint8_t* dst = ring + s * C::kTile;
-          uint32_t bytes = 0;
-          const bool whole = !slab || y.row0 + kT <= rows;
-          if (!whole) {
-            // a sequence's last rows: gathered, so that the rows behind them arrive as zeros
-            // (a weight of zero times what lies there could be NaN)
-            int ri[kT / 32];
-#pragma unroll
-            for (int k = 0; k < kT / 32; ++k) {
-              const int r = y.row0 + k * 32 + lane;
-              ri[k] = r < rows ? row_base + r : -1;
-            }
-            paged_gather<D, kT / 32>(smem_u32(dst), C::kPanel, base, Hy, y.h, lane, ri);
-            cp_async_commit();
-            cp_async_wait<0>();
-            fence_proxy_async_smem();
-            __syncwarp();
-          } else {
-            bytes = C::kTile;
-          }
-          if (KV && first) bytes += C::kExt;
-          if (bytes) mbar_arrive_expect_tx_e(&full[s], bytes);
-          else if (lane == 0) mbar_arrive(&full[s]);
-          if (whole) {
-#pragma unroll
-            for (int p = 0; p < C::kPanels; ++p) {
-              if (slab && KV) tma_load_4d_e(dst + p * C::kPanel, map, &full[s], p * 64, y.h, row_base + y.row0, 0);
-              else tma_load_4d_e(dst + p * C::kPanel, map, &full[s], p * 64, y.h, y.row0, w.b);
-            }
-          }
-          if (KV && first) {
-            const size_t i = a.cu_q ? (size_t)y.h * a.total_q + row_base + y.row0
-                                    : ((size_t)w.b * a.Hq + y.h) * a.Sq + y.row0;
-            bulk_load_e(smem + C::kExtOff + s * C::kExt, a.ext + i, C::kExt, &full[s]);
-          }
         }
-      }
-      if (!ok)  // aborted: the copies in flight land before shared memory is released
-        for (int v = max(0, it - stages); v < it; ++v)
-          mbar_wait(&full[v % stages], (uint32_t)(v / stages) & 1u, nullptr, nullptr, 100000000ull);
-    } else if (warp == 11) {
-      // ---- F tiles of the runs ----
-      if (lane == 0) {
-        tma_prefetch_desc(&tm_f1);
-        tma_prefetch_desc(&tm_f2);
-      }
-      int run = 0;
-      bool ok = true;
-      while (ok && w.next(h, i0, n)) {
-        ok = mbar_wait_warp(emptyF, ((uint32_t)run & 1u) ^ 1u, a.err, abort_flag);
-        if (!ok) break;
-        mbar_arrive_expect_tx_e(fullF, 2 * C::kTile);
-        const bool packed = !KV && a.cu_q != nullptr;
-        const int row = packed ? w.u.qbase + w.x * kT : w.x * kT, bb = packed ? 0 : w.b;
-#pragma unroll
-        for (int p = 0; p < C::kPanels; ++p) {
-          tma_load_4d_e(smem + p * C::kPanel, &tm_f1, fullF, p * 64, h, row, bb);
-          tma_load_4d_e(smem + C::kTile + p * C::kPanel, &tm_f2, fullF, p * 64, h, row, bb);
-        }
-        ++run;
-      }
-      if (!ok && run > 0) mbar_wait(fullF, (uint32_t)(run - 1) & 1u, nullptr, nullptr, 100000000ull);
-    } else {
-      // ---- MMA issue ----
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, kT, 0, 0);
-      constexpr uint32_t idesc_a = idesc_bf16_f32(128, D, 0, 1);
-      const uint64_t df1 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-      const uint64_t df2 = smem_desc(smem_u32(smem + C::kTile), 16, 1024, kSwizzle128B);
-      const uint64_t dy1 = smem_desc(smem_u32(smem + C::kY1Off), 16, 1024, kSwizzle128B);
-      const uint64_t dy2 = smem_desc(smem_u32(smem + C::kY2Off), 16, 1024, kSwizzle128B);
-      const uint64_t my1 = smem_desc(smem_u32(smem + C::kY1Off), C::kPanel, 1024, kSwizzle128B);
-      const uint64_t my2 = smem_desc(smem_u32(smem + C::kY2Off), C::kPanel, 1024, kSwizzle128B);
-      // the two products' first halves run one item ahead of the second ones: `ahead` walks
-      // the slice in front of w
-      Walk<KV> ahead = w;
-      int ah, ai0, an = 0, am = 0, arun = -1, ait = 0;  // item ait, the am-th of its run's an
-      bool ok = true, more = true;
-      auto advance = [&] {  // to the next item of `ahead`
-        ++am;
-        if (am >= an) {
-          more = ahead.next(ah, ai0, an);
-          am = 0;
-          ++arun;
-        }
-      };
-      auto issue_s = [&]() -> bool {  // S of item ait
-        const int s = ait % C::kSt1;
-        if (am == 0 && !mbar_wait_warp(fullF, (uint32_t)arun & 1u, a.err, abort_flag)) return false;
-        if (!mbar_wait_warp(&full1[s], (uint32_t)(ait / C::kSt1) & 1u, a.err, abort_flag)) return false;
         tc_fence_after();
-        const uint64_t y = dy1 + (uint64_t)((s * C::kTile) >> 4);
-        const uint32_t d = tmem + C::kS + (ait % NS) * 128;
+        const uint64_t y = dy + (uint64_t)((s * C::kYTile) >> 4);
+        const uint32_t d = out + buf * TN;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t o = (uint64_t)(((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4);
-          mma_ss_e(d, df1 + o, y + o, idesc_s, kk > 0 ? 1u : 0u);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss_e(d, df + (uint64_t)(((kk >> 2) * C::kFPanel + (kk & 3) * 32) >> 4),
+                   y + (uint64_t)(((kk >> 2) * C::kYPanel + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
         if constexpr (KV) {
-          const uint32_t e = smem_u32(smem + C::kExtOff + s * C::kExt);
-          const uint32_t z = smem_u32(smem + C::kZeroOff), l = smem_u32(smem + C::kOnesLOff);
-          mma_ss_e(d, smem_desc(l, z - l, 128, kSwizzleNone), smem_desc(e, z - e, 128, kSwizzleNone), idesc_s, 1u);
+          const uint32_t e = ext + s * C::kExt;
+          mma_ss_e(d, d1, smem_desc(e, zero - e, 128, kSwizzleNone), idesc, 1u);
         }
-        mma_commit_e(&bar_S[ait % NS]);
-        return true;
-      };
-      auto issue_dp = [&]() -> bool {  // dP of item ait (its F tiles and, KV, its Y1 slot have been waited for)
-        const int s = ait % C::kSt2, s1 = ait % C::kSt1;
-        if (KV && NS == 1) {  // here dP runs ahead of S
-          if (am == 0 && !mbar_wait_warp(fullF, (uint32_t)arun & 1u, a.err, abort_flag)) return false;
-          if (!mbar_wait_warp(&full1[s1], (uint32_t)(ait / C::kSt1) & 1u, a.err, abort_flag)) return false;
-        }
-        if (!mbar_wait_warp(&full2[s], (uint32_t)(ait / C::kSt2) & 1u, a.err, abort_flag)) return false;
-        if (ait > 0 && !mbar_wait_warp(bar_dPr, (uint32_t)(ait - 1) & 1u, a.err, abort_flag)) return false;
-        tc_fence_after();
-        const uint64_t y = dy2 + (uint64_t)((s * C::kTile) >> 4);
-        const uint32_t d = tmem + C::kDP;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t o = (uint64_t)(((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4);
-          mma_ss_e(d, df2 + o, y + o, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        if constexpr (KV) {
-          const uint32_t e = smem_u32(smem + C::kExtOff + s1 * C::kExt);
-          const uint32_t z = smem_u32(smem + C::kZeroOff), l = smem_u32(smem + C::kOnesDOff);
-          mma_ss_e(d, smem_desc(l, z - l, 128, kSwizzleNone), smem_desc(e, z - e, 128, kSwizzleNone), idesc_s, 1u);
-        }
-        mma_commit_e(bar_dP);
-        if constexpr (!KV) mma_commit_e(&empty2[s]);
-        return true;
-      };
-      // acc (+)= A (TMEM, 64 columns of bf16 pairs in two halves) * Y (MN-major)
-      auto issue_acc = [&](uint32_t acc, uint32_t p, uint64_t y, bool fresh) {
-#pragma unroll
-        for (int kk = 0; kk < kT / 16; ++kk)
-          mma_ts_e(tmem + acc, p + (kk >> 2) * 64 + (kk & 3) * 8, y + (uint64_t)(kk * (2048 >> 4)), idesc_a,
-                   (!fresh || kk > 0) ? 1u : 0u);
-      };
-      am = an = 0;
-      more = ahead.next(ah, ai0, an);
-      arun = 0;
-      if (more) {
-        ok = issue_s() && issue_dp();
-        if (ok && am == an - 1) mma_commit_e(emptyF);
+        mma_commit_e(&done[buf]);
+        if (!first) mma_commit_e(&empty2[s]);
+        if (m == n - 1) mma_commit_e(eF);
       }
-      int it = 0, run = 0;
-      while (ok && w.next(h, i0, n)) {
-        for (int m = 0; ok && m < n; ++m, ++it) {
-          const int buf = it % NS, s1 = it % C::kSt1, s2 = it % C::kSt2;
-          const uint32_t sb = tmem + C::kS + buf * 128, ph = (uint32_t)(it / NS) & 1u;
-          advance();
-          ++ait;
-          // the next item's first products, under this one's softmax; those of another unit
-          // (whose F tiles are still on their way) after this one's second products
-          const bool early = more && am > 0;
-          if (early) {
-            if (NS > 1) ok = issue_s();
-            if (ok) ok = issue_dp();
-            if (NS > 1 && ok && am == an - 1) mma_commit_e(emptyF);
-          }
-          if (ok && m == 0 && run > 0) ok = mbar_wait_warp(bar_accr, (uint32_t)(run - 1) & 1u, a.err, abort_flag);
-          if constexpr (KV) {
-            ok = ok && mbar_wait_warp(&bar_P[buf], ph, a.err, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            issue_acc(0, sb, my2 + (uint64_t)((s2 * C::kTile) >> 4), m == 0);
-            mma_commit_e(&empty2[s2]);
-          }
-          ok = ok && mbar_wait_warp(&bar_dS[buf], ph, a.err, abort_flag);
+      ++run;
+    }
+    // (aborted: the last copy lands before shared memory is released)
+    if (!ok && run > 0) mbar_wait(fF, (uint32_t)(run - 1) & 1u, nullptr, nullptr, 100000000ull);
+  } else if (warp == 10) {
+    // ---- second products: acc0 += P Y2 (dV), acc1 += dS Y1 ----
+    constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
+    const uint64_t my1 = smem_desc(smem_u32(smem + C::kY1Off), C::kYPanel, 1024, kSwizzle128B);
+    const uint64_t my2 = smem_desc(smem_u32(smem + C::kY2Off), C::kYPanel, 1024, kSwizzle128B);
+    // A in TMEM: 32 columns of bf16 pairs for each 64 columns of S; Y MN-major
+    auto issue = [&](uint32_t acc, uint32_t p, uint64_t y, bool fresh) {
+#pragma unroll
+      for (int kk = 0; kk < TN / 16; ++kk)
+        mma_ts_e(tmem + acc, p + (kk >> 2) * 64 + (kk & 3) * 8, y + (uint64_t)(kk * (2048 >> 4)), idesc,
+                 (!fresh || kk > 0) ? 1u : 0u);
+    };
+    int it = 0, run = 0;
+    bool ok = true;
+    while (ok && w.next(h, i0, n)) {
+      if (run > 0) ok = mbar_wait_warp(bar_accr, (uint32_t)(run - 1) & 1u, a.err, abort_flag);
+      for (int m = 0; ok && m < n; ++m, ++it) {
+        const int buf = it % NS, s1 = it % C::kSt1, s2 = it % C::kSt2;
+        const uint32_t sb = tmem + C::kS + buf * TN, ph = (uint32_t)(it / NS) & 1u;
+        if constexpr (KV) {
+          // (g's tile is whole where its dP is waited for: the softmax stores P before)
+          ok = mbar_wait_warp(&full2[s2], (uint32_t)(it / C::kSt2) & 1u, a.err, abort_flag) &&
+               mbar_wait_warp(&bar_P[buf], ph, a.err, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          issue_acc(C::kAcc1, sb + (KV ? 32 : 0), my1 + (uint64_t)((s1 * C::kTile) >> 4), m == 0);
-          mma_commit_e(&empty1[s1]);
-          if (m == n - 1) mma_commit_e(bar_acc);
-          if (early ? NS == 1 : more) {
-            ok = issue_s();
-            if (ok && !early) ok = issue_dp();
-            if (ok && am == an - 1) mma_commit_e(emptyF);
-          }
+          issue(0, sb, my2 + (uint64_t)((s2 * C::kYTile) >> 4), m == 0);
+          mma_commit_e(&empty2[s2]);
         }
-        ++run;
+        ok = mbar_wait_warp(&bar_dS[buf], ph, a.err, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        issue(C::kAcc1, sb + (KV ? 32 : 0), my1 + (uint64_t)((s1 * C::kYTile) >> 4), m == 0);
+        mma_commit_e(&bar_Sr[buf]);
+        mma_commit_e(&empty1[s1]);
+        if (m == n - 1) mma_commit_e(bar_acc);
+      }
+      ++run;
+    }
+  } else if (warp == 11) {
+    // ---- the rings of Y1 and Y2, each slot filled as soon as it is free ----
+    Stream<KV> st[2] = {Stream<KV>(a, w), Stream<KV>(a, w)};
+    if (lane == 0) {
+      tma_prefetch_desc(KV ? &a.tm_qy : &a.tm_k);
+      tma_prefetch_desc(KV ? &a.tm_doy : &a.tm_v);
+    }
+    bool ok = true;
+    long long t0 = clock64();
+    uint32_t idle = 0;
+    while (ok && (st[0].live || st[1].live)) {
+      bool moved = false;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        Stream<KV>& t = st[k];
+        if (!t.live) continue;
+        const int stages = k == 0 ? C::kSt1 : C::kSt2, s = t.it % stages;
+        uint64_t *full = k == 0 ? full1 : full2, *empty = k == 0 ? empty1 : empty2;
+        if (!mbar_test_warp(&empty[s], ((uint32_t)(t.it / stages) & 1u) ^ 1u)) continue;
+        moved = true;
+        const Unit& u = t.w.u;
+        const CUtensorMap* map = KV ? (k == 0 ? &a.tm_qy : &a.tm_doy) : (k == 0 ? &a.tm_k : &a.tm_v);
+        uint8_t* dst = smem + (k == 0 ? C::kY1Off : C::kY2Off) + s * C::kYTile;
+        const int rows = KV ? u.Sq : u.Skv;  // Y rows of the sequence
+        const int row_base = KV ? u.qbase : u.kbase;
+        // a packed batch: other rows follow a sequence's own
+        const bool whole = a.cu_q == nullptr || t.y.row0 + TN <= rows;
+        uint32_t bytes = KV ? C::kExt : 0;
+        if (whole) {
+          bytes += C::kYTile;
+        } else {
+          // its last rows are gathered, so that the rows behind them arrive as zeros (a weight of
+          // zero times what lies there could be NaN)
+          const uint16_t* base = KV ? (k == 0 ? a.q : a.dout) : (k == 0 ? a.k : a.v);
+          int ri[TN / 32];
+#pragma unroll
+          for (int e = 0; e < TN / 32; ++e) {
+            const int r = t.y.row0 + e * 32 + lane;
+            ri[e] = r < rows ? row_base + r : -1;
+          }
+          paged_gather<D, TN / 32>(smem_u32(dst), C::kYPanel, base, KV ? a.Hq : a.Hkv, t.y.h, lane, ri);
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (bytes) mbar_arrive_expect_tx_e(&full[s], bytes);
+        else if (lane == 0) mbar_arrive(&full[s]);
+        if (whole) {
+          if (KV && a.cu_q) tma_load_5d_e(dst, map, &full[s], 0, row_base + t.y.row0, 0, t.y.h, 0);
+          else tma_load_5d_e(dst, map, &full[s], 0, t.y.row0, 0, t.y.h, t.w.b);
+        }
+        if constexpr (KV) {
+          const size_t i = a.cu_q ? (size_t)t.y.h * a.total_q + row_base + t.y.row0
+                                  : ((size_t)t.w.b * a.Hq + t.y.h) * a.Sq + t.y.row0;
+          bulk_load_e(smem + (k == 0 ? C::kExt1Off : C::kExt2Off) + s * C::kExt, (k == 0 ? a.ext1 : a.ext2) + i,
+                      C::kExt, &full[s]);
+        }
+        t.step(a);
+      }
+      if (moved) {
+        idle = 0;
+        t0 = clock64();
+      } else if ((++idle & 63u) == 0) {  // bounded, as every wait here
+        bool out = *abort_flag != 0;
+        if (!out && clock64() - t0 > (long long)(ATTN_WAIT_LIMIT_NS * kMaxSmClockGHz)) {
+          atomicCAS(a.err, kErrNone, kErrWaitTimeout);
+          *abort_flag = 1;
+          out = true;
+        }
+        ok = !__any_sync(0xFFFFFFFFu, out);
+      }
+    }
+    if (!ok) {  // aborted: the copies in flight land before shared memory is released
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int stages = k == 0 ? C::kSt1 : C::kSt2;
+        for (int v = max(0, st[k].it - stages); v < st[k].it; ++v)
+          mbar_wait(&(k == 0 ? full1 : full2)[v % stages], (uint32_t)(v / stages) & 1u, nullptr, nullptr, 100000000ull);
       }
     }
   } else {
-    setmaxnreg_inc<C::kSoftRegs>();
     // ---- softmax: P and dS ----
     const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sl2 = a.scale * kLog2e;
     const uint64_t sl2x2 = f2pack(sl2, sl2);
+    const int c0 = TN == 128 ? wg * 64 : 0;  // this thread's columns of an item: c0 .. c0 + 63
     int it = 0, run = 0;
     bool ok = true;
     while (ok && w.next(h, i0, n)) {
@@ -618,71 +639,49 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
       }
       const uint64_t nlse2 = f2pack(-lse2, -lse2), ndd = f2pack(-dd, -dd);
       ItemWalk<KV> y(a, w.u, h, i0);
-      for (int m = 0; m < n; ++m, ++it, y.step(w.u)) {
-        const int buf = it % NS;
-        const uint32_t sc = lanes + C::kS + buf * 128 + wg * 64;
+      for (int m = 0; m < n; ++m, ++it, y.step(a, w.u)) {
+        if (TN == 64 && (it & 1) != wg) continue;  // the other warpgroup's
+        const int buf = it % NS, bd = it % ND;
+        const uint32_t sc = lanes + C::kS + buf * TN + c0, dc = lanes + C::kDP + bd * TN + c0;
         ok = mbar_wait_warp(&bar_S[buf], (uint32_t)(it / NS) & 1u, a.err, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[64], p[64];
+        uint32_t s[64];
         tmem_ld32(sc, s);
         tmem_ld32(sc + 32, s + 32);
-        ok = mbar_wait_warp(bar_dP, (uint32_t)it & 1u, a.err, abort_flag);
-        if (!ok) {
-          tmem_wait_ld();
-          break;
-        }
-        tc_fence_after();
-        tmem_ld32(lanes + C::kDP + wg * 64, p);
-        tmem_ld32(lanes + C::kDP + wg * 64 + 32, p + 32);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_dPr);
         // columns of this thread's row: [lo, hi) and, dQ pass, those before `sink`
-        int lo = 0, hi = kT, sink = 0;
+        int lo = 0, hi = TN, sink = 0;
         bool mask;
-        const int c0 = wg * 64;
         if constexpr (KV) {
           const long long d0 = w.u.off + y.row0;  // key index of the tile's first row
           const int j = f0 + r;
-          mask = y.row0 + kT > w.u.Sq;
-          hi = min(kT, w.u.Sq - y.row0);
+          mask = y.row0 + TN > w.u.Sq;
+          hi = min(TN, w.u.Sq - y.row0);
           if (a.causal) {
             mask = mask || f0 + kT - 1 > d0;
-            lo = (int)min((long long)kT, max(0LL, j - d0));
+            lo = (int)min((long long)TN, max(0LL, j - d0));
           }
           if (a.window > 0) {
-            mask = mask || f0 + (long long)a.window < d0 + kT;
+            mask = mask || f0 + (long long)a.window < d0 + TN;
             if (j >= a.n_sink) hi = (int)min((long long)hi, max(0LL, j + (long long)a.window - d0));
           }
         } else {
           const long long pos = f0 + r + w.u.off;  // key index of this row
           const long long p0 = f0 + w.u.off;
-          mask = y.row0 + kT > w.u.Skv;
-          hi = min(kT, w.u.Skv - y.row0);
+          mask = y.row0 + TN > w.u.Skv;
+          hi = min(TN, w.u.Skv - y.row0);
           if (a.causal) {
-            mask = mask || y.row0 + kT - 1 > p0;
+            mask = mask || y.row0 + TN - 1 > p0;
             hi = (int)min((long long)hi, max(0LL, pos + 1 - y.row0));
           }
           if (a.window > 0) {
             mask = mask || y.row0 <= p0 + kT - 1 - a.window;
-            lo = (int)min((long long)kT, max(0LL, pos - a.window + 1 - y.row0));
-            sink = min(kT, max(0, a.n_sink - y.row0));
+            lo = (int)min((long long)TN, max(0LL, pos - a.window + 1 - y.row0));
+            sink = min(TN, max(0, a.n_sink - y.row0));
           }
         }
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const uint64_t x = f2pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          float e0, e1;
-          f2unpack(KV ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
-          e0 = ex2_approx(e0);
-          e1 = ex2_approx(e1);
-          s[c] = __float_as_uint(e0);
-          s[c + 1] = __float_as_uint(e1);
-        }
-        // this thread's columns as bits (a weight out of them may be inf, dP of a column that is no
-        // row anything: both products' operands are cleared after their rounding)
+        // as bits (a weight out of them may be inf, dP of a column that is no row anything: both
+        // products' operands are cleared after their rounding)
         uint32_t in[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
         if (mask) {
 #pragma unroll
@@ -690,6 +689,15 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
             const int c1 = c0 + q * 32;
             in[q] = (bits_below(hi - c1) & ~bits_below(lo - c1)) | bits_below(min(sink, hi) - c1);
           }
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const uint64_t x = f2pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          float e0, e1;
+          f2unpack(KV ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
+          s[c] = __float_as_uint(ex2_approx(e0));
+          s[c + 1] = __float_as_uint(ex2_approx(e1));
         }
         if constexpr (KV) {
 #pragma unroll
@@ -706,20 +714,31 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_P[buf]);
         }
-        uint32_t t[32];
+        ok = mbar_wait_warp(&bar_dP[bd], (uint32_t)(it / ND) & 1u, a.err, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t p[64];
+        tmem_ld32(dc, p);
+        tmem_ld32(dc + 32, p + 32);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_dPr[bd]);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          uint64_t g = f2pack(__uint_as_float(p[2 * c]), __uint_as_float(p[2 * c + 1]));
-          if constexpr (!KV) g = add2(g, ndd);
-          float x0, x1;
-          f2unpack(mul2(g, f2pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]))), x0, x1);
-          t[c] = pack_bf16x2(x0, x1);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t t[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int k = q * 32 + 2 * c;
+            uint64_t g = f2pack(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
+            if constexpr (!KV) g = add2(g, ndd);
+            float x0, x1;
+            f2unpack(mul2(g, f2pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1]))), x0, x1);
+            t[c] = pack_bf16x2(x0, x1);
+          }
+          if (mask) keep_bits<16>(t, in[q]);
+          tmem_st16(sc + (KV ? 32 : 0) + q * 16, t);
         }
-        if (mask) {
-          keep_bits<16>(t, in[0]);
-          keep_bits<16>(t + 16, in[1]);
-        }
-        tmem_st32(sc + (KV ? 32 : 0), t);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -735,14 +754,17 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
       constexpr int kCols = KV ? D : D / 2;
       const uint32_t col0 = KV ? (wg == 0 ? 0 : C::kAcc1) : C::kAcc1 + wg * kCols;
       const float f = (KV && wg == 0) ? 1.f : a.scale;
-      const int row = f0 + r;
-      uint16_t* out = nullptr;
-      bool live = true;
+      // rows [0, live) are the sequence's, [live, wrote) written as zeros
+      const int live = min(kT, (KV ? w.u.Skv : w.u.Sq) - f0);
+      const int wrote = KV && a.fill ? min(kT, a.Skv - f0) : live;
+      uint16_t* out;
+      size_t row_w;  // elements from row to row
       if constexpr (KV) {
-        if (row < (a.fill ? a.Skv : w.u.Skv)) out = (wg == 0 ? a.dv : a.dk) + (((size_t)w.b * a.Skv + row) * a.Hkv + h) * D;
-        live = row < w.u.Skv;
-      } else if (row < w.u.Sq) {
-        out = a.dq + ((size_t)(w.u.qbase + row) * a.Hq + h) * D + wg * kCols;
+        out = (wg == 0 ? a.dv : a.dk) + (((size_t)w.b * a.Skv + f0) * a.Hkv + h) * D;
+        row_w = (size_t)a.Hkv * D;
+      } else {
+        out = a.dq + ((size_t)(w.u.qbase + f0) * a.Hq + h) * D + wg * kCols;
+        row_w = (size_t)a.Hq * D;
       }
       float4* pp = reinterpret_cast<float4*>(KV ? a.part_k : a.part_q) +
                    ((size_t)blockIdx.x * 2 + (i0 > 0 ? 0 : 1)) * (kT * D * (KV ? 2 : 1) / 4) +
@@ -757,14 +779,24 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
           for (int e = 0; e < 32; e += 4)
             pp[(size_t)((c + e) / 4) * kT] = make_float4(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f,
                                                          __uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
-        } else if (out) {
+        } else {
+          // four lanes write 64 bytes of a row side by side: a row a lane made each store 32 lines
+          uint4 q[4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t q[4];
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t* x = v + e * 8;
+            q[e] = make_uint4(pack_bf16x2(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f),
+                              pack_bf16x2(__uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f),
+                              pack_bf16x2(__uint_as_float(x[4]) * f, __uint_as_float(x[5]) * f),
+                              pack_bf16x2(__uint_as_float(x[6]) * f, __uint_as_float(x[7]) * f));
+          }
+          transpose4(q, lane);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              q[k] = live ? pack_bf16x2(__uint_as_float(v[e + 2 * k]) * f, __uint_as_float(v[e + 2 * k + 1]) * f) : 0u;
-            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(q[0], q[1], q[2], q[3]);
+          for (int e = 0; e < 4; ++e) {
+            const int row = (r & ~3) + e;
+            if (row < wrote)
+              *reinterpret_cast<uint4*>(out + (size_t)row * row_w + c + (lane & 3) * 8) =
+                  row < live ? q[e] : make_uint4(0, 0, 0, 0);
           }
         }
       }
@@ -905,6 +937,8 @@ cudaError_t launch_d(const BackwardArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+int backward_tile_rows(int d) { return d == 64 ? BwdCfg<64, true>::TN : BwdCfg<128, true>::TN; }
 
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t stream) {
   switch (a.d) {
