@@ -29,8 +29,8 @@ int check_sizes(const Sizes& z) {
   if (z.d != 64 && z.d != 128) return ATTN_ERR_UNSUPPORTED;
   if (z.rows * z.Hq >= (1LL << 31) || (long long)z.B * z.Skv * z.Hkv >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
   if ((long long)z.Hq * z.d >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
-  // tiles of 64 x 128 of all heads (and some for each unit's start), which the kernels count in 32 bits
-  const long long tq = (z.Sq + 63LL) / 64, tk = (z.Skv + 127LL) / 128;
+  // tiles of 64 x 64 of all heads (more than there are, and some for each unit's start), which the kernels count in 32 bits
+  const long long tq = (z.Sq + 63LL) / 64, tk = (z.Skv + 63LL) / 64;
   if ((tq + 8) * z.B * (tk + 8) >= (1LL << 31) / z.Hq) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -85,13 +85,15 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   if (rows && keys && z.Sq > 0) {
     // packed rows are one batch slab
     const int ns = cu_q ? (int)z.rows : z.Sq, nb = cu_q ? 1 : z.B;
-    const int tn = attn::backward_tile_rows(z.d);
+    const int tk = attn::backward_tile_rows(z.d, true), tq = attn::backward_tile_rows(z.d, false);
     rc = attn::encode_panel_map(&a.tm_q, q, z.d, z.Hq, ns, nb, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_do, dout, z.d, z.Hq, ns, nb, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_k, k, z.d, z.Hkv, z.Skv, z.B, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_v, v, z.d, z.Hkv, z.Skv, z.B, 128);
-    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_qy, q, z.d, z.Hq, ns, nb, tn);
-    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_doy, dout, z.d, z.Hq, ns, nb, tn);
+    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_qy, q, z.d, z.Hq, ns, nb, tk);
+    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_doy, dout, z.d, z.Hq, ns, nb, tk);
+    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_ky, k, z.d, z.Hkv, z.Skv, z.B, tq);
+    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_vy, v, z.d, z.Hkv, z.Skv, z.B, tq);
     if (rc != ATTN_OK) return rc;
   }
   a.q = q; a.dout = dout; a.k = k; a.v = v; a.o = o; a.lse = lse; a.dlse = dlse;
@@ -108,7 +110,6 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   a.stat = reinterpret_cast<float2*>(w + l.stat);
   a.ext1 = reinterpret_cast<uint4*>(w + l.ext1);
   a.ext2 = reinterpret_cast<uint4*>(w + l.ext2);
-  a.tn_k = attn::backward_tile_rows(z.d);
   a.part_k = reinterpret_cast<float*>(w + l.part_k);
   a.part_q = reinterpret_cast<float*>(w + l.part_q);
   a.ctas_k = a.ctas_q = l.ctas;

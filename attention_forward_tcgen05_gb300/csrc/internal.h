@@ -208,7 +208,9 @@ struct EvictArgs {
 // [Hq][total_q], Sq the longest sequence, kv_lens set.  k, v, dk, dv [B][Skv][Hkv][d].
 struct BackwardArgs {
   CUtensorMap tm_q, tm_do, tm_k, tm_v;  // encode_panel_map, 128 rows
-  CUtensorMap tm_qy, tm_doy;            // tn_k rows
+  // The streamed tiles of the dK/dV pass (Q, dout) and of the dQ pass (K, V): the same with the
+  // rows of backward_tile_rows
+  CUtensorMap tm_qy, tm_doy, tm_ky, tm_vy;
   const uint16_t *q, *dout, *k, *v;
   const void* o;
   const float *lse, *dlse;              // dlse may be nullptr
@@ -223,9 +225,8 @@ struct BackwardArgs {
   uint4 *ext1, *ext2;                   // the same as bf16 columns of the dK/dV pass, 128 rows more
   float *part_k, *part_q;               // [ctas][2][accumulators * d / 4][128][4] sums of cut units
   int ctas_k, ctas_q;
-  int tn_k;                             // rows of a streamed tile of the dK/dV pass
 };
-int backward_tile_rows(int d);  // tn_k
+int backward_tile_rows(int d, bool dkdv);  // rows of a pass's streamed tiles
 
 // Rows of a K / V stage loaded by one TMA box in the decode kernel (two
 // consumer warps share a stage, 32 rows each).

@@ -51,40 +51,52 @@ constexpr int kT = 128;           // rows of a tile
 constexpr int kRunCost = 3;
 constexpr int kMinCost = 2 + kRunCost;  // of a slice
 
-// Columns of S and dP per item.  128, halved between the softmax warpgroups, where TMEM holds
-// two S and one dP beside the sums; the dK/dV pass at d = 128 has 256 columns for both: 64, two
-// buffers of each, an item for each warpgroup in turn.
+// TN: columns of S and dP per item.  64: the softmax warpgroups take an item each in turn, so that
+// one's loads and stores run under the other's exponentials; S, dP and the bf16 P and dS have columns
+// of their own, so that the next S waits for the softmax's load only.  128, halved between the
+// warpgroups (dQ pass, d = 128): a product of 64 columns re-reads as much of F for half of the work
+// (49 cycles a step, bound by shared memory, against 65 for 128 columns), which its one small
+// second product does not make up for; there dS lies over S, two S beside one dP.
 template <int D, bool KV>
 struct BwdCfg {
-  static constexpr int TN = (KV && D == 128) ? 64 : 128;  // rows of a Y tile
-  static constexpr int NS = 2;                            // S buffers
-  static constexpr int ND = TN == 64 ? 2 : 1;             // dP buffers
-  static constexpr int kArrive = TN == 64 ? 4 : 8;        // softmax warps of an item
+  static constexpr int TN = (D == 128 && !KV) ? 128 : 64;
+  // Rows of a Y tile: a copy takes 300 to 400 cycles of the copy engine whatever its size, so tiles of
+  // 64 rows of 64 columns would take longer to bring than to use.  kSub items a tile.
+  static constexpr int TY = (D == 128 && KV) ? 64 : 128;
+  static constexpr int kSub = TY / TN;
+  static constexpr bool kSep = TN == 64;                   // P and dS in columns of their own
+  static constexpr int NS = (D == 128 && KV) ? 1 : 2;      // S buffers
+  static constexpr int ND = D == 128 ? 1 : 2;              // dP buffers
+  static constexpr int kArrive = TN == 64 ? 4 : 8;         // softmax warps of an item
   static constexpr int kPanels = D / 64;
   static constexpr int kFPanel = kT * 128;
   static constexpr int kFTile = kPanels * kFPanel;
-  static constexpr int kYPanel = TN * 128;
+  static constexpr int kYPanel = TY * 128;
   static constexpr int kYTile = kPanels * kYPanel;
-  static constexpr int kSt1 = (D == 128 && !KV) ? 3 : 4;  // ring of Y1
-  static constexpr int kSt2 = (D == 128 && !KV) ? 2 : 4;  // ring of Y2
+  static constexpr int kSt1 = D == 64 ? 4 : (KV ? 5 : 3);  // ring of Y1
+  static constexpr int kSt2 = D == 64 ? 4 : (KV ? 4 : 2);  // ring of Y2
   static constexpr int kY1Off = 2 * kFTile;
   static constexpr int kY2Off = kY1Off + kSt1 * kYTile;
   // columns beside the dK/dV pass's tiles, 16 bytes a row: lse beside Q, D beside g, ones beside K
   // and V, and zeros, the second eight columns of all of them
-  static constexpr int kExt = KV ? TN * 16 : 0;
+  static constexpr int kExt = KV ? TY * 16 : 0;
+  static constexpr int kExtSlots = 4;
   static constexpr int kOnes = KV ? kT * 16 : 0;
   static constexpr int kExt1Off = kY2Off + kSt2 * kYTile;
-  static constexpr int kExt2Off = kExt1Off + kSt1 * kExt;
-  static constexpr int kOnesOff = kExt2Off + kSt2 * kExt;
+  static constexpr int kExt2Off = kExt1Off + kExtSlots * kExt;
+  static constexpr int kOnesOff = kExt2Off + kExtSlots * kExt;
   static constexpr int kZeroOff = kOnesOff + kOnes;
   static constexpr int kBarOff = kZeroOff + kOnes;
-  static constexpr int kNumBars = 2 * kSt1 + 2 * kSt2 + 4 + 4 * NS + 2 * ND + 2;
+  static constexpr int kNumBars = 2 * kSt1 + 2 * kSt2 + 4 + 2 + NS + 2 + ND + 4 + 2;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static constexpr uint32_t kAcc1 = KV ? D : 0;  // TMEM columns; acc0 at 0
   static constexpr uint32_t kS = kAcc1 + D;
   static constexpr uint32_t kDP = kS + NS * TN;
-  static_assert(kDP + ND * TN <= 512, "TMEM budget");
+  // P and dS of an item (two buffers): kP + buffer * kPStep
+  static constexpr uint32_t kP = kSep ? kDP + ND * TN : kS;
+  static constexpr uint32_t kPStep = kSep ? (KV ? 64 : 32) : TN;
+  static_assert(kP + 2 * kPStep <= 512 && kDP + ND * TN <= 512, "TMEM budget");
   static constexpr int kThreads = 384;
 };
 
@@ -95,7 +107,7 @@ struct Unit {
   int nt, t0;                 // Y tiles, dK/dV pass: from t0 on; dQ pass: by the tile list
   TileList tl;
 };
-template <bool KV>
+template <int TY, bool KV>
 __device__ __forceinline__ Unit unit_of(const BackwardArgs& a, int b, int x) {
   Unit u;
   const SeqExtent e = seq_extent(b, a.Sq, a.Skv, a.cu_q, a.kv_lens, a.total_q);
@@ -113,14 +125,14 @@ __device__ __forceinline__ Unit unit_of(const BackwardArgs& a, int b, int x) {
     long long hi = u.Sq;
     if (a.window > 0 && f0 >= a.n_sink) hi = min(hi, last + (long long)a.window - u.off);
     if (hi <= lo) return u;
-    u.t0 = (int)(lo / a.tn_k);
-    u.nt = (int)((hi + a.tn_k - 1) / a.tn_k) - u.t0;
+    u.t0 = (int)(lo / TY);
+    u.nt = (int)((hi + TY - 1) / TY) - u.t0;
   } else {
     if (f0 >= u.Sq) return u;
     const int last = min(u.Sq, f0 + kT) - 1;
     const long long hi = a.causal ? min((long long)u.Skv, max(0LL, last + u.off + 1)) : u.Skv;
-    const int n = (int)((hi + kT - 1) / kT);
-    u.tl = tile_list(f0 + u.off, n, a.window, a.n_sink, u.Skv, kT);
+    const int n = (int)((hi + TY - 1) / TY);
+    u.tl = tile_list(f0 + u.off, n, a.window, a.n_sink, u.Skv, TY);
     u.nt = tile_list_len(u.tl, n);
   }
   return u;
@@ -166,7 +178,7 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi, uint32_t& mid, uin
 }
 
 // Exclusive prefix of the groups' costs (all heads of a group) by one CTA; pre[n] the total.
-template <bool KV>
+template <int TY, bool KV>
 __device__ void scan_costs(const BackwardArgs& a, int* pre) {
   __shared__ int sums[kPrepThreads / 32];
   const int nx = f_tiles(a, KV), n = a.B * nx, H = KV ? a.Hkv : a.Hq;
@@ -179,7 +191,7 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
       const int c0 = min(max(a.cu_q[b], 0), a.total_q), c1 = min(a.cu_q[b + 1], a.total_q);
       if (c1 - c0 > a.Sq) atomicCAS(a.err, kErrNone, kErrBadShape);
     }
-  for (int g = lo; g < hi; ++g) s += unit_cost(unit_items<KV>(a, unit_of<KV>(a, g / nx, g % nx))) * H;
+  for (int g = lo; g < hi; ++g) s += unit_cost(unit_items<KV>(a, unit_of<TY, KV>(a, g / nx, g % nx))) * H;
   int incl = s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -193,7 +205,7 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
   for (int w = 0; w < warp; ++w) at += sums[w];
   for (int g = lo; g < hi; ++g) {
     pre[g] = at;
-    at += unit_cost(unit_items<KV>(a, unit_of<KV>(a, g / nx, g % nx))) * H;
+    at += unit_cost(unit_items<KV>(a, unit_of<TY, KV>(a, g / nx, g % nx))) * H;
   }
   if (hi == n && lo < n) pre[n] = at;
   if (n == 0 && threadIdx.x == 0) pre[0] = 0;
@@ -203,8 +215,8 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
 template <int D, bool OBF16>
 __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __grid_constant__ BackwardArgs a) {
   if (blockIdx.x < 2) {
-    if (blockIdx.x == 0) scan_costs<true>(a, a.pre_k);
-    else scan_costs<false>(a, a.pre_q);
+    if (blockIdx.x == 0) scan_costs<BwdCfg<D, true>::TY, true>(a, a.pre_k);
+    else scan_costs<BwdCfg<D, false>::TY, false>(a, a.pre_q);
     return;
   }
   constexpr int L = D / 8;
@@ -241,30 +253,32 @@ __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __gri
 }
 
 // ------------------------------------------------------------------ the two passes
+// A run: items [i0, i0 + n) of the unit of head h in group (b, x); n = 0: none.
+struct Run {
+  Unit u;
+  int b, x, h, i0, n, cnt;  // cnt: items of the unit
+};
 // The items of a slice in order, run by run of one unit.
-template <bool KV>
+template <int TY, bool KV>
 struct Walk {
   const BackwardArgs& a;
-  const int* pre;
-  int nx, n_groups, H, pos, end;  // place in the list of costs, end of the slice
-  int g, g0, cnt;                 // group, its place, items of one of its units
-  Unit u;
-  int b, x;
-  __device__ __forceinline__ Walk(const BackwardArgs& a_, int lane)
-      : a(a_), pre(KV ? a_.pre_k : a_.pre_q), H(KV ? a_.Hkv : a_.Hq) {
-    nx = f_tiles(a, KV);
-    n_groups = a.B * nx;
-    const int total = pre[n_groups], per = slice_cost(total, (int)gridDim.x);
+  int pos, end;  // place in the list of costs, end of the slice
+  int g, g0;     // group, its place
+  Run at;        // of the group: u, b, x, cnt
+  __device__ __forceinline__ const int* pre() const { return KV ? a.pre_k : a.pre_q; }
+  __device__ __forceinline__ Walk(const BackwardArgs& a_, int lane) : a(a_) {
+    const int n_groups = a.B * f_tiles(a, KV);
+    const int total = pre()[n_groups], per = slice_cost(total, (int)gridDim.x);
     pos = (int)min((long long)total, (long long)blockIdx.x * per);
     end = min(total, pos + per);
-    g = 0; g0 = 0; cnt = 0; b = x = 0;
+    g = g0 = 0;
     if (pos >= end) return;
     // the last group that starts at or before pos (those without items start where the next does)
     int lo = 0, hi = n_groups;  // pre[lo] <= pos < pre[hi]
     while (hi - lo > 1) {
       const int step = max(1, (hi - lo) / 32);
       const int p = min(lo + (lane + 1) * step, hi);
-      const unsigned over = __ballot_sync(0xFFFFFFFFu, p >= hi || pre[p] > pos);
+      const unsigned over = __ballot_sync(0xFFFFFFFFu, p >= hi || pre()[p] > pos);
       const int k = over ? __ffs(over) - 1 : 32;  // probes at or before pos
       hi = k < 32 ? min(lo + (k + 1) * step, hi) : hi;
       lo = lo + k * step;
@@ -273,58 +287,63 @@ struct Walk {
     enter();
   }
   __device__ __forceinline__ void enter() {
-    b = g / nx;
-    x = g % nx;
-    u = unit_of<KV>(a, b, x);
-    cnt = unit_items<KV>(a, u);
-    g0 = pre[g];
+    const int nx = f_tiles(a, KV);
+    at.b = g / nx;
+    at.x = g - at.b * nx;
+    at.u = unit_of<TY, KV>(a, at.b, at.x);
+    at.cnt = unit_items<KV>(a, at.u);
+    g0 = pre()[g];
   }
-  // the next run: head h, its items [i0, i0 + n); false at the end of the slice
-  __device__ __forceinline__ bool next(int& h, int& i0, int& n) {
+  // The next run.  Roles take it while they still work on the one before: a new group costs
+  // dependent loads and divisions.
+  __device__ __forceinline__ Run next() {
+    const int H = KV ? a.Hkv : a.Hq;
+    at.n = 0;
     while (pos < end) {
-      while (pos >= g0 + unit_cost(cnt) * H) {
+      while (pos >= g0 + unit_cost(at.cnt) * H) {
         ++g;
         enter();
       }
-      const int cost = unit_cost(cnt);
-      h = (pos - g0) / cost;
-      const int at = pos - g0 - h * cost, to = min(cost, at + end - pos);  // of the unit's cost
-      pos += to - at;
-      i0 = max(0, at - kRunCost);
-      n = max(0, to - kRunCost) - i0;
-      if (n > 0) return true;
+      const int cost = unit_cost(at.cnt);
+      at.h = (pos - g0) / cost;
+      const int from = pos - g0 - at.h * cost, to = min(cost, from + end - pos);  // of the unit's cost
+      pos += to - from;
+      at.i0 = max(0, from - kRunCost);
+      at.n = max(0, to - kRunCost) - at.i0;
+      if (at.n > 0) break;
     }
-    return false;
+    return at;
   }
 };
 
-// Y tile of item i of a unit: its first row (query rows of head h, or keys), and the head.
-template <bool KV>
+// Y tile of an item of a run: its first row (query rows of head h, or keys), and the head.
+template <int TY, bool KV>
 struct ItemWalk {
   int h, t, row0;
-  __device__ __forceinline__ ItemWalk() : h(0), t(0), row0(0) {}
-  __device__ __forceinline__ ItemWalk(const BackwardArgs& a, const Unit& u, int unit_head, int i) {
+  __device__ __forceinline__ ItemWalk(const BackwardArgs& a, const Run& r) : h(0), t(0), row0(0) {
+    if (r.n == 0) return;
+    const int G = a.Hq / a.Hkv;
     if constexpr (KV) {
-      const int q = i / u.nt;
-      h = unit_head * (a.Hq / a.Hkv) + q;
-      t = i - q * u.nt;
-      row0 = (u.t0 + t) * a.tn_k;
+      const int q = r.i0 / r.u.nt;
+      h = r.h * G + q;
+      t = r.i0 - q * r.u.nt;
+      row0 = (r.u.t0 + t) * TY;
     } else {
-      h = unit_head / (a.Hq / a.Hkv);
-      t = i;
-      row0 = tile_list_key(u.tl, t) * kT;
+      h = r.h / G;
+      t = r.i0;
+      row0 = tile_list_key(r.u.tl, t) * TY;
     }
   }
-  __device__ __forceinline__ void step(const BackwardArgs& a, const Unit& u) {
+  __device__ __forceinline__ void step(const Unit& u) {
     ++t;
     if constexpr (KV) {
       if (t == u.nt) {
         t = 0;
         ++h;
       }
-      row0 = (u.t0 + t) * a.tn_k;
+      row0 = (u.t0 + t) * TY;
     } else {
-      row0 = tile_list_key(u.tl, t) * kT;
+      row0 = tile_list_key(u.tl, t) * TY;
     }
   }
 };
@@ -362,26 +381,25 @@ __device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
   }
 }
 
-// A ring of Y tiles and the items it still has to bring.
-template <bool KV>
+// The items whose tiles (or lse / D columns) a warp still has to bring.
+template <int TY, bool KV>
 struct Stream {
-  Walk<KV> w;
-  ItemWalk<KV> y;
-  int h, i0, n, m, it;
-  bool live;
-  __device__ __forceinline__ Stream(const BackwardArgs& a, const Walk<KV>& w_) : w(w_), y(), m(0), it(0) {
-    live = w.next(h, i0, n);
-    if (live) y = ItemWalk<KV>(a, w.u, h, i0);
-  }
+  Walk<TY, KV> w;
+  Run r, next;
+  ItemWalk<TY, KV> y;
+  int m, it;
+  __device__ __forceinline__ Stream(const BackwardArgs& a, const Walk<TY, KV>& w_)
+      : w(w_), r(w.next()), next(w.next()), y(a, r), m(0), it(0) {}
   __device__ __forceinline__ void step(const BackwardArgs& a) {
     ++it;
-    if (++m < n) {
-      y.step(a, w.u);
+    if (++m < r.n) {
+      y.step(r.u);
       return;
     }
     m = 0;
-    live = w.next(h, i0, n);
-    if (live) y = ItemWalk<KV>(a, w.u, h, i0);
+    r = next;
+    y = ItemWalk<TY, KV>(a, r);
+    next = w.next();
   }
 };
 
@@ -389,7 +407,7 @@ template <int D, bool KV>
 __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
     backward_kernel(const __grid_constant__ BackwardArgs a) {
   using C = BwdCfg<D, KV>;
-  constexpr int NS = C::NS, ND = C::ND, TN = C::TN;
+  constexpr int NS = C::NS, ND = C::ND, TN = C::TN, TY = C::TY, SUB = C::kSub;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -399,28 +417,26 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
   uint64_t* empty2 = full2 + C::kSt2;
   uint64_t* fullF = empty2 + C::kSt2;  // [2] F tiles
   uint64_t* emptyF = fullF + 2;
-  uint64_t* bar_S = emptyF + 2;        // [NS] S computed
-  uint64_t* bar_Sr = bar_S + NS;       // [NS] its P and dS used up
-  uint64_t* bar_P = bar_Sr + NS;       // [NS] P stored
-  uint64_t* bar_dS = bar_P + NS;       // [NS] dS stored
-  uint64_t* bar_dP = bar_dS + NS;      // [ND] dP computed
-  uint64_t* bar_dPr = bar_dP + ND;     // [ND] dP read
-  uint64_t* bar_acc = bar_dPr + ND;    // a run's sums complete
+  // S and dP computed: two each whatever the buffers, as a warpgroup may wait for every other item
+  uint64_t* bar_S = emptyF + 2;
+  uint64_t* bar_Sr = bar_S + 2;        // [NS] S read (where dS lies over it: dS used up)
+  uint64_t* bar_dP = bar_Sr + NS;
+  uint64_t* bar_dPr = bar_dP + 2;      // [ND] dP read
+  uint64_t* bar_P = bar_dPr + ND;      // [2] P and dS stored
+  uint64_t* bar_Pr = bar_P + 2;        // [2] P and dS used up
+  uint64_t* bar_acc = bar_Pr + 2;      // a run's sums complete
   uint64_t* bar_accr = bar_acc + 1;    // they are read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_accr + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kSt1; ++s) { mbar_init(&full1[s], 1); mbar_init(&empty1[s], 1); }
-    for (int s = 0; s < C::kSt2; ++s) { mbar_init(&full2[s], 1); mbar_init(&empty2[s], KV ? 2 : 1); }
+    for (int s = 0; s < C::kSt2; ++s) { mbar_init(&full2[s], 1); mbar_init(&empty2[s], 1); }
     for (int s = 0; s < 2; ++s) { mbar_init(&fullF[s], 1); mbar_init(&emptyF[s], 1); }
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&bar_S[s], 1);
-      mbar_init(&bar_Sr[s], 1);
-      mbar_init(&bar_P[s], C::kArrive);
-      mbar_init(&bar_dS[s], C::kArrive);
-    }
-    for (int s = 0; s < ND; ++s) { mbar_init(&bar_dP[s], 1); mbar_init(&bar_dPr[s], C::kArrive); }
+    for (int s = 0; s < NS; ++s) mbar_init(&bar_Sr[s], C::kSep ? C::kArrive : 1);
+    for (int s = 0; s < ND; ++s) mbar_init(&bar_dPr[s], C::kArrive);
+    for (int s = 0; s < 2; ++s) { mbar_init(&bar_S[s], 1); mbar_init(&bar_dP[s], 1); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&bar_P[s], C::kArrive); mbar_init(&bar_Pr[s], 1); }
     mbar_init(bar_acc, 1);
     mbar_init(bar_accr, 8);
     *abort_flag = 0;
@@ -442,8 +458,8 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Walk<KV> w(a, lane);
-  int h, i0, n;
+  Walk<TY, KV> w(a, lane);
+  Run run = w.next();
   if (warp == 8 || warp == 9) {
     // ---- first products: S = F1 Y1^T (warp 8), dP = F2 Y2^T (warp 9), and their F tiles ----
     constexpr uint32_t idesc = idesc_bf16_f32(128, TN, 0, 0);
@@ -460,145 +476,186 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
     const uint32_t ext = smem_u32(smem + (first ? C::kExt1Off : C::kExt2Off)), zero = smem_u32(smem + C::kZeroOff);
     const uint64_t d1 = smem_desc(smem_u32(smem + C::kOnesOff), C::kOnes, 128, kSwizzleNone);
     if (lane == 0) tma_prefetch_desc(map);
-    int it = 0, run = 0;
+    // the lse / D columns of an item, two items ahead (a tensor or bulk copy of them would take the
+    // copy engine as long as a tile)
+    Stream<TY, KV> ex(a, Walk<TY, KV>(a, lane));
+    auto load_ext = [&] {
+      if constexpr (KV) {
+        if (ex.r.n > 0) {
+          const size_t i = a.cu_q ? (size_t)ex.y.h * a.total_q + ex.r.u.qbase + ex.y.row0
+                                  : ((size_t)ex.r.b * a.Hq + ex.y.h) * a.Sq + ex.y.row0;
+          const uint4* src = (first ? a.ext1 : a.ext2) + i;
+          const uint32_t dst = ext + ex.it % C::kExtSlots * C::kExt;
+#pragma unroll
+          for (int k = 0; k < TY; k += 32) cp_async16(dst + (k + lane) * 16, src + k + lane, 16);
+          ex.step(a);
+        }
+        cp_async_commit();
+      }
+    };
+    // item `it`'s columns are whole for the tensor core; those of it + 2 on their way, into the slot
+    // of it - 2, whose product the softmax has read where that of it is issued
+    auto next_ext = [&] {
+      if constexpr (KV) {
+        load_ext();
+        cp_async_wait<2>();
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+    };
+    load_ext();
+    load_ext();
+    next_ext();
+    int it = 0, n_run = 0;
     bool ok = true;
-    while (ok && w.next(h, i0, n)) {
-      if (!mbar_wait_warp(eF, ((uint32_t)run & 1u) ^ 1u, a.err, abort_flag)) break;
+    while (ok && run.n > 0) {
+      if (!mbar_wait_warp(eF, ((uint32_t)n_run & 1u) ^ 1u, a.err, abort_flag)) break;
       const bool packed = !KV && a.cu_q != nullptr;
       mbar_arrive_expect_tx_e(fF, C::kFTile);
-      tma_load_5d_e(sF, map, fF, 0, packed ? w.u.qbase + w.x * kT : w.x * kT, 0, h, packed ? 0 : w.b);
-      ok = mbar_wait_warp(fF, (uint32_t)run & 1u, a.err, abort_flag);
+      tma_load_5d_e(sF, map, fF, 0, packed ? run.u.qbase + run.x * kT : run.x * kT, 0, run.h, packed ? 0 : run.b);
+      const int n = run.n;
+      run = w.next();
+      ok = mbar_wait_warp(fF, (uint32_t)n_run & 1u, a.err, abort_flag);
       for (int m = 0; ok && m < n; ++m, ++it) {
-        const int s = it % stages, buf = it % bufs;
-        const uint32_t ph_f = (uint32_t)(it / stages) & 1u, ph_b = ((uint32_t)(it / bufs) & 1u) ^ 1u;
-        // both at once, one by one only where they are not ready
-        const bool r0 = mbar_test(&full[s], ph_f), r1 = mbar_test(&freed[buf], ph_b);
-        if (!__all_sync(0xFFFFFFFFu, r0 & r1)) {
-          ok = mbar_wait_warp(&freed[buf], ph_b, a.err, abort_flag) &&
-               mbar_wait_warp(&full[s], ph_f, a.err, abort_flag);
-          if (!ok) break;
-        }
-        tc_fence_after();
-        const uint64_t y = dy + (uint64_t)((s * C::kYTile) >> 4);
-        const uint32_t d = out + buf * TN;
+        const int s = it % stages;
+        const uint32_t ph_f = (uint32_t)(it / stages) & 1u;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss_e(d, df + (uint64_t)(((kk >> 2) * C::kFPanel + (kk & 3) * 32) >> 4),
-                   y + (uint64_t)(((kk >> 2) * C::kYPanel + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
-        if constexpr (KV) {
-          const uint32_t e = ext + s * C::kExt;
-          mma_ss_e(d, d1, smem_desc(e, zero - e, 128, kSwizzleNone), idesc, 1u);
+        for (int sub = 0; sub < SUB; ++sub) {
+          const int si = it * SUB + sub, buf = si % bufs;
+          const uint32_t ph_b = ((uint32_t)(si / bufs) & 1u) ^ 1u;
+          // both at once, one by one only where they are not ready
+          const bool r0 = sub > 0 || mbar_test(&full[s], ph_f), r1 = mbar_test(&freed[buf], ph_b);
+          if (!__all_sync(0xFFFFFFFFu, r0 & r1)) {
+            ok = mbar_wait_warp(&freed[buf], ph_b, a.err, abort_flag) &&
+                 mbar_wait_warp(&full[s], ph_f, a.err, abort_flag);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          const uint64_t y = dy + (uint64_t)((s * C::kYTile + sub * TN * 128) >> 4);
+          const uint32_t d = out + buf * TN;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss_e(d, df + (uint64_t)(((kk >> 2) * C::kFPanel + (kk & 3) * 32) >> 4),
+                     y + (uint64_t)(((kk >> 2) * C::kYPanel + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+          if constexpr (KV) {
+            const uint32_t e = ext + it % C::kExtSlots * C::kExt + sub * TN * 16;
+            mma_ss_e(d, d1, smem_desc(e, zero - e, 128, kSwizzleNone), idesc, 1u);
+          }
+          mma_commit_e(&done[si & 1]);
         }
-        mma_commit_e(&done[buf]);
-        if (!first) mma_commit_e(&empty2[s]);
+        if (!ok) break;
+        if (!KV && !first) mma_commit_e(&empty2[s]);
         if (m == n - 1) mma_commit_e(eF);
+        next_ext();  // (of item it + 1, off the way from one product to the next)
       }
-      ++run;
+      ++n_run;
     }
+    cp_async_wait<0>();
     // (aborted: the last copy lands before shared memory is released)
-    if (!ok && run > 0) mbar_wait(fF, (uint32_t)(run - 1) & 1u, nullptr, nullptr, 100000000ull);
+    if (!ok && n_run > 0) mbar_wait(fF, (uint32_t)(n_run - 1) & 1u, nullptr, nullptr, 100000000ull);
   } else if (warp == 10) {
     // ---- second products: acc0 += P Y2 (dV), acc1 += dS Y1 ----
     constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
     const uint64_t my1 = smem_desc(smem_u32(smem + C::kY1Off), C::kYPanel, 1024, kSwizzle128B);
     const uint64_t my2 = smem_desc(smem_u32(smem + C::kY2Off), C::kYPanel, 1024, kSwizzle128B);
-    // A in TMEM: 32 columns of bf16 pairs for each 64 columns of S; Y MN-major
+    // A in TMEM, 16 columns of Y's rows at a time (where dS lies over S: 32 columns for each 64 of
+    // S); Y MN-major
     auto issue = [&](uint32_t acc, uint32_t p, uint64_t y, bool fresh) {
 #pragma unroll
       for (int kk = 0; kk < TN / 16; ++kk)
         mma_ts_e(tmem + acc, p + (kk >> 2) * 64 + (kk & 3) * 8, y + (uint64_t)(kk * (2048 >> 4)), idesc,
                  (!fresh || kk > 0) ? 1u : 0u);
     };
-    int it = 0, run = 0;
+    int it = 0, n_run = 0;
     bool ok = true;
-    while (ok && w.next(h, i0, n)) {
-      if (run > 0) ok = mbar_wait_warp(bar_accr, (uint32_t)(run - 1) & 1u, a.err, abort_flag);
+    while (ok && run.n > 0) {
+      const int n = run.n;
+      run = w.next();
+      if (n_run > 0) ok = mbar_wait_warp(bar_accr, (uint32_t)(n_run - 1) & 1u, a.err, abort_flag);
       for (int m = 0; ok && m < n; ++m, ++it) {
-        const int buf = it % NS, s1 = it % C::kSt1, s2 = it % C::kSt2;
-        const uint32_t sb = tmem + C::kS + buf * TN, ph = (uint32_t)(it / NS) & 1u;
-        if constexpr (KV) {
-          // (g's tile is whole where its dP is waited for: the softmax stores P before)
-          ok = mbar_wait_warp(&full2[s2], (uint32_t)(it / C::kSt2) & 1u, a.err, abort_flag) &&
-               mbar_wait_warp(&bar_P[buf], ph, a.err, abort_flag);
+        const int s1 = it % C::kSt1, s2 = it % C::kSt2;
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub) {
+          const int si = it * SUB + sub, buf = si & 1;
+          const uint32_t p = tmem + C::kP + buf * C::kPStep;
+          const uint64_t off = (uint64_t)((sub * TN * 128) >> 4);
+          // (dP is done where dS is stored, so g's tile is whole)
+          ok = mbar_wait_warp(&bar_P[buf], (uint32_t)(si >> 1) & 1u, a.err, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          issue(0, sb, my2 + (uint64_t)((s2 * C::kYTile) >> 4), m == 0);
-          mma_commit_e(&empty2[s2]);
+          const bool fresh = m == 0 && sub == 0;
+          if constexpr (KV) {
+            issue(0, p, my2 + (uint64_t)((s2 * C::kYTile) >> 4) + off, fresh);
+            if (sub == SUB - 1) mma_commit_e(&empty2[s2]);
+          }
+          issue(C::kAcc1, p + (KV ? 32 : 0), my1 + (uint64_t)((s1 * C::kYTile) >> 4) + off, fresh);
+          mma_commit_e(C::kSep ? &bar_Pr[buf] : &bar_Sr[buf]);
         }
-        ok = mbar_wait_warp(&bar_dS[buf], ph, a.err, abort_flag);
         if (!ok) break;
-        tc_fence_after();
-        issue(C::kAcc1, sb + (KV ? 32 : 0), my1 + (uint64_t)((s1 * C::kYTile) >> 4), m == 0);
-        mma_commit_e(&bar_Sr[buf]);
         mma_commit_e(&empty1[s1]);
         if (m == n - 1) mma_commit_e(bar_acc);
       }
-      ++run;
+      ++n_run;
     }
   } else if (warp == 11) {
     // ---- the rings of Y1 and Y2, each slot filled as soon as it is free ----
-    Stream<KV> st[2] = {Stream<KV>(a, w), Stream<KV>(a, w)};
+    Stream<TY, KV> st[2] = {Stream<TY, KV>(a, Walk<TY, KV>(a, lane)), Stream<TY, KV>(a, Walk<TY, KV>(a, lane))};
     if (lane == 0) {
-      tma_prefetch_desc(KV ? &a.tm_qy : &a.tm_k);
-      tma_prefetch_desc(KV ? &a.tm_doy : &a.tm_v);
+      tma_prefetch_desc(KV ? &a.tm_qy : &a.tm_ky);
+      tma_prefetch_desc(KV ? &a.tm_doy : &a.tm_vy);
     }
     bool ok = true;
     long long t0 = clock64();
     uint32_t idle = 0;
-    while (ok && (st[0].live || st[1].live)) {
+    while (ok && (st[0].r.n > 0 || st[1].r.n > 0)) {
       bool moved = false;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        Stream<KV>& t = st[k];
-        if (!t.live) continue;
+        Stream<TY, KV>& t = st[k];
+        if (t.r.n == 0) continue;
         const int stages = k == 0 ? C::kSt1 : C::kSt2, s = t.it % stages;
         uint64_t *full = k == 0 ? full1 : full2, *empty = k == 0 ? empty1 : empty2;
         if (!mbar_test_warp(&empty[s], ((uint32_t)(t.it / stages) & 1u) ^ 1u)) continue;
         moved = true;
-        const Unit& u = t.w.u;
-        const CUtensorMap* map = KV ? (k == 0 ? &a.tm_qy : &a.tm_doy) : (k == 0 ? &a.tm_k : &a.tm_v);
+        const Unit& u = t.r.u;
+        const CUtensorMap* map = KV ? (k == 0 ? &a.tm_qy : &a.tm_doy) : (k == 0 ? &a.tm_ky : &a.tm_vy);
         uint8_t* dst = smem + (k == 0 ? C::kY1Off : C::kY2Off) + s * C::kYTile;
         const int rows = KV ? u.Sq : u.Skv;  // Y rows of the sequence
         const int row_base = KV ? u.qbase : u.kbase;
         // a packed batch: other rows follow a sequence's own
-        const bool whole = a.cu_q == nullptr || t.y.row0 + TN <= rows;
-        uint32_t bytes = KV ? C::kExt : 0;
-        if (whole) {
-          bytes += C::kYTile;
-        } else {
+        const bool whole = a.cu_q == nullptr || t.y.row0 + TY <= rows;
+        if (!whole) {
           // its last rows are gathered, so that the rows behind them arrive as zeros (a weight of
           // zero times what lies there could be NaN)
           const uint16_t* base = KV ? (k == 0 ? a.q : a.dout) : (k == 0 ? a.k : a.v);
-          int ri[TN / 32];
+          int ri[TY / 32];
 #pragma unroll
-          for (int e = 0; e < TN / 32; ++e) {
+          for (int e = 0; e < TY / 32; ++e) {
             const int r = t.y.row0 + e * 32 + lane;
             ri[e] = r < rows ? row_base + r : -1;
           }
-          paged_gather<D, TN / 32>(smem_u32(dst), C::kYPanel, base, KV ? a.Hq : a.Hkv, t.y.h, lane, ri);
+          paged_gather<D, TY / 32>(smem_u32(dst), C::kYPanel, base, KV ? a.Hq : a.Hkv, t.y.h, lane, ri);
           cp_async_commit();
           cp_async_wait<0>();
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (bytes) mbar_arrive_expect_tx_e(&full[s], bytes);
-        else if (lane == 0) mbar_arrive(&full[s]);
         if (whole) {
+          mbar_arrive_expect_tx_e(&full[s], C::kYTile);
           if (KV && a.cu_q) tma_load_5d_e(dst, map, &full[s], 0, row_base + t.y.row0, 0, t.y.h, 0);
-          else tma_load_5d_e(dst, map, &full[s], 0, t.y.row0, 0, t.y.h, t.w.b);
-        }
-        if constexpr (KV) {
-          const size_t i = a.cu_q ? (size_t)t.y.h * a.total_q + row_base + t.y.row0
-                                  : ((size_t)t.w.b * a.Hq + t.y.h) * a.Sq + t.y.row0;
-          bulk_load_e(smem + (k == 0 ? C::kExt1Off : C::kExt2Off) + s * C::kExt, (k == 0 ? a.ext1 : a.ext2) + i,
-                      C::kExt, &full[s]);
+          else tma_load_5d_e(dst, map, &full[s], 0, t.y.row0, 0, t.y.h, t.r.b);
+        } else if (lane == 0) {
+          mbar_arrive(&full[s]);
         }
         t.step(a);
       }
       if (moved) {
         idle = 0;
         t0 = clock64();
-      } else if ((++idle & 63u) == 0) {  // bounded, as every wait here
+        continue;
+      }
+      __nanosleep(100);  // (the softmax warps beside it want the issue slots)
+      if ((++idle & 63u) == 0) {  // bounded, as every wait here
         bool out = *abort_flag != 0;
         if (!out && clock64() - t0 > (long long)(ATTN_WAIT_LIMIT_NS * kMaxSmClockGHz)) {
           atomicCAS(a.err, kErrNone, kErrWaitTimeout);
@@ -623,40 +680,36 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
     const float sl2 = a.scale * kLog2e;
     const uint64_t sl2x2 = f2pack(sl2, sl2);
     const int c0 = TN == 128 ? wg * 64 : 0;  // this thread's columns of an item: c0 .. c0 + 63
-    int it = 0, run = 0;
-    bool ok = true;
-    while (ok && w.next(h, i0, n)) {
-      const int f0 = w.x * kT;
-      float lse2 = INFINITY, dd = 0.f;
-      if constexpr (!KV) {
-        if (f0 + r < w.u.Sq) {
-          const size_t i = a.cu_q ? (size_t)h * a.total_q + w.u.qbase + f0 + r
-                                  : ((size_t)w.b * a.Hq + h) * a.Sq + f0 + r;
-          const float2 st = a.stat[i];
-          lse2 = st.x;
-          dd = st.y;
-        }
+    // lse and D of this thread's row (dQ pass; elsewhere they are in the products)
+    auto row_stat = [&](const Run& q) {
+      float2 v = make_float2(INFINITY, 0.f);
+      if (!KV && q.n > 0 && q.x * kT + r < q.u.Sq) {
+        const size_t i = a.cu_q ? (size_t)q.h * a.total_q + q.u.qbase + q.x * kT + r
+                                : ((size_t)q.b * a.Hq + q.h) * a.Sq + q.x * kT + r;
+        v = a.stat[i];
       }
-      const uint64_t nlse2 = f2pack(-lse2, -lse2), ndd = f2pack(-dd, -dd);
-      ItemWalk<KV> y(a, w.u, h, i0);
-      for (int m = 0; m < n; ++m, ++it, y.step(a, w.u)) {
+      return v;
+    };
+    float2 stat = row_stat(run);
+    int it = 0, n_run = 0;
+    bool ok = true;
+    while (ok && run.n > 0) {
+      const int f0 = run.x * kT;
+      const Unit& u = run.u;
+      const uint64_t nlse2 = f2pack(-stat.x, -stat.x), ndd = f2pack(-stat.y, -stat.y);
+      ItemWalk<TY, KV> y(a, run);
+      for (int m = 0; m < run.n * SUB; ++m, ++it) {  // (it counts 64- or 128-column items here)
+        if (m > 0 && (SUB == 1 || (m & 1) == 0)) y.step(u);
         if (TN == 64 && (it & 1) != wg) continue;  // the other warpgroup's
-        const int buf = it % NS, bd = it % ND;
-        const uint32_t sc = lanes + C::kS + buf * TN + c0, dc = lanes + C::kDP + bd * TN + c0;
-        ok = mbar_wait_warp(&bar_S[buf], (uint32_t)(it / NS) & 1u, a.err, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t s[64];
-        tmem_ld32(sc, s);
-        tmem_ld32(sc + 32, s + 32);
+        const int row0 = y.row0 + (SUB == 1 ? 0 : (m & 1) * TN);
         // columns of this thread's row: [lo, hi) and, dQ pass, those before `sink`
         int lo = 0, hi = TN, sink = 0;
         bool mask;
         if constexpr (KV) {
-          const long long d0 = w.u.off + y.row0;  // key index of the tile's first row
+          const long long d0 = u.off + row0;  // key index of the tile's first row
           const int j = f0 + r;
-          mask = y.row0 + TN > w.u.Sq;
-          hi = min(TN, w.u.Sq - y.row0);
+          mask = row0 + TN > u.Sq;
+          hi = min(TN, u.Sq - row0);
           if (a.causal) {
             mask = mask || f0 + kT - 1 > d0;
             lo = (int)min((long long)TN, max(0LL, j - d0));
@@ -666,144 +719,152 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
             if (j >= a.n_sink) hi = (int)min((long long)hi, max(0LL, j + (long long)a.window - d0));
           }
         } else {
-          const long long pos = f0 + r + w.u.off;  // key index of this row
-          const long long p0 = f0 + w.u.off;
-          mask = y.row0 + TN > w.u.Skv;
-          hi = min(TN, w.u.Skv - y.row0);
+          const long long pos = f0 + r + u.off;  // key index of this row
+          const long long p0 = f0 + u.off;
+          mask = row0 + TN > u.Skv;
+          hi = min(TN, u.Skv - row0);
           if (a.causal) {
-            mask = mask || y.row0 + TN - 1 > p0;
-            hi = (int)min((long long)hi, max(0LL, pos + 1 - y.row0));
+            mask = mask || row0 + TN - 1 > p0;
+            hi = (int)min((long long)hi, max(0LL, pos + 1 - row0));
           }
           if (a.window > 0) {
-            mask = mask || y.row0 <= p0 + kT - 1 - a.window;
-            lo = (int)min((long long)TN, max(0LL, pos - a.window + 1 - y.row0));
-            sink = min(TN, max(0, a.n_sink - y.row0));
+            mask = mask || row0 <= p0 + kT - 1 - a.window;
+            lo = (int)min((long long)TN, max(0LL, pos - a.window + 1 - row0));
+            sink = min(TN, max(0, a.n_sink - row0));
           }
         }
-        // as bits (a weight out of them may be inf, dP of a column that is no row anything: both
-        // products' operands are cleared after their rounding)
-        uint32_t in[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (mask) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int c1 = c0 + q * 32;
-            in[q] = (bits_below(hi - c1) & ~bits_below(lo - c1)) | bits_below(min(sink, hi) - c1);
-          }
-        }
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const uint64_t x = f2pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          float e0, e1;
-          f2unpack(KV ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
-          s[c] = __float_as_uint(ex2_approx(e0));
-          s[c + 1] = __float_as_uint(ex2_approx(e1));
-        }
-        if constexpr (KV) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t t[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              t[c] = pack_bf16x2(__uint_as_float(s[q * 32 + 2 * c]), __uint_as_float(s[q * 32 + 2 * c + 1]));
-            if (mask) keep_bits<16>(t, in[q]);
-            tmem_st16(sc + q * 16, t);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_P[buf]);
-        }
-        ok = mbar_wait_warp(&bar_dP[bd], (uint32_t)(it / ND) & 1u, a.err, abort_flag);
+        const int bs = it % NS, bd = it % ND, bp = it & 1;
+        const uint32_t sc = lanes + C::kS + bs * TN + c0, dc = lanes + C::kDP + bd * TN + c0;
+        const uint32_t pc = lanes + C::kP + bp * C::kPStep + c0;
+        uint32_t s[64], p[64];
+        ok = mbar_wait_warp(&bar_S[bp], (uint32_t)(it >> 1) & 1u, a.err, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        uint32_t p[64];
+        tmem_ld32(sc, s);
+        tmem_ld32(sc + 32, s + 32);
+        tmem_wait_ld();
+        if constexpr (C::kSep) {  // the next S need not wait for this dP
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_Sr[bs]);
+        }
+        ok = mbar_wait_warp(&bar_dP[bp], (uint32_t)(it >> 1) & 1u, a.err, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
         tmem_ld32(dc, p);
         tmem_ld32(dc + 32, p + 32);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_dPr[bd]);
+        if constexpr (C::kSep) {
+          ok = mbar_wait_warp(&bar_Pr[bp], ((uint32_t)(it >> 1) & 1u) ^ 1u, a.err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+        }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t t[16];
+          uint32_t t[16], tp[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             const int k = q * 32 + 2 * c;
+            const uint64_t x = f2pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
             uint64_t g = f2pack(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
-            if constexpr (!KV) g = add2(g, ndd);
-            float x0, x1;
-            f2unpack(mul2(g, f2pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1]))), x0, x1);
+            float e0, e1, x0, x1;
+            f2unpack(KV ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
+            e0 = ex2_approx(e0);
+            e1 = ex2_approx(e1);
+            if constexpr (KV) tp[c] = pack_bf16x2(e0, e1);
+            else g = add2(g, ndd);
+            f2unpack(mul2(g, f2pack(e0, e1)), x0, x1);
             t[c] = pack_bf16x2(x0, x1);
           }
-          if (mask) keep_bits<16>(t, in[q]);
-          tmem_st16(sc + (KV ? 32 : 0) + q * 16, t);
+          if (mask) {
+            // (a weight out of the row's columns may be inf, dP of a column that is no row anything:
+            // both operands are cleared after their rounding)
+            const int c1 = c0 + q * 32;
+            const uint32_t in = (bits_below(hi - c1) & ~bits_below(lo - c1)) | bits_below(min(sink, hi) - c1);
+            if constexpr (KV) keep_bits<16>(tp, in);
+            keep_bits<16>(t, in);
+          }
+          if constexpr (KV) tmem_st16(pc + q * 16, tp);
+          tmem_st16(pc + (KV ? 32 : 0) + q * 16, t);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_dS[buf]);
+        if (lane == 0) mbar_arrive(&bar_P[bp]);
       }
       if (!ok) break;
       // ---- the run's sums: rows of the output, or fp32 partials ----
-      ok = mbar_wait_warp(bar_acc, (uint32_t)run & 1u, a.err, abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      const bool part = n != w.cnt;
+      const Run next = w.next();
+      stat = row_stat(next);
+      const bool part = run.n != run.cnt;
       // KV: warpgroup 0 dV, 1 dK; else a half of dQ's columns each
       constexpr int kCols = KV ? D : D / 2;
       const uint32_t col0 = KV ? (wg == 0 ? 0 : C::kAcc1) : C::kAcc1 + wg * kCols;
       const float f = (KV && wg == 0) ? 1.f : a.scale;
       // rows [0, live) are the sequence's, [live, wrote) written as zeros
-      const int live = min(kT, (KV ? w.u.Skv : w.u.Sq) - f0);
+      const int live = min(kT, (KV ? u.Skv : u.Sq) - f0);
       const int wrote = KV && a.fill ? min(kT, a.Skv - f0) : live;
       uint16_t* out;
       size_t row_w;  // elements from row to row
       if constexpr (KV) {
-        out = (wg == 0 ? a.dv : a.dk) + (((size_t)w.b * a.Skv + f0) * a.Hkv + h) * D;
+        out = (wg == 0 ? a.dv : a.dk) + (((size_t)run.b * a.Skv + f0) * a.Hkv + run.h) * D;
         row_w = (size_t)a.Hkv * D;
       } else {
-        out = a.dq + ((size_t)(w.u.qbase + f0) * a.Hq + h) * D + wg * kCols;
+        out = a.dq + ((size_t)(u.qbase + f0) * a.Hq + run.h) * D + wg * kCols;
         row_w = (size_t)a.Hq * D;
       }
       float4* pp = reinterpret_cast<float4*>(KV ? a.part_k : a.part_q) +
-                   ((size_t)blockIdx.x * 2 + (i0 > 0 ? 0 : 1)) * (kT * D * (KV ? 2 : 1) / 4) +
+                   ((size_t)blockIdx.x * 2 + (run.i0 > 0 ? 0 : 1)) * (kT * D * (KV ? 2 : 1) / 4) +
                    (size_t)wg * (kCols / 4) * kT + r;
+      ok = mbar_wait_warp(bar_acc, (uint32_t)n_run & 1u, a.err, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      constexpr int kStep = kCols >= 64 ? 64 : kCols;
+#pragma unroll 1
+      for (int c1 = 0; c1 < kCols; c1 += kStep) {
+        uint32_t v[kStep];
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(lanes + col0 + c, v);
+        for (int e = 0; e < kStep; e += 32) tmem_ld32(lanes + col0 + c1 + e, v + e);
         tmem_wait_ld();
-        if (part) {
+        if (c1 + kStep == kCols) {  // the next run's sums may start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_accr);
+        }
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            pp[(size_t)((c + e) / 4) * kT] = make_float4(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f,
-                                                         __uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
-        } else {
-          // four lanes write 64 bytes of a row side by side: a row a lane made each store 32 lines
-          uint4 q[4];
+        for (int c = 0; c < kStep; c += 32) {
+          const uint32_t* x = v + c;
+          if (part) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t* x = v + e * 8;
-            q[e] = make_uint4(pack_bf16x2(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f),
-                              pack_bf16x2(__uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f),
-                              pack_bf16x2(__uint_as_float(x[4]) * f, __uint_as_float(x[5]) * f),
-                              pack_bf16x2(__uint_as_float(x[6]) * f, __uint_as_float(x[7]) * f));
-          }
-          transpose4(q, lane);
+            for (int e = 0; e < 32; e += 4)
+              pp[(size_t)((c1 + c + e) / 4) * kT] =
+                  make_float4(__uint_as_float(x[e]) * f, __uint_as_float(x[e + 1]) * f, __uint_as_float(x[e + 2]) * f,
+                              __uint_as_float(x[e + 3]) * f);
+          } else {
+            // four lanes write 64 bytes of a row side by side: a row a lane made each store 32 lines
+            uint4 q[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = (r & ~3) + e;
-            if (row < wrote)
-              *reinterpret_cast<uint4*>(out + (size_t)row * row_w + c + (lane & 3) * 8) =
-                  row < live ? q[e] : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 4; ++e, x += 8)
+              q[e] = make_uint4(pack_bf16x2(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f),
+                                pack_bf16x2(__uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f),
+                                pack_bf16x2(__uint_as_float(x[4]) * f, __uint_as_float(x[5]) * f),
+                                pack_bf16x2(__uint_as_float(x[6]) * f, __uint_as_float(x[7]) * f));
+            transpose4(q, lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int row = (r & ~3) + e;
+              if (row < wrote)
+                *reinterpret_cast<uint4*>(out + (size_t)row * row_w + c1 + c + (lane & 3) * 8) =
+                    row < live ? q[e] : make_uint4(0, 0, 0, 0);
+            }
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_accr);
-      ++run;
+      run = next;
+      ++n_run;
     }
   }
   tc_fence_before();
@@ -839,7 +900,7 @@ __device__ void join(const BackwardArgs& a, int c, int ctas, int zero_cta, int z
     for (int g = zero_cta; g < n_groups; g += zero_ctas) {
       if (pre[g + 1] != pre[g]) continue;
       const int b = g / nx, f0 = g % nx * kT;
-      const Unit u = unit_of<KV>(a, b, g % nx);
+      const Unit u = unit_of<BwdCfg<D, KV>::TY, KV>(a, b, g % nx);
       for (int i = threadIdx.x; i < kAccs * H * kT * (D / 8); i += kJoinThreads) {
         const int e = i % (D / 8), h = i / (D / 8) % H, r = i / (D / 8) / H % kT, acc = i / (D / 8) / H / kT;
         uint16_t* out = row_ptr(u, b, f0, h, r, acc);
@@ -867,7 +928,7 @@ __device__ void join(const BackwardArgs& a, int c, int ctas, int zero_cta, int z
     lo = lo + k * step;
   }
   const int b = lo / nx, f0 = lo % nx * kT;
-  const Unit u = unit_of<KV>(a, b, lo % nx);
+  const Unit u = unit_of<BwdCfg<D, KV>::TY, KV>(a, b, lo % nx);
   const int cnt = unit_items<KV>(a, u);
   const int cost = unit_cost(cnt), h = (int)(at - pre[lo]) / cost;
   const int u0 = pre[lo] + h * cost + kRunCost, u1 = u0 + cnt;  // the places of the unit's items
@@ -938,7 +999,10 @@ cudaError_t launch_d(const BackwardArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int backward_tile_rows(int d) { return d == 64 ? BwdCfg<64, true>::TN : BwdCfg<128, true>::TN; }
+int backward_tile_rows(int d, bool dkdv) {
+  if (d == 64) return dkdv ? BwdCfg<64, true>::TY : BwdCfg<64, false>::TY;
+  return dkdv ? BwdCfg<128, true>::TY : BwdCfg<128, false>::TY;
+}
 
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t stream) {
   switch (a.d) {

@@ -574,7 +574,7 @@ int attn_evict(const float* weights, float* weights_out, long long w_stride, att
  *             scale in [1e-30, 1e30]
  *   work      attn_prefill_backward_workspace(B, Hq, Hkv, B * Sq, Sq, Skv, d) bytes, 256-byte
  *             aligned, contents of no matter; calls that may run at the same time need their own
- *   d in {64, 128};  B * Sq * Hq, B * Skv * Hkv and the number of 64 x 128 tiles of all heads
+ *   d in {64, 128};  B * Sq * Hq, B * Skv * Hkv and the number of 64 x 64 tiles of all heads
  *   below 2^31
  * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.  Can be captured
  * into a CUDA graph after a first call of its head dim on the device.
