@@ -10,8 +10,6 @@
 
 namespace {
 
-constexpr int kSms = 152;  // SMs of a GB300
-
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool ok16(const void* p) { return p != nullptr && aligned(p, 16); }
 bool ok4(const void* p) { return p != nullptr && aligned(p, 4); }
@@ -37,14 +35,14 @@ int check_sizes(const Sizes& z) {
 
 // Byte offsets of the workspace's parts.
 struct Layout {
-  size_t pre_k, pre_q, stat, ext1, ext2, part_k, part_q, bytes;
+  size_t pre_k, pre_q, joined, stat, ext1, ext2, part_k, part_q, bytes;
   int ctas;
 };
 Layout layout_of(const Sizes& z) {
   Layout l;
   const long long tq = (z.Sq + 127LL) / 128, tk = (z.Skv + 127LL) / 128;
   // one CTA an SM, none without an item of its own
-  l.ctas = (int)std::max(1LL, std::min<long long>(kSms, tq * z.B * tk * z.Hq));
+  l.ctas = (int)std::max(1LL, std::min<long long>(attn::kBackwardCtas, tq * z.B * tk * z.Hq));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t p = at;
@@ -53,6 +51,7 @@ Layout layout_of(const Sizes& z) {
   };
   l.pre_k = take((size_t)(z.B * tk + 1) * 4);
   l.pre_q = take((size_t)(z.B * tq + 1) * 4);
+  l.joined = take((size_t)2 * attn::kBackwardCtas * 4);
   l.stat = take((size_t)z.rows * z.Hq * 8);
   l.ext1 = take(((size_t)z.rows * z.Hq + 128) * 16);
   l.ext2 = take(((size_t)z.rows * z.Hq + 128) * 16);
@@ -107,6 +106,7 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   uint8_t* w = static_cast<uint8_t*>(work);
   a.pre_k = reinterpret_cast<int*>(w + l.pre_k);
   a.pre_q = reinterpret_cast<int*>(w + l.pre_q);
+  a.joined = reinterpret_cast<int*>(w + l.joined);
   a.stat = reinterpret_cast<float2*>(w + l.stat);
   a.ext1 = reinterpret_cast<uint4*>(w + l.ext1);
   a.ext2 = reinterpret_cast<uint4*>(w + l.ext2);

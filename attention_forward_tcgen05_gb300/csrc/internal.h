@@ -224,8 +224,10 @@ struct BackwardArgs {
   float2* stat;                         // [rows of lse] lse log2 e (+inf: the row takes no part), D
   uint4 *ext1, *ext2;                   // the same as bf16 columns of the dK/dV pass, 128 rows more
   float *part_k, *part_q;               // [ctas][2][accumulators * d / 4][128][4] sums of cut units
-  int ctas_k, ctas_q;
+  int* joined;                          // [2][kBackwardCtas] parts of cut units that are out, by their first slice
+  int ctas_k, ctas_q;                   // at most kBackwardCtas
 };
+constexpr int kBackwardCtas = 152;
 int backward_tile_rows(int d, bool dkdv);  // rows of a pass's streamed tiles
 
 // Rows of a K / V stage loaded by one TMA box in the decode kernel (two

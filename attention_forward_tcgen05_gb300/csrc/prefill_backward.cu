@@ -29,7 +29,7 @@
 // heads of the group in the dK/dV pass).  The units' items form one list, which the CTAs (one
 // per SM) cut into equal slices: neither causal triangles, the few key blocks of the sinks
 // that every row sees, nor groups of odd sizes leave SMs idle.  A unit cut between CTAs
-// goes out as fp32 partials, which a last launch sums in slice order.
+// goes out as fp32 partials, which the one that finishes last sums in slice order.
 //
 // Warps: 0-7 softmax (thread = row of F, 64 columns of an item), 8 / 9 S and dP with their F tiles, 10
 // the second products, 11 the rings of Y1 and Y2.
@@ -45,6 +45,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kT = 128;           // rows of a tile
+constexpr int kMaxCtas = kBackwardCtas;
 // A run of a unit's items costs its start and end (the F tiles' copy, the sums' way out) beside its
 // items, about as much as kRunCost of them: units of few items would otherwise fill some slices
 // with nothing but starts and ends.
@@ -87,8 +88,8 @@ struct BwdCfg {
   static constexpr int kOnesOff = kExt2Off + kExtSlots * kExt;
   static constexpr int kZeroOff = kOnesOff + kOnes;
   static constexpr int kBarOff = kZeroOff + kOnes;
-  static constexpr int kNumBars = 2 * kSt1 + 2 * kSt2 + 4 + 2 + NS + 2 + ND + 4 + 2;
-  static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
+  static constexpr int kNumBars = 2 * kSt1 + 2 * kSt2 + 4 + 2 + NS + 2 + ND + 4 + 4;
+  static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;  // (16: TMEM address, abort and last flags)
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static constexpr uint32_t kAcc1 = KV ? D : 0;  // TMEM columns; acc0 at 0
   static constexpr uint32_t kS = kAcc1 + D;
@@ -211,43 +212,92 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
   if (n == 0 && threadIdx.x == 0) pre[0] = 0;
 }
 
-// D / 8 lanes to a (row, head), rows in memory order of o: [rows][Hq][D].
+// Zeros for the gradients of units without items: keys that no row sees, rows that see no key and,
+// with `fill`, rows of no sequence and slots behind a sequence's keys.  CTA c of n.
+template <int D, bool KV>
+__device__ void zero_units(const BackwardArgs& a, int c, int n) {
+  const int nx = f_tiles(a, KV), n_groups = a.B * nx, H = KV ? a.Hkv : a.Hq;
+  for (int g = c; g < n_groups; g += n) {
+    const int b = g / nx, f0 = (g - b * nx) * kT;
+    const Unit u = unit_of<BwdCfg<D, KV>::TY, KV>(a, b, g - b * nx);
+    if (unit_items<KV>(a, u) > 0) continue;
+    const int rows = min(kT, (KV ? (a.fill ? a.Skv : u.Skv) : u.Sq) - f0);
+    const size_t at = ((size_t)(KV ? u.kbase : u.qbase) + f0) * H * D;
+    const int w = H * (D / 8);
+    for (long long i = threadIdx.x; i < (long long)rows * w; i += kPrepThreads) {
+      if (KV) {
+        reinterpret_cast<uint4*>(a.dk + at)[i] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(a.dv + at)[i] = make_uint4(0, 0, 0, 0);
+      } else {
+        reinterpret_cast<uint4*>(a.dq + at)[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  if (!KV && a.cu_q && a.fill) {
+    const long long w = (long long)a.Hq * (D / 8), step = (long long)n * kPrepThreads;
+    const int c0 = min(max(a.cu_q[0], 0), a.total_q), c1 = min(max(a.cu_q[a.B], c0), a.total_q);
+    for (long long i = (long long)c * kPrepThreads + threadIdx.x; i < (c0 + (long long)a.total_q - c1) * w; i += step)
+      reinterpret_cast<uint4*>(a.dq)[i < c0 * w ? i : i + (c1 - c0) * w] = make_uint4(0, 0, 0, 0);
+  }
+}
+constexpr int kZeroCtas = 304;
+
+// D / 8 lanes to a (row, head), kPrepRows of them in flight, in memory order of o: [rows][Hq][D].
+constexpr int kPrepRows = 4;
 template <int D, bool OBF16>
 __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __grid_constant__ BackwardArgs a) {
   if (blockIdx.x < 2) {
     if (blockIdx.x == 0) scan_costs<BwdCfg<D, true>::TY, true>(a, a.pre_k);
     else scan_costs<BwdCfg<D, false>::TY, false>(a, a.pre_q);
+    for (int i = threadIdx.x; i < kMaxCtas; i += kPrepThreads) a.joined[blockIdx.x * kMaxCtas + i] = 0;
     return;
   }
-  constexpr int L = D / 8;
+  const int n_rows = (int)gridDim.x - 2 - kZeroCtas;  // CTAs of the rows' sums
+  if ((int)blockIdx.x - 2 >= n_rows) {
+    zero_units<D, true>(a, (int)blockIdx.x - 2 - n_rows, kZeroCtas);
+    zero_units<D, false>(a, (int)blockIdx.x - 2 - n_rows, kZeroCtas);
+    return;
+  }
+  constexpr int L = D / 8, kPer = kPrepThreads / L;
   const long long n = (long long)a.total_q * a.Hq;
-  const long long at = ((long long)(blockIdx.x - 2) * kPrepThreads + threadIdx.x) / L;
+  const long long at0 = (long long)(blockIdx.x - 2) * kPer * kPrepRows + threadIdx.x / L;
   const int c = threadIdx.x % L;
-  const long long rh = min(at, n - 1);  // (every lane takes part in the sums)
-  const uint4 g = *reinterpret_cast<const uint4*>(a.dout + rh * D + c * 8);
-  float s;
-  if constexpr (OBF16) {
-    s = dot8(g, *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.o) + rh * D + c * 8));
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.o) + rh * D + c * 8);
-    s = dot8(g, p[0], p[1]);
+  float s[kPrepRows];
+#pragma unroll
+  for (int k = 0; k < kPrepRows; ++k) {
+    const long long rh = min(at0 + k * kPer, n - 1);  // (every lane takes part in the sums)
+    const uint4 g = __ldg(reinterpret_cast<const uint4*>(a.dout + rh * D + c * 8));
+    if constexpr (OBF16) {
+      s[k] = dot8(g, __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.o) + rh * D + c * 8)));
+    } else {
+      const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.o) + rh * D + c * 8);
+      s[k] = dot8(g, __ldg(p), __ldg(p + 1));
+    }
   }
 #pragma unroll
-  for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  if (c != 0 || at >= n) return;
+  for (int k = 0; k < kPrepRows; ++k) {
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
+  }
+  // lane k of a row's lanes writes the k-th row's
+  float D_i = s[0];
+#pragma unroll
+  for (int k = 1; k < kPrepRows; ++k) D_i = c == k ? s[k] : D_i;
+  const long long rh = at0 + c * kPer;
+  if (c >= kPrepRows || rh >= n) return;
   const int row = (int)(rh / a.Hq), h = (int)(rh % a.Hq);
   // [B][Hq][Sq], or packed [Hq][total_q]
   const size_t i = a.cu_q ? (size_t)h * a.total_q + row
                           : ((size_t)(row / a.Sq) * a.Hq + h) * a.Sq + row % a.Sq;
   const float lse = a.lse[i];
-  if (a.dlse) s -= a.dlse[i];
+  if (a.dlse) D_i -= a.dlse[i];
   // a row that saw no key (lse = -inf) takes no part
-  a.stat[i] = make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, s);
+  a.stat[i] = make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, D_i);
   float x = -lse / a.scale;
   if (x > 1e38f || x < -1e38f) x = -1e38f;
   uint32_t l0, l1, l2, d0, d1, d2;
   split3(x, l0, l1, l2);
-  split3(-s, d0, d1, d2);
+  split3(-D_i, d0, d1, d2);
   a.ext1[i] = make_uint4(l0 | l1 << 16, l2, 0u, 0u);
   a.ext2[i] = make_uint4(d0 | d1 << 16, d2, 0u, 0u);
 }
@@ -256,19 +306,20 @@ __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __gri
 // A run: items [i0, i0 + n) of the unit of head h in group (b, x); n = 0: none.
 struct Run {
   Unit u;
-  int b, x, h, i0, n, cnt;  // cnt: items of the unit
+  int b, x, h, i0, n, cnt, first;  // cnt: items of the unit, first: the place of its first one
 };
 // The items of a slice in order, run by run of one unit.
 template <int TY, bool KV>
 struct Walk {
   const BackwardArgs& a;
-  int pos, end;  // place in the list of costs, end of the slice
+  int per, pos, end;  // a slice's share of the list of costs, place in it, end of the slice
   int g, g0;     // group, its place
   Run at;        // of the group: u, b, x, cnt
   __device__ __forceinline__ const int* pre() const { return KV ? a.pre_k : a.pre_q; }
   __device__ __forceinline__ Walk(const BackwardArgs& a_, int lane) : a(a_) {
     const int n_groups = a.B * f_tiles(a, KV);
-    const int total = pre()[n_groups], per = slice_cost(total, (int)gridDim.x);
+    const int total = pre()[n_groups];
+    per = slice_cost(total, (int)gridDim.x);
     pos = (int)min((long long)total, (long long)blockIdx.x * per);
     end = min(total, pos + per);
     g = g0 = 0;
@@ -308,6 +359,7 @@ struct Walk {
       at.h = (pos - g0) / cost;
       const int from = pos - g0 - at.h * cost, to = min(cost, from + end - pos);  // of the unit's cost
       pos += to - from;
+      at.first = g0 + at.h * cost + kRunCost;
       at.i0 = max(0, from - kRunCost);
       at.n = max(0, to - kRunCost) - at.i0;
       if (at.n > 0) break;
@@ -385,11 +437,11 @@ __device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
 template <int TY, bool KV>
 struct Stream {
   Walk<TY, KV> w;
-  Run r, next;
+  Run r;
   ItemWalk<TY, KV> y;
   int m, it;
   __device__ __forceinline__ Stream(const BackwardArgs& a, const Walk<TY, KV>& w_)
-      : w(w_), r(w.next()), next(w.next()), y(a, r), m(0), it(0) {}
+      : w(w_), r(w.next()), y(a, r), m(0), it(0) {}
   __device__ __forceinline__ void step(const BackwardArgs& a) {
     ++it;
     if (++m < r.n) {
@@ -397,9 +449,8 @@ struct Stream {
       return;
     }
     m = 0;
-    r = next;
+    r = w.next();
     y = ItemWalk<TY, KV>(a, r);
-    next = w.next();
   }
 };
 
@@ -426,8 +477,11 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
   uint64_t* bar_Pr = bar_P + 2;        // [2] P and dS used up
   uint64_t* bar_acc = bar_Pr + 2;      // a run's sums complete
   uint64_t* bar_accr = bar_acc + 1;    // they are read
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_accr + 1);
+  uint64_t* bar_out = bar_accr + 1;    // a partial is written
+  uint64_t* bar_last = bar_out + 1;    // last_flag is set
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_last + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = abort_flag + 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kSt1; ++s) { mbar_init(&full1[s], 1); mbar_init(&empty1[s], 1); }
@@ -439,6 +493,8 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
     for (int s = 0; s < 2; ++s) { mbar_init(&bar_P[s], C::kArrive); mbar_init(&bar_Pr[s], 1); }
     mbar_init(bar_acc, 1);
     mbar_init(bar_accr, 8);
+    mbar_init(bar_out, 8);
+    mbar_init(bar_last, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -691,48 +747,47 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
       return v;
     };
     float2 stat = row_stat(run);
-    int it = 0, n_run = 0;
+    int it = 0, n_run = 0, n_part = 0;
     bool ok = true;
     while (ok && run.n > 0) {
       const int f0 = run.x * kT;
       const Unit& u = run.u;
       const uint64_t nlse2 = f2pack(-stat.x, -stat.x), ndd = f2pack(-stat.y, -stat.y);
+      // Rows of Y that this thread's row admits: [lo, hi) and (dQ pass) those below `sink`; tiles inside
+      // [full_lo, full_hi) are admitted whole by every row of the F tile.
+      int lo = 0, hi, sink = 0, full_lo = 0, full_hi;
+      {
+        auto cl = [](long long x) { return (int)max(-(1LL << 30), min(x, 1LL << 30)); };
+        const long long first = KV ? f0 - u.off : f0 + u.off, own = first + r;  // of the tile, of this row
+        if constexpr (KV) {
+          hi = full_hi = u.Sq;
+          if (a.causal) {
+            lo = cl(own);
+            full_lo = cl(first + kT - 1);
+          }
+          if (a.window > 0) {
+            if (f0 + r >= a.n_sink) hi = min(hi, cl(own + a.window));
+            full_hi = min(full_hi, cl(first + a.window));
+          }
+        } else {
+          hi = full_hi = u.Skv;
+          if (a.causal) {
+            hi = min(hi, cl(own + 1));
+            full_hi = min(full_hi, cl(first + 1));
+          }
+          if (a.window > 0) {
+            lo = cl(own - a.window + 1);
+            full_lo = cl(first + kT - a.window);
+            sink = min(a.n_sink, hi);
+          }
+        }
+      }
       ItemWalk<TY, KV> y(a, run);
       for (int m = 0; m < run.n * SUB; ++m, ++it) {  // (it counts 64- or 128-column items here)
         if (m > 0 && (SUB == 1 || (m & 1) == 0)) y.step(u);
         if (TN == 64 && (it & 1) != wg) continue;  // the other warpgroup's
         const int row0 = y.row0 + (SUB == 1 ? 0 : (m & 1) * TN);
-        // columns of this thread's row: [lo, hi) and, dQ pass, those before `sink`
-        int lo = 0, hi = TN, sink = 0;
-        bool mask;
-        if constexpr (KV) {
-          const long long d0 = u.off + row0;  // key index of the tile's first row
-          const int j = f0 + r;
-          mask = row0 + TN > u.Sq;
-          hi = min(TN, u.Sq - row0);
-          if (a.causal) {
-            mask = mask || f0 + kT - 1 > d0;
-            lo = (int)min((long long)TN, max(0LL, j - d0));
-          }
-          if (a.window > 0) {
-            mask = mask || f0 + (long long)a.window < d0 + TN;
-            if (j >= a.n_sink) hi = (int)min((long long)hi, max(0LL, j + (long long)a.window - d0));
-          }
-        } else {
-          const long long pos = f0 + r + u.off;  // key index of this row
-          const long long p0 = f0 + u.off;
-          mask = row0 + TN > u.Skv;
-          hi = min(TN, u.Skv - row0);
-          if (a.causal) {
-            mask = mask || row0 + TN - 1 > p0;
-            hi = (int)min((long long)hi, max(0LL, pos + 1 - row0));
-          }
-          if (a.window > 0) {
-            mask = mask || row0 <= p0 + kT - 1 - a.window;
-            lo = (int)min((long long)TN, max(0LL, pos - a.window + 1 - row0));
-            sink = min(TN, max(0, a.n_sink - row0));
-          }
-        }
+        const bool mask = row0 < full_lo || row0 + TN > full_hi;
         const int bs = it % NS, bd = it % ND, bp = it & 1;
         const uint32_t sc = lanes + C::kS + bs * TN + c0, dc = lanes + C::kDP + bd * TN + c0;
         const uint32_t pc = lanes + C::kP + bp * C::kPStep + c0;
@@ -782,8 +837,8 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
           if (mask) {
             // (a weight out of the row's columns may be inf, dP of a column that is no row anything:
             // both operands are cleared after their rounding)
-            const int c1 = c0 + q * 32;
-            const uint32_t in = (bits_below(hi - c1) & ~bits_below(lo - c1)) | bits_below(min(sink, hi) - c1);
+            const int c1 = row0 + c0 + q * 32;
+            const uint32_t in = (bits_below(hi - c1) & ~bits_below(lo - c1)) | bits_below(sink - c1);
             if constexpr (KV) keep_bits<16>(tp, in);
             keep_bits<16>(t, in);
           }
@@ -816,9 +871,21 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
         out = a.dq + ((size_t)(u.qbase + f0) * a.Hq + run.h) * D + wg * kCols;
         row_w = (size_t)a.Hq * D;
       }
-      float4* pp = reinterpret_cast<float4*>(KV ? a.part_k : a.part_q) +
-                   ((size_t)blockIdx.x * 2 + (run.i0 > 0 ? 0 : 1)) * (kT * D * (KV ? 2 : 1) / 4) +
-                   (size_t)wg * (kCols / 4) * kT + r;
+      // 32 columns of the thread's row from `col` on; four lanes write 64 bytes of a row side by side (a
+      // row a lane made each store 32 lines)
+      auto put_rows = [&](uint4 (&q)[4], int col) {
+        transpose4(q, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = (r & ~3) + e;
+          if (row < wrote)
+            *reinterpret_cast<uint4*>(out + (size_t)row * row_w + col + (lane & 3) * 8) =
+                row < live ? q[e] : make_uint4(0, 0, 0, 0);
+        }
+      };
+      constexpr int kSlot = kT * D * (KV ? 2 : 1) / 4;  // float4s of a partial: [column / 4][row]
+      float4* const parts = reinterpret_cast<float4*>(KV ? a.part_k : a.part_q) + (size_t)wg * (kCols / 4) * kT + r;
+      float4* pp = parts + ((size_t)blockIdx.x * 2 + (run.i0 > 0 ? 0 : 1)) * kSlot;
       ok = mbar_wait_warp(bar_acc, (uint32_t)n_run & 1u, a.err, abort_flag);
       if (!ok) break;
       tc_fence_after();
@@ -844,7 +911,6 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
                   make_float4(__uint_as_float(x[e]) * f, __uint_as_float(x[e + 1]) * f, __uint_as_float(x[e + 2]) * f,
                               __uint_as_float(x[e + 3]) * f);
           } else {
-            // four lanes write 64 bytes of a row side by side: a row a lane made each store 32 lines
             uint4 q[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e, x += 8)
@@ -852,13 +918,57 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
                                 pack_bf16x2(__uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f),
                                 pack_bf16x2(__uint_as_float(x[4]) * f, __uint_as_float(x[5]) * f),
                                 pack_bf16x2(__uint_as_float(x[6]) * f, __uint_as_float(x[7]) * f));
-            transpose4(q, lane);
+            put_rows(q, c1 + c);
+          }
+        }
+      }
+      if (part) {
+        // The slice that finishes a cut unit last sums its parts, in slice order whoever it is.
+        const int c0 = run.first / w.per, c1 = (run.first + run.cnt - 1) / w.per;  // the unit's slices
+        // (mbarriers, whose waits end, in place of a barrier that a warp after a failed wait would miss)
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_out);
+        if (warp == 0) {
+          ok = mbar_wait_warp(bar_out, (uint32_t)n_part & 1u, a.err, abort_flag);
+          if (!ok) break;
+          if (lane == 0) {
+            __threadfence();
+            *last_flag = atomicAdd(a.joined + (KV ? 0 : kMaxCtas) + c0, 1) == c1 - c0;
+            mbar_arrive(bar_last);
+          }
+          __syncwarp();
+        }
+        ok = mbar_wait_warp(bar_last, (uint32_t)n_part & 1u, a.err, abort_flag);
+        if (!ok) break;
+        ++n_part;
+        if (*last_flag) {
+          __threadfence();
+          // (kStep columns of two parts in flight: one 8-column group at a time took 20 us a unit)
+#pragma unroll 1
+          for (int c = 0; c < kCols; c += kStep) {
+            float4 x[kStep / 4], y[kStep / 4];
+            const float4* p = parts + (size_t)(c / 4) * kT;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int row = (r & ~3) + e;
-              if (row < wrote)
-                *reinterpret_cast<uint4*>(out + (size_t)row * row_w + c1 + c + (lane & 3) * 8) =
-                    row < live ? q[e] : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < kStep / 4; ++e) x[e] = __ldcg(p + ((size_t)c0 * 2 + 1) * kSlot + (size_t)e * kT);
+#pragma unroll 1
+            for (int k = c0 + 1; k <= c1; ++k) {
+#pragma unroll
+              for (int e = 0; e < kStep / 4; ++e) y[e] = __ldcg(p + (size_t)k * 2 * kSlot + (size_t)e * kT);
+#pragma unroll
+              for (int e = 0; e < kStep / 4; ++e) {
+                x[e].x += y[e].x; x[e].y += y[e].y; x[e].z += y[e].z; x[e].w += y[e].w;
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < kStep / 32; ++h) {
+              uint4 q[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 u = x[h * 8 + 2 * e], v = x[h * 8 + 2 * e + 1];
+                q[e] = make_uint4(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w), pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+              }
+              put_rows(q, c + h * 32);
             }
           }
         }
@@ -871,105 +981,6 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, 512);
-}
-
-// ------------------------------------------------------------------ cut units, units without items
-constexpr int kJoinThreads = 256;
-
-// CTA c > 0 of the first `ctas`: the unit cut at the start of slice c, if no earlier slice cuts it
-// too; the further CTAs: zeros for units without items.
-template <int D, bool KV>
-__device__ void join(const BackwardArgs& a, int c, int ctas, int zero_cta, int zero_ctas) {
-  constexpr int kAccs = KV ? 2 : 1;
-  const int* pre = KV ? a.pre_k : a.pre_q;
-  const int nx = f_tiles(a, KV), n_groups = a.B * nx, H = KV ? a.Hkv : a.Hq;
-  const int total = pre[n_groups];
-  const int lane = threadIdx.x & 31;
-  // a unit's rows: [b][f0 + r], dK/dV or dQ
-  auto row_ptr = [&](const Unit& u, int b, int f0, int h, int r, int acc) -> uint16_t* {
-    const int row = f0 + r;
-    if constexpr (KV) {
-      if (row >= (a.fill ? a.Skv : u.Skv)) return nullptr;
-      return (acc == 0 ? a.dv : a.dk) + (((size_t)b * a.Skv + row) * a.Hkv + h) * D;
-    } else {
-      if (row >= u.Sq) return nullptr;
-      return a.dq + ((size_t)(u.qbase + row) * a.Hq + h) * D;
-    }
-  };
-  if (zero_cta >= 0) {
-    for (int g = zero_cta; g < n_groups; g += zero_ctas) {
-      if (pre[g + 1] != pre[g]) continue;
-      const int b = g / nx, f0 = g % nx * kT;
-      const Unit u = unit_of<BwdCfg<D, KV>::TY, KV>(a, b, g % nx);
-      for (int i = threadIdx.x; i < kAccs * H * kT * (D / 8); i += kJoinThreads) {
-        const int e = i % (D / 8), h = i / (D / 8) % H, r = i / (D / 8) / H % kT, acc = i / (D / 8) / H / kT;
-        uint16_t* out = row_ptr(u, b, f0, h, r, acc);
-        if (out) *reinterpret_cast<uint4*>(out + e * 8) = make_uint4(0, 0, 0, 0);
-      }
-    }
-    if (!KV && a.cu_q && a.fill) {  // rows of no sequence
-      const long long w = (long long)a.Hq * (D / 8), step = (long long)zero_ctas * kJoinThreads;
-      const int c0 = min(max(a.cu_q[0], 0), a.total_q), c1 = min(max(a.cu_q[a.B], c0), a.total_q);
-      for (long long i = (long long)zero_cta * kJoinThreads + threadIdx.x; i < (c0 + (long long)a.total_q - c1) * w; i += step)
-        reinterpret_cast<uint4*>(a.dq)[i < c0 * w ? i : i + (c1 - c0) * w] = make_uint4(0, 0, 0, 0);
-    }
-    return;
-  }
-  const int per = slice_cost(total, ctas);
-  const long long at = (long long)c * per;
-  if (c == 0 || at >= total) return;
-  int lo = 0, hi = n_groups;
-  while (hi - lo > 1) {
-    const int step = max(1, (hi - lo) / 32);
-    const int p = min(lo + (lane + 1) * step, hi);
-    const unsigned over = __ballot_sync(0xFFFFFFFFu, p >= hi || pre[p] > at);
-    const int k = over ? __ffs(over) - 1 : 32;
-    hi = k < 32 ? min(lo + (k + 1) * step, hi) : hi;
-    lo = lo + k * step;
-  }
-  const int b = lo / nx, f0 = lo % nx * kT;
-  const Unit u = unit_of<BwdCfg<D, KV>::TY, KV>(a, b, lo % nx);
-  const int cnt = unit_items<KV>(a, u);
-  const int cost = unit_cost(cnt), h = (int)(at - pre[lo]) / cost;
-  const int u0 = pre[lo] + h * cost + kRunCost, u1 = u0 + cnt;  // the places of the unit's items
-  const int c0 = u0 / per, c1 = (u1 - 1) / per;                 // its slices
-  if (at <= u0 || c != c0 + 1) return;
-  const float4* part = reinterpret_cast<const float4*>(KV ? a.part_k : a.part_q);
-  constexpr int kSlot = kT * D * kAccs / 4;
-  // 8 columns of a row at a time
-  for (int i = (int)blockIdx.y * kJoinThreads + threadIdx.x; i < kAccs * (D / 8) * kT; i += kJoinThreads * gridDim.y) {
-    const int r = i % kT, e = i / kT % (D / 8), acc = i / kT / (D / 8);
-    const size_t off = ((size_t)acc * (D / 4) + 2 * e) * kT + r;
-    const float4* p = part + ((size_t)c0 * 2 + 1) * kSlot + off;
-    float4 x = __ldcg(p), y = __ldcg(p + kT);
-    for (int k = c0 + 1; k <= c1; ++k) {
-      p = part + (size_t)k * 2 * kSlot + off;
-      const float4 x2 = __ldcg(p), y2 = __ldcg(p + kT);
-      x.x += x2.x; x.y += x2.y; x.z += x2.z; x.w += x2.w;
-      y.x += y2.x; y.y += y2.y; y.z += y2.z; y.w += y2.w;
-    }
-    uint16_t* out = row_ptr(u, b, f0, h, r, acc);
-    if (out == nullptr) continue;
-    const bool live = !KV || f0 + r < u.Skv;
-    *reinterpret_cast<uint4*>(out + e * 8) =
-        live ? make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w))
-             : make_uint4(0, 0, 0, 0);
-  }
-}
-
-constexpr int kZeroCtas = 16;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) backward_join_kernel(const __grid_constant__ BackwardArgs a, int ck, int cq) {
-  // dK/dV slices, dQ slices, then the units without items
-  const int x = (int)blockIdx.x;
-  if (x < ck) join<D, true>(a, x, ck, -1, 0);
-  else if (x < ck + cq) join<D, false>(a, x - ck, cq, -1, 0);
-  else {
-    const int z = (x - ck - cq) * (int)gridDim.y + (int)blockIdx.y, nz = kZeroCtas * (int)gridDim.y;
-    join<D, true>(a, 0, ck, z, nz);
-    join<D, false>(a, 0, cq, z, nz);
-  }
 }
 
 template <int D, bool KV>
@@ -986,15 +997,13 @@ template <int D>
 cudaError_t launch_d(const BackwardArgs& a, cudaStream_t stream) {
   const bool any = a.total_q > 0 && a.Sq > 0 && a.Skv > 0;  // else the gradients are zeros
   const long long threads = any ? (long long)a.total_q * a.Hq * (D / 8) : 0;
-  const unsigned grid = 2 + (unsigned)((threads + kPrepThreads - 1) / kPrepThreads);
+  const unsigned grid = 2 + kZeroCtas + (unsigned)((threads + kPrepThreads * kPrepRows - 1) / (kPrepThreads * kPrepRows));
   if (a.o_bf16) backward_prep_kernel<D, true><<<grid, kPrepThreads, 0, stream>>>(a);
   else backward_prep_kernel<D, false><<<grid, kPrepThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (any && e == cudaSuccess) e = launch_pass<D, true>(a, a.ctas_k, stream);
   if (any && e == cudaSuccess) e = launch_pass<D, false>(a, a.ctas_q, stream);
-  if (e != cudaSuccess) return e;
-  backward_join_kernel<D><<<dim3(a.ctas_k + a.ctas_q + kZeroCtas, 4), kJoinThreads, 0, stream>>>(a, a.ctas_k, a.ctas_q);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
