@@ -14,9 +14,10 @@ from ._binding import (  # noqa: F401
     decode_packed, decode_split, decode_split_packed, load, merge, prefill, prefill_schedule,
     prefill_varlen, prefill_window, sync_check)
 from ._serving import (  # noqa: F401
-    attn_decode_paged, attn_decode_paged_splits, attn_evict, attn_key_weights, attn_prefill_paged,
-    attn_prefill_paged_splits, attn_rope_append, decode_paged, evict, key_weights, prefill_paged, rope_append,
-    rope_frequencies)
+    attn_decode_paged, attn_decode_paged_splits, attn_decode_window, attn_decode_window_splits, attn_evict,
+    attn_key_weights, attn_prefill_paged, attn_prefill_paged_splits, attn_rope_append, attn_rope_append_axes,
+    attn_rope_rotate, decode_paged, decode_window, evict, key_weights, prefill_paged, rope_append, rope_axes,
+    rope_frequencies, rope_rotate)
 from ._backward import (  # noqa: F401
     attn_prefill_backward, attn_prefill_backward_workspace, attn_prefill_varlen_backward, prefill_backward,
     prefill_varlen_backward)

@@ -85,7 +85,12 @@ def load(path: str | None = None):
         lib.attn_prefill_varlen_backward.argtypes = [vp] * 12 + [i] * 10 + [f, i, i, vp, ull, vp]
         lib.attn_prefill_backward_workspace.argtypes = [i] * 3 + [ll] + [i] * 3
         lib.attn_prefill_backward_workspace.restype = ull
-        for name in ("attn_prefill_backward", "attn_prefill_varlen_backward", "attn_rope_append", "attn_prefill_paged", "attn_prefill_paged_splits", "attn_decode_paged",
+        lib.attn_rope_append_axes.argtypes = [vp] * 3 + [ll] * 3 + [vp] * 2 + [i] + [vp] * 7 + [i] * 7 + [f] + [i] * 3 + [vp]
+        lib.attn_rope_rotate.argtypes = [vp, vp, ll, ll, vp, vp, i, vp, vp, vp, ll, ll] + [i] * 7 + [f, vp]
+        lib.attn_decode_window.argtypes = [vp] * 5 + [i] * 9 + [f, i, i, vp, vp, vp, vp, i, vp, vp]
+        lib.attn_decode_window_splits.argtypes = [i] * 7 + [vp]
+        for name in ("attn_prefill_backward", "attn_prefill_varlen_backward", "attn_rope_append_axes",
+                     "attn_rope_rotate", "attn_decode_window", "attn_decode_window_splits", "attn_rope_append", "attn_prefill_paged", "attn_prefill_paged_splits", "attn_decode_paged",
                      "attn_decode_paged_splits", "attn_key_weights", "attn_evict"):
             getattr(lib, name).restype = i
         for name in ("attn_prefill_fwd", "attn_prefill_varlen", "attn_prefill_window",

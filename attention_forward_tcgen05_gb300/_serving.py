@@ -1,6 +1,7 @@
-"""The paged-cache serving calls: rotary positions with the cache append, attention of
-new tokens over pages (chunks and single tokens), accumulated attention weights and
-eviction by them (the second half of include/attn.h).
+"""The paged-cache serving calls: rotary positions (of one or several axes) with the cache
+append or without a cache, attention of new tokens over pages (chunks and single tokens,
+windowed too), accumulated attention weights and eviction by them (the second half of
+include/attn.h).
 
 As in ``_binding``: the raw entry points keep the C names and argument order, and the
 torch helpers only check, allocate outputs and pass pointers and the stream.
@@ -34,6 +35,22 @@ def _torch():
 # ------------------------------------------------------------------ raw C ABI
 def attn_rope_append(*args) -> int:
     return load().attn_rope_append(*args)
+
+
+def attn_rope_append_axes(*args) -> int:
+    return load().attn_rope_append_axes(*args)
+
+
+def attn_rope_rotate(*args) -> int:
+    return load().attn_rope_rotate(*args)
+
+
+def attn_decode_window(*args) -> int:
+    return load().attn_decode_window(*args)
+
+
+def attn_decode_window_splits(B, Hq, Hkv, max_kv, window, n_sink, d, min_rows) -> int:
+    return load().attn_decode_window_splits(B, Hq, Hkv, max_kv, window, n_sink, d, min_rows)
 
 
 def attn_prefill_paged(*args) -> int:
@@ -177,7 +194,14 @@ def _decode_splits(B, Hq, Hkv, max_kv, d, code):
     return max(n, 1), rows.value
 
 
-# Workspaces of prefill_paged and decode_paged: kept for each stream, whose launches are
+@functools.lru_cache(maxsize=1024)
+def _window_splits(B, Hq, Hkv, max_kv, window, n_sink, d):
+    rows = ctypes.c_int(1)
+    n = attn_decode_window_splits(B, Hq, Hkv, max_kv, window, n_sink, d, ctypes.addressof(rows))
+    return max(n, 1), rows.value
+
+
+# Workspaces of prefill_paged, decode_paged and decode_window: kept for each stream, whose launches are
 # ordered; a call holds _launching while it makes its launches, so that another thread's on the
 # same stream do not come between two of them.  A call being captured gets its own (two graphs
 # may replay at the same time).  They grow to the largest call seen and stay for the process.
@@ -247,6 +271,32 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, device="cuda", factor:
     return f.to(device), amp
 
 
+def rope_axes(sections, base: float = 10000.0, layout: str = "blocks", device="cuda"):
+    """Frequencies and axes of positions with several axes, for ``rope_append`` and
+    ``rope_rotate``: (inv_freq float64 [n], axes int32 [n]), n = sum(sections) = rot_dim / 2.
+
+    sections[a] rotated pairs follow axis a.  ``"blocks"``: the first sections[0] pairs, then
+    the next sections[1], ..., with the frequencies base^(-m / n) of one series over all
+    pairs; ``"dealt"``: pairs dealt to the axes in turn while an axis has any left, same
+    frequencies; ``"separate"``: blocks, each axis with a series of its own,
+    base^(-i / sections[a])."""
+    torch = _torch()
+    sections = [int(s) for s in sections]
+    n = sum(sections)
+    if not 1 <= len(sections) <= 8 or min(sections) < 0 or n < 1:
+        raise ValueError("sections: pairs of 1 to 8 axes, at least one in all")
+    if not (base > 0 and math.isfinite(base)):
+        raise ValueError("base must be positive and finite")
+    series = lambda k: torch.pow(torch.tensor(base, dtype=torch.float64), -torch.arange(k, dtype=torch.float64) / max(k, 1))
+    axes = [a for a, s in enumerate(sections) for _ in range(s)]
+    if layout == "dealt":
+        axes = [a for i in range(max(sections)) for a, s in enumerate(sections) if i < s]
+    elif layout not in ("blocks", "separate"):
+        raise ValueError(f"unknown layout {layout!r}")
+    f = torch.cat([series(s) for s in sections]) if layout == "separate" else series(n)
+    return f.to(device), torch.tensor(axes, dtype=torch.int32, device=device)
+
+
 def _token_rows(t, name, bf16, dev, total, H, d):
     """Rows of tokens [total, H, d] with any stride between tokens (a view of a fused
     projection's output, say): (pointer, stride in elements)."""
@@ -265,7 +315,7 @@ def _token_rows(t, name, bf16, dev, total, H, d):
 
 
 def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_seqlens_q=None, positions=None,
-                interleaved: bool = False, amp: float = 1.0, out=None, stream=None):
+                interleaved: bool = False, amp: float = 1.0, out=None, stream=None, axes=None):
     """Rotate the new tokens' queries and keys and append keys and values to the cache
     (attn_rope_append).
 
@@ -274,14 +324,16 @@ def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_
     tokens are its last ones.  cu_seqlens_q int32 [B+1] gives each sequence's tokens; None
     means one token per sequence.  inv_freq float64 [rot_dim / 2] (None: no rotation), amp
     as from ``rope_frequencies``; positions int32 [total] (None: a token's key index).
+    With axes int32 [rot_dim / 2] (``rope_axes``), positions int32 [n_axes, total] holds a
+    token's position on each axis, and pair m follows row axes[m] (attn_rope_append_axes).
     Writes kcache / vcache; returns the rotated q [total,Hq,d] (``out`` if given; it may be
     q itself when q is contiguous), or None without q."""
     torch = _torch()
     dev = _device(k, "k")
     if stream is not None or dev != torch._C._cuda_getDevice():
         return _elsewhere(lambda: rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table, cu_seqlens_q,
-                                              positions, interleaved, amp, out), k, stream,
-                          (q, k, v, kcache, vcache, kv_lens, inv_freq, page_table, cu_seqlens_q, positions, out))
+                                              positions, interleaved, amp, out, None, axes), k, stream,
+                          (q, k, v, kcache, vcache, kv_lens, inv_freq, page_table, cu_seqlens_q, positions, out, axes))
     handle = torch._C._cuda_getCurrentRawStream(dev)
     np_ = _need(kv_lens, "kv_lens", torch.int32, 1, dev)
     total, B = k.shape[0], kv_lens.shape[0]
@@ -304,17 +356,93 @@ def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_
         cu = _sized(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, B + 1)
     elif total != B:
         raise ValueError("without cu_seqlens_q there must be one token per sequence")
-    if positions is not None:
+    if axes is not None:
+        if inv_freq is None or positions is None:
+            raise ValueError("axes need inv_freq and positions")
+        pos = _need(positions, "positions", torch.int32, 2, dev)
+        n_axes = positions.shape[0]
+        _sized(positions, "positions", torch.int32, dev, n_axes, total)
+    elif positions is not None:
         pos = _sized(positions, "positions", torch.int32, dev, total)
     rot = 0
     if inv_freq is not None:
         fr = _need(inv_freq, "inv_freq", torch.float64, 1, dev)
         rot = 2 * inv_freq.shape[0]
+    if axes is not None:
+        ap = _sized(axes, "axes", torch.int32, dev, rot // 2)
+        rc = load().attn_rope_append_axes(qr, kr, vr, qs, ks, vs, pos, ap, n_axes, fr, op, kp, vp, tp, cu, np_, B, Hq,
+                                          Hkv, total, d, rot, int(interleaved), amp, max_pages, page, n_pages, handle)
+        if rc != ATTN_OK:
+            raise AttnError(rc, "attn_rope_append_axes")
+        return out
     rc = load().attn_rope_append(qr, kr, vr, qs, ks, vs, pos, fr, op, kp, vp, tp, cu, np_, B, Hq, Hkv, total, d, rot,
                                  int(interleaved), amp, max_pages, page, n_pages, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_rope_append")
     return out
+
+
+def _rotated(t, name, out, dev, total):
+    """(pointer, stride, out, its pointer, its stride, heads, head dim) of a side of
+    rope_rotate."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        _refuse(t, name, torch.bfloat16, 3, dev, contiguous=False)
+    n, H, d = t.shape
+    p, s = _token_rows(t, name, torch.bfloat16, dev, total, H, d)
+    if out is None:
+        out = torch.empty((total, H, d), dtype=torch.bfloat16, device="cuda")
+        return p, s, out, out.data_ptr(), H * d, H, d
+    op, os = _token_rows(out, f"out of {name}", torch.bfloat16, dev, total, H, d)
+    return p, s, out, op, os, H, d
+
+
+def rope_rotate(q, k, inv_freq, positions, axes=None, interleaved: bool = False, amp: float = 1.0,
+                inverse: bool = False, out=None, stream=None):
+    """Rotate queries and keys that go to no cache (attn_rope_rotate): an encoder's, or a
+    training step's.  inverse=True rotates back (amp as in the forward call): with the
+    gradients of the rotated q and k for q and k it returns those of the unrotated ones.
+
+    q [total,Hq,d] and k [total,Hk,d] bf16 (either may be None), rows of tokens at any
+    stride; inv_freq float64 [rot_dim / 2]; positions int32 [total], or with axes int32
+    [rot_dim / 2] (``rope_axes``) int32 [n_axes, total].  Returns (q, k) rotated, into ``out``
+    = (q_out, k_out) if given: rows at any stride, which do not overlap the inputs, or are
+    the inputs themselves."""
+    torch = _torch()
+    lead, name = (q, "q") if q is not None else (k, "k")
+    dev = _device(lead, name)
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: rope_rotate(q, k, inv_freq, positions, axes, interleaved, amp, inverse, out), lead,
+                          stream, (q, k, inv_freq, positions, axes, out))
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    total = lead.shape[0]
+    qo, ko = out if out is not None else (None, None)
+    qr = kr = qop = kop = None
+    qs = ks = qos = kos = Hq = Hk = 0
+    if q is not None:
+        qr, qs, qo, qop, qos, Hq, d = _rotated(q, "q", qo, dev, total)
+    if k is not None:
+        kr, ks, ko, kop, kos, Hk, dk = _rotated(k, "k", ko, dev, total)
+        if q is not None and dk != d:
+            raise ValueError(f"q and k differ in head dim: {d} and {dk}")
+        d = dk
+    if (q is None and qo is not None) or (k is None and ko is not None):
+        raise ValueError("out without its input")
+    fr = _need(inv_freq, "inv_freq", torch.float64, 1, dev)
+    rot = 2 * inv_freq.shape[0]
+    ap, n_axes = None, 1
+    if axes is None:
+        pos = _sized(positions, "positions", torch.int32, dev, total)
+    else:
+        ap = _sized(axes, "axes", torch.int32, dev, rot // 2)
+        pos = _need(positions, "positions", torch.int32, 2, dev)
+        n_axes = positions.shape[0]
+        _sized(positions, "positions", torch.int32, dev, n_axes, total)
+    rc = load().attn_rope_rotate(qr, kr, qs, ks, pos, ap, n_axes, fr, qop, kop, qos, kos, Hq, Hk, total, d, rot,
+                                 int(interleaved), int(inverse), amp, handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope_rotate")
+    return qo, ko
 
 
 # ------------------------------------------------------------------ attention over pages
@@ -442,6 +570,76 @@ def decode_paged(q, kcache, vcache, page_table, kv_lens, n_splits: int = 0, min_
                                    min_rows_per_split, pp, ps, op, lp, code, cp, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged")
+    return o, lse
+
+
+def decode_window(q, kcache, vcache, kv_lens, window: int, n_sink: int = 0, page_table=None, n_splits: int = 0,
+                  min_rows_per_split: int = 1, scale: float | None = None, out_dtype=None, stream=None, out=None,
+                  parts=None, counters=None, max_kv: int | None = None):
+    """``decode`` with the sliding window and sinks of ``prefill_window``, over a paged or
+    dense cache (attn_decode_window): a sequence's token attends to its last ``window`` keys
+    and its first ``n_sink``.  Returns (o [B,Hq,d], lse [B,Hq]).
+
+    q [B,Hq,d]; kv_lens int32 [B] counts the token's own key; page_table None means the dense
+    cache [B,max_kv,Hkv,d].  Pages that hold none of those keys are not looked up: their
+    table entries may be anything.  n_splits = 0 chooses the key splits and their least rows from
+    the sizes and max_kv (the longest sequence's keys, by default the cache's capacity).  The
+    split partials and counters are kept for the stream, as decode_paged's."""
+    torch = _torch()
+    dev = _device(q, "q")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: decode_window(q, kcache, vcache, kv_lens, window, n_sink, page_table, n_splits,
+                                                min_rows_per_split, scale, out_dtype, None, out, parts, counters,
+                                                max_kv), q, stream,
+                          (q, kcache, vcache, kv_lens, page_table, out, parts, counters))
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    qp = _need(q, "q", torch.bfloat16, 3, dev)
+    B, Hq, dq = q.shape
+    np_ = _sized(kv_lens, "kv_lens", torch.int32, dev, B)
+    if vcache is None:
+        raise TypeError("vcache must be a CUDA tensor")
+    kp, vp, tp, Hkv, d, max_pages, page, n_pages = _cache(kcache, vcache, page_table, B, dev)
+    if dq != d:
+        raise ValueError(f"q and the cache differ in head dim: {dq} and {d}")
+    window, n_sink = int(window), int(n_sink)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        o = torch.empty_like(q) if out_dtype in (None, torch.bfloat16) else torch.empty_like(q, dtype=out_dtype)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device="cuda")
+        op, lp = o.data_ptr(), lse.data_ptr()
+    else:
+        o, lse = out
+        op = _sized(o, "out[0]", o.dtype, dev, B, Hq, d)
+        lp = _sized(lse, "out[1]", torch.float32, dev, B, Hq)
+    code = _out_code(o.dtype)
+    lib = load()
+    if n_splits == 0:
+        if parts is not None:
+            n_splits = parts[0].shape[2]
+        else:
+            n_splits, min_rows_per_split = _window_splits(B, Hq, Hkv, max_pages * page if max_kv is None else max_kv,
+                                                          window, n_sink, d)
+    pp = ps = cp = None
+    if n_splits > 1:
+        rows = B * Hq * n_splits
+        if parts is None:
+            work = _workspace(rows * (d + 1), dev, handle)
+            pp = work.data_ptr()
+            ps = pp + rows * d * 4
+        else:
+            pp = _sized(parts[0], "parts[0]", torch.float32, dev, B, Hq, n_splits, d)
+            ps = _sized(parts[1], "parts[1]", torch.float32, dev, B, Hq, n_splits)
+        if counters is None:
+            counters = _stream_counters(B * Hq, dev, handle)
+        elif counters.dtype != torch.int32 or counters.get_device() != dev or counters.numel() < B * Hq:
+            raise TypeError("counters must be a CUDA int32 tensor of at least B*Hq entries")
+        cp = counters.data_ptr()
+    with _launching:
+        rc = lib.attn_decode_window(qp, kp, vp, tp, np_, B, Hq, Hkv, d, max_pages, page, n_pages, window, n_sink,
+                                    scale, n_splits, min_rows_per_split, pp, ps, op, lp, code, cp, handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_window")
     return o, lse
 
 

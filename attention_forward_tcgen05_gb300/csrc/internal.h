@@ -140,7 +140,9 @@ struct DecodeArgs {
   void* o;       // [B][Hq][d], fp32 or bf16 (o_bf16)
   float* lse;    // [B][Hq]
   int o_bf16;
-  PagedKV kv;    // decode_paged.cu only: the cache instead of tm_k / tm_v
+  PagedKV kv;    // decode_paged.cuh only: the cache instead of tm_k / tm_v
+  // decode_window.cu only: keys admitted, CTAs of a (sequence, KV head, split) and their query heads
+  int window, n_sink, head_ctas, cta_heads;
 };
 
 struct MergeArgs {
@@ -160,13 +162,29 @@ struct MergeArgs {
 struct RopeArgs {
   const uint16_t *q, *k, *v;              // rows of token t at + t * stride (elements)
   long long q_stride, k_stride, v_stride;
-  const int* positions;                   // [total], or nullptr: the token's key index
+  const int* positions;                   // [n_axes][total], or nullptr: the token's key index
+  const int* axes;                        // [rot / 2] row of positions of each pair, or nullptr: the first
+  int n_axes;
   const double* inv_freq;                 // [rot / 2]
   uint16_t* q_out;                        // [total][Hq][d]
   uint16_t *kc, *vc;                      // the pools of kv, written
   PagedKV kv;
   const int *cu_q, *kv_lens;              // cu_q == nullptr: one token per sequence
   int B, Hq, Hkv, total, d, rot, interleaved;
+  float amp;
+  uint32_t* err;
+};
+
+// Rotary positions without a cache (rope.cu); heads of q first, then of k.
+struct RotateArgs {
+  const uint16_t *q, *k;                  // rows of token t at + t * stride (elements)
+  uint16_t *q_out, *k_out;
+  long long q_stride, k_stride, qo_stride, ko_stride;
+  const int* positions;                   // [n_axes][total]
+  const int* axes;
+  int n_axes;
+  const double* inv_freq;
+  int Hq, Hk, total, d, rot, interleaved, inverse;
   float amp;
   uint32_t* err;
 };
@@ -282,6 +300,7 @@ cudaError_t launch_prefill_paged_f32(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_empty_kv(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_split(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_paged(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_window(const DecodeArgs& a, cudaStream_t stream);
 // CTAs of that kernel that `sms` SMs run at once.
 int decode_paged_slots(int d, int G, int sms);
 // The persistent prefill's unit schedule for BH = B * Hq heads over `grid` CTAs:
@@ -289,7 +308,9 @@ int decode_paged_slots(int d, int G, int sms);
 // 0 when the launch keeps the wave deal (sched left empty), -1 on bad arguments.
 int build_prefill_schedule(int BH, int Sq, int Skv, int causal, int grid, std::vector<int>& sched);
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream);
+constexpr int kMaxRopeAxes = 8;
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_rotate(const RotateArgs& a, cudaStream_t stream);
 cudaError_t launch_key_weights(const KeyWeightArgs& a, cudaStream_t stream);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t stream);

@@ -1,6 +1,6 @@
 // paged_api.cu -- the C ABI of the paged-cache serving calls (include/attn.h): argument
-// validation and launches of rope.cu, prefill_paged.cu, decode_paged.cu, key_weights.cu
-// and evict.cu.
+// validation and launches of rope.cu, prefill_paged.cu, decode_paged.cu, decode_window.cu,
+// key_weights.cu and evict.cu.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -100,6 +100,35 @@ int prefill_splits(int B, int Hq, int total_q, int max_sq, int max_kv, int d, in
   return n_best;
 }
 
+// Key splits of a decode on warp-level mma, `units` CTAs a split of up to `heads` query heads over at
+// most max_kv keys, and their least rows.
+int mma_splits(double units, int heads, int B, int max_kv, int d, int* min_rows) {
+  const long long alone = (long long)(kSms / units);  // splits of a unit while each has an SM
+  long long n;
+  if (alone >= (d == 256 ? 1 : 4)) {
+    // one CTA of many warps an SM; above 32 splits only of 1024 keys and more, as the merge
+    // grows with them (4 units of 16000 keys: 13.8 us with 32, 14.9 with 38; of 117000: 48 with
+    // 38, 52 with 19; one unit of 100000: 24 with 64, 31 with 32)
+    n = std::min(std::min(alone, 64LL), std::max(32LL, max_kv / 1024LL));
+  } else if (alone == 1 && max_kv <= 2048) {
+    n = 1;  // short sequences whole, with an SM each (128 units: 15.8 us, 21 with narrow CTAs)
+  } else {
+    // as many narrow CTAs as run at once.  A batch's lengths differ, so a few splits are
+    // rounded up (64 units of up to 8000 keys: 26.6 us with 8 splits, 29.3 with 2 wide ones);
+    // from half a wave of units on, whole sequences do best (1024 units of up to 1000 keys: 51
+    // against 59 us)
+    const double q = attn::decode_paged_slots(d, heads, kSms) / units;
+    n = q < 2 ? 1 : (long long)(q <= 8 && B > 1 ? std::ceil(q) : q);
+  }
+  n = std::max(1LL, std::min(n, (max_kv + 191LL) / 192));
+  *min_rows = n > 1 ? 192 : 1;
+  return (int)n;
+}
+
+// Query heads of a CTA of the windowed decode and its CTAs a group: groups of more than 16 are shared
+// evenly.
+int window_head_ctas(int G) { return (G + attn::kMaxHeadsPerCta - 1) / attn::kMaxHeadsPerCta; }
+
 // The launches of a prefill over pages (arguments checked, a.pack and the rows set): query and
 // output maps over [nb][ns][Hq][d], pool maps, the kernel, and the merge of key splits into
 // m.
@@ -128,13 +157,9 @@ int launch_paged(attn::PrefillArgs& a, const attn_bf16_t* q, int ns, int nb, att
   return from_cuda(attn::launch_merge(m, s));
 }
 
-}  // namespace
-
-extern "C" {
-
-int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16_t* v, long long q_stride,
-                     long long k_stride, long long v_stride, const int* positions, const double* inv_freq,
-                     attn_bf16_t* q_out, attn_bf16_t* kcache, attn_bf16_t* vcache, const int* page_table,
+int rope_append_impl(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16_t* v, long long q_stride,
+                     long long k_stride, long long v_stride, const int* positions, const int* axes, int n_axes,
+                     const double* inv_freq, attn_bf16_t* q_out, attn_bf16_t* kcache, attn_bf16_t* vcache, const int* page_table,
                      const int* cu_seqlens_q, const int* kv_lens, int B, int Hq, int Hkv, int total, int d,
                      int rot_dim, int interleaved, float amp, int max_pages, int page_size, int num_pages,
                      attn_stream_t stream) {
@@ -147,6 +172,7 @@ int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16
   if (B == 0 || total == 0) return ATTN_OK;
   if (!ok16(k) || !ok16(v) || !ok16(kcache) || !ok16(vcache) || !ok4(kv_lens)) return ATTN_ERR_INVALID_ARG;
   if ((q == nullptr) != (q_out == nullptr) || !aligned(q, 16) || !aligned(q_out, 16)) return ATTN_ERR_INVALID_ARG;
+  if (axes && (n_axes < 1 || n_axes > attn::kMaxRopeAxes || !ok4(axes) || !positions)) return ATTN_ERR_INVALID_ARG;
   if (!aligned(positions, 4) || !aligned(cu_seqlens_q, 4)) return ATTN_ERR_INVALID_ARG;
   if (rot_dim > 0 && (inv_freq == nullptr || !aligned(inv_freq, 8))) return ATTN_ERR_INVALID_ARG;
   // rows of tokens: at least the heads' width, in whole 16-byte units
@@ -160,7 +186,7 @@ int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16
   std::memset(&a, 0, sizeof(a));
   a.q = q; a.k = k; a.v = v;
   a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
-  a.positions = positions; a.inv_freq = inv_freq; a.q_out = q_out;
+  a.positions = positions; a.axes = axes; a.n_axes = axes ? n_axes : 1; a.inv_freq = inv_freq; a.q_out = q_out;
   a.kc = kcache; a.vc = vcache;
   a.kv = cache(kcache, vcache, page_table, max_pages, page_size, num_pages);
   a.cu_q = cu_seqlens_q; a.kv_lens = kv_lens;
@@ -169,6 +195,71 @@ int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16
   a.err = attn::device_err_word();
   if (a.err == nullptr) return ATTN_ERR_CUDA;
   return from_cuda(attn::launch_rope_append(a, stream_of(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16_t* v, long long q_stride,
+                     long long k_stride, long long v_stride, const int* positions, const double* inv_freq,
+                     attn_bf16_t* q_out, attn_bf16_t* kcache, attn_bf16_t* vcache, const int* page_table,
+                     const int* cu_seqlens_q, const int* kv_lens, int B, int Hq, int Hkv, int total, int d,
+                     int rot_dim, int interleaved, float amp, int max_pages, int page_size, int num_pages,
+                     attn_stream_t stream) {
+  return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, nullptr, 1, inv_freq, q_out, kcache, vcache,
+                          page_table, cu_seqlens_q, kv_lens, B, Hq, Hkv, total, d, rot_dim, interleaved, amp,
+                          max_pages, page_size, num_pages, stream);
+}
+
+int attn_rope_append_axes(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16_t* v, long long q_stride,
+                          long long k_stride, long long v_stride, const int* positions, const int* axes, int n_axes,
+                          const double* inv_freq, attn_bf16_t* q_out, attn_bf16_t* kcache, attn_bf16_t* vcache,
+                          const int* page_table, const int* cu_seqlens_q, const int* kv_lens, int B, int Hq, int Hkv,
+                          int total, int d, int rot_dim, int interleaved, float amp, int max_pages, int page_size,
+                          int num_pages, attn_stream_t stream) {
+  if (n_axes < 1 || n_axes > attn::kMaxRopeAxes) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim == 0) return ATTN_ERR_UNSUPPORTED;  // (an append alone has no axes)
+  if (B > 0 && total > 0 && (!ok4(axes) || !ok4(positions))) return ATTN_ERR_INVALID_ARG;
+  return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, axes, n_axes, inv_freq, q_out, kcache,
+                          vcache, page_table, cu_seqlens_q, kv_lens, B, Hq, Hkv, total, d, rot_dim, interleaved, amp,
+                          max_pages, page_size, num_pages, stream);
+}
+
+int attn_rope_rotate(const attn_bf16_t* q, const attn_bf16_t* k, long long q_stride, long long k_stride,
+                     const int* positions, const int* axes, int n_axes, const double* inv_freq, attn_bf16_t* q_out,
+                     attn_bf16_t* k_out, long long q_out_stride, long long k_out_stride, int Hq, int Hk, int total,
+                     int d, int rot_dim, int interleaved, int inverse, float amp, attn_stream_t stream) {
+  if (Hq < 0 || Hk < 0 || Hq + (long long)Hk < 1 || total < 0 || !std::isfinite(amp)) return ATTN_ERR_INVALID_ARG;
+  if (n_axes < 1 || n_axes > attn::kMaxRopeAxes || (axes == nullptr && n_axes != 1)) return ATTN_ERR_INVALID_ARG;
+  if (d < 16 || d > 256 || d % 16 != 0 || rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+  if (total == 0) return ATTN_OK;
+  const struct {
+    const attn_bf16_t *in, *out;
+    long long stride, out_stride;
+    int H;
+  } sides[2] = {{q, q_out, q_stride, q_out_stride, Hq}, {k, k_out, k_stride, k_out_stride, Hk}};
+  for (const auto& x : sides) {
+    if (x.H == 0) continue;
+    const long long w = (long long)x.H * d;
+    if (!ok16(x.in) || !ok16(x.out) || x.stride < w || x.out_stride < w || x.stride % 8 || x.out_stride % 8)
+      return ATTN_ERR_INVALID_ARG;
+    // in place only over itself
+    if (x.in == x.out && x.stride != x.out_stride) return ATTN_ERR_INVALID_ARG;
+  }
+  if (!ok4(positions) || !aligned(axes, 4) || inv_freq == nullptr || !aligned(inv_freq, 8)) return ATTN_ERR_INVALID_ARG;
+  // (eight tokens' chunks are counted in 32 bits)
+  if ((Hq + (long long)Hk) * (d / 16) > 0x7FFFFFFFLL / 8) return ATTN_ERR_INVALID_ARG;
+  attn::RotateArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.qo_stride = q_out_stride; a.ko_stride = k_out_stride;
+  a.positions = positions; a.axes = axes; a.n_axes = n_axes; a.inv_freq = inv_freq;
+  a.Hq = Hq; a.Hk = Hk; a.total = total; a.d = d; a.rot = rot_dim;
+  a.interleaved = interleaved ? 1 : 0; a.inverse = inverse ? 1 : 0; a.amp = amp;
+  a.err = attn::device_err_word();
+  if (a.err == nullptr) return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_rope_rotate(a, stream_of(stream)));
 }
 
 int attn_prefill_paged_splits(int B, int Hq, int Hkv, int total_q, int max_sq, int max_kv, int d, int* min_rows) {
@@ -235,27 +326,7 @@ int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int o_dt
     return ATTN_ERR_INVALID_ARG;
   if (decode_on_tiles(B, Hq, Hkv, o_dtype))
     return prefill_splits(B, Hq, B, 1, max_kv, d, std::min(Hq / Hkv, attn::kPrefillTileM), min_rows);
-  const double units = std::max(1.0, (double)B * Hkv);
-  const long long alone = (long long)(kSms / units);  // splits of a unit while each has an SM
-  long long n;
-  if (alone >= (d == 256 ? 1 : 4)) {
-    // one CTA of many warps an SM; above 32 splits only of 1024 keys and more, as the merge
-    // grows with them (4 units of 16000 keys: 13.8 us with 32, 14.9 with 38; of 117000: 48 with
-    // 38, 52 with 19; one unit of 100000: 24 with 64, 31 with 32)
-    n = std::min(std::min(alone, 64LL), std::max(32LL, max_kv / 1024LL));
-  } else if (alone == 1 && max_kv <= 2048) {
-    n = 1;  // short sequences whole, with an SM each (128 units: 15.8 us, 21 with narrow CTAs)
-  } else {
-    // as many narrow CTAs as run at once.  A batch's lengths differ, so a few splits are
-    // rounded up (64 units of up to 8000 keys: 26.6 us with 8 splits, 29.3 with 2 wide ones);
-    // from half a wave of units on, whole sequences do best (1024 units of up to 1000 keys: 51
-    // against 59 us)
-    const double q = attn::decode_paged_slots(d, Hq / Hkv, kSms) / units;
-    n = q < 2 ? 1 : (long long)(q <= 8 && B > 1 ? std::ceil(q) : q);
-  }
-  n = std::max(1LL, std::min(n, (max_kv + 191LL) / 192));
-  *min_rows = n > 1 ? 192 : 1;
-  return (int)n;
+  return mma_splits(std::max(1.0, (double)B * Hkv), Hq / Hkv, B, max_kv, d, min_rows);
 }
 
 int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const attn_bf16_t* vcache,
@@ -306,6 +377,47 @@ int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const att
   a.err = attn::device_err_word();
   if (a.err == nullptr) return ATTN_ERR_CUDA;
   return from_cuda(attn::launch_decode_paged(a, stream_of(stream)));
+}
+
+int attn_decode_window_splits(int B, int Hq, int Hkv, int max_kv, int window, int n_sink, int d, int* min_rows) {
+  if (check_heads(B, Hq, Hkv) != ATTN_OK || max_kv < 0 || window < 1 || n_sink < 0 || !ok_dim(d) ||
+      min_rows == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  const int keys = (int)std::min<long long>(max_kv, (long long)window + n_sink);
+  const int G = Hq / Hkv, ctas = window_head_ctas(G);
+  return mma_splits(std::max(1.0, (double)B * Hkv * ctas), (G + ctas - 1) / ctas, B, keys, d, min_rows);
+}
+
+int attn_decode_window(const attn_bf16_t* q, const attn_bf16_t* kcache, const attn_bf16_t* vcache,
+                       const int* page_table, const int* kv_lens, int B, int Hq, int Hkv, int d, int max_pages,
+                       int page_size, int num_pages, int window, int n_sink, float scale, int n_splits,
+                       int min_rows_per_split, float* part_o, float* part_lse, void* o, float* lse, int o_dtype,
+                       unsigned int* counters, attn_stream_t stream) {
+  int rc = check_heads(B, Hq, Hkv);
+  if (rc == ATTN_OK && (window < 1 || n_sink < 0)) rc = ATTN_ERR_INVALID_ARG;
+  if (rc == ATTN_OK) rc = check_cache(page_table, B, max_pages, page_size, num_pages);
+  if (rc == ATTN_OK && ok_dim(d)) rc = check_slot(Hkv, d);
+  if (rc == ATTN_OK)
+    // (the dense cache's row limit does not apply: max_kv = 1 here)
+    rc = attn::check_decode_split_args(q, kcache, vcache, kv_lens, B, Hq, Hkv, d, 1, scale, n_splits,
+                                       min_rows_per_split, part_o, part_lse, n_splits > 1);
+  if (rc == ATTN_OK)
+    rc = attn::check_merge_args(part_o, part_lse, o, lse, B, Hq, n_splits, d, o_dtype, n_splits > 1);
+  if (rc != ATTN_OK || B == 0) return rc;
+  if (n_splits > 1 && !ok4(counters)) return ATTN_ERR_INVALID_ARG;
+  attn::DecodeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q; a.kv_lens = kv_lens; a.part_o = part_o; a.part_lse = part_lse;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.d = d; a.max_kv = max_pages * page_size;
+  a.n_splits = n_splits; a.min_rows = min_rows_per_split; a.scale = scale;
+  a.done = counters; a.o = o; a.lse = lse; a.o_bf16 = o_dtype == ATTN_BF16 ? 1 : 0;
+  a.kv = cache(kcache, vcache, page_table, max_pages, page_size, num_pages);
+  a.window = window; a.n_sink = n_sink;
+  a.head_ctas = window_head_ctas(Hq / Hkv);
+  a.cta_heads = (Hq / Hkv + a.head_ctas - 1) / a.head_ctas;
+  a.err = attn::device_err_word();
+  if (a.err == nullptr) return ATTN_ERR_CUDA;
+  return from_cuda(attn::launch_decode_window(a, stream_of(stream)));
 }
 
 int attn_key_weights(const attn_bf16_t* q, const float* lse, const attn_bf16_t* kcache, const int* page_table,

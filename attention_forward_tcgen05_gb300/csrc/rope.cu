@@ -13,6 +13,12 @@
 // product with the 32-bit position wraps modulo one turn by itself, exactly.  The top 32 bits
 // go to sincospi as a signed half turn (2^-25 of it, 2^-26 of a turn, rounded away).  fp64 per token instead would
 // cost the few fp64 lanes of this GPU about as long as the copy itself.
+//
+// Several axes (time, height and width of a picture's or a clip's tokens, say): pair i then
+// follows position axes[i] of its token.  A CTA's tokens' positions on all axes lie in shared
+// memory, so an angle costs one more shared load.  rope_rotate_kernel is the same pass without a
+// cache, for encoders and training; its inverse, the rotation by -p f_i times amp, is the gradient
+// of the forward one, whose matrix is orthogonal up to amp.
 #include <cmath>
 
 #include "internal.h"
@@ -50,21 +56,54 @@ __device__ __forceinline__ void rotate_inter(uint4& a, const float2* cs) {
   }
 }
 
+// frequencies as fractions of a turn, units of 2^-64 turns
+__device__ __forceinline__ void load_turns(unsigned long long* turn, const double* inv_freq, int half) {
+  for (int i = threadIdx.x; i < half; i += kThreads) {
+    const double x = inv_freq[i] * 0.15915494309189535, y = fabs(x);  // 1 / (2 pi)
+    // the fraction of |x|, which is exact (that of a small negative x would be rounded to 2^-54)
+    const unsigned long long f = (unsigned long long)((y - floor(y)) * 18446744073709551616.0);
+    turn[i] = x < 0 ? 0ull - f : f;
+  }
+}
+// (cos, sin) * amp of a position times a frequency
+__device__ __forceinline__ float2 angle_at(unsigned long long turn, int pos, float amp) {
+  const unsigned long long w = turn * (unsigned long long)(long long)pos;
+  const float x = (float)(int)(w >> 32) * 4.656612873077393e-10f;  // half turns in [-1, 1): 2^-31
+  float sn, c;
+  sincospif(x, &sn, &c);
+  return make_float2(c * amp, sn * amp);
+}
+// the axis of each pair (one that is none is reported and becomes the first)
+__device__ __forceinline__ void load_axes(uint8_t* axis, const int* axes, int n_axes, int half, uint32_t* err) {
+  for (int i = threadIdx.x; i < half; i += kThreads) {
+    int x = axes[i];
+    if ((unsigned)x >= (unsigned)n_axes) {
+      atomicCAS(err, kErrNone, kErrBadShape);
+      x = 0;
+    }
+    axis[i] = (uint8_t)x;
+  }
+}
+
 // One CTA takes up to kTokens consecutive tokens: their places in the cache (a chain of
 // dependent loads) and their angles are found side by side, and the copies of all of them
 // follow without a barrier between.  A work item is two chunks of one head: the two partners
 // of the half layout, or two neighbours.  rot = 0 copies.
-template <bool INTER, int kTokens>
+template <bool INTER, int kTokens, bool AXES>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a) {
   __shared__ unsigned long long turn[128];       // f_i / 2 pi, units of 2^-64 turns
   __shared__ float2 cs[kTokens * 128];           // (cos, sin) * amp of each token's pairs
-  __shared__ int place[kTokens], at[kTokens];    // cache row (-1: none, -2: no sequence), position
+  __shared__ int place[kTokens];                 // cache row (-1: none, -2: no sequence)
+  __shared__ int at[(AXES ? kMaxRopeAxes : 1) * kTokens];  // [axis][token] position
+  __shared__ uint8_t axis[AXES ? 128 : 1];
   const int half = a.rot / 2, t0 = blockIdx.x * kTokens, nt = min(kTokens, a.total - t0);
-  for (int i = threadIdx.x; i < half; i += kThreads) {
-    const double x = a.inv_freq[i] * 0.15915494309189535, y = fabs(x);  // 1 / (2 pi)
-    // the fraction of |x|, which is exact (that of a small negative x would be rounded to 2^-54)
-    const unsigned long long f = (unsigned long long)((y - floor(y)) * 18446744073709551616.0);
-    turn[i] = x < 0 ? 0ull - f : f;
+  load_turns(turn, a.inv_freq, half);
+  if constexpr (AXES) {
+    load_axes(axis, a.axes, a.n_axes, half, a.err);
+    for (int i = threadIdx.x; i < a.n_axes * kTokens; i += kThreads) {
+      const int s = i % kTokens;
+      if (s < nt) at[i] = a.positions[(size_t)(i / kTokens) * a.total + t0 + s];
+    }
   }
   if ((int)threadIdx.x >= kThreads - nt) {
     // (the last threads, whose warp has no frequency to convert up to d = 256)
@@ -94,18 +133,14 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
       } else {
         row = paged_row(a.kv, b, (int)j, a.err);
       }
-      at[s] = a.positions ? a.positions[t] : (int)j;
+      if constexpr (!AXES) at[s] = a.positions ? a.positions[t] : (int)j;
     }
     place[s] = row;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int s = kTokens == 1 ? 0 : i / half, m = i - s * half;
-    const unsigned long long w = turn[m] * (unsigned long long)(long long)at[s];
-    const float x = (float)(int)(w >> 32) * 4.656612873077393e-10f;  // half turns in [-1, 1): 2^-31
-    float sn, c;
-    sincospif(x, &sn, &c);
-    cs[s * 128 + m] = make_float2(c * a.amp, sn * a.amp);
+    cs[s * 128 + m] = angle_at(turn[m], AXES ? at[axis[m] * kTokens + s] : at[s], a.amp);
   }
   __syncthreads();
   const int cpr = a.d / 8, rc = a.rot / 8;  // chunks of a head, rotated ones (rot % 16 == 0)
@@ -144,19 +179,82 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
   }
 }
 
-template <int kTokens>
+// The same without a cache: q and k rows to rows of their own (or themselves: each chunk is read and
+// written by one thread), items as above.
+template <bool INTER, int kTokens>
+__global__ void __launch_bounds__(kThreads) rope_rotate_kernel(const RotateArgs a) {
+  __shared__ unsigned long long turn[128];
+  __shared__ float2 cs[kTokens * 128];
+  __shared__ int at[kMaxRopeAxes * kTokens];
+  __shared__ uint8_t axis[128];
+  const int half = a.rot / 2, t0 = blockIdx.x * kTokens, nt = min(kTokens, a.total - t0);
+  load_turns(turn, a.inv_freq, half);
+  if (a.axes) load_axes(axis, a.axes, a.n_axes, half, a.err);
+  for (int i = threadIdx.x; i < a.n_axes * kTokens; i += kThreads) {
+    const int s = i % kTokens;
+    if (s < nt) at[i] = a.positions[(size_t)(i / kTokens) * a.total + t0 + s];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+    const int s = kTokens == 1 ? 0 : i / half, m = i - s * half;
+    float2 c = angle_at(turn[m], at[(a.axes ? axis[m] : 0) * kTokens + s], a.amp);
+    if (a.inverse) c.y = -c.y;
+    cs[s * 128 + m] = c;
+  }
+  __syncthreads();
+  const int rc = a.rot / 8, ipr = a.d / 16, items = (a.Hq + a.Hk) * ipr;
+#pragma unroll 2
+  for (int it = threadIdx.x; it < nt * items; it += kThreads) {
+    const int s = kTokens == 1 ? 0 : it / items, in = it - s * items;
+    const size_t t = (size_t)(t0 + s);
+    const int h = in / ipr, x = in - h * ipr;
+    const bool is_q = h < a.Hq;
+    const size_t head = (size_t)(is_q ? h : h - a.Hq) * a.d;
+    const uint16_t* src = (is_q ? a.q + t * a.q_stride : a.k + t * a.k_stride) + head;
+    uint16_t* dst = (is_q ? a.q_out + t * a.qo_stride : a.k_out + t * a.ko_stride) + head;
+    int c0, c1;
+    if (!INTER && x < rc / 2) { c0 = x; c1 = x + rc / 2; }
+    else { c0 = 2 * x; c1 = 2 * x + 1; }
+    uint4 u0 = *reinterpret_cast<const uint4*>(src + c0 * 8), u1 = *reinterpret_cast<const uint4*>(src + c1 * 8);
+    const float2* c = cs + s * 128;
+    if (INTER) {
+      if (c0 < rc) rotate_inter(u0, c + c0 * 4);
+      if (c1 < rc) rotate_inter(u1, c + c1 * 4);
+    } else if (x < rc / 2) {
+      rotate_half(u0, u1, c + c0 * 8);
+    }
+    *reinterpret_cast<uint4*>(dst + c0 * 8) = u0;
+    *reinterpret_cast<uint4*>(dst + c1 * 8) = u1;
+  }
+}
+
+template <int kTokens, bool AXES>
 cudaError_t launch_t(const RopeArgs& a, cudaStream_t stream) {
   const unsigned grid = (unsigned)((a.total + kTokens - 1) / kTokens);
-  if (a.interleaved) rope_append_kernel<true, kTokens><<<grid, kThreads, 0, stream>>>(a);
-  else rope_append_kernel<false, kTokens><<<grid, kThreads, 0, stream>>>(a);
+  if (a.interleaved) rope_append_kernel<true, kTokens, AXES><<<grid, kThreads, 0, stream>>>(a);
+  else rope_append_kernel<false, kTokens, AXES><<<grid, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
+template <int kTokens>
+cudaError_t launch_rotate_t(const RotateArgs& a, cudaStream_t stream) {
+  const unsigned grid = (unsigned)((a.total + kTokens - 1) / kTokens);
+  if (a.interleaved) rope_rotate_kernel<true, kTokens><<<grid, kThreads, 0, stream>>>(a);
+  else rope_rotate_kernel<false, kTokens><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// one token a CTA while that leaves SMs idle, else eight
+bool many_tokens(int total) { return total >= 8 * 152 * 2; }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream) {
-  // one token a CTA while that leaves SMs idle, else eight
-  return a.total >= 8 * 152 * 2 ? launch_t<8>(a, stream) : launch_t<1>(a, stream);
+  if (a.axes) return many_tokens(a.total) ? launch_t<8, true>(a, stream) : launch_t<1, true>(a, stream);
+  return many_tokens(a.total) ? launch_t<8, false>(a, stream) : launch_t<1, false>(a, stream);
+}
+
+cudaError_t launch_rope_rotate(const RotateArgs& a, cudaStream_t stream) {
+  return many_tokens(a.total) ? launch_rotate_t<8>(a, stream) : launch_rotate_t<1>(a, stream);
 }
 
 }  // namespace attn

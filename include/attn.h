@@ -442,6 +442,43 @@ int attn_rope_append(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16
                      attn_stream_t stream);
 
 /*
+ * attn_rope_append_axes -- attn_rope_append with several positions a token (time, height and width
+ * of a picture's or a clip's tokens, say): pair m turns by positions[axes[m]][t] * inv_freq[m].
+ *
+ * Arguments: as attn_rope_append, with
+ *   positions    int32 [n_axes][total] (device, may be negative)
+ *   axes         int32 [rot_dim/2] (device), in [0, n_axes); another value is reported as
+ *                ATTN_ERR_DEVICE_INPUT by attn_sync_check and read as 0
+ *   n_axes       1 .. 8;  rot_dim 16, 32, .. d
+ */
+int attn_rope_append_axes(const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16_t* v, long long q_stride,
+                          long long k_stride, long long v_stride, const int* positions, const int* axes, int n_axes,
+                          const double* inv_freq, attn_bf16_t* q_out, attn_bf16_t* kcache, attn_bf16_t* vcache,
+                          const int* page_table, const int* cu_seqlens_q, const int* kv_lens, int B, int Hq, int Hkv,
+                          int total, int d, int rot_dim, int interleaved, float amp, int max_pages, int page_size,
+                          int num_pages, attn_stream_t stream);
+
+/*
+ * attn_rope_rotate -- the rotation alone, of queries and keys that go to no cache (encoders,
+ * training), and its inverse (inverse != 0: by -p * inv_freq, times amp), which is the gradient of
+ * the forward one.  Angles and rounding as in attn_rope_append.
+ *
+ * Arguments
+ *   q, k         bf16, token t's heads [Hq][d] / [Hk][d] at t * stride elements, q_out and k_out
+ *                likewise; strides at least the heads' width and multiples of 8.  Outputs do not
+ *                overlap inputs, or are the inputs with the same strides.  Hq or Hk may be 0
+ *   positions    int32 [n_axes][total] (device, may be negative)
+ *   axes         int32 [rot_dim/2] as in attn_rope_append_axes, or NULL (n_axes = 1)
+ *   inv_freq     fp64 [rot_dim/2] (device), radians per position
+ *   d            16, 32, .. 256;  rot_dim 16, 32, .. d;  amp finite
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
+ */
+int attn_rope_rotate(const attn_bf16_t* q, const attn_bf16_t* k, long long q_stride, long long k_stride,
+                     const int* positions, const int* axes, int n_axes, const double* inv_freq, attn_bf16_t* q_out,
+                     attn_bf16_t* k_out, long long q_out_stride, long long k_out_stride, int Hq, int Hk, int total,
+                     int d, int rot_dim, int interleaved, int inverse, float amp, attn_stream_t stream);
+
+/*
  * attn_prefill_paged -- attn_prefill_varlen over a paged cache (window = 0), or
  * attn_prefill_varlen_window (window >= 1, causal).
  *
@@ -490,6 +527,28 @@ int attn_decode_paged(const attn_bf16_t* q, const attn_bf16_t* kcache, const att
 /* The n_splits (>= 1) and min_rows_per_split that suit a decode of these sizes and output
  * type, max_kv keys in the longest sequence (host only); ATTN_ERR_INVALID_ARG for bad ones. */
 int attn_decode_paged_splits(int B, int Hq, int Hkv, int max_kv, int d, int o_dtype, int* min_rows_per_split);
+
+/*
+ * attn_decode_window -- attn_decode_paged with the causal sliding window and sinks of
+ * attn_prefill_window: of a sequence of L keys its token admits the last `window` (its own among
+ * them) and the first n_sink.  Only those rows are read; pages that hold none of them are not looked up,
+ * so their table entries may be anything (a serving loop gives such pages back).  The split rule cuts
+ * the list of admitted keys, min(L, window) + min(n_sink, max(0, L - window)) long.  One launch for
+ * any Hq / Hkv up to 128.
+ *
+ * Arguments: as attn_decode_paged, with window >= 1, n_sink >= 0; page_table may be NULL (dense cache).
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
+ */
+int attn_decode_window(const attn_bf16_t* q, const attn_bf16_t* kcache, const attn_bf16_t* vcache,
+                       const int* page_table, const int* kv_lens, int B, int Hq, int Hkv, int d, int max_pages,
+                       int page_size, int num_pages, int window, int n_sink, float scale, int n_splits,
+                       int min_rows_per_split, float* part_o, float* part_lse, void* o, float* lse, int o_dtype,
+                       unsigned int* counters, attn_stream_t stream);
+
+/* The n_splits (>= 1) and min_rows_per_split that suit it, max_kv keys in the longest sequence (host
+ * only); ATTN_ERR_INVALID_ARG for bad sizes. */
+int attn_decode_window_splits(int B, int Hq, int Hkv, int max_kv, int window, int n_sink, int d,
+                              int* min_rows_per_split);
 
 /*
  * attn_key_weights -- the attention weight that every cached key received.
