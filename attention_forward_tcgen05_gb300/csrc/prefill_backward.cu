@@ -797,14 +797,17 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
         tc_fence_after();
         tmem_ld32(sc, s);
         tmem_ld32(sc + 32, s + 32);
-        tmem_wait_ld();
         if constexpr (C::kSep) {  // the next S need not wait for this dP
+          tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_Sr[bs]);
         }
         ok = mbar_wait_warp(&bar_dP[bp], (uint32_t)(it >> 1) & 1u, a.err, abort_flag);
-        if (!ok) break;
+        if (!ok) {
+          tmem_wait_ld();
+          break;
+        }
         tc_fence_after();
         tmem_ld32(dc, p);
         tmem_ld32(dc + 32, p + 32);
