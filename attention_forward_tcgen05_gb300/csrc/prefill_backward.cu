@@ -316,11 +316,11 @@ struct Walk {
   int g, g0;     // group, its place
   Run at;        // of the group: u, b, x, cnt
   __device__ __forceinline__ const int* pre() const { return KV ? a.pre_k : a.pre_q; }
-  __device__ __forceinline__ Walk(const BackwardArgs& a_, int lane) : a(a_) {
+  __device__ __forceinline__ Walk(const BackwardArgs& a_, int cta, int ctas, int lane) : a(a_) {
     const int n_groups = a.B * f_tiles(a, KV);
     const int total = pre()[n_groups];
-    per = slice_cost(total, (int)gridDim.x);
-    pos = (int)min((long long)total, (long long)blockIdx.x * per);
+    per = slice_cost(total, ctas);
+    pos = (int)min((long long)total, (long long)cta * per);
     end = min(total, pos + per);
     g = g0 = 0;
     if (pos >= end) return;
@@ -454,9 +454,9 @@ struct Stream {
   }
 };
 
+// One CTA's slice of a pass: `cta` of `ctas`.
 template <int D, bool KV>
-__global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
-    backward_kernel(const __grid_constant__ BackwardArgs a) {
+__device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, int ctas) {
   using C = BwdCfg<D, KV>;
   constexpr int NS = C::NS, ND = C::ND, TN = C::TN, TY = C::TY, SUB = C::kSub;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Walk<TY, KV> w(a, lane);
+  Walk<TY, KV> w(a, cta, ctas, lane);
   Run run = w.next();
   if (warp == 8 || warp == 9) {
     // ---- first products: S = F1 Y1^T (warp 8), dP = F2 Y2^T (warp 9), and their F tiles ----
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
     if (lane == 0) tma_prefetch_desc(map);
     // the lse / D columns of an item, two items ahead (a tensor or bulk copy of them would take the
     // copy engine as long as a tile)
-    Stream<TY, KV> ex(a, Walk<TY, KV>(a, lane));
+    Stream<TY, KV> ex(a, Walk<TY, KV>(a, cta, ctas, lane));
     auto load_ext = [&] {
       if constexpr (KV) {
         if (ex.r.n > 0) {
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
     }
   } else if (warp == 11) {
     // ---- the rings of Y1 and Y2, each slot filled as soon as it is free ----
-    Stream<TY, KV> st[2] = {Stream<TY, KV>(a, Walk<TY, KV>(a, lane)), Stream<TY, KV>(a, Walk<TY, KV>(a, lane))};
+    Stream<TY, KV> st[2] = {Stream<TY, KV>(a, Walk<TY, KV>(a, cta, ctas, lane)), Stream<TY, KV>(a, Walk<TY, KV>(a, cta, ctas, lane))};
     if (lane == 0) {
       tma_prefetch_desc(KV ? &a.tm_qy : &a.tm_ky);
       tma_prefetch_desc(KV ? &a.tm_doy : &a.tm_vy);
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
       };
       constexpr int kSlot = kT * D * (KV ? 2 : 1) / 4;  // float4s of a partial: [column / 4][row]
       float4* const parts = reinterpret_cast<float4*>(KV ? a.part_k : a.part_q) + (size_t)wg * (kCols / 4) * kT + r;
-      float4* pp = parts + ((size_t)blockIdx.x * 2 + (run.i0 > 0 ? 0 : 1)) * kSlot;
+      float4* pp = parts + ((size_t)cta * 2 + (run.i0 > 0 ? 0 : 1)) * kSlot;
       ok = mbar_wait_warp(bar_acc, (uint32_t)n_run & 1u, a.err, abort_flag);
       if (!ok) break;
       tc_fence_after();
@@ -986,14 +986,12 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::kThreads, 1)
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool KV>
-cudaError_t launch_pass(const BackwardArgs& a, int ctas, cudaStream_t stream) {
-  using C = BwdCfg<D, KV>;
-  auto kern = backward_kernel<D, KV>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<ctas, C::kThreads, C::kSmem, stream>>>(a);
-  return cudaGetLastError();
+// Both passes: dQ's CTAs start as dK/dV's end.
+template <int D>
+__global__ void __launch_bounds__(BwdCfg<D, true>::kThreads, 1)
+    backward_kernel(const __grid_constant__ BackwardArgs a) {
+  if ((int)blockIdx.x < a.ctas_k) backward_pass<D, true>(a, (int)blockIdx.x, a.ctas_k);
+  else backward_pass<D, false>(a, (int)blockIdx.x - a.ctas_k, a.ctas_q);
 }
 
 template <int D>
@@ -1004,9 +1002,12 @@ cudaError_t launch_d(const BackwardArgs& a, cudaStream_t stream) {
   if (a.o_bf16) backward_prep_kernel<D, true><<<grid, kPrepThreads, 0, stream>>>(a);
   else backward_prep_kernel<D, false><<<grid, kPrepThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (any && e == cudaSuccess) e = launch_pass<D, true>(a, a.ctas_k, stream);
-  if (any && e == cudaSuccess) e = launch_pass<D, false>(a, a.ctas_q, stream);
-  return e;
+  if (!any || e != cudaSuccess) return e;
+  constexpr int kSmem = std::max(BwdCfg<D, true>::kSmem, BwdCfg<D, false>::kSmem);
+  e = cudaFuncSetAttribute(backward_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  backward_kernel<D><<<a.ctas_k + a.ctas_q, BwdCfg<D, true>::kThreads, kSmem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
