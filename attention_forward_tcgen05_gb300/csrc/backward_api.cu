@@ -29,7 +29,7 @@ int check_sizes(const Sizes& z) {
   if ((long long)z.Hq * z.d >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
   // tiles of 64 x 64 of all heads (more than there are, and some for each unit's start), which the kernels count in 32 bits
   const long long tq = (z.Sq + 63LL) / 64, tk = (z.Skv + 63LL) / 64;
-  if ((tq + 8) * z.B * (tk + 8) >= (1LL << 31) / z.Hq) return ATTN_ERR_INVALID_ARG;
+  if ((tq + 16) * z.B * (tk + 16) >= (1LL << 31) / z.Hq) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 
@@ -89,10 +89,12 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_do, dout, z.d, z.Hq, ns, nb, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_k, k, z.d, z.Hkv, z.Skv, z.B, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_v, v, z.d, z.Hkv, z.Skv, z.B, 128);
-    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_qy, q, z.d, z.Hq, ns, nb, tk);
-    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_doy, dout, z.d, z.Hq, ns, nb, tk);
-    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_ky, k, z.d, z.Hkv, z.Skv, z.B, tq);
-    if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_vy, v, z.d, z.Hkv, z.Skv, z.B, tq);
+    // (a pass whose streamed tiles are of 128 rows shares the other's maps)
+    a.tm_qy = a.tm_q; a.tm_doy = a.tm_do; a.tm_ky = a.tm_k; a.tm_vy = a.tm_v;
+    if (rc == ATTN_OK && tk != 128) rc = attn::encode_panel_map(&a.tm_qy, q, z.d, z.Hq, ns, nb, tk);
+    if (rc == ATTN_OK && tk != 128) rc = attn::encode_panel_map(&a.tm_doy, dout, z.d, z.Hq, ns, nb, tk);
+    if (rc == ATTN_OK && tq != 128) rc = attn::encode_panel_map(&a.tm_ky, k, z.d, z.Hkv, z.Skv, z.B, tq);
+    if (rc == ATTN_OK && tq != 128) rc = attn::encode_panel_map(&a.tm_vy, v, z.d, z.Hkv, z.Skv, z.B, tq);
     if (rc != ATTN_OK) return rc;
   }
   a.q = q; a.dout = dout; a.k = k; a.v = v; a.o = o; a.lse = lse; a.dlse = dlse;

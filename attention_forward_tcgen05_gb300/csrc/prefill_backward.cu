@@ -46,11 +46,13 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kT = 128;           // rows of a tile
 constexpr int kMaxCtas = kBackwardCtas;
-// A run of a unit's items costs its start and end (the F tiles' copy, the sums' way out) beside its
-// items, about as much as kRunCost of them: units of few items would otherwise fill some slices
-// with nothing but starts and ends.
-constexpr int kRunCost = 3;
-constexpr int kMinCost = 2 + kRunCost;  // of a slice
+// A run of a unit's items costs its start and end (the F tiles' copy, the sums' way out, the sum of a
+// cut unit's parts) beside its items: units of few items would otherwise fill some slices with
+// nothing but starts and ends.  In rows of Y: 640 in the dK/dV pass, 128 in the dQ pass (of 64 to
+// 768 and 128 to 384; 3314 rows, window 1024: 183 us, 192 with 192 and 384; eight packed sequences:
+// 283 and 303).
+constexpr int run_cost(bool kv, int ty) { return (kv ? 640 : 128) / ty; }
+constexpr int kMinCost = 8;  // of a slice
 
 // TN: columns of S and dP per item.  64: the softmax warpgroups take an item each in turn, so that
 // one's loads and stores run under the other's exponentials; S, dP and the bf16 P and dS have columns
@@ -142,7 +144,10 @@ template <bool KV>
 __device__ __forceinline__ int unit_items(const BackwardArgs& a, const Unit& u) {
   return KV ? u.nt * (a.Hq / a.Hkv) : u.nt;
 }
-__device__ __forceinline__ int unit_cost(int items) { return items > 0 ? items + kRunCost : 0; }
+template <int TY, bool KV>
+__device__ __forceinline__ int unit_cost(int items) {
+  return items > 0 ? items + run_cost(KV, TY) : 0;
+}
 // Groups (sequence, F tile) of the pass: each holds a unit per head.
 __host__ __device__ __forceinline__ int f_tiles(const BackwardArgs& a, bool kv) {
   return ((kv ? a.Skv : a.Sq) + kT - 1) / kT;
@@ -192,7 +197,7 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
       const int c0 = min(max(a.cu_q[b], 0), a.total_q), c1 = min(a.cu_q[b + 1], a.total_q);
       if (c1 - c0 > a.Sq) atomicCAS(a.err, kErrNone, kErrBadShape);
     }
-  for (int g = lo; g < hi; ++g) s += unit_cost(unit_items<KV>(a, unit_of<TY, KV>(a, g / nx, g % nx))) * H;
+  for (int g = lo; g < hi; ++g) s += unit_cost<TY, KV>(unit_items<KV>(a, unit_of<TY, KV>(a, g / nx, g % nx))) * H;
   int incl = s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -206,7 +211,7 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
   for (int w = 0; w < warp; ++w) at += sums[w];
   for (int g = lo; g < hi; ++g) {
     pre[g] = at;
-    at += unit_cost(unit_items<KV>(a, unit_of<TY, KV>(a, g / nx, g % nx))) * H;
+    at += unit_cost<TY, KV>(unit_items<KV>(a, unit_of<TY, KV>(a, g / nx, g % nx))) * H;
   }
   if (hi == n && lo < n) pre[n] = at;
   if (n == 0 && threadIdx.x == 0) pre[0] = 0;
@@ -217,14 +222,16 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
 template <int D, bool KV>
 __device__ void zero_units(const BackwardArgs& a, int c, int n) {
   const int nx = f_tiles(a, KV), n_groups = a.B * nx, H = KV ? a.Hkv : a.Hq;
-  for (int g = c; g < n_groups; g += n) {
-    const int b = g / nx, f0 = (g - b * nx) * kT;
-    const Unit u = unit_of<BwdCfg<D, KV>::TY, KV>(a, b, g - b * nx);
+  constexpr int kRows = 16;  // of a CTA's turn
+  for (int gc = c; gc < n_groups * (kT / kRows); gc += n) {
+    const int g = gc / (kT / kRows), b = g / nx, x = g - b * nx;
+    const Unit u = unit_of<BwdCfg<D, KV>::TY, KV>(a, b, x);
     if (unit_items<KV>(a, u) > 0) continue;
-    const int rows = min(kT, (KV ? (a.fill ? a.Skv : u.Skv) : u.Sq) - f0);
+    const int f0 = x * kT + gc % (kT / kRows) * kRows;
+    const int rows = min(kRows, (KV ? (a.fill ? a.Skv : u.Skv) : u.Sq) - f0);
     const size_t at = ((size_t)(KV ? u.kbase : u.qbase) + f0) * H * D;
     const int w = H * (D / 8);
-    for (long long i = threadIdx.x; i < (long long)rows * w; i += kPrepThreads) {
+    for (int i = threadIdx.x; i < rows * w; i += kPrepThreads) {
       if (KV) {
         reinterpret_cast<uint4*>(a.dk + at)[i] = make_uint4(0, 0, 0, 0);
         reinterpret_cast<uint4*>(a.dv + at)[i] = make_uint4(0, 0, 0, 0);
@@ -351,17 +358,17 @@ struct Walk {
     const int H = KV ? a.Hkv : a.Hq;
     at.n = 0;
     while (pos < end) {
-      while (pos >= g0 + unit_cost(at.cnt) * H) {
+      while (pos >= g0 + unit_cost<TY, KV>(at.cnt) * H) {
         ++g;
         enter();
       }
-      const int cost = unit_cost(at.cnt);
+      const int cost = unit_cost<TY, KV>(at.cnt);
       at.h = (pos - g0) / cost;
       const int from = pos - g0 - at.h * cost, to = min(cost, from + end - pos);  // of the unit's cost
       pos += to - from;
-      at.first = g0 + at.h * cost + kRunCost;
-      at.i0 = max(0, from - kRunCost);
-      at.n = max(0, to - kRunCost) - at.i0;
+      at.first = g0 + at.h * cost + run_cost(KV, TY);
+      at.i0 = max(0, from - run_cost(KV, TY));
+      at.n = max(0, to - run_cost(KV, TY)) - at.i0;
       if (at.n > 0) break;
     }
     return at;
@@ -514,7 +521,8 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Walk<TY, KV> w(a, cta, ctas, lane);
+  const Walk<TY, KV> start(a, cta, ctas, lane);  // (a chain of dependent loads: made once)
+  Walk<TY, KV> w = start;
   Run run = w.next();
   if (warp == 8 || warp == 9) {
     // ---- first products: S = F1 Y1^T (warp 8), dP = F2 Y2^T (warp 9), and their F tiles ----
@@ -534,7 +542,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     if (lane == 0) tma_prefetch_desc(map);
     // the lse / D columns of an item, two items ahead (a tensor or bulk copy of them would take the
     // copy engine as long as a tile)
-    Stream<TY, KV> ex(a, Walk<TY, KV>(a, cta, ctas, lane));
+    Stream<TY, KV> ex(a, start);
     auto load_ext = [&] {
       if constexpr (KV) {
         if (ex.r.n > 0) {
@@ -655,7 +663,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     }
   } else if (warp == 11) {
     // ---- the rings of Y1 and Y2, each slot filled as soon as it is free ----
-    Stream<TY, KV> st[2] = {Stream<TY, KV>(a, Walk<TY, KV>(a, cta, ctas, lane)), Stream<TY, KV>(a, Walk<TY, KV>(a, cta, ctas, lane))};
+    Stream<TY, KV> st[2] = {Stream<TY, KV>(a, start), Stream<TY, KV>(a, start)};
     if (lane == 0) {
       tma_prefetch_desc(KV ? &a.tm_qy : &a.tm_ky);
       tma_prefetch_desc(KV ? &a.tm_doy : &a.tm_vy);
