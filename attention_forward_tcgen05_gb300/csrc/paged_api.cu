@@ -125,6 +125,40 @@ int mma_splits(double units, int heads, int B, int max_kv, int d, int* min_rows)
   return (int)n;
 }
 
+// The same for the windowed decode, whose sequences are mostly as long as the window: the splits of
+// least estimated time.  A call's start and end take 7.5 us and a merge 4 and more; a warp takes 0.7 us
+// for 16 keys (more with two mma sides or d = 256) while HBM keeps up; launches of up to an SM's worth of
+// CTAs run wide ones (decode_paged.cuh), others waves of narrow ones, the last of which is not
+// full.  (512 units of 4100 keys, a wave and an eighth whole: 173 us whole, 160 in three; 1024 units of
+// 260: 37 whole, 60 in two; 64 units of 2000, groups of 20: 18 whole, 25 in five; 8 units of 4100: 29
+// whole, 14 in 19.)
+int window_splits(double units, int heads, int keys, int d, int* min_rows) {
+  const bool two = heads > 8;  // mma sides
+  const double step = 0.7 * (two ? 1.2 : 1.0) * (d == 256 ? 2.0 : 1.0) / 16;
+  const int wide = d == 256 ? (two ? 4 : 6) : (d == 64 && !two ? 12 : 8);
+  const double slots = attn::decode_paged_slots(d, heads, kSms);
+  const double row_us = 4.0 * d / 6.5e6;  // of K and V of a key at the rate of HBM
+  double best = 0;
+  int n_best = 1;
+  for (int n = 1; n <= 64 && n <= std::max(1, (keys + 63) / 64); ++n) {
+    const double rows = std::ceil((double)keys / n), ctas = units * n;
+    double us = 7.5 + (n > 1 ? 4.0 + 0.08 * n : 0.0);
+    if (ctas <= kSms) {
+      us += std::max(rows * step / wide, ctas * rows * row_us);
+    } else {
+      const double full = std::floor(ctas / slots), rest = ctas - full * slots;
+      us += full * (1.5 + std::max(rows * step / 4, slots * rows * row_us));
+      if (rest > 0) us += std::max(rows * step / 4, rest * rows * row_us);
+    }
+    if (n == 1 || us < best * 0.99) {
+      best = us;
+      n_best = n;
+    }
+  }
+  *min_rows = n_best > 1 ? 64 : 1;
+  return n_best;
+}
+
 // Query heads of a CTA of the windowed decode and its CTAs a group: groups of more than 16 are shared
 // evenly.
 int window_head_ctas(int G) { return (G + attn::kMaxHeadsPerCta - 1) / attn::kMaxHeadsPerCta; }
@@ -385,7 +419,7 @@ int attn_decode_window_splits(int B, int Hq, int Hkv, int max_kv, int window, in
     return ATTN_ERR_INVALID_ARG;
   const int keys = (int)std::min<long long>(max_kv, (long long)window + n_sink);
   const int G = Hq / Hkv, ctas = window_head_ctas(G);
-  return mma_splits(std::max(1.0, (double)B * Hkv * ctas), (G + ctas - 1) / ctas, B, keys, d, min_rows);
+  return window_splits(std::max(1.0, (double)B * Hkv * ctas), (G + ctas - 1) / ctas, keys, d, min_rows);
 }
 
 int attn_decode_window(const attn_bf16_t* q, const attn_bf16_t* kcache, const attn_bf16_t* vcache,
