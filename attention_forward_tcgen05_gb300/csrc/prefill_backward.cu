@@ -59,7 +59,9 @@ constexpr int kMinCost = 8;  // of a slice
 // of their own, so that the next S waits for the softmax's load only.  128, halved between the
 // warpgroups (dQ pass, d = 128): a product of 64 columns re-reads as much of F for half of the work
 // (49 cycles a step, bound by shared memory, against 65 for 128 columns), which its one small
-// second product does not make up for; there dS lies over S, two S beside one dP.
+// second product does not make up for; there dS lies over dP, two dP beside one S: of an item's
+// two products the one that waits for the second product two items back is then the one that
+// the softmax needs last, after its exponentials.
 template <int D, bool KV>
 struct BwdCfg {
   static constexpr int TN = (D == 128 && !KV) ? 128 : 64;
@@ -68,8 +70,8 @@ struct BwdCfg {
   static constexpr int TY = (D == 128 && KV) ? 64 : 128;
   static constexpr int kSub = TY / TN;
   static constexpr bool kSep = TN == 64;                   // P and dS in columns of their own
-  static constexpr int NS = (D == 128 && KV) ? 1 : 2;      // S buffers
-  static constexpr int ND = D == 128 ? 1 : 2;              // dP buffers
+  static constexpr int NS = D == 128 ? 1 : 2;              // S buffers
+  static constexpr int ND = (D == 128 && KV) ? 1 : 2;      // dP buffers
   static constexpr int kArrive = TN == 64 ? 4 : 8;         // softmax warps of an item
   static constexpr int kPanels = D / 64;
   static constexpr int kFPanel = kT * 128;
@@ -90,14 +92,14 @@ struct BwdCfg {
   static constexpr int kOnesOff = kExt2Off + kExtSlots * kExt;
   static constexpr int kZeroOff = kOnesOff + kOnes;
   static constexpr int kBarOff = kZeroOff + kOnes;
-  static constexpr int kNumBars = 2 * kSt1 + 2 * kSt2 + 4 + 2 + NS + 2 + ND + 4 + 4;
+  static constexpr int kNumBars = 2 * kSt1 + 2 * kSt2 + 4 + 2 + NS + 2 + ND + 4 + 5;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;  // (16: TMEM address, abort and last flags)
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static constexpr uint32_t kAcc1 = KV ? D : 0;  // TMEM columns; acc0 at 0
   static constexpr uint32_t kS = kAcc1 + D;
   static constexpr uint32_t kDP = kS + NS * TN;
   // P and dS of an item (two buffers): kP + buffer * kPStep
-  static constexpr uint32_t kP = kSep ? kDP + ND * TN : kS;
+  static constexpr uint32_t kP = kSep ? kDP + ND * TN : kDP;
   static constexpr uint32_t kPStep = kSep ? (KV ? 64 : 32) : TN;
   static_assert(kP + 2 * kPStep <= 512 && kDP + ND * TN <= 512, "TMEM budget");
   static constexpr int kThreads = 384;
@@ -477,16 +479,17 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
   uint64_t* emptyF = fullF + 2;
   // S and dP computed: two each whatever the buffers, as a warpgroup may wait for every other item
   uint64_t* bar_S = emptyF + 2;
-  uint64_t* bar_Sr = bar_S + 2;        // [NS] S read (where dS lies over it: dS used up)
+  uint64_t* bar_Sr = bar_S + 2;        // [NS] S read
   uint64_t* bar_dP = bar_Sr + NS;
-  uint64_t* bar_dPr = bar_dP + 2;      // [ND] dP read
+  uint64_t* bar_dPr = bar_dP + 2;      // [ND] dP read (where dS lies over it: dS used up)
   uint64_t* bar_P = bar_dPr + ND;      // [2] P and dS stored
   uint64_t* bar_Pr = bar_P + 2;        // [2] P and dS used up
   uint64_t* bar_acc = bar_Pr + 2;      // a run's sums complete
   uint64_t* bar_accr = bar_acc + 1;    // they are read
   uint64_t* bar_out = bar_accr + 1;    // a partial is written
   uint64_t* bar_last = bar_out + 1;    // last_flag is set
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_last + 1);
+  uint64_t* bar_go = bar_last + 1;     // a run's last second product is issued
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_go + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last_flag = abort_flag + 1;
 
@@ -494,14 +497,15 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     for (int s = 0; s < C::kSt1; ++s) { mbar_init(&full1[s], 1); mbar_init(&empty1[s], 1); }
     for (int s = 0; s < C::kSt2; ++s) { mbar_init(&full2[s], 1); mbar_init(&empty2[s], 1); }
     for (int s = 0; s < 2; ++s) { mbar_init(&fullF[s], 1); mbar_init(&emptyF[s], 1); }
-    for (int s = 0; s < NS; ++s) mbar_init(&bar_Sr[s], C::kSep ? C::kArrive : 1);
-    for (int s = 0; s < ND; ++s) mbar_init(&bar_dPr[s], C::kArrive);
+    for (int s = 0; s < NS; ++s) mbar_init(&bar_Sr[s], C::kArrive);
+    for (int s = 0; s < ND; ++s) mbar_init(&bar_dPr[s], C::kSep ? C::kArrive : 1);
     for (int s = 0; s < 2; ++s) { mbar_init(&bar_S[s], 1); mbar_init(&bar_dP[s], 1); }
     for (int s = 0; s < 2; ++s) { mbar_init(&bar_P[s], C::kArrive); mbar_init(&bar_Pr[s], 1); }
     mbar_init(bar_acc, 1);
     mbar_init(bar_accr, 8);
     mbar_init(bar_out, 8);
     mbar_init(bar_last, 1);
+    mbar_init(bar_go, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -580,6 +584,8 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       const int n = run.n;
       run = w.next();
       ok = mbar_wait_warp(fF, (uint32_t)n_run & 1u, a.err, abort_flag);
+      // behind the run before: its sums go out under these products, not after them
+      if (ok && n_run > 0) ok = mbar_wait_warp(bar_go, (uint32_t)(n_run - 1) & 1u, a.err, abort_flag);
       for (int m = 0; ok && m < n; ++m, ++it) {
         const int s = it % stages;
         const uint32_t ph_f = (uint32_t)(it / stages) & 1u;
@@ -622,8 +628,8 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
     const uint64_t my1 = smem_desc(smem_u32(smem + C::kY1Off), C::kYPanel, 1024, kSwizzle128B);
     const uint64_t my2 = smem_desc(smem_u32(smem + C::kY2Off), C::kYPanel, 1024, kSwizzle128B);
-    // A in TMEM, 16 columns of Y's rows at a time (where dS lies over S: 32 columns for each 64 of
-    // S); Y MN-major
+    // A in TMEM, 16 columns of Y's rows at a time (where dS lies over dP: 32 columns for each 64 of
+    // dP); Y MN-major
     auto issue = [&](uint32_t acc, uint32_t p, uint64_t y, bool fresh) {
 #pragma unroll
       for (int kk = 0; kk < TN / 16; ++kk)
@@ -653,11 +659,14 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
             if (sub == SUB - 1) mma_commit_e(&empty2[s2]);
           }
           issue(C::kAcc1, p + (KV ? 32 : 0), my1 + (uint64_t)((s1 * C::kYTile) >> 4) + off, fresh);
-          mma_commit_e(C::kSep ? &bar_Pr[buf] : &bar_Sr[buf]);
+          mma_commit_e(C::kSep ? &bar_Pr[buf] : &bar_dPr[buf]);
         }
         if (!ok) break;
         mma_commit_e(&empty1[s1]);
-        if (m == n - 1) mma_commit_e(bar_acc);
+        if (m == n - 1) {
+          mma_commit_e(bar_acc);
+          if (lane == 0) mbar_arrive(bar_go);
+        }
       }
       ++n_run;
     }
@@ -754,48 +763,55 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       }
       return v;
     };
+    // Rows of Y that this thread's row admits: [lo, hi) and (dQ pass) those below `sink`; tiles inside
+    // [full_lo, full_hi) are admitted whole by every row of the F tile.
+    struct Limits {
+      int lo, hi, sink, full_lo, full_hi;
+    };
+    auto limits_of = [&](const Run& q) {
+      Limits l{0, 0, 0, 0, 0};
+      const Unit& u = q.u;
+      const int f0 = q.x * kT;
+      auto cl = [](long long x) { return (int)max(-(1LL << 30), min(x, 1LL << 30)); };
+      const long long first = KV ? f0 - u.off : f0 + u.off, own = first + r;  // of the tile, of this row
+      if constexpr (KV) {
+        l.hi = l.full_hi = u.Sq;
+        if (a.causal) {
+          l.lo = cl(own);
+          l.full_lo = cl(first + kT - 1);
+        }
+        if (a.window > 0) {
+          if (f0 + r >= a.n_sink) l.hi = min(l.hi, cl(own + a.window));
+          l.full_hi = min(l.full_hi, cl(first + a.window));
+        }
+      } else {
+        l.hi = l.full_hi = u.Skv;
+        if (a.causal) {
+          l.hi = min(l.hi, cl(own + 1));
+          l.full_hi = min(l.full_hi, cl(first + 1));
+        }
+        if (a.window > 0) {
+          l.lo = cl(own - a.window + 1);
+          l.full_lo = cl(first + kT - a.window);
+          l.sink = min(a.n_sink, l.hi);
+        }
+      }
+      return l;
+    };
+    Limits lim = limits_of(run);
     float2 stat = row_stat(run);
+    ItemWalk<TY, KV> y(a, run);
     int it = 0, n_run = 0, n_part = 0;
     bool ok = true;
     while (ok && run.n > 0) {
       const int f0 = run.x * kT;
       const Unit& u = run.u;
       const uint64_t nlse2 = f2pack(-stat.x, -stat.x), ndd = f2pack(-stat.y, -stat.y);
-      // Rows of Y that this thread's row admits: [lo, hi) and (dQ pass) those below `sink`; tiles inside
-      // [full_lo, full_hi) are admitted whole by every row of the F tile.
-      int lo = 0, hi, sink = 0, full_lo = 0, full_hi;
-      {
-        auto cl = [](long long x) { return (int)max(-(1LL << 30), min(x, 1LL << 30)); };
-        const long long first = KV ? f0 - u.off : f0 + u.off, own = first + r;  // of the tile, of this row
-        if constexpr (KV) {
-          hi = full_hi = u.Sq;
-          if (a.causal) {
-            lo = cl(own);
-            full_lo = cl(first + kT - 1);
-          }
-          if (a.window > 0) {
-            if (f0 + r >= a.n_sink) hi = min(hi, cl(own + a.window));
-            full_hi = min(full_hi, cl(first + a.window));
-          }
-        } else {
-          hi = full_hi = u.Skv;
-          if (a.causal) {
-            hi = min(hi, cl(own + 1));
-            full_hi = min(full_hi, cl(first + 1));
-          }
-          if (a.window > 0) {
-            lo = cl(own - a.window + 1);
-            full_lo = cl(first + kT - a.window);
-            sink = min(a.n_sink, hi);
-          }
-        }
-      }
-      ItemWalk<TY, KV> y(a, run);
       for (int m = 0; m < run.n * SUB; ++m, ++it) {  // (it counts 64- or 128-column items here)
         if (m > 0 && (SUB == 1 || (m & 1) == 0)) y.step(u);
         if (TN == 64 && (it & 1) != wg) continue;  // the other warpgroup's
         const int row0 = y.row0 + (SUB == 1 ? 0 : (m & 1) * TN);
-        const bool mask = row0 < full_lo || row0 + TN > full_hi;
+        const bool mask = row0 < lim.full_lo || row0 + TN > lim.full_hi;
         const int bs = it % NS, bd = it % ND, bp = it & 1;
         const uint32_t sc = lanes + C::kS + bs * TN + c0, dc = lanes + C::kDP + bd * TN + c0;
         const uint32_t pc = lanes + C::kP + bp * C::kPStep + c0;
@@ -805,24 +821,31 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
         tc_fence_after();
         tmem_ld32(sc, s);
         tmem_ld32(sc + 32, s + 32);
-        if constexpr (C::kSep) {  // the next S need not wait for this dP
-          tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_Sr[bs]);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_Sr[bs]);  // (the next S need not wait for this dP)
+        // the exponentials before dP is waited for (under its product; in one loop with dS: 174 and 239 us for
+        // 3314 rows with and without a window, so: 169 and 234)
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const uint64_t x = f2pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          float e0, e1;
+          f2unpack(KV ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
+          s[c] = __float_as_uint(ex2_approx(e0));
+          s[c + 1] = __float_as_uint(ex2_approx(e1));
         }
         ok = mbar_wait_warp(&bar_dP[bp], (uint32_t)(it >> 1) & 1u, a.err, abort_flag);
-        if (!ok) {
-          tmem_wait_ld();
-          break;
-        }
+        if (!ok) break;
         tc_fence_after();
         tmem_ld32(dc, p);
         tmem_ld32(dc + 32, p + 32);
         tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_dPr[bd]);
+        if constexpr (C::kSep) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_dPr[bd]);
+        }
         if constexpr (C::kSep) {
           ok = mbar_wait_warp(&bar_Pr[bp], ((uint32_t)(it >> 1) & 1u) ^ 1u, a.err, abort_flag);
           if (!ok) break;
@@ -834,12 +857,9 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             const int k = q * 32 + 2 * c;
-            const uint64_t x = f2pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
             uint64_t g = f2pack(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
-            float e0, e1, x0, x1;
-            f2unpack(KV ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
-            e0 = ex2_approx(e0);
-            e1 = ex2_approx(e1);
+            const float e0 = __uint_as_float(s[k]), e1 = __uint_as_float(s[k + 1]);
+            float x0, x1;
             if constexpr (KV) tp[c] = pack_bf16x2(e0, e1);
             else g = add2(g, ndd);
             f2unpack(mul2(g, f2pack(e0, e1)), x0, x1);
@@ -849,7 +869,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
             // (a weight out of the row's columns may be inf, dP of a column that is no row anything:
             // both operands are cleared after their rounding)
             const int c1 = row0 + c0 + q * 32;
-            const uint32_t in = (bits_below(hi - c1) & ~bits_below(lo - c1)) | bits_below(sink - c1);
+            const uint32_t in = (bits_below(lim.hi - c1) & ~bits_below(lim.lo - c1)) | bits_below(lim.sink - c1);
             if constexpr (KV) keep_bits<16>(tp, in);
             keep_bits<16>(t, in);
           }
@@ -863,8 +883,11 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       }
       if (!ok) break;
       // ---- the run's sums: rows of the output, or fp32 partials ----
+      // (what the next run needs, while this one's last products end)
       const Run next = w.next();
       stat = row_stat(next);
+      lim = limits_of(next);
+      y = ItemWalk<TY, KV>(a, next);
       const bool part = run.n != run.cnt;
       // KV: warpgroup 0 dV, 1 dK; else a half of dQ's columns each
       constexpr int kCols = KV ? D : D / 2;
