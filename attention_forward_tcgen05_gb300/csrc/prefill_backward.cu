@@ -54,29 +54,26 @@ constexpr int kMaxCtas = kBackwardCtas;
 constexpr int run_cost(bool kv, int ty) { return (kv ? 640 : 128) / ty; }
 constexpr int kMinCost = 8;  // of a slice
 
-// TN: columns of S and dP per item.  64: the softmax warpgroups take an item each in turn, so that
-// one's loads and stores run under the other's exponentials; S, dP and the bf16 P and dS have columns
-// of their own, so that the next S waits for the softmax's load only.  128, halved between the
-// warpgroups (dQ pass, d = 128): a product of 64 columns re-reads as much of F for half of the work
-// (49 cycles a step, bound by shared memory, against 65 for 128 columns), which its one small
-// second product does not make up for; there dS lies over dP, two dP beside one S: of an item's
-// two products the one that waits for the second product two items back is then the one that
-// the softmax needs last, after its exponentials.
+// TN: rows of a Y tile, the columns of an item's S and dP.
+//   128, halved between the softmax warpgroups.  P and dS go back over dP, two dP beside one S: of
+//     an item's two products the one that waits for the second products two items back is then the
+//     one that the softmax needs last, after its exponentials.
+//   64 (dK/dV pass, d = 128, whose sums leave 256 columns): the warpgroups take an item each in turn;
+//     one S, one dP and two of P and dS, so that the next S waits for the softmax's load only.  A
+//     product of 64 columns re-reads as much of F for half of the work (49 cycles a step, bound by
+//     shared memory, against 65 for 128 columns); elsewhere items of 64 were slower (d = 64, 2 x 16
+//     heads of 4096, not causal: 552 us, with three warpgroups of softmax 623, against 436).
 template <int D, bool KV>
 struct BwdCfg {
-  static constexpr int TN = (D == 128 && !KV) ? 128 : 64;
-  // Rows of a Y tile: a copy takes 300 to 400 cycles of the copy engine whatever its size, so tiles of
-  // 64 rows of 64 columns would take longer to bring than to use.  kSub items a tile.
-  static constexpr int TY = (D == 128 && KV) ? 64 : 128;
-  static constexpr int kSub = TY / TN;
-  static constexpr bool kSep = TN == 64;                   // P and dS in columns of their own
-  static constexpr int NS = D == 128 ? 1 : 2;              // S buffers
-  static constexpr int ND = (D == 128 && KV) ? 1 : 2;      // dP buffers
+  static constexpr int TN = (D == 128 && KV) ? 64 : 128;
+  static constexpr bool kSep = TN == 64;                   // P and dS in columns of their own, not over dP
+  static constexpr int NS = 1;                             // S buffers
+  static constexpr int ND = kSep ? 1 : 2;                  // dP buffers
   static constexpr int kArrive = TN == 64 ? 4 : 8;         // softmax warps of an item
   static constexpr int kPanels = D / 64;
   static constexpr int kFPanel = kT * 128;
   static constexpr int kFTile = kPanels * kFPanel;
-  static constexpr int kYPanel = TY * 128;
+  static constexpr int kYPanel = TN * 128;
   static constexpr int kYTile = kPanels * kYPanel;
   static constexpr int kSt1 = D == 64 ? 4 : (KV ? 5 : 3);  // ring of Y1
   static constexpr int kSt2 = D == 64 ? 4 : (KV ? 4 : 2);  // ring of Y2
@@ -84,8 +81,8 @@ struct BwdCfg {
   static constexpr int kY2Off = kY1Off + kSt1 * kYTile;
   // columns beside the dK/dV pass's tiles, 16 bytes a row: lse beside Q, D beside g, ones beside K
   // and V, and zeros, the second eight columns of all of them
-  static constexpr int kExt = KV ? TY * 16 : 0;
-  static constexpr int kExtSlots = 4;
+  static constexpr int kExt = KV ? TN * 16 : 0;
+  static constexpr int kExtSlots = 5;
   static constexpr int kOnes = KV ? kT * 16 : 0;
   static constexpr int kExt1Off = kY2Off + kSt2 * kYTile;
   static constexpr int kExt2Off = kExt1Off + kExtSlots * kExt;
@@ -100,7 +97,7 @@ struct BwdCfg {
   static constexpr uint32_t kDP = kS + NS * TN;
   // P and dS of an item (two buffers): kP + buffer * kPStep
   static constexpr uint32_t kP = kSep ? kDP + ND * TN : kDP;
-  static constexpr uint32_t kPStep = kSep ? (KV ? 64 : 32) : TN;
+  static constexpr uint32_t kPStep = TN;
   static_assert(kP + 2 * kPStep <= 512 && kDP + ND * TN <= 512, "TMEM budget");
   static constexpr int kThreads = 384;
 };
@@ -112,7 +109,7 @@ struct Unit {
   int nt, t0;                 // Y tiles, dK/dV pass: from t0 on; dQ pass: by the tile list
   TileList tl;
 };
-template <int TY, bool KV>
+template <int TN, bool KV>
 __device__ __forceinline__ Unit unit_of(const BackwardArgs& a, int b, int x) {
   Unit u;
   const SeqExtent e = seq_extent(b, a.Sq, a.Skv, a.cu_q, a.kv_lens, a.total_q);
@@ -130,14 +127,14 @@ __device__ __forceinline__ Unit unit_of(const BackwardArgs& a, int b, int x) {
     long long hi = u.Sq;
     if (a.window > 0 && f0 >= a.n_sink) hi = min(hi, last + (long long)a.window - u.off);
     if (hi <= lo) return u;
-    u.t0 = (int)(lo / TY);
-    u.nt = (int)((hi + TY - 1) / TY) - u.t0;
+    u.t0 = (int)(lo / TN);
+    u.nt = (int)((hi + TN - 1) / TN) - u.t0;
   } else {
     if (f0 >= u.Sq) return u;
     const int last = min(u.Sq, f0 + kT) - 1;
     const long long hi = a.causal ? min((long long)u.Skv, max(0LL, last + u.off + 1)) : u.Skv;
-    const int n = (int)((hi + TY - 1) / TY);
-    u.tl = tile_list(f0 + u.off, n, a.window, a.n_sink, u.Skv, TY);
+    const int n = (int)((hi + TN - 1) / TN);
+    u.tl = tile_list(f0 + u.off, n, a.window, a.n_sink, u.Skv, TN);
     u.nt = tile_list_len(u.tl, n);
   }
   return u;
@@ -146,9 +143,9 @@ template <bool KV>
 __device__ __forceinline__ int unit_items(const BackwardArgs& a, const Unit& u) {
   return KV ? u.nt * (a.Hq / a.Hkv) : u.nt;
 }
-template <int TY, bool KV>
+template <int TN, bool KV>
 __device__ __forceinline__ int unit_cost(int items) {
-  return items > 0 ? items + run_cost(KV, TY) : 0;
+  return items > 0 ? items + run_cost(KV, TN) : 0;
 }
 // Groups (sequence, F tile) of the pass: each holds a unit per head.
 __host__ __device__ __forceinline__ int f_tiles(const BackwardArgs& a, bool kv) {
@@ -186,7 +183,7 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi, uint32_t& mid, uin
 }
 
 // Exclusive prefix of the groups' costs (all heads of a group) by one CTA; pre[n] the total.
-template <int TY, bool KV>
+template <int TN, bool KV>
 __device__ void scan_costs(const BackwardArgs& a, int* pre) {
   __shared__ int sums[kPrepThreads / 32];
   const int nx = f_tiles(a, KV), n = a.B * nx, H = KV ? a.Hkv : a.Hq;
@@ -199,7 +196,7 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
       const int c0 = min(max(a.cu_q[b], 0), a.total_q), c1 = min(a.cu_q[b + 1], a.total_q);
       if (c1 - c0 > a.Sq) atomicCAS(a.err, kErrNone, kErrBadShape);
     }
-  for (int g = lo; g < hi; ++g) s += unit_cost<TY, KV>(unit_items<KV>(a, unit_of<TY, KV>(a, g / nx, g % nx))) * H;
+  for (int g = lo; g < hi; ++g) s += unit_cost<TN, KV>(unit_items<KV>(a, unit_of<TN, KV>(a, g / nx, g % nx))) * H;
   int incl = s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -213,7 +210,7 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
   for (int w = 0; w < warp; ++w) at += sums[w];
   for (int g = lo; g < hi; ++g) {
     pre[g] = at;
-    at += unit_cost<TY, KV>(unit_items<KV>(a, unit_of<TY, KV>(a, g / nx, g % nx))) * H;
+    at += unit_cost<TN, KV>(unit_items<KV>(a, unit_of<TN, KV>(a, g / nx, g % nx))) * H;
   }
   if (hi == n && lo < n) pre[n] = at;
   if (n == 0 && threadIdx.x == 0) pre[0] = 0;
@@ -227,7 +224,7 @@ __device__ void zero_units(const BackwardArgs& a, int c, int n) {
   constexpr int kRows = 16;  // of a CTA's turn
   for (int gc = c; gc < n_groups * (kT / kRows); gc += n) {
     const int g = gc / (kT / kRows), b = g / nx, x = g - b * nx;
-    const Unit u = unit_of<BwdCfg<D, KV>::TY, KV>(a, b, x);
+    const Unit u = unit_of<BwdCfg<D, KV>::TN, KV>(a, b, x);
     if (unit_items<KV>(a, u) > 0) continue;
     const int f0 = x * kT + gc % (kT / kRows) * kRows;
     const int rows = min(kRows, (KV ? (a.fill ? a.Skv : u.Skv) : u.Sq) - f0);
@@ -256,8 +253,8 @@ constexpr int kPrepRows = 4;
 template <int D, bool OBF16>
 __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __grid_constant__ BackwardArgs a) {
   if (blockIdx.x < 2) {
-    if (blockIdx.x == 0) scan_costs<BwdCfg<D, true>::TY, true>(a, a.pre_k);
-    else scan_costs<BwdCfg<D, false>::TY, false>(a, a.pre_q);
+    if (blockIdx.x == 0) scan_costs<BwdCfg<D, true>::TN, true>(a, a.pre_k);
+    else scan_costs<BwdCfg<D, false>::TN, false>(a, a.pre_q);
     for (int i = threadIdx.x; i < kMaxCtas; i += kPrepThreads) a.joined[blockIdx.x * kMaxCtas + i] = 0;
     return;
   }
@@ -318,7 +315,7 @@ struct Run {
   int b, x, h, i0, n, cnt, first;  // cnt: items of the unit, first: the place of its first one
 };
 // The items of a slice in order, run by run of one unit.
-template <int TY, bool KV>
+template <int TN, bool KV>
 struct Walk {
   const BackwardArgs& a;
   int per, pos, end;  // a slice's share of the list of costs, place in it, end of the slice
@@ -350,7 +347,7 @@ struct Walk {
     const int nx = f_tiles(a, KV);
     at.b = g / nx;
     at.x = g - at.b * nx;
-    at.u = unit_of<TY, KV>(a, at.b, at.x);
+    at.u = unit_of<TN, KV>(a, at.b, at.x);
     at.cnt = unit_items<KV>(a, at.u);
     g0 = pre()[g];
   }
@@ -360,17 +357,17 @@ struct Walk {
     const int H = KV ? a.Hkv : a.Hq;
     at.n = 0;
     while (pos < end) {
-      while (pos >= g0 + unit_cost<TY, KV>(at.cnt) * H) {
+      while (pos >= g0 + unit_cost<TN, KV>(at.cnt) * H) {
         ++g;
         enter();
       }
-      const int cost = unit_cost<TY, KV>(at.cnt);
+      const int cost = unit_cost<TN, KV>(at.cnt);
       at.h = (pos - g0) / cost;
       const int from = pos - g0 - at.h * cost, to = min(cost, from + end - pos);  // of the unit's cost
       pos += to - from;
-      at.first = g0 + at.h * cost + run_cost(KV, TY);
-      at.i0 = max(0, from - run_cost(KV, TY));
-      at.n = max(0, to - run_cost(KV, TY)) - at.i0;
+      at.first = g0 + at.h * cost + run_cost(KV, TN);
+      at.i0 = max(0, from - run_cost(KV, TN));
+      at.n = max(0, to - run_cost(KV, TN)) - at.i0;
       if (at.n > 0) break;
     }
     return at;
@@ -378,7 +375,7 @@ struct Walk {
 };
 
 // Y tile of an item of a run: its first row (query rows of head h, or keys), and the head.
-template <int TY, bool KV>
+template <int TN, bool KV>
 struct ItemWalk {
   int h, t, row0;
   __device__ __forceinline__ ItemWalk(const BackwardArgs& a, const Run& r) : h(0), t(0), row0(0) {
@@ -388,11 +385,11 @@ struct ItemWalk {
       const int q = r.i0 / r.u.nt;
       h = r.h * G + q;
       t = r.i0 - q * r.u.nt;
-      row0 = (r.u.t0 + t) * TY;
+      row0 = (r.u.t0 + t) * TN;
     } else {
       h = r.h / G;
       t = r.i0;
-      row0 = tile_list_key(r.u.tl, t) * TY;
+      row0 = tile_list_key(r.u.tl, t) * TN;
     }
   }
   __device__ __forceinline__ void step(const Unit& u) {
@@ -402,9 +399,9 @@ struct ItemWalk {
         t = 0;
         ++h;
       }
-      row0 = (u.t0 + t) * TY;
+      row0 = (u.t0 + t) * TN;
     } else {
-      row0 = tile_list_key(u.tl, t) * TY;
+      row0 = tile_list_key(u.tl, t) * TN;
     }
   }
 };
@@ -443,13 +440,13 @@ __device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
 }
 
 // The items whose tiles (or lse / D columns) a warp still has to bring.
-template <int TY, bool KV>
+template <int TN, bool KV>
 struct Stream {
-  Walk<TY, KV> w;
+  Walk<TN, KV> w;
   Run r;
-  ItemWalk<TY, KV> y;
+  ItemWalk<TN, KV> y;
   int m, it;
-  __device__ __forceinline__ Stream(const BackwardArgs& a, const Walk<TY, KV>& w_)
+  __device__ __forceinline__ Stream(const BackwardArgs& a, const Walk<TN, KV>& w_)
       : w(w_), r(w.next()), y(a, r), m(0), it(0) {}
   __device__ __forceinline__ void step(const BackwardArgs& a) {
     ++it;
@@ -459,7 +456,7 @@ struct Stream {
     }
     m = 0;
     r = w.next();
-    y = ItemWalk<TY, KV>(a, r);
+    y = ItemWalk<TN, KV>(a, r);
   }
 };
 
@@ -467,7 +464,7 @@ struct Stream {
 template <int D, bool KV>
 __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, int ctas) {
   using C = BwdCfg<D, KV>;
-  constexpr int NS = C::NS, ND = C::ND, TN = C::TN, TY = C::TY, SUB = C::kSub;
+  constexpr int NS = C::NS, ND = C::ND, TN = C::TN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -481,7 +478,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
   uint64_t* bar_S = emptyF + 2;
   uint64_t* bar_Sr = bar_S + 2;        // [NS] S read
   uint64_t* bar_dP = bar_Sr + NS;
-  uint64_t* bar_dPr = bar_dP + 2;      // [ND] dP read (where dS lies over it: dS used up)
+  uint64_t* bar_dPr = bar_dP + 2;      // [ND] dP read (where P and dS lie over it: they are used up)
   uint64_t* bar_P = bar_dPr + ND;      // [2] P and dS stored
   uint64_t* bar_Pr = bar_P + 2;        // [2] P and dS used up
   uint64_t* bar_acc = bar_Pr + 2;      // a run's sums complete
@@ -525,8 +522,8 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const Walk<TY, KV> start(a, cta, ctas, lane);  // (a chain of dependent loads: made once)
-  Walk<TY, KV> w = start;
+  const Walk<TN, KV> start(a, cta, ctas, lane);  // (a chain of dependent loads: made once)
+  Walk<TN, KV> w = start;
   Run run = w.next();
   if (warp == 8 || warp == 9) {
     // ---- first products: S = F1 Y1^T (warp 8), dP = F2 Y2^T (warp 9), and their F tiles ----
@@ -544,9 +541,9 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     const uint32_t ext = smem_u32(smem + (first ? C::kExt1Off : C::kExt2Off)), zero = smem_u32(smem + C::kZeroOff);
     const uint64_t d1 = smem_desc(smem_u32(smem + C::kOnesOff), C::kOnes, 128, kSwizzleNone);
     if (lane == 0) tma_prefetch_desc(map);
-    // the lse / D columns of an item, two items ahead (a tensor or bulk copy of them would take the
-    // copy engine as long as a tile)
-    Stream<TY, KV> ex(a, start);
+    // the lse / D columns of an item (a tensor or bulk copy of them would take the copy engine as long
+    // as a tile: 300 to 400 cycles whatever its size)
+    Stream<TN, KV> ex(a, start);
     auto load_ext = [&] {
       if constexpr (KV) {
         if (ex.r.n > 0) {
@@ -555,14 +552,15 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
           const uint4* src = (first ? a.ext1 : a.ext2) + i;
           const uint32_t dst = ext + ex.it % C::kExtSlots * C::kExt;
 #pragma unroll
-          for (int k = 0; k < TY; k += 32) cp_async16(dst + (k + lane) * 16, src + k + lane, 16);
+          for (int k = 0; k < TN; k += 32) cp_async16(dst + (k + lane) * 16, src + k + lane, 16);
           ex.step(a);
         }
         cp_async_commit();
       }
     };
-    // item `it`'s columns are whole for the tensor core; those of it + 2 on their way, into the slot
-    // of it - 2, whose product the softmax has read where that of it is issued
+    // The next item's columns are whole for the tensor core, those three items on are on their way: after
+    // item `it` is issued, into the slot of it - 2, whose product is done, as `it` waited for a buffer
+    // (with two of them for that of it - 2, else for it - 1).
     auto next_ext = [&] {
       if constexpr (KV) {
         load_ext();
@@ -587,33 +585,27 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       // behind the run before: its sums go out under these products, not after them
       if (ok && n_run > 0) ok = mbar_wait_warp(bar_go, (uint32_t)(n_run - 1) & 1u, a.err, abort_flag);
       for (int m = 0; ok && m < n; ++m, ++it) {
-        const int s = it % stages;
-        const uint32_t ph_f = (uint32_t)(it / stages) & 1u;
-#pragma unroll
-        for (int sub = 0; sub < SUB; ++sub) {
-          const int si = it * SUB + sub, buf = si % bufs;
-          const uint32_t ph_b = ((uint32_t)(si / bufs) & 1u) ^ 1u;
-          // both at once, one by one only where they are not ready
-          const bool r0 = sub > 0 || mbar_test(&full[s], ph_f), r1 = mbar_test(&freed[buf], ph_b);
-          if (!__all_sync(0xFFFFFFFFu, r0 & r1)) {
-            ok = mbar_wait_warp(&freed[buf], ph_b, a.err, abort_flag) &&
-                 mbar_wait_warp(&full[s], ph_f, a.err, abort_flag);
-            if (!ok) break;
-          }
-          tc_fence_after();
-          const uint64_t y = dy + (uint64_t)((s * C::kYTile + sub * TN * 128) >> 4);
-          const uint32_t d = out + buf * TN;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss_e(d, df + (uint64_t)(((kk >> 2) * C::kFPanel + (kk & 3) * 32) >> 4),
-                     y + (uint64_t)(((kk >> 2) * C::kYPanel + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
-          if constexpr (KV) {
-            const uint32_t e = ext + it % C::kExtSlots * C::kExt + sub * TN * 16;
-            mma_ss_e(d, d1, smem_desc(e, zero - e, 128, kSwizzleNone), idesc, 1u);
-          }
-          mma_commit_e(&done[si & 1]);
+        const int s = it % stages, buf = it % bufs;
+        const uint32_t ph_f = (uint32_t)(it / stages) & 1u, ph_b = ((uint32_t)(it / bufs) & 1u) ^ 1u;
+        // both at once, one by one only where they are not ready
+        const bool r0 = mbar_test(&full[s], ph_f), r1 = mbar_test(&freed[buf], ph_b);
+        if (!__all_sync(0xFFFFFFFFu, r0 & r1)) {
+          ok = mbar_wait_warp(&freed[buf], ph_b, a.err, abort_flag) &&
+               mbar_wait_warp(&full[s], ph_f, a.err, abort_flag);
+          if (!ok) break;
         }
-        if (!ok) break;
+        tc_fence_after();
+        const uint64_t y = dy + (uint64_t)((s * C::kYTile) >> 4);
+        const uint32_t d = out + buf * TN;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss_e(d, df + (uint64_t)(((kk >> 2) * C::kFPanel + (kk & 3) * 32) >> 4),
+                   y + (uint64_t)(((kk >> 2) * C::kYPanel + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+        if constexpr (KV) {
+          const uint32_t e = ext + it % C::kExtSlots * C::kExt;
+          mma_ss_e(d, d1, smem_desc(e, zero - e, 128, kSwizzleNone), idesc, 1u);
+        }
+        mma_commit_e(&done[it & 1]);
         if (!KV && !first) mma_commit_e(&empty2[s]);
         if (m == n - 1) mma_commit_e(eF);
         next_ext();  // (of item it + 1, off the way from one product to the next)
@@ -628,8 +620,8 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
     const uint64_t my1 = smem_desc(smem_u32(smem + C::kY1Off), C::kYPanel, 1024, kSwizzle128B);
     const uint64_t my2 = smem_desc(smem_u32(smem + C::kY2Off), C::kYPanel, 1024, kSwizzle128B);
-    // A in TMEM, 16 columns of Y's rows at a time (where dS lies over dP: 32 columns for each 64 of
-    // dP); Y MN-major
+    // A in TMEM, 16 rows of Y at a time (8 columns; of each half of dP's where it lies over dP); Y
+    // MN-major
     auto issue = [&](uint32_t acc, uint32_t p, uint64_t y, bool fresh) {
 #pragma unroll
       for (int kk = 0; kk < TN / 16; ++kk)
@@ -643,25 +635,18 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       run = w.next();
       if (n_run > 0) ok = mbar_wait_warp(bar_accr, (uint32_t)(n_run - 1) & 1u, a.err, abort_flag);
       for (int m = 0; ok && m < n; ++m, ++it) {
-        const int s1 = it % C::kSt1, s2 = it % C::kSt2;
-#pragma unroll
-        for (int sub = 0; sub < SUB; ++sub) {
-          const int si = it * SUB + sub, buf = si & 1;
-          const uint32_t p = tmem + C::kP + buf * C::kPStep;
-          const uint64_t off = (uint64_t)((sub * TN * 128) >> 4);
-          // (dP is done where dS is stored, so g's tile is whole)
-          ok = mbar_wait_warp(&bar_P[buf], (uint32_t)(si >> 1) & 1u, a.err, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const bool fresh = m == 0 && sub == 0;
-          if constexpr (KV) {
-            issue(0, p, my2 + (uint64_t)((s2 * C::kYTile) >> 4) + off, fresh);
-            if (sub == SUB - 1) mma_commit_e(&empty2[s2]);
-          }
-          issue(C::kAcc1, p + (KV ? 32 : 0), my1 + (uint64_t)((s1 * C::kYTile) >> 4) + off, fresh);
-          mma_commit_e(C::kSep ? &bar_Pr[buf] : &bar_dPr[buf]);
-        }
+        const int s1 = it % C::kSt1, s2 = it % C::kSt2, buf = it & 1;
+        const uint32_t p = tmem + C::kP + buf * C::kPStep;
+        // (dP is done where dS is stored, so g's tile is whole)
+        ok = mbar_wait_warp(&bar_P[buf], (uint32_t)(it >> 1) & 1u, a.err, abort_flag);
         if (!ok) break;
+        tc_fence_after();
+        if constexpr (KV) {
+          issue(0, p, my2 + (uint64_t)((s2 * C::kYTile) >> 4), m == 0);
+          mma_commit_e(&empty2[s2]);
+        }
+        issue(C::kAcc1, p + (KV ? 32 : 0), my1 + (uint64_t)((s1 * C::kYTile) >> 4), m == 0);
+        mma_commit_e(C::kSep ? &bar_Pr[buf] : &bar_dPr[buf]);
         mma_commit_e(&empty1[s1]);
         if (m == n - 1) {
           mma_commit_e(bar_acc);
@@ -672,7 +657,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     }
   } else if (warp == 11) {
     // ---- the rings of Y1 and Y2, each slot filled as soon as it is free ----
-    Stream<TY, KV> st[2] = {Stream<TY, KV>(a, start), Stream<TY, KV>(a, start)};
+    Stream<TN, KV> st[2] = {Stream<TN, KV>(a, start), Stream<TN, KV>(a, start)};
     if (lane == 0) {
       tma_prefetch_desc(KV ? &a.tm_qy : &a.tm_ky);
       tma_prefetch_desc(KV ? &a.tm_doy : &a.tm_vy);
@@ -684,7 +669,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       bool moved = false;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        Stream<TY, KV>& t = st[k];
+        Stream<TN, KV>& t = st[k];
         if (t.r.n == 0) continue;
         const int stages = k == 0 ? C::kSt1 : C::kSt2, s = t.it % stages;
         uint64_t *full = k == 0 ? full1 : full2, *empty = k == 0 ? empty1 : empty2;
@@ -696,18 +681,18 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
         const int rows = KV ? u.Sq : u.Skv;  // Y rows of the sequence
         const int row_base = KV ? u.qbase : u.kbase;
         // a packed batch: other rows follow a sequence's own
-        const bool whole = a.cu_q == nullptr || t.y.row0 + TY <= rows;
+        const bool whole = a.cu_q == nullptr || t.y.row0 + TN <= rows;
         if (!whole) {
           // its last rows are gathered, so that the rows behind them arrive as zeros (a weight of
           // zero times what lies there could be NaN)
           const uint16_t* base = KV ? (k == 0 ? a.q : a.dout) : (k == 0 ? a.k : a.v);
-          int ri[TY / 32];
+          int ri[TN / 32];
 #pragma unroll
-          for (int e = 0; e < TY / 32; ++e) {
+          for (int e = 0; e < TN / 32; ++e) {
             const int r = t.y.row0 + e * 32 + lane;
             ri[e] = r < rows ? row_base + r : -1;
           }
-          paged_gather<D, TY / 32>(smem_u32(dst), C::kYPanel, base, KV ? a.Hq : a.Hkv, t.y.h, lane, ri);
+          paged_gather<D, TN / 32>(smem_u32(dst), C::kYPanel, base, KV ? a.Hq : a.Hkv, t.y.h, lane, ri);
           cp_async_commit();
           cp_async_wait<0>();
           fence_proxy_async_smem();
@@ -800,17 +785,17 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     };
     Limits lim = limits_of(run);
     float2 stat = row_stat(run);
-    ItemWalk<TY, KV> y(a, run);
+    ItemWalk<TN, KV> y(a, run);
     int it = 0, n_run = 0, n_part = 0;
     bool ok = true;
     while (ok && run.n > 0) {
       const int f0 = run.x * kT;
       const Unit& u = run.u;
       const uint64_t nlse2 = f2pack(-stat.x, -stat.x), ndd = f2pack(-stat.y, -stat.y);
-      for (int m = 0; m < run.n * SUB; ++m, ++it) {  // (it counts 64- or 128-column items here)
-        if (m > 0 && (SUB == 1 || (m & 1) == 0)) y.step(u);
+      for (int m = 0; m < run.n; ++m, ++it) {
+        if (m > 0) y.step(u);
         if (TN == 64 && (it & 1) != wg) continue;  // the other warpgroup's
-        const int row0 = y.row0 + (SUB == 1 ? 0 : (m & 1) * TN);
+        const int row0 = y.row0;
         const bool mask = row0 < lim.full_lo || row0 + TN > lim.full_hi;
         const int bs = it % NS, bd = it % ND, bp = it & 1;
         const uint32_t sc = lanes + C::kS + bs * TN + c0, dc = lanes + C::kDP + bd * TN + c0;
@@ -887,7 +872,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       const Run next = w.next();
       stat = row_stat(next);
       lim = limits_of(next);
-      y = ItemWalk<TY, KV>(a, next);
+      y = ItemWalk<TN, KV>(a, next);
       const bool part = run.n != run.cnt;
       // KV: warpgroup 0 dV, 1 dK; else a half of dQ's columns each
       constexpr int kCols = KV ? D : D / 2;
@@ -1044,8 +1029,8 @@ cudaError_t launch_d(const BackwardArgs& a, cudaStream_t stream) {
 }  // namespace
 
 int backward_tile_rows(int d, bool dkdv) {
-  if (d == 64) return dkdv ? BwdCfg<64, true>::TY : BwdCfg<64, false>::TY;
-  return dkdv ? BwdCfg<128, true>::TY : BwdCfg<128, false>::TY;
+  if (d == 64) return dkdv ? BwdCfg<64, true>::TN : BwdCfg<64, false>::TN;
+  return dkdv ? BwdCfg<128, true>::TN : BwdCfg<128, false>::TN;
 }
 
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t stream) {
