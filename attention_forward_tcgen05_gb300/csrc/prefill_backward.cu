@@ -908,37 +908,34 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       ok = mbar_wait_warp(bar_acc, (uint32_t)n_run & 1u, a.err, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      constexpr int kStep = kCols >= 64 ? 64 : kCols;
 #pragma unroll 1
-      for (int c1 = 0; c1 < kCols; c1 += kStep) {
-        uint32_t v[kStep];
-#pragma unroll
-        for (int e = 0; e < kStep; e += 32) tmem_ld32(lanes + col0 + c1 + e, v + e);
+      for (int c = 0; c < kCols; c += 32) {
+        uint32_t x[32];
+        tmem_ld32(lanes + col0 + c, x);
         tmem_wait_ld();
-        if (c1 + kStep == kCols) {  // the next run's sums may start
+        if (c + 32 == kCols) {  // the next run's sums may start
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_accr);
         }
 #pragma unroll
-        for (int c = 0; c < kStep; c += 32) {
-          const uint32_t* x = v + c;
-          if (part) {
+        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+        if (part) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              pp[(size_t)((c1 + c + e) / 4) * kT] =
-                  make_float4(__uint_as_float(x[e]) * f, __uint_as_float(x[e + 1]) * f, __uint_as_float(x[e + 2]) * f,
-                              __uint_as_float(x[e + 3]) * f);
-          } else {
-            uint4 q[4];
+          for (int e = 0; e < 32; e += 4)
+            pp[(size_t)((c + e) / 4) * kT] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
+                                                         __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+        } else {
+          uint4 q[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e, x += 8)
-              q[e] = make_uint4(pack_bf16x2(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f),
-                                pack_bf16x2(__uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f),
-                                pack_bf16x2(__uint_as_float(x[4]) * f, __uint_as_float(x[5]) * f),
-                                pack_bf16x2(__uint_as_float(x[6]) * f, __uint_as_float(x[7]) * f));
-            put_rows(q, c1 + c);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t* y = x + 8 * e;
+            q[e] = make_uint4(pack_bf16x2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                              pack_bf16x2(__uint_as_float(y[2]), __uint_as_float(y[3])),
+                              pack_bf16x2(__uint_as_float(y[4]), __uint_as_float(y[5])),
+                              pack_bf16x2(__uint_as_float(y[6]), __uint_as_float(y[7])));
           }
+          put_rows(q, c);
         }
       }
       if (part) {
@@ -963,32 +960,29 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
         ++n_part;
         if (*last_flag) {
           __threadfence();
-          // (kStep columns of two parts in flight: one 8-column group at a time took 20 us a unit)
+          // (32 columns of two parts in flight: one 8-column group at a time took 20 us a unit)
 #pragma unroll 1
-          for (int c = 0; c < kCols; c += kStep) {
-            float4 x[kStep / 4], y[kStep / 4];
+          for (int c = 0; c < kCols; c += 32) {
+            float4 x[8], y[8];
             const float4* p = parts + (size_t)(c / 4) * kT;
 #pragma unroll
-            for (int e = 0; e < kStep / 4; ++e) x[e] = __ldcg(p + ((size_t)c0 * 2 + 1) * kSlot + (size_t)e * kT);
+            for (int e = 0; e < 8; ++e) x[e] = __ldcg(p + ((size_t)c0 * 2 + 1) * kSlot + (size_t)e * kT);
 #pragma unroll 1
             for (int k = c0 + 1; k <= c1; ++k) {
 #pragma unroll
-              for (int e = 0; e < kStep / 4; ++e) y[e] = __ldcg(p + (size_t)k * 2 * kSlot + (size_t)e * kT);
+              for (int e = 0; e < 8; ++e) y[e] = __ldcg(p + (size_t)k * 2 * kSlot + (size_t)e * kT);
 #pragma unroll
-              for (int e = 0; e < kStep / 4; ++e) {
+              for (int e = 0; e < 8; ++e) {
                 x[e].x += y[e].x; x[e].y += y[e].y; x[e].z += y[e].z; x[e].w += y[e].w;
               }
             }
+            uint4 q[4];
 #pragma unroll
-            for (int h = 0; h < kStep / 32; ++h) {
-              uint4 q[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 u = x[h * 8 + 2 * e], v = x[h * 8 + 2 * e + 1];
-                q[e] = make_uint4(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w), pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-              }
-              put_rows(q, c + h * 32);
+            for (int e = 0; e < 4; ++e) {
+              const float4 u = x[2 * e], v = x[2 * e + 1];
+              q[e] = make_uint4(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w), pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
             }
+            put_rows(q, c);
           }
         }
       }
