@@ -297,6 +297,15 @@ def rope_axes(sections, base: float = 10000.0, layout: str = "blocks", device="c
     return f.to(device), torch.tensor(axes, dtype=torch.int32, device=device)
 
 
+def _positions(t, dev, total):
+    """int32 [n_axes, total]: its pointer and n_axes."""
+    p = _need(t, "positions", _torch().int32, 2, dev)
+    n_axes, n = t.shape
+    if n != total:
+        raise ValueError(f"positions must have shape {[n_axes, total]}, got {list(t.shape)}")
+    return p, n_axes
+
+
 def _token_rows(t, name, bf16, dev, total, H, d):
     """Rows of tokens [total, H, d] with any stride between tokens (a view of a fused
     projection's output, say): (pointer, stride in elements)."""
@@ -345,7 +354,7 @@ def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_
         Hq = q.shape[1]
         qr, qs = _token_rows(q, "q", torch.bfloat16, dev, total, Hq, d)
         if out is None:
-            out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device="cuda")  # (q may be strided)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)  # (q may be strided)
             op = out.data_ptr()
         else:
             op = _sized(out, "out", torch.bfloat16, dev, total, Hq, d)
@@ -359,9 +368,7 @@ def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_
     if axes is not None:
         if inv_freq is None or positions is None:
             raise ValueError("axes need inv_freq and positions")
-        pos = _need(positions, "positions", torch.int32, 2, dev)
-        n_axes = positions.shape[0]
-        _sized(positions, "positions", torch.int32, dev, n_axes, total)
+        pos, n_axes = _positions(positions, dev, total)
     elif positions is not None:
         pos = _sized(positions, "positions", torch.int32, dev, total)
     rot = 0
@@ -391,7 +398,7 @@ def _rotated(t, name, out, dev, total):
     n, H, d = t.shape
     p, s = _token_rows(t, name, torch.bfloat16, dev, total, H, d)
     if out is None:
-        out = torch.empty((total, H, d), dtype=torch.bfloat16, device="cuda")
+        out = torch.empty_like(t, memory_format=torch.contiguous_format)
         return p, s, out, out.data_ptr(), H * d, H, d
     op, os = _token_rows(out, f"out of {name}", torch.bfloat16, dev, total, H, d)
     return p, s, out, op, os, H, d
@@ -435,9 +442,7 @@ def rope_rotate(q, k, inv_freq, positions, axes=None, interleaved: bool = False,
         pos = _sized(positions, "positions", torch.int32, dev, total)
     else:
         ap = _sized(axes, "axes", torch.int32, dev, rot // 2)
-        pos = _need(positions, "positions", torch.int32, 2, dev)
-        n_axes = positions.shape[0]
-        _sized(positions, "positions", torch.int32, dev, n_axes, total)
+        pos, n_axes = _positions(positions, dev, total)
     rc = load().attn_rope_rotate(qr, kr, qs, ks, pos, ap, n_axes, fr, qop, kop, qos, kos, Hq, Hk, total, d, rot,
                                  int(interleaved), int(inverse), amp, handle)
     if rc != ATTN_OK:
