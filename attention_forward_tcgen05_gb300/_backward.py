@@ -123,6 +123,8 @@ def prefill_varlen_backward(do, q, kcache, vcache, o, lse, cu_seqlens_q, kv_lens
     max_sq = int(max_sq)
     fill = int(out is None)
     out, (dq, dk, dv) = _gradients(out, q, kcache, vcache, dev)
+    if fill and B == 0:
+        out[0].zero_()  # (a call of no sequences writes nothing)
     n = attn_prefill_backward_workspace(B, Hq, Hkv, total, max_sq, max_kv, d)
     work, wp = _work(n)
     rc = load().attn_prefill_varlen_backward(gp, qp, kp, vp, op, lp, dp, dq, dk, dv, cu, np_, B, Hq, Hkv, total, max_sq,

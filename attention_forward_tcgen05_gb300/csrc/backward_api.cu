@@ -27,9 +27,13 @@ int check_sizes(const Sizes& z) {
   if (z.d != 64 && z.d != 128) return ATTN_ERR_UNSUPPORTED;
   if (z.rows * z.Hq >= (1LL << 31) || (long long)z.B * z.Skv * z.Hkv >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
   if ((long long)z.Hq * z.d >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
-  // tiles of 64 x 64 of all heads (more than there are, and some for each unit's start), which the kernels count in 32 bits
-  const long long tq = (z.Sq + 63LL) / 64, tk = (z.Skv + 63LL) / 64;
-  if ((tq + 16) * z.B * (tk + 16) >= (1LL << 31) / z.Hq) return ATTN_ERR_INVALID_ARG;
+  // items of all heads, 16 more a block for its run's cost (prefill_backward.cu): counted in 32 bits, a
+  // CTA's share of them beyond the last
+  const long long tq = (z.Sq + 63LL) / 64, tk = (z.Skv + 63LL) / 64, heads = (long long)z.B * z.Hq;
+  auto over = [&](long long blocks, long long items) {
+    return (double)heads * (double)blocks * (double)(items + 16) > 2e9;
+  };
+  if (over((tk + 1) / 2, tq) || over((tq + 1) / 2, tk)) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 

@@ -229,8 +229,8 @@ __device__ void zero_units(const BackwardArgs& a, int c, int n) {
     const int f0 = x * kT + gc % (kT / kRows) * kRows;
     const int rows = min(kRows, (KV ? (a.fill ? a.Skv : u.Skv) : u.Sq) - f0);
     const size_t at = ((size_t)(KV ? u.kbase : u.qbase) + f0) * H * D;
-    const int w = H * (D / 8);
-    for (int i = threadIdx.x; i < rows * w; i += kPrepThreads) {
+    const long long w = (long long)H * (D / 8);
+    for (long long i = threadIdx.x; i < rows * w; i += kPrepThreads) {
       if (KV) {
         reinterpret_cast<uint4*>(a.dk + at)[i] = make_uint4(0, 0, 0, 0);
         reinterpret_cast<uint4*>(a.dv + at)[i] = make_uint4(0, 0, 0, 0);

@@ -235,6 +235,21 @@ def test_no_rows_no_keys():
 
 
 @pytest.mark.gpu
+def test_packed_rows_of_no_sequences_at_all():
+    torch.full((1 << 20,), 3.0, device="cuda")  # (what the outputs' memory may hold)
+    full = lambda *s: torch.full(s, 3.0, dtype=torch.bfloat16, device="cuda")
+    cu, kl = torch.zeros(1, dtype=torch.int32).cuda(), torch.zeros(0, dtype=torch.int32).cuda()
+    args = (full(5, 4, 64), full(5, 4, 64), full(0, 6, 2, 64), full(0, 6, 2, 64), full(5, 4, 64),
+            torch.zeros(4, 5, device="cuda"), cu, kl, 0)
+    out = attn.prefill_varlen_backward(*args)
+    assert (out[0] == 0).all() and out[1].shape == out[2].shape == (0, 6, 2, 64)
+    given = full(5, 4, 64), full(0, 6, 2, 64), full(0, 6, 2, 64)
+    attn.prefill_varlen_backward(*args, out=given)
+    assert (given[0] == 3).all()
+    attn.sync_check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d,window,sink", [(64, 0, 0), (128, 40, 2)])
 def test_against_differences(d, window, sink):
     """dL/dx . u against (L(x + h u) - L(x - h u)) / 2h of the fp64 forward, L = <o, do> + <lse, dlse>,

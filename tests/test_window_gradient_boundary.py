@@ -118,6 +118,10 @@ def test_workspace():
     for bad in ((-1, 4, 2, 70, 70, 90, 64), (1, 3, 2, 70, 70, 90, 64), (1, 4, 2, -1, 70, 90, 64), (1, 4, 2, 70, 70, 90, 256),
                 (1, 1 << 10, 1 << 10, 1 << 21, 1 << 21, 5, 64)):
         assert w(*bad) == 0
+    # eight sequences of 128k rows, one of a million; items of all heads past 2 * 10^9
+    assert w(8, 64, 8, 8 << 17, 1 << 17, 1 << 17, 128) > 0
+    assert w(1, 8, 1, 1 << 20, 1 << 20, 1 << 20, 128) > 0
+    assert w(1, 32, 8, 1 << 20, 1 << 20, 1 << 20, 128) == 0
     n = w(1, 4, 2, 70, 70, 90, 64)
     assert n > 0 and n % 256 == 0
     assert GRAD(B=1, Sq=70, Skv=90, work_bytes=n - 1) == INVALID
