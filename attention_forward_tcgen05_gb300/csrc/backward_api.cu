@@ -101,7 +101,7 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
     if (rc == ATTN_OK && tq != 128) rc = attn::encode_panel_map(&a.tm_vy, v, z.d, z.Hkv, z.Skv, z.B, tq);
     if (rc != ATTN_OK) return rc;
   }
-  a.q = q; a.dout = dout; a.k = k; a.v = v; a.o = o; a.lse = lse; a.dlse = dlse;
+  a.dout = dout; a.o = o; a.lse = lse; a.dlse = dlse;
   a.dq = dq; a.dk = dk; a.dv = dv;
   a.cu_q = cu_q; a.kv_lens = kv_lens;
   a.B = z.B; a.Hq = z.Hq; a.Hkv = z.Hkv; a.Sq = z.Sq; a.Skv = z.Skv; a.total_q = (int)z.rows; a.d = z.d;

@@ -229,7 +229,7 @@ struct BackwardArgs {
   // The streamed tiles of the dK/dV pass (Q, dout) and of the dQ pass (K, V): the same with the
   // rows of backward_tile_rows
   CUtensorMap tm_qy, tm_doy, tm_ky, tm_vy;
-  const uint16_t *q, *dout, *k, *v;
+  const uint16_t* dout;
   const void* o;
   const float *lse, *dlse;              // dlse may be nullptr
   uint16_t *dq, *dk, *dv;

@@ -460,8 +460,8 @@ struct Stream {
   }
 };
 
-// One CTA's slice of a pass: `cta` of `ctas`.
-template <int D, bool KV>
+// One CTA's slice of a pass: `cta` of `ctas`.  PK: a packed batch.
+template <int D, bool KV, bool PK>
 __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, int ctas) {
   using C = BwdCfg<D, KV>;
   constexpr int NS = C::NS, ND = C::ND, TN = C::TN;
@@ -547,7 +547,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     auto load_ext = [&] {
       if constexpr (KV) {
         if (ex.r.n > 0) {
-          const size_t i = a.cu_q ? (size_t)ex.y.h * a.total_q + ex.r.u.qbase + ex.y.row0
+          const size_t i = PK ? (size_t)ex.y.h * a.total_q + ex.r.u.qbase + ex.y.row0
                                   : ((size_t)ex.r.b * a.Hq + ex.y.h) * a.Sq + ex.y.row0;
           const uint4* src = (first ? a.ext1 : a.ext2) + i;
           const uint32_t dst = ext + ex.it % C::kExtSlots * C::kExt;
@@ -576,7 +576,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     bool ok = true;
     while (ok && run.n > 0) {
       if (!mbar_wait_warp(eF, ((uint32_t)n_run & 1u) ^ 1u, a.err, abort_flag)) break;
-      const bool packed = !KV && a.cu_q != nullptr;
+      constexpr bool packed = !KV && PK;
       mbar_arrive_expect_tx_e(fF, C::kFTile);
       tma_load_5d_e(sF, map, fF, 0, packed ? run.u.qbase + run.x * kT : run.x * kT, 0, run.h, packed ? 0 : run.b);
       const int n = run.n;
@@ -678,33 +678,9 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
         const Unit& u = t.r.u;
         const CUtensorMap* map = KV ? (k == 0 ? &a.tm_qy : &a.tm_doy) : (k == 0 ? &a.tm_ky : &a.tm_vy);
         uint8_t* dst = smem + (k == 0 ? C::kY1Off : C::kY2Off) + s * C::kYTile;
-        const int rows = KV ? u.Sq : u.Skv;  // Y rows of the sequence
-        const int row_base = KV ? u.qbase : u.kbase;
-        // a packed batch: other rows follow a sequence's own
-        const bool whole = a.cu_q == nullptr || t.y.row0 + TN <= rows;
-        if (!whole) {
-          // its last rows are gathered, so that the rows behind them arrive as zeros (a weight of
-          // zero times what lies there could be NaN)
-          const uint16_t* base = KV ? (k == 0 ? a.q : a.dout) : (k == 0 ? a.k : a.v);
-          int ri[TN / 32];
-#pragma unroll
-          for (int e = 0; e < TN / 32; ++e) {
-            const int r = t.y.row0 + e * 32 + lane;
-            ri[e] = r < rows ? row_base + r : -1;
-          }
-          paged_gather<D, TN / 32>(smem_u32(dst), C::kYPanel, base, KV ? a.Hq : a.Hkv, t.y.h, lane, ri);
-          cp_async_commit();
-          cp_async_wait<0>();
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (whole) {
-          mbar_arrive_expect_tx_e(&full[s], C::kYTile);
-          if (KV && a.cu_q) tma_load_5d_e(dst, map, &full[s], 0, row_base + t.y.row0, 0, t.y.h, 0);
-          else tma_load_5d_e(dst, map, &full[s], 0, t.y.row0, 0, t.y.h, t.r.b);
-        } else if (lane == 0) {
-          mbar_arrive(&full[s]);
-        }
+        mbar_arrive_expect_tx_e(&full[s], C::kYTile);
+        if (KV && PK) tma_load_5d_e(dst, map, &full[s], 0, u.qbase + t.y.row0, 0, t.y.h, 0);
+        else tma_load_5d_e(dst, map, &full[s], 0, t.y.row0, 0, t.y.h, t.r.b);
         t.step(a);
       }
       if (moved) {
@@ -742,7 +718,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     auto row_stat = [&](const Run& q) {
       float2 v = make_float2(INFINITY, 0.f);
       if (!KV && q.n > 0 && q.x * kT + r < q.u.Sq) {
-        const size_t i = a.cu_q ? (size_t)q.h * a.total_q + q.u.qbase + q.x * kT + r
+        const size_t i = PK ? (size_t)q.h * a.total_q + q.u.qbase + q.x * kT + r
                                 : ((size_t)q.b * a.Hq + q.h) * a.Sq + q.x * kT + r;
         v = a.stat[i];
       }
@@ -860,6 +836,23 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
           }
           if constexpr (KV) tmem_st16(pc + q * 16, tp);
           tmem_st16(pc + (KV ? 32 : 0) + q * 16, t);
+        }
+        if (PK && mask) {
+          // rows of other sequences, or of none, behind this one's last: zeros for the second products, as
+          // a weight of zero times what lies there could be NaN (the first ones have read the tile; gathered
+          // instead of copied, such tiles held up the rings: eight packed sequences 249 us, so 231)
+          const int from = max(0, (KV ? u.Sq : u.Skv) - row0);
+          uint8_t* y1 = smem + C::kY1Off + it % C::kSt1 * C::kYTile;
+          uint8_t* y2 = smem + C::kY2Off + it % C::kSt2 * C::kYTile;
+#pragma unroll 1
+          for (int i = from * 8 + (TN == 128 ? (int)threadIdx.x : r); i < TN * 8; i += TN == 128 ? 256 : 128) {
+#pragma unroll
+            for (int c = 0; c < C::kPanels; ++c) {
+              *reinterpret_cast<uint4*>(y1 + c * C::kYPanel + i * 16) = make_uint4(0, 0, 0, 0);
+              if (KV) *reinterpret_cast<uint4*>(y2 + c * C::kYPanel + i * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
         }
         tmem_wait_st();
         tc_fence_before();
@@ -997,11 +990,11 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
 }
 
 // Both passes: dQ's CTAs start as dK/dV's end.
-template <int D>
+template <int D, bool PK>
 __global__ void __launch_bounds__(BwdCfg<D, true>::kThreads, 1)
     backward_kernel(const __grid_constant__ BackwardArgs a) {
-  if ((int)blockIdx.x < a.ctas_k) backward_pass<D, true>(a, (int)blockIdx.x, a.ctas_k);
-  else backward_pass<D, false>(a, (int)blockIdx.x - a.ctas_k, a.ctas_q);
+  if ((int)blockIdx.x < a.ctas_k) backward_pass<D, true, PK>(a, (int)blockIdx.x, a.ctas_k);
+  else backward_pass<D, false, PK>(a, (int)blockIdx.x - a.ctas_k, a.ctas_q);
 }
 
 template <int D>
@@ -1014,9 +1007,10 @@ cudaError_t launch_d(const BackwardArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (!any || e != cudaSuccess) return e;
   constexpr int kSmem = std::max(BwdCfg<D, true>::kSmem, BwdCfg<D, false>::kSmem);
-  e = cudaFuncSetAttribute(backward_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  auto kern = a.cu_q ? backward_kernel<D, true> : backward_kernel<D, false>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  backward_kernel<D><<<a.ctas_k + a.ctas_q, BwdCfg<D, true>::kThreads, kSmem, stream>>>(a);
+  kern<<<a.ctas_k + a.ctas_q, BwdCfg<D, true>::kThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
