@@ -248,8 +248,10 @@ __device__ void zero_units(const BackwardArgs& a, int c, int n) {
 }
 constexpr int kZeroCtas = 304;
 
-// D / 8 lanes to a (row, head), kPrepRows of them in flight, in memory order of o: [rows][Hq][D].
+// D / 8 lanes to a row of a head, kPrepRows consecutive rows of it in flight: a row is 128 or 256 bytes, so
+// that nothing is lost by reading a head's rows and what is written, by head, lies side by side.
 constexpr int kPrepRows = 4;
+constexpr int prep_rows(int d) { return kPrepThreads / (d / 8) * kPrepRows; }  // of a CTA
 template <int D, bool OBF16>
 __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __grid_constant__ BackwardArgs a) {
   if (blockIdx.x < 2) {
@@ -258,25 +260,25 @@ __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __gri
     for (int i = threadIdx.x; i < kMaxCtas; i += kPrepThreads) a.joined[blockIdx.x * kMaxCtas + i] = 0;
     return;
   }
-  const int n_rows = (int)gridDim.x - 2 - kZeroCtas;  // CTAs of the rows' sums
-  if ((int)blockIdx.x - 2 >= n_rows) {
-    zero_units<D, true>(a, (int)blockIdx.x - 2 - n_rows, kZeroCtas);
-    zero_units<D, false>(a, (int)blockIdx.x - 2 - n_rows, kZeroCtas);
+  if (blockIdx.x < 2 + kZeroCtas) {
+    zero_units<D, true>(a, (int)blockIdx.x - 2, kZeroCtas);
+    zero_units<D, false>(a, (int)blockIdx.x - 2, kZeroCtas);
     return;
   }
-  constexpr int L = D / 8, kPer = kPrepThreads / L;
-  const long long n = (long long)a.total_q * a.Hq;
-  const long long at0 = (long long)(blockIdx.x - 2) * kPer * kPrepRows + threadIdx.x / L;
+  constexpr int L = D / 8;
+  const int h = ((int)blockIdx.x - 2 - kZeroCtas) % a.Hq;
+  const int row0 = ((int)blockIdx.x - 2 - kZeroCtas) / a.Hq * prep_rows(D) + (int)threadIdx.x / L * kPrepRows;
   const int c = threadIdx.x % L;
   float s[kPrepRows];
 #pragma unroll
   for (int k = 0; k < kPrepRows; ++k) {
-    const long long rh = min(at0 + k * kPer, n - 1);  // (every lane takes part in the sums)
-    const uint4 g = __ldg(reinterpret_cast<const uint4*>(a.dout + rh * D + c * 8));
+    // (every lane takes part in the sums)
+    const size_t at = ((size_t)min(row0 + k, a.total_q - 1) * a.Hq + h) * D + c * 8;
+    const uint4 g = __ldg(reinterpret_cast<const uint4*>(a.dout + at));
     if constexpr (OBF16) {
-      s[k] = dot8(g, __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.o) + rh * D + c * 8)));
+      s[k] = dot8(g, __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.o) + at)));
     } else {
-      const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.o) + rh * D + c * 8);
+      const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.o) + at);
       s[k] = dot8(g, __ldg(p), __ldg(p + 1));
     }
   }
@@ -289,9 +291,8 @@ __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __gri
   float D_i = s[0];
 #pragma unroll
   for (int k = 1; k < kPrepRows; ++k) D_i = c == k ? s[k] : D_i;
-  const long long rh = at0 + c * kPer;
-  if (c >= kPrepRows || rh >= n) return;
-  const int row = (int)(rh / a.Hq), h = (int)(rh % a.Hq);
+  const int row = row0 + c;
+  if (c >= kPrepRows || row >= a.total_q) return;
   // [B][Hq][Sq], or packed [Hq][total_q]
   const size_t i = a.cu_q ? (size_t)h * a.total_q + row
                           : ((size_t)(row / a.Sq) * a.Hq + h) * a.Sq + row % a.Sq;
@@ -1000,8 +1001,8 @@ __global__ void __launch_bounds__(BwdCfg<D, true>::kThreads, 1)
 template <int D>
 cudaError_t launch_d(const BackwardArgs& a, cudaStream_t stream) {
   const bool any = a.total_q > 0 && a.Sq > 0 && a.Skv > 0;  // else the gradients are zeros
-  const long long threads = any ? (long long)a.total_q * a.Hq * (D / 8) : 0;
-  const unsigned grid = 2 + kZeroCtas + (unsigned)((threads + kPrepThreads * kPrepRows - 1) / (kPrepThreads * kPrepRows));
+  const long long blocks = any ? (a.total_q + prep_rows(D) - 1LL) / prep_rows(D) * a.Hq : 0;
+  const unsigned grid = 2 + kZeroCtas + (unsigned)blocks;
   if (a.o_bf16) backward_prep_kernel<D, true><<<grid, kPrepThreads, 0, stream>>>(a);
   else backward_prep_kernel<D, false><<<grid, kPrepThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
