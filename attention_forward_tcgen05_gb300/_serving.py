@@ -391,17 +391,27 @@ def rope_append(q, k, v, kcache, vcache, kv_lens, inv_freq, page_table=None, cu_
 
 def _rotated(t, name, out, dev, total):
     """(pointer, stride, out, its pointer, its stride, heads, head dim) of a side of
-    rope_rotate."""
+    rope_rotate (the checks of _token_rows, made once)."""
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+    try:
+        good = t.get_device() == dev and t.dtype is torch.bfloat16 and t.dim() == 3
+    except AttributeError:
+        good = False
+    if not good:
         _refuse(t, name, torch.bfloat16, 3, dev, contiguous=False)
     n, H, d = t.shape
-    p, s = _token_rows(t, name, torch.bfloat16, dev, total, H, d)
+    s, head, one = t.stride()
+    if n != total:
+        raise ValueError(f"{name} must have {total} rows, got {n}")
+    if one != 1 or (H > 1 and head != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if n <= 1:
+        s = H * d
     if out is None:
         out = torch.empty_like(t, memory_format=torch.contiguous_format)
-        return p, s, out, out.data_ptr(), H * d, H, d
+        return t.data_ptr(), s, out, out.data_ptr(), H * d, H, d
     op, os = _token_rows(out, f"out of {name}", torch.bfloat16, dev, total, H, d)
-    return p, s, out, op, os, H, d
+    return t.data_ptr(), s, out, op, os, H, d
 
 
 def rope_rotate(q, k, inv_freq, positions, axes=None, interleaved: bool = False, amp: float = 1.0,

@@ -56,14 +56,12 @@ __device__ __forceinline__ void rotate_inter(uint4& a, const float2* cs) {
   }
 }
 
-// frequencies as fractions of a turn, units of 2^-64 turns
-__device__ __forceinline__ void load_turns(unsigned long long* turn, const double* inv_freq, int half) {
-  for (int i = threadIdx.x; i < half; i += kThreads) {
-    const double x = inv_freq[i] * 0.15915494309189535, y = fabs(x);  // 1 / (2 pi)
-    // the fraction of |x|, which is exact (that of a small negative x would be rounded to 2^-54)
-    const unsigned long long f = (unsigned long long)((y - floor(y)) * 18446744073709551616.0);
-    turn[i] = x < 0 ? 0ull - f : f;
-  }
+// a frequency as a fraction of a turn, units of 2^-64 turns
+__device__ __forceinline__ unsigned long long turn_of(double inv_freq) {
+  const double x = inv_freq * 0.15915494309189535, y = fabs(x);  // 1 / (2 pi)
+  // the fraction of |x|, which is exact (that of a small negative x would be rounded to 2^-54)
+  const unsigned long long f = (unsigned long long)((y - floor(y)) * 18446744073709551616.0);
+  return x < 0 ? 0ull - f : f;
 }
 // (cos, sin) * amp of a position times a frequency
 __device__ __forceinline__ float2 angle_at(unsigned long long turn, int pos, float amp) {
@@ -73,15 +71,33 @@ __device__ __forceinline__ float2 angle_at(unsigned long long turn, int pos, flo
   sincospif(x, &sn, &c);
   return make_float2(c * amp, sn * amp);
 }
-// the axis of each pair (one that is none is reported and becomes the first)
-__device__ __forceinline__ void load_axes(uint8_t* axis, const int* axes, int n_axes, int half, uint32_t* err) {
-  for (int i = threadIdx.x; i < half; i += kThreads) {
-    int x = axes[i];
-    if ((unsigned)x >= (unsigned)n_axes) {
-      atomicCAS(err, kErrNone, kErrBadShape);
-      x = 0;
+// The frequencies, and with AXES the pairs' axes (one that is none is reported and becomes the first) and
+// the positions, to shared memory: a thread has at most one of each, and asks for all before it uses any
+// (one loop after the other, each with its own wait: an append of 64 tokens 3.6 us, so 3.05).
+template <int kTokens, bool AXES>
+__device__ __forceinline__ void load_tables(unsigned long long* turn, uint8_t* axis, int* at, const double* inv_freq,
+                                            const int* axes, const int* positions, int n_axes, int half, int total,
+                                            int t0, int nt, uint32_t* err) {
+  static_assert(kMaxRopeAxes * kTokens <= kThreads);
+  const int i = threadIdx.x, s = i % kTokens;
+  const bool has_pos = AXES && i < n_axes * kTokens && s < nt;
+  double f = 0;
+  int x = 0, p = 0;
+  if (i < half) {
+    f = inv_freq[i];
+    if (AXES && axes) x = axes[i];
+  }
+  if (has_pos) p = positions[(size_t)(i / kTokens) * total + t0 + s];
+  if (has_pos) at[i] = p;
+  if (i < half) {
+    turn[i] = turn_of(f);
+    if (AXES) {
+      if ((unsigned)x >= (unsigned)n_axes) {
+        atomicCAS(err, kErrNone, kErrBadShape);
+        x = 0;
+      }
+      axis[i] = (uint8_t)x;
     }
-    axis[i] = (uint8_t)x;
   }
 }
 
@@ -97,14 +113,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
   __shared__ int at[(AXES ? kMaxRopeAxes : 1) * kTokens];  // [axis][token] position
   __shared__ uint8_t axis[AXES ? 128 : 1];
   const int half = a.rot / 2, t0 = blockIdx.x * kTokens, nt = min(kTokens, a.total - t0);
-  load_turns(turn, a.inv_freq, half);
-  if constexpr (AXES) {
-    load_axes(axis, a.axes, a.n_axes, half, a.err);
-    for (int i = threadIdx.x; i < a.n_axes * kTokens; i += kThreads) {
-      const int s = i % kTokens;
-      if (s < nt) at[i] = a.positions[(size_t)(i / kTokens) * a.total + t0 + s];
-    }
-  }
+  load_tables<kTokens, AXES>(turn, axis, at, a.inv_freq, a.axes, a.positions, a.n_axes, half, a.total, t0, nt, a.err);
   if ((int)threadIdx.x >= kThreads - nt) {
     // (the last threads, whose warp has no frequency to convert up to d = 256)
     const int s = kThreads - 1 - (int)threadIdx.x, t = t0 + s;
@@ -182,49 +191,66 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
 // The same without a cache: q and k rows to rows of their own (or themselves: each chunk is read and
 // written by one thread), items as above.
 template <bool INTER, int kTokens>
-__global__ void __launch_bounds__(kThreads) rope_rotate_kernel(const RotateArgs a) {
+__global__ void __launch_bounds__(kThreads, kTokens == 8 ? 6 : 1) rope_rotate_kernel(const RotateArgs a) {
   __shared__ unsigned long long turn[128];
   __shared__ float2 cs[kTokens * 128];
   __shared__ int at[kMaxRopeAxes * kTokens];
   __shared__ uint8_t axis[128];
   const int half = a.rot / 2, t0 = blockIdx.x * kTokens, nt = min(kTokens, a.total - t0);
-  load_turns(turn, a.inv_freq, half);
-  if (a.axes) load_axes(axis, a.axes, a.n_axes, half, a.err);
-  for (int i = threadIdx.x; i < a.n_axes * kTokens; i += kThreads) {
-    const int s = i % kTokens;
-    if (s < nt) at[i] = a.positions[(size_t)(i / kTokens) * a.total + t0 + s];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int s = kTokens == 1 ? 0 : i / half, m = i - s * half;
-    float2 c = angle_at(turn[m], at[(a.axes ? axis[m] : 0) * kTokens + s], a.amp);
-    if (a.inverse) c.y = -c.y;
-    cs[s * 128 + m] = c;
-  }
-  __syncthreads();
-  const int rc = a.rot / 8, ipr = a.d / 16, items = (a.Hq + a.Hk) * ipr;
-#pragma unroll 2
-  for (int it = threadIdx.x; it < nt * items; it += kThreads) {
-    const int s = kTokens == 1 ? 0 : it / items, in = it - s * items;
-    const size_t t = (size_t)(t0 + s);
-    const int h = in / ipr, x = in - h * ipr;
+  const int rc = a.rot / 8, ipr = a.d / 16, items = (a.Hq + a.Hk) * ipr, n = nt * items;
+  struct Item {
+    uint4 u0, u1;
+    uint16_t *d0, *d1;
+    int c0, c1, s, x;
+  };
+  auto fetch = [&](int it) {
+    Item y;
+    y.s = kTokens == 1 ? 0 : it / items;
+    const int in = it - y.s * items, h = in / ipr;
+    y.x = in - h * ipr;
+    const size_t t = (size_t)(t0 + y.s);
     const bool is_q = h < a.Hq;
     const size_t head = (size_t)(is_q ? h : h - a.Hq) * a.d;
     const uint16_t* src = (is_q ? a.q + t * a.q_stride : a.k + t * a.k_stride) + head;
     uint16_t* dst = (is_q ? a.q_out + t * a.qo_stride : a.k_out + t * a.ko_stride) + head;
-    int c0, c1;
-    if (!INTER && x < rc / 2) { c0 = x; c1 = x + rc / 2; }
-    else { c0 = 2 * x; c1 = 2 * x + 1; }
-    uint4 u0 = *reinterpret_cast<const uint4*>(src + c0 * 8), u1 = *reinterpret_cast<const uint4*>(src + c1 * 8);
-    const float2* c = cs + s * 128;
+    if (!INTER && y.x < rc / 2) { y.c0 = y.x; y.c1 = y.x + rc / 2; }
+    else { y.c0 = 2 * y.x; y.c1 = 2 * y.x + 1; }
+    y.u0 = *reinterpret_cast<const uint4*>(src + y.c0 * 8);
+    y.u1 = *reinterpret_cast<const uint4*>(src + y.c1 * 8);
+    y.d0 = dst + y.c0 * 8;
+    y.d1 = dst + y.c1 * 8;
+    return y;
+  };
+  auto finish = [&](Item& y) {
+    const float2* c = cs + y.s * 128;
     if (INTER) {
-      if (c0 < rc) rotate_inter(u0, c + c0 * 4);
-      if (c1 < rc) rotate_inter(u1, c + c1 * 4);
-    } else if (x < rc / 2) {
-      rotate_half(u0, u1, c + c0 * 8);
+      if (y.c0 < rc) rotate_inter(y.u0, c + y.c0 * 4);
+      if (y.c1 < rc) rotate_inter(y.u1, c + y.c1 * 4);
+    } else if (y.x < rc / 2) {
+      rotate_half(y.u0, y.u1, c + y.c0 * 8);
     }
-    *reinterpret_cast<uint4*>(dst + c0 * 8) = u0;
-    *reinterpret_cast<uint4*>(dst + c1 * 8) = u1;
+    *reinterpret_cast<uint4*>(y.d0) = y.u0;
+    *reinterpret_cast<uint4*>(y.d1) = y.u1;
+  };
+  // (a thread's first item is on its way while the angles are found: 8192 tokens of 32 heads of 64 17.0 us
+  // without this and load_tables, so 15.2; six CTAs an SM: 32768 tokens of 32 heads of 128 87.5 us, five 90.8)
+  Item y;
+  const bool any = (int)threadIdx.x < n;
+  if (any) y = fetch(threadIdx.x);
+  load_tables<kTokens, true>(turn, axis, at, a.inv_freq, a.axes, a.positions, a.n_axes, half, a.total, t0, nt, a.err);
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+    const int s = kTokens == 1 ? 0 : i / half, m = i - s * half;
+    float2 c = angle_at(turn[m], at[axis[m] * kTokens + s], a.amp);
+    if (a.inverse) c.y = -c.y;
+    cs[s * 128 + m] = c;
+  }
+  __syncthreads();
+  if (any) finish(y);
+#pragma unroll 2
+  for (int it = threadIdx.x + kThreads; it < n; it += kThreads) {
+    Item z = fetch(it);
+    finish(z);
   }
 }
 
