@@ -49,8 +49,8 @@ constexpr int kMaxCtas = kBackwardCtas;
 // A run of a unit's items costs its start and end (the F tiles' copy, the sums' way out, the sum of a
 // cut unit's parts) beside its items: units of few items would otherwise fill some slices with
 // nothing but starts and ends.  In rows of Y: 640 in the dK/dV pass, 128 in the dQ pass (of 64 to
-// 768 and 128 to 384; 3314 rows, window 1024: 183 us, 192 with 192 and 384; eight packed sequences:
-// 283 and 303).
+// 768 and 128 to 384; 3314 rows without a window: 227 us, 235 with 192 and 384; eight packed sequences:
+// 224 and 229).
 constexpr int run_cost(bool kv, int ty) { return (kv ? 640 : 128) / ty; }
 constexpr int kMinCost = 8;  // of a slice
 
@@ -62,7 +62,7 @@ constexpr int kMinCost = 8;  // of a slice
 //     one S, one dP and two of P and dS, so that the next S waits for the softmax's load only.  A
 //     product of 64 columns re-reads as much of F for half of the work (49 cycles a step, bound by
 //     shared memory, against 65 for 128 columns); elsewhere items of 64 were slower (d = 64, 2 x 16
-//     heads of 4096, not causal: 552 us, with three warpgroups of softmax 623, against 436).
+//     heads of 4096, not causal: 494 us in the dK/dV pass alone so, against 434).
 template <int D, bool KV>
 struct BwdCfg {
   static constexpr int TN = (D == 128 && KV) ? 64 : 128;
@@ -787,16 +787,20 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_Sr[bs]);  // (the next S need not wait for this dP)
-        // the exponentials before dP is waited for (under its product; in one loop with dS: 174 and 239 us for
-        // 3314 rows with and without a window, so: 169 and 234)
+        // At d = 128 the exponentials before dP is waited for, under its product (after it: 172 and 233 us for
+        // 3314 rows with and without a window, so 167 and 227); at d = 64, whose products are short, after
+        // it, beside the rest of the chain's instructions (2 x 16 heads of 4096, not causal: 427 us, before it 434).
+        auto exponentials = [&] {
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const uint64_t x = f2pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          float e0, e1;
-          f2unpack(KV ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
-          s[c] = __float_as_uint(ex2_approx(e0));
-          s[c + 1] = __float_as_uint(ex2_approx(e1));
-        }
+          for (int c = 0; c < 64; c += 2) {
+            const uint64_t x = f2pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            float e0, e1;
+            f2unpack(KV ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
+            s[c] = __float_as_uint(ex2_approx(e0));
+            s[c + 1] = __float_as_uint(ex2_approx(e1));
+          }
+        };
+        if constexpr (D == 128) exponentials();
         ok = mbar_wait_warp(&bar_dP[bp], (uint32_t)(it >> 1) & 1u, a.err, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -808,6 +812,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_dPr[bd]);
         }
+        if constexpr (D == 64) exponentials();
         if constexpr (C::kSep) {
           ok = mbar_wait_warp(&bar_Pr[bp], ((uint32_t)(it >> 1) & 1u) ^ 1u, a.err, abort_flag);
           if (!ok) break;
