@@ -1,7 +1,8 @@
-"""GB300 (sm_103a) attention-forward engine: exact SDPA with online softmax.
+"""GB300 (sm_103a) attention engine: exact SDPA with online softmax, and its gradients.
 
 Prefill FMHA on tcgen05 tensor cores (TMA-fed, TMEM accumulators) and a GQA
-split-KV decode with an LSE-weighted merge, behind the C ABI of
+split-KV decode with an LSE-weighted merge, serving calls over a paged cache and the
+gradients of the dense prefill, behind the C ABI of
 ``include/attn.h``.  ``libattn.so`` is built in-tree by ``build.build()``.
 """
 from ._binding import (  # noqa: F401

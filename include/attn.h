@@ -1,11 +1,12 @@
 /*
- * attn.h -- C ABI of the GB300 (sm_103a) attention-forward engine.
+ * attn.h -- C ABI of the GB300 (sm_103a) attention engine.
  *
  * Exact scaled-dot-product attention with online softmax,
  *     O = softmax(scale * Q K^T + causal mask) V,   LSE_i = ln sum_j exp(scale * q_i . k_j),
  * in two shapes: a prefill FMHA (tcgen05 tensor cores, TMEM accumulators, TMA
  * loads) and a GQA split-KV decode (per-split partials, then an LSE-weighted
- * merge) on CUDA cores.
+ * merge) on CUDA cores; then the serving calls over a paged cache, and the gradients of the dense
+ * prefill.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
