@@ -6,10 +6,11 @@ stream.
 """
 from __future__ import annotations
 
+import functools
 import math
 
-from ._binding import ATTN_OK, AttnError, load
-from ._serving import _device, _elsewhere, _need, _out_code, _sized, _torch
+from ._binding import ATTN_OK, AttnError, _launching, load
+from ._serving import _device, _elsewhere, _need, _out_code, _sized, _torch, _workspace
 
 
 # ------------------------------------------------------------------ raw C ABI
@@ -26,10 +27,21 @@ def attn_prefill_backward_workspace(B, Hq, Hkv, total_q, max_sq, max_kv, d) -> i
 
 
 # ------------------------------------------------------------------ torch helpers
-def _work(n):
-    """A workspace of n bytes, the call's own: it goes back to the stream's allocations."""
-    torch = _torch()
-    t = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+_KEPT = 64 << 20  # bytes; a larger call takes far longer than an allocation
+
+
+@functools.lru_cache(maxsize=1024)
+def _work_bytes(*sizes):
+    return attn_prefill_backward_workspace(*sizes)
+
+
+def _work(n, dev, handle):
+    """A workspace of n bytes and its pointer: the stream's kept one, or a large call's own, which
+    goes back to the stream's allocations."""
+    if n <= _KEPT:
+        t = _workspace((n + 3) // 4, dev, handle)
+    else:
+        t = _torch().empty(n, dtype=_torch().uint8, device="cuda")
     return t, t.data_ptr()
 
 
@@ -37,8 +49,8 @@ def _gradients(out, q, k, v, dev):
     """(tensors, pointers) of dq, dk, dv."""
     torch = _torch()
     if out is None:
-        out = tuple(torch.empty_like(t) for t in (q, k, v))
-        return out, [t.data_ptr() for t in out]
+        out = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        return out, (out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr())
     if len(out) != 3:
         raise ValueError("out must be (dq, dk, dv)")
     return tuple(out), [_sized(t, f"out[{i}]", torch.bfloat16, dev, *like.shape)
@@ -83,10 +95,11 @@ def prefill_backward(do, q, k, v, o, lse, causal: bool = True, window: int = 0, 
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     out, (dq, dk, dv) = _gradients(out, q, k, v, dev)
-    n = attn_prefill_backward_workspace(B, Hq, Hkv, B * Sq, Sq, Skv, d)
-    work, wp = _work(n)
-    rc = load().attn_prefill_backward(gp, qp, kp, vp, op, lp, dp, dq, dk, dv, B, Hq, Hkv, Sq, Skv, d, int(causal),
-                                      int(window), int(n_sink), scale, code, wp, n, handle)
+    n = _work_bytes(B, Hq, Hkv, B * Sq, Sq, Skv, d)
+    work, wp = _work(n, dev, handle)
+    with _launching:
+        rc = load().attn_prefill_backward(gp, qp, kp, vp, op, lp, dp, dq, dk, dv, B, Hq, Hkv, Sq, Skv, d, int(causal),
+                                          int(window), int(n_sink), scale, code, wp, n, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_prefill_backward")
     return out
@@ -125,11 +138,12 @@ def prefill_varlen_backward(do, q, kcache, vcache, o, lse, cu_seqlens_q, kv_lens
     out, (dq, dk, dv) = _gradients(out, q, kcache, vcache, dev)
     if fill and B == 0:
         out[0].zero_()  # (a call of no sequences writes nothing)
-    n = attn_prefill_backward_workspace(B, Hq, Hkv, total, max_sq, max_kv, d)
-    work, wp = _work(n)
-    rc = load().attn_prefill_varlen_backward(gp, qp, kp, vp, op, lp, dp, dq, dk, dv, cu, np_, B, Hq, Hkv, total, max_sq,
-                                             max_kv, d, int(causal), int(window), int(n_sink), scale, code, fill, wp,
-                                             n, handle)
+    n = _work_bytes(B, Hq, Hkv, total, max_sq, max_kv, d)
+    work, wp = _work(n, dev, handle)
+    with _launching:
+        rc = load().attn_prefill_varlen_backward(gp, qp, kp, vp, op, lp, dp, dq, dk, dv, cu, np_, B, Hq, Hkv, total,
+                                                 max_sq, max_kv, d, int(causal), int(window), int(n_sink), scale, code,
+                                                 fill, wp, n, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_prefill_varlen_backward")
     return out

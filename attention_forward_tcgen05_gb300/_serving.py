@@ -201,7 +201,7 @@ def _window_splits(B, Hq, Hkv, max_kv, window, n_sink, d):
     return max(n, 1), rows.value
 
 
-# Workspaces of prefill_paged, decode_paged and decode_window: kept for each stream, whose launches are
+# Workspaces of prefill_paged, decode_paged, decode_window and the gradients: kept for each stream, whose launches are
 # ordered; a call holds _launching while it makes its launches, so that another thread's on the
 # same stream do not come between two of them.  A call being captured gets its own (two graphs
 # may replay at the same time).  They grow to the largest call seen and stay for the process.

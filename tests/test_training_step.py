@@ -1,6 +1,7 @@
 """The rotations, the windowed attention and their gradients together, as a training step makes
 them, and a windowed serving loop over pages whose far pages are given back."""
 import math
+import threading
 
 import pytest
 import torch
@@ -95,6 +96,35 @@ def test_training_step_in_a_graph_and_on_two_streams():
         assert all(torch.equal(g, e) for g, e in zip(got, w))
         assert all(torch.equal(g, e) for g, e in zip(other, want[1]))
     attn.sync_check()
+
+
+def test_threads_on_one_stream():
+    """Calls of several threads on the same stream share its kept workspace and keep their results, small
+    calls beside ones whose workspace is larger."""
+    g = torch.Generator().manual_seed(8)
+    sets = []
+    for i, (S, H, d) in enumerate(((40, 4, 64), (700, 8, 128), (333, 2, 64), (1500, 4, 128))):
+        q, do = ((torch.randn(1, S, H, d, generator=g)).bfloat16().cuda() for _ in range(2))
+        k, v = ((torch.randn(1, S, 2, d, generator=g)).bfloat16().cuda() for _ in range(2))
+        o, lse = attn.prefill(q, k, v)
+        sets.append((do, q, k, v, o, lse))
+    want = [attn.prefill_backward(*x) for x in sets]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        for _ in range(25):
+            got = attn.prefill_backward(*sets[i])
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    attn.sync_check()
+    assert not bad
 
 
 def test_a_stream_given():
