@@ -282,8 +282,8 @@ int attn_rope_rotate(const attn_bf16_t* q, const attn_bf16_t* k, long long q_str
     if (x.in == x.out && x.stride != x.out_stride) return ATTN_ERR_INVALID_ARG;
   }
   if (!ok4(positions) || !aligned(axes, 4) || inv_freq == nullptr || !aligned(inv_freq, 8)) return ATTN_ERR_INVALID_ARG;
-  // (eight tokens' chunks are counted in 32 bits)
-  if ((Hq + (long long)Hk) * (d / 16) > 0x7FFFFFFFLL / 8) return ATTN_ERR_INVALID_ARG;
+  // (eight tokens' chunks, and a CTA's threads beyond them, are counted in 32 bits)
+  if ((Hq + (long long)Hk) * (d / 16) > (1LL << 27)) return ATTN_ERR_INVALID_ARG;
   attn::RotateArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out;

@@ -471,7 +471,7 @@ int attn_rope_append_axes(const attn_bf16_t* q, const attn_bf16_t* k, const attn
  *   positions    int32 [n_axes][total] (device, may be negative)
  *   axes         int32 [rot_dim/2] as in attn_rope_append_axes, or NULL (n_axes = 1)
  *   inv_freq     fp64 [rot_dim/2] (device), radians per position
- *   d            16, 32, .. 256;  rot_dim 16, 32, .. d;  amp finite
+ *   d            16, 32, .. 256;  rot_dim 16, 32, .. d;  amp finite;  (Hq + Hk) * d at most 2^31
  * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
  */
 int attn_rope_rotate(const attn_bf16_t* q, const attn_bf16_t* k, long long q_stride, long long k_stride,

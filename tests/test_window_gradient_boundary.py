@@ -89,6 +89,7 @@ def test_rope_rotate():
     assert ROTATE(Hq=0, Hk=0) == INVALID
     assert ROTATE(qo=P, qs=264) == INVALID  # in place at another stride
     assert ROTATE(Hq=1 << 30, qs=1 << 36, qos=1 << 36) == INVALID
+    assert ROTATE(Hq=(1 << 25) - 1, qs=1 << 32, qos=1 << 32) == INVALID  # two heads of k beside them
     assert ROTATE(total=0, q=N, k=N, positions=N, axes=N, n_axes=1) == OK
 
 
