@@ -81,6 +81,15 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   if (rows && (!ok16(dout) || !ok16(q) || !ok16(o) || !ok4(lse) || !aligned(dlse, 4) || !ok16(dq)))
     return ATTN_ERR_INVALID_ARG;
   if (keys && (!ok16(k) || !ok16(v) || !ok16(dk) || !ok16(dv))) return ATTN_ERR_INVALID_ARG;
+  // one pass's gradients are written while the other still reads
+  const void* outs[3] = {rows ? dq : nullptr, keys ? dk : nullptr, keys ? dv : nullptr};
+  const void* ins[5] = {rows ? dout : nullptr, rows ? q : nullptr, rows ? o : nullptr, keys ? k : nullptr,
+                        keys ? v : nullptr};
+  for (int i = 0; i < 3; ++i) {
+    for (const void* p : ins)
+      if (outs[i] && outs[i] == p) return ATTN_ERR_INVALID_ARG;
+    if (outs[i] && outs[i] == outs[(i + 1) % 3]) return ATTN_ERR_INVALID_ARG;
+  }
   const Layout l = layout_of(z);
   if (!work || !aligned(work, 256) || work_bytes < l.bytes) return ATTN_ERR_INVALID_ARG;
   attn::BackwardArgs a;

@@ -281,6 +281,8 @@ int attn_rope_rotate(const attn_bf16_t* q, const attn_bf16_t* k, long long q_str
     // in place only over itself
     if (x.in == x.out && x.stride != x.out_stride) return ATTN_ERR_INVALID_ARG;
   }
+  // (a shared output, or one over the other's input, would be turned twice)
+  if (Hq > 0 && Hk > 0 && (q_out == k_out || q_out == k || k_out == q)) return ATTN_ERR_INVALID_ARG;
   if (!ok4(positions) || !aligned(axes, 4) || inv_freq == nullptr || !aligned(inv_freq, 8)) return ATTN_ERR_INVALID_ARG;
   // (eight tokens' chunks, and a CTA's threads beyond them, are counted in 32 bits)
   if ((Hq + (long long)Hk) * (d / 16) > (1LL << 27)) return ATTN_ERR_INVALID_ARG;

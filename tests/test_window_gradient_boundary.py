@@ -30,11 +30,13 @@ DECODE = Call(attn.attn_decode_window, q=P, kc=P, vc=P, table=P, lens=P, B=2, Hq
 APPEND = Call(attn.attn_rope_append_axes, q=P, k=P, v=P, qs=256, ks=128, vs=128, positions=P, axes=P, n_axes=3,
               inv_freq=P, q_out=P, kc=P, vc=P, table=P, cu=P, lens=P, B=2, Hq=4, Hkv=2, total=7, d=64, rot=64, inter=0,
               amp=1.0, max_pages=4, page=16, pages=9, stream=N)
-ROTATE = Call(attn.attn_rope_rotate, q=P, k=P, qs=256, ks=128, positions=P, axes=P, n_axes=3, inv_freq=P, qo=2 * P,
-              ko=2 * P, qos=256, kos=128, Hq=4, Hk=2, total=7, d=64, rot=64, inter=0, inverse=0, amp=1.0, stream=N)
-GRAD = Call(attn.attn_prefill_backward, do=P, q=P, k=P, v=P, o=P, lse=P, dlse=N, dq=P, dk=P, dv=P, B=2, Hq=4, Hkv=2,
+ROTATE = Call(attn.attn_rope_rotate, q=P, k=5 * P, qs=256, ks=128, positions=P, axes=P, n_axes=3, inv_freq=P, qo=2 * P,
+              ko=3 * P, qos=256, kos=128, Hq=4, Hk=2, total=7, d=64, rot=64, inter=0, inverse=0, amp=1.0, stream=N)
+GRAD = Call(attn.attn_prefill_backward, do=P, q=2 * P, k=3 * P, v=4 * P, o=5 * P, lse=6 * P, dlse=N, dq=7 * P,
+            dk=8 * P, dv=9 * P, B=2, Hq=4, Hkv=2,
             Sq=70, Skv=90, d=64, causal=1, window=0, sink=0, scale=0.5, o_dtype=1, work=P, work_bytes=BIG, stream=N)
-VARLEN = Call(attn.attn_prefill_varlen_backward, do=P, q=P, k=P, v=P, o=P, lse=P, dlse=N, dq=P, dk=P, dv=P, cu=P,
+VARLEN = Call(attn.attn_prefill_varlen_backward, do=P, q=2 * P, k=3 * P, v=4 * P, o=5 * P, lse=6 * P, dlse=N, dq=7 * P,
+              dk=8 * P, dv=9 * P, cu=P,
               lens=P, B=2, Hq=4, Hkv=2, total=70, max_sq=50, max_kv=90, d=64, causal=1, window=0, sink=0, scale=0.5,
               o_dtype=1, fill=1, work=P, work_bytes=BIG, stream=N)
 
@@ -90,6 +92,10 @@ def test_rope_rotate():
     assert ROTATE(qo=P, qs=264) == INVALID  # in place at another stride
     assert ROTATE(Hq=1 << 30, qs=1 << 36, qos=1 << 36) == INVALID
     assert ROTATE(Hq=(1 << 25) - 1, qs=1 << 32, qos=1 << 32) == INVALID  # two heads of k beside them
+    # one output for both, or over the other's input
+    assert ROTATE(qo=2 * P, ko=2 * P) == INVALID
+    assert ROTATE(k=4 * P, qo=4 * P, ko=6 * P) == INVALID
+    assert ROTATE(q=4 * P, qo=6 * P, ko=4 * P) == INVALID
     assert ROTATE(total=0, q=N, k=N, positions=N, axes=N, n_axes=1) == OK
 
 
@@ -101,6 +107,14 @@ def test_gradients(call):
     refused(call, UNSUPPORTED, d=(32, 256, 512), o_dtype=(2, -1), scale=(1e-31, 1e31))
     assert call(window=4, causal=0) == INVALID
     assert call(B=0) == OK
+
+
+@pytest.mark.parametrize("call", [GRAD, VARLEN], ids=["fixed", "varlen"])
+def test_gradients_over_inputs(call):
+    for out in ("dq", "dk", "dv"):
+        for i, x in enumerate(("do", "q", "k", "v", "o", "lse", "dq", "dk", "dv")):
+            if x not in (out, "lse"):
+                assert call(**{out: (i + 1) * P}) == INVALID, (out, x)
 
 
 def test_gradients_sizes():
