@@ -79,11 +79,14 @@ struct BwdCfg {
   static constexpr int kSt2 = D == 64 ? 4 : (KV ? 4 : 2);  // ring of Y2
   static constexpr int kY1Off = 2 * kFTile;
   static constexpr int kY2Off = kY1Off + kSt1 * kYTile;
-  // columns beside the dK/dV pass's tiles, 16 bytes a row: lse beside Q, D beside g, ones beside K
-  // and V, and zeros, the second eight columns of all of them
-  static constexpr int kExt = KV ? TN * 16 : 0;
-  static constexpr int kExtSlots = 5;
-  static constexpr int kOnes = KV ? kT * 16 : 0;
+  // columns beside the tiles, 16 bytes a row: lse beside Q, D beside g, ones beside K and V, and zeros,
+  // the second eight columns of all of them.  In the dQ pass, whose rows are a thread's own, at d = 64
+  // only, where issue slots bound it: an addition fewer a pair of columns, no loads of stat, against a step more a
+  // product (2 x 16 heads of 4096, not causal: 429 us without, 417 so)
+  static constexpr bool kRowExt = !KV && D == 64;
+  static constexpr int kExt = KV ? TN * 16 : (kRowExt ? kT * 16 : 0);
+  static constexpr int kExtSlots = KV ? 5 : 1;
+  static constexpr int kOnes = KV || kRowExt ? kT * 16 : 0;
   static constexpr int kExt1Off = kY2Off + kSt2 * kYTile;
   static constexpr int kExt2Off = kExt1Off + kExtSlots * kExt;
   static constexpr int kOnesOff = kExt2Off + kExtSlots * kExt;
@@ -511,7 +514,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  if constexpr (KV) {
+  if constexpr (KV || C::kRowExt) {
     for (int i = threadIdx.x; i < kT; i += C::kThreads) {
       *reinterpret_cast<uint4*>(smem + C::kOnesOff + i * 16) = make_uint4(0x3F803F80u, 0x00003F80u, 0, 0);
       *reinterpret_cast<uint4*>(smem + C::kZeroOff + i * 16) = make_uint4(0, 0, 0, 0);
@@ -580,8 +583,22 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       constexpr bool packed = !KV && PK;
       mbar_arrive_expect_tx_e(fF, C::kFTile);
       tma_load_5d_e(sF, map, fF, 0, packed ? run.u.qbase + run.x * kT : run.x * kT, 0, run.h, packed ? 0 : run.b);
+      if constexpr (C::kRowExt) {
+        // (its rows past the sequence's, anything, belong to rows that are not written)
+        const size_t i = PK ? (size_t)run.h * a.total_q + run.u.qbase + run.x * kT
+                            : ((size_t)run.b * a.Hq + run.h) * a.Sq + run.x * kT;
+        const uint4* src = (first ? a.ext1 : a.ext2) + i;
+#pragma unroll
+        for (int k = 0; k < kT; k += 32) cp_async16(ext + (k + lane) * 16, src + k + lane, 16);
+        cp_async_commit();
+      }
       const int n = run.n;
       run = w.next();
+      if constexpr (C::kRowExt) {
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
       ok = mbar_wait_warp(fF, (uint32_t)n_run & 1u, a.err, abort_flag);
       // behind the run before: its sums go out under these products, not after them
       if (ok && n_run > 0) ok = mbar_wait_warp(bar_go, (uint32_t)(n_run - 1) & 1u, a.err, abort_flag);
@@ -605,6 +622,8 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
         if constexpr (KV) {
           const uint32_t e = ext + it % C::kExtSlots * C::kExt;
           mma_ss_e(d, d1, smem_desc(e, zero - e, 128, kSwizzleNone), idesc, 1u);
+        } else if constexpr (C::kRowExt) {
+          mma_ss_e(d, smem_desc(ext, zero - ext, 128, kSwizzleNone), d1, idesc, 1u);
         }
         mma_commit_e(&done[it & 1]);
         if (!KV && !first) mma_commit_e(&empty2[s]);
@@ -715,10 +734,10 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     const float sl2 = a.scale * kLog2e;
     const uint64_t sl2x2 = f2pack(sl2, sl2);
     const int c0 = TN == 128 ? wg * 64 : 0;  // this thread's columns of an item: c0 .. c0 + 63
-    // lse and D of this thread's row (dQ pass; elsewhere they are in the products)
+    // lse and D of this thread's row (dQ pass, d = 128; elsewhere they are in the products)
     auto row_stat = [&](const Run& q) {
       float2 v = make_float2(INFINITY, 0.f);
-      if (!KV && q.n > 0 && q.x * kT + r < q.u.Sq) {
+      if (!KV && !C::kRowExt && q.n > 0 && q.x * kT + r < q.u.Sq) {
         const size_t i = PK ? (size_t)q.h * a.total_q + q.u.qbase + q.x * kT + r
                                 : ((size_t)q.b * a.Hq + q.h) * a.Sq + q.x * kT + r;
         v = a.stat[i];
@@ -795,7 +814,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
           for (int c = 0; c < 64; c += 2) {
             const uint64_t x = f2pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
             float e0, e1;
-            f2unpack(KV ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
+            f2unpack(KV || C::kRowExt ? mul2(x, sl2x2) : fma2(x, sl2x2, nlse2), e0, e1);
             s[c] = __float_as_uint(ex2_approx(e0));
             s[c + 1] = __float_as_uint(ex2_approx(e1));
           }
@@ -828,7 +847,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
             const float e0 = __uint_as_float(s[k]), e1 = __uint_as_float(s[k + 1]);
             float x0, x1;
             if constexpr (KV) tp[c] = pack_bf16x2(e0, e1);
-            else g = add2(g, ndd);
+            else if constexpr (!C::kRowExt) g = add2(g, ndd);
             f2unpack(mul2(g, f2pack(e0, e1)), x0, x1);
             t[c] = pack_bf16x2(x0, x1);
           }
