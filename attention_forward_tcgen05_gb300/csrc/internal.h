@@ -238,9 +238,9 @@ struct BackwardArgs {
   float scale;
   uint32_t* err;
   // workspace
-  int *pre_k, *pre_q;                   // items before each group of the two passes, and all of them
+  int *pre_k, *pre_q;                   // costs before each group of the two passes, and of all of them
   float2* stat;                         // [rows of lse] lse log2 e (+inf: the row takes no part), D
-  uint4 *ext1, *ext2;                   // the same as bf16 columns of the dK/dV pass, 128 rows more
+  uint4 *ext1, *ext2;                   // the same as bf16 columns of the products, 128 rows more
   float *part_k, *part_q;               // [ctas][2][accumulators * d / 4][128][4] sums of cut units
   int* joined;                          // [2][kBackwardCtas] parts of cut units that are out, by their first slice
   int ctas_k, ctas_q;                   // at most kBackwardCtas
