@@ -1,5 +1,5 @@
 // backward_api.cu -- the C ABI of the prefill's gradients (include/attn.h): argument
-// validation, the workspace's layout and the launches of prefill_backward.cu.
+// validation, the workspace's layout and the launches of prefill_backward.cuh.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -27,7 +27,7 @@ int check_sizes(const Sizes& z) {
   if (z.d != 64 && z.d != 128) return ATTN_ERR_UNSUPPORTED;
   if (z.rows * z.Hq >= (1LL << 31) || (long long)z.B * z.Skv * z.Hkv >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
   if ((long long)z.Hq * z.d >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
-  // items of all heads, 16 more a block for its run's cost (prefill_backward.cu): counted in 32 bits, a
+  // items of all heads, 16 more a block for its run's cost (prefill_backward.cuh): counted in 32 bits, a
   // CTA's share of them beyond the last
   const long long tq = (z.Sq + 63LL) / 64, tk = (z.Skv + 63LL) / 64, heads = (long long)z.B * z.Hq;
   auto over = [&](long long blocks, long long items) {
@@ -35,6 +35,15 @@ int check_sizes(const Sizes& z) {
   };
   if (over((tk + 1) / 2, tq) || over((tq + 1) / 2, tk)) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
+}
+
+// Calls for prefill_backward_fine.cu: of so few (row, key) pairs of all heads that the rounding of single
+// terms would show, and that a call's launches and one tile's chain bound either form (64 rows, 4
+// heads of 64: 14.7 us, 17.8 with one term; at the limit, 4 sequences of 16 rows and 64 keys, 32 heads of 64:
+// 20.8 and 22.7, of 128: 23.7 and 21.8; far above it, 32 of 64 rows and 256 keys: 145 and 88).
+bool few_pairs(const Sizes& z, int window, int n_sink) {
+  const long long keys = window > 0 ? std::min<long long>(z.Skv, (long long)window + n_sink) : z.Skv;
+  return (double)(z.rows * z.Hq) * (double)keys <= 131072.0;
 }
 
 // Byte offsets of the workspace's parts.
@@ -90,6 +99,7 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
       if (outs[i] && outs[i] == p) return ATTN_ERR_INVALID_ARG;
     if (outs[i] && outs[i] == outs[(i + 1) % 3]) return ATTN_ERR_INVALID_ARG;
   }
+  const bool fine = few_pairs(z, window, n_sink);
   const Layout l = layout_of(z);
   if (!work || !aligned(work, 256) || work_bytes < l.bytes) return ATTN_ERR_INVALID_ARG;
   attn::BackwardArgs a;
@@ -97,7 +107,8 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   if (rows && keys && z.Sq > 0) {
     // packed rows are one batch slab
     const int ns = cu_q ? (int)z.rows : z.Sq, nb = cu_q ? 1 : z.B;
-    const int tk = attn::backward_tile_rows(z.d, true), tq = attn::backward_tile_rows(z.d, false);
+    const int tk = fine ? attn::backward_fine_tile_rows(z.d, true) : attn::backward_tile_rows(z.d, true);
+    const int tq = fine ? attn::backward_fine_tile_rows(z.d, false) : attn::backward_tile_rows(z.d, false);
     rc = attn::encode_panel_map(&a.tm_q, q, z.d, z.Hq, ns, nb, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_do, dout, z.d, z.Hq, ns, nb, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_k, k, z.d, z.Hkv, z.Skv, z.B, 128);
@@ -130,7 +141,8 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   a.ctas_k = a.ctas_q = l.ctas;
   a.err = attn::device_err_word();
   if (a.err == nullptr) return ATTN_ERR_CUDA;
-  return attn::launch_backward(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return (fine ? attn::launch_backward_fine(a, s) : attn::launch_backward(a, s)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace

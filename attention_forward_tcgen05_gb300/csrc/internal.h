@@ -221,7 +221,7 @@ struct EvictArgs {
   uint32_t* err;
 };
 
-// Gradients of the prefill (prefill_backward.cu).  Fixed-length (cu_q == nullptr): q, o, dout,
+// Gradients of the prefill (prefill_backward.cuh).  Fixed-length (cu_q == nullptr): q, o, dout,
 // dq [B][Sq][Hq][d], lse [B][Hq][Sq], total_q = B * Sq; packed: [total_q][Hq][d], lse
 // [Hq][total_q], Sq the longest sequence, kv_lens set.  k, v, dk, dv [B][Skv][Hkv][d].
 struct BackwardArgs {
@@ -247,6 +247,7 @@ struct BackwardArgs {
 };
 constexpr int kBackwardCtas = 152;
 int backward_tile_rows(int d, bool dkdv);  // rows of a pass's streamed tiles
+int backward_fine_tile_rows(int d, bool dkdv);
 
 // Rows of a K / V stage loaded by one TMA box in the decode kernel (two
 // consumer warps share a stage, 32 rows each).
@@ -314,6 +315,7 @@ cudaError_t launch_rope_rotate(const RotateArgs& a, cudaStream_t stream);
 cudaError_t launch_key_weights(const KeyWeightArgs& a, cudaStream_t stream);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t stream);
+cudaError_t launch_backward_fine(const BackwardArgs& a, cudaStream_t stream);
 // This device's error word (attn_api.cu), or nullptr.
 uint32_t* device_err_word();
 // 5-D query map of the packed tiles: {d, G, Hq / G, ns, nb}, box {64, G, 1, rows / G, 1}.

@@ -1,6 +1,6 @@
 """The barrier schedule of the prefill's gradients, modelled on the CPU.
 
-A CTA of prefill_backward.cu has two warps that issue the first products (S, dP), one for the
+A CTA of prefill_backward.cuh has two warps that issue the first products (S, dP), one for the
 second products, one that fills the rings of Y1 and Y2, and eight of softmax.  They meet at
 mbarriers, whose waits test a phase *parity*: a wait is sound only if the barrier can be
 neither one phase short of what it takes for done nor one beyond it.
@@ -41,10 +41,15 @@ CONFIGS = {  # dK/dV or dQ, rows of a Y tile, stages of Y1 and Y2
     "dkdv-64": dict(kv=True, sep=False, st1=4, st2=4),
     "dq-128": dict(kv=False, sep=False, st1=3, st2=2),
     "dq-64": dict(kv=False, sep=False, st1=4, st2=4),
+    # P and dS as two terms (where the sums are wide, in one buffer)
+    "dkdv-128-fine": dict(kv=True, sep=True, st1=5, st2=4, one_p=True),
+    "dkdv-64-fine": dict(kv=True, sep=True, st1=4, st2=4),
+    "dq-128-fine": dict(kv=False, sep=True, st1=3, st2=2),
+    "dq-64-fine": dict(kv=False, sep=True, st1=4, st2=4),
 }
 
 
-def simulate(kv, sep, st1, st2, runs, parts, seed, ext_slots=5):
+def simulate(kv, sep, st1, st2, runs, parts, seed, ext_slots=5, one_p=False):
     rng = random.Random(seed)
     nd, arrive = (1, 4) if sep else (2, 8)
     stages = (st1, st2)
@@ -148,7 +153,7 @@ def simulate(kv, sep, st1, st2, runs, parts, seed, ext_slots=5):
 
                 def product(k, it=it, r=r, m=m, buf=buf):
                     nonlocal sums
-                    assert p_buf[buf] == it and p_parts[it] == arrive
+                    assert p_buf[0 if one_p else buf] == it and p_parts[it] == arrive
                     assert y[0][it % st1] == it if k == "2b" else y[1][it % st2] == it
                     if m == 0 and r > 0:
                         assert sums_read.get(r - 1) == 8, "sums overwritten"
@@ -195,12 +200,16 @@ def simulate(kv, sep, st1, st2, runs, parts, seed, ext_slots=5):
                 dp_read[it] = dp_read.get(it, 0) + 1
                 if sep:
                     freed[1][0].arrive()
-                    yield lambda: bar_pr[bp].done(it // 2)
-                assert it < 2 or it - 2 in executed["2b"], "P or dS overwritten"
+                    if one_p:
+                        yield lambda: it == 0 or bar_pr[bp ^ 1].done((it - 1) // 2 + 1)
+                    else:
+                        yield lambda: bar_pr[bp].done(it // 2)
+                last_p = it - (1 if one_p else 2)
+                assert last_p < 0 or last_p in executed["2b"], "P or dS overwritten"
                 # (where rows behind a sequence's last are cleared: both tiles are whole and read once)
                 assert y[0][it % st1] == it and it in executed["S"] and it in executed["dP"]
                 assert not kv or y[1][it % st2] == it
-                p_buf[bp] = it
+                p_buf[0 if one_p else bp] = it
                 p_parts[it] = p_parts.get(it, 0) + 1
                 bar_p[bp].arrive()
                 it += 1

@@ -305,3 +305,63 @@ def test_same_bits_each_time():
     b = attn.prefill_backward(do, q, k, v, o, lse, window=200, n_sink=4)
     attn.sync_check()
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+FEW = [  # B, Hq, Hkv, Sq, Skv, causal, window, sink: at most 131072 rows x heads x admitted keys
+    (3, 8, 1, 3, 3, True, 0, 0), (1, 4, 4, 2, 2, True, 0, 0), (1, 8, 2, 17, 200, True, 20, 1), (1, 4, 2, 64, 256, False, 0, 0),
+    (1, 6, 2, 64, 64, True, 9, 3), (1, 2, 1, 1, 256, True, 0, 0), (1, 4, 2, 63, 129, True, 0, 0), (5, 4, 1, 40, 33, True, 0, 0),
+    (1, 2, 1, 1500, 1500, True, 12, 2), (2, 4, 1, 1, 8000, True, 0, 0), (1, 1, 1, 300, 200, True, 0, 0), (4, 32, 8, 16, 64, True, 0, 0),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", FEW, ids=lambda c: "-".join(map(str, c)))
+def test_few_pairs_show_no_rounding_of_terms(case, d):
+    """P and dS enter their products as two terms (2^-17 of each left out), so that a gradient is off by
+    its own rounding, 2^-8 of it, and by far less of the sum of its terms' magnitudes: 2^-16 for the terms,
+    2^-20 for exponentials and fp32 sums.  In D and dP the same happens before the difference dP - D:
+    2^-20 of what they are sums of, in every term."""
+    B, Hq, Hkv, Sq, Skv, causal, window, sink = case
+    q, k, v, do = (t.cuda() for t in _inputs(B, Hq, Hkv, Sq, Skv, d, 31))
+    sc, G = 1 / math.sqrt(d), Hq // Hkv
+    ok = _mask(Sq, Skv, causal, window, sink, "cuda")
+    o, lse = torch.empty(q.shape, device="cuda"), torch.empty(B, Hq, Sq, device="cuda")
+    for b in range(B):
+        x, y = _forward(q[b], k[b], v[b], ok, sc)
+        o[b], lse[b] = x.float(), y.float()
+    for fixed in (True, False):
+        if fixed:
+            got = attn.prefill_backward(do, q, k, v, o, lse, causal=causal, window=window, n_sink=sink)
+        else:
+            cu = torch.arange(B + 1, dtype=torch.int32).cuda() * Sq
+            flat = lambda t: t.reshape(B * Sq, Hq, d)
+            got = attn.prefill_varlen_backward(flat(do), flat(q), k, v, flat(o),
+                                               lse.transpose(0, 1).reshape(Hq, B * Sq).contiguous(), cu,
+                                               torch.full((B,), Skv, dtype=torch.int32).cuda(), Sq, causal=causal,
+                                               window=window, n_sink=sink)
+            got = got[0].view(q.shape), got[1], got[2]
+        attn.sync_check()
+        for b in range(B):
+            x, kk, vv, g = (t[b].double() for t in (q, k, v, do))
+            kr, vr = kk.repeat_interleave(G, 1), vv.repeat_interleave(G, 1)
+            l = lse[b].double()[..., None]
+            p = torch.exp(torch.einsum("ihd,jhd->hij", x, kr) * sc - torch.where(l.isinf(), 0.0, l))
+            p = torch.where(ok & ~l.isinf(), p, 0.0)
+            dd = (g * o[b].double()).sum(-1).T[..., None]
+            dp = torch.einsum("ihd,jhd->hij", g, vr)
+            ds = p * (dp - dd)
+            # off by: two terms of it, and 2^-20 of what P's exponent, dP and D are made of
+            size = torch.einsum("ihd,jhd->hij", g.abs(), vr.abs()) + (g * o[b].double()).abs().sum(-1).T[..., None]
+            expo = torch.einsum("ihd,jhd->hij", x.abs(), kr.abs()) * sc + torch.where(l.isinf(), 0.0, l).abs() + 1
+            dp_off = p * 2.0 ** -16 + p * expo * 2.0 ** -20
+            ds_off = ds.abs() * 2.0 ** -16 + ds.abs() * expo * 2.0 ** -20 + p * size * 2.0 ** -20
+            fold = lambda t: t.unflatten(1, (Hkv, G)).sum(2)
+            want = (torch.einsum("hij,jhd->ihd", ds, kr) * sc, fold(torch.einsum("hij,ihd->jhd", ds, x)) * sc,
+                    fold(torch.einsum("hij,ihd->jhd", p, g)))
+            off = (torch.einsum("hij,jhd->ihd", ds_off, kr.abs()) * sc,
+                   fold(torch.einsum("hij,ihd->jhd", ds_off, x.abs())) * sc,
+                   fold(torch.einsum("hij,ihd->jhd", dp_off, g.abs())))
+            for i, name in enumerate(("dq", "dk", "dv")):
+                bad = (got[i][b].double() - want[i]).abs() > want[i].abs() * 2.0 ** -8 + off[i] * 1.01 + 1e-30
+                assert not bad.any(), (name, int(bad.sum()))
