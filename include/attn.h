@@ -641,7 +641,7 @@ int attn_evict(const float* weights, float* weights_out, long long w_stride, att
  *   d in {64, 128};  B * Sq * Hq and B * Skv * Hkv below 2^31;  B * Hq times the key blocks of 128
  *   times (query blocks of 64, plus 16), and the same with queries and keys exchanged, at most 2 * 10^9
  * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.  Can be captured
- * into a CUDA graph after a first call of its head dim on the device.
+ * into a CUDA graph after a first call of its sizes on the device.
  */
 int attn_prefill_backward(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16_t* k, const attn_bf16_t* v,
                           const void* o, const float* lse, const float* dlse, attn_bf16_t* dq, attn_bf16_t* dk,
