@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libattn.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["attn_api.cu", "paged_api.cu", "prefill.cu", "prefill_paged.cu", "prefill_paged_f32.cu", "prefill_pair.cu", "prefill_d512.cu",
            "prefill_persist.cu", "decode.cu", "decode_paged.cu", "decode_window.cu", "decode_noalloc.cu", "rope.cu", "key_weights.cu",
-           "evict.cu", "backward_api.cu", "prefill_backward.cu", "prefill_backward_fine.cu"]
+           "evict.cu", "backward_api.cu", "prefill_backward.cu", "prefill_backward_fine.cu",
+           "prefill_backward_packed.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "paged.cuh", "prefill_kernel.cuh", "prefill_paged.cuh", "decode_common.cuh", "decode_paged.cuh",
            "mma.cuh", "prefill_backward.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -37,34 +37,24 @@ int check_sizes(const Sizes& z) {
   return ATTN_OK;
 }
 
-// Calls for prefill_backward_fine.cu: of so few (row, key) pairs of all heads that the rounding of single
-// terms would show, and that a call's launches and one tile's chain bound either form (64 rows, 4
-// heads of 64: 14.7 us, 17.8 with one term; at the limit, 4 sequences of 16 rows and 64 keys, 32 heads of 64:
-// 20.8 and 22.7, of 128: 23.7 and 21.8; far above it, 32 of 64 rows and 256 keys: 145 and 88).
-bool few_pairs(const Sizes& z, int window, int n_sink) {
-  const long long keys = window > 0 ? std::min<long long>(z.Skv, (long long)window + n_sink) : z.Skv;
-  return (double)(z.rows * z.Hq) * (double)keys <= 131072.0;
-}
-
 // Byte offsets of the workspace's parts.
 struct Layout {
-  size_t pre_k, pre_q, joined, stat, ext1, ext2, part_k, part_q, bytes;
+  size_t pre[4], joined, stat, ext1, ext2, part_k, part_q, bytes;
   int ctas;
 };
 Layout layout_of(const Sizes& z) {
   Layout l;
   const long long tq = (z.Sq + 127LL) / 128, tk = (z.Skv + 127LL) / 128;
-  // one CTA an SM, none without an item of its own
-  l.ctas = (int)std::max(1LL, std::min<long long>(attn::kBackwardCtas, tq * z.B * tk * z.Hq));
+  // one CTA an SM, none without an item of its own (two for two forms)
+  l.ctas = (int)std::max(2LL, std::min<long long>(attn::kBackwardCtas, tq * z.B * tk * z.Hq));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t p = at;
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  l.pre_k = take((size_t)(z.B * tk + 1) * 4);
-  l.pre_q = take((size_t)(z.B * tq + 1) * 4);
-  l.joined = take((size_t)2 * attn::kBackwardCtas * 4);
+  for (int i = 0; i < 4; ++i) l.pre[i] = take((size_t)(z.B * (i % 2 == 0 ? tk : tq) + 1) * 4);
+  l.joined = take((size_t)4 * attn::kBackwardCtas * 4);
   l.stat = take((size_t)z.rows * z.Hq * 8);
   l.ext1 = take(((size_t)z.rows * z.Hq + 128) * 16);
   l.ext2 = take(((size_t)z.rows * z.Hq + 128) * 16);
@@ -99,26 +89,27 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
       if (outs[i] && outs[i] == p) return ATTN_ERR_INVALID_ARG;
     if (outs[i] && outs[i] == outs[(i + 1) % 3]) return ATTN_ERR_INVALID_ARG;
   }
-  const bool fine = few_pairs(z, window, n_sink);
   const Layout l = layout_of(z);
   if (!work || !aligned(work, 256) || work_bytes < l.bytes) return ATTN_ERR_INVALID_ARG;
   attn::BackwardArgs a;
   std::memset(&a, 0, sizeof(a));
-  if (rows && keys && z.Sq > 0) {
+  // (the longest sequence has the most pairs; shorter ones of a packed batch may have few all the same)
+  const bool two = attn::backward_two_terms(z.Sq, z.Skv, causal, window, n_sink);
+  a.forms = two ? attn::kTwoTerms : (cu_q ? attn::kOneTerm | attn::kTwoTerms : attn::kOneTerm);
+  const bool any = rows && keys && z.Sq > 0;  // else the gradients are zeros
+  if (any) {
     // packed rows are one batch slab
     const int ns = cu_q ? (int)z.rows : z.Sq, nb = cu_q ? 1 : z.B;
-    const int tk = fine ? attn::backward_fine_tile_rows(z.d, true) : attn::backward_tile_rows(z.d, true);
-    const int tq = fine ? attn::backward_fine_tile_rows(z.d, false) : attn::backward_tile_rows(z.d, false);
     rc = attn::encode_panel_map(&a.tm_q, q, z.d, z.Hq, ns, nb, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_do, dout, z.d, z.Hq, ns, nb, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_k, k, z.d, z.Hkv, z.Skv, z.B, 128);
     if (rc == ATTN_OK) rc = attn::encode_panel_map(&a.tm_v, v, z.d, z.Hkv, z.Skv, z.B, 128);
-    // (a pass whose streamed tiles are of 128 rows shares the other's maps)
-    a.tm_qy = a.tm_q; a.tm_doy = a.tm_do; a.tm_ky = a.tm_k; a.tm_vy = a.tm_v;
-    if (rc == ATTN_OK && tk != 128) rc = attn::encode_panel_map(&a.tm_qy, q, z.d, z.Hq, ns, nb, tk);
-    if (rc == ATTN_OK && tk != 128) rc = attn::encode_panel_map(&a.tm_doy, dout, z.d, z.Hq, ns, nb, tk);
-    if (rc == ATTN_OK && tq != 128) rc = attn::encode_panel_map(&a.tm_ky, k, z.d, z.Hkv, z.Skv, z.B, tq);
-    if (rc == ATTN_OK && tq != 128) rc = attn::encode_panel_map(&a.tm_vy, v, z.d, z.Hkv, z.Skv, z.B, tq);
+    // (tiles of 64 rows: BwdCfg::TN)
+    const bool fine = (a.forms & attn::kTwoTerms) != 0, kv64 = fine || z.d == 128;
+    if (rc == ATTN_OK && kv64) rc = attn::encode_panel_map(&a.tm_q64, q, z.d, z.Hq, ns, nb, 64);
+    if (rc == ATTN_OK && kv64) rc = attn::encode_panel_map(&a.tm_do64, dout, z.d, z.Hq, ns, nb, 64);
+    if (rc == ATTN_OK && fine) rc = attn::encode_panel_map(&a.tm_k64, k, z.d, z.Hkv, z.Skv, z.B, 64);
+    if (rc == ATTN_OK && fine) rc = attn::encode_panel_map(&a.tm_v64, v, z.d, z.Hkv, z.Skv, z.B, 64);
     if (rc != ATTN_OK) return rc;
   }
   a.dout = dout; a.o = o; a.lse = lse; a.dlse = dlse;
@@ -130,19 +121,21 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   a.scale = scale;
   a.fill = fill ? 1 : 0;
   uint8_t* w = static_cast<uint8_t*>(work);
-  a.pre_k = reinterpret_cast<int*>(w + l.pre_k);
-  a.pre_q = reinterpret_cast<int*>(w + l.pre_q);
+  for (int i = 0; i < 4; ++i) a.pre[i] = reinterpret_cast<int*>(w + l.pre[i]);
   a.joined = reinterpret_cast<int*>(w + l.joined);
   a.stat = reinterpret_cast<float2*>(w + l.stat);
   a.ext1 = reinterpret_cast<uint4*>(w + l.ext1);
   a.ext2 = reinterpret_cast<uint4*>(w + l.ext2);
   a.part_k = reinterpret_cast<float*>(w + l.part_k);
   a.part_q = reinterpret_cast<float*>(w + l.part_q);
-  a.ctas_k = a.ctas_q = l.ctas;
+  a.ctas = l.ctas;
   a.err = attn::device_err_word();
   if (a.err == nullptr) return ATTN_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return (fine ? attn::launch_backward_fine(a, s) : attn::launch_backward(a, s)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  cudaError_t e = attn::launch_backward_prep(a, any, s);
+  if (e == cudaSuccess && any)
+    e = two ? attn::launch_backward_fine(a, s) : (cu_q ? attn::launch_backward_packed(a, s) : attn::launch_backward(a, s));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace

@@ -225,10 +225,8 @@ struct EvictArgs {
 // dq [B][Sq][Hq][d], lse [B][Hq][Sq], total_q = B * Sq; packed: [total_q][Hq][d], lse
 // [Hq][total_q], Sq the longest sequence, kv_lens set.  k, v, dk, dv [B][Skv][Hkv][d].
 struct BackwardArgs {
-  CUtensorMap tm_q, tm_do, tm_k, tm_v;  // encode_panel_map, 128 rows
-  // The streamed tiles of the dK/dV pass (Q, dout) and of the dQ pass (K, V): the same with the
-  // rows of backward_tile_rows
-  CUtensorMap tm_qy, tm_doy, tm_ky, tm_vy;
+  CUtensorMap tm_q, tm_do, tm_k, tm_v;          // encode_panel_map, 128 rows
+  CUtensorMap tm_q64, tm_do64, tm_k64, tm_v64;  // and 64, for the passes whose streamed tiles are so
   const uint16_t* dout;
   const void* o;
   const float *lse, *dlse;              // dlse may be nullptr
@@ -238,16 +236,38 @@ struct BackwardArgs {
   float scale;
   uint32_t* err;
   // workspace
-  int *pre_k, *pre_q;                   // costs before each group of the two passes, and of all of them
+  int* pre[4];                          // of a pass of a form: costs before each group, and of all of them
   float2* stat;                         // [rows of lse] lse log2 e (+inf: the row takes no part), D
   uint4 *ext1, *ext2;                   // the same as bf16 columns of the products, 128 rows more
   float *part_k, *part_q;               // [ctas][2][accumulators * d / 4][128][4] sums of cut units
-  int* joined;                          // [2][kBackwardCtas] parts of cut units that are out, by their first slice
-  int ctas_k, ctas_q;                   // at most kBackwardCtas
+  int* joined;                          // [4][kBackwardCtas] parts of cut units that are out, by their first slice
+  int forms;                            // of the call's sequences: kOneTerm, kTwoTerms or both
+  int ctas;                             // of a pass, at most kBackwardCtas (of both forms: at least 2)
 };
 constexpr int kBackwardCtas = 152;
-int backward_tile_rows(int d, bool dkdv);  // rows of a pass's streamed tiles
-int backward_fine_tile_rows(int d, bool dkdv);
+constexpr int kOneTerm = 1, kTwoTerms = 2;
+// Whether a sequence's P and dS go into their products as two bf16 terms each, not one: where few pairs of a
+// row and a key make up a head's gradients their error is not the usual mean of the terms' roundings
+// but may be that of one, up to 2^-8, as much again as the gradient's own.  By the sequence's own
+// pairs, so that it does not matter what it is batched with, how many heads there are or how large its cache
+// is.  Two terms take 1.05 to 1.75 times as long whatever the size (256 sequences of 64 rows, 32 heads of 64: 357 us
+// and 344, of 128: 463 and 333; 16 of 200 rows, 28 heads of 128: 125 and 85; 3314 rows: 390 and 223),
+// hence the limit.
+constexpr long long kTwoTermPairs = 24576;
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline bool backward_two_terms(long long rows, long long keys, int causal, int window, int n_sink) {
+  // (causal: a triangle of the keys' size where there are more rows)
+  const long long n = causal && rows > keys ? keys : rows;
+  // (a product of two ints' range fits)
+  long long pairs = causal ? n * (keys - n) + n * (n + 1) / 2 : n * keys;
+  if (window > 0) {
+    const long long w = rows * ((long long)window + n_sink);
+    pairs = w < pairs ? w : pairs;
+  }
+  return pairs <= kTwoTermPairs;
+}
 
 // Rows of a K / V stage loaded by one TMA box in the decode kernel (two
 // consumer warps share a stage, 32 rows each).
@@ -314,8 +334,12 @@ cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_rotate(const RotateArgs& a, cudaStream_t stream);
 cudaError_t launch_key_weights(const KeyWeightArgs& a, cudaStream_t stream);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+// The item lists, lse and D, zeros for what has no items (any: something has); then the gradients: of
+// fixed-length calls with one term, of calls of two terms, of packed ones that may have both.
+cudaError_t launch_backward_prep(const BackwardArgs& a, bool any, cudaStream_t stream);
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t stream);
 cudaError_t launch_backward_fine(const BackwardArgs& a, cudaStream_t stream);
+cudaError_t launch_backward_packed(const BackwardArgs& a, cudaStream_t stream);
 // This device's error word (attn_api.cu), or nullptr.
 uint32_t* device_err_word();
 // 5-D query map of the packed tiles: {d, G, Hq / G, ns, nb}, box {64, G, 1, rows / G, 1}.

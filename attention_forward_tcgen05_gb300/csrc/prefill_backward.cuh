@@ -64,9 +64,9 @@ constexpr int kMinCost = 8;  // of a slice
 //     product of 64 columns re-reads as much of F for half of the work (49 cycles a step, bound by
 //     shared memory, against 65 for 128 columns); elsewhere items of 64 were slower (d = 64, 2 x 16
 //     heads of 4096, not causal: 494 us in the dK/dV pass alone so, against 434).
-// FINE (prefill_backward_fine.cu): P and dS as two bf16 terms each (2^-17 of them left out, not 2^-8), both
-// multiplied by the same rows of Y.  Items of 64 columns, whose terms have columns of their own: one
-// buffer of them where the dK/dV pass's sums leave no room for two.
+// FINE: P and dS as two bf16 terms each (2^-17 of them left out, not 2^-8), both multiplied by the same rows
+// of Y, in sequences of few pairs (backward_two_terms).  Items of 64 columns, whose terms have columns of
+// their own: one buffer of them where the dK/dV pass's sums leave no room for two.
 template <int D, bool KV, bool FINE>
 struct BwdCfg {
   static constexpr int TN = ((D == 128 && KV) || FINE) ? 64 : 128;
@@ -111,14 +111,14 @@ struct BwdCfg {
   static constexpr int kThreads = 384;
 };
 
-// Extent of a unit: which Y tiles its F tile meets.
+// Extent of a unit: which Y tiles its F tile meets.  SEL: none for sequences of the other form (FINE or not).
 struct Unit {
   int Sq, Skv, qbase, kbase;  // rows and keys of the sequence, first row of q, first row of k
   long long off;              // key index of row i: i + off
   int nt, t0;                 // Y tiles, dK/dV pass: from t0 on; dQ pass: by the tile list
   TileList tl;
 };
-template <int TN, bool KV>
+template <int TN, bool KV, bool FINE, bool SEL>
 __device__ __forceinline__ Unit unit_of(const BackwardArgs& a, int b, int x) {
   Unit u;
   const SeqExtent e = seq_extent(b, a.Sq, a.Skv, a.cu_q, a.kv_lens, a.total_q);
@@ -128,6 +128,8 @@ __device__ __forceinline__ Unit unit_of(const BackwardArgs& a, int b, int x) {
   u.off = (long long)u.Skv - u.Sq;
   u.nt = 0; u.t0 = 0;
   u.tl = TileList{0x7FFFFFFF, 0};
+  // (a fixed-length call has sequences, and lists, of one form only)
+  if (SEL && a.cu_q && backward_two_terms(u.Sq, u.Skv, a.causal, a.window, a.n_sink) != FINE) return u;
   const int f0 = x * kT;
   if constexpr (KV) {
     if (f0 >= u.Skv) return u;
@@ -192,20 +194,15 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi, uint32_t& mid, uin
 }
 
 // Exclusive prefix of the groups' costs (all heads of a group) by one CTA; pre[n] the total.
-template <int TN, bool KV>
+template <int TN, bool KV, bool FINE>
 __device__ void scan_costs(const BackwardArgs& a, int* pre) {
   __shared__ int sums[kPrepThreads / 32];
   const int nx = f_tiles(a, KV), n = a.B * nx, H = KV ? a.Hkv : a.Hq;
   const int per = (n + kPrepThreads - 1) / kPrepThreads;
   const int lo = min(n, (int)threadIdx.x * per), hi = min(n, lo + per);
   int s = 0;
-  // a sequence above max_sq is reported, as the positions of its first rows would be taken for the last ones
-  if (KV && a.cu_q)
-    for (int b = threadIdx.x; b < a.B; b += kPrepThreads) {
-      const int c0 = min(max(a.cu_q[b], 0), a.total_q), c1 = min(a.cu_q[b + 1], a.total_q);
-      if (c1 - c0 > a.Sq) atomicCAS(a.err, kErrNone, kErrBadShape);
-    }
-  for (int g = lo; g < hi; ++g) s += unit_cost<TN, KV>(unit_items<KV>(a, unit_of<TN, KV>(a, g / nx, g % nx))) * H;
+  auto cost = [&](int g) { return unit_cost<TN, KV>(unit_items<KV>(a, unit_of<TN, KV, FINE, true>(a, g / nx, g % nx))) * H; };
+  for (int g = lo; g < hi; ++g) s += cost(g);
   int incl = s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -219,7 +216,7 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
   for (int w = 0; w < warp; ++w) at += sums[w];
   for (int g = lo; g < hi; ++g) {
     pre[g] = at;
-    at += unit_cost<TN, KV>(unit_items<KV>(a, unit_of<TN, KV>(a, g / nx, g % nx))) * H;
+    at += cost(g);
   }
   if (hi == n && lo < n) pre[n] = at;
   if (n == 0 && threadIdx.x == 0) pre[0] = 0;
@@ -227,13 +224,13 @@ __device__ void scan_costs(const BackwardArgs& a, int* pre) {
 
 // Zeros for the gradients of units without items: keys that no row sees, rows that see no key and,
 // with `fill`, rows of no sequence and slots behind a sequence's keys.  CTA c of n.
-template <int D, bool KV, bool FINE>
+template <int D, bool KV>
 __device__ void zero_units(const BackwardArgs& a, int c, int n) {
   const int nx = f_tiles(a, KV), n_groups = a.B * nx, H = KV ? a.Hkv : a.Hq;
   constexpr int kRows = 16;  // of a CTA's turn
   for (int gc = c; gc < n_groups * (kT / kRows); gc += n) {
     const int g = gc / (kT / kRows), b = g / nx, x = g - b * nx;
-    const Unit u = unit_of<BwdCfg<D, KV, FINE>::TN, KV>(a, b, x);
+    const Unit u = unit_of<kT, KV, false, false>(a, b, x);
     if (unit_items<KV>(a, u) > 0) continue;
     const int f0 = x * kT + gc % (kT / kRows) * kRows;
     const int rows = min(kRows, (KV ? (a.fill ? a.Skv : u.Skv) : u.Sq) - f0);
@@ -256,27 +253,40 @@ __device__ void zero_units(const BackwardArgs& a, int c, int n) {
   }
 }
 constexpr int kZeroCtas = 304;
+// The item lists: dK/dV and dQ of the sequences of two terms, then of those of one.
+constexpr int kLists = 4;
+constexpr int list_of(bool kv, bool fine) { return (fine ? 0 : 2) + (kv ? 0 : 1); }
 
 // D / 8 lanes to a row of a head, kPrepRows consecutive rows of it in flight: a row is 128 or 256 bytes, so
 // that nothing is lost by reading a head's rows and what is written, by head, lies side by side.
 constexpr int kPrepRows = 4;
 constexpr int prep_rows(int d) { return kPrepThreads / (d / 8) * kPrepRows; }  // of a CTA
-template <int D, bool OBF16, bool FINE>
+template <int D, bool OBF16>
 __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __grid_constant__ BackwardArgs a) {
-  if (blockIdx.x < 2) {
-    if (blockIdx.x == 0) scan_costs<BwdCfg<D, true, FINE>::TN, true>(a, a.pre_k);
-    else scan_costs<BwdCfg<D, false, FINE>::TN, false>(a, a.pre_q);
-    for (int i = threadIdx.x; i < kMaxCtas; i += kPrepThreads) a.joined[blockIdx.x * kMaxCtas + i] = 0;
+  if (blockIdx.x < kLists) {
+    const int i = (int)blockIdx.x;  // list_of
+    // a sequence above max_sq is reported, as the positions of its first rows would be taken for the last ones
+    if (i == 0 && a.cu_q)
+      for (int b = threadIdx.x; b < a.B; b += kPrepThreads) {
+        const int c0 = min(max(a.cu_q[b], 0), a.total_q), c1 = min(a.cu_q[b + 1], a.total_q);
+        if (c1 - c0 > a.Sq) atomicCAS(a.err, kErrNone, kErrBadShape);
+      }
+    if (!(a.forms & (i < 2 ? kTwoTerms : kOneTerm))) return;
+    if (i == 0) scan_costs<BwdCfg<D, true, true>::TN, true, true>(a, a.pre[0]);
+    else if (i == 1) scan_costs<BwdCfg<D, false, true>::TN, false, true>(a, a.pre[1]);
+    else if (i == 2) scan_costs<BwdCfg<D, true, false>::TN, true, false>(a, a.pre[2]);
+    else scan_costs<BwdCfg<D, false, false>::TN, false, false>(a, a.pre[3]);
+    for (int c = threadIdx.x; c < kMaxCtas; c += kPrepThreads) a.joined[i * kMaxCtas + c] = 0;
     return;
   }
-  if (blockIdx.x < 2 + kZeroCtas) {
-    zero_units<D, true, FINE>(a, (int)blockIdx.x - 2, kZeroCtas);
-    zero_units<D, false, FINE>(a, (int)blockIdx.x - 2, kZeroCtas);
+  if (blockIdx.x < kLists + kZeroCtas) {
+    zero_units<D, true>(a, (int)blockIdx.x - kLists, kZeroCtas);
+    zero_units<D, false>(a, (int)blockIdx.x - kLists, kZeroCtas);
     return;
   }
   constexpr int L = D / 8;
-  const int h = ((int)blockIdx.x - 2 - kZeroCtas) % a.Hq;
-  const int row0 = ((int)blockIdx.x - 2 - kZeroCtas) / a.Hq * prep_rows(D) + (int)threadIdx.x / L * kPrepRows;
+  const int h = ((int)blockIdx.x - kLists - kZeroCtas) % a.Hq;
+  const int row0 = ((int)blockIdx.x - kLists - kZeroCtas) / a.Hq * prep_rows(D) + (int)threadIdx.x / L * kPrepRows;
   const int c = threadIdx.x % L;
   float s[kPrepRows];
 #pragma unroll
@@ -325,13 +335,13 @@ struct Run {
   int b, x, h, i0, n, cnt, first;  // cnt: items of the unit, first: the place of its first one
 };
 // The items of a slice in order, run by run of one unit.
-template <int TN, bool KV>
+template <int TN, bool KV, bool FINE, bool SEL>
 struct Walk {
   const BackwardArgs& a;
   int per, pos, end;  // a slice's share of the list of costs, place in it, end of the slice
   int g, g0;     // group, its place
   Run at;        // of the group: u, b, x, cnt
-  __device__ __forceinline__ const int* pre() const { return KV ? a.pre_k : a.pre_q; }
+  __device__ __forceinline__ const int* pre() const { return a.pre[list_of(KV, FINE)]; }
   __device__ __forceinline__ Walk(const BackwardArgs& a_, int cta, int ctas, int lane) : a(a_) {
     const int n_groups = a.B * f_tiles(a, KV);
     const int total = pre()[n_groups];
@@ -357,7 +367,7 @@ struct Walk {
     const int nx = f_tiles(a, KV);
     at.b = g / nx;
     at.x = g - at.b * nx;
-    at.u = unit_of<TN, KV>(a, at.b, at.x);
+    at.u = unit_of<TN, KV, FINE, SEL>(a, at.b, at.x);
     at.cnt = unit_items<KV>(a, at.u);
     g0 = pre()[g];
   }
@@ -454,13 +464,13 @@ __device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
 }
 
 // The items whose tiles (or lse / D columns) a warp still has to bring.
-template <int TN, bool KV>
+template <int TN, bool KV, bool FINE, bool SEL>
 struct Stream {
-  Walk<TN, KV> w;
+  Walk<TN, KV, FINE, SEL> w;
   Run r;
   ItemWalk<TN, KV> y;
   int m, it;
-  __device__ __forceinline__ Stream(const BackwardArgs& a, const Walk<TN, KV>& w_)
+  __device__ __forceinline__ Stream(const BackwardArgs& a, const Walk<TN, KV, FINE, SEL>& w_)
       : w(w_), r(w.next()), y(a, r), m(0), it(0) {}
   __device__ __forceinline__ void step(const BackwardArgs& a) {
     ++it;
@@ -474,10 +484,12 @@ struct Stream {
   }
 };
 
-// One CTA's slice of a pass: `cta` of `ctas`.  PK: a packed batch.
+// One CTA's slice of a pass: `cta` of `ctas`, whose partials start at slot `slot0`.  PK: a packed batch.
 template <int D, bool KV, bool PK, bool FINE>
-__device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, int ctas) {
+__device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, int ctas, int slot0) {
   using C = BwdCfg<D, KV, FINE>;
+  using W = Walk<C::TN, KV, FINE, PK>;
+  using S = Stream<C::TN, KV, FINE, PK>;
   constexpr int NS = C::NS, ND = C::ND, TN = C::TN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   extern __shared__ uint8_t smem_raw[];
@@ -536,8 +548,8 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const Walk<TN, KV> start(a, cta, ctas, lane);  // (a chain of dependent loads: made once)
-  Walk<TN, KV> w = start;
+  const W start(a, cta, ctas, lane);  // (a chain of dependent loads: made once)
+  W w = start;
   Run run = w.next();
   if (warp == 8 || warp == 9) {
     // ---- first products: S = F1 Y1^T (warp 8), dP = F2 Y2^T (warp 9), and their F tiles ----
@@ -557,7 +569,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     if (lane == 0) tma_prefetch_desc(map);
     // the lse / D columns of an item (a tensor or bulk copy of them would take the copy engine as long
     // as a tile: 300 to 400 cycles whatever its size)
-    Stream<TN, KV> ex(a, start);
+    S ex(a, start);
     auto load_ext = [&] {
       if constexpr (KV) {
         if (ex.r.n > 0) {
@@ -689,10 +701,12 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
     }
   } else if (warp == 11) {
     // ---- the rings of Y1 and Y2, each slot filled as soon as it is free ----
-    Stream<TN, KV> st[2] = {Stream<TN, KV>(a, start), Stream<TN, KV>(a, start)};
+    const CUtensorMap* my1 = KV ? (TN == 64 ? &a.tm_q64 : &a.tm_q) : (TN == 64 ? &a.tm_k64 : &a.tm_k);
+    const CUtensorMap* my2 = KV ? (TN == 64 ? &a.tm_do64 : &a.tm_do) : (TN == 64 ? &a.tm_v64 : &a.tm_v);
+    S st[2] = {S(a, start), S(a, start)};
     if (lane == 0) {
-      tma_prefetch_desc(KV ? &a.tm_qy : &a.tm_ky);
-      tma_prefetch_desc(KV ? &a.tm_doy : &a.tm_vy);
+      tma_prefetch_desc(my1);
+      tma_prefetch_desc(my2);
     }
     bool ok = true;
     long long t0 = clock64();
@@ -701,14 +715,14 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       bool moved = false;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        Stream<TN, KV>& t = st[k];
+        S& t = st[k];
         if (t.r.n == 0) continue;
         const int stages = k == 0 ? C::kSt1 : C::kSt2, s = t.it % stages;
         uint64_t *full = k == 0 ? full1 : full2, *empty = k == 0 ? empty1 : empty2;
         if (!mbar_test_warp(&empty[s], ((uint32_t)(t.it / stages) & 1u) ^ 1u)) continue;
         moved = true;
         const Unit& u = t.r.u;
-        const CUtensorMap* map = KV ? (k == 0 ? &a.tm_qy : &a.tm_doy) : (k == 0 ? &a.tm_ky : &a.tm_vy);
+        const CUtensorMap* map = k == 0 ? my1 : my2;
         uint8_t* dst = smem + (k == 0 ? C::kY1Off : C::kY2Off) + s * C::kYTile;
         mbar_arrive_expect_tx_e(&full[s], C::kYTile);
         if (KV && PK) tma_load_5d_e(dst, map, &full[s], 0, u.qbase + t.y.row0, 0, t.y.h, 0);
@@ -943,7 +957,8 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
         }
       };
       constexpr int kSlot = kT * D * (KV ? 2 : 1) / 4;  // float4s of a partial: [column / 4][row]
-      float4* const parts = reinterpret_cast<float4*>(KV ? a.part_k : a.part_q) + (size_t)wg * (kCols / 4) * kT + r;
+      float4* const parts = reinterpret_cast<float4*>(KV ? a.part_k : a.part_q) + (size_t)slot0 * kSlot +
+                            (size_t)wg * (kCols / 4) * kT + r;
       float4* pp = parts + ((size_t)cta * 2 + (run.i0 > 0 ? 0 : 1)) * kSlot;
       ok = mbar_wait_warp(bar_acc, (uint32_t)n_run & 1u, a.err, abort_flag);
       if (!ok) break;
@@ -990,7 +1005,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
           if (!ok) break;
           if (lane == 0) {
             __threadfence();
-            *last_flag = atomicAdd(a.joined + (KV ? 0 : kMaxCtas) + c0, 1) == c1 - c0;
+            *last_flag = atomicAdd(a.joined + list_of(KV, FINE) * kMaxCtas + c0, 1) == c1 - c0;
             mbar_arrive(bar_last);
           }
           __syncwarp();
@@ -1036,42 +1051,60 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// Both passes: dQ's CTAs start as dK/dV's end.
+// Both passes: dQ's CTAs start as dK/dV's end.  A pass of a packed batch (PK) may have sequences of both forms,
+// which then share its CTAs by their lists' costs.
 constexpr int kThreads = 384;
-template <int D, bool PK, bool FINE>
+// CTAs of a pass that take the sequences of two terms, whose tiles cost about 1.7 times as much a row.
+template <int D, bool KV>
+__device__ __forceinline__ int two_term_ctas(const BackwardArgs& a) {
+  const int n = a.B * f_tiles(a, KV);
+  const float two = a.forms & kTwoTerms ? a.pre[list_of(KV, true)][n] * (1.7f * BwdCfg<D, KV, true>::TN) : 0.f;
+  const float one = a.forms & kOneTerm ? a.pre[list_of(KV, false)][n] * (1.f * BwdCfg<D, KV, false>::TN) : 0.f;
+  if (two == 0.f || one == 0.f) return two == 0.f ? 0 : a.ctas;
+  return min(max((int)(a.ctas * (two / (two + one)) + 0.5f), 1), a.ctas - 1);
+}
+template <int D, bool KV, bool PK, bool ONE, bool TWO>
+__device__ __forceinline__ void backward_forms(const BackwardArgs& a, int cta) {
+  int n = 0;
+  if constexpr (TWO) n = ONE ? two_term_ctas<D, KV>(a) : a.ctas;
+  // (one term first: eight packed sequences of 1000 rows, 32 heads of 128, 290 us, 294 behind two)
+  if constexpr (ONE) {
+    if (!TWO || cta >= n) return backward_pass<D, KV, PK, false>(a, cta - n, a.ctas - n, 2 * n);
+  }
+  if constexpr (TWO) backward_pass<D, KV, PK, true>(a, cta, n, 0);
+}
+template <int D, bool PK, bool ONE, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_constant__ BackwardArgs a) {
-  static_assert(BwdCfg<D, true, FINE>::kThreads == kThreads && BwdCfg<D, false, FINE>::kThreads == kThreads);
-  if ((int)blockIdx.x < a.ctas_k) backward_pass<D, true, PK, FINE>(a, (int)blockIdx.x, a.ctas_k);
-  else backward_pass<D, false, PK, FINE>(a, (int)blockIdx.x - a.ctas_k, a.ctas_q);
+  static_assert(BwdCfg<D, true, ONE>::kThreads == kThreads && BwdCfg<D, false, TWO>::kThreads == kThreads);
+  if ((int)blockIdx.x < a.ctas) backward_forms<D, true, PK, ONE, TWO>(a, (int)blockIdx.x);
+  else backward_forms<D, false, PK, ONE, TWO>(a, (int)blockIdx.x - a.ctas);
 }
 
-template <int D, bool FINE>
-cudaError_t launch_d(const BackwardArgs& a, cudaStream_t stream) {
-  const bool any = a.total_q > 0 && a.Sq > 0 && a.Skv > 0;  // else the gradients are zeros
+template <int D>
+cudaError_t launch_prep(const BackwardArgs& a, bool any, cudaStream_t stream) {
   const long long blocks = any ? (a.total_q + prep_rows(D) - 1LL) / prep_rows(D) * a.Hq : 0;
-  const unsigned grid = 2 + kZeroCtas + (unsigned)blocks;
-  if (a.o_bf16) backward_prep_kernel<D, true, FINE><<<grid, kPrepThreads, 0, stream>>>(a);
-  else backward_prep_kernel<D, false, FINE><<<grid, kPrepThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (!any || e != cudaSuccess) return e;
-  constexpr int kSmem = std::max(BwdCfg<D, true, FINE>::kSmem, BwdCfg<D, false, FINE>::kSmem);
-  auto kern = a.cu_q ? backward_kernel<D, true, FINE> : backward_kernel<D, false, FINE>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<a.ctas_k + a.ctas_q, kThreads, kSmem, stream>>>(a);
+  const unsigned grid = kLists + kZeroCtas + (unsigned)blocks;
+  if (a.o_bf16) backward_prep_kernel<D, true><<<grid, kPrepThreads, 0, stream>>>(a);
+  else backward_prep_kernel<D, false><<<grid, kPrepThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <bool FINE>
-int tile_rows(int d, bool dkdv) {
-  if (d == 64) return dkdv ? BwdCfg<64, true, FINE>::TN : BwdCfg<64, false, FINE>::TN;
-  return dkdv ? BwdCfg<128, true, FINE>::TN : BwdCfg<128, false, FINE>::TN;
+template <int D, bool PK, bool ONE, bool TWO>
+cudaError_t launch_d(const BackwardArgs& a, cudaStream_t stream) {
+  constexpr int one = ONE ? std::max(BwdCfg<D, true, false>::kSmem, BwdCfg<D, false, false>::kSmem) : 0;
+  constexpr int two = TWO ? std::max(BwdCfg<D, true, true>::kSmem, BwdCfg<D, false, true>::kSmem) : 0;
+  constexpr int kSmem = std::max(one, two);
+  auto kern = backward_kernel<D, PK, ONE, TWO>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<2 * a.ctas, kThreads, kSmem, stream>>>(a);
+  return cudaGetLastError();
 }
-template <bool FINE>
+template <bool PK, bool ONE, bool TWO>
 cudaError_t launch_all(const BackwardArgs& a, cudaStream_t stream) {
   switch (a.d) {
-    case 64: return launch_d<64, FINE>(a, stream);
-    case 128: return launch_d<128, FINE>(a, stream);
+    case 64: return launch_d<64, PK, ONE, TWO>(a, stream);
+    case 128: return launch_d<128, PK, ONE, TWO>(a, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -621,8 +621,9 @@ int attn_evict(const float* weights, float* weights_out, long long w_stride, att
  *   dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dout_i . v_j - D_i),
  *   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,
  * dk and dv summed over the query heads of a KV head.  P and dS go into their products rounded to
- * bf16 (2^-8 of each; the gradients' own rounding is 2^-8), or as two terms (2^-17) in calls of at most
- * 131072 rows x query heads x keys (with a window: window + n_sink of them), everything else is fp32.  The tensor
+ * bf16 (2^-8 of each; the gradients' own rounding is 2^-8), or as two terms (2^-17) for a sequence of at most
+ * 24576 pairs of a row and a key (all, or with causal those up to the row's position; with a window at most
+ * window + n_sink a row), whatever the batch, the heads and the cache around it; everything else is fp32.  The tensor
  * cores' fp32 sums round towards zero, once for 16 terms: up to 2^-24 of a sum each time, which shows from about
  * 10^6 terms on (the first keys of 700001 rows of 8 heads: dk and dv off by 0.7 %, the last ones by 0.3 %).  A row that
  * admits no key (lse = -inf) takes no part: its dq is 0.  Every sum has a fixed order: the same
