@@ -74,18 +74,37 @@ class Batch:
             few = pairs(n, L, causal, window, sink) <= LIMIT
             self.seqs.append(dict(q=q, do=do, k=k, v=v, o=o, lse=lse, dl=dl, want=want, one=one, two=two, few=few))
 
-    def packed(self, max_kv=None, **kw):
+    def packed(self, max_kv=None, first=0, spare=0, give_out=False, **kw):
+        """first, spare: rows of no sequence before and behind, which with the slots behind a sequence's keys
+        hold NaN."""
         max_kv = max_kv or max(self.lens_k)
-        cat = lambda name, dim=0: torch.cat([s[name] for s in self.seqs], dim).contiguous()
-        cache = lambda name: torch.stack([torch.cat([s[name], torch.full((max_kv - s[name].shape[0], self.Hkv, self.d), math.nan,
-                                                                         dtype=torch.bfloat16, device="cuda")]) for s in self.seqs])
+        nan = lambda *s, dtype=torch.bfloat16: torch.full(s, math.nan, dtype=dtype, device="cuda")
+
+        def rows(name):
+            x = [s[name] for s in self.seqs]
+            return torch.cat([nan(first, self.Hq, self.d, dtype=x[0].dtype), *x, nan(spare, self.Hq, self.d, dtype=x[0].dtype)])
+
+        def stats(name):
+            if self.seqs[0][name] is None:
+                return None
+            f = lambda n: nan(self.Hq, n, dtype=torch.float32)
+            return torch.cat([f(first), *(s[name] for s in self.seqs), f(spare)], 1).contiguous()
+
+        cache = lambda name: torch.stack([torch.cat([s[name], nan(max_kv - s[name].shape[0], self.Hkv, self.d)])
+                                          for s in self.seqs])
         cu = torch.zeros(len(self.seqs) + 1, dtype=torch.int32)
         cu[1:] = torch.cumsum(torch.tensor(self.lens_q), 0)
-        dl = cat("dl", 1) if self.seqs[0]["dl"] is not None else None
-        dq, dk, dv = attn.prefill_varlen_backward(cat("do"), cat("q"), cache("k"), cache("v"), cat("o"), cat("lse", 1),
-                                                  cu.cuda(), torch.tensor(self.lens_k, dtype=torch.int32).cuda(),
-                                                  max(self.lens_q), dlse=dl, **self.mask, **kw)
+        cu += first
+        q, k = rows("q"), cache("k")
+        out = tuple(torch.full_like(t, 7.0) for t in (q, k, k)) if give_out else None
+        dq, dk, dv = attn.prefill_varlen_backward(rows("do"), q, k, cache("v"), rows("o"), stats("lse"), cu.cuda(),
+                                                  torch.tensor(self.lens_k, dtype=torch.int32).cuda(),
+                                                  max(self.lens_q), dlse=stats("dl"), out=out, **self.mask, **kw)
         attn.sync_check()
+        rest = 7.0 if give_out else 0.0
+        assert (dq[:first] == rest).all() and (dq[int(cu[-1]):] == rest).all()
+        for b, L in enumerate(self.lens_k):
+            assert (dk[b, L:] == rest).all() and (dv[b, L:] == rest).all()
         return [(dq[cu[b]:cu[b + 1]], dk[b, :L], dv[b, :L]) for b, L in enumerate(self.lens_k)]
 
     def fixed(self, **kw):
