@@ -54,6 +54,10 @@ constexpr int kMaxCtas = kBackwardCtas;
 // 224 and 229).
 constexpr int run_cost(bool kv, int ty) { return (kv ? 640 : 128) / ty; }
 constexpr int kMinCost = 8;  // of a slice
+// Rows of Y that a run sums in TMEM.  The tensor core's fp32 sums round towards zero, by up to 2^-23 of the sum for
+// every 16 terms (2^-24 on average), so that a sum of 4.2 million terms of one sign came out 1.6 % short; a unit's
+// longer part of a slice is cut into runs, 2^-12 of each left out at most, whose sums are added to nearest.
+constexpr int kRunRows = 32768;
 
 // TN: rows of a Y tile, the columns of an item's S and dP.
 //   128, halved between the softmax warpgroups.  P and dS go back over dP, two dP beside one S: of
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __gri
 }
 
 // ------------------------------------------------------------------ the two passes
-// A run: items [i0, i0 + n) of the unit of head h in group (b, x); n = 0: none.
+// A run: items [i0, i0 + n) of the unit of head h in group (b, x), at most kRunRows of rows; n = 0: none.
 struct Run {
   Unit u;
   int b, x, h, i0, n, cnt, first;  // cnt: items of the unit, first: the place of its first one
@@ -383,10 +387,11 @@ struct Walk {
       }
       const int cost = unit_cost<TN, KV>(at.cnt);
       at.h = (pos - g0) / cost;
-      const int from = pos - g0 - at.h * cost, to = min(cost, from + end - pos);  // of the unit's cost
-      pos += to - from;
+      const int from = pos - g0 - at.h * cost;  // of the unit's cost
       at.first = g0 + at.h * cost + run_cost(KV, TN);
       at.i0 = max(0, from - run_cost(KV, TN));
+      const int to = min(min(cost, from + end - pos), at.i0 + kRunRows / TN + run_cost(KV, TN));
+      pos += to - from;
       at.n = max(0, to - run_cost(KV, TN)) - at.i0;
       if (at.n > 0) break;
     }
@@ -928,6 +933,10 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       lim = limits_of(next);
       y = ItemWalk<TN, KV>(a, next);
       const bool part = run.n != run.cnt;
+      // Of the unit's part in this slice, which starts at item s0 (or with the unit): whether there were runs
+      // before this one, and whether there are more.
+      const int s0 = cta * w.per - run.first;
+      const bool more = run.i0 > max(0, s0), ends = run.i0 + run.n == min(run.cnt, s0 + w.per);
       // KV: warpgroup 0 dV, 1 dK; else a half of dQ's columns each
       constexpr int kCols = KV ? D : D / 2;
       const uint32_t col0 = KV ? (wg == 0 ? 0 : C::kAcc1) : C::kAcc1 + wg * kCols;
@@ -959,7 +968,7 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
       constexpr int kSlot = kT * D * (KV ? 2 : 1) / 4;  // float4s of a partial: [column / 4][row]
       float4* const parts = reinterpret_cast<float4*>(KV ? a.part_k : a.part_q) + (size_t)slot0 * kSlot +
                             (size_t)wg * (kCols / 4) * kT + r;
-      float4* pp = parts + ((size_t)cta * 2 + (run.i0 > 0 ? 0 : 1)) * kSlot;
+      float4* pp = parts + ((size_t)cta * 2 + (s0 > 0 ? 0 : 1)) * kSlot;
       ok = mbar_wait_warp(bar_acc, (uint32_t)n_run & 1u, a.err, abort_flag);
       if (!ok) break;
       tc_fence_after();
@@ -977,9 +986,16 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
         for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
         if (part) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            pp[(size_t)((c + e) / 4) * kT] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
-                                                         __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+          for (int e = 0; e < 32; e += 4) {
+            float4 v = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]),
+                                   __uint_as_float(x[e + 3]));
+            float4* const to = pp + (size_t)((c + e) / 4) * kT;
+            if (more) {  // (this thread's own, of the run before)
+              const float4 u = *to;
+              v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+            }
+            *to = v;
+          }
         } else {
           uint4 q[4];
 #pragma unroll
@@ -993,28 +1009,32 @@ __device__ __forceinline__ void backward_pass(const BackwardArgs& a, int cta, in
           put_rows(q, c);
         }
       }
-      if (part) {
+      if (part && ends) {
         // The slice that finishes a cut unit last sums its parts, in slice order whoever it is.
         const int c0 = run.first / w.per, c1 = (run.first + run.cnt - 1) / w.per;  // the unit's slices
-        // (mbarriers, whose waits end, in place of a barrier that a warp after a failed wait would miss)
+        bool sum = c0 == c1;  // (a whole one of several runs is this slice's alone, and the counters are not its)
         __threadfence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_out);
-        if (warp == 0) {
-          ok = mbar_wait_warp(bar_out, (uint32_t)n_part & 1u, a.err, abort_flag);
-          if (!ok) break;
-          if (lane == 0) {
-            __threadfence();
-            *last_flag = atomicAdd(a.joined + list_of(KV, FINE) * kMaxCtas + c0, 1) == c1 - c0;
-            mbar_arrive(bar_last);
-          }
+        if (!sum) {
+          // (mbarriers, whose waits end, in place of a barrier that a warp after a failed wait would miss)
           __syncwarp();
-        }
-        ok = mbar_wait_warp(bar_last, (uint32_t)n_part & 1u, a.err, abort_flag);
-        if (!ok) break;
-        ++n_part;
-        if (*last_flag) {
+          if (lane == 0) mbar_arrive(bar_out);
+          if (warp == 0) {
+            ok = mbar_wait_warp(bar_out, (uint32_t)n_part & 1u, a.err, abort_flag);
+            if (!ok) break;
+            if (lane == 0) {
+              __threadfence();
+              *last_flag = atomicAdd(a.joined + list_of(KV, FINE) * kMaxCtas + c0, 1) == c1 - c0;
+              mbar_arrive(bar_last);
+            }
+            __syncwarp();
+          }
+          ok = mbar_wait_warp(bar_last, (uint32_t)n_part & 1u, a.err, abort_flag);
+          if (!ok) break;
+          ++n_part;
+          sum = *last_flag;
           __threadfence();
+        }
+        if (sum) {
           // (32 columns of two parts in flight: one 8-column group at a time took 20 us a unit)
 #pragma unroll 1
           for (int c = 0; c < kCols; c += 32) {
