@@ -80,17 +80,23 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   if (rows && (!ok16(dout) || !ok16(q) || !ok16(o) || !ok4(lse) || !aligned(dlse, 4) || !ok16(dq)))
     return ATTN_ERR_INVALID_ARG;
   if (keys && (!ok16(k) || !ok16(v) || !ok16(dk) || !ok16(dv))) return ATTN_ERR_INVALID_ARG;
-  // one pass's gradients are written while the other still reads
-  const void* outs[3] = {rows ? dq : nullptr, keys ? dk : nullptr, keys ? dv : nullptr};
-  const void* ins[5] = {rows ? dout : nullptr, rows ? q : nullptr, rows ? o : nullptr, keys ? k : nullptr,
-                        keys ? v : nullptr};
-  for (int i = 0; i < 3; ++i) {
-    for (const void* p : ins)
-      if (outs[i] && outs[i] == p) return ATTN_ERR_INVALID_ARG;
-    if (outs[i] && outs[i] == outs[(i + 1) % 3]) return ATTN_ERR_INVALID_ARG;
-  }
   const Layout l = layout_of(z);
   if (!work || !aligned(work, 256) || work_bytes < l.bytes) return ATTN_ERR_INVALID_ARG;
+  // one pass's gradients are written while the other still reads, the workspace all along
+  const long long nq = z.rows * z.Hq, nk = (long long)z.B * z.Skv * z.Hkv;
+  auto whole = [](const void* p, long long bytes) { return attn::ByteRows{p, bytes, bytes, 1}; };
+  const attn::ByteRows written[4] = {whole(dq, nq * z.d * 2), whole(dk, nk * z.d * 2), whole(dv, nk * z.d * 2),
+                                     whole(work, (long long)l.bytes)};
+  const attn::ByteRows read[9] = {whole(dout, nq * z.d * 2), whole(q, nq * z.d * 2),
+                                  whole(o, nq * z.d * (o_dtype == ATTN_BF16 ? 2 : 4)), whole(k, nk * z.d * 2),
+                                  whole(v, nk * z.d * 2), whole(lse, nq * 4), whole(dlse, nq * 4),
+                                  whole(cu_q, (z.B + 1LL) * 4), whole(kv_lens, z.B * 4LL)};
+  for (int i = 0; i < 4; ++i) {
+    for (const auto& x : read)
+      if (attn::rows_overlap(written[i], x)) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (attn::rows_overlap(written[i], written[j])) return ATTN_ERR_INVALID_ARG;
+  }
   attn::BackwardArgs a;
   std::memset(&a, 0, sizeof(a));
   // (the longest sequence has the most pairs; shorter ones of a packed batch may have few all the same)

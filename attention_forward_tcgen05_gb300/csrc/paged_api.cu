@@ -278,11 +278,20 @@ int attn_rope_rotate(const attn_bf16_t* q, const attn_bf16_t* k, long long q_str
     const long long w = (long long)x.H * d;
     if (!ok16(x.in) || !ok16(x.out) || x.stride < w || x.out_stride < w || x.stride % 8 || x.out_stride % 8)
       return ATTN_ERR_INVALID_ARG;
-    // in place only over itself
-    if (x.in == x.out && x.stride != x.out_stride) return ATTN_ERR_INVALID_ARG;
   }
-  // (a shared output, or one over the other's input, would be turned twice)
-  if (Hq > 0 && Hk > 0 && (q_out == k_out || q_out == k || k_out == q)) return ATTN_ERR_INVALID_ARG;
+  // outputs over inputs or one another would be turned twice, but for a side in place over itself
+  attn::ByteRows in[2], out[2];
+  for (int i = 0; i < 2; ++i) {
+    const auto& x = sides[i];
+    in[i] = attn::ByteRows{x.in, x.stride * 2, x.H * (long long)d * 2, total};
+    out[i] = attn::ByteRows{x.out, x.out_stride * 2, x.H * (long long)d * 2, total};
+  }
+  for (int i = 0; i < 2; ++i) {
+    const bool same = sides[i].in == sides[i].out && sides[i].stride == sides[i].out_stride;
+    if (!same && attn::rows_overlap(out[i], in[i])) return ATTN_ERR_INVALID_ARG;
+    if (attn::rows_overlap(out[i], in[1 - i])) return ATTN_ERR_INVALID_ARG;
+  }
+  if (attn::rows_overlap(out[0], out[1])) return ATTN_ERR_INVALID_ARG;
   if (!ok4(positions) || !aligned(axes, 4) || inv_freq == nullptr || !aligned(inv_freq, 8)) return ATTN_ERR_INVALID_ARG;
   // (eight tokens' chunks, and a CTA's threads beyond them, are counted in 32 bits)
   if ((Hq + (long long)Hk) * (d / 16) > (1LL << 27)) return ATTN_ERR_INVALID_ARG;

@@ -467,7 +467,7 @@ int attn_rope_append_axes(const attn_bf16_t* q, const attn_bf16_t* k, const attn
  * Arguments
  *   q, k         bf16, token t's heads [Hq][d] / [Hk][d] at t * stride elements, q_out and k_out
  *                likewise; strides at least the heads' width and multiples of 8.  Outputs do not
- *                overlap inputs or one another, or each is its own input with the same stride.  Hq or Hk
+ *                overlap inputs or one another (refused), or each is its own input with the same stride.  Hq or Hk
  *                may be 0
  *   positions    int32 [n_axes][total] (device, may be negative)
  *   axes         int32 [rot_dim/2] as in attn_rope_append_axes, or NULL (n_axes = 1)
@@ -634,7 +634,8 @@ int attn_evict(const float* weights, float* weights_out, long long w_stride, att
  *   o         the forward call's o (fp32 or bf16 per o_dtype; D is as exact as it), lse its
  *             fp32 [B][Hq][Sq]
  *   dlse      fp32 [B][Hq][Sq]: dL/dlse, or NULL where the loss does not use lse
- *   dq, dk, dv  like q, k, v, written whole; they overlap no input and not one another
+ *   dq, dk, dv  like q, k, v, written whole; with work they overlap no input and not one another
+ *             (refused)
  *   causal, window, n_sink, scale  as in the forward call (window = 0: none, >= 1: causal);
  *             scale in [1e-30, 1e30]
  *   work      attn_prefill_backward_workspace(B, Hq, Hkv, B * Sq, Sq, Skv, d) bytes, 256-byte
