@@ -9,7 +9,7 @@ from __future__ import annotations
 import functools
 import math
 
-from ._binding import ATTN_OK, AttnError, _launching, load
+from ._binding import ATTN_OK, AttnError, _keys, _launching, load
 from ._serving import _device, _elsewhere, _need, _out_code, _sized, _torch, _workspace
 
 
@@ -99,7 +99,7 @@ def prefill_backward(do, q, k, v, o, lse, causal: bool = True, window: int = 0, 
     work, wp = _work(n, dev, handle)
     with _launching:
         rc = load().attn_prefill_backward(gp, qp, kp, vp, op, lp, dp, dq, dk, dv, B, Hq, Hkv, Sq, Skv, d, int(causal),
-                                          int(window), int(n_sink), scale, code, wp, n, handle)
+                                          _keys(window), _keys(n_sink), scale, code, wp, n, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_prefill_backward")
     return out
@@ -142,8 +142,8 @@ def prefill_varlen_backward(do, q, kcache, vcache, o, lse, cu_seqlens_q, kv_lens
     work, wp = _work(n, dev, handle)
     with _launching:
         rc = load().attn_prefill_varlen_backward(gp, qp, kp, vp, op, lp, dp, dq, dk, dv, cu, np_, B, Hq, Hkv, total,
-                                                 max_sq, max_kv, d, int(causal), int(window), int(n_sink), scale, code,
-                                                 fill, wp, n, handle)
+                                                 max_sq, max_kv, d, int(causal), _keys(window), _keys(n_sink), scale,
+                                                 code, fill, wp, n, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_prefill_varlen_backward")
     return out

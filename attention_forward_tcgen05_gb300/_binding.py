@@ -276,6 +276,12 @@ def prefill(q, k, v, causal: bool = True, scale: float | None = None, out_dtype=
     return o, lse
 
 
+def _keys(n) -> int:
+    """A window or a number of sinks for a C call: its int holds as many keys as a sequence can have (a larger
+    number would lose its upper bits)."""
+    return min(max(int(n), -1), 0x7FFFFFFF)
+
+
 def prefill_window(q, k, v, window: int, n_sink: int = 0, scale: float | None = None,
                    out_dtype=None, stream=None, out=None):
     """Causal prefill over a sliding window of ``window`` positions plus the first
@@ -295,7 +301,7 @@ def prefill_window(q, k, v, window: int, n_sink: int = 0, scale: float | None = 
     else:
         o, lse = out
     rc = attn_prefill_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, Skv, d,
-                             window, n_sink, scale, _out_code(o.dtype), _stream_handle(stream))
+                             _keys(window), _keys(n_sink), scale, _out_code(o.dtype), _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_prefill_window")
     return o, lse
@@ -334,7 +340,7 @@ def prefill_varlen(q, kcache, vcache, cu_seqlens_q, kv_lens, max_sq: int, causal
             raise ValueError("a sliding window is causal")
         rc = attn_prefill_varlen_window(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(o), _ptr(lse),
                                         _ptr(cu_seqlens_q), _ptr(kv_lens), B, Hq, Hkv, total_q,
-                                        int(max_sq), max_kv, d, window, n_sink, scale,
+                                        int(max_sq), max_kv, d, _keys(window), _keys(n_sink), scale,
                                         _out_code(o.dtype), _stream_handle(stream))
         if rc != ATTN_OK:
             raise AttnError(rc, "attn_prefill_varlen_window")

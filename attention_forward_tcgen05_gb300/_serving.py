@@ -18,7 +18,7 @@ import ctypes
 import functools
 import math
 
-from ._binding import ATTN_BF16, ATTN_F32, ATTN_OK, AttnError, _counters, _launching, _lock, load
+from ._binding import ATTN_BF16, ATTN_F32, ATTN_OK, AttnError, _counters, _keys, _launching, _lock, load
 
 
 _module = None
@@ -527,8 +527,8 @@ def prefill_paged(q, kcache, vcache, page_table, cu_seqlens_q, kv_lens, max_sq: 
             ps = _sized(parts[1], "parts[1]", torch.float32, dev, total, Hq, n_splits)
     with _launching:
         rc = lib.attn_prefill_paged(qp, kp, vp, op, lp, tp, cu, np_, B, Hq, Hkv, total, max_sq, max_pages, page,
-                                    n_pages, d, int(causal), int(window), int(n_sink), scale, n_splits, min_rows_per_split, pp,
-                                    ps, code, handle)
+                                    n_pages, d, int(causal), _keys(window), _keys(n_sink), scale, n_splits,
+                                    min_rows_per_split, pp, ps, code, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_prefill_paged")
     return o, lse
@@ -623,7 +623,7 @@ def decode_window(q, kcache, vcache, kv_lens, window: int, n_sink: int = 0, page
     kp, vp, tp, Hkv, d, max_pages, page, n_pages = _cache(kcache, vcache, page_table, B, dev)
     if dq != d:
         raise ValueError(f"q and the cache differ in head dim: {dq} and {d}")
-    window, n_sink = int(window), int(n_sink)
+    window, n_sink = _keys(window), _keys(n_sink)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -715,7 +715,7 @@ def key_weights(q, lse, kcache, kv_lens, weights, page_table=None, cu_seqlens_q=
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     rc = load().attn_key_weights(qp, lp, kp, tp, cu, np_, wp, w_stride, B, Hq, Hkv, total, int(max_sq), d, max_pages, page,
-                                 n_pages, int(causal), int(window), int(n_sink), scale, int(accumulate), handle)
+                                 n_pages, int(causal), _keys(window), _keys(n_sink), scale, int(accumulate), handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_key_weights")
     return weights
