@@ -279,7 +279,8 @@ def prefill(q, k, v, causal: bool = True, scale: float | None = None, out_dtype=
 def _keys(n) -> int:
     """A window or a number of sinks for a C call: its int holds as many keys as a sequence can have (a larger
     number would lose its upper bits)."""
-    return min(max(int(n), -1), 0x7FFFFFFF)
+    n = int(n)
+    return n if -1 <= n <= 0x7FFFFFFF else (-1 if n < 0 else 0x7FFFFFFF)
 
 
 def prefill_window(q, k, v, window: int, n_sink: int = 0, scale: float | None = None,

@@ -5,12 +5,10 @@
 // errors that only the device can see (a bounded pipeline wait that ran out).
 // Its device address is looked up once per device with cudaGetSymbolAddress
 // and handed to every kernel; attn_sync_check() reads and clears it.
-#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <utility>
 #include <vector>
 
 #include "attn.h"
@@ -126,30 +124,6 @@ int encode_panel_map(CUtensorMap* map, const void* base, int d, int H, int S, in
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
-}
-
-bool rows_overlap(ByteRows a, ByteRows b) {
-  for (ByteRows* x : {&a, &b}) {
-    if (x->p == nullptr || x->n <= 0 || x->width <= 0) return false;
-    if (x->stride == x->width) *x = ByteRows{x->p, x->n * x->width, x->n * x->width, 1};
-  }
-  if (a.n > b.n) std::swap(a, b);
-  const long long d = (long long)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
-  auto down = [](long long x, long long y) { return x / y - (x % y < 0); };
-  if (a.stride == b.stride) {
-    // rows i of a and j of b meet where -b.width < d + (j - i) * stride < a.width: at most two j - i
-    const long long m0 = down(-d, a.stride);
-    for (long long m = m0; m <= m0 + 1; ++m)
-      if (m > -a.n && m < b.n && d + m * a.stride > -b.width && d + m * a.stride < a.width) return true;
-    return false;
-  }
-  if (d >= (a.n - 1) * a.stride + a.width || d + (b.n - 1) * b.stride + b.width <= 0) return false;
-  for (long long i = 0; i < a.n; ++i) {  // (one row, but where both have gaps of their own)
-    const long long at = i * a.stride - d;                                  // of the row, from b's first
-    const long long j = std::max(0LL, down(at - b.width, b.stride) + 1);  // the first row of b that ends behind it
-    if (j < b.n && j * b.stride < at + a.width) return true;
-  }
-  return false;
 }
 
 int check_decode_split_args(const void* q, const void* kcache, const void* vcache, const int* kv_lens,

@@ -84,18 +84,23 @@ int backward_impl(const attn_bf16_t* dout, const attn_bf16_t* q, const attn_bf16
   if (!work || !aligned(work, 256) || work_bytes < l.bytes) return ATTN_ERR_INVALID_ARG;
   // one pass's gradients are written while the other still reads, the workspace all along
   const long long nq = z.rows * z.Hq, nk = (long long)z.B * z.Skv * z.Hkv;
-  auto whole = [](const void* p, long long bytes) { return attn::ByteRows{p, bytes, bytes, 1}; };
-  const attn::ByteRows written[4] = {whole(dq, nq * z.d * 2), whole(dk, nk * z.d * 2), whole(dv, nk * z.d * 2),
-                                     whole(work, (long long)l.bytes)};
-  const attn::ByteRows read[9] = {whole(dout, nq * z.d * 2), whole(q, nq * z.d * 2),
-                                  whole(o, nq * z.d * (o_dtype == ATTN_BF16 ? 2 : 4)), whole(k, nk * z.d * 2),
-                                  whole(v, nk * z.d * 2), whole(lse, nq * 4), whole(dlse, nq * 4),
-                                  whole(cu_q, (z.B + 1LL) * 4), whole(kv_lens, z.B * 4LL)};
+  struct Bytes {
+    const void* p;
+    long long n;
+  };
+  const Bytes written[4] = {{dq, nq * z.d * 2}, {dk, nk * z.d * 2}, {dv, nk * z.d * 2}, {work, (long long)l.bytes}};
+  const Bytes read[9] = {{dout, nq * z.d * 2}, {q, nq * z.d * 2}, {o, nq * z.d * (o_dtype == ATTN_BF16 ? 2 : 4)},
+                         {k, nk * z.d * 2}, {v, nk * z.d * 2}, {lse, nq * 4}, {dlse, nq * 4},
+                         {cu_q, (z.B + 1LL) * 4}, {kv_lens, z.B * 4LL}};
+  auto meet = [](const Bytes& x, const Bytes& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return a && b && x.n > 0 && y.n > 0 && a < b + y.n && b < a + x.n;
+  };
   for (int i = 0; i < 4; ++i) {
-    for (const auto& x : read)
-      if (attn::rows_overlap(written[i], x)) return ATTN_ERR_INVALID_ARG;
+    for (const Bytes& x : read)
+      if (meet(written[i], x)) return ATTN_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
-      if (attn::rows_overlap(written[i], written[j])) return ATTN_ERR_INVALID_ARG;
+      if (meet(written[i], written[j])) return ATTN_ERR_INVALID_ARG;
   }
   attn::BackwardArgs a;
   std::memset(&a, 0, sizeof(a));

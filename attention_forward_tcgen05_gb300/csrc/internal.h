@@ -340,13 +340,6 @@ cudaError_t launch_backward_prep(const BackwardArgs& a, bool any, cudaStream_t s
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t stream);
 cudaError_t launch_backward_fine(const BackwardArgs& a, cudaStream_t stream);
 cudaError_t launch_backward_packed(const BackwardArgs& a, cudaStream_t stream);
-// Bytes [p + t * stride, p + t * stride + width) for t in [0, n) (stride >= width), and whether two such
-// sets meet (attn_api.cu).
-struct ByteRows {
-  const void* p;
-  long long stride, width, n;
-};
-bool rows_overlap(ByteRows a, ByteRows b);
 // This device's error word (attn_api.cu), or nullptr.
 uint32_t* device_err_word();
 // 5-D query map of the packed tiles: {d, G, Hq / G, ns, nb}, box {64, G, 1, rows / G, 1}.

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <utility>
 
 #include "attn.h"
 #include "internal.h"
@@ -39,6 +40,36 @@ int check_heads(int B, int Hq, int Hkv) {
 
 // Bytes of a slot (its Hkv rows), which the row gathers hold in 32 bits.
 int check_slot(int Hkv, int d) { return (long long)Hkv * d >= (1LL << 31) ? ATTN_ERR_INVALID_ARG : ATTN_OK; }
+
+// Bytes [p + t * stride, p + t * stride + width) for t in [0, n) (stride >= width), and whether two such
+// sets meet.
+struct ByteRows {
+  const void* p;
+  long long stride, width, n;
+};
+bool rows_overlap(ByteRows a, ByteRows b) {
+  for (ByteRows* x : {&a, &b}) {
+    if (x->p == nullptr || x->n <= 0 || x->width <= 0) return false;
+    if (x->stride == x->width) *x = ByteRows{x->p, x->n * x->width, x->n * x->width, 1};
+  }
+  if (a.n > b.n) std::swap(a, b);
+  const long long d = (long long)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  auto down = [](long long x, long long y) { return x / y - (x % y < 0); };
+  if (a.stride == b.stride) {
+    // rows i of a and j of b meet where -b.width < d + (j - i) * stride < a.width: at most two j - i
+    const long long m0 = down(-d, a.stride);
+    for (long long m = m0; m <= m0 + 1; ++m)
+      if (m > -a.n && m < b.n && d + m * a.stride > -b.width && d + m * a.stride < a.width) return true;
+    return false;
+  }
+  if (d >= (a.n - 1) * a.stride + a.width || d + (b.n - 1) * b.stride + b.width <= 0) return false;
+  for (long long i = 0; i < a.n; ++i) {  // (one row, but where both have gaps of their own)
+    const long long at = i * a.stride - d;                                  // of the row, from b's first
+    const long long j = std::max(0LL, down(at - b.width, b.stride) + 1);  // the first row of b that ends behind it
+    if (j < b.n && j * b.stride < at + a.width) return true;
+  }
+  return false;
+}
 
 attn::PagedKV cache(const attn_bf16_t* k, const attn_bf16_t* v, const int* table, int max_pages, int page_size,
                     int num_pages) {
@@ -280,18 +311,18 @@ int attn_rope_rotate(const attn_bf16_t* q, const attn_bf16_t* k, long long q_str
       return ATTN_ERR_INVALID_ARG;
   }
   // outputs over inputs or one another would be turned twice, but for a side in place over itself
-  attn::ByteRows in[2], out[2];
+  ByteRows in[2], out[2];
   for (int i = 0; i < 2; ++i) {
     const auto& x = sides[i];
-    in[i] = attn::ByteRows{x.in, x.stride * 2, x.H * (long long)d * 2, total};
-    out[i] = attn::ByteRows{x.out, x.out_stride * 2, x.H * (long long)d * 2, total};
+    in[i] = ByteRows{x.in, x.stride * 2, x.H * (long long)d * 2, total};
+    out[i] = ByteRows{x.out, x.out_stride * 2, x.H * (long long)d * 2, total};
   }
   for (int i = 0; i < 2; ++i) {
     const bool same = sides[i].in == sides[i].out && sides[i].stride == sides[i].out_stride;
-    if (!same && attn::rows_overlap(out[i], in[i])) return ATTN_ERR_INVALID_ARG;
-    if (attn::rows_overlap(out[i], in[1 - i])) return ATTN_ERR_INVALID_ARG;
+    if (!same && rows_overlap(out[i], in[i])) return ATTN_ERR_INVALID_ARG;
+    if (rows_overlap(out[i], in[1 - i])) return ATTN_ERR_INVALID_ARG;
   }
-  if (attn::rows_overlap(out[0], out[1])) return ATTN_ERR_INVALID_ARG;
+  if (rows_overlap(out[0], out[1])) return ATTN_ERR_INVALID_ARG;
   if (!ok4(positions) || !aligned(axes, 4) || inv_freq == nullptr || !aligned(inv_freq, 8)) return ATTN_ERR_INVALID_ARG;
   // (eight tokens' chunks, and a CTA's threads beyond them, are counted in 32 bits)
   if ((Hq + (long long)Hk) * (d / 16) > (1LL << 27)) return ATTN_ERR_INVALID_ARG;
