@@ -13,7 +13,7 @@
 // dQ into global memory: every sum has one owner and a fixed order, so the same inputs give
 // the same bits, no fp32 copy of dQ is zeroed, added to by atomics and converted, and the
 // accumulators, S and dP of a 128 x 128 tile fill TMEM (512 columns) in either pass at
-// d = 128; a third accumulator would not fit.  Both passes are one kernel: with
+// d = 128; a third accumulator would not fit beside them.  Both passes are one kernel: with
 //   the fixed pair F1, F2 and the streamed pair Y1, Y2
 //     dK/dV pass:  F = K, V    Y = Q, g
 //     dQ pass:     F = Q, g    Y = K, V
@@ -89,7 +89,7 @@ struct BwdCfg {
   static constexpr int kY2Off = kY1Off + kSt1 * kYTile;
   // columns beside the tiles, 16 bytes a row: lse beside Q, D beside g, ones beside K and V, and zeros,
   // the second eight columns of all of them.  In the dQ pass, whose rows are a thread's own, at d = 64
-  // only, where issue slots bound it: an addition fewer a pair of columns, no loads of stat, against a step more a
+  // only, where the softmax warps' work is longest: an addition fewer a pair of columns, no loads of stat, against a step more a
   // product (2 x 16 heads of 4096, not causal: 429 us without, 417 so)
   static constexpr bool kRowExt = !KV && D == 64;
   static constexpr int kExt = KV ? TN * 16 : (kRowExt ? kT * 16 : 0);
