@@ -56,8 +56,9 @@ constexpr int run_cost(bool kv, int ty) { return (kv ? 640 : 128) / ty; }
 constexpr int kMinCost = 8;  // of a slice
 // Rows of Y that a run sums in TMEM.  The tensor core's fp32 sums round towards zero, by up to 2^-23 of the sum for
 // every 16 terms (2^-24 on average), so that a sum of 4.2 million terms of one sign came out 1.6 % short; a unit's
-// longer part of a slice is cut into runs, 2^-12 of each left out at most, whose sums are added to nearest.
-constexpr int kRunRows = 32768;
+// longer part of a slice is cut into runs, 2^-12 of each left out at most, whose sums are added to nearest.  (Two
+// terms are two sums a step.)
+constexpr int run_rows(bool fine) { return fine ? 16384 : 32768; }
 
 // TN: rows of a Y tile, the columns of an item's S and dP.
 //   128, halved between the softmax warpgroups.  P and dS go back over dP, two dP beside one S: of
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __gri
 }
 
 // ------------------------------------------------------------------ the two passes
-// A run: items [i0, i0 + n) of the unit of head h in group (b, x), at most kRunRows of rows; n = 0: none.
+// A run: items [i0, i0 + n) of the unit of head h in group (b, x), at most run_rows of Y; n = 0: none.
 struct Run {
   Unit u;
   int b, x, h, i0, n, cnt, first;  // cnt: items of the unit, first: the place of its first one
@@ -390,7 +391,7 @@ struct Walk {
       const int from = pos - g0 - at.h * cost;  // of the unit's cost
       at.first = g0 + at.h * cost + run_cost(KV, TN);
       at.i0 = max(0, from - run_cost(KV, TN));
-      const int to = min(min(cost, from + end - pos), at.i0 + kRunRows / TN + run_cost(KV, TN));
+      const int to = min(min(cost, from + end - pos), at.i0 + run_rows(FINE) / TN + run_cost(KV, TN));
       pos += to - from;
       at.n = max(0, to - run_cost(KV, TN)) - at.i0;
       if (at.n > 0) break;
