@@ -179,3 +179,36 @@ def test_both_forms_in_one_batch(i, o_dtype):
     x = Batch(**MIXED[i], o_dtype=o_dtype)
     assert {s["few"] for s in x.seqs} == {True, False}
     x.check(x.packed(max(x.lens_k) + 77))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_graph_replayed_with_other_lengths(d):
+    """The lengths are read when the call runs: a replay has each sequence in its form of then."""
+    first = dict(lens_q=[700, 5, 300, 64], lens_k=[700, 90, 300, 64])
+    then = dict(lens_q=[5, 700, 64, 300], lens_k=[90, 700, 64, 300])
+    a, b = Batch(**first, Hq=4, Hkv=2, d=d), Batch(**then, Hq=4, Hkv=2, d=d, seed=8)
+
+    def tensors(x):
+        pad = lambda t: torch.cat([t, t.new_zeros(700 - t.shape[0], *t.shape[1:])])
+        cat = lambda n, dim=0: torch.cat([s[n] for s in x.seqs], dim).contiguous()
+        cu = torch.zeros(5, dtype=torch.int32)
+        cu[1:] = torch.cumsum(torch.tensor(x.lens_q), 0)
+        return [cat("do"), cat("q"), *(torch.stack([pad(s[n]) for s in x.seqs]) for n in "kv"), cat("o"), cat("lse", 1),
+                cu.cuda(), torch.tensor(x.lens_k, dtype=torch.int32).cuda()]
+
+    def outputs(x, got):
+        cu = [sum(x.lens_q[:i]) for i in range(5)]
+        return [(got[0][cu[i]:cu[i + 1]], got[1][i, :L], got[2][i, :L]) for i, L in enumerate(x.lens_k)]
+
+    args = tensors(a)
+    a.check(outputs(a, attn.prefill_varlen_backward(*args, 700)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = attn.prefill_varlen_backward(*args, 700)
+    for x in (a, b, a):
+        for t, new in zip(args, tensors(x)):
+            t.copy_(new)
+        graph.replay()
+        attn.sync_check()
+        x.check(outputs(x, got))
