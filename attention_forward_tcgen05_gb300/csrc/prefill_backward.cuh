@@ -334,6 +334,19 @@ __global__ void __launch_bounds__(kPrepThreads) backward_prep_kernel(const __gri
 }
 
 // ------------------------------------------------------------------ the two passes
+// The last group of [lo, hi) that starts at or before pos (pre[lo] <= pos < pre[hi]): those without items start
+// where the next does.  By a whole warp, first `step` groups apart.
+__device__ __forceinline__ int group_at(const int* pre, int lo, int hi, int pos, int lane, int step) {
+  while (hi - lo > 1) {
+    const int p = min(lo + (lane + 1) * step, hi);
+    const unsigned over = __ballot_sync(0xFFFFFFFFu, p >= hi || pre[p] > pos);
+    const int k = over ? __ffs(over) - 1 : 32;  // probes at or before pos
+    hi = k < 32 ? min(lo + (k + 1) * step, hi) : hi;
+    lo = lo + k * step;
+    step = max(1, (hi - lo) / 32);
+  }
+  return lo;
+}
 // A run: items [i0, i0 + n) of the unit of head h in group (b, x), at most run_rows of Y; n = 0: none.
 struct Run {
   Unit u;
@@ -355,17 +368,7 @@ struct Walk {
     end = min(total, pos + per);
     g = g0 = 0;
     if (pos >= end) return;
-    // the last group that starts at or before pos (those without items start where the next does)
-    int lo = 0, hi = n_groups;  // pre[lo] <= pos < pre[hi]
-    while (hi - lo > 1) {
-      const int step = max(1, (hi - lo) / 32);
-      const int p = min(lo + (lane + 1) * step, hi);
-      const unsigned over = __ballot_sync(0xFFFFFFFFu, p >= hi || pre()[p] > pos);
-      const int k = over ? __ffs(over) - 1 : 32;  // probes at or before pos
-      hi = k < 32 ? min(lo + (k + 1) * step, hi) : hi;
-      lo = lo + k * step;
-    }
-    g = lo;
+    g = group_at(pre(), 0, n_groups, pos, lane, max(1, n_groups / 32));
     enter();
   }
   __device__ __forceinline__ void enter() {
@@ -384,6 +387,11 @@ struct Walk {
     while (pos < end) {
       while (pos >= g0 + unit_cost<TN, KV>(at.cnt) * H) {
         ++g;
+        enter();
+        if (at.cnt > 0) continue;
+        // groups without items, of which there may be many: tiles behind short sequences' ends, sequences of the
+        // other form (one by one, 4000 sequences of 8 rows between two of 2000 took 40 ms)
+        g = group_at(pre(), g, a.B * f_tiles(a, KV), pos, (int)threadIdx.x & 31, 1);
         enter();
       }
       const int cost = unit_cost<TN, KV>(at.cnt);
@@ -1082,13 +1090,15 @@ __device__ __forceinline__ int two_term_ctas(const BackwardArgs& a) {
   const float two = a.forms & kTwoTerms ? a.pre[list_of(KV, true)][n] * (1.7f * BwdCfg<D, KV, true>::TN) : 0.f;
   const float one = a.forms & kOneTerm ? a.pre[list_of(KV, false)][n] * (1.f * BwdCfg<D, KV, false>::TN) : 0.f;
   if (two == 0.f || one == 0.f) return two == 0.f ? 0 : a.ctas;
-  return min(max((int)(a.ctas * (two / (two + one)) + 0.5f), 1), a.ctas - 1);
+  // (rounded up, as a few CTAs' share too large shows and a few too small does not: 64 sequences of 100 to 1990
+  // rows, four heads of 64, 332 us with it rounded to nearest)
+  return min(max((int)(a.ctas * (two / (two + one)) + 0.9f), 1), a.ctas - 1);
 }
 template <int D, bool KV, bool PK, bool ONE, bool TWO>
 __device__ __forceinline__ void backward_forms(const BackwardArgs& a, int cta) {
   int n = 0;
   if constexpr (TWO) n = ONE ? two_term_ctas<D, KV>(a) : a.ctas;
-  // (one term first: eight packed sequences of 1000 rows, 32 heads of 128, 290 us, 294 behind two)
+  // (one term first: behind two, eight packed sequences of 1000 rows, 32 heads of 128, took 4 us more of 290)
   if constexpr (ONE) {
     if (!TWO || cta >= n) return backward_pass<D, KV, PK, false>(a, cta - n, a.ctas - n, 2 * n);
   }

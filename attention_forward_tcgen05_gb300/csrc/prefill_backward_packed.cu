@@ -1,6 +1,6 @@
 // prefill_backward_packed.cu -- prefill_backward.cuh's kernels for packed batches that may hold sequences of both
 // forms, in one launch: as a launch each, one short sequence beside four of 1000 rows (32 heads of 128) made a call
-// 37 us longer, so 7, and one without any 5.
+// 37 us longer, so 3, and one without any 5.
 #include "prefill_backward.cuh"
 
 namespace attn {

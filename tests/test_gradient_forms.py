@@ -212,3 +212,36 @@ def test_a_graph_replayed_with_other_lengths(d):
         graph.replay()
         attn.sync_check()
         x.check(outputs(x, got))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_short_and_empty_sequences_between_long_ones(d):
+    x = Batch([300] + [0] * 200 + [8] * 100 + [0] * 100 + [300, 1], [300] + [9] * 200 + [8] * 100 + [0] * 100 + [340, 60], 4, 2, d)
+    x.check(x.packed(400, first=3, spare=2))
+
+
+@pytest.mark.gpu
+def test_time_beside_many_short_and_empty_sequences():
+    """Item lists are searched, not walked, where sequences have no items of a form: 1 and 2.2 ms here (one by
+    one, 26 and 41 ms)."""
+    for between in (0, 8):
+        lens = [2000] + [between] * 4000 + [2000]
+        B, T, mk = len(lens), sum(lens), 2000
+        z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+        cu = torch.tensor([0] + lens).cumsum(0).int().cuda()
+        q, k, lse = z(T, 4, 64), z(B, mk, 2, 64), torch.full((4, T), 7.0, device="cuda")
+        out = z(T, 4, 64), z(B, mk, 2, 64), z(B, mk, 2, 64)
+        call = lambda: attn.prefill_varlen_backward(q, q, k, k, q, lse, cu, torch.tensor(lens).int().cuda(), mk, out=out)
+        call()
+        times = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            a.record()
+            call()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        attn.sync_check()
+        assert sorted(times)[2] < 10.0, times
