@@ -625,8 +625,8 @@ int attn_evict(const float* weights, float* weights_out, long long w_stride, att
  * bf16 (2^-8 of each; the gradients' own rounding is 2^-8), or as two terms (2^-17) for a sequence of at most
  * 24576 pairs of a row and a key (all, or with causal those up to the row's position; with a window at most
  * window + n_sink a row), whatever the batch, the heads and the cache around it; everything else is fp32.  The tensor
- * cores' fp32 sums round towards zero, once for 16 terms; after 32768 rows or keys a sum goes on in fp32
- * to nearest, so that at most 2^-12 of it is left out however many terms it has.  A row that
+ * cores' fp32 sums round towards zero, once for 16 terms; after 32768 rows or keys (16384 of two
+ * terms) a sum goes on in fp32 to nearest, so that at most 2^-12 of it is left out however many terms it has.  A row that
  * admits no key (lse = -inf) takes no part: its dq is 0.  Every sum has a fixed order: the same
  * inputs give the same bits.
  *
